@@ -13,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,9 +21,10 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libgdn_cpr.so")
 PROBE_LIB = os.path.join(PKG, "libgdn_probe.so")
 PROBE_SOURCES = ["probe_fp32.cu"]
-SOURCES = ["gdn_cpr.cu", "identity.cu"]
+SOURCES = ["gdn_cpr.cu", "identity.cu", "layer_ops.cu"]
 DEPS = ["gdn_cpr.cu", "identity.cu", "kernels.cuh", "schedule.cuh", "tma.cuh", "k_tables.cuh", "k_ptok.cuh",
-        "k_tc.cuh", "k_prep.cuh", "k_pchunk.cuh", "k_decode.cuh", "k_bwd.cuh", "k_bgrad.cuh"]
+        "k_tc.cuh", "k_prep.cuh", "k_pchunk.cuh", "k_decode.cuh", "k_bwd.cuh", "k_bgrad.cuh",
+        "layer_ops.cu", "layer_common.cuh", "k_conv.cuh", "k_norm.cuh", "k_ssm.cuh", "k_ssm_bwd.cuh"]
 HEADERS = [os.path.join(ROOT, "include", "gdn_cpr.h")]
 
 
@@ -46,7 +48,7 @@ def nvcc_path() -> str:
 
 def flags(verbose: bool = False):
     f = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
-         "-Xcompiler", "-fPIC", "-shared",
+         "-Xcompiler", "-fPIC",
          # the schedule's arithmetic is written with explicit _rn intrinsics;
          # these keep any other fp expression exact too
          "-fmad=false", "-ftz=false", "-prec-div=true", "-prec-sqrt=true",
@@ -66,14 +68,27 @@ def up_to_date(lib: str, deps) -> bool:
 
 
 def _nvcc(lib: str, sources, verbose: bool):
+    """One object per source, compiled side by side, then linked."""
     tmp = lib + f".tmp{os.getpid()}"
-    cmd = [nvcc_path(), *flags(verbose), *[os.path.join(CSRC, s) for s in sources], "-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + r.stdout + r.stderr)
-    if verbose:
-        sys.stderr.write(r.stdout + r.stderr)
-    os.replace(tmp, lib)
+    objs = [f"{tmp}.{i}.o" for i in range(len(sources))]
+
+    def run(cmd):
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError("nvcc failed:\n" + r.stdout + r.stderr)
+        if verbose:
+            sys.stderr.write(r.stdout + r.stderr)
+
+    try:
+        with ThreadPoolExecutor(len(sources)) as pool:
+            list(pool.map(run, [[nvcc_path(), *flags(verbose), "-c", os.path.join(CSRC, s), "-o", o]
+                                for s, o in zip(sources, objs)]))
+        run([nvcc_path(), *flags(), "-shared", *objs, "-o", tmp])
+        os.replace(tmp, lib)
+    finally:
+        for o in objs:
+            if os.path.exists(o):
+                os.remove(o)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

@@ -1,0 +1,350 @@
+// k_conv.cuh -- the short causal convolution of a packed batch (sm_100a).
+//
+// Per sequence and channel c, with W = 2..4 taps and earlier inputs from the
+// cached state (zeros without one):
+//     pre[t] = bias + sum_{i<W} w[c][i] x[t - (W-1) + i],   y[t] = act(pre[t])
+// with act = silu or the identity.  Its gradients, with g = dy act'(pre):
+//     dx[t] = sum_j w[c][W-1-j] g[t+j],   dw[c][i] = sum_t g[t] x[t - (W-1) + i]
+//
+// Bound by memory: one read of x (and dy) and one write.  A thread keeps a
+// rolling window of W rows of a few channels in registers and walks a run of
+// tokens, so that x is read once plus W-1 rows per run, which the neighbouring
+// run brings into L2 anyway.
+#pragma once
+
+#include "layer_common.cuh"
+
+namespace gdn {
+
+struct ConvArgs {
+    Seqs s;
+    const void* x;
+    int64_t ldx;
+    const void *w, *bias;
+    const void* state_in;
+    int32_t D;
+    int silu, w_bf16;
+    // forward
+    void *y, *state_out;
+    // backward
+    const void* dy;
+    int64_t lddy;
+    const float* dstate_out;
+    void* dx;
+    float *dstate_in, *part;
+    // grid: ncb channel blocks x (token tiles, then one state tile per sequence)
+    int32_t ncb, cx;  // cx threads along the channels, 128 / cx runs of tokens per block
+    int64_t ntiles;
+    int32_t run;      // tokens per run
+    int32_t* status;
+};
+
+template <typename T, int W, int V>
+struct ConvTaps {
+    float w[W][V], b[V];
+    __device__ __forceinline__ void load(const ConvArgs& a, int64_t c)
+    {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+#pragma unroll
+            for (int i = 0; i < W; ++i) w[i][v] = load_w(a.w, a.w_bf16, (c + v) * W + i);
+            b[v] = a.bias != nullptr ? load_w(a.bias, a.w_bf16, c + v) : 0.0f;
+        }
+    }
+};
+
+// The window before row t of sequence n: win[i] = x[t - (W-1) + i] for i < W-1.
+template <typename T, int W, int V>
+__device__ __forceinline__ void conv_window(const ConvArgs& a, int n, int64_t lo, int64_t t, int64_t c,
+                                            float (&win)[W][V])
+{
+    const T* x = static_cast<const T*>(a.x);
+    const T* st = static_cast<const T*>(a.state_in);
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) {
+        const int64_t r = t - (W - 1) + i;
+        Vec<T, V> v;
+        bool have = true;
+        if (r >= lo) v = load_vec<T, V>(x + r * a.ldx + c);
+        else if (st != nullptr) v = load_vec<T, V>(st + ((int64_t)n * (W - 1) + (W - 1) + (r - lo)) * a.D + c);
+        else have = false;
+#pragma unroll
+        for (int k = 0; k < V; ++k) win[i][k] = have ? to_f<T>(v.v[k]) : 0.0f;
+    }
+}
+
+// state_out of one sequence: its last W-1 inputs, the old state's where it is shorter.
+template <typename T, int W, int V>
+__device__ __forceinline__ void conv_tail(const ConvArgs& a, int n, int64_t c)
+{
+    const int64_t lo = a.s.lo(n), L = a.s.hi(n) - lo;
+    const T* x = static_cast<const T*>(a.x);
+    const T* st = static_cast<const T*>(a.state_in);
+    T* out = static_cast<T*>(a.state_out) + (int64_t)n * (W - 1) * a.D + c;
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) {
+        const int64_t p = L - (W - 1) + i;
+        Vec<T, V> v;
+        if (p >= 0) v = load_vec<T, V>(x + (lo + p) * a.ldx + c);
+        else if (st != nullptr) v = load_vec<T, V>(st + ((int64_t)n * (W - 1) + (W - 1) + p) * a.D + c);
+        else {
+#pragma unroll
+            for (int k = 0; k < V; ++k) v.v[k] = from_f<T>(0.0f);
+        }
+        *reinterpret_cast<Vec<T, V>*>(out + (int64_t)i * a.D) = v;
+    }
+}
+
+// U rows are loaded together, so that a thread has U accesses in flight.
+template <typename T, int W, int V>
+__global__ void __launch_bounds__(128) k_conv_fwd(const ConvArgs a)
+{
+    constexpr int U = 8;
+    if (blockIdx.x == 0) check_seqs(a.s, a.status);
+    const int64_t tile = blockIdx.x / a.ncb;
+    const int cb = (int)(blockIdx.x - tile * a.ncb);
+    const int tx = threadIdx.x % a.cx, ty = threadIdx.x / a.cx, ny = 128 / a.cx;
+    const int64_t c = ((int64_t)cb * a.cx + tx) * V;
+    if (c >= a.D) return;
+    if (tile >= a.ntiles) {
+        const int64_t n = (tile - a.ntiles) * ny + ty;
+        if (n < a.s.N) conv_tail<T, W, V>(a, (int)n, c);
+        return;
+    }
+    int64_t t = (tile * ny + ty) * a.run;
+    const int64_t end = min(t + a.run, a.s.T);
+    if (t >= end) return;
+    int n = a.s.find(t);
+    if (n < 0) {  // rows before the first sequence
+        n = 0;
+        t = min(a.s.lo(0), end);
+        if (t >= end) return;
+        n = a.s.find(t);
+    }
+    ConvTaps<T, W, V> taps;
+    taps.load(a, c);
+    const T* x = static_cast<const T*>(a.x);
+    T* y = static_cast<T*>(a.y);
+    int64_t lo = a.s.lo(n), hi = a.s.hi(n);
+    float win[W][V];
+    conv_window<T, W, V>(a, n, lo, t, c, win);
+    for (; t < end; t += U) {
+        Vec<T, V> raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (t + u < end) raw[u] = load_vec<T, V>(x + (t + u) * a.ldx + c);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (t + u < end) {
+                if (t + u >= hi && n + 1 < a.s.N && t + u >= a.s.lo(n + 1)) {  // the next sequence's first token
+                    n = a.s.find(t + u);
+                    lo = a.s.lo(n);
+                    hi = a.s.hi(n);
+                    conv_window<T, W, V>(a, n, lo, t + u, c, win);
+                }
+                float o[V];
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    win[W - 1][k] = to_f<T>(raw[u].v[k]);
+                    float p = taps.b[k];
+#pragma unroll
+                    for (int i = 0; i < W; ++i) p = __fmaf_rn(taps.w[i][k], win[i][k], p);
+                    o[k] = a.silu ? silu(p) : p;
+#pragma unroll
+                    for (int i = 0; i < W - 1; ++i) win[i][k] = win[i + 1][k];
+                }
+                if (t + u < hi) store_vec<T, V>(y + (t + u) * a.D + c, o);  // rows behind the last sequence stay
+            }
+        }
+    }
+}
+
+// Gradients.  acc[i] is the unfinished dx of row t - (W-1) + i; after row t is
+// added, acc[0] is finished.  At a sequence's end the W-1 open rows are
+// finished too: they are the rows that the final state holds, in its order, so
+// dstate_out[i] is added to acc[i].  A row before the sequence's start is a row of
+// the initial state: its sum goes to dstate_in.  A run owns the rows [t0, t1)
+// and reads on up to W-1 rows behind them; a state tile owns the rows before
+// the start.
+template <typename T, int W, int V>
+__device__ __forceinline__ void conv_bwd_run(const ConvArgs& a, int64_t t0, int64_t t1, int only_seq, int64_t c,
+                                             const ConvTaps<T, W, V>& taps, float (&dw)[W][V], float (&db)[V])
+{
+    const T* x = static_cast<const T*>(a.x);
+    const T* dy = static_cast<const T*>(a.dy);
+    T* dx = static_cast<T*>(a.dx);
+    int64_t t = t0;
+    int n = only_seq >= 0 ? only_seq : a.s.find(t);
+    if (n < 0) {
+        t = min(a.s.lo(0), t1);
+        if (t >= t1) return;
+        n = a.s.find(t);
+    }
+    while (true) {  // one sequence's part of the run per pass
+        const int64_t lo = a.s.lo(n), hi = a.s.hi(n);
+        // rows this pass reads, and the last row it may add to a row that it owns
+        const int64_t stop = only_seq >= 0 ? min(hi, lo + (W - 1)) : min(hi, t1 + (W - 1));
+        float win[W][V], acc[W][V];
+        conv_window<T, W, V>(a, n, lo, t, c, win);
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+#pragma unroll
+            for (int k = 0; k < V; ++k) acc[i][k] = 0.0f;
+        auto emit = [&](int64_t r, const float (&v)[V]) {
+            if (only_seq >= 0) {
+                if (r < lo) {
+                    float* p = a.dstate_in + ((int64_t)n * (W - 1) + (W - 1) + (r - lo)) * a.D + c;
+#pragma unroll
+                    for (int k = 0; k < V; ++k) p[k] = v[k];
+                }
+            } else if (r >= lo && r >= t0 && r < t1) {
+                store_vec<T, V>(dx + r * a.D + c, v);
+            }
+        };
+        if (t < stop) {
+            Vec<T, V> rx = load_vec<T, V>(x + t * a.ldx + c), rg = load_vec<T, V>(dy + t * a.lddy + c);
+            for (; t < stop; ++t) {
+                const Vec<T, V> cx = rx, cg = rg;
+                if (t + 1 < stop) {
+                    rx = load_vec<T, V>(x + (t + 1) * a.ldx + c);
+                    rg = load_vec<T, V>(dy + (t + 1) * a.lddy + c);
+                }
+                const bool own = t < t1;
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    win[W - 1][k] = to_f<T>(cx.v[k]);
+                    float p = taps.b[k];
+#pragma unroll
+                    for (int i = 0; i < W; ++i) p = __fmaf_rn(taps.w[i][k], win[i][k], p);
+                    float g = to_f<T>(cg.v[k]);
+                    if (a.silu) g *= silu_grad(p);
+                    const float go = own ? g : 0.0f;
+                    db[k] += go;
+#pragma unroll
+                    for (int i = 0; i < W; ++i) {
+                        acc[i][k] = __fmaf_rn(taps.w[i][k], g, acc[i][k]);
+                        dw[i][k] = __fmaf_rn(go, win[i][k], dw[i][k]);
+                    }
+                }
+                emit(t - (W - 1), acc[0]);
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+#pragma unroll
+                    for (int i = 0; i < W - 1; ++i) {
+                        win[i][k] = win[i + 1][k];
+                        acc[i][k] = acc[i + 1][k];
+                    }
+                    acc[W - 1][k] = 0.0f;
+                }
+            }
+        }
+        if (stop == hi) {  // the sequence's end: the open rows hi - (W-1) + i
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i) {
+                if (a.dstate_out != nullptr) {
+                    const float* p = a.dstate_out + ((int64_t)n * (W - 1) + i) * a.D + c;
+#pragma unroll
+                    for (int k = 0; k < V; ++k) acc[i][k] += p[k];
+                }
+                emit(hi - (W - 1) + i, acc[i]);
+            }
+        }
+        if (only_seq >= 0 || hi >= t1) return;
+        // the next sequence of this run
+        if (n + 1 >= a.s.N) return;
+        t = max(hi, a.s.lo(n + 1));
+        if (t >= t1) return;
+        const int m = a.s.find(t);
+        if (m <= n) return;
+        n = m;
+    }
+}
+
+template <typename T, int W, int V>
+__global__ void __launch_bounds__(128) k_conv_bwd(const ConvArgs a)
+{
+    extern __shared__ float sh[];  // [(W + 1) * V][128]: joins the runs of a block
+    if (blockIdx.x == 0) check_seqs(a.s, a.status);
+    const int64_t tile = blockIdx.x / a.ncb;
+    const int cb = (int)(blockIdx.x - tile * a.ncb);
+    const int tx = threadIdx.x % a.cx, ty = threadIdx.x / a.cx, ny = 128 / a.cx;
+    const int64_t c = ((int64_t)cb * a.cx + tx) * V;
+    float dw[W][V], db[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        db[k] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) dw[i][k] = 0.0f;
+    }
+    if (c < a.D) {
+        ConvTaps<T, W, V> taps;
+        taps.load(a, c);
+        if (tile >= a.ntiles) {
+            const int64_t n = (tile - a.ntiles) * ny + ty;
+            // no rows are owned: only the state's gradient is written
+            if (n < a.s.N) conv_bwd_run<T, W, V>(a, a.s.lo((int)n), a.s.lo((int)n), (int)n, c, taps, dw, db);
+        } else {
+            const int64_t t0 = (tile * ny + ty) * a.run, t1 = min(t0 + a.run, a.s.T);
+            if (t0 < t1) conv_bwd_run<T, W, V>(a, t0, t1, -1, c, taps, dw, db);
+        }
+    }
+    if (tile >= a.ntiles) return;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) sh[(i * V + k) * 128 + threadIdx.x] = dw[i][k];
+        sh[(W * V + k) * 128 + threadIdx.x] = db[k];
+    }
+    __syncthreads();
+    if (ty == 0 && c < a.D) {
+#pragma unroll
+        for (int j = 0; j < (W + 1) * V; ++j) {
+            float s = 0.0f;
+            for (int r = 0; r < ny; ++r) s += sh[j * 128 + r * a.cx + tx];
+            a.part[(tile * (W + 1) + j / V) * a.D + c + j % V] = s;
+        }
+    }
+}
+
+// [W + 1][D] column sums -> dweight [D][W] and dbias [D]
+struct ConvGradMap {
+    float *dw, *db;
+    int32_t D, W;
+    __device__ void operator()(int64_t m, float s) const
+    {
+        const int i = (int)(m / D);
+        const int64_t c = m - (int64_t)i * D;
+        if (i < W) dw[c * W + i] = s;
+        else if (db != nullptr) db[c] = s;
+    }
+};
+
+// One token per sequence: window = [state, x]; state_out = the window without its first row.
+template <typename T, int W, int V>
+__global__ void __launch_bounds__(128) k_conv_step(const T* __restrict__ x, int64_t ldx, const void* w,
+                                                   const void* bias, const T* state, T* state_out, int64_t N,
+                                                   int32_t D, int silu_on, int w_bf16, T* __restrict__ y)
+{
+    const int64_t per = D / V;
+    const int64_t id = (int64_t)blockIdx.x * 128 + threadIdx.x;
+    if (id >= N * per) return;
+    const int64_t n = id / per, c = (id - n * per) * V;
+    Vec<T, V> win[W];
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) win[i] = load_vec<T, V>(state + (n * (W - 1) + i) * D + c);
+    win[W - 1] = load_vec<T, V>(x + n * ldx + c);
+    float o[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        float p = bias != nullptr ? load_w(bias, w_bf16, c + k) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) p = __fmaf_rn(load_w(w, w_bf16, (c + k) * W + i), to_f<T>(win[i].v[k]), p);
+        o[k] = silu_on ? silu(p) : p;
+    }
+    store_vec<T, V>(y + n * D + c, o);
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i)
+        *reinterpret_cast<Vec<T, V>*>(state_out + (n * (W - 1) + i) * D + c) = win[i + 1];
+}
+
+}  // namespace gdn

@@ -1,0 +1,167 @@
+// layer_common.cuh -- device helpers shared by the layer operators around the
+// recurrence (k_conv.cuh, k_norm.cuh, k_ssm.cuh, k_ssm_bwd.cuh).
+//
+// Unlike the CPR path these operators have no bitwise contract between their
+// entry points.  Their sums are fp32 in a fixed order, without atomics, so
+// repeated calls give the same bits.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "schedule.cuh"
+
+namespace gdn {
+
+// Element types: float, or bf16 widened exactly on load and rounded to
+// nearest-even once, on store.
+template <typename T>
+__device__ __forceinline__ float to_f(T x);
+template <>
+__device__ __forceinline__ float to_f<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+template <typename T>
+__device__ __forceinline__ T from_f(float x);
+template <>
+__device__ __forceinline__ float from_f<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// V consecutive elements as one memory access (V * sizeof(T) in {2, 4, 8, 16}).
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Vec {
+    T v[V];
+};
+
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> load_vec(const T* p)
+{
+    return *reinterpret_cast<const Vec<T, V>*>(p);
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_vec(T* p, const float* x)
+{
+    Vec<T, V> r;
+#pragma unroll
+    for (int i = 0; i < V; ++i) r.v[i] = from_f<T>(x[i]);
+    *reinterpret_cast<Vec<T, V>*>(p) = r;
+}
+
+// Weights and biases may be fp32 or bf16 whatever the tokens are.
+__device__ __forceinline__ float load_w(const void* w, int bf16, int64_t i)
+{
+    return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i]) : static_cast<const float*>(w)[i];
+}
+
+// The packed batch: sequence n holds rows [lo(n), hi(n)).  Offsets come from
+// device memory and are clamped to [0, T], so that no value of them makes an
+// access leave the tensors.  cu == nullptr: one sequence of T rows.
+struct Seqs {
+    const int32_t* cu;
+    int32_t N;
+    int64_t T;
+    __device__ __forceinline__ int64_t at(int n) const
+    {
+        if (cu == nullptr) return n == 0 ? 0 : T;
+        const int64_t c = cu[n];
+        return c < 0 ? 0 : (c > T ? T : c);
+    }
+    __device__ __forceinline__ int64_t lo(int n) const { return at(n); }
+    __device__ __forceinline__ int64_t hi(int n) const
+    {
+        const int64_t a = at(n), b = at(n + 1);
+        return b < a ? a : b;
+    }
+    // The last sequence that starts at or before row t; -1 if none does.
+    __device__ __forceinline__ int find(int64_t t) const
+    {
+        int a = -1, b = N;  // lo(a) <= t < lo(b)
+        while (b - a > 1) {
+            const int m = (a + b) >> 1;
+            if (at(m) <= t) a = m;
+            else b = m;
+        }
+        return a;
+    }
+    // Chunks of `len` tokens per sequence, numbered without a table: chunk c of
+    // sequence n is slot lo(n) / len + n + c.  Slots are distinct, because
+    // floor((a + L) / len) - floor(a / len) + 1 >= ceil(L / len), and lie below
+    // T / len + N.
+    __device__ __forceinline__ int64_t first_slot(int n, int64_t len) const { return lo(n) / len + n; }
+    __device__ __forceinline__ int find_slot(int64_t slot, int64_t len) const
+    {
+        int a = 0, b = N;
+        while (b - a > 1) {
+            const int m = (a + b) >> 1;
+            if (first_slot(m, len) <= slot) a = m;
+            else b = m;
+        }
+        return a;
+    }
+};
+
+// One block of a kernel checks the device offsets (0 <= cu[0], non-decreasing,
+// cu[N] <= T) and records the first error it sees.
+__device__ __forceinline__ void check_seqs(const Seqs& s, int32_t* status)
+{
+    if (status == nullptr || s.cu == nullptr) return;
+    for (int n = threadIdx.x; n <= s.N; n += blockDim.x) {
+        const int64_t c = s.cu[n];
+        const bool bad = c < 0 || c > s.T || (n > 0 && c < s.cu[n - 1]);
+        if (bad) atomicCAS(status, GDN_OK, GDN_ERR_DEVICE_INPUT);
+    }
+}
+
+// 2^x in one instruction.  Measured against the exact value over [-10, -1e-5]:
+// relative error at most 1.5e-7, 3e-8 to 6e-8 rms, and biased by 6e-9 (near 0)
+// to 5e-8, the same size as expf's.  A state that decays slowly multiplies
+// thousands of such factors close to 1, where the bias is the smallest.
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.0f, 1.0f + ex2(-kLog2e * v)); }
+
+// v * sigmoid(v) and its derivative
+__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.0f + ex2(-kLog2e * v)); }
+__device__ __forceinline__ float silu_grad(float v)
+{
+    const float s = sigmoid(v);
+    return s * __fmaf_rn(v, 1.0f - s, 1.0f);
+}
+
+// log(1 + e^v), accurate relative to its value on both sides
+__device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.0f) + log1pf(ex2(-kLog2e * fabsf(v))); }
+
+// Column sums out[map(m)] = sum_r in[r][m], r < R, m < M, in a fixed order: 8
+// row slices per block, each summed in ascending rows, then joined in order.
+// OutMap: m -> pointer to write (may be nullptr: not wanted).
+template <typename OutMap>
+__global__ void __launch_bounds__(256) k_colsum(const float* __restrict__ in, int64_t R, int64_t M, OutMap out)
+{
+    __shared__ float part[8][32];
+    const int64_t m = (int64_t)blockIdx.x * 32 + threadIdx.x;
+    float s = 0.0f;
+    if (m < M) {
+#pragma unroll 8
+        for (int64_t r = threadIdx.y; r < R; r += 8) s += in[r * M + m];
+    }
+    part[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.y == 0 && m < M) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) s += part[i][threadIdx.x];
+        out(m, s);
+    }
+}
+
+}  // namespace gdn

@@ -1,0 +1,727 @@
+// layer_ops.cu -- host side of the layer operators of gdn_cpr.h: the short
+// causal convolution, the selective state space scan and layer norm.
+//
+// As gdn_cpr.cu: it validates on the host, carves the caller's workspace and
+// enqueues on the caller's stream; it allocates nothing, keeps no state and
+// never synchronises.
+#include "gdn_cpr.h"
+#include "k_conv.cuh"
+#include "k_norm.cuh"
+#include "k_ssm.cuh"
+#include "k_ssm_bwd.cuh"
+
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+namespace {
+
+using gdn::Seqs;
+
+constexpr size_t kAlign = 256;
+
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+bool dtype_ok(gdn_dtype_t t) { return t == GDN_F32 || t == GDN_BF16; }
+size_t esize(gdn_dtype_t t) { return t == GDN_BF16 ? 2 : 4; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+bool launched() { return cudaGetLastError() == cudaSuccess; }
+
+int sm_count()
+{
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+        return 0;
+    return sms;
+}
+
+// A [rows, width] tensor with rows `stride` elements apart, as a byte range.
+struct Span {
+    uintptr_t lo, hi;
+    Span(const void* p, int64_t rows, int64_t stride, int64_t width, size_t esz)
+        : lo(reinterpret_cast<uintptr_t>(p)),
+          hi(p == nullptr || rows <= 0 ? lo : lo + (size_t)((rows - 1) * stride + width) * esz)
+    {
+    }
+    bool hits(const Span& o) const { return lo < o.hi && o.lo < hi; }
+};
+
+// 16-byte accesses: the row's address, stride and width are multiples of 16 bytes.
+bool wide(const void* p, int64_t stride, int64_t width, gdn_dtype_t t)
+{
+    const int64_t v = 16 / (int64_t)esize(t);
+    return p == nullptr || (aligned(p, 16) && stride % v == 0 && width % v == 0);
+}
+
+bool rows_ok(const void* p, int64_t stride, int64_t width, gdn_dtype_t t)
+{
+    return p != nullptr && stride >= width && stride <= INT64_MAX / 8 && aligned(p, esize(t));
+}
+
+// ------------------------------------------------------------------- convolution
+
+// Threads along the channels of a 128-thread block: a power of two that covers
+// the channels' vectors, so that narrow tensors fill their blocks with token runs.
+int conv_cx(int64_t nvec)
+{
+    int cx = 8;
+    while (cx < 128 && cx < nvec) cx *= 2;
+    return cx;
+}
+
+// Tokens per run.  A run reads W - 1 rows of its neighbour again and (backward)
+// leaves W + 1 partial sums per channel, so it is as long as 8 blocks of 128 threads
+// per SM allow, within [8, 64].
+int conv_run(int64_t T, int64_t nvec, int sms)
+{
+    const int64_t threads = (int64_t)sms * 1024;
+    const int64_t run = T * nvec / threads;
+    return (int)std::min<int64_t>(64, std::max<int64_t>(8, run / 8 * 8));
+}
+
+// Grid of the convolution kernels for V channels per thread; false if it does not fit.
+bool conv_grid(gdn::ConvArgs& a, int V, bool state_tiles, unsigned* blocks)
+{
+    const int sms = sm_count();
+    if (sms == 0) return false;
+    const int64_t nvec = ceil_div(a.D, V);
+    a.cx = conv_cx(nvec);
+    a.ncb = (int32_t)ceil_div(nvec, a.cx);
+    a.run = conv_run(a.s.T, nvec, sms);
+    const int ny = 128 / a.cx;
+    a.ntiles = ceil_div(a.s.T, (int64_t)a.run * ny);
+    const int64_t n = (a.ntiles + (state_tiles ? ceil_div(a.s.N, ny) : 0)) * a.ncb;
+    if (n > INT32_MAX) return false;
+    *blocks = (unsigned)n;
+    return true;
+}
+
+// Rows of partial weight gradients for any vector width and any number of SMs:
+// a tile holds at least 8 tokens.
+int64_t conv_tiles_max(int64_t T) { return ceil_div(T, 8); }
+
+template <typename T, int V>
+void launch_conv_fwd(const gdn::ConvArgs& a, int W, unsigned blocks, cudaStream_t st)
+{
+    if (W == 2) gdn::k_conv_fwd<T, 2, V><<<blocks, 128, 0, st>>>(a);
+    else if (W == 3) gdn::k_conv_fwd<T, 3, V><<<blocks, 128, 0, st>>>(a);
+    else gdn::k_conv_fwd<T, 4, V><<<blocks, 128, 0, st>>>(a);
+}
+
+template <typename T, int V>
+void launch_conv_bwd(const gdn::ConvArgs& a, int W, unsigned blocks, cudaStream_t st)
+{
+    const size_t sm = sizeof(float) * (W + 1) * V * 128;
+    if (W == 2) gdn::k_conv_bwd<T, 2, V><<<blocks, 128, sm, st>>>(a);
+    else if (W == 3) gdn::k_conv_bwd<T, 3, V><<<blocks, 128, sm, st>>>(a);
+    else gdn::k_conv_bwd<T, 4, V><<<blocks, 128, sm, st>>>(a);
+}
+
+template <typename T, int V>
+void launch_conv_step(const void* x, int64_t ldx, const void* w, const void* b, const void* s, void* so, int64_t N,
+                      int32_t D, int W, int silu, int wb, void* y, cudaStream_t st)
+{
+    const unsigned blocks = (unsigned)ceil_div(N * (D / V), 128);
+    const T *tx = static_cast<const T*>(x), *ts = static_cast<const T*>(s);
+    T *to = static_cast<T*>(so), *ty = static_cast<T*>(y);
+    if (W == 2) gdn::k_conv_step<T, 2, V><<<blocks, 128, 0, st>>>(tx, ldx, w, b, ts, to, N, D, silu, wb, ty);
+    else if (W == 3) gdn::k_conv_step<T, 3, V><<<blocks, 128, 0, st>>>(tx, ldx, w, b, ts, to, N, D, silu, wb, ty);
+    else gdn::k_conv_step<T, 4, V><<<blocks, 128, 0, st>>>(tx, ldx, w, b, ts, to, N, D, silu, wb, ty);
+}
+
+gdn_status_t conv_check(const void* x, int64_t x_stride, const void* weight, const void* bias, const void* state,
+                        const int32_t* cu, int32_t num_seqs, int64_t T, int32_t D, int32_t W, gdn_dtype_t in,
+                        gdn_dtype_t wt)
+{
+    if (num_seqs < 0 || T < 0 || T > INT32_MAX || D <= 0 || W <= 0) return GDN_ERR_INVALID_ARG;
+    if (!dtype_ok(in) || !dtype_ok(wt)) return GDN_ERR_INVALID_ARG;
+    if (W < 2 || W > 4) return GDN_ERR_UNSUPPORTED;
+    if (cu == nullptr && num_seqs != 1) return GDN_ERR_INVALID_ARG;
+    if (T > 0 && !rows_ok(x, x_stride, D, in)) return GDN_ERR_INVALID_ARG;
+    if (weight == nullptr || !aligned(weight, esize(wt)) || (bias && !aligned(bias, esize(wt))))
+        return GDN_ERR_INVALID_ARG;
+    if (state != nullptr && !aligned(state, 16)) return GDN_ERR_INVALID_ARG;
+    return GDN_OK;
+}
+
+// ------------------------------------------------------------------- layer norm
+
+struct NormPlan {
+    int V, NV, tpr, threads;
+    bool wide;  // one block per row, the row read again
+};
+
+// A row's threads: enough that a thread holds at most `most` vectors, in blocks
+// of at least 128 threads.
+NormPlan norm_plan(int32_t D, int V, int most, int max_threads)
+{
+    NormPlan p{};
+    const int64_t nvec = ceil_div(D, V);
+    p.V = V;
+    int tpr = 8;
+    while (tpr < max_threads && (int64_t)tpr * 2 <= nvec && tpr < 32) tpr *= 2;
+    while (tpr < max_threads && (int64_t)tpr * most < nvec) tpr *= 2;
+    p.tpr = tpr;
+    const int64_t nv = ceil_div(nvec, tpr);
+    p.NV = nv <= 1 ? 1 : nv <= 2 ? 2 : 4;
+    p.wide = nv > most;
+    p.threads = std::max(tpr, 128);
+    return p;
+}
+
+template <typename T, int V>
+bool launch_norm_fwd(const gdn::NormArgs& a, const NormPlan& p, cudaStream_t st)
+{
+    const int64_t blocks = ceil_div(a.R, p.threads / p.tpr);
+    if (p.NV == 1) gdn::k_norm_fwd<T, V, 1><<<(unsigned)blocks, p.threads, 0, st>>>(a);
+    else if (p.NV == 2) gdn::k_norm_fwd<T, V, 2><<<(unsigned)blocks, p.threads, 0, st>>>(a);
+    else gdn::k_norm_fwd<T, V, 4><<<(unsigned)blocks, p.threads, 0, st>>>(a);
+    return launched();
+}
+
+template <typename T, int V>
+bool launch_norm_bwd(const gdn::NormArgs& a, const NormPlan& p, unsigned blocks, cudaStream_t st)
+{
+    const size_t sm = sizeof(float) * (64 + (p.threads > p.tpr ? 2 * (size_t)a.D : 0));
+    if (p.NV == 1) gdn::k_norm_bwd<T, V, 1><<<blocks, p.threads, sm, st>>>(a);
+    else gdn::k_norm_bwd<T, V, 2><<<blocks, p.threads, sm, st>>>(a);
+    return launched();
+}
+
+constexpr int64_t kNormParts = 148 * 4;  // blocks that keep a share of dw and db
+int64_t norm_parts(int64_t rows) { return std::max<int64_t>(1, std::min<int64_t>(rows, kNormParts)); }
+
+// ------------------------------------------------------------------- scan
+
+// Tokens per chunk: enough chunks that `warps` warps are at work, at least
+// `least` tokens; T or more means that no sequence is cut.
+int64_t ssm_chunk(int64_t T, int32_t D, int32_t S, int channels_per_warp, int64_t least, int64_t warps)
+{
+    (void)S;
+    const int64_t across = ceil_div(D, channels_per_warp);
+    const int64_t chunks = std::max<int64_t>(1, warps / across);
+    const int64_t len = ceil_div(ceil_div(T, chunks), gdn::kSsmSave) * gdn::kSsmSave;
+    return std::max<int64_t>(len, least);
+}
+
+constexpr int64_t kSsmWarps = 148 * 8;
+constexpr int64_t kSsmLeast = 64;
+
+int64_t ssm_fwd_chunk(int64_t T, int32_t D, int32_t S) { return ssm_chunk(T, D, S, 4 * 128 / S, kSsmLeast, kSsmWarps); }
+int64_t ssm_bwd_chunk(int64_t T, int32_t D, int32_t S) { return ssm_chunk(T, D, S, 2 * 128 / S, kSsmLeast, kSsmWarps); }
+
+struct SsmWorkspace {
+    float *hbuf, *dsum, *partA, *partD, *partBC;
+    size_t bytes;
+};
+
+SsmWorkspace ssm_carve(void* base, int64_t T, int32_t N, int32_t D, int32_t G, int32_t S, bool backward)
+{
+    SsmWorkspace w{};
+    size_t off = 0;
+    char* b = static_cast<char*>(base);
+    auto take = [&](size_t floats) {
+        float* p = b != nullptr ? reinterpret_cast<float*>(b + off) : nullptr;
+        off = align_up(off + sizeof(float) * floats);
+        return p;
+    };
+    const int64_t Lc = backward ? ssm_bwd_chunk(T, D, S) : ssm_fwd_chunk(T, D, S);
+    const size_t slots = (size_t)(T / Lc + N), per = (size_t)D * S;
+    if (T > Lc) {
+        w.hbuf = take(slots * per);
+        w.dsum = take(slots * D);
+    }
+    if (backward) {
+        const int64_t cpg = ceil_div(D / G, 2 * 128 / S * 4);
+        w.partA = take(slots * per);
+        w.partD = take(slots * 2 * D);
+        w.partBC = take((size_t)cpg * T * G * 2 * S);
+    }
+    w.bytes = std::max<size_t>(off, kAlign);
+    return w;
+}
+
+gdn_status_t ssm_check(const gdn_ssm_t* s, bool step)
+{
+    if (s == nullptr) return GDN_ERR_INVALID_ARG;
+    if (s->num_seqs < 0 || s->total_tokens < 0 || s->total_tokens > INT32_MAX || s->channels <= 0 || s->groups <= 0 ||
+        s->states <= 0 || s->channels % s->groups != 0)
+        return GDN_ERR_INVALID_ARG;
+    if (!dtype_ok(s->in_dtype)) return GDN_ERR_INVALID_ARG;
+    if (s->states != 16 && s->states != 32 && s->states != 64) return GDN_ERR_UNSUPPORTED;
+    if (s->A == nullptr || !aligned(s->A, 16)) return GDN_ERR_INVALID_ARG;
+    if ((s->D && !aligned(s->D, 4)) || (s->dt_bias && !aligned(s->dt_bias, 4))) return GDN_ERR_INVALID_ARG;
+    if (step ? s->total_tokens != s->num_seqs : (s->cu_seqlens == nullptr && s->num_seqs != 1))
+        return GDN_ERR_INVALID_ARG;
+    if (s->total_tokens > 0) {
+        const int64_t bc = (int64_t)s->groups * s->states;
+        if (!rows_ok(s->x, s->x_stride, s->channels, s->in_dtype) ||
+            !rows_ok(s->dt, s->dt_stride, s->channels, s->in_dtype) || !rows_ok(s->B, s->B_stride, bc, s->in_dtype) ||
+            !rows_ok(s->C, s->C_stride, bc, s->in_dtype) ||
+            (s->z != nullptr && !rows_ok(s->z, s->z_stride, s->channels, s->in_dtype)))
+            return GDN_ERR_INVALID_ARG;
+    }
+    return GDN_OK;
+}
+
+gdn::SsmArgs ssm_args(const gdn_ssm_t* s, int64_t Lc, int block_channels)
+{
+    gdn::SsmArgs a{};
+    a.s = Seqs{s->cu_seqlens, s->num_seqs, s->total_tokens};
+    a.x = s->x; a.dt = s->dt; a.z = s->z; a.B = s->B; a.C = s->C;
+    a.ldx = s->x_stride; a.lddt = s->dt_stride; a.ldz = s->z_stride; a.ldB = s->B_stride; a.ldC = s->C_stride;
+    a.A = s->A; a.Dp = s->D; a.dt_bias = s->dt_bias;
+    a.D = s->channels; a.G = s->groups; a.Dg = s->channels / s->groups;
+    a.cpg = (int32_t)ceil_div(a.Dg, block_channels);
+    a.softplus = s->delta_softplus != 0;
+    a.Lc = Lc;
+    return a;
+}
+
+// All token tensors in 16-byte accesses (a group's channels have to be whole vectors).
+bool ssm_wide(const gdn_ssm_t* s)
+{
+    const int64_t Dg = s->channels / s->groups;
+    const int64_t v = 16 / (int64_t)esize(s->in_dtype);
+    return Dg % v == 0 && wide(s->x, s->x_stride, Dg, s->in_dtype) && wide(s->dt, s->dt_stride, Dg, s->in_dtype) &&
+           wide(s->z, s->z_stride, Dg, s->in_dtype);
+}
+
+template <typename T, int S, int V>
+gdn_status_t ssm_forward_launch(gdn::SsmArgs a, cudaStream_t st)
+{
+    const int64_t slots = a.s.T / a.Lc + a.s.N, nb = (int64_t)a.G * a.cpg;
+    if (slots * nb > INT32_MAX) return GDN_ERR_INVALID_ARG;
+    const unsigned blocks = (unsigned)(slots * nb);
+    if (a.s.T > a.Lc) {
+        gdn::k_ssm_scan<T, S, V, 1><<<blocks, gdn::kSsmThreads, 0, st>>>(a);
+        const int64_t ids = (int64_t)a.s.N * a.D * (S / 4);
+        gdn::k_ssm_pass<S><<<(unsigned)ceil_div(ids, 128), 128, 0, st>>>(a);
+    }
+    gdn::k_ssm_scan<T, S, V, 0><<<blocks, gdn::kSsmThreads, 0, st>>>(a);
+    return launched() ? GDN_OK : GDN_ERR_CUDA;
+}
+
+template <typename T, int S, int V>
+gdn_status_t ssm_backward_launch(const gdn::SsmBwdArgs& b, int scan_cpg, void* dB, void* dC, float* dA, float* dD,
+                                 float* ddt_bias, cudaStream_t st)
+{
+    const gdn::SsmArgs& a = b.f;
+    const int64_t slots = a.s.T / a.Lc + a.s.N;
+    if (slots * a.G * std::max(a.cpg, scan_cpg) > INT32_MAX) return GDN_ERR_INVALID_ARG;
+    if (a.s.T > a.Lc) {
+        gdn::SsmArgs r = a;  // the reverse scan: x is dy, B is C
+        r.x = b.dy;
+        r.ldx = b.lddy;
+        r.B = a.C;
+        r.ldB = a.ldC;
+        r.cpg = scan_cpg;
+        gdn::k_ssm_scan<T, S, V, 2><<<(unsigned)(slots * a.G * scan_cpg), gdn::kSsmThreads, 0, st>>>(r);
+        const int64_t ids = (int64_t)a.s.N * a.D * (S / 4);
+        gdn::k_ssm_bwd_pass<S><<<(unsigned)ceil_div(ids, 128), 128, 0, st>>>(a, b.dstate_out);
+    }
+    constexpr size_t sm = gdn::SsmBwdCfg<S>::SMEM;
+    auto k = a.z != nullptr ? gdn::k_ssm_bwd<T, S, V, true> : gdn::k_ssm_bwd<T, S, V, false>;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm) != cudaSuccess)
+        return GDN_ERR_CUDA;
+    k<<<(unsigned)(slots * a.G * a.cpg), gdn::kSsmThreads, sm, st>>>(b);
+    if (a.s.T > 0) {
+        const int64_t ids = a.s.T * a.G * 2 * S;
+        gdn::k_ssm_dbc<T, S><<<(unsigned)ceil_div(ids, 256), 256, 0, st>>>(a.s, b.partBC, a.G, a.cpg,
+                                                                           static_cast<T*>(dB), static_cast<T*>(dC));
+    }
+    const dim3 blk(32, 8);
+    const int64_t mA = (int64_t)a.D * S, mD = 2 * (int64_t)a.D;
+    gdn::k_colsum<<<(unsigned)ceil_div(mA, 32), blk, 0, st>>>(b.partA, slots, mA, gdn::PlainMap{dA});
+    if (dD != nullptr || ddt_bias != nullptr)
+        gdn::k_colsum<<<(unsigned)ceil_div(mD, 32), blk, 0, st>>>(b.partD, slots, mD,
+                                                                  gdn::SsmGradMap{dD, ddt_bias, a.D});
+    return launched() ? GDN_OK : GDN_ERR_CUDA;
+}
+
+// in_dtype, states and vector width as template arguments of f<T, S, V>(...)
+#define SSM_DISPATCH(f, in_dtype, states, is_wide, ...)                                                        \
+    do {                                                                                                       \
+        if ((in_dtype) == GDN_BF16) {                                                                          \
+            if ((states) == 16) return (is_wide) ? f<__nv_bfloat16, 16, 8>(__VA_ARGS__) : f<__nv_bfloat16, 16, 1>(__VA_ARGS__); \
+            if ((states) == 32) return (is_wide) ? f<__nv_bfloat16, 32, 8>(__VA_ARGS__) : f<__nv_bfloat16, 32, 1>(__VA_ARGS__); \
+            return (is_wide) ? f<__nv_bfloat16, 64, 8>(__VA_ARGS__) : f<__nv_bfloat16, 64, 1>(__VA_ARGS__);    \
+        }                                                                                                      \
+        if ((states) == 16) return (is_wide) ? f<float, 16, 4>(__VA_ARGS__) : f<float, 16, 1>(__VA_ARGS__);    \
+        if ((states) == 32) return (is_wide) ? f<float, 32, 4>(__VA_ARGS__) : f<float, 32, 1>(__VA_ARGS__);    \
+        return (is_wide) ? f<float, 64, 4>(__VA_ARGS__) : f<float, 64, 1>(__VA_ARGS__);                        \
+    } while (0)
+
+template <typename T, int S>
+gdn_status_t ssm_step_launch(const gdn::SsmArgs& a, cudaStream_t st)
+{
+    const int64_t blocks = ceil_div((int64_t)a.s.N * a.D * (S / 4), 256);
+    if (blocks > INT32_MAX) return GDN_ERR_INVALID_ARG;
+    gdn::k_ssm_step<T, S><<<(unsigned)blocks, 256, 0, st>>>(a);
+    return launched() ? GDN_OK : GDN_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+gdn_status_t gdn_conv_forward(const void* x, int64_t x_stride, const void* weight, const void* bias,
+                              const void* state_in, const int32_t* cu_seqlens, int32_t num_seqs,
+                              int64_t total_tokens, int32_t channels, int32_t width, int32_t silu,
+                              gdn_dtype_t in_dtype, gdn_dtype_t w_dtype, void* y, void* state_out, int32_t* status,
+                              void* stream)
+{
+    const gdn_status_t bad = conv_check(x, x_stride, weight, bias, state_in, cu_seqlens, num_seqs, total_tokens,
+                                        channels, width, in_dtype, w_dtype);
+    if (bad != GDN_OK) return bad;
+    if (num_seqs == 0) return GDN_OK;
+    if (state_out == nullptr || !aligned(state_out, 16)) return GDN_ERR_INVALID_ARG;
+    if (total_tokens > 0 && !rows_ok(y, channels, channels, in_dtype)) return GDN_ERR_INVALID_ARG;
+    const size_t es = esize(in_dtype);
+    const Span sx(x, total_tokens, x_stride, channels, es), sy(y, total_tokens, channels, channels, es);
+    const Span si(state_in, (int64_t)num_seqs * (width - 1), channels, channels, es);
+    const Span so(state_out, (int64_t)num_seqs * (width - 1), channels, channels, es);
+    if (sx.hits(sy) || sx.hits(so) || si.hits(sy) || si.hits(so) || sy.hits(so)) return GDN_ERR_INVALID_ARG;
+    gdn::ConvArgs a{};
+    a.s = Seqs{cu_seqlens, num_seqs, total_tokens};
+    a.x = x; a.ldx = x_stride; a.w = weight; a.bias = bias; a.state_in = state_in;
+    a.D = channels; a.silu = silu != 0; a.w_bf16 = w_dtype == GDN_BF16;
+    a.y = y; a.state_out = state_out; a.status = status;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool v16 = wide(x, x_stride, channels, in_dtype) && wide(y, channels, channels, in_dtype);
+    const int V = v16 ? (int)(16 / es) : 1;
+    unsigned blocks = 0;
+    if (!conv_grid(a, V, true, &blocks)) return GDN_ERR_INVALID_ARG;
+    if (in_dtype == GDN_BF16) {
+        if (v16) launch_conv_fwd<__nv_bfloat16, 8>(a, width, blocks, st);
+        else launch_conv_fwd<__nv_bfloat16, 1>(a, width, blocks, st);
+    } else {
+        if (v16) launch_conv_fwd<float, 4>(a, width, blocks, st);
+        else launch_conv_fwd<float, 1>(a, width, blocks, st);
+    }
+    return launched() ? GDN_OK : GDN_ERR_CUDA;
+}
+
+size_t gdn_conv_backward_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t channels, int32_t width)
+{
+    if (total_tokens < 0 || num_seqs < 0 || channels <= 0 || width < 2 || width > 4) return 0;
+    return align_up(sizeof(float) * (size_t)std::max<int64_t>(1, conv_tiles_max(total_tokens)) * (width + 1) *
+                    channels);
+}
+
+gdn_status_t gdn_conv_backward(const void* x, int64_t x_stride, const void* weight, const void* bias,
+                               const void* state_in, const void* dy, int64_t dy_stride, const float* dstate_out,
+                               const int32_t* cu_seqlens, int32_t num_seqs, int64_t total_tokens, int32_t channels,
+                               int32_t width, int32_t silu, gdn_dtype_t in_dtype, gdn_dtype_t w_dtype, void* dx,
+                               float* dweight, float* dbias, float* dstate_in, void* workspace,
+                               size_t workspace_bytes, int32_t* status, void* stream)
+{
+    const gdn_status_t bad = conv_check(x, x_stride, weight, bias, state_in, cu_seqlens, num_seqs, total_tokens,
+                                        channels, width, in_dtype, w_dtype);
+    if (bad != GDN_OK) return bad;
+    if (dweight == nullptr || !aligned(dweight, 16) || (dbias && !aligned(dbias, 16))) return GDN_ERR_INVALID_ARG;
+    if (num_seqs > 0 && (dstate_in == nullptr || !aligned(dstate_in, 16))) return GDN_ERR_INVALID_ARG;
+    if (dstate_out != nullptr && !aligned(dstate_out, 16)) return GDN_ERR_INVALID_ARG;
+    if (total_tokens > 0 && (!rows_ok(dy, dy_stride, channels, in_dtype) || !rows_ok(dx, channels, channels, in_dtype)))
+        return GDN_ERR_INVALID_ARG;
+    const size_t es = esize(in_dtype);
+    const Span sx(x, total_tokens, x_stride, channels, es), sg(dy, total_tokens, dy_stride, channels, es);
+    const Span sd(dx, total_tokens, channels, channels, es);
+    if (sd.hits(sx) || sd.hits(sg)) return GDN_ERR_INVALID_ARG;
+    if (workspace == nullptr ||
+        workspace_bytes < gdn_conv_backward_workspace_size(total_tokens, num_seqs, channels, width))
+        return GDN_ERR_WORKSPACE;
+    if (!aligned(workspace, kAlign)) return GDN_ERR_INVALID_ARG;
+    gdn::ConvArgs a{};
+    a.s = Seqs{cu_seqlens, num_seqs, num_seqs > 0 ? total_tokens : 0};
+    a.x = x; a.ldx = x_stride; a.w = weight; a.bias = bias; a.state_in = state_in;
+    a.D = channels; a.silu = silu != 0; a.w_bf16 = w_dtype == GDN_BF16;
+    a.dy = dy; a.lddy = dy_stride; a.dstate_out = dstate_out; a.dx = dx; a.dstate_in = dstate_in;
+    a.part = static_cast<float*>(workspace);
+    a.status = status;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool v4 = wide(x, x_stride, channels, in_dtype) && wide(dy, dy_stride, channels, in_dtype) &&
+                    wide(dx, channels, channels, in_dtype);
+    unsigned blocks = 0;
+    if (!conv_grid(a, v4 ? 4 : 1, true, &blocks)) return GDN_ERR_INVALID_ARG;
+    if (blocks > 0) {
+        if (in_dtype == GDN_BF16) {
+            if (v4) launch_conv_bwd<__nv_bfloat16, 4>(a, width, blocks, st);
+            else launch_conv_bwd<__nv_bfloat16, 1>(a, width, blocks, st);
+        } else {
+            if (v4) launch_conv_bwd<float, 4>(a, width, blocks, st);
+            else launch_conv_bwd<float, 1>(a, width, blocks, st);
+        }
+    }
+    const int64_t M = (int64_t)channels * (width + 1);
+    gdn::k_colsum<<<(unsigned)ceil_div(M, 32), dim3(32, 8), 0, st>>>(a.part, a.ntiles, M,
+                                                                     gdn::ConvGradMap{dweight, dbias, channels, width});
+    return launched() ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn_status_t gdn_conv_step(const void* x, int64_t x_stride, const void* weight, const void* bias, const void* state,
+                           void* state_out, int32_t num_seqs, int32_t channels, int32_t width, int32_t silu,
+                           gdn_dtype_t in_dtype, gdn_dtype_t w_dtype, void* y, void* stream)
+{
+    static const int32_t none = 0;  // conv_check wants offsets for num_seqs != 1; the step reads none
+    const gdn_status_t bad =
+        conv_check(x, x_stride, weight, bias, state, &none, num_seqs, num_seqs, channels, width, in_dtype, w_dtype);
+    if (bad != GDN_OK) return bad;
+    if (num_seqs == 0) return GDN_OK;
+    if (state == nullptr || state_out == nullptr || !aligned(state_out, 16) || !rows_ok(y, channels, channels, in_dtype))
+        return GDN_ERR_INVALID_ARG;
+    const size_t es = esize(in_dtype);
+    const Span sx(x, num_seqs, x_stride, channels, es), sy(y, num_seqs, channels, channels, es);
+    const Span si(state, (int64_t)num_seqs * (width - 1), channels, channels, es);
+    const Span so(state_out, (int64_t)num_seqs * (width - 1), channels, channels, es);
+    if (sx.hits(sy) || sx.hits(so) || sy.hits(si) || sy.hits(so) || (state != state_out && si.hits(so)))
+        return GDN_ERR_INVALID_ARG;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool v16 = wide(x, x_stride, channels, in_dtype) && wide(y, channels, channels, in_dtype);
+    if (ceil_div((int64_t)num_seqs * (channels / (v16 ? 16 / (int)es : 1)), 128) > INT32_MAX) return GDN_ERR_INVALID_ARG;
+    const int wb = w_dtype == GDN_BF16, sl = silu != 0;
+    if (in_dtype == GDN_BF16) {
+        if (v16) launch_conv_step<__nv_bfloat16, 8>(x, x_stride, weight, bias, state, state_out, num_seqs, channels, width, sl, wb, y, st);
+        else launch_conv_step<__nv_bfloat16, 1>(x, x_stride, weight, bias, state, state_out, num_seqs, channels, width, sl, wb, y, st);
+    } else {
+        if (v16) launch_conv_step<float, 4>(x, x_stride, weight, bias, state, state_out, num_seqs, channels, width, sl, wb, y, st);
+        else launch_conv_step<float, 1>(x, x_stride, weight, bias, state, state_out, num_seqs, channels, width, sl, wb, y, st);
+    }
+    return launched() ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn_status_t gdn_layer_norm_forward(const void* x, int64_t x_stride, const void* weight, const void* bias, float eps,
+                                    int64_t rows, int32_t width, gdn_dtype_t in_dtype, gdn_dtype_t w_dtype, void* y,
+                                    float* mean, float* rstd, void* stream)
+{
+    if (rows < 0 || rows > INT32_MAX || width <= 0 || !(eps >= 0.0f) || !dtype_ok(in_dtype) || !dtype_ok(w_dtype))
+        return GDN_ERR_INVALID_ARG;
+    if (weight == nullptr || !aligned(weight, esize(w_dtype)) || (bias && !aligned(bias, esize(w_dtype))))
+        return GDN_ERR_INVALID_ARG;
+    if (rows == 0) return GDN_OK;
+    if (!rows_ok(x, x_stride, width, in_dtype) || !rows_ok(y, width, width, in_dtype) || mean == nullptr ||
+        rstd == nullptr || !aligned(mean, 4) || !aligned(rstd, 4))
+        return GDN_ERR_INVALID_ARG;
+    const size_t es = esize(in_dtype);
+    if (Span(x, rows, x_stride, width, es).hits(Span(y, rows, width, width, es))) return GDN_ERR_INVALID_ARG;
+    gdn::NormArgs a{};
+    a.x = x; a.ldx = x_stride; a.w = weight; a.b = bias; a.w_bf16 = w_dtype == GDN_BF16;
+    a.eps = eps; a.R = rows; a.D = width; a.y = y; a.mean = mean; a.rstd = rstd;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool v16 = wide(x, x_stride, width, in_dtype) && wide(y, width, width, in_dtype);
+    const NormPlan p = norm_plan(width, v16 ? (int)(16 / es) : 1, 4, gdn::kNormMaxThreads);
+    a.tpr = p.tpr;
+    if (p.wide) {
+        if (in_dtype == GDN_BF16) gdn::k_norm_fwd_wide<__nv_bfloat16><<<(unsigned)rows, 1024, 0, st>>>(a);
+        else gdn::k_norm_fwd_wide<float><<<(unsigned)rows, 1024, 0, st>>>(a);
+        return launched() ? GDN_OK : GDN_ERR_CUDA;
+    }
+    bool ok;
+    if (in_dtype == GDN_BF16) ok = v16 ? launch_norm_fwd<__nv_bfloat16, 8>(a, p, st) : launch_norm_fwd<__nv_bfloat16, 1>(a, p, st);
+    else ok = v16 ? launch_norm_fwd<float, 4>(a, p, st) : launch_norm_fwd<float, 1>(a, p, st);
+    return ok ? GDN_OK : GDN_ERR_CUDA;
+}
+
+size_t gdn_layer_norm_backward_workspace_size(int64_t rows, int32_t width)
+{
+    if (rows < 0 || width <= 0) return 0;
+    return align_up(sizeof(float) * 2 * (size_t)norm_parts(rows) * width);
+}
+
+gdn_status_t gdn_layer_norm_backward(const void* x, int64_t x_stride, const void* dy, int64_t dy_stride,
+                                     const void* weight, const float* mean, const float* rstd, int64_t rows,
+                                     int32_t width, gdn_dtype_t in_dtype, gdn_dtype_t w_dtype, void* dx,
+                                     float* dweight, float* dbias, void* workspace, size_t workspace_bytes,
+                                     void* stream)
+{
+    if (rows < 0 || rows > INT32_MAX || width <= 0 || !dtype_ok(in_dtype) || !dtype_ok(w_dtype))
+        return GDN_ERR_INVALID_ARG;
+    if (weight == nullptr || !aligned(weight, esize(w_dtype)) || dweight == nullptr || !aligned(dweight, 4) ||
+        (dbias && !aligned(dbias, 4)))
+        return GDN_ERR_INVALID_ARG;
+    if (rows > 0 && (!rows_ok(x, x_stride, width, in_dtype) || !rows_ok(dy, dy_stride, width, in_dtype) ||
+                     !rows_ok(dx, width, width, in_dtype) || mean == nullptr || rstd == nullptr))
+        return GDN_ERR_INVALID_ARG;
+    const size_t es = esize(in_dtype);
+    const Span sd(dx, rows, width, width, es);
+    if (sd.hits(Span(x, rows, x_stride, width, es)) || sd.hits(Span(dy, rows, dy_stride, width, es)))
+        return GDN_ERR_INVALID_ARG;
+    if (workspace == nullptr || workspace_bytes < gdn_layer_norm_backward_workspace_size(rows, width))
+        return GDN_ERR_WORKSPACE;
+    if (!aligned(workspace, kAlign)) return GDN_ERR_INVALID_ARG;
+    gdn::NormArgs a{};
+    a.x = x; a.ldx = x_stride; a.dy = dy; a.lddy = dy_stride; a.w = weight; a.w_bf16 = w_dtype == GDN_BF16;
+    a.R = rows; a.D = width; a.dx = dx;
+    a.mean = const_cast<float*>(mean); a.rstd = const_cast<float*>(rstd);
+    a.part = static_cast<float*>(workspace);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool v16 = wide(x, x_stride, width, in_dtype) && wide(dy, dy_stride, width, in_dtype) &&
+                     wide(dx, width, width, in_dtype);
+    const NormPlan p = norm_plan(width, v16 ? (int)(16 / es) : 1, 2, gdn::kNormBwdThreads);
+    a.tpr = p.tpr;
+    int64_t parts = 0;
+    if (rows > 0 && p.wide) {
+        parts = std::min<int64_t>(rows, 64);
+        const dim3 grid((unsigned)ceil_div(width, 256), (unsigned)parts);
+        if (in_dtype == GDN_BF16) {
+            gdn::k_norm_bwd_wide<__nv_bfloat16><<<(unsigned)rows, 1024, 0, st>>>(a);
+            gdn::k_norm_bwd_wide_w<__nv_bfloat16><<<grid, 256, 0, st>>>(a);
+        } else {
+            gdn::k_norm_bwd_wide<float><<<(unsigned)rows, 1024, 0, st>>>(a);
+            gdn::k_norm_bwd_wide_w<float><<<grid, 256, 0, st>>>(a);
+        }
+        if (!launched()) return GDN_ERR_CUDA;
+    } else if (rows > 0) {
+        parts = std::min<int64_t>(ceil_div(rows, p.threads / p.tpr), norm_parts(rows));
+        bool ok;
+        if (in_dtype == GDN_BF16)
+            ok = v16 ? launch_norm_bwd<__nv_bfloat16, 8>(a, p, (unsigned)parts, st)
+                     : launch_norm_bwd<__nv_bfloat16, 1>(a, p, (unsigned)parts, st);
+        else
+            ok = v16 ? launch_norm_bwd<float, 4>(a, p, (unsigned)parts, st)
+                     : launch_norm_bwd<float, 1>(a, p, (unsigned)parts, st);
+        if (!ok) return GDN_ERR_CUDA;
+    }
+    const int64_t M = 2 * (int64_t)width;
+    gdn::k_colsum<<<(unsigned)ceil_div(M, 32), dim3(32, 8), 0, st>>>(a.part, parts, M,
+                                                                     gdn::NormGradMap{dweight, dbias, width});
+    return launched() ? GDN_OK : GDN_ERR_CUDA;
+}
+
+int64_t gdn_ssm_num_chunk_states(int64_t total_tokens, int32_t num_seqs)
+{
+    if (total_tokens < 0 || total_tokens > INT32_MAX || num_seqs < 0) return -1;
+    return total_tokens / GDN_SSM_CHUNK + num_seqs;
+}
+
+size_t gdn_ssm_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t channels, int32_t states)
+{
+    if (total_tokens < 0 || num_seqs < 0 || channels <= 0 || (states != 16 && states != 32 && states != 64)) return 0;
+    return ssm_carve(nullptr, total_tokens, num_seqs, channels, 1, states, false).bytes;
+}
+
+size_t gdn_ssm_backward_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t channels, int32_t groups,
+                                       int32_t states)
+{
+    if (total_tokens < 0 || num_seqs < 0 || channels <= 0 || groups <= 0 || channels % groups != 0 ||
+        (states != 16 && states != 32 && states != 64))
+        return 0;
+    return ssm_carve(nullptr, total_tokens, num_seqs, channels, groups, states, true).bytes;
+}
+
+gdn_status_t gdn_ssm_forward(const gdn_ssm_t* args, const float* state_in, void* y, float* state_out,
+                             float* chunk_states, void* workspace, size_t workspace_bytes, int32_t* status,
+                             void* stream)
+{
+    const gdn_status_t bad = ssm_check(args, false);
+    if (bad != GDN_OK) return bad;
+    const gdn_ssm_t& s = *args;
+    if (s.num_seqs == 0) return GDN_OK;
+    if (state_out == nullptr || !aligned(state_out, 16) || (state_in && !aligned(state_in, 16)) ||
+        (chunk_states && !aligned(chunk_states, 16)))
+        return GDN_ERR_INVALID_ARG;
+    if (s.total_tokens > 0 && !rows_ok(y, s.channels, s.channels, s.in_dtype)) return GDN_ERR_INVALID_ARG;
+    const size_t es = esize(s.in_dtype);
+    const int64_t T = s.total_tokens, per = (int64_t)s.channels * s.states;
+    const Span sy(y, T, s.channels, s.channels, es), so(state_out, s.num_seqs, per, per, 4);
+    if (sy.hits(Span(s.x, T, s.x_stride, s.channels, es)) || sy.hits(Span(s.dt, T, s.dt_stride, s.channels, es)) ||
+        sy.hits(Span(s.z, T, s.z_stride, s.channels, es)) || so.hits(Span(state_in, s.num_seqs, per, per, 4)))
+        return GDN_ERR_INVALID_ARG;
+    if (workspace == nullptr || workspace_bytes < gdn_ssm_workspace_size(T, s.num_seqs, s.channels, s.states))
+        return GDN_ERR_WORKSPACE;
+    if (!aligned(workspace, kAlign)) return GDN_ERR_INVALID_ARG;
+    const SsmWorkspace w = ssm_carve(workspace, T, s.num_seqs, s.channels, 1, s.states, false);
+    gdn::SsmArgs a = ssm_args(args, ssm_fwd_chunk(T, s.channels, s.states), 4 * 128 / s.states * 4);
+    a.state_in = state_in; a.y = y; a.state_out = state_out; a.saved = chunk_states;
+    a.hbuf = w.hbuf; a.dsum = w.dsum; a.status = status;
+    const bool v16 = ssm_wide(args) && aligned(y, 16);
+    SSM_DISPATCH(ssm_forward_launch, s.in_dtype, s.states, v16, a, static_cast<cudaStream_t>(stream));
+}
+
+gdn_status_t gdn_ssm_backward(const gdn_ssm_t* args, const void* dy, int64_t dy_stride, const float* chunk_states,
+                              const float* dstate_out, void* dx, void* ddt, float* dA, void* dB, void* dC, float* dD,
+                              void* dz, float* ddt_bias, float* dstate_in, void* workspace, size_t workspace_bytes,
+                              int32_t* status, void* stream)
+{
+    const gdn_status_t bad = ssm_check(args, false);
+    if (bad != GDN_OK) return bad;
+    const gdn_ssm_t& s = *args;
+    const int64_t T = s.num_seqs > 0 ? s.total_tokens : 0;
+    if (dA == nullptr || !aligned(dA, 4) || (dD && !aligned(dD, 4)) || (ddt_bias && !aligned(ddt_bias, 4)))
+        return GDN_ERR_INVALID_ARG;
+    if (s.num_seqs > 0 && (chunk_states == nullptr || !aligned(chunk_states, 16) || dstate_in == nullptr ||
+                           !aligned(dstate_in, 16) || (dstate_out && !aligned(dstate_out, 16))))
+        return GDN_ERR_INVALID_ARG;
+    if (T > 0 && (!rows_ok(dy, dy_stride, s.channels, s.in_dtype) || !rows_ok(dx, s.channels, s.channels, s.in_dtype) ||
+                  !rows_ok(ddt, s.channels, s.channels, s.in_dtype) || dB == nullptr || dC == nullptr ||
+                  (s.z != nullptr && !rows_ok(dz, s.channels, s.channels, s.in_dtype))))
+        return GDN_ERR_INVALID_ARG;
+    const size_t es = esize(s.in_dtype);
+    const int64_t bc = (int64_t)s.groups * s.states;
+    const Span in[] = {Span(s.x, T, s.x_stride, s.channels, es), Span(s.dt, T, s.dt_stride, s.channels, es),
+                       Span(s.z, T, s.z_stride, s.channels, es), Span(dy, T, dy_stride, s.channels, es),
+                       Span(s.B, T, s.B_stride, bc, es), Span(s.C, T, s.C_stride, bc, es)};
+    const Span out[] = {Span(dx, T, s.channels, s.channels, es), Span(ddt, T, s.channels, s.channels, es),
+                        Span(s.z ? dz : nullptr, T, s.channels, s.channels, es), Span(dB, T, bc, bc, es),
+                        Span(dC, T, bc, bc, es)};
+    for (const Span& i : in)
+        for (const Span& o : out)
+            if (i.hits(o)) return GDN_ERR_INVALID_ARG;
+    if (workspace == nullptr ||
+        workspace_bytes < gdn_ssm_backward_workspace_size(s.total_tokens, s.num_seqs, s.channels, s.groups, s.states))
+        return GDN_ERR_WORKSPACE;
+    if (!aligned(workspace, kAlign)) return GDN_ERR_INVALID_ARG;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (s.num_seqs == 0) {  // no token, no state: the parameters' gradients are zero
+        if (cudaMemsetAsync(dA, 0, sizeof(float) * (size_t)s.channels * s.states, st) != cudaSuccess ||
+            (dD && cudaMemsetAsync(dD, 0, sizeof(float) * (size_t)s.channels, st) != cudaSuccess) ||
+            (ddt_bias && cudaMemsetAsync(ddt_bias, 0, sizeof(float) * (size_t)s.channels, st) != cudaSuccess))
+            return GDN_ERR_CUDA;
+        return GDN_OK;
+    }
+    const SsmWorkspace w = ssm_carve(workspace, T, s.num_seqs, s.channels, s.groups, s.states, true);
+    const int64_t Lc = ssm_bwd_chunk(T, s.channels, s.states);
+    gdn::SsmBwdArgs b{};
+    b.f = ssm_args(args, Lc, 2 * 128 / s.states * 4);
+    b.f.saved = const_cast<float*>(chunk_states);
+    b.f.hbuf = w.hbuf; b.f.dsum = w.dsum; b.f.status = status;
+    b.dy = dy; b.lddy = dy_stride; b.dstate_out = dstate_out;
+    b.dx = dx; b.ddt = ddt; b.dz = dz; b.dstate_in = dstate_in;
+    b.partA = w.partA; b.partD = w.partD; b.partBC = w.partBC;
+    const int scan_cpg = (int)ceil_div(b.f.Dg, 4 * 128 / s.states * 4);
+    const bool v16 = ssm_wide(args) && wide(dy, dy_stride, b.f.Dg, s.in_dtype) && aligned(dx, 16) && aligned(ddt, 16) &&
+                     (s.z == nullptr || aligned(dz, 16));
+    SSM_DISPATCH(ssm_backward_launch, s.in_dtype, s.states, v16, b, scan_cpg, dB, dC, dA, dD, ddt_bias, st);
+}
+
+gdn_status_t gdn_ssm_step(const gdn_ssm_t* args, const float* state, float* state_out, void* y, void* stream)
+{
+    const gdn_status_t bad = ssm_check(args, true);
+    if (bad != GDN_OK) return bad;
+    const gdn_ssm_t& s = *args;
+    if (s.num_seqs == 0) return GDN_OK;
+    if (state == nullptr || state_out == nullptr || !aligned(state, 16) || !aligned(state_out, 16) ||
+        !rows_ok(y, s.channels, s.channels, s.in_dtype))
+        return GDN_ERR_INVALID_ARG;
+    const size_t es = esize(s.in_dtype);
+    const int64_t N = s.num_seqs, per = (int64_t)s.channels * s.states;
+    const Span sy(y, N, s.channels, s.channels, es), si(state, N, per, per, 4), so(state_out, N, per, per, 4);
+    if (sy.hits(Span(s.x, N, s.x_stride, s.channels, es)) || sy.hits(Span(s.dt, N, s.dt_stride, s.channels, es)) ||
+        sy.hits(Span(s.z, N, s.z_stride, s.channels, es)) || (state != state_out && si.hits(so)))
+        return GDN_ERR_INVALID_ARG;
+    gdn::SsmArgs a = ssm_args(args, gdn::kSsmSave, 4 * 128 / s.states * 4);
+    a.state_in = state; a.state_out = state_out; a.y = y;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (s.in_dtype == GDN_BF16) {
+        if (s.states == 16) return ssm_step_launch<__nv_bfloat16, 16>(a, st);
+        if (s.states == 32) return ssm_step_launch<__nv_bfloat16, 32>(a, st);
+        return ssm_step_launch<__nv_bfloat16, 64>(a, st);
+    }
+    if (s.states == 16) return ssm_step_launch<float, 16>(a, st);
+    if (s.states == 32) return ssm_step_launch<float, 32>(a, st);
+    return ssm_step_launch<float, 64>(a, st);
+}
+
+}  // extern "C"

@@ -29,10 +29,17 @@ SYMBOLS = ("gdn_contract_id", "gdn_status_string", "gdn_num_chunk_states", "gdn_
            "gdn_decode_step_ex",
            "gdn_cpr_forward_noalloc", "gdn_contract_text", "gdn_contract_identity", "gdn_sha256_hex",
            "gdn_cpr_backward_workspace_size", "gdn_cpr_backward", "gdn_cpr_backward_timed",
-           "gdn_read_device_status", "gdn_test_fault_injection")
+           "gdn_read_device_status", "gdn_test_fault_injection",
+           "gdn_conv_forward", "gdn_conv_backward_workspace_size", "gdn_conv_backward", "gdn_conv_step",
+           "gdn_ssm_num_chunk_states", "gdn_ssm_workspace_size", "gdn_ssm_forward",
+           "gdn_ssm_backward_workspace_size", "gdn_ssm_backward", "gdn_ssm_step",
+           "gdn_layer_norm_forward", "gdn_layer_norm_backward_workspace_size", "gdn_layer_norm_backward")
 
 #: gdn_identity_kind_t
 ID_SEMANTIC, ID_NUMERICAL_POLICY, ID_DEPLOYMENT = 0, 1, 2
+
+#: tokens between two saved states of the selective scan (GDN_SSM_CHUNK)
+SSM_CHUNK = 32
 
 #: size of the fixed device array behind gdn_cpr_forward_noalloc (GDN_NOALLOC_SCRATCH_BYTES)
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -48,6 +55,14 @@ class CacheStruct(ctypes.Structure):
     _fields_ = [("S_b", ctypes.c_void_p), ("R", ctypes.c_void_p), ("rscale", ctypes.c_void_p),
                 ("kbuf", ctypes.c_void_p), ("vbuf", ctypes.c_void_p), ("abuf", ctypes.c_void_p),
                 ("bbuf", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+
+
+class SsmStruct(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "dt", "B", "C", "z", "A", "D", "dt_bias", "cu_seqlens")] + \
+               [(n, ctypes.c_int64) for n in ("x_stride", "dt_stride", "B_stride", "C_stride", "z_stride",
+                                              "total_tokens")] + \
+               [(n, ctypes.c_int32) for n in ("num_seqs", "channels", "groups", "states", "delta_softplus",
+                                              "in_dtype")]
 
 
 _lib = None
@@ -102,6 +117,35 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.gdn_read_device_status.argtypes = [P, P, P]
     lib.gdn_test_fault_injection.restype = ctypes.c_int
     lib.gdn_test_fault_injection.argtypes = [i32, i64]
+    e = ctypes.c_int
+    lib.gdn_conv_forward.restype = e
+    lib.gdn_conv_forward.argtypes = [P, i64, P, P, P, P, i32, i64, i32, i32, i32, e, e, P, P, P, P]
+    lib.gdn_conv_backward_workspace_size.restype = sz
+    lib.gdn_conv_backward_workspace_size.argtypes = [i64, i32, i32, i32]
+    lib.gdn_conv_backward.restype = e
+    lib.gdn_conv_backward.argtypes = [P, i64, P, P, P, P, i64, P, P, i32, i64, i32, i32, i32, e, e, P, P, P, P, P, sz,
+                                      P, P]
+    lib.gdn_conv_step.restype = e
+    lib.gdn_conv_step.argtypes = [P, i64, P, P, P, P, i32, i32, i32, i32, e, e, P, P]
+    ssm = ctypes.POINTER(SsmStruct)
+    lib.gdn_ssm_num_chunk_states.restype = i64
+    lib.gdn_ssm_num_chunk_states.argtypes = [i64, i32]
+    lib.gdn_ssm_workspace_size.restype = sz
+    lib.gdn_ssm_workspace_size.argtypes = [i64, i32, i32, i32]
+    lib.gdn_ssm_forward.restype = e
+    lib.gdn_ssm_forward.argtypes = [ssm, P, P, P, P, P, sz, P, P]
+    lib.gdn_ssm_backward_workspace_size.restype = sz
+    lib.gdn_ssm_backward_workspace_size.argtypes = [i64, i32, i32, i32, i32]
+    lib.gdn_ssm_backward.restype = e
+    lib.gdn_ssm_backward.argtypes = [ssm, P, i64, P, P, P, P, P, P, P, P, P, P, P, P, sz, P, P]
+    lib.gdn_ssm_step.restype = e
+    lib.gdn_ssm_step.argtypes = [ssm, P, P, P, P]
+    lib.gdn_layer_norm_forward.restype = e
+    lib.gdn_layer_norm_forward.argtypes = [P, i64, P, P, ctypes.c_float, i64, i32, e, e, P, P, P, P]
+    lib.gdn_layer_norm_backward_workspace_size.restype = sz
+    lib.gdn_layer_norm_backward_workspace_size.argtypes = [i64, i32]
+    lib.gdn_layer_norm_backward.restype = e
+    lib.gdn_layer_norm_backward.argtypes = [P, i64, P, i64, P, P, P, i64, i32, e, e, P, P, P, P, sz, P]
     _lib = lib
     return lib
 
@@ -375,3 +419,352 @@ def gdn_cpr_forward_noalloc(q, k, v, alpha, beta, cu_seqlens, C: int, *, cu_seql
     if cache_out is not None:
         _set_pos_host(cache_out, cu_seqlens_host, C)
     return o, chunk_states
+
+
+# ------------------------------------------------------------------ layer operators
+# The short causal convolution, the selective state space scan and layer norm
+# (include/gdn_cpr.h, "layer operators").  Token tensors may be row-strided
+# views (slices of one projection's output); everything else is contiguous.
+# All tensors of a call lie on one GPU, which need not be the current one.
+
+def _where(like: torch.Tensor, what: str, *tensors: Optional[torch.Tensor]) -> torch.device:
+    """The call's device; every given tensor has to be on it."""
+    dev = like.device
+    if dev.type != "cuda":
+        raise ValueError(f"{what}: tensors must be on a CUDA device")
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{what}: tensors on {dev} and {t.device}")
+    return dev
+
+
+def _typed(what: str, dtype: torch.dtype, **tensors: Optional[torch.Tensor]) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.dtype != dtype:
+            raise ValueError(f"{what}: {name} must be {dtype}, not {t.dtype}")
+
+
+def _shaped(what: str, shape, **tensors: Optional[torch.Tensor]) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{what}: {name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+
+
+def _row_stride(what: str, name: str, t: torch.Tensor) -> int:
+    """Elements between the rows of a token tensor whose rows are dense."""
+    width = 1
+    for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if n != 1 and s != width:
+            raise ValueError(f"{what}: the rows of {name} must be contiguous")
+        width *= n
+    if t.shape[0] <= 1:
+        return width
+    if t.stride(0) < width:
+        raise ValueError(f"{what}: the rows of {name} overlap")
+    return t.stride(0)
+
+
+def _p(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _dense(what: str, **tensors: Optional[torch.Tensor]) -> None:
+    for name, t in tensors.items():
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{what}: {name} must be contiguous")
+
+
+def _call(dev: torch.device, what: str, fn, *args) -> None:
+    """Run fn(*args, stream) on dev's current stream, with dev current."""
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    _check(st, what)
+
+
+def _sequences(what: str, cu: Optional[torch.Tensor]) -> int:
+    if cu is None:
+        return 1
+    if cu.dtype != torch.int32 or cu.dim() != 1 or cu.shape[0] < 1 or not cu.is_contiguous():
+        raise ValueError(f"{what}: cu_seqlens must be a contiguous int32 vector")
+    return cu.shape[0] - 1
+
+
+def _scratch(what: str, workspace: Optional[torch.Tensor], nbytes: int, dev: torch.device) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _dense(what, workspace=workspace)
+    return workspace
+
+
+def _conv_sizes(what, x, weight, bias):
+    if x.dim() != 2 or weight.dim() != 2 or weight.shape[0] != x.shape[1]:
+        raise ValueError(f"{what}: x must be [tokens, channels] and weight [channels, width]")
+    _dense(what, weight=weight, bias=bias)
+    _typed(what, weight.dtype, bias=bias)
+    _shaped(what, (x.shape[1],), bias=bias)
+    return x.shape[0], x.shape[1], weight.shape[1]
+
+
+def gdn_conv_forward(x, weight, cu_seqlens=None, *, bias=None, state_in=None, silu: bool = True, y=None,
+                     state_out=None, status=None):
+    """Short causal convolution of a packed batch (gdn_conv_forward).
+
+    x [T, channels] (bf16 or fp32, rows may be strided); weight [channels, W], bias [channels] or
+    None (bf16 or fp32), W in 2..4; cu_seqlens int32 device [N+1] or None (one
+    sequence); state_in [N, W-1, channels] in x's dtype or None for zeros.
+    Returns (y [T, channels], state_out [N, W-1, channels]): the last inputs, for
+    :func:`gdn_conv_step` or the next part of the sequence.  ``y`` and
+    ``state_out``: optional buffers to write; rows of y outside every sequence
+    keep their contents.  ``status``: an optional int32 that records bad offsets."""
+    what = "gdn_conv_forward"
+    T, D, W = _conv_sizes(what, x, weight, bias)
+    N = _sequences(what, cu_seqlens)
+    dev = _where(x, what, weight, bias, cu_seqlens, state_in, y, state_out, status)
+    y = torch.empty(T, D, dtype=x.dtype, device=dev) if y is None else y
+    state_out = torch.empty(N, W - 1, D, dtype=x.dtype, device=dev) if state_out is None else state_out
+    _typed(what, x.dtype, y=y, state_in=state_in, state_out=state_out)
+    _typed(what, torch.int32, status=status)
+    _shaped(what, (T, D), y=y)
+    _shaped(what, (N, W - 1, D), state_in=state_in, state_out=state_out)
+    _dense(what, y=y, state_in=state_in, state_out=state_out)
+    _call(dev, what, load_library().gdn_conv_forward, _p(x), _row_stride(what, "x", x), _p(weight), _p(bias),
+          _p(state_in), _p(cu_seqlens), N, T, D, W, int(silu), _dt(x.dtype), _dt(weight.dtype), _p(y), _p(state_out),
+          _p(status))
+    return y, state_out
+
+
+def gdn_conv_backward(x, weight, dy, cu_seqlens=None, *, bias=None, state_in=None, silu: bool = True,
+                      dstate_out=None, workspace=None, grads=None, status=None):
+    """Gradients of sum(dy y) + sum(dstate_out state_out) for :func:`gdn_conv_forward` of the same inputs.
+
+    dy [T, channels] in x's dtype (rows may be strided); dstate_out [N, W-1, channels] fp32 or None.
+    Returns (dx in x's dtype, dweight, dbias (None without a bias), dstate_in), the
+    last three fp32.  ``grads``: an optional tuple of those four to write into."""
+    what = "gdn_conv_backward"
+    T, D, W = _conv_sizes(what, x, weight, bias)
+    N = _sequences(what, cu_seqlens)
+    f32 = torch.float32
+    dev = _where(x, what, weight, bias, cu_seqlens, state_in, dy, dstate_out, workspace, status, *(grads or ()))
+    if grads is None:
+        grads = (torch.empty(T, D, dtype=x.dtype, device=dev), torch.empty(D, W, dtype=f32, device=dev),
+                 None if bias is None else torch.empty(D, dtype=f32, device=dev),
+                 torch.empty(N, W - 1, D, dtype=f32, device=dev))
+    dx, dw, db, ds = grads
+    _typed(what, x.dtype, dy=dy, dx=dx, state_in=state_in)
+    _typed(what, f32, dweight=dw, dbias=db, dstate_in=ds, dstate_out=dstate_out)
+    _typed(what, torch.int32, status=status)
+    _shaped(what, (T, D), dy=dy, dx=dx)
+    _shaped(what, (D, W), dweight=dw)
+    _shaped(what, (D,), dbias=db)
+    _shaped(what, (N, W - 1, D), state_in=state_in, dstate_in=ds, dstate_out=dstate_out)
+    _dense(what, dx=dx, dweight=dw, dbias=db, dstate_in=ds, dstate_out=dstate_out, state_in=state_in)
+    lib = load_library()
+    workspace = _scratch(what, workspace, lib.gdn_conv_backward_workspace_size(T, N, D, W), dev)
+    _call(dev, what, lib.gdn_conv_backward, _p(x), _row_stride(what, "x", x), _p(weight), _p(bias), _p(state_in),
+          _p(dy), _row_stride(what, "dy", dy), _p(dstate_out), _p(cu_seqlens), N, T, D, W, int(silu), _dt(x.dtype),
+          _dt(weight.dtype), _p(dx), _p(dw), _p(db), _p(ds), _p(workspace), workspace.numel() * workspace.element_size(),
+          _p(status))
+    return grads
+
+
+def gdn_conv_step(x, weight, state, *, bias=None, silu: bool = True, y=None, state_out=None):
+    """One token per sequence: x [N, channels], state [N, W-1, channels] (from
+    :func:`gdn_conv_forward`), updated in place or written to ``state_out``.  Returns y [N, channels]."""
+    what = "gdn_conv_step"
+    N, D, W = _conv_sizes(what, x, weight, bias)
+    dev = _where(x, what, weight, bias, state, y, state_out)
+    y = torch.empty(N, D, dtype=x.dtype, device=dev) if y is None else y
+    state_out = state if state_out is None else state_out
+    _typed(what, x.dtype, y=y, state=state, state_out=state_out)
+    _shaped(what, (N, D), y=y)
+    _shaped(what, (N, W - 1, D), state=state, state_out=state_out)
+    _dense(what, y=y, state=state, state_out=state_out)
+    _call(dev, what, load_library().gdn_conv_step, _p(x), _row_stride(what, "x", x), _p(weight), _p(bias), _p(state),
+          _p(state_out), N, D, W, int(silu), _dt(x.dtype), _dt(weight.dtype), _p(y))
+    return y
+
+
+def _ssm_struct(what, x, dt, A, B, C, cu, N, D, z, dt_bias, dt_softplus) -> SsmStruct:
+    if x.dim() != 2 or B.dim() != 3:
+        raise ValueError(f"{what}: x must be [tokens, channels] and B [tokens, groups, states]")
+    (T, ch), (G, S) = x.shape, B.shape[1:]
+    _typed(what, x.dtype, dt=dt, B=B, C=C, z=z)
+    _typed(what, torch.float32, A=A, D=D, dt_bias=dt_bias)
+    _shaped(what, (T, ch), dt=dt, z=z)
+    _shaped(what, (T, G, S), B=B, C=C)
+    _shaped(what, (ch, S), A=A)
+    _shaped(what, (ch,), D=D, dt_bias=dt_bias)
+    _dense(what, A=A, D=D, dt_bias=dt_bias)
+    return SsmStruct(_p(x), _p(dt), _p(B), _p(C), _p(z), _p(A), _p(D), _p(dt_bias), _p(cu),
+                     _row_stride(what, "x", x), _row_stride(what, "dt", dt), _row_stride(what, "B", B),
+                     _row_stride(what, "C", C), 0 if z is None else _row_stride(what, "z", z), T, N, ch, G, S,
+                     int(dt_softplus), _dt(x.dtype))
+
+
+def gdn_ssm_num_chunk_states(total_tokens: int, num_seqs: int) -> int:
+    n = load_library().gdn_ssm_num_chunk_states(total_tokens, num_seqs)
+    if n < 0:
+        raise GdnError(1, "gdn_ssm_num_chunk_states")
+    return int(n)
+
+
+def gdn_ssm_forward(x, dt, A, B, C, cu_seqlens=None, *, D=None, z=None, dt_bias=None, dt_softplus: bool = True,
+                    state_in=None, save_states: bool = False, y=None, state_out=None, chunk_states=None,
+                    workspace=None, status=None):
+    """Selective state space scan of a packed batch (gdn_ssm_forward): per channel c of group g
+        delta = softplus(dt + dt_bias),  h = exp(delta A) h + delta x B[g],  y = (h . C[g] + D x) silu(z)
+
+    x, dt, z [T, channels], B, C [T, groups, states] (bf16 or fp32, rows may be strided); A [channels, states], D,
+    dt_bias [channels] fp32; z, D, dt_bias may be None; states in {16, 32, 64}; cu_seqlens int32
+    device [N+1] or None (one sequence); state_in [N, channels, states] fp32 or None.
+    Returns (y, state_out, chunk_states).  chunk_states (with ``save_states``; else
+    None) is what :func:`gdn_ssm_backward` reads."""
+    what = "gdn_ssm_forward"
+    N = _sequences(what, cu_seqlens)
+    s = _ssm_struct(what, x, dt, A, B, C, cu_seqlens, N, D, z, dt_bias, dt_softplus)
+    dev = _where(x, what, dt, A, B, C, cu_seqlens, D, z, dt_bias, state_in, y, state_out, chunk_states, workspace,
+                 status)
+    T, ch, S, f32 = s.total_tokens, s.channels, s.states, torch.float32
+    lib = load_library()
+    y = torch.empty(T, ch, dtype=x.dtype, device=dev) if y is None else y
+    state_out = torch.empty(N, ch, S, dtype=f32, device=dev) if state_out is None else state_out
+    if chunk_states is None and save_states:
+        chunk_states = torch.empty(gdn_ssm_num_chunk_states(T, N), ch, S, dtype=f32, device=dev)
+    if chunk_states is not None:
+        _shaped(what, (gdn_ssm_num_chunk_states(T, N), ch, S), chunk_states=chunk_states)
+    _typed(what, x.dtype, y=y)
+    _typed(what, f32, state_in=state_in, state_out=state_out, chunk_states=chunk_states)
+    _typed(what, torch.int32, status=status)
+    _shaped(what, (T, ch), y=y)
+    _shaped(what, (N, ch, S), state_in=state_in, state_out=state_out)
+    _dense(what, y=y, state_in=state_in, state_out=state_out, chunk_states=chunk_states)
+    workspace = _scratch(what, workspace, lib.gdn_ssm_workspace_size(T, N, ch, S), dev)
+    _call(dev, what, lib.gdn_ssm_forward, s, _p(state_in), _p(y), _p(state_out), _p(chunk_states), _p(workspace),
+          workspace.numel() * workspace.element_size(), _p(status))
+    return y, state_out, chunk_states
+
+
+def gdn_ssm_backward(x, dt, A, B, C, dy, chunk_states, cu_seqlens=None, *, D=None, z=None, dt_bias=None,
+                     dt_softplus: bool = True, dstate_out=None, workspace=None, grads=None, status=None):
+    """Gradients of sum(dy y) + sum(dstate_out state_out) for :func:`gdn_ssm_forward` of the same inputs.
+
+    dy [T, channels] in x's dtype (rows may be strided); chunk_states: that forward's; dstate_out
+    [N, channels, states] fp32 or None.  Returns (dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dstate_in): dx, ddt, dB, dC and
+    dz in x's dtype, the others fp32; dD, dz and ddt_bias are None where the
+    forward had no D, z or dt_bias.  ``grads``: an optional tuple of those nine to write into."""
+    what = "gdn_ssm_backward"
+    N = _sequences(what, cu_seqlens)
+    s = _ssm_struct(what, x, dt, A, B, C, cu_seqlens, N, D, z, dt_bias, dt_softplus)
+    dev = _where(x, what, dt, A, B, C, dy, chunk_states, cu_seqlens, D, z, dt_bias, dstate_out, workspace, status,
+                 *(grads or ()))
+    T, ch, G, S, f32 = s.total_tokens, s.channels, s.groups, s.states, torch.float32
+    lib = load_library()
+    if grads is None:
+        tok = dict(dtype=x.dtype, device=dev)
+        par = dict(dtype=f32, device=dev)
+        grads = (torch.empty(T, ch, **tok), torch.empty(T, ch, **tok), torch.empty(ch, S, **par),
+                 torch.empty(T, G, S, **tok), torch.empty(T, G, S, **tok),
+                 None if D is None else torch.empty(ch, **par), None if z is None else torch.empty(T, ch, **tok),
+                 None if dt_bias is None else torch.empty(ch, **par), torch.empty(N, ch, S, **par))
+    dx, ddt, dA, dB, dC, dD, dz, dbias, ds = grads
+    if z is not None and dz is None:
+        raise ValueError(f"{what}: dz is needed with z")
+    _typed(what, x.dtype, dy=dy, dx=dx, ddt=ddt, dB=dB, dC=dC, dz=dz)
+    _typed(what, f32, dA=dA, dD=dD, ddt_bias=dbias, dstate_in=ds, dstate_out=dstate_out, chunk_states=chunk_states)
+    _typed(what, torch.int32, status=status)
+    _shaped(what, (T, ch), dy=dy, dx=dx, ddt=ddt, dz=dz)
+    _shaped(what, (T, G, S), dB=dB, dC=dC)
+    _shaped(what, (ch, S), dA=dA)
+    _shaped(what, (ch,), dD=dD, ddt_bias=dbias)
+    _shaped(what, (N, ch, S), dstate_in=ds, dstate_out=dstate_out)
+    _shaped(what, (gdn_ssm_num_chunk_states(T, N), ch, S), chunk_states=chunk_states)
+    _dense(what, dx=dx, ddt=ddt, dA=dA, dB=dB, dC=dC, dD=dD, dz=dz, ddt_bias=dbias, dstate_in=ds,
+           dstate_out=dstate_out, chunk_states=chunk_states)
+    workspace = _scratch(what, workspace, lib.gdn_ssm_backward_workspace_size(T, N, ch, G, S), dev)
+    _call(dev, what, lib.gdn_ssm_backward, s, _p(dy), _row_stride(what, "dy", dy), _p(chunk_states), _p(dstate_out),
+          _p(dx), _p(ddt), _p(dA), _p(dB), _p(dC), _p(dD), _p(dz), _p(dbias), _p(ds), _p(workspace),
+          workspace.numel() * workspace.element_size(), _p(status))
+    return grads
+
+
+def gdn_ssm_step(x, dt, A, B, C, state, *, D=None, z=None, dt_bias=None, dt_softplus: bool = True, y=None,
+                 state_out=None):
+    """One token per sequence: x, dt, z [N, channels], B, C [N, groups, states]; state [N, channels, states] fp32 (from
+    :func:`gdn_ssm_forward`), updated in place or written to ``state_out``.  Returns y [N, channels]."""
+    what = "gdn_ssm_step"
+    s = _ssm_struct(what, x, dt, A, B, C, None, x.shape[0], D, z, dt_bias, dt_softplus)
+    dev = _where(x, what, dt, A, B, C, state, D, z, dt_bias, y, state_out)
+    N, ch = x.shape
+    y = torch.empty(N, ch, dtype=x.dtype, device=dev) if y is None else y
+    state_out = state if state_out is None else state_out
+    _typed(what, x.dtype, y=y)
+    _typed(what, torch.float32, state=state, state_out=state_out)
+    _shaped(what, (N, ch), y=y)
+    _shaped(what, (N, ch, s.states), state=state, state_out=state_out)
+    _dense(what, y=y, state=state, state_out=state_out)
+    _call(dev, what, load_library().gdn_ssm_step, s, _p(state), _p(state_out), _p(y))
+    return y
+
+
+def _rows2d(what: str, name: str, t: torch.Tensor) -> torch.Tensor:
+    """[.., width] as [rows, width] without a copy."""
+    if t.dim() == 2:
+        return t
+    if t.dim() < 1:
+        raise ValueError(f"{what}: {name} must have at least one axis")
+    try:
+        return t.view(-1, t.shape[-1])
+    except RuntimeError:
+        raise ValueError(f"{what}: the leading axes of {name} must be one stride apart") from None
+
+
+def gdn_layer_norm_forward(x, weight, *, bias=None, eps: float = 1e-5, y=None):
+    """Layer norm over the last axis (gdn_layer_norm_forward): x [.., width] (bf16 or fp32, rows
+    may be strided), weight [width] and bias [width] or None (bf16 or fp32).  A recurrence's output
+    [T, H, d_v] is normalised per head.  Returns (y in x's shape and dtype, mean, rstd fp32 [..])."""
+    what = "gdn_layer_norm_forward"
+    x2 = _rows2d(what, "x", x)
+    R, D = x2.shape
+    dev = _where(x, what, weight, bias, y)
+    _dense(what, weight=weight, bias=bias, y=y)
+    _typed(what, weight.dtype, bias=bias)
+    _shaped(what, (D,), weight=weight, bias=bias)
+    y = torch.empty(x.shape, dtype=x.dtype, device=dev) if y is None else y
+    _typed(what, x.dtype, y=y)
+    _shaped(what, x.shape, y=y)
+    stats = torch.empty((2,) + x.shape[:-1], dtype=torch.float32, device=dev)
+    mean, rstd = stats[0], stats[1]
+    _call(dev, what, load_library().gdn_layer_norm_forward, _p(x2), _row_stride(what, "x", x2), _p(weight), _p(bias),
+          eps, R, D, _dt(x.dtype), _dt(weight.dtype), _p(y), _p(mean), _p(rstd))
+    return y, mean, rstd
+
+
+def gdn_layer_norm_backward(x, weight, dy, mean, rstd, *, workspace=None, grads=None):
+    """Gradients of sum(dy y) for :func:`gdn_layer_norm_forward`: dy in x's shape and dtype,
+    mean and rstd as that call returned them.  Returns (dx in x's dtype, dweight,
+    dbias), the last two fp32, summed over the rows.  ``grads``: an optional tuple of those three to
+    write into (dbias may be None)."""
+    what = "gdn_layer_norm_backward"
+    x2, g2 = _rows2d(what, "x", x), _rows2d(what, "dy", dy)
+    R, D = x2.shape
+    f32 = torch.float32
+    dev = _where(x, what, weight, dy, mean, rstd, workspace, *(grads or ()))
+    if grads is None:
+        par = torch.empty(2, D, dtype=f32, device=dev)
+        grads = (torch.empty(x.shape, dtype=x.dtype, device=dev), par[0], par[1])
+    dx, dw, db = grads
+    _typed(what, x.dtype, dy=dy, dx=dx)
+    _typed(what, f32, mean=mean, rstd=rstd, dweight=dw, dbias=db)
+    _shaped(what, x.shape, dy=dy, dx=dx)
+    _shaped(what, x.shape[:-1], mean=mean, rstd=rstd)
+    _shaped(what, (D,), weight=weight, dweight=dw, dbias=db)
+    _dense(what, weight=weight, mean=mean, rstd=rstd, dx=dx, dweight=dw, dbias=db)
+    lib = load_library()
+    workspace = _scratch(what, workspace, lib.gdn_layer_norm_backward_workspace_size(R, D), dev)
+    _call(dev, what, lib.gdn_layer_norm_backward, _p(x2), _row_stride(what, "x", x2), _p(g2),
+          _row_stride(what, "dy", g2), _p(weight), _p(mean), _p(rstd), R, D, _dt(x.dtype), _dt(weight.dtype), _p(dx),
+          _p(dw), _p(db), _p(workspace), workspace.numel() * workspace.element_size())
+    return grads

@@ -445,6 +445,149 @@ gdn_status_t gdn_cpr_forward_noalloc(const void* q, const void* k, const void* v
                                      void* o, float* chunk_states, const gdn_cache_t* cache_out,
                                      void* stream);
 
+/*
+ * ------------------------------------------------------------------ layer operators
+ * The operators around the recurrence, for prefill, training and decode: the short causal
+ * convolution in front of a recurrent mixer, the selective state space scan (a mixer of
+ * its own kind, with a diagonal decay per channel and state), and layer norm.
+ * They take the conventions at the top of this file, with these differences:
+ *  - Token tensors ([T, channels], [T, G, S]) may be views of wider rows, such as the slices
+ *    of one projection's output: `*_stride` is the distance between tokens in
+ *    elements (at least the row's width).  They need the alignment of one
+ *    element only; rows whose width, stride and address are multiples of 16 bytes
+ *    are read in 16-byte accesses.  Outputs are dense.  States, parameters in fp32 and
+ *    gradients of either are 16-byte aligned.
+ *  - cu_seqlens is read on the device only, so that a captured graph can be
+ *    replayed with other lengths: 0 <= cu[0], non-decreasing, cu[num_seqs] <=
+ *    total_tokens.  NULL stands for one sequence of total_tokens rows (num_seqs = 1).
+ *    Rows outside every sequence (padding behind the last one) are left as they
+ *    are in every output.  An offset that breaks this is clamped, so no access
+ *    leaves the tensors, the results are unspecified, and *status (one int32 on the
+ *    device, or NULL; never cleared by the library) becomes GDN_ERR_DEVICE_INPUT.
+ *  - Outputs must not overlap inputs, except where a call says so.
+ *  - Every sum is fp32 and in a fixed order, without atomics: repeated calls
+ *    give the same bits.  Inputs that are not finite spread as IEEE arithmetic does,
+ *    within the rows (norm) or sequences (convolution, scan) and channels they
+ *    belong to, and into the gradients of the parameters.
+ */
+
+/*
+ * Short causal convolution, per sequence and channel c, width W in {2, 3, 4}:
+ *   pre[t] = bias[c] + sum_{i<W} weight[c][i] x[t - (W-1) + i][c],  y = silu ? pre sigmoid(pre) : pre
+ *   x        [total_tokens, channels] in in_dtype, rows x_stride apart
+ *   weight   [channels, W], bias [channels] or NULL, both in w_dtype
+ *   state_in [num_seqs, W-1, channels] in in_dtype: the inputs before each
+ *            sequence's first token, oldest first; NULL: zeros
+ *   y        [total_tokens, channels] in in_dtype
+ *   state_out [num_seqs, W-1, channels] in in_dtype: the last W-1 inputs
+ *            (state_in's, where a sequence is shorter), for the next call or step
+ */
+gdn_status_t gdn_conv_forward(const void* x, int64_t x_stride, const void* weight, const void* bias,
+                              const void* state_in, const int32_t* cu_seqlens, int32_t num_seqs,
+                              int64_t total_tokens, int32_t channels, int32_t width, int32_t silu,
+                              gdn_dtype_t in_dtype, gdn_dtype_t w_dtype, void* y, void* state_out,
+                              int32_t* status, void* stream);
+
+/*
+ * Gradients of sum(dy y) + sum(dstate_out state_out).
+ *   dy [total_tokens, channels] in in_dtype; dstate_out fp32 in state_out's shape, or NULL for zeros
+ *   dx [total_tokens, channels] in in_dtype; dweight [channels, W], dbias [channels] (NULL: not
+ *   wanted) and dstate_in [num_seqs, W-1, channels] in fp32
+ */
+size_t gdn_conv_backward_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t channels, int32_t width);
+gdn_status_t gdn_conv_backward(const void* x, int64_t x_stride, const void* weight, const void* bias,
+                               const void* state_in, const void* dy, int64_t dy_stride, const float* dstate_out,
+                               const int32_t* cu_seqlens, int32_t num_seqs, int64_t total_tokens, int32_t channels,
+                               int32_t width, int32_t silu, gdn_dtype_t in_dtype, gdn_dtype_t w_dtype, void* dx,
+                               float* dweight, float* dbias, float* dstate_in, void* workspace,
+                               size_t workspace_bytes, int32_t* status, void* stream);
+
+/*
+ * One token per sequence: x [num_seqs, channels]; state as the forward's
+ * state_out.  state_out may be state itself (updated in place) or a buffer apart from it.
+ */
+gdn_status_t gdn_conv_step(const void* x, int64_t x_stride, const void* weight, const void* bias, const void* state,
+                           void* state_out, int32_t num_seqs, int32_t channels, int32_t width, int32_t silu,
+                           gdn_dtype_t in_dtype, gdn_dtype_t w_dtype, void* y, void* stream);
+
+/*
+ * Selective state space scan, per channel c of group e = c / (channels / groups):
+ *   delta = softplus(dt + dt_bias[c])   (delta_softplus = 0: dt + dt_bias[c])
+ *   h_t[s] = exp(delta A[c][s]) h_{t-1}[s] + delta x B_t[e][s]
+ *   y_t    = (sum_s h_t[s] C_t[e][s] + D[c] x) silu(z_t[c])
+ * x, dt, z [T, channels] and B, C [T, groups, states] in in_dtype, rows *_stride apart; A [channels, states],
+ * D and dt_bias [channels] fp32; z, D, dt_bias may be NULL (no gate, no skip, no
+ * bias).  states in {16, 32, 64}; groups divides channels.  A is meant to be
+ * negative: a positive one grows the state as the formula says.
+ */
+typedef struct {
+    const void *x, *dt, *B, *C, *z;
+    const float *A, *D, *dt_bias;
+    const int32_t* cu_seqlens;
+    int64_t x_stride, dt_stride, B_stride, C_stride, z_stride;
+    int64_t total_tokens;
+    int32_t num_seqs, channels, groups, states;
+    int32_t delta_softplus;
+    gdn_dtype_t in_dtype;
+} gdn_ssm_t;
+
+#define GDN_SSM_CHUNK 32
+
+/* Rows of the saved states that gdn_ssm_backward reads: total_tokens / GDN_SSM_CHUNK + num_seqs; -1 for invalid sizes. */
+int64_t gdn_ssm_num_chunk_states(int64_t total_tokens, int32_t num_seqs);
+size_t gdn_ssm_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t channels, int32_t states);
+
+/*
+ * Prefill and trainer forward.
+ *   state_in [num_seqs, channels, states] fp32 or NULL for zeros
+ *   y [T, channels] in in_dtype; state_out [num_seqs, channels, states] fp32
+ *   chunk_states [gdn_ssm_num_chunk_states(), channels, states] fp32, or NULL where no
+ *     backward follows: the states before every GDN_SSM_CHUNK-th token of a
+ *     sequence; row lo / GDN_SSM_CHUNK + n + k belongs to token lo + k GDN_SSM_CHUNK of
+ *     sequence n, which starts at row lo.  Rows that belong to no token are not written.
+ *   workspace: gdn_ssm_workspace_size(...) bytes, 256-byte aligned
+ */
+gdn_status_t gdn_ssm_forward(const gdn_ssm_t* args, const float* state_in, void* y, float* state_out,
+                             float* chunk_states, void* workspace, size_t workspace_bytes, int32_t* status,
+                             void* stream);
+
+/*
+ * Gradients of sum(dy y) + sum(dstate_out state_out).  args and chunk_states: as given to and written by
+ * the forward.  dx, ddt, dz [T, channels] and dB, dC [T, groups, states] in in_dtype; dA [channels, states], dD,
+ * ddt_bias [channels] and dstate_in [num_seqs, channels, states] fp32.  dD, dz and ddt_bias
+ * may be NULL where the forward had no D, z or dt_bias (dz must be given with z).
+ */
+size_t gdn_ssm_backward_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t channels, int32_t groups,
+                                       int32_t states);
+gdn_status_t gdn_ssm_backward(const gdn_ssm_t* args, const void* dy, int64_t dy_stride, const float* chunk_states,
+                              const float* dstate_out, void* dx, void* ddt, float* dA, void* dB, void* dC, float* dD,
+                              void* dz, float* ddt_bias, float* dstate_in, void* workspace, size_t workspace_bytes,
+                              int32_t* status, void* stream);
+
+/*
+ * One token per sequence: args with total_tokens = num_seqs (cu_seqlens is not read);
+ * state [num_seqs, channels, states] fp32.  state_out may be state itself (updated in place) or
+ * a buffer apart from it.
+ */
+gdn_status_t gdn_ssm_step(const gdn_ssm_t* args, const float* state, float* state_out, void* y, void* stream);
+
+/*
+ * Layer norm of each row of x [rows, width]:
+ *   y = (x - mean) rstd weight + bias,  rstd = (mean((x - mean)^2) + eps)^(-1/2)
+ * weight and bias (NULL: none) [width] in w_dtype; y in in_dtype; mean, rstd [rows] fp32.
+ * The backward gives the gradients of sum(dy y): dx in in_dtype, dweight and dbias (NULL: not
+ * wanted) fp32, summed over the rows.
+ */
+gdn_status_t gdn_layer_norm_forward(const void* x, int64_t x_stride, const void* weight, const void* bias, float eps,
+                                    int64_t rows, int32_t width, gdn_dtype_t in_dtype, gdn_dtype_t w_dtype, void* y,
+                                    float* mean, float* rstd, void* stream);
+size_t gdn_layer_norm_backward_workspace_size(int64_t rows, int32_t width);
+gdn_status_t gdn_layer_norm_backward(const void* x, int64_t x_stride, const void* dy, int64_t dy_stride,
+                                     const void* weight, const float* mean, const float* rstd, int64_t rows,
+                                     int32_t width, gdn_dtype_t in_dtype, gdn_dtype_t w_dtype, void* dx,
+                                     float* dweight, float* dbias, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
 #ifdef __cplusplus
 }
 #endif
