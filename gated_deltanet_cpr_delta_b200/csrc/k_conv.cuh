@@ -95,9 +95,11 @@ __device__ __forceinline__ void conv_tail(const ConvArgs& a, int n, int64_t c)
     }
 }
 
-// U rows are loaded together, so that a thread has U accesses in flight.
+// U rows are loaded together and the next U are on their way while they are
+// worked on.  Where these lie in one sequence (almost everywhere) there is no test
+// per row.
 template <typename T, int W, int V>
-__global__ void __launch_bounds__(128) k_conv_fwd(const ConvArgs a)
+__global__ void __launch_bounds__(128, 8) k_conv_fwd(const ConvArgs a)
 {
     constexpr int U = 8;
     if (blockIdx.x == 0) check_seqs(a.s, a.status);
@@ -111,50 +113,67 @@ __global__ void __launch_bounds__(128) k_conv_fwd(const ConvArgs a)
         if (n < a.s.N) conv_tail<T, W, V>(a, (int)n, c);
         return;
     }
-    int64_t t = (tile * ny + ty) * a.run;
-    const int64_t end = min(t + a.run, a.s.T);
-    if (t >= end) return;
+    const int64_t t64 = (tile * ny + ty) * a.run;
+    if (t64 >= a.s.T) return;
+    int t = (int)t64;  // rows are below 2^31
+    const int end = (int)min(t64 + a.run, a.s.T);
     int n = a.s.find(t);
     if (n < 0) {  // rows before the first sequence
-        n = 0;
-        t = min(a.s.lo(0), end);
+        t = (int)min(a.s.lo(0), (int64_t)end);
         if (t >= end) return;
         n = a.s.find(t);
     }
     ConvTaps<T, W, V> taps;
     taps.load(a, c);
-    const T* x = static_cast<const T*>(a.x);
-    T* y = static_cast<T*>(a.y);
-    int64_t lo = a.s.lo(n), hi = a.s.hi(n);
+    const int64_t ldx = a.ldx, ldy = a.D;
+    const T* x = static_cast<const T*>(a.x) + c + t * ldx;  // row t
+    T* y = static_cast<T*>(a.y) + c + t * ldy;
+    int hi = (int)a.s.hi(n);
     float win[W][V];
-    conv_window<T, W, V>(a, n, lo, t, c, win);
-    for (; t < end; t += U) {
-        Vec<T, V> raw[U];
+    conv_window<T, W, V>(a, n, a.s.lo(n), t, c, win);
+    auto row = [&](const Vec<T, V>& r, T* out, bool store) {
+        float o[V];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (t + u < end) raw[u] = load_vec<T, V>(x + (t + u) * a.ldx + c);
+        for (int k = 0; k < V; ++k) {
+            win[W - 1][k] = to_f<T>(r.v[k]);
+            float p = taps.b[k];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (t + u < end) {
+            for (int i = 0; i < W; ++i) p = __fmaf_rn(taps.w[i][k], win[i][k], p);
+            o[k] = a.silu ? silu(p) : p;
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i) win[i][k] = win[i + 1][k];
+        }
+        if (store) store_vec<T, V>(out, o);
+    };
+    Vec<T, V> next[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (t + u < end) next[u] = load_vec<T, V>(x + u * ldx);
+    for (; t < end; t += U, x += U * ldx, y += U * ldy) {
+        const T* ahead = x + U * ldx;
+        if (t + 2 * U <= min(hi, end)) {  // this group and the next are whole and of one sequence
+            Vec<T, V> raw[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                raw[u] = next[u];
+                next[u] = load_vec<T, V>(ahead + u * ldx);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) row(raw[u], y + u * ldy, true);
+        } else {
+#pragma unroll 1
+            for (int u = 0; u < U && t + u < end; ++u) {
                 if (t + u >= hi && n + 1 < a.s.N && t + u >= a.s.lo(n + 1)) {  // the next sequence's first token
                     n = a.s.find(t + u);
-                    lo = a.s.lo(n);
-                    hi = a.s.hi(n);
-                    conv_window<T, W, V>(a, n, lo, t + u, c, win);
+                    hi = (int)a.s.hi(n);
+                    conv_window<T, W, V>(a, n, a.s.lo(n), t + u, c, win);
                 }
-                float o[V];
-#pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    win[W - 1][k] = to_f<T>(raw[u].v[k]);
-                    float p = taps.b[k];
-#pragma unroll
-                    for (int i = 0; i < W; ++i) p = __fmaf_rn(taps.w[i][k], win[i][k], p);
-                    o[k] = a.silu ? silu(p) : p;
-#pragma unroll
-                    for (int i = 0; i < W - 1; ++i) win[i][k] = win[i + 1][k];
-                }
-                if (t + u < hi) store_vec<T, V>(y + (t + u) * a.D + c, o);  // rows behind the last sequence stay
+                // rows behind the last sequence stay
+                row(load_vec<T, V>(x + u * ldx), y + u * ldy, t + u < hi);
             }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (t + U + u < end) next[u] = load_vec<T, V>(ahead + u * ldx);
         }
     }
 }
@@ -201,41 +220,72 @@ __device__ __forceinline__ void conv_bwd_run(const ConvArgs& a, int64_t t0, int6
                 store_vec<T, V>(dx + r * a.D + c, v);
             }
         };
-        if (t < stop) {
-            Vec<T, V> rx = load_vec<T, V>(x + t * a.ldx + c), rg = load_vec<T, V>(dy + t * a.lddy + c);
-            for (; t < stop; ++t) {
-                const Vec<T, V> cx = rx, cg = rg;
-                if (t + 1 < stop) {
-                    rx = load_vec<T, V>(x + (t + 1) * a.ldx + c);
-                    rg = load_vec<T, V>(dy + (t + 1) * a.lddy + c);
+        // One row.  `inner`: the row and the finished one are the run's own.
+        auto row = [&](const Vec<T, V>& rx, const Vec<T, V>& rg, int64_t at, T* out, bool inner) {
+            const bool own = inner || at < t1;
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                win[W - 1][k] = to_f<T>(rx.v[k]);
+                float p = taps.b[k];
+#pragma unroll
+                for (int i = 0; i < W; ++i) p = __fmaf_rn(taps.w[i][k], win[i][k], p);
+                float g = to_f<T>(rg.v[k]);
+                if (a.silu) g *= silu_grad(p);
+                const float go = own ? g : 0.0f;
+                db[k] += go;
+#pragma unroll
+                for (int i = 0; i < W; ++i) {
+                    acc[i][k] = i < W - 1 ? __fmaf_rn(taps.w[i][k], g, acc[i][k]) : taps.w[i][k] * g;
+                    dw[i][k] = __fmaf_rn(go, win[i][k], dw[i][k]);
                 }
-                const bool own = t < t1;
+            }
+            if (inner) store_vec<T, V>(out, acc[0]);
+            else emit(at - (W - 1), acc[0]);
 #pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    win[W - 1][k] = to_f<T>(cx.v[k]);
-                    float p = taps.b[k];
+            for (int k = 0; k < V; ++k)
 #pragma unroll
-                    for (int i = 0; i < W; ++i) p = __fmaf_rn(taps.w[i][k], win[i][k], p);
-                    float g = to_f<T>(cg.v[k]);
-                    if (a.silu) g *= silu_grad(p);
-                    const float go = own ? g : 0.0f;
-                    db[k] += go;
+                for (int i = 0; i < W - 1; ++i) {
+                    win[i][k] = win[i + 1][k];
+                    acc[i][k] = acc[i + 1][k];
+                }
+        };
+        // U rows are loaded together; the next U are on their way meanwhile
+        constexpr int U = 16 / sizeof(T);
+        const int64_t ldx = a.ldx, ldg = a.lddy;
+        const T* px = x + t * ldx + c;  // row t
+        const T* pg = dy + t * ldg + c;
+        T* pd = dx + (t - (W - 1)) * (int64_t)a.D + c;  // the row finished at t
+        const int64_t first = max(lo, t0) + (W - 1), last = only_seq >= 0 ? first : min(stop - U, t1);
+        Vec<T, V> nx[U], ng[U];
 #pragma unroll
-                    for (int i = 0; i < W; ++i) {
-                        acc[i][k] = __fmaf_rn(taps.w[i][k], g, acc[i][k]);
-                        dw[i][k] = __fmaf_rn(go, win[i][k], dw[i][k]);
+        for (int u = 0; u < U; ++u)
+            if (t + u < stop) {
+                nx[u] = load_vec<T, V>(px + u * ldx);
+                ng[u] = load_vec<T, V>(pg + u * ldg);
+            }
+        for (; t < stop; t += U, px += U * ldx, pg += U * ldg, pd += U * (int64_t)a.D) {
+            const T *ax = px + U * ldx, *ag = pg + U * ldg;
+            if (t >= first && t + U <= last) {
+                Vec<T, V> rx[U], rg[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    rx[u] = nx[u];
+                    rg[u] = ng[u];
+                    nx[u] = load_vec<T, V>(ax + u * ldx);
+                    ng[u] = load_vec<T, V>(ag + u * ldg);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) row(rx[u], rg[u], t + u, pd + u * (int64_t)a.D, true);
+            } else {
+#pragma unroll 1
+                for (int u = 0; u < U && t + u < stop; ++u)
+                    row(load_vec<T, V>(px + u * ldx), load_vec<T, V>(pg + u * ldg), t + u, nullptr, false);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (t + U + u < stop) {
+                        nx[u] = load_vec<T, V>(ax + u * ldx);
+                        ng[u] = load_vec<T, V>(ag + u * ldg);
                     }
-                }
-                emit(t - (W - 1), acc[0]);
-#pragma unroll
-                for (int k = 0; k < V; ++k) {
-#pragma unroll
-                    for (int i = 0; i < W - 1; ++i) {
-                        win[i][k] = win[i + 1][k];
-                        acc[i][k] = acc[i + 1][k];
-                    }
-                    acc[W - 1][k] = 0.0f;
-                }
             }
         }
         if (stop == hi) {  // the sequence's end: the open rows hi - (W-1) + i
@@ -261,7 +311,7 @@ __device__ __forceinline__ void conv_bwd_run(const ConvArgs& a, int64_t t0, int6
 }
 
 template <typename T, int W, int V>
-__global__ void __launch_bounds__(128) k_conv_bwd(const ConvArgs a)
+__global__ void __launch_bounds__(128, 4) k_conv_bwd(const ConvArgs a)
 {
     extern __shared__ float sh[];  // [(W + 1) * V][128]: joins the runs of a block
     if (blockIdx.x == 0) check_seqs(a.s, a.status);

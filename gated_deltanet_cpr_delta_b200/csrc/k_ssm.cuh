@@ -40,6 +40,7 @@ struct SsmArgs {
     int32_t D, G, Dg;   // channels, groups, channels per group
     int32_t cpg;        // channel blocks per group
     int softplus;
+    int bc16;           // rows of B and C in 16-byte accesses
     int64_t Lc;         // tokens per chunk (a multiple of kSsmTile and kSsmSave)
     const float* state_in;
     void* y;
@@ -323,6 +324,246 @@ __global__ void __launch_bounds__(128) k_ssm_pass(const SsmArgs a)
         h[1] = __fmaf_rn(ex2(d * A2[1]), h[1], v.y);
         h[2] = __fmaf_rn(ex2(d * A2[2]), h[2], v.z);
         h[3] = __fmaf_rn(ex2(d * A2[3]), h[3], v.w);
+    }
+}
+
+// ------------------------------------------------------------------ forward
+// One warp walks a sequence for 32 / SEG channels, tile by tile.  Its lanes
+// are SEG time segments x 32 / SEG channels; a segment is 8 tokens, so a tile is
+// 8 SEG tokens, and a lane keeps delta, delta x and y of its 8 tokens in registers.
+// For each pair of states the lane makes its 8 decays once, runs its tokens
+// from zero (the first segment from the carried state), the segments are joined by a
+// warp scan of (product of decays, end state), and the lane runs its tokens
+// again from its true state, with the decays it kept.  So every exponential is
+// made once, sequences of few channels still fill the GPU, and y needs no sum
+// over lanes.
+template <typename T, int S, int SEG>
+struct SsmFwdCfg {
+    static constexpr int K = 8;                        // tokens per segment
+    static constexpr int TT = K * SEG;                 // tokens per tile
+    static constexpr int CL = 32 / SEG;                // channels per warp
+    static constexpr int NW = SEG == 32 ? 8 : 4;       // warps per block
+    static constexpr int CB = CL * NW;                 // channels per block
+    static constexpr int THREADS = 32 * NW;
+    // Token rows in shared memory: CB elements; 16 bytes of padding per segment
+    // put the segments of a warp's access into different banks.
+    static constexpr int SEGROW = K * CB + 16 / (int)sizeof(T);
+    static constexpr int TOK = SEG * SEGROW;           // elements of a staged token tensor
+    static constexpr int PS = SEG * (K + 2);           // float2 per state pair of a B or C plane
+    static constexpr size_t BYTES = sizeof(T) * (2 * 3 * TOK + 2 * TT * S) + sizeof(float2) * 2 * (S / 2) * PS +
+                                    sizeof(float) * 2 * S * CB;
+};
+
+__device__ __forceinline__ void ssm_cp_async16(void* smem, const void* gmem)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(smem)), "l"(gmem)
+                 : "memory");
+}
+
+template <typename T, int S, int V, int SEG>
+__global__ void __launch_bounds__(SsmFwdCfg<T, S, SEG>::THREADS, SEG == 32 ? 2 : 4) k_ssm_fwd(const SsmArgs a)
+{
+    using Cf = SsmFwdCfg<T, S, SEG>;
+    constexpr int K = Cf::K, TT = Cf::TT, CL = Cf::CL, CB = Cf::CB, NT = Cf::THREADS, NP = S / 2;
+    extern __shared__ __align__(16) unsigned char ssm_smem[];
+    T* raw = reinterpret_cast<T*>(ssm_smem);           // [2 stages][x, dt, z][TOK]
+    T* rawB = raw + 2 * 3 * Cf::TOK;                   // [B, C][TT][S]
+    float2* sB = reinterpret_cast<float2*>(rawB + 2 * TT * S);      // [NP][PS]
+    float2* sC = sB + NP * Cf::PS;
+    float2* sA = sC + NP * Cf::PS;                     // [NP][CB]: A log2 e
+    float2* sH = sA + NP * CB;                         // [NP][CB]: the carried states
+
+    if (blockIdx.x == 0) check_seqs(a.s, a.status);
+    const int nb = a.G * a.cpg;
+    const int n = blockIdx.x / nb, cb = blockIdx.x - n * nb, e = cb / a.cpg;
+    const int cbase = e * a.Dg + (cb - e * a.cpg) * CB, cend = (e + 1) * a.Dg;
+    const int64_t lo = a.s.lo(n), L = a.s.hi(n) - lo;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int seg = lane / CL, ch = warp * CL + lane % CL;          // the lane's channel in the block
+    const int ch0 = cbase + ch;
+    const bool on = ch0 < cend;
+
+    // parameters and initial states of the block's channels
+    for (int i = tid; i < CB * S; i += NT) {
+        const int c = i / S, st = i % S;
+        const bool ok = cbase + c < cend;
+        const int at = ((st / 2) * CB + c) * 2 + (st & 1);
+        reinterpret_cast<float*>(sA)[at] = ok ? a.A[(int64_t)(cbase + c) * S + st] * kLog2e : 0.0f;
+        reinterpret_cast<float*>(sH)[at] =
+            ok && a.state_in != nullptr ? a.state_in[((int64_t)n * a.D + cbase + c) * S + st] : 0.0f;
+    }
+    const float bias = on && a.dt_bias != nullptr ? a.dt_bias[ch0] : 0.0f;
+    const float Dv = on && a.Dp != nullptr ? a.Dp[ch0] : 0.0f;
+    const T* B = static_cast<const T*>(a.B) + e * S;
+    const T* C = static_cast<const T*>(a.C) + e * S;
+
+    // a row's offset, from 32-bit factors (rows and strides are below 2^31)
+    auto at = [](int row, int64_t ld) { return (int64_t)row * (int)ld; };
+    auto stage = [&](int64_t p, int buf) {
+        T* dst = raw + buf * 3 * Cf::TOK;
+        const int rows = (int)min((int64_t)TT, L - p);
+        for (int i = tid; i < TT * (CB / V); i += NT) {
+            const int t = i / (CB / V), v = (i % (CB / V)) * V;
+            if (t < rows && cbase + v < cend) {
+                const int row = (int)(lo + p) + t;
+                T* d = dst + (t / K) * Cf::SEGROW + (t % K) * CB + v;
+                const T* px = static_cast<const T*>(a.x) + at(row, a.ldx) + cbase + v;
+                const T* pd = static_cast<const T*>(a.dt) + at(row, a.lddt) + cbase + v;
+                const T* pz = a.z != nullptr ? static_cast<const T*>(a.z) + at(row, a.ldz) + cbase + v : nullptr;
+                if (V * sizeof(T) == 16) {
+                    ssm_cp_async16(d, px);
+                    ssm_cp_async16(d + Cf::TOK, pd);
+                    if (pz != nullptr) ssm_cp_async16(d + 2 * Cf::TOK, pz);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < V; ++k) {
+                        d[k] = px[k];
+                        d[Cf::TOK + k] = pd[k];
+                        if (pz != nullptr) d[2 * Cf::TOK + k] = pz[k];
+                    }
+                }
+            }
+        }
+    };
+    constexpr int VB = 16 / (int)sizeof(T);            // states per 16-byte access
+    auto stage_bc = [&](int64_t p) {
+        const int rows = (int)min((int64_t)TT, L - p);
+        if (a.bc16) {
+            for (int i = tid; i < rows * (S / VB); i += NT) {
+                const int t = i / (S / VB), v = (i % (S / VB)) * VB;
+                ssm_cp_async16(rawB + t * S + v, B + at((int)(lo + p) + t, a.ldB) + v);
+                ssm_cp_async16(rawB + (TT + t) * S + v, C + at((int)(lo + p) + t, a.ldC) + v);
+            }
+        } else {
+            for (int i = tid; i < rows * S; i += NT) {
+                const int t = i / S, v = i % S;
+                rawB[i] = B[(lo + p + t) * a.ldB + v];
+                rawB[TT * S + i] = C[(lo + p + t) * a.ldC + v];
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+
+    if (L > 0) {
+        stage(0, 0);
+        stage_bc(0);
+    }
+    const f2x later = seg == 0 ? pk2(0.0f, 0.0f) : pk2(1.0f, 1.0f);
+    int buf = 0;
+    for (int64_t p = 0; p < L; p += TT, buf ^= 1) {
+        const int rows = (int)min((int64_t)TT, L - p);
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+        // B and C as planes of state pairs, in fp32 (zero behind the sequence's end)
+        for (int i = tid; i < 2 * TT * (S / VB); i += NT) {
+            const int t = i % TT, j = i / TT;  // neighbouring threads, neighbouring tokens
+            const int v = (j % (S / VB)) * VB;
+            const bool isC = j >= S / VB;
+            const Vec<T, VB> r = load_vec<T, VB>(rawB + ((isC ? TT : 0) + t) * S + v);
+            float2* d = (isC ? sC : sB) + (v / 2) * Cf::PS + (t / K) * (K + 2) + t % K;
+            if (t < rows) {
+#pragma unroll
+                for (int q = 0; q < VB / 2; ++q)
+                    d[q * Cf::PS] = make_float2(to_f<T>(r.v[2 * q]), to_f<T>(r.v[2 * q + 1]));
+            } else {
+#pragma unroll
+                for (int q = 0; q < VB / 2; ++q) d[q * Cf::PS] = make_float2(0.f, 0.f);
+            }
+        }
+        if (p + TT < L) stage(p + TT, buf ^ 1);
+        T* mine = raw + buf * 3 * Cf::TOK + seg * Cf::SEGROW + ch;
+        f2x dl[K], u[K], y[K];  // delta and delta x in both halves
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const float d = ssm_delta(a, to_f<T>(mine[Cf::TOK + k * CB]), bias), w = d * to_f<T>(mine[k * CB]);
+            dl[k] = pk2(d, d);
+            u[k] = pk2(w, w);
+            y[k] = pk2(0.0f, 0.0f);
+        }
+        if (rows < TT) {  // behind the sequence's end: the state stays
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (seg * K + k >= rows) dl[k] = u[k] = pk2(0.0f, 0.0f);
+        }
+        __syncthreads();
+        if (p + TT < L) stage_bc(p + TT);
+#pragma unroll 1
+        for (int np = 0; np < NP; ++np) {
+            const f2x A2 = *reinterpret_cast<const f2x*>(sA + np * CB + ch);
+            const f2x h0 = *reinterpret_cast<const f2x*>(sH + np * CB + ch);
+            const ulonglong2* pB = reinterpret_cast<const ulonglong2*>(sB + np * Cf::PS + seg * (K + 2));
+            const ulonglong2* pC = reinterpret_cast<const ulonglong2*>(sC + np * Cf::PS + seg * (K + 2));
+            f2x am[K], bm[K], P, H;
+#pragma unroll
+            for (int k2 = 0; k2 < K / 2; ++k2) {
+                const ulonglong2 b2 = pB[k2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int k = 2 * k2 + q;
+                    float e0, e1;
+                    up2(fmul2(dl[k], A2), e0, e1);
+                    am[k] = pk2(ex2(e0), ex2(e1));
+                    bm[k] = fmul2(u[k], q ? b2.y : b2.x);
+                    if (k == 0) {
+                        P = fmul2(am[0], later);
+                        H = seg == 0 ? ffma2(am[0], h0, bm[0]) : bm[0];
+                    } else {
+                        P = fmul2(P, am[k]);
+                        H = ffma2(am[k], H, bm[k]);
+                    }
+                }
+            }
+            // inclusive scan over the segments: (P, H) o (Pp, Hp) = (P Pp, P Hp + H).  The
+            // first segment's P is 0, as its H holds the carried state already; so P
+            // becomes 0 in every lane that has joined it, and the lanes without an
+            // earlier segment, which get their own H back, keep it.
+#pragma unroll
+            for (int o = 1; o < SEG; o <<= 1) {
+                H = ffma2(P, __shfl_up_sync(kFullMask, H, o * CL), H);
+                if (2 * o < SEG) P = fmul2(P, __shfl_up_sync(kFullMask, P, o * CL));
+            }
+            const f2x from = __shfl_sync(kFullMask, H, (lane - CL) & 31);  // the first segment gets the last's
+            f2x h = seg == 0 ? h0 : from;
+            if (seg == 0) *reinterpret_cast<f2x*>(sH + np * CB + ch) = from;
+            if (a.saved != nullptr && on && (seg * K) % kSsmSave == 0 && seg * K < rows) {
+                const int64_t at = a.s.first_slot(n, kSsmSave) + (p + seg * K) / kSsmSave;
+                *reinterpret_cast<f2x*>(a.saved + (at * a.D + ch0) * S + 2 * np) = h;
+            }
+#pragma unroll
+            for (int k2 = 0; k2 < K / 2; ++k2) {
+                const ulonglong2 c2 = pC[k2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int k = 2 * k2 + q;
+                    h = ffma2(am[k], h, bm[k]);
+                    y[k] = ffma2(h, q ? c2.y : c2.x, y[k]);
+                }
+            }
+        }
+        // y in the place of x
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            float y0, y1;
+            up2(y[k], y0, y1);
+            float o = __fmaf_rn(Dv, to_f<T>(mine[k * CB]), y0 + y1);
+            if (a.z != nullptr) o *= silu(to_f<T>(mine[2 * Cf::TOK + k * CB]));
+            mine[k * CB] = from_f<T>(o);
+        }
+        __syncthreads();
+        const T* out = raw + buf * 3 * Cf::TOK;
+        for (int i = tid; i < TT * (CB / V); i += NT) {
+            const int t = i / (CB / V), v = (i % (CB / V)) * V;
+            if (t < rows && cbase + v < cend)
+                *reinterpret_cast<Vec<T, V>*>(static_cast<T*>(a.y) + at((int)(lo + p) + t, a.D) + cbase + v) =
+                    load_vec<T, V>(out + (t / K) * Cf::SEGROW + (t % K) * CB + v);
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < CB * S; i += NT) {
+        const int c = i / S, st = i % S;
+        if (cbase + c < cend)
+            a.state_out[((int64_t)n * a.D + cbase + c) * S + st] =
+                reinterpret_cast<const float*>(sH)[((st / 2) * CB + c) * 2 + (st & 1)];
     }
 }
 

@@ -129,18 +129,44 @@ __device__ __forceinline__ float ex2(float x)
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.0f, 1.0f + ex2(-kLog2e * v)); }
+// 1 / x in one instruction, off by at most one unit; 0 for x above 2^126
+__device__ __forceinline__ float rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float sigmoid(float v) { return rcp(1.0f + ex2(-kLog2e * v)); }
 
 // v * sigmoid(v) and its derivative
-__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.0f + ex2(-kLog2e * v)); }
+__device__ __forceinline__ float silu(float v) { return v * sigmoid(v); }
 __device__ __forceinline__ float silu_grad(float v)
 {
     const float s = sigmoid(v);
     return s * __fmaf_rn(v, 1.0f - s, 1.0f);
 }
 
-// log(1 + e^v), accurate relative to its value on both sides
-__device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.0f) + log1pf(ex2(-kLog2e * fabsf(v))); }
+// log(1 + e^v), accurate relative to its value on both sides: max(v, 0) + log1p(e),
+// e = e^-|v| in (0, 1], with log1p(e) = e P(e).  P is the polynomial of degree 9 with the
+// smallest largest relative error on [0, 1] (4.7e-9, by the exchange algorithm); in
+// fp32 the product is off by at most 1.5e-7.  Nine multiply-adds in place of the
+// library's log1pf, which took a quarter of the scan's instructions.
+__device__ __forceinline__ float softplus(float v)
+{
+    const float e = ex2(-kLog2e * fabsf(v));
+    float p = -0.0032440251670777798f;
+    p = __fmaf_rn(p, e, 0.01985146291553974f);
+    p = __fmaf_rn(p, e, -0.05695953592658043f);
+    p = __fmaf_rn(p, e, 0.10603655129671097f);
+    p = __fmaf_rn(p, e, -0.15305592119693756f);
+    p = __fmaf_rn(p, e, 0.1967593878507614f);
+    p = __fmaf_rn(p, e, -0.24954134225845337f);
+    p = __fmaf_rn(p, e, 0.3332996368408203f);
+    p = __fmaf_rn(p, e, -0.4999990165233612f);
+    p = __fmaf_rn(p, e, 1.0f);
+    return __fmaf_rn(p, e, fmaxf(v, 0.0f));
+}
 
 // Column sums out[map(m)] = sum_r in[r][m], r < R, m < M, in a fixed order: 8
 // row slices per block, each summed in ascending rows, then joined in order.

@@ -57,7 +57,7 @@ bool wide(const void* p, int64_t stride, int64_t width, gdn_dtype_t t)
 
 bool rows_ok(const void* p, int64_t stride, int64_t width, gdn_dtype_t t)
 {
-    return p != nullptr && stride >= width && stride <= INT64_MAX / 8 && aligned(p, esize(t));
+    return p != nullptr && stride >= width && stride <= INT32_MAX && aligned(p, esize(t));
 }
 
 // ------------------------------------------------------------------- convolution
@@ -71,28 +71,28 @@ int conv_cx(int64_t nvec)
     return cx;
 }
 
-// Tokens per run.  A run reads W - 1 rows of its neighbour again and (backward)
-// leaves W + 1 partial sums per channel, so it is as long as 8 blocks of 128 threads
-// per SM allow, within [8, 64].
-int conv_run(int64_t T, int64_t nvec, int sms)
+// Tokens per run.  A run reads W - 1 rows of its neighbour again, loads the taps and
+// (backward) leaves W + 1 partial sums per channel, so it is as long as one full wave of
+// blocks allows (`resident` per SM), within [8, 512].
+int conv_run(int64_t T, int64_t nvec, int sms, int resident)
 {
-    const int64_t threads = (int64_t)sms * 1024;
-    const int64_t run = T * nvec / threads;
-    return (int)std::min<int64_t>(64, std::max<int64_t>(8, run / 8 * 8));
+    const int64_t threads = (int64_t)sms * resident * 128;
+    const int64_t run = ceil_div(T * nvec, threads);
+    return (int)std::max<int64_t>(8, std::min<int64_t>(512, ceil_div(run, 8) * 8));
 }
 
 // Grid of the convolution kernels for V channels per thread; false if it does not fit.
-bool conv_grid(gdn::ConvArgs& a, int V, bool state_tiles, unsigned* blocks)
+bool conv_grid(gdn::ConvArgs& a, int V, int resident, unsigned* blocks)
 {
     const int sms = sm_count();
     if (sms == 0) return false;
     const int64_t nvec = ceil_div(a.D, V);
     a.cx = conv_cx(nvec);
     a.ncb = (int32_t)ceil_div(nvec, a.cx);
-    a.run = conv_run(a.s.T, nvec, sms);
+    a.run = conv_run(a.s.T, (int64_t)a.ncb * a.cx, sms, resident);
     const int ny = 128 / a.cx;
     a.ntiles = ceil_div(a.s.T, (int64_t)a.run * ny);
-    const int64_t n = (a.ntiles + (state_tiles ? ceil_div(a.s.N, ny) : 0)) * a.ncb;
+    const int64_t n = (a.ntiles + ceil_div(a.s.N, ny)) * a.ncb;
     if (n > INT32_MAX) return false;
     *blocks = (unsigned)n;
     return true;
@@ -276,6 +276,7 @@ gdn::SsmArgs ssm_args(const gdn_ssm_t* s, int64_t Lc, int block_channels)
     a.D = s->channels; a.G = s->groups; a.Dg = s->channels / s->groups;
     a.cpg = (int32_t)ceil_div(a.Dg, block_channels);
     a.softplus = s->delta_softplus != 0;
+    a.bc16 = wide(s->B, s->B_stride, s->states, s->in_dtype) && wide(s->C, s->C_stride, s->states, s->in_dtype);
     a.Lc = Lc;
     return a;
 }
@@ -289,19 +290,25 @@ bool ssm_wide(const gdn_ssm_t* s)
            wide(s->z, s->z_stride, Dg, s->in_dtype);
 }
 
-template <typename T, int S, int V>
-gdn_status_t ssm_forward_launch(gdn::SsmArgs a, cudaStream_t st)
+template <typename T, int S, int V, int SEG>
+gdn_status_t ssm_forward_seg(gdn::SsmArgs a, cudaStream_t st)
 {
-    const int64_t slots = a.s.T / a.Lc + a.s.N, nb = (int64_t)a.G * a.cpg;
-    if (slots * nb > INT32_MAX) return GDN_ERR_INVALID_ARG;
-    const unsigned blocks = (unsigned)(slots * nb);
-    if (a.s.T > a.Lc) {
-        gdn::k_ssm_scan<T, S, V, 1><<<blocks, gdn::kSsmThreads, 0, st>>>(a);
-        const int64_t ids = (int64_t)a.s.N * a.D * (S / 4);
-        gdn::k_ssm_pass<S><<<(unsigned)ceil_div(ids, 128), 128, 0, st>>>(a);
-    }
-    gdn::k_ssm_scan<T, S, V, 0><<<blocks, gdn::kSsmThreads, 0, st>>>(a);
+    using Cf = gdn::SsmFwdCfg<T, S, SEG>;
+    a.cpg = (int32_t)ceil_div(a.Dg, Cf::CB);
+    const int64_t blocks = (int64_t)a.s.N * a.G * a.cpg;
+    if (blocks > INT32_MAX) return GDN_ERR_INVALID_ARG;
+    auto k = gdn::k_ssm_fwd<T, S, V, SEG>;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cf::BYTES) != cudaSuccess)
+        return GDN_ERR_CUDA;
+    k<<<(unsigned)blocks, Cf::THREADS, Cf::BYTES, st>>>(a);
     return launched() ? GDN_OK : GDN_ERR_CUDA;
+}
+
+template <typename T, int S, int V>
+gdn_status_t ssm_forward_launch(const gdn::SsmArgs& a, cudaStream_t st)
+{
+    if ((int64_t)a.s.N * a.D >= 16 * 1024) return ssm_forward_seg<T, S, V, 8>(a, st);
+    return ssm_forward_seg<T, S, V, 16>(a, st);
 }
 
 template <typename T, int S, int V>
@@ -391,14 +398,13 @@ gdn_status_t gdn_conv_forward(const void* x, int64_t x_stride, const void* weigh
     a.y = y; a.state_out = state_out; a.status = status;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool v16 = wide(x, x_stride, channels, in_dtype) && wide(y, channels, channels, in_dtype);
-    const int V = v16 ? (int)(16 / es) : 1;
     unsigned blocks = 0;
-    if (!conv_grid(a, V, true, &blocks)) return GDN_ERR_INVALID_ARG;
+    if (!conv_grid(a, v16 ? 2 : 1, 8, &blocks)) return GDN_ERR_INVALID_ARG;
     if (in_dtype == GDN_BF16) {
-        if (v16) launch_conv_fwd<__nv_bfloat16, 8>(a, width, blocks, st);
+        if (v16) launch_conv_fwd<__nv_bfloat16, 2>(a, width, blocks, st);
         else launch_conv_fwd<__nv_bfloat16, 1>(a, width, blocks, st);
     } else {
-        if (v16) launch_conv_fwd<float, 4>(a, width, blocks, st);
+        if (v16) launch_conv_fwd<float, 2>(a, width, blocks, st);
         else launch_conv_fwd<float, 1>(a, width, blocks, st);
     }
     return launched() ? GDN_OK : GDN_ERR_CUDA;
@@ -445,13 +451,13 @@ gdn_status_t gdn_conv_backward(const void* x, int64_t x_stride, const void* weig
     const bool v4 = wide(x, x_stride, channels, in_dtype) && wide(dy, dy_stride, channels, in_dtype) &&
                     wide(dx, channels, channels, in_dtype);
     unsigned blocks = 0;
-    if (!conv_grid(a, v4 ? 4 : 1, true, &blocks)) return GDN_ERR_INVALID_ARG;
+    if (!conv_grid(a, v4 ? 2 : 1, 4, &blocks)) return GDN_ERR_INVALID_ARG;
     if (blocks > 0) {
         if (in_dtype == GDN_BF16) {
-            if (v4) launch_conv_bwd<__nv_bfloat16, 4>(a, width, blocks, st);
+            if (v4) launch_conv_bwd<__nv_bfloat16, 2>(a, width, blocks, st);
             else launch_conv_bwd<__nv_bfloat16, 1>(a, width, blocks, st);
         } else {
-            if (v4) launch_conv_bwd<float, 4>(a, width, blocks, st);
+            if (v4) launch_conv_bwd<float, 2>(a, width, blocks, st);
             else launch_conv_bwd<float, 1>(a, width, blocks, st);
         }
     }
