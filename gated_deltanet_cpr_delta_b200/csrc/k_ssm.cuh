@@ -9,28 +9,14 @@
 // 16 a cycle against 128 fused multiply-adds, of which a state takes 4.  The
 // decay is 2^(delta A log2 e), with A log2 e formed once per lane.
 //
-// Lane layout.  S / 4 lanes share a channel, 4 states each; a lane holds the
-// same 4 states of 4 neighbouring channels (16 state elements, in packed fp32
-// pairs).  Per token it reads four float4 from shared memory (delta and delta x
-// of its channels, B and C of its states) for 16 elements, and the sums over
-// the states of 4 channels take 3 shuffles (each step halves the values that
-// a lane still carries), not 4 x 2.
-//
-// Time.  A sequence is cut into chunks of Lc tokens, so that a batch with few
-// channels fills the GPU: k_ssm_state finds each chunk's end state from zero,
-// k_ssm_pass carries the states over the chunks (h_end + exp(A sum delta) h_in),
-// and k_ssm_out runs every chunk from its true state.  That makes every
-// exponential twice; with enough channels Lc covers a sequence and only
-// k_ssm_out runs.
+// k_ssm_fwd serves prompts and training, k_ssm_step single tokens.
 #pragma once
 
 #include "layer_common.cuh"
 
 namespace gdn {
 
-constexpr int kSsmTile = 16;   // tokens staged together
 constexpr int kSsmSave = 32;   // saved states: one every 32 tokens of a sequence (GDN_SSM_CHUNK)
-constexpr int kSsmThreads = 128;
 
 struct SsmArgs {
     Seqs s;
@@ -41,290 +27,16 @@ struct SsmArgs {
     int32_t cpg;        // channel blocks per group
     int softplus;
     int bc16;           // rows of B and C in 16-byte accesses
-    int64_t Lc;         // tokens per chunk (a multiple of kSsmTile and kSsmSave)
     const float* state_in;
     void* y;
     float *state_out, *saved;
-    float *hbuf, *dsum;  // [slots][D][S] chunk states, [slots][D] sums of delta
     int32_t* status;
 };
-
-template <int S>
-struct SsmCfg {
-    static constexpr int LN = S / 4;              // lanes per channel
-    static constexpr int CW = 4 * (32 / LN);      // channels per warp
-    static constexpr int CB = CW * (kSsmThreads / 32);
-};
-
-// Sum over the LN lanes of a channel, of 4 values (one per channel of the
-// lane): returns the sum of channel ssm_own<LN>(lane).
-template <int LN>
-__device__ __forceinline__ float sum_channels(float v0, float v1, float v2, float v3, int q)
-{
-    constexpr int H1 = LN / 2, H2 = LN / 4;
-    const bool up = (q & H1) != 0;
-    const float s0 = up ? v0 : v2, s1 = up ? v1 : v3;
-    float k0 = up ? v2 : v0, k1 = up ? v3 : v1;
-    k0 += __shfl_xor_sync(kFullMask, s0, H1);
-    k1 += __shfl_xor_sync(kFullMask, s1, H1);
-    const bool odd = (q & H2) != 0;
-    const float s = odd ? k0 : k1;
-    float k = odd ? k1 : k0;
-    k += __shfl_xor_sync(kFullMask, s, H2);
-#pragma unroll
-    for (int o = H2 / 2; o > 0; o >>= 1) k += __shfl_xor_sync(kFullMask, k, o);
-    return k;
-}
-template <int LN>
-__device__ __forceinline__ int ssm_own(int q)
-{
-    return ((q & (LN / 2)) ? 2 : 0) + ((q & (LN / 4)) ? 1 : 0);
-}
 
 __device__ __forceinline__ float ssm_delta(const SsmArgs& a, float dt, float bias)
 {
     const float v = dt + bias;
     return a.softplus ? softplus(v) : v;
-}
-
-// MODE 0: outputs; MODE 1: the chunk's end state from zero and its sum of delta;
-// MODE 2: the adjoint of MODE 1, tokens in reverse: e = a (C dy' + e) from zero,
-// with dy' = dy silu(z) (x holds dy and B holds C), and the sum of delta
-template <typename T, int S, int V, int MODE>
-__global__ void __launch_bounds__(kSsmThreads) k_ssm_scan(const SsmArgs a)
-{
-    using Cf = SsmCfg<S>;
-    constexpr int LN = Cf::LN, CW = Cf::CW, CB = Cf::CB;
-    constexpr int PER_ROW = CB / V;                            // vectors per token row
-    constexpr int NVEC = (kSsmTile * PER_ROW + kSsmThreads - 1) / kSsmThreads;
-    constexpr int RSTEP = kSsmThreads / PER_ROW;               // rows between a thread's vectors
-    static_assert(kSsmThreads % PER_ROW == 0, "a thread's vectors share their columns");
-    __shared__ __align__(16) float sd[kSsmTile][CB];           // delta, then the sums over the states
-    __shared__ __align__(16) float su[kSsmTile][CB];           // delta x
-    __shared__ __align__(16) float sB[kSsmTile][S], sC[kSsmTile][S];
-
-    if (MODE == 0 && blockIdx.x == 0) check_seqs(a.s, a.status);
-    const int nb = a.G * a.cpg;
-    const int64_t slot = blockIdx.x / nb;
-    const int cb = (int)(blockIdx.x - slot * nb), e = cb / a.cpg;
-    const int cbase = e * a.Dg + (cb - e * a.cpg) * CB, cend = (e + 1) * a.Dg;  // this block's channels, below cend
-    const int n = a.s.find_slot(slot, a.Lc);
-    const int64_t lo = a.s.lo(n), L = a.s.hi(n) - lo, chunk = slot - a.s.first_slot(n, a.Lc);
-    const int64_t nch = L > 0 ? (L + a.Lc - 1) / a.Lc : 1;
-    if (chunk < 0 || chunk >= nch || (MODE == 1 && chunk == nch - 1) || (MODE == 2 && chunk == 0)) return;
-    const int64_t p0 = chunk * a.Lc, p1 = min(p0 + a.Lc, L);
-
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int q = lane & (LN - 1);
-    const int col = warp * CW + (lane / LN) * 4;               // the lane's first column of the block
-    // A log2 e and the state of the lane's 4 channels x 4 states
-    f2x A2[4][2], h[4][2];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int c = cbase + col + i;
-        float4 av = make_float4(0.f, 0.f, 0.f, 0.f), hv = av;
-        if (c < cend) {
-            av = *reinterpret_cast<const float4*>(a.A + (int64_t)c * S + 4 * q);
-            if (MODE == 0) {
-                const float* src = nullptr;
-                if (nch > 1) src = a.hbuf + (slot * a.D + c) * S;
-                else if (a.state_in != nullptr) src = a.state_in + ((int64_t)n * a.D + c) * S;
-                if (src != nullptr) hv = *reinterpret_cast<const float4*>(src + 4 * q);
-            }
-        }
-        A2[i][0] = pk2(av.x * kLog2e, av.y * kLog2e);
-        A2[i][1] = pk2(av.z * kLog2e, av.w * kLog2e);
-        h[i][0] = pk2(hv.x, hv.y);
-        h[i][1] = pk2(hv.z, hv.w);
-    }
-    float dsum[4] = {0.f, 0.f, 0.f, 0.f};
-
-    // staging: thread -> columns vc .. vc + V - 1, rows vr, vr + RSTEP, ...
-    const int vc = (tid % PER_ROW) * V, vr = tid / PER_ROW;
-    const bool vok = cbase + vc < cend;  // V divides Dg and cbase where V > 1
-    float bias[V], Dv[V];
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-        bias[k] = vok && a.dt_bias != nullptr ? a.dt_bias[cbase + vc + k] : 0.0f;
-        Dv[k] = MODE == 0 && vok && a.Dp != nullptr ? a.Dp[cbase + vc + k] : 0.0f;
-    }
-    const T* x = static_cast<const T*>(a.x) + cbase + vc;
-    const T* dt = static_cast<const T*>(a.dt) + cbase + vc;
-    const T* z = a.z != nullptr ? static_cast<const T*>(a.z) + cbase + vc : nullptr;
-    const T* B = static_cast<const T*>(a.B) + e * S;
-    const T* C = static_cast<const T*>(a.C) + e * S;
-
-    Vec<T, V> rx[NVEC], rd[NVEC], rz[NVEC];
-    auto fetch = [&](int64_t p) {
-#pragma unroll
-        for (int i = 0; i < NVEC; ++i) {
-            const int r = vr + i * RSTEP;
-            if (vok && r < kSsmTile && p + r < p1) {
-                const int64_t row = lo + p + r;
-                rx[i] = load_vec<T, V>(x + row * a.ldx);
-                rd[i] = load_vec<T, V>(dt + row * a.lddt);
-                if (MODE != 1 && z != nullptr) rz[i] = load_vec<T, V>(z + row * a.ldz);
-            }
-        }
-    };
-    const int64_t ntile = (p1 - p0 + kSsmTile - 1) / kSsmTile;
-    auto tile_at = [&](int64_t i) { return p0 + (MODE == 2 ? ntile - 1 - i : i) * kSsmTile; };
-    if (ntile > 0) fetch(tile_at(0));
-    for (int64_t it = 0; it < ntile; ++it) {
-        const int64_t p = tile_at(it);
-        const int rows = (int)min((int64_t)kSsmTile, p1 - p);
-        if (MODE == 0 && a.saved != nullptr && p % kSsmSave == 0) {
-            const int64_t at = a.s.first_slot(n, kSsmSave) + p / kSsmSave;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int c = cbase + col + i;
-                float4 v;
-                up2(h[i][0], v.x, v.y);
-                up2(h[i][1], v.z, v.w);
-                if (c < cend) *reinterpret_cast<float4*>(a.saved + (at * a.D + c) * S + 4 * q) = v;
-            }
-        }
-        Vec<T, V> kx[NVEC], kz[NVEC];  // this tile's x and z, for the epilogue
-#pragma unroll
-        for (int i = 0; i < NVEC; ++i) {
-            const int r = vr + i * RSTEP;
-            kx[i] = rx[i];
-            kz[i] = rz[i];
-            if (r < kSsmTile) {
-#pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    const bool in = vok && r < rows;
-                    const float d = in ? ssm_delta(a, to_f<T>(rd[i].v[k]), bias[k]) : 0.0f;
-                    sd[r][vc + k] = d;
-                    float u = to_f<T>(rx[i].v[k]);
-                    if (MODE != 2) u *= d;
-                    else if (z != nullptr) u *= silu(to_f<T>(rz[i].v[k]));
-                    su[r][vc + k] = in ? u : 0.0f;
-                }
-            }
-        }
-        for (int i = tid; i < kSsmTile * S; i += kSsmThreads) {
-            const int r = i / S, s = i % S;
-            if (r < rows) {
-                sB[r][s] = to_f<T>(B[(lo + p + r) * a.ldB + s]);
-                if (MODE == 0) sC[r][s] = to_f<T>(C[(lo + p + r) * a.ldC + s]);
-            }
-        }
-        __syncthreads();
-        if (it + 1 < ntile) fetch(tile_at(it + 1));
-#pragma unroll 2
-        for (int j = 0; j < rows; ++j) {
-            const int t = MODE == 2 ? rows - 1 - j : j;
-            const float4 d4 = *reinterpret_cast<const float4*>(&sd[t][col]);
-            const float4 u4 = *reinterpret_cast<const float4*>(&su[t][col]);
-            const ulonglong2 b4 = *reinterpret_cast<const ulonglong2*>(&sB[t][4 * q]);
-            ulonglong2 c4 = b4;
-            if (MODE == 0) c4 = *reinterpret_cast<const ulonglong2*>(&sC[t][4 * q]);
-            const float d[4] = {d4.x, d4.y, d4.z, d4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w};
-            float o[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const f2x d2 = pk2(d[i], d[i]), u2 = pk2(u[i], u[i]);
-                const f2x g0 = fmul2(d2, A2[i][0]), g1 = fmul2(d2, A2[i][1]);
-                float e0, e1, e2, e3;
-                up2(g0, e0, e1);
-                up2(g1, e2, e3);
-                const f2x a0 = pk2(ex2(e0), ex2(e1)), a1 = pk2(ex2(e2), ex2(e3));
-                if (MODE == 2) {
-                    h[i][0] = fmul2(a0, ffma2(u2, b4.x, h[i][0]));
-                    h[i][1] = fmul2(a1, ffma2(u2, b4.y, h[i][1]));
-                } else {
-                    h[i][0] = ffma2(a0, h[i][0], fmul2(u2, b4.x));
-                    h[i][1] = ffma2(a1, h[i][1], fmul2(u2, b4.y));
-                }
-                if (MODE == 0) {
-                    const f2x y2 = ffma2(h[i][1], c4.y, fmul2(h[i][0], c4.x));
-                    float ya, yb;
-                    up2(y2, ya, yb);
-                    o[i] = ya + yb;
-                } else {
-                    dsum[i] += d[i];
-                }
-            }
-            if (MODE == 0) {
-                const float s = sum_channels<LN>(o[0], o[1], o[2], o[3], q);
-                // the row's delta has been read by every lane of the warp (the shuffles order it)
-                if (LN == 4 || (q & (LN / 4 - 1)) == 0) sd[t][col + ssm_own<LN>(q)] = s;
-            }
-        }
-        __syncthreads();
-        if (MODE == 0) {
-            T* y = static_cast<T*>(a.y) + cbase + vc;
-#pragma unroll
-            for (int i = 0; i < NVEC; ++i) {
-                const int r = vr + i * RSTEP;
-                if (vok && r < rows) {
-                    float o[V];
-#pragma unroll
-                    for (int k = 0; k < V; ++k) {
-                        o[k] = __fmaf_rn(Dv[k], to_f<T>(kx[i].v[k]), sd[r][vc + k]);
-                        if (z != nullptr) o[k] *= silu(to_f<T>(kz[i].v[k]));
-                    }
-                    store_vec<T, V>(y + (lo + p + r) * a.D, o);
-                }
-            }
-            __syncthreads();  // sd is rewritten for the next tile
-        }
-    }
-    // the end state
-    float* out = nullptr;
-    if (MODE != 0) out = a.hbuf + slot * a.D * S;
-    else if (chunk == nch - 1) out = a.state_out + (int64_t)n * a.D * S;
-    if (out != nullptr) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = cbase + col + i;
-            float4 v;
-            up2(h[i][0], v.x, v.y);
-            up2(h[i][1], v.z, v.w);
-            if (c < cend) {
-                *reinterpret_cast<float4*>(out + (int64_t)c * S + 4 * q) = v;
-                if (MODE != 0 && q == 0) a.dsum[slot * a.D + c] = dsum[i];
-            }
-        }
-    }
-}
-
-// Carries the states over the chunks of a sequence that has more than one:
-// hbuf[chunk] becomes the state before the chunk.  One thread per 4 states.
-template <int S>
-__global__ void __launch_bounds__(128) k_ssm_pass(const SsmArgs a)
-{
-    const int64_t per = (int64_t)a.D * (S / 4);
-    const int64_t id = (int64_t)blockIdx.x * 128 + threadIdx.x;
-    if (id >= per * a.s.N) return;
-    const int n = (int)(id / per);
-    const int64_t r = id - n * per;
-    const int c = (int)(r / (S / 4)), s = (int)(r % (S / 4)) * 4;
-    const int64_t L = a.s.hi(n) - a.s.lo(n), nch = (L + a.Lc - 1) / a.Lc;
-    if (nch <= 1) return;
-    const float4 av = *reinterpret_cast<const float4*>(a.A + (int64_t)c * S + s);
-    const float A2[4] = {av.x * kLog2e, av.y * kLog2e, av.z * kLog2e, av.w * kLog2e};
-    float h[4] = {0.f, 0.f, 0.f, 0.f};
-    if (a.state_in != nullptr) {
-        const float4 v = *reinterpret_cast<const float4*>(a.state_in + ((int64_t)n * a.D + c) * S + s);
-        h[0] = v.x, h[1] = v.y, h[2] = v.z, h[3] = v.w;
-    }
-    int64_t slot = a.s.first_slot(n, a.Lc);
-    for (int64_t k = 0; k < nch; ++k, ++slot) {
-        float4* p = reinterpret_cast<float4*>(a.hbuf + (slot * a.D + c) * S + s);
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        float d = 0.0f;
-        if (k + 1 < nch) {  // the last chunk's end state is not needed
-            v = *p;
-            d = a.dsum[slot * a.D + c];
-        }
-        *p = make_float4(h[0], h[1], h[2], h[3]);
-        h[0] = __fmaf_rn(ex2(d * A2[0]), h[0], v.x);
-        h[1] = __fmaf_rn(ex2(d * A2[1]), h[1], v.y);
-        h[2] = __fmaf_rn(ex2(d * A2[2]), h[2], v.z);
-        h[3] = __fmaf_rn(ex2(d * A2[3]), h[3], v.w);
-    }
 }
 
 // ------------------------------------------------------------------ forward

@@ -9,9 +9,9 @@
 //     dA   = sum_t delta g (a_t h_{t-1})
 //     ddelta = sum_s g (a_t h_{t-1}) A + x sum_s g B,   ddt = ddelta softplus'(dt + bias)
 //
-// Time is cut into chunks of Lc tokens as in the forward: k_ssm_scan MODE 2 and
-// k_ssm_bwd_pass find the e that enters each chunk, then k_ssm_bwd walks the
-// chunks in parallel.  A chunk is walked in reverse in parts of 32 tokens, each
+// Time is cut into chunks of Lc tokens, so that few channels fill the GPU: k_ssm_rev finds
+// each chunk's e from zero, k_ssm_bwd_pass carries it over the chunks, then k_ssm_bwd walks
+// the chunks in parallel.  A chunk is walked in reverse in parts of 32 tokens, each
 // from the state that the forward saved there.  A part runs forward once,
 // leaving the state before every 4th token in shared memory; then the 4-token
 // tiles run in reverse: a tile is recomputed from its state, its 4 decays and
@@ -29,8 +29,45 @@
 
 namespace gdn {
 
+constexpr int kSsmThreads = 128;
+constexpr int kSsmTile = 16;   // tokens that k_ssm_rev stages together
+
+template <int S>
+struct SsmRevCfg {
+    static constexpr int LN = S / 4;              // lanes per channel
+    static constexpr int CW = 4 * (32 / LN);      // channels per warp
+    static constexpr int CB = CW * (kSsmThreads / 32);
+};
+
+// Sum over the LN lanes of a channel, of 4 values (one per channel of the
+// lane): returns the sum of channel ssm_own<LN>(lane).
+template <int LN>
+__device__ __forceinline__ float sum_channels(float v0, float v1, float v2, float v3, int q)
+{
+    constexpr int H1 = LN / 2, H2 = LN / 4;
+    const bool up = (q & H1) != 0;
+    const float s0 = up ? v0 : v2, s1 = up ? v1 : v3;
+    float k0 = up ? v2 : v0, k1 = up ? v3 : v1;
+    k0 += __shfl_xor_sync(kFullMask, s0, H1);
+    k1 += __shfl_xor_sync(kFullMask, s1, H1);
+    const bool odd = (q & H2) != 0;
+    const float s = odd ? k0 : k1;
+    float k = odd ? k1 : k0;
+    k += __shfl_xor_sync(kFullMask, s, H2);
+#pragma unroll
+    for (int o = H2 / 2; o > 0; o >>= 1) k += __shfl_xor_sync(kFullMask, k, o);
+    return k;
+}
+template <int LN>
+__device__ __forceinline__ int ssm_own(int q)
+{
+    return ((q & (LN / 2)) ? 2 : 0) + ((q & (LN / 4)) ? 1 : 0);
+}
+
 struct SsmBwdArgs {
-    SsmArgs f;          // f.hbuf: the adjoint that enters each chunk from behind
+    SsmArgs f;
+    int64_t Lc;         // tokens per chunk (a multiple of kSsmTile and kSsmSave)
+    float *ebuf, *dsum; // [slots][D][S] the adjoint that enters each chunk from behind, [slots][D] sums of delta
     const void* dy;
     int64_t lddy;
     const float* dstate_out;
@@ -51,18 +88,144 @@ struct SsmBwdCfg {
     static constexpr size_t SMEM = sizeof(float) * (4 * kSsmSave * CB + 2 * kSsmSave * S + 4 * NT * SLOT);
 };
 
-// Carries the adjoint back over the chunks: hbuf[chunk] becomes the gradient
+// The adjoint of a chunk from zero, tokens in reverse: e = a (C dy' + e), and the chunk's
+// sum of delta.  S / 4 lanes share 4 channels, 4 states each; the tokens are staged 16 at a time.
+template <typename T, int S, int V>
+__global__ void __launch_bounds__(kSsmThreads, 4) k_ssm_rev(const SsmBwdArgs b)
+{
+    using Cf = SsmRevCfg<S>;
+    constexpr int LN = Cf::LN, CW = Cf::CW, CB = Cf::CB, TT = kSsmTile;
+    constexpr int PER_ROW = CB / V;                            // vectors per token row
+    constexpr int NVEC = (TT * PER_ROW + kSsmThreads - 1) / kSsmThreads;
+    constexpr int RSTEP = kSsmThreads / PER_ROW;               // rows between a thread's vectors
+    constexpr int NC = TT * S / kSsmThreads;                   // elements of C per thread and tile
+    static_assert(kSsmThreads % PER_ROW == 0, "a thread's vectors share their columns");
+    __shared__ __align__(16) float sd[TT][CB];                 // delta
+    __shared__ __align__(16) float su[TT][CB];                 // dy'
+    __shared__ __align__(16) float sC[TT][S];
+
+    const SsmArgs& a = b.f;
+    const int cpg = (a.Dg + CB - 1) / CB, nb = a.G * cpg;
+    const int64_t slot = blockIdx.x / nb;
+    const int cb = (int)(blockIdx.x - slot * nb), e = cb / cpg;
+    const int cbase = e * a.Dg + (cb - e * cpg) * CB, cend = (e + 1) * a.Dg;  // this block's channels, below cend
+    const int n = a.s.find_slot(slot, b.Lc);
+    const int64_t lo = a.s.lo(n), L = a.s.hi(n) - lo, chunk = slot - a.s.first_slot(n, b.Lc);
+    const int64_t nch = L > 0 ? (L + b.Lc - 1) / b.Lc : 1;
+    if (chunk < 1 || chunk >= nch) return;                     // the first chunk's is made by its own walk
+    const int64_t p0 = chunk * b.Lc, p1 = min(p0 + b.Lc, L);
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int q = lane & (LN - 1);
+    const int col = warp * CW + (lane / LN) * 4;               // the lane's first column of the block
+    f2x A2[4][2], h[4][2];                                     // A log2 e, and the adjoint
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int c = cbase + col + i;
+        float4 av = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c < cend) av = *reinterpret_cast<const float4*>(a.A + (int64_t)c * S + 4 * q);
+        A2[i][0] = pk2(av.x * kLog2e, av.y * kLog2e);
+        A2[i][1] = pk2(av.z * kLog2e, av.w * kLog2e);
+        h[i][0] = h[i][1] = pk2(0.f, 0.f);
+    }
+    float dsum[4] = {0.f, 0.f, 0.f, 0.f};
+
+    const int vc = (tid % PER_ROW) * V, vr = tid / PER_ROW;
+    const bool vok = cbase + vc < cend;  // V divides Dg and cbase where V > 1
+    const float* bias = a.dt_bias != nullptr && vok ? a.dt_bias + cbase + vc : nullptr;
+    const T* x = static_cast<const T*>(b.dy) + cbase + vc;
+    const T* dt = static_cast<const T*>(a.dt) + cbase + vc;
+    const T* z = a.z != nullptr ? static_cast<const T*>(a.z) + cbase + vc : nullptr;
+    const T* C = static_cast<const T*>(a.C) + e * S;
+
+    Vec<T, V> rx[NVEC], rd[NVEC], rz[NVEC];
+    T rc[NC];
+    auto fetch = [&](int64_t p) {
+#pragma unroll
+        for (int i = 0; i < NVEC; ++i) {
+            const int r = vr + i * RSTEP;
+            if (vok && r < TT && p + r < p1) {
+                const int64_t row = lo + p + r;
+                rx[i] = load_vec<T, V>(x + row * b.lddy);
+                rd[i] = load_vec<T, V>(dt + row * a.lddt);
+                if (z != nullptr) rz[i] = load_vec<T, V>(z + row * a.ldz);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int r = (i * kSsmThreads + tid) / S, s = (i * kSsmThreads + tid) % S;
+            if (p + r < p1) rc[i] = C[(lo + p + r) * a.ldC + s];
+        }
+    };
+    const int64_t ntile = (p1 - p0 + TT - 1) / TT;
+    fetch(p0 + (ntile - 1) * TT);
+    for (int64_t it = ntile - 1; it >= 0; --it) {
+        const int64_t p = p0 + it * TT;
+        const int rows = (int)min((int64_t)TT, p1 - p);
+#pragma unroll
+        for (int i = 0; i < NVEC; ++i) {
+            const int r = vr + i * RSTEP;
+            if (r < TT) {
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    const bool in = vok && r < rows;
+                    float u = to_f<T>(rx[i].v[k]);
+                    if (z != nullptr) u *= silu(to_f<T>(rz[i].v[k]));
+                    sd[r][vc + k] = in ? ssm_delta(a, to_f<T>(rd[i].v[k]), bias != nullptr ? bias[k] : 0.0f) : 0.0f;
+                    su[r][vc + k] = in ? u : 0.0f;
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NC; ++i) (&sC[0][0])[i * kSsmThreads + tid] = to_f<T>(rc[i]);
+        __syncthreads();
+        if (it > 0) fetch(p - TT);
+#pragma unroll 2
+        for (int t = rows - 1; t >= 0; --t) {
+            const float4 d4 = *reinterpret_cast<const float4*>(&sd[t][col]);
+            const float4 u4 = *reinterpret_cast<const float4*>(&su[t][col]);
+            const ulonglong2 c4 = *reinterpret_cast<const ulonglong2*>(&sC[t][4 * q]);
+            const float d[4] = {d4.x, d4.y, d4.z, d4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const f2x d2 = pk2(d[i], d[i]), u2 = pk2(u[i], u[i]);
+                float e0, e1, e2, e3;
+                up2(fmul2(d2, A2[i][0]), e0, e1);
+                up2(fmul2(d2, A2[i][1]), e2, e3);
+                h[i][0] = fmul2(pk2(ex2(e0), ex2(e1)), ffma2(u2, c4.x, h[i][0]));
+                h[i][1] = fmul2(pk2(ex2(e2), ex2(e3)), ffma2(u2, c4.y, h[i][1]));
+                dsum[i] += d[i];
+            }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int c = cbase + col + i;
+        float4 v;
+        up2(h[i][0], v.x, v.y);
+        up2(h[i][1], v.z, v.w);
+        if (c < cend) {
+            *reinterpret_cast<float4*>(b.ebuf + (slot * a.D + c) * S + 4 * q) = v;
+            if (q == 0) b.dsum[slot * a.D + c] = dsum[i];
+        }
+    }
+}
+
+// Carries the adjoint back over the chunks: ebuf[chunk] becomes the gradient
 // for the state after the chunk.
 template <int S>
-__global__ void __launch_bounds__(128) k_ssm_bwd_pass(const SsmArgs a, const float* dstate_out)
+__global__ void __launch_bounds__(128) k_ssm_bwd_pass(const SsmBwdArgs b)
 {
+    const SsmArgs& a = b.f;
+    const float* dstate_out = b.dstate_out;
     const int64_t per = (int64_t)a.D * (S / 4);
     const int64_t id = (int64_t)blockIdx.x * 128 + threadIdx.x;
     if (id >= per * a.s.N) return;
     const int n = (int)(id / per);
     const int64_t r = id - n * per;
     const int c = (int)(r / (S / 4)), s = (int)(r % (S / 4)) * 4;
-    const int64_t L = a.s.hi(n) - a.s.lo(n), nch = (L + a.Lc - 1) / a.Lc;
+    const int64_t L = a.s.hi(n) - a.s.lo(n), nch = (L + b.Lc - 1) / b.Lc;
     if (nch <= 1) return;
     const float4 av = *reinterpret_cast<const float4*>(a.A + (int64_t)c * S + s);
     const float A2[4] = {av.x * kLog2e, av.y * kLog2e, av.z * kLog2e, av.w * kLog2e};
@@ -72,13 +235,13 @@ __global__ void __launch_bounds__(128) k_ssm_bwd_pass(const SsmArgs a, const flo
         e[0] = v.x, e[1] = v.y, e[2] = v.z, e[3] = v.w;
     }
     for (int64_t k = nch - 1; k >= 0; --k) {
-        const int64_t slot = a.s.first_slot(n, a.Lc) + k;
-        float4* p = reinterpret_cast<float4*>(a.hbuf + (slot * a.D + c) * S + s);
+        const int64_t slot = a.s.first_slot(n, b.Lc) + k;
+        float4* p = reinterpret_cast<float4*>(b.ebuf + (slot * a.D + c) * S + s);
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         float d = 0.0f;
         if (k > 0) {  // the first chunk's part is made by its own walk
             v = *p;
-            d = a.dsum[slot * a.D + c];
+            d = b.dsum[slot * a.D + c];
         }
         *p = make_float4(e[0], e[1], e[2], e[3]);
         e[0] = __fmaf_rn(ex2(d * A2[0]), e[0], v.x);
@@ -109,6 +272,8 @@ __device__ __forceinline__ void sum_groups(float (&v)[8], int lane)
     }
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 template <typename T, int S, int V, bool GATE>
 __global__ void __launch_bounds__(kSsmThreads, 3) k_ssm_bwd(const SsmBwdArgs b)
 {
@@ -132,11 +297,11 @@ __global__ void __launch_bounds__(kSsmThreads, 3) k_ssm_bwd(const SsmBwdArgs b)
     const int64_t slot = blockIdx.x / nb;
     const int cb = (int)(blockIdx.x - slot * nb), e = cb / a.cpg, cbg = cb - e * a.cpg;
     const int cbase = e * a.Dg + cbg * CB, cend = (e + 1) * a.Dg;
-    const int n = a.s.find_slot(slot, a.Lc);
-    const int64_t lo = a.s.lo(n), L = a.s.hi(n) - lo, chunk = slot - a.s.first_slot(n, a.Lc);
-    const int64_t nch = L > 0 ? (L + a.Lc - 1) / a.Lc : 1;
+    const int n = a.s.find_slot(slot, b.Lc);
+    const int64_t lo = a.s.lo(n), L = a.s.hi(n) - lo, chunk = slot - a.s.first_slot(n, b.Lc);
+    const int64_t nch = L > 0 ? (L + b.Lc - 1) / b.Lc : 1;
     const bool idle = chunk < 0 || chunk >= nch;
-    const int64_t p0 = idle ? 0 : chunk * a.Lc, p1 = idle ? 0 : min(p0 + a.Lc, L);
+    const int64_t p0 = idle ? 0 : chunk * b.Lc, p1 = idle ? 0 : min(p0 + b.Lc, L);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int q = lane & (LN - 1);
@@ -150,7 +315,7 @@ __global__ void __launch_bounds__(kSsmThreads, 3) k_ssm_bwd(const SsmBwdArgs b)
         if (c < cend && !idle) {
             av = *reinterpret_cast<const float4*>(a.A + (int64_t)c * S + 4 * q);
             const float* src = nullptr;
-            if (nch > 1) src = a.hbuf + (slot * a.D + c) * S;
+            if (nch > 1) src = b.ebuf + (slot * a.D + c) * S;
             else if (b.dstate_out != nullptr) src = b.dstate_out + ((int64_t)n * a.D + c) * S;
             if (src != nullptr) w = *reinterpret_cast<const float4*>(src + 4 * q);
         }
@@ -199,6 +364,17 @@ __global__ void __launch_bounds__(kSsmThreads, 3) k_ssm_bwd(const SsmBwdArgs b)
 
     for (int64_t p = p0 + (p1 > p0 ? (p1 - p0 - 1) / P * P : -1); p >= p0; p -= P) {
         const int rows = (int)min((int64_t)P, p1 - p);
+        if (p > p0) {  // the part before this one, on its way to L2
+            for (int r = vr; r < P; r += RSTEP) {
+                if (vok) {
+                    const int64_t row = lo + p - P + r;
+                    prefetch_l2(x + row * a.ldx);
+                    prefetch_l2(dt + row * a.lddt);
+                    prefetch_l2(dy + row * b.lddy);
+                    if (GATE) prefetch_l2(z + row * a.ldz);
+                }
+            }
+        }
         for (int r = vr; r < P; r += RSTEP) {
             const bool in = vok && r < rows;
             Vec<T, V> wx, wd, wg, wz;

@@ -195,29 +195,21 @@ int64_t norm_parts(int64_t rows) { return std::max<int64_t>(1, std::min<int64_t>
 
 // ------------------------------------------------------------------- scan
 
-// Tokens per chunk: enough chunks that `warps` warps are at work, at least
-// `least` tokens; T or more means that no sequence is cut.
-int64_t ssm_chunk(int64_t T, int32_t D, int32_t S, int channels_per_warp, int64_t least, int64_t warps)
+// Tokens per chunk of the backward: about 32 warps per SM over the whole batch, at least 64.
+// T or more means that no sequence is cut.
+int64_t ssm_bwd_chunk(int64_t T, int32_t D, int32_t S)
 {
-    (void)S;
-    const int64_t across = ceil_div(D, channels_per_warp);
-    const int64_t chunks = std::max<int64_t>(1, warps / across);
-    const int64_t len = ceil_div(ceil_div(T, chunks), gdn::kSsmSave) * gdn::kSsmSave;
-    return std::max<int64_t>(len, least);
+    const int64_t across = ceil_div(D, 2 * 128 / S);  // warps that walk one sequence
+    const int64_t chunks = std::max<int64_t>(1, 148 * 32 / across);
+    return std::max<int64_t>(64, ceil_div(ceil_div(T, chunks), gdn::kSsmSave) * gdn::kSsmSave);
 }
 
-constexpr int64_t kSsmWarps = 148 * 8;
-constexpr int64_t kSsmLeast = 64;
-
-int64_t ssm_fwd_chunk(int64_t T, int32_t D, int32_t S) { return ssm_chunk(T, D, S, 4 * 128 / S, kSsmLeast, kSsmWarps); }
-int64_t ssm_bwd_chunk(int64_t T, int32_t D, int32_t S) { return ssm_chunk(T, D, S, 2 * 128 / S, kSsmLeast, kSsmWarps); }
-
 struct SsmWorkspace {
-    float *hbuf, *dsum, *partA, *partD, *partBC;
+    float *ebuf, *dsum, *partA, *partD, *partBC;
     size_t bytes;
 };
 
-SsmWorkspace ssm_carve(void* base, int64_t T, int32_t N, int32_t D, int32_t G, int32_t S, bool backward)
+SsmWorkspace ssm_carve(void* base, int64_t T, int32_t N, int32_t D, int32_t G, int32_t S)
 {
     SsmWorkspace w{};
     size_t off = 0;
@@ -227,18 +219,15 @@ SsmWorkspace ssm_carve(void* base, int64_t T, int32_t N, int32_t D, int32_t G, i
         off = align_up(off + sizeof(float) * floats);
         return p;
     };
-    const int64_t Lc = backward ? ssm_bwd_chunk(T, D, S) : ssm_fwd_chunk(T, D, S);
+    const int64_t Lc = ssm_bwd_chunk(T, D, S), cpg = ceil_div(D / G, 2 * 128 / S * 4);
     const size_t slots = (size_t)(T / Lc + N), per = (size_t)D * S;
     if (T > Lc) {
-        w.hbuf = take(slots * per);
+        w.ebuf = take(slots * per);
         w.dsum = take(slots * D);
     }
-    if (backward) {
-        const int64_t cpg = ceil_div(D / G, 2 * 128 / S * 4);
-        w.partA = take(slots * per);
-        w.partD = take(slots * 2 * D);
-        w.partBC = take((size_t)cpg * T * G * 2 * S);
-    }
+    w.partA = take(slots * per);
+    w.partD = take(slots * 2 * D);
+    w.partBC = take((size_t)cpg * T * G * 2 * S);
     w.bytes = std::max<size_t>(off, kAlign);
     return w;
 }
@@ -266,7 +255,7 @@ gdn_status_t ssm_check(const gdn_ssm_t* s, bool step)
     return GDN_OK;
 }
 
-gdn::SsmArgs ssm_args(const gdn_ssm_t* s, int64_t Lc, int block_channels)
+gdn::SsmArgs ssm_args(const gdn_ssm_t* s, int block_channels)
 {
     gdn::SsmArgs a{};
     a.s = Seqs{s->cu_seqlens, s->num_seqs, s->total_tokens};
@@ -277,7 +266,6 @@ gdn::SsmArgs ssm_args(const gdn_ssm_t* s, int64_t Lc, int block_channels)
     a.cpg = (int32_t)ceil_div(a.Dg, block_channels);
     a.softplus = s->delta_softplus != 0;
     a.bc16 = wide(s->B, s->B_stride, s->states, s->in_dtype) && wide(s->C, s->C_stride, s->states, s->in_dtype);
-    a.Lc = Lc;
     return a;
 }
 
@@ -312,22 +300,17 @@ gdn_status_t ssm_forward_launch(const gdn::SsmArgs& a, cudaStream_t st)
 }
 
 template <typename T, int S, int V>
-gdn_status_t ssm_backward_launch(const gdn::SsmBwdArgs& b, int scan_cpg, void* dB, void* dC, float* dA, float* dD,
-                                 float* ddt_bias, cudaStream_t st)
+gdn_status_t ssm_backward_launch(const gdn::SsmBwdArgs& b, void* dB, void* dC, float* dA, float* dD, float* ddt_bias,
+                                 cudaStream_t st)
 {
     const gdn::SsmArgs& a = b.f;
-    const int64_t slots = a.s.T / a.Lc + a.s.N;
-    if (slots * a.G * std::max(a.cpg, scan_cpg) > INT32_MAX) return GDN_ERR_INVALID_ARG;
-    if (a.s.T > a.Lc) {
-        gdn::SsmArgs r = a;  // the reverse scan: x is dy, B is C
-        r.x = b.dy;
-        r.ldx = b.lddy;
-        r.B = a.C;
-        r.ldB = a.ldC;
-        r.cpg = scan_cpg;
-        gdn::k_ssm_scan<T, S, V, 2><<<(unsigned)(slots * a.G * scan_cpg), gdn::kSsmThreads, 0, st>>>(r);
+    const int64_t slots = a.s.T / b.Lc + a.s.N;
+    if (slots * a.G * a.cpg > INT32_MAX) return GDN_ERR_INVALID_ARG;
+    if (a.s.T > b.Lc) {
+        const int64_t rev = slots * a.G * ceil_div(a.Dg, gdn::SsmRevCfg<S>::CB);
+        gdn::k_ssm_rev<T, S, V><<<(unsigned)rev, gdn::kSsmThreads, 0, st>>>(b);
         const int64_t ids = (int64_t)a.s.N * a.D * (S / 4);
-        gdn::k_ssm_bwd_pass<S><<<(unsigned)ceil_div(ids, 128), 128, 0, st>>>(a, b.dstate_out);
+        gdn::k_ssm_bwd_pass<S><<<(unsigned)ceil_div(ids, 128), 128, 0, st>>>(b);
     }
     constexpr size_t sm = gdn::SsmBwdCfg<S>::SMEM;
     auto k = a.z != nullptr ? gdn::k_ssm_bwd<T, S, V, true> : gdn::k_ssm_bwd<T, S, V, false>;
@@ -602,24 +585,17 @@ int64_t gdn_ssm_num_chunk_states(int64_t total_tokens, int32_t num_seqs)
     return total_tokens / GDN_SSM_CHUNK + num_seqs;
 }
 
-size_t gdn_ssm_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t channels, int32_t states)
-{
-    if (total_tokens < 0 || num_seqs < 0 || channels <= 0 || (states != 16 && states != 32 && states != 64)) return 0;
-    return ssm_carve(nullptr, total_tokens, num_seqs, channels, 1, states, false).bytes;
-}
-
 size_t gdn_ssm_backward_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t channels, int32_t groups,
                                        int32_t states)
 {
     if (total_tokens < 0 || num_seqs < 0 || channels <= 0 || groups <= 0 || channels % groups != 0 ||
         (states != 16 && states != 32 && states != 64))
         return 0;
-    return ssm_carve(nullptr, total_tokens, num_seqs, channels, groups, states, true).bytes;
+    return ssm_carve(nullptr, total_tokens, num_seqs, channels, groups, states).bytes;
 }
 
 gdn_status_t gdn_ssm_forward(const gdn_ssm_t* args, const float* state_in, void* y, float* state_out,
-                             float* chunk_states, void* workspace, size_t workspace_bytes, int32_t* status,
-                             void* stream)
+                             float* chunk_states, int32_t* status, void* stream)
 {
     const gdn_status_t bad = ssm_check(args, false);
     if (bad != GDN_OK) return bad;
@@ -635,13 +611,9 @@ gdn_status_t gdn_ssm_forward(const gdn_ssm_t* args, const float* state_in, void*
     if (sy.hits(Span(s.x, T, s.x_stride, s.channels, es)) || sy.hits(Span(s.dt, T, s.dt_stride, s.channels, es)) ||
         sy.hits(Span(s.z, T, s.z_stride, s.channels, es)) || so.hits(Span(state_in, s.num_seqs, per, per, 4)))
         return GDN_ERR_INVALID_ARG;
-    if (workspace == nullptr || workspace_bytes < gdn_ssm_workspace_size(T, s.num_seqs, s.channels, s.states))
-        return GDN_ERR_WORKSPACE;
-    if (!aligned(workspace, kAlign)) return GDN_ERR_INVALID_ARG;
-    const SsmWorkspace w = ssm_carve(workspace, T, s.num_seqs, s.channels, 1, s.states, false);
-    gdn::SsmArgs a = ssm_args(args, ssm_fwd_chunk(T, s.channels, s.states), 4 * 128 / s.states * 4);
+    gdn::SsmArgs a = ssm_args(args, 1);  // the launch sets the channel blocks
     a.state_in = state_in; a.y = y; a.state_out = state_out; a.saved = chunk_states;
-    a.hbuf = w.hbuf; a.dsum = w.dsum; a.status = status;
+    a.status = status;
     const bool v16 = ssm_wide(args) && aligned(y, 16);
     SSM_DISPATCH(ssm_forward_launch, s.in_dtype, s.states, v16, a, static_cast<cudaStream_t>(stream));
 }
@@ -687,19 +659,18 @@ gdn_status_t gdn_ssm_backward(const gdn_ssm_t* args, const void* dy, int64_t dy_
             return GDN_ERR_CUDA;
         return GDN_OK;
     }
-    const SsmWorkspace w = ssm_carve(workspace, T, s.num_seqs, s.channels, s.groups, s.states, true);
-    const int64_t Lc = ssm_bwd_chunk(T, s.channels, s.states);
+    const SsmWorkspace w = ssm_carve(workspace, T, s.num_seqs, s.channels, s.groups, s.states);
     gdn::SsmBwdArgs b{};
-    b.f = ssm_args(args, Lc, 2 * 128 / s.states * 4);
+    b.f = ssm_args(args, 2 * 128 / s.states * 4);
+    b.Lc = ssm_bwd_chunk(T, s.channels, s.states);
     b.f.saved = const_cast<float*>(chunk_states);
-    b.f.hbuf = w.hbuf; b.f.dsum = w.dsum; b.f.status = status;
+    b.ebuf = w.ebuf; b.dsum = w.dsum; b.f.status = status;
     b.dy = dy; b.lddy = dy_stride; b.dstate_out = dstate_out;
     b.dx = dx; b.ddt = ddt; b.dz = dz; b.dstate_in = dstate_in;
     b.partA = w.partA; b.partD = w.partD; b.partBC = w.partBC;
-    const int scan_cpg = (int)ceil_div(b.f.Dg, 4 * 128 / s.states * 4);
     const bool v16 = ssm_wide(args) && wide(dy, dy_stride, b.f.Dg, s.in_dtype) && aligned(dx, 16) && aligned(ddt, 16) &&
                      (s.z == nullptr || aligned(dz, 16));
-    SSM_DISPATCH(ssm_backward_launch, s.in_dtype, s.states, v16, b, scan_cpg, dB, dC, dA, dD, ddt_bias, st);
+    SSM_DISPATCH(ssm_backward_launch, s.in_dtype, s.states, v16, b, dB, dC, dA, dD, ddt_bias, st);
 }
 
 gdn_status_t gdn_ssm_step(const gdn_ssm_t* args, const float* state, float* state_out, void* y, void* stream)
@@ -717,7 +688,7 @@ gdn_status_t gdn_ssm_step(const gdn_ssm_t* args, const float* state, float* stat
     if (sy.hits(Span(s.x, N, s.x_stride, s.channels, es)) || sy.hits(Span(s.dt, N, s.dt_stride, s.channels, es)) ||
         sy.hits(Span(s.z, N, s.z_stride, s.channels, es)) || (state != state_out && si.hits(so)))
         return GDN_ERR_INVALID_ARG;
-    gdn::SsmArgs a = ssm_args(args, gdn::kSsmSave, 4 * 128 / s.states * 4);
+    gdn::SsmArgs a = ssm_args(args, 1);
     a.state_in = state; a.state_out = state_out; a.y = y;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (s.in_dtype == GDN_BF16) {

@@ -31,7 +31,7 @@ SYMBOLS = ("gdn_contract_id", "gdn_status_string", "gdn_num_chunk_states", "gdn_
            "gdn_cpr_backward_workspace_size", "gdn_cpr_backward", "gdn_cpr_backward_timed",
            "gdn_read_device_status", "gdn_test_fault_injection",
            "gdn_conv_forward", "gdn_conv_backward_workspace_size", "gdn_conv_backward", "gdn_conv_step",
-           "gdn_ssm_num_chunk_states", "gdn_ssm_workspace_size", "gdn_ssm_forward",
+           "gdn_ssm_num_chunk_states", "gdn_ssm_forward",
            "gdn_ssm_backward_workspace_size", "gdn_ssm_backward", "gdn_ssm_step",
            "gdn_layer_norm_forward", "gdn_layer_norm_backward_workspace_size", "gdn_layer_norm_backward")
 
@@ -130,10 +130,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     ssm = ctypes.POINTER(SsmStruct)
     lib.gdn_ssm_num_chunk_states.restype = i64
     lib.gdn_ssm_num_chunk_states.argtypes = [i64, i32]
-    lib.gdn_ssm_workspace_size.restype = sz
-    lib.gdn_ssm_workspace_size.argtypes = [i64, i32, i32, i32]
     lib.gdn_ssm_forward.restype = e
-    lib.gdn_ssm_forward.argtypes = [ssm, P, P, P, P, P, sz, P, P]
+    lib.gdn_ssm_forward.argtypes = [ssm, P, P, P, P, P, P]
     lib.gdn_ssm_backward_workspace_size.restype = sz
     lib.gdn_ssm_backward_workspace_size.argtypes = [i64, i32, i32, i32, i32]
     lib.gdn_ssm_backward.restype = e
@@ -613,7 +611,7 @@ def gdn_ssm_num_chunk_states(total_tokens: int, num_seqs: int) -> int:
 
 def gdn_ssm_forward(x, dt, A, B, C, cu_seqlens=None, *, D=None, z=None, dt_bias=None, dt_softplus: bool = True,
                     state_in=None, save_states: bool = False, y=None, state_out=None, chunk_states=None,
-                    workspace=None, status=None):
+                    status=None):
     """Selective state space scan of a packed batch (gdn_ssm_forward): per channel c of group g
         delta = softplus(dt + dt_bias),  h = exp(delta A) h + delta x B[g],  y = (h . C[g] + D x) silu(z)
 
@@ -625,8 +623,7 @@ def gdn_ssm_forward(x, dt, A, B, C, cu_seqlens=None, *, D=None, z=None, dt_bias=
     what = "gdn_ssm_forward"
     N = _sequences(what, cu_seqlens)
     s = _ssm_struct(what, x, dt, A, B, C, cu_seqlens, N, D, z, dt_bias, dt_softplus)
-    dev = _where(x, what, dt, A, B, C, cu_seqlens, D, z, dt_bias, state_in, y, state_out, chunk_states, workspace,
-                 status)
+    dev = _where(x, what, dt, A, B, C, cu_seqlens, D, z, dt_bias, state_in, y, state_out, chunk_states, status)
     T, ch, S, f32 = s.total_tokens, s.channels, s.states, torch.float32
     lib = load_library()
     y = torch.empty(T, ch, dtype=x.dtype, device=dev) if y is None else y
@@ -641,9 +638,7 @@ def gdn_ssm_forward(x, dt, A, B, C, cu_seqlens=None, *, D=None, z=None, dt_bias=
     _shaped(what, (T, ch), y=y)
     _shaped(what, (N, ch, S), state_in=state_in, state_out=state_out)
     _dense(what, y=y, state_in=state_in, state_out=state_out, chunk_states=chunk_states)
-    workspace = _scratch(what, workspace, lib.gdn_ssm_workspace_size(T, N, ch, S), dev)
-    _call(dev, what, lib.gdn_ssm_forward, s, _p(state_in), _p(y), _p(state_out), _p(chunk_states), _p(workspace),
-          workspace.numel() * workspace.element_size(), _p(status))
+    _call(dev, what, lib.gdn_ssm_forward, s, _p(state_in), _p(y), _p(state_out), _p(chunk_states), _p(status))
     return y, state_out, chunk_states
 
 

@@ -535,7 +535,6 @@ typedef struct {
 
 /* Rows of the saved states that gdn_ssm_backward reads: total_tokens / GDN_SSM_CHUNK + num_seqs; -1 for invalid sizes. */
 int64_t gdn_ssm_num_chunk_states(int64_t total_tokens, int32_t num_seqs);
-size_t gdn_ssm_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t channels, int32_t states);
 
 /*
  * Prefill and trainer forward.
@@ -545,11 +544,10 @@ size_t gdn_ssm_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t ch
  *     backward follows: the states before every GDN_SSM_CHUNK-th token of a
  *     sequence; row lo / GDN_SSM_CHUNK + n + k belongs to token lo + k GDN_SSM_CHUNK of
  *     sequence n, which starts at row lo.  Rows that belong to no token are not written.
- *   workspace: gdn_ssm_workspace_size(...) bytes, 256-byte aligned
+ * It needs no workspace.
  */
 gdn_status_t gdn_ssm_forward(const gdn_ssm_t* args, const float* state_in, void* y, float* state_out,
-                             float* chunk_states, void* workspace, size_t workspace_bytes, int32_t* status,
-                             void* stream);
+                             float* chunk_states, int32_t* status, void* stream);
 
 /*
  * Gradients of sum(dy y) + sum(dstate_out state_out).  args and chunk_states: as given to and written by
