@@ -15,8 +15,6 @@
 
 namespace gdn {
 
-constexpr int kNormMaxThreads = 1024;
-constexpr int kNormBwdThreads = 512;
 
 struct NormArgs {
     const void* x;
@@ -38,13 +36,15 @@ struct NormArgs {
 template <int K>
 __device__ __forceinline__ void row_sum(float (&v)[K], int tpr, float* red)
 {
+    auto fold = [&](int o) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        if (o < tpr) {
-#pragma unroll
-            for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(kFullMask, v[k], o);
-        }
-    }
+        for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(kFullMask, v[k], o);
+    };
+    if (tpr >= 32) fold(16);
+    if (tpr >= 16) fold(8);
+    fold(4);  // a row has at least 8 threads
+    fold(2);
+    fold(1);
     if (tpr > 32) {
         const int warp = threadIdx.x >> 5, wpr = tpr >> 5, first = warp & ~(wpr - 1);
         __syncthreads();  // the previous sums have been read
@@ -53,75 +53,191 @@ __device__ __forceinline__ void row_sum(float (&v)[K], int tpr, float* red)
             for (int k = 0; k < K; ++k) red[k * 32 + warp] = v[k];
         }
         __syncthreads();
+        // every warp sums the row's warps itself, wpr (2 to 32) neighbouring lanes at a time
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            float s = 0.0f;
-            for (int i = 0; i < wpr; ++i) s += red[k * 32 + first + i];
-            v[k] = s;
-        }
+        for (int k = 0; k < K; ++k) v[k] = red[k * 32 + first + (threadIdx.x & (wpr - 1))];
+        if (wpr > 16) fold(16);
+        if (wpr > 8) fold(8);
+        if (wpr > 4) fold(4);
+        if (wpr > 2) fold(2);
+        fold(1);
     }
 }
 
-template <typename T, int V, int NV>
-__global__ void __launch_bounds__(kNormMaxThreads) k_norm_fwd(const NormArgs a)
+// V elements of a weight or bias, as they are stored
+template <typename WT, int V>
+__device__ __forceinline__ Vec<WT, V> norm_weight(const void* w, int c)
 {
+    const WT* p = static_cast<const WT*>(w) + c;
+    Vec<WT, V> r;
+    if (V > 1 && (reinterpret_cast<uintptr_t>(p) & (sizeof(r) < 16 ? sizeof(r) - 1 : 15)) == 0) {
+        constexpr int E = sizeof(r) > 16 ? 16 / sizeof(WT) : V;  // elements per access
+#pragma unroll
+        for (int i = 0; i < V / E; ++i) {
+            const Vec<WT, E> q = load_vec<WT, E>(p + i * E);
+#pragma unroll
+            for (int k = 0; k < E; ++k) r.v[i * E + k] = q.v[k];
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k) r.v[k] = p[k];
+    }
+    return r;
+}
+
+__host__ __device__ constexpr int norm_threads(int V) { return V == 1 ? 1024 : 512; }  // most threads of a block
+
+// x^(-1/2): the approximate instruction and one step of Newton's method
+__device__ __forceinline__ float inv_sqrt(float x)
+{
+    const float r = rsqrtf(x);
+    const float e = __fmaf_rn(-x * r, r, 1.0f);  // 1 - x r^2
+    return x > 0.0f && x < 3.0e38f ? __fmaf_rn(0.5f * e, r, r) : r;
+}
+
+// Keeps r packed: without it the compiler widens the weights once, before the loop
+// over the rows, into twice the registers.
+template <typename WT, int V>
+__device__ __forceinline__ void keep_packed(Vec<WT, V>& r)
+{
+    if constexpr (sizeof(r) % 4 == 0) {
+        uint32_t* u = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(r) / 4; ++i) asm volatile("" : "+r"(u[i]));
+    }
+}
+
+// A thread's own vectors of the rows that it will work on next, in a ring in shared
+// memory that cp.async fills: memory stays busy through the sums of the current row, at no cost
+// in registers, and since a thread reads only what it has copied itself, the ring needs no
+// barrier.  (Prefetching into registers instead left half the threads and was
+// slower than no prefetch: 131 us against 95 at 16384 x 4096.)
+template <typename T, int V, int NV, int DEP>
+struct NormRing {
+    static constexpr bool ON = V * sizeof(T) == 16;
+    static constexpr size_t BYTES = ON ? (size_t)DEP * NV * 16 : 0;  // per thread and tensor
+    unsigned char* base;
+    __device__ __forceinline__ unsigned char* at(int slot, int i) const
+    {
+        return base + ((slot * NV + i) * blockDim.x + threadIdx.x) * 16u;
+    }
+    __device__ __forceinline__ void copy(int slot, int i, const T* src) const
+    {
+        if constexpr (ON)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                             (unsigned)__cvta_generic_to_shared(at(slot, i))), "l"(src) : "memory");
+    }
+    __device__ __forceinline__ Vec<T, V> get(int slot, int i, const T* src) const
+    {
+        if constexpr (ON) return *reinterpret_cast<const Vec<T, V>*>(at(slot, i));
+        else return load_vec<T, V>(src);
+    }
+    __device__ static void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    __device__ static void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(DEP - 1) : "memory"); }
+};
+
+__host__ __device__ constexpr int norm_depth(int NV) { return NV == 1 ? 4 : 2; }  // rows ahead
+
+// Blocks walk the rows with a stride, the weights in registers.  Columns beyond D hold zeros.
+template <typename T, typename WT, int V, int NV>
+__global__ void __launch_bounds__(norm_threads(V)) k_norm_fwd(const NormArgs a)
+{
+    using L = Lanes<V>;
+    using P = typename L::type;
+    constexpr int DEP = norm_depth(NV);
+    extern __shared__ __align__(16) unsigned char norm_smem[];
     __shared__ float red[32];
+    const NormRing<T, V, NV, DEP> ring{norm_smem};
     const int rpb = blockDim.x / a.tpr;
     const int lane = threadIdx.x & (a.tpr - 1);
-    const int64_t row = (int64_t)blockIdx.x * rpb + threadIdx.x / a.tpr;
-    const bool on = row < a.R;
-    const T* x = static_cast<const T*>(a.x) + (on ? row : 0) * a.ldx;
-    float v[NV][V];
-    float s[1] = {0.0f};
+    auto col = [&](int i) { return (i * a.tpr + lane) * V; };
+    const int R = (int)a.R, step = gridDim.x * rpb, first = blockIdx.x * rpb + threadIdx.x / a.tpr;  // below 2^31
+    const int64_t stepx = step * a.ldx, stepy = step * (int64_t)a.D;
+    const T* px = static_cast<const T*>(a.x) + lane * V + first * a.ldx;  // the row to copy next
+    const T* cx = px;                                                     // the row to work on
+    T* py = static_cast<T*>(a.y) + lane * V + first * (int64_t)a.D;
+    Vec<WT, V> w[NV], b[NV];
+    auto fetch = [&](int left, int slot) {  // left: rows from this one to the last
+        if (left > 0) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (col(i) < a.D) ring.copy(slot, i, px + i * a.tpr * V);
+        }
+        px += stepx;
+        ring.commit();
+    };
+    int left = R - first;  // rows from the thread's current one to the last
+#pragma unroll
+    for (int j = 0; j < DEP; ++j) fetch(left - j * step, j);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * a.tpr + lane) * V;
-        if (on && c < a.D) {
-            const Vec<T, V> r = load_vec<T, V>(x + c);
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                v[i][k] = to_f<T>(r.v[k]);
-                s[0] += v[i][k];
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < V; ++k) v[i][k] = 0.0f;
+        if (col(i) < a.D) {
+            w[i] = norm_weight<WT, V>(a.w, col(i));
+            if (a.b != nullptr) b[i] = norm_weight<WT, V>(a.b, col(i));
         }
     }
-    row_sum<1>(s, a.tpr, red);
-    const float mean = s[0] / (float)a.D;
-    s[0] = 0.0f;
+    const float inv = 1.0f / (float)a.D;
+    int slot = 0;
+    float *pm = a.mean + first, *pr = a.rstd + first;
+    for (int rest = R - blockIdx.x * rpb; rest > 0;
+         rest -= step, left -= step, cx += stepx, py += stepy, pm += step, pr += step) {
+        const bool on = left > 0;
+        P v[NV][L::N];
+        P acc = pset<V>(0.0f);
+        ring.wait();
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        if ((i * a.tpr + lane) * V < a.D) {
+        for (int i = 0; i < NV; ++i) {
+            const bool in = on && col(i) < a.D;
+            Vec<T, V> r;
+            if (in) r = ring.get(slot, i, cx + i * a.tpr * V);
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-                v[i][k] -= mean;
-                s[0] = __fmaf_rn(v[i][k], v[i][k], s[0]);
+            for (int k = 0; k < L::N; ++k) {
+                v[i][k] = in ? pget<T, V>(r, k) : pset<V>(0.0f);
+                acc = padd(acc, v[i][k]);
             }
         }
-    }
-    row_sum<1>(s, a.tpr, red);
-    const float rstd = 1.0f / sqrtf(s[0] / (float)a.D + a.eps);
-    if (!on) return;
-    T* y = static_cast<T*>(a.y) + row * a.D;
+        fetch(left - DEP * step, slot);
+        slot = slot + 1 == DEP ? 0 : slot + 1;
+        float s[1] = {psum(acc)};
+        row_sum<1>(s, a.tpr, red);
+        const float mean = s[0] * inv;
+        acc = pset<V>(0.0f);
+        const P minus = pset<V>(-mean);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * a.tpr + lane) * V;
-        if (c < a.D) {
-            float o[V];
+        for (int i = 0; i < NV; ++i) {
+            if (col(i) < a.D) {
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const float n = v[i][k] * rstd;
-                o[k] = a.b != nullptr ? __fmaf_rn(n, load_w(a.w, a.w_bf16, c + k), load_w(a.b, a.w_bf16, c + k))
-                                      : n * load_w(a.w, a.w_bf16, c + k);
+                for (int k = 0; k < L::N; ++k) {
+                    v[i][k] = padd(v[i][k], minus);
+                    acc = pfma(v[i][k], v[i][k], acc);
+                }
             }
-            store_vec<T, V>(y + c, o);
         }
-    }
-    if (lane == 0) {
-        a.mean[row] = mean;
-        a.rstd[row] = rstd;
+        s[0] = psum(acc);
+        row_sum<1>(s, a.tpr, red);
+        const float rstd = inv_sqrt(__fmaf_rn(s[0], inv, a.eps));
+        if (on) {
+            const P r2 = pset<V>(rstd);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                keep_packed(w[i]);
+                keep_packed(b[i]);
+                if (col(i) < a.D) {
+                    P o[L::N];
+#pragma unroll
+                    for (int k = 0; k < L::N; ++k) {
+                        o[k] = pmul(v[i][k], r2);
+                        o[k] = a.b != nullptr ? pfma(o[k], pget<WT, V>(w[i], k), pget<WT, V>(b[i], k))
+                                              : pmul(o[k], pget<WT, V>(w[i], k));
+                    }
+                    pstore<T, V>(py + i * a.tpr * V, o);
+                }
+            }
+            if (lane == 0) {
+                *pm = mean;
+                *pr = rstd;
+            }
+        }
     }
 }
 
@@ -144,7 +260,7 @@ __global__ void __launch_bounds__(1024) k_norm_fwd_wide(const NormArgs a)
         s[0] = __fmaf_rn(d, d, s[0]);
     }
     row_sum<1>(s, 1024, red);
-    const float rstd = 1.0f / sqrtf(s[0] / (float)a.D + a.eps);
+    const float rstd = inv_sqrt(s[0] / (float)a.D + a.eps);
     for (int c = threadIdx.x; c < a.D; c += 1024) {
         const float n = (to_f<T>(x[c]) - mean) * rstd, w = load_w(a.w, a.w_bf16, c);
         y[c] = from_f<T>(a.b != nullptr ? __fmaf_rn(n, w, load_w(a.b, a.w_bf16, c)) : n * w);
@@ -156,96 +272,149 @@ __global__ void __launch_bounds__(1024) k_norm_fwd_wide(const NormArgs a)
 }
 
 // Each block walks rows with a stride and keeps its share of dw and db in
-// registers: a thread's columns are the same in every row.  The shares of the
-// blocks ([grid][2][D]) are joined by k_colsum.
-template <typename T, int V, int NV>
-__global__ void __launch_bounds__(kNormBwdThreads) k_norm_bwd(const NormArgs a)
+// registers: a thread's columns are the same in every row.  The next rows and their statistics
+// are on their way meanwhile.  The shares of the blocks ([grid][2][D]) are joined by k_colsum.
+template <typename T, typename WT, int V, int NV>
+__global__ void __launch_bounds__(512) k_norm_bwd(const NormArgs a)
 {
-    extern __shared__ float sh[];  // [64] row sums, then [2][D] when several rows share a block
-    float* red = sh;
+    using L = Lanes<V>;
+    using P = typename L::type;
+    constexpr int DEP = norm_depth(NV);
+    using Ring = NormRing<T, V, NV, DEP>;
+    extern __shared__ __align__(16) unsigned char norm_smem[];  // two rings; later [2][D] when several rows share a block
+    __shared__ float red[64];
+    const Ring ringx{norm_smem}, ringg{norm_smem + Ring::BYTES * blockDim.x};
     const int rpb = blockDim.x / a.tpr;
     const int lane = threadIdx.x & (a.tpr - 1), sub = threadIdx.x / a.tpr;
-    float w[NV][V], dw[NV][V], db[NV][V];
+    auto col = [&](int i) { return (i * a.tpr + lane) * V; };
+    const int R = (int)a.R, step = gridDim.x * rpb, first = blockIdx.x * rpb + sub;  // below 2^31
+    const int64_t stepx = step * a.ldx, stepg = step * a.lddy, stepd = step * (int64_t)a.D;
+    const T* px = static_cast<const T*>(a.x) + lane * V + first * a.ldx;  // the row to copy next
+    const T* pg = static_cast<const T*>(a.dy) + lane * V + first * a.lddy;
+    const T *qx = px, *qg = pg;                                           // the row to work on
+    T* pd = static_cast<T*>(a.dx) + lane * V + first * (int64_t)a.D;
+    Vec<WT, V> w[NV];
+    P dw[NV][L::N], db[NV][L::N];
+    auto fetch = [&](int left, int slot) {  // left: rows from this one to the last
+        if (left > 0) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const int c = (i * a.tpr + lane) * V + k;
-            w[i][k] = c < a.D ? load_w(a.w, a.w_bf16, c) : 0.0f;
-            dw[i][k] = db[i][k] = 0.0f;
+            for (int i = 0; i < NV; ++i)
+                if (col(i) < a.D) {
+                    ringx.copy(slot, i, px + i * a.tpr * V);
+                    ringg.copy(slot, i, pg + i * a.tpr * V);
+                }
         }
+        px += stepx;
+        pg += stepg;
+        Ring::commit();
+    };
+    const float *pm = a.mean + first, *pr = a.rstd + first;
+    float mean_next = first < R ? *pm : 0.0f, rstd_next = first < R ? *pr : 0.0f;
+    int left = R - first;  // rows from the thread's current one to the last
+#pragma unroll
+    for (int j = 0; j < DEP; ++j) fetch(left - j * step, j);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (col(i) < a.D) w[i] = norm_weight<WT, V>(a.w, col(i));
+#pragma unroll
+        for (int k = 0; k < L::N; ++k) dw[i][k] = db[i][k] = pset<V>(0.0f);
+    }
     const float inv = 1.0f / (float)a.D;
-    for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < a.R; r0 += (int64_t)gridDim.x * rpb) {
-        const int64_t row = r0 + sub;
-        const bool on = row < a.R;
-        const T* x = static_cast<const T*>(a.x) + (on ? row : 0) * a.ldx;
-        const T* dy = static_cast<const T*>(a.dy) + (on ? row : 0) * a.lddy;
-        const float mean = on ? a.mean[row] : 0.0f, rstd = on ? a.rstd[row] : 0.0f;
-        float n[NV][V], g[NV][V];
-        float s[2] = {0.0f, 0.0f};
+    int slot = 0;
+    for (int rest = R - blockIdx.x * rpb; rest > 0;
+         rest -= step, left -= step, qx += stepx, qg += stepg, pd += stepd) {
+        const bool on = left > 0;
+        const float rstd = rstd_next;
+        const P minus = pset<V>(-mean_next), r2 = pset<V>(rstd);
+        pm += step;
+        pr += step;
+        if (left > step) {
+            mean_next = *pm;
+            rstd_next = *pr;
+        }
+        Vec<T, V> cx[NV], cg[NV];
+        P s0 = pset<V>(0.0f), s1 = pset<V>(0.0f);
+        Ring::wait();
+        if (on) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * a.tpr + lane) * V;
-            if (on && c < a.D) {
-                const Vec<T, V> rx = load_vec<T, V>(x + c), rg = load_vec<T, V>(dy + c);
+            for (int i = 0; i < NV; ++i) {
+                if (col(i) < a.D) {
+                    cx[i] = ringx.get(slot, i, qx + i * a.tpr * V);
+                    cg[i] = ringg.get(slot, i, qg + i * a.tpr * V);
 #pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    n[i][k] = (to_f<T>(rx.v[k]) - mean) * rstd;
-                    const float d = to_f<T>(rg.v[k]);
-                    dw[i][k] = __fmaf_rn(d, n[i][k], dw[i][k]);
-                    db[i][k] += d;
-                    g[i][k] = d * w[i][k];
-                    s[0] += g[i][k];
-                    s[1] = __fmaf_rn(g[i][k], n[i][k], s[1]);
+                    for (int k = 0; k < L::N; ++k) {
+                        const P n = padd(pget<T, V>(cx[i], k), minus), d = pget<T, V>(cg[i], k);  // n without rstd
+                        dw[i][k] = pfma(pmul(d, r2), n, dw[i][k]);
+                        db[i][k] = padd(db[i][k], d);
+                        const P g = pmul(d, pget<WT, V>(w[i], k));
+                        s0 = padd(s0, g);
+                        s1 = pfma(g, n, s1);
+                    }
                 }
             }
         }
+        fetch(left - DEP * step, slot);
+        slot = slot + 1 == DEP ? 0 : slot + 1;
+        float s[2] = {psum(s0), psum(s1)};
         row_sum<2>(s, a.tpr, red);
-        const float mg = s[0] * inv, mgn = s[1] * inv;
         if (on) {
-            T* dx = static_cast<T*>(a.dx) + row * a.D;
+            // dx = rstd g + c1 (x - mean) + c0
+            const P c0 = pset<V>(-rstd * s[0] * inv), c1 = pset<V>(-rstd * rstd * rstd * s[1] * inv);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int c = (i * a.tpr + lane) * V;
-                if (c < a.D) {
-                    float o[V];
+                keep_packed(w[i]);  // widened again, not kept in twice the registers
+                keep_packed(cx[i]);
+                keep_packed(cg[i]);
+                if (col(i) < a.D) {
+                    P o[L::N];
 #pragma unroll
-                    for (int k = 0; k < V; ++k) o[k] = rstd * (g[i][k] - __fmaf_rn(n[i][k], mgn, mg));
-                    store_vec<T, V>(dx + c, o);
+                    for (int k = 0; k < L::N; ++k) {
+                        const P n = padd(pget<T, V>(cx[i], k), minus);
+                        o[k] = pfma(pget<T, V>(cg[i], k), pmul(pget<WT, V>(w[i], k), r2), pfma(n, c1, c0));
+                    }
+                    pstore<T, V>(pd + i * a.tpr * V, o);
                 }
             }
         }
     }
     float* part = a.part + (int64_t)blockIdx.x * 2 * a.D;
-    if (rpb == 1) {
+    auto each = [&](auto f) {  // f(column, dw, db) for this thread's columns
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const int c = (i * a.tpr + lane) * V + k;
-                if (c < a.D) {
-                    part[c] = dw[i][k];
-                    part[a.D + c] = db[i][k];
+            for (int k = 0; k < L::N; ++k) {
+                float x[2], y[2];
+                if constexpr (V == 1) {
+                    x[0] = dw[i][k];
+                    y[0] = db[i][k];
+                } else {
+                    up2(dw[i][k], x[0], x[1]);
+                    up2(db[i][k], y[0], y[1]);
+                }
+#pragma unroll
+                for (int h = 0; h < (V == 1 ? 1 : 2); ++h) {
+                    const int c = col(i) + 2 * k + h;
+                    if (c < a.D) f(c, x[h], y[h]);
                 }
             }
+    };
+    if (rpb == 1) {
+        each([&](int c, float x, float y) {
+            part[c] = x;
+            part[a.D + c] = y;
+        });
         return;
     }
     // the rows of a block, joined one after the other (their order is fixed)
-    float* acc = sh + 64;
+    float* acc = reinterpret_cast<float*>(norm_smem);
+    __syncthreads();  // every thread is done with its ring
     for (int r = 0; r < rpb; ++r) {
         __syncthreads();
-        if (sub == r) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    const int c = (i * a.tpr + lane) * V + k;
-                    if (c < a.D) {
-                        acc[c] = (r ? acc[c] : 0.0f) + dw[i][k];
-                        acc[a.D + c] = (r ? acc[a.D + c] : 0.0f) + db[i][k];
-                    }
-                }
-        }
+        if (sub == r)
+            each([&](int c, float x, float y) {
+                acc[c] = (r ? acc[c] : 0.0f) + x;
+                acc[a.D + c] = (r ? acc[a.D + c] : 0.0f) + y;
+            });
     }
     __syncthreads();
     for (int c = threadIdx.x; c < 2 * a.D; c += blockDim.x) part[c] = acc[c];

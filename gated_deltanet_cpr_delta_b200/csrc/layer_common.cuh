@@ -42,13 +42,106 @@ __device__ __forceinline__ Vec<T, V> load_vec(const T* p)
     return *reinterpret_cast<const Vec<T, V>*>(p);
 }
 
+// Two bf16 at once: widening is a shift or a mask, rounding one instruction.
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// the V values of r, widened
+template <typename T, int V>
+__device__ __forceinline__ void widen(const Vec<T, V>& r, float (&x)[V])
+{
+    if constexpr (sizeof(T) == 2 && V % 2 == 0) {
+        const uint32_t* u = reinterpret_cast<const uint32_t*>(&r);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            x[2 * i] = __uint_as_float(u[i] << 16);
+            x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = to_f<T>(r.v[i]);
+    }
+}
+
 template <typename T, int V>
 __device__ __forceinline__ void store_vec(T* p, const float* x)
 {
     Vec<T, V> r;
+    if constexpr (sizeof(T) == 2 && V % 2 == 0) {
+        uint32_t* u = reinterpret_cast<uint32_t*>(&r);
 #pragma unroll
-    for (int i = 0; i < V; ++i) r.v[i] = from_f<T>(x[i]);
+        for (int i = 0; i < V / 2; ++i) u[i] = bf16_pair(x[2 * i], x[2 * i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) r.v[i] = from_f<T>(x[i]);
+    }
     *reinterpret_cast<Vec<T, V>*>(p) = r;
+}
+
+// Pairs of fp32 values in one packed register (f2x), or single ones where a
+// thread has no neighbour (V = 1): the same code for both.
+template <int V>
+struct Lanes {
+    using type = f2x;
+    static constexpr int N = V / 2;
+};
+template <>
+struct Lanes<1> {
+    using type = float;
+    static constexpr int N = 1;
+};
+__device__ __forceinline__ f2x fadd2(f2x a, f2x b)
+{
+    f2x d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f2x padd(f2x a, f2x b) { return fadd2(a, b); }
+__device__ __forceinline__ float padd(float a, float b) { return a + b; }
+__device__ __forceinline__ f2x pmul(f2x a, f2x b) { return fmul2(a, b); }
+__device__ __forceinline__ float pmul(float a, float b) { return a * b; }
+__device__ __forceinline__ f2x pfma(f2x a, f2x b, f2x c) { return ffma2(a, b, c); }
+__device__ __forceinline__ float pfma(float a, float b, float c) { return __fmaf_rn(a, b, c); }
+__device__ __forceinline__ float psum(f2x a)
+{
+    float x, y;
+    up2(a, x, y);
+    return x + y;
+}
+__device__ __forceinline__ float psum(float a) { return a; }
+template <int V>
+__device__ __forceinline__ typename Lanes<V>::type pset(float x)
+{
+    if constexpr (V == 1) return x;
+    else return pk2(x, x);
+}
+// element or pair i of V elements of type T, widened
+template <typename T, int V>
+__device__ __forceinline__ typename Lanes<V>::type pget(const Vec<T, V>& r, int i)
+{
+    if constexpr (V == 1) {
+        return to_f<T>(r.v[0]);
+    } else if constexpr (sizeof(T) == 2) {
+        const uint32_t u = reinterpret_cast<const uint32_t*>(&r)[i];
+        return pk2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+    } else {
+        return pk2(to_f<T>(r.v[2 * i]), to_f<T>(r.v[2 * i + 1]));
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ void pstore(T* p, const typename Lanes<V>::type* x)
+{
+    float o[V];
+    if constexpr (V == 1) o[0] = x[0];
+    else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) up2(x[i], o[2 * i], o[2 * i + 1]);
+    }
+    store_vec<T, V>(p, o);
 }
 
 // Weights and biases may be fp32 or bf16 whatever the tokens are.

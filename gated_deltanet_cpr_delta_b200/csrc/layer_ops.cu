@@ -28,6 +28,14 @@ size_t esize(gdn_dtype_t t) { return t == GDN_BF16 ? 2 : 4; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 bool launched() { return cudaGetLastError() == cudaSuccess; }
 
+// Shared memory beyond the 48 KB that every launch may have
+template <typename K>
+bool raise_smem(K* kernel, size_t bytes)
+{
+    return bytes <= 48 * 1024 ||
+           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+}
+
 int sm_count()
 {
     int dev = 0, sms = 0;
@@ -153,44 +161,76 @@ struct NormPlan {
     bool wide;  // one block per row, the row read again
 };
 
-// A row's threads: enough that a thread holds at most `most` vectors, in blocks
-// of at least 128 threads.
+// A row's threads: up to a warp with one vector each, then more vectors (up to
+// `most`) before more threads, so that a row's sums cross few warps.
 NormPlan norm_plan(int32_t D, int V, int most, int max_threads)
 {
     NormPlan p{};
     const int64_t nvec = ceil_div(D, V);
     p.V = V;
     int tpr = 8;
-    while (tpr < max_threads && (int64_t)tpr * 2 <= nvec && tpr < 32) tpr *= 2;
+    while (tpr < 32 && (int64_t)tpr < nvec) tpr *= 2;
     while (tpr < max_threads && (int64_t)tpr * most < nvec) tpr *= 2;
     p.tpr = tpr;
     const int64_t nv = ceil_div(nvec, tpr);
-    p.NV = nv <= 1 ? 1 : nv <= 2 ? 2 : 4;
-    p.wide = nv > most;
+    p.NV = 1;
+    while (p.NV < nv) p.NV *= 2;
+    p.wide = p.NV > most;
     p.threads = std::max(tpr, 128);
     return p;
+}
+
+// Blocks that walk the rows: a full GPU of about `resident` threads per SM.
+int64_t norm_blocks(int64_t rows, const NormPlan& p, int resident)
+{
+    return std::min<int64_t>(ceil_div(rows, p.threads / p.tpr), (int64_t)148 * std::max(1, resident / p.threads));
+}
+
+template <typename T, typename WT, int V, int NV>
+bool norm_fwd_nv(const gdn::NormArgs& a, const NormPlan& p, cudaStream_t st)
+{
+    if (p.NV == NV) {
+        const size_t sm = gdn::NormRing<T, V, NV, gdn::norm_depth(NV)>::BYTES * p.threads;
+        const int resident = V == 1 ? 2048 : NV == 1 ? 1280 : NV == 2 ? 1024 : 512;
+        auto k = gdn::k_norm_fwd<T, WT, V, NV>;
+        if (!raise_smem(k, sm)) return false;
+        k<<<(unsigned)norm_blocks(a.R, p, resident), p.threads, sm, st>>>(a);
+    } else if constexpr (NV < (V == 1 ? 16 : 4)) {
+        return norm_fwd_nv<T, WT, V, NV * 2>(a, p, st);
+    }
+    return launched();
 }
 
 template <typename T, int V>
 bool launch_norm_fwd(const gdn::NormArgs& a, const NormPlan& p, cudaStream_t st)
 {
-    const int64_t blocks = ceil_div(a.R, p.threads / p.tpr);
-    if (p.NV == 1) gdn::k_norm_fwd<T, V, 1><<<(unsigned)blocks, p.threads, 0, st>>>(a);
-    else if (p.NV == 2) gdn::k_norm_fwd<T, V, 2><<<(unsigned)blocks, p.threads, 0, st>>>(a);
-    else gdn::k_norm_fwd<T, V, 4><<<(unsigned)blocks, p.threads, 0, st>>>(a);
-    return launched();
+    return a.w_bf16 ? norm_fwd_nv<T, __nv_bfloat16, V, 1>(a, p, st) : norm_fwd_nv<T, float, V, 1>(a, p, st);
 }
 
-template <typename T, int V>
-bool launch_norm_bwd(const gdn::NormArgs& a, const NormPlan& p, unsigned blocks, cudaStream_t st)
+template <typename T, typename WT, int V, int NV>
+bool norm_bwd_nv(const gdn::NormArgs& a, const NormPlan& p, int64_t* blocks, cudaStream_t st)
 {
-    const size_t sm = sizeof(float) * (64 + (p.threads > p.tpr ? 2 * (size_t)a.D : 0));
-    if (p.NV == 1) gdn::k_norm_bwd<T, V, 1><<<blocks, p.threads, sm, st>>>(a);
-    else gdn::k_norm_bwd<T, V, 2><<<blocks, p.threads, sm, st>>>(a);
+    if (p.NV == NV) {
+        const size_t sm = std::max(2 * gdn::NormRing<T, V, NV, gdn::norm_depth(NV)>::BYTES * p.threads,
+                                   p.threads > p.tpr ? sizeof(float) * 2 * (size_t)a.D : 0);
+        auto k = gdn::k_norm_bwd<T, WT, V, NV>;
+        if (!raise_smem(k, sm)) return false;
+        *blocks = norm_blocks(a.R, p, NV == 1 && V > 1 ? 1024 : 512);
+        k<<<(unsigned)*blocks, p.threads, sm, st>>>(a);
+    } else if constexpr (NV < (V == 1 ? 16 : 4)) {
+        return norm_bwd_nv<T, WT, V, NV * 2>(a, p, blocks, st);
+    }
     return launched();
 }
 
-constexpr int64_t kNormParts = 148 * 4;  // blocks that keep a share of dw and db
+// *blocks: how many shares of dw and db it leaves
+template <typename T, int V>
+bool launch_norm_bwd(const gdn::NormArgs& a, const NormPlan& p, int64_t* blocks, cudaStream_t st)
+{
+    return a.w_bf16 ? norm_bwd_nv<T, __nv_bfloat16, V, 1>(a, p, blocks, st) : norm_bwd_nv<T, float, V, 1>(a, p, blocks, st);
+}
+
+constexpr int64_t kNormParts = 148 * 8;  // most blocks that keep a share of dw and db (1024 threads per SM, 128 to a block)
 int64_t norm_parts(int64_t rows) { return std::max<int64_t>(1, std::min<int64_t>(rows, kNormParts)); }
 
 // ------------------------------------------------------------------- scan
@@ -286,8 +326,7 @@ gdn_status_t ssm_forward_seg(gdn::SsmArgs a, cudaStream_t st)
     const int64_t blocks = (int64_t)a.s.N * a.G * a.cpg;
     if (blocks > INT32_MAX) return GDN_ERR_INVALID_ARG;
     auto k = gdn::k_ssm_fwd<T, S, V, SEG>;
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cf::BYTES) != cudaSuccess)
-        return GDN_ERR_CUDA;
+    if (!raise_smem(k, Cf::BYTES)) return GDN_ERR_CUDA;
     k<<<(unsigned)blocks, Cf::THREADS, Cf::BYTES, st>>>(a);
     return launched() ? GDN_OK : GDN_ERR_CUDA;
 }
@@ -314,8 +353,7 @@ gdn_status_t ssm_backward_launch(const gdn::SsmBwdArgs& b, void* dB, void* dC, f
     }
     constexpr size_t sm = gdn::SsmBwdCfg<S>::SMEM;
     auto k = a.z != nullptr ? gdn::k_ssm_bwd<T, S, V, true> : gdn::k_ssm_bwd<T, S, V, false>;
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm) != cudaSuccess)
-        return GDN_ERR_CUDA;
+    if (!raise_smem(k, sm)) return GDN_ERR_CUDA;
     k<<<(unsigned)(slots * a.G * a.cpg), gdn::kSsmThreads, sm, st>>>(b);
     if (a.s.T > 0) {
         const int64_t ids = a.s.T * a.G * 2 * S;
@@ -500,7 +538,9 @@ gdn_status_t gdn_layer_norm_forward(const void* x, int64_t x_stride, const void*
     a.eps = eps; a.R = rows; a.D = width; a.y = y; a.mean = mean; a.rstd = rstd;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool v16 = wide(x, x_stride, width, in_dtype) && wide(y, width, width, in_dtype);
-    const NormPlan p = norm_plan(width, v16 ? (int)(16 / es) : 1, 4, gdn::kNormMaxThreads);
+    // two vectors per thread measured best at 4096 x 16384 rows (63 us; four: 79, one: 101)
+    NormPlan p = v16 ? norm_plan(width, (int)(16 / es), 2, 512) : norm_plan(width, 1, 16, 1024);
+    if (p.wide && v16) p = norm_plan(width, (int)(16 / es), 4, 512);
     a.tpr = p.tpr;
     if (p.wide) {
         if (in_dtype == GDN_BF16) gdn::k_norm_fwd_wide<__nv_bfloat16><<<(unsigned)rows, 1024, 0, st>>>(a);
@@ -548,7 +588,9 @@ gdn_status_t gdn_layer_norm_backward(const void* x, int64_t x_stride, const void
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool v16 = wide(x, x_stride, width, in_dtype) && wide(dy, dy_stride, width, in_dtype) &&
                      wide(dx, width, width, in_dtype);
-    const NormPlan p = norm_plan(width, v16 ? (int)(16 / es) : 1, 2, gdn::kNormBwdThreads);
+    NormPlan p = v16 ? norm_plan(width, (int)(16 / es), 2, 256) : norm_plan(width, 1, 16, 256);
+    if (p.wide && v16) p = norm_plan(width, (int)(16 / es), 2, 512);
+    if (p.wide && v16) p = norm_plan(width, (int)(16 / es), 4, 512);
     a.tpr = p.tpr;
     int64_t parts = 0;
     if (rows > 0 && p.wide) {
@@ -563,14 +605,13 @@ gdn_status_t gdn_layer_norm_backward(const void* x, int64_t x_stride, const void
         }
         if (!launched()) return GDN_ERR_CUDA;
     } else if (rows > 0) {
-        parts = std::min<int64_t>(ceil_div(rows, p.threads / p.tpr), norm_parts(rows));
         bool ok;
         if (in_dtype == GDN_BF16)
-            ok = v16 ? launch_norm_bwd<__nv_bfloat16, 8>(a, p, (unsigned)parts, st)
-                     : launch_norm_bwd<__nv_bfloat16, 1>(a, p, (unsigned)parts, st);
+            ok = v16 ? launch_norm_bwd<__nv_bfloat16, 8>(a, p, &parts, st)
+                     : launch_norm_bwd<__nv_bfloat16, 1>(a, p, &parts, st);
         else
-            ok = v16 ? launch_norm_bwd<float, 4>(a, p, (unsigned)parts, st)
-                     : launch_norm_bwd<float, 1>(a, p, (unsigned)parts, st);
+            ok = v16 ? launch_norm_bwd<float, 4>(a, p, &parts, st)
+                     : launch_norm_bwd<float, 1>(a, p, &parts, st);
         if (!ok) return GDN_ERR_CUDA;
     }
     const int64_t M = 2 * (int64_t)width;
