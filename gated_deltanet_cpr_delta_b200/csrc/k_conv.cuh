@@ -99,9 +99,9 @@ __device__ __forceinline__ void conv_tail(const ConvArgs& a, int n, int64_t c)
 // worked on.  Where these lie in one sequence (almost everywhere) there is no test
 // per row.
 template <typename T, int W, int V>
-__global__ void __launch_bounds__(128, 8) k_conv_fwd(const ConvArgs a)
+__global__ void __launch_bounds__(128, 5) k_conv_fwd(const ConvArgs a)
 {
-    constexpr int U = 8;
+    constexpr int U = 6;
     if (blockIdx.x == 0) check_seqs(a.s, a.status);
     const int64_t tile = blockIdx.x / a.ncb;
     const int cb = (int)(blockIdx.x - tile * a.ncb);
@@ -133,9 +133,9 @@ __global__ void __launch_bounds__(128, 8) k_conv_fwd(const ConvArgs a)
     conv_window<T, W, V>(a, n, a.s.lo(n), t, c, win);
     auto row = [&](const Vec<T, V>& r, T* out, bool store) {
         float o[V];
-        widen<T, V>(r, win[W - 1]);
 #pragma unroll
         for (int k = 0; k < V; ++k) {
+            win[W - 1][k] = to_f<T>(r.v[k]);
             float p = taps.b[k];
 #pragma unroll
             for (int i = 0; i < W; ++i) p = __fmaf_rn(taps.w[i][k], win[i][k], p);
@@ -223,15 +223,13 @@ __device__ __forceinline__ void conv_bwd_run(const ConvArgs& a, int64_t t0, int6
         // One row.  `inner`: the row and the finished one are the run's own.
         auto row = [&](const Vec<T, V>& rx, const Vec<T, V>& rg, int64_t at, T* out, bool inner) {
             const bool own = inner || at < t1;
-            float gy[V];
-            widen<T, V>(rx, win[W - 1]);
-            widen<T, V>(rg, gy);
 #pragma unroll
             for (int k = 0; k < V; ++k) {
+                win[W - 1][k] = to_f<T>(rx.v[k]);
                 float p = taps.b[k];
 #pragma unroll
                 for (int i = 0; i < W; ++i) p = __fmaf_rn(taps.w[i][k], win[i][k], p);
-                float g = gy[k];
+                float g = to_f<T>(rg.v[k]);
                 if (a.silu) g *= silu_grad(p);
                 const float go = own ? g : 0.0f;
                 db[k] += go;

@@ -42,29 +42,12 @@ __device__ __forceinline__ Vec<T, V> load_vec(const T* p)
     return *reinterpret_cast<const Vec<T, V>*>(p);
 }
 
-// Two bf16 at once: widening is a shift or a mask, rounding one instruction.
+// Two bf16 rounded at once.
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
 {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
-}
-
-// the V values of r, widened
-template <typename T, int V>
-__device__ __forceinline__ void widen(const Vec<T, V>& r, float (&x)[V])
-{
-    if constexpr (sizeof(T) == 2 && V % 2 == 0) {
-        const uint32_t* u = reinterpret_cast<const uint32_t*>(&r);
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-            x[2 * i] = __uint_as_float(u[i] << 16);
-            x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = to_f<T>(r.v[i]);
-    }
 }
 
 template <typename T, int V>

@@ -420,12 +420,12 @@ gdn_status_t gdn_conv_forward(const void* x, int64_t x_stride, const void* weigh
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool v16 = wide(x, x_stride, channels, in_dtype) && wide(y, channels, channels, in_dtype);
     unsigned blocks = 0;
-    if (!conv_grid(a, v16 ? 2 : 1, 8, &blocks)) return GDN_ERR_INVALID_ARG;
+    if (!conv_grid(a, v16 ? 4 : 1, 5, &blocks)) return GDN_ERR_INVALID_ARG;
     if (in_dtype == GDN_BF16) {
-        if (v16) launch_conv_fwd<__nv_bfloat16, 2>(a, width, blocks, st);
+        if (v16) launch_conv_fwd<__nv_bfloat16, 4>(a, width, blocks, st);
         else launch_conv_fwd<__nv_bfloat16, 1>(a, width, blocks, st);
     } else {
-        if (v16) launch_conv_fwd<float, 2>(a, width, blocks, st);
+        if (v16) launch_conv_fwd<float, 4>(a, width, blocks, st);
         else launch_conv_fwd<float, 1>(a, width, blocks, st);
     }
     return launched() ? GDN_OK : GDN_ERR_CUDA;

@@ -9,6 +9,7 @@ calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Dict, Optional, Sequence
 
@@ -424,85 +425,112 @@ def gdn_cpr_forward_noalloc(q, k, v, alpha, beta, cu_seqlens, C: int, *, cu_seql
 # (include/gdn_cpr.h, "layer operators").  Token tensors may be row-strided
 # views (slices of one projection's output); everything else is contiguous.
 # All tensors of a call lie on one GPU, which need not be the current one.
+# The checks are written to cost little: a single-token step runs a few microseconds.
 
-def _where(like: torch.Tensor, what: str, *tensors: Optional[torch.Tensor]) -> torch.device:
-    """The call's device; every given tensor has to be on it."""
-    dev = like.device
-    if dev.type != "cuda":
+_F32 = torch.float32
+_DT = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16}
+
+
+def _dense(what: str, name: str, t: torch.Tensor, dtype: torch.dtype, shape, dev: int) -> int:
+    """The address of a contiguous tensor of this type and shape on device `dev`."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{what}: {name} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: {name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: tensors on cuda:{dev} and {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: {name} must be contiguous")
+    return t.data_ptr()
+
+
+def _opt(what: str, name: str, t: Optional[torch.Tensor], dtype: torch.dtype, shape, dev: int):
+    return None if t is None else _dense(what, name, t, dtype, shape, dev)
+
+
+def _out(what: str, name: str, t: Optional[torch.Tensor], dtype: torch.dtype, shape, dev: int):
+    """(tensor, address) of an output: a new one, or the caller's."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=dev)
+        return t, t.data_ptr()
+    return t, _dense(what, name, t, dtype, shape, dev)
+
+
+def _rows(what: str, name: str, t: torch.Tensor, dtype: torch.dtype, shape, dev: int):
+    """(address, elements between rows) of a token tensor whose rows are dense."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{what}: {name} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: {name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: tensors on cuda:{dev} and {t.device}")
+    width = 1
+    for n in shape[1:]:
+        width *= n
+    if t.is_contiguous():
+        return t.data_ptr(), width
+    w = 1
+    for n, st in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
+        if n != 1 and st != w:
+            raise ValueError(f"{what}: the rows of {name} must be contiguous")
+        w *= n
+    if shape[0] > 1 and t.stride(0) < width:
+        raise ValueError(f"{what}: the rows of {name} overlap")
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else width
+
+
+def _type(what: str, t: torch.Tensor) -> int:
+    dt = _DT.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{what}: unsupported dtype {t.dtype}")
+    return dt
+
+
+def _gpu(what: str, t: torch.Tensor) -> int:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{what}: tensors must be on a CUDA device")
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{what}: tensors on {dev} and {t.device}")
     return dev
 
 
-def _typed(what: str, dtype: torch.dtype, **tensors: Optional[torch.Tensor]) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.dtype != dtype:
-            raise ValueError(f"{what}: {name} must be {dtype}, not {t.dtype}")
-
-
-def _shaped(what: str, shape, **tensors: Optional[torch.Tensor]) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.shape != shape:
-            raise ValueError(f"{what}: {name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-
-
-def _row_stride(what: str, name: str, t: torch.Tensor) -> int:
-    """Elements between the rows of a token tensor whose rows are dense."""
-    width = 1
-    for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if n != 1 and s != width:
-            raise ValueError(f"{what}: the rows of {name} must be contiguous")
-        width *= n
-    if t.shape[0] <= 1:
-        return width
-    if t.stride(0) < width:
-        raise ValueError(f"{what}: the rows of {name} overlap")
-    return t.stride(0)
-
-
-def _p(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
-def _dense(what: str, **tensors: Optional[torch.Tensor]) -> None:
-    for name, t in tensors.items():
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"{what}: {name} must be contiguous")
-
-
-def _call(dev: torch.device, what: str, fn, *args) -> None:
-    """Run fn(*args, stream) on dev's current stream, with dev current."""
-    if torch.cuda.current_device() == dev.index:
-        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+def _call(dev: int, what: str, fn, *args) -> None:
+    """Run fn(*args, stream) on the current stream of device `dev`, with that device current."""
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
-    _check(st, what)
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if st != 0:
+        raise GdnError(st, what)
 
 
-def _sequences(what: str, cu: Optional[torch.Tensor]) -> int:
+def _sequences(what: str, cu: Optional[torch.Tensor], dev: int):
+    """(address, number of sequences) of device offsets; None: one sequence."""
     if cu is None:
-        return 1
-    if cu.dtype != torch.int32 or cu.dim() != 1 or cu.shape[0] < 1 or not cu.is_contiguous():
+        return None, 1
+    if cu.dtype is not torch.int32 or cu.dim() != 1 or cu.shape[0] < 1:
         raise ValueError(f"{what}: cu_seqlens must be a contiguous int32 vector")
-    return cu.shape[0] - 1
+    return _dense(what, "cu_seqlens", cu, torch.int32, cu.shape, dev), cu.shape[0] - 1
 
 
-def _scratch(what: str, workspace: Optional[torch.Tensor], nbytes: int, dev: torch.device) -> torch.Tensor:
+@functools.lru_cache(maxsize=1024)
+def _scratch_size(name: str, *sizes: int) -> int:
+    return int(getattr(load_library(), name)(*sizes))
+
+
+def _scratch(what: str, workspace: Optional[torch.Tensor], nbytes: int, dev: int):
+    """(tensor to keep alive, address, bytes)"""
     if workspace is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _dense(what, workspace=workspace)
-    return workspace
+        w = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        return w, w.data_ptr(), nbytes
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"{what}: workspace must be contiguous and on cuda:{dev}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _conv_sizes(what, x, weight, bias):
+def _conv_sizes(what, x, weight):
     if x.dim() != 2 or weight.dim() != 2 or weight.shape[0] != x.shape[1]:
         raise ValueError(f"{what}: x must be [tokens, channels] and weight [channels, width]")
-    _dense(what, weight=weight, bias=bias)
-    _typed(what, weight.dtype, bias=bias)
-    _shaped(what, (x.shape[1],), bias=bias)
     return x.shape[0], x.shape[1], weight.shape[1]
 
 
@@ -518,19 +546,18 @@ def gdn_conv_forward(x, weight, cu_seqlens=None, *, bias=None, state_in=None, si
     ``state_out``: optional buffers to write; rows of y outside every sequence
     keep their contents.  ``status``: an optional int32 that records bad offsets."""
     what = "gdn_conv_forward"
-    T, D, W = _conv_sizes(what, x, weight, bias)
-    N = _sequences(what, cu_seqlens)
-    dev = _where(x, what, weight, bias, cu_seqlens, state_in, y, state_out, status)
-    y = torch.empty(T, D, dtype=x.dtype, device=dev) if y is None else y
-    state_out = torch.empty(N, W - 1, D, dtype=x.dtype, device=dev) if state_out is None else state_out
-    _typed(what, x.dtype, y=y, state_in=state_in, state_out=state_out)
-    _typed(what, torch.int32, status=status)
-    _shaped(what, (T, D), y=y)
-    _shaped(what, (N, W - 1, D), state_in=state_in, state_out=state_out)
-    _dense(what, y=y, state_in=state_in, state_out=state_out)
-    _call(dev, what, load_library().gdn_conv_forward, _p(x), _row_stride(what, "x", x), _p(weight), _p(bias),
-          _p(state_in), _p(cu_seqlens), N, T, D, W, int(silu), _dt(x.dtype), _dt(weight.dtype), _p(y), _p(state_out),
-          _p(status))
+    T, D, W = _conv_sizes(what, x, weight)
+    dt, wt = x.dtype, weight.dtype
+    ti, wi = _type(what, x), _type(what, weight)
+    pc, N = _sequences(what, cu_seqlens, x.get_device())
+    dev = _gpu(what, x)
+    px, ldx = _rows(what, "x", x, dt, (T, D), dev)
+    pw = _dense(what, "weight", weight, wt, (D, W), dev)
+    y, py = _out(what, "y", y, dt, (T, D), dev)
+    state_out, ps = _out(what, "state_out", state_out, dt, (N, W - 1, D), dev)
+    _call(dev, what, load_library().gdn_conv_forward, px, ldx, pw, _opt(what, "bias", bias, wt, (D,), dev),
+          _opt(what, "state_in", state_in, dt, (N, W - 1, D), dev), pc, N, T, D, W, silu, ti, wi, py, ps,
+          _opt(what, "status", status, torch.int32, (1,), dev))
     return y, state_out
 
 
@@ -542,29 +569,25 @@ def gdn_conv_backward(x, weight, dy, cu_seqlens=None, *, bias=None, state_in=Non
     Returns (dx in x's dtype, dweight, dbias (None without a bias), dstate_in), the
     last three fp32.  ``grads``: an optional tuple of those four to write into."""
     what = "gdn_conv_backward"
-    T, D, W = _conv_sizes(what, x, weight, bias)
-    N = _sequences(what, cu_seqlens)
-    f32 = torch.float32
-    dev = _where(x, what, weight, bias, cu_seqlens, state_in, dy, dstate_out, workspace, status, *(grads or ()))
+    T, D, W = _conv_sizes(what, x, weight)
+    dt, wt = x.dtype, weight.dtype
+    ti, wi = _type(what, x), _type(what, weight)
+    dev = _gpu(what, x)
+    pc, N = _sequences(what, cu_seqlens, dev)
     if grads is None:
-        grads = (torch.empty(T, D, dtype=x.dtype, device=dev), torch.empty(D, W, dtype=f32, device=dev),
-                 None if bias is None else torch.empty(D, dtype=f32, device=dev),
-                 torch.empty(N, W - 1, D, dtype=f32, device=dev))
+        grads = (torch.empty((T, D), dtype=dt, device=dev), torch.empty((D, W), dtype=_F32, device=dev),
+                 None if bias is None else torch.empty((D,), dtype=_F32, device=dev),
+                 torch.empty((N, W - 1, D), dtype=_F32, device=dev))
     dx, dw, db, ds = grads
-    _typed(what, x.dtype, dy=dy, dx=dx, state_in=state_in)
-    _typed(what, f32, dweight=dw, dbias=db, dstate_in=ds, dstate_out=dstate_out)
-    _typed(what, torch.int32, status=status)
-    _shaped(what, (T, D), dy=dy, dx=dx)
-    _shaped(what, (D, W), dweight=dw)
-    _shaped(what, (D,), dbias=db)
-    _shaped(what, (N, W - 1, D), state_in=state_in, dstate_in=ds, dstate_out=dstate_out)
-    _dense(what, dx=dx, dweight=dw, dbias=db, dstate_in=ds, dstate_out=dstate_out, state_in=state_in)
-    lib = load_library()
-    workspace = _scratch(what, workspace, lib.gdn_conv_backward_workspace_size(T, N, D, W), dev)
-    _call(dev, what, lib.gdn_conv_backward, _p(x), _row_stride(what, "x", x), _p(weight), _p(bias), _p(state_in),
-          _p(dy), _row_stride(what, "dy", dy), _p(dstate_out), _p(cu_seqlens), N, T, D, W, int(silu), _dt(x.dtype),
-          _dt(weight.dtype), _p(dx), _p(dw), _p(db), _p(ds), _p(workspace), workspace.numel() * workspace.element_size(),
-          _p(status))
+    px, ldx = _rows(what, "x", x, dt, (T, D), dev)
+    pg, ldg = _rows(what, "dy", dy, dt, (T, D), dev)
+    keep, ws, nbytes = _scratch(what, workspace, _scratch_size("gdn_conv_backward_workspace_size", T, N, D, W), dev)
+    _call(dev, what, load_library().gdn_conv_backward, px, ldx, _dense(what, "weight", weight, wt, (D, W), dev),
+          _opt(what, "bias", bias, wt, (D,), dev), _opt(what, "state_in", state_in, dt, (N, W - 1, D), dev), pg, ldg,
+          _opt(what, "dstate_out", dstate_out, _F32, (N, W - 1, D), dev), pc, N, T, D, W, silu, ti, wi,
+          _dense(what, "dx", dx, dt, (T, D), dev), _dense(what, "dweight", dw, _F32, (D, W), dev),
+          _opt(what, "dbias", db, _F32, (D,), dev), _dense(what, "dstate_in", ds, _F32, (N, W - 1, D), dev), ws, nbytes,
+          _opt(what, "status", status, torch.int32, (1,), dev))
     return grads
 
 
@@ -572,34 +595,38 @@ def gdn_conv_step(x, weight, state, *, bias=None, silu: bool = True, y=None, sta
     """One token per sequence: x [N, channels], state [N, W-1, channels] (from
     :func:`gdn_conv_forward`), updated in place or written to ``state_out``.  Returns y [N, channels]."""
     what = "gdn_conv_step"
-    N, D, W = _conv_sizes(what, x, weight, bias)
-    dev = _where(x, what, weight, bias, state, y, state_out)
-    y = torch.empty(N, D, dtype=x.dtype, device=dev) if y is None else y
-    state_out = state if state_out is None else state_out
-    _typed(what, x.dtype, y=y, state=state, state_out=state_out)
-    _shaped(what, (N, D), y=y)
-    _shaped(what, (N, W - 1, D), state=state, state_out=state_out)
-    _dense(what, y=y, state=state, state_out=state_out)
-    _call(dev, what, load_library().gdn_conv_step, _p(x), _row_stride(what, "x", x), _p(weight), _p(bias), _p(state),
-          _p(state_out), N, D, W, int(silu), _dt(x.dtype), _dt(weight.dtype), _p(y))
+    N, D, W = _conv_sizes(what, x, weight)
+    dt, wt = x.dtype, weight.dtype
+    ti, wi = _type(what, x), _type(what, weight)
+    dev = _gpu(what, x)
+    px, ldx = _rows(what, "x", x, dt, (N, D), dev)
+    y, py = _out(what, "y", y, dt, (N, D), dev)
+    ps = _dense(what, "state", state, dt, (N, W - 1, D), dev)
+    _call(dev, what, load_library().gdn_conv_step, px, ldx, _dense(what, "weight", weight, wt, (D, W), dev),
+          _opt(what, "bias", bias, wt, (D,), dev), ps,
+          ps if state_out is None else _dense(what, "state_out", state_out, dt, (N, W - 1, D), dev), N, D, W, silu, ti,
+          wi, py)
     return y
 
 
-def _ssm_struct(what, x, dt, A, B, C, cu, N, D, z, dt_bias, dt_softplus) -> SsmStruct:
+def _ssm_struct(what, x, dt, A, B, C, pc, N, D, z, dt_bias, dt_softplus) -> SsmStruct:
     if x.dim() != 2 or B.dim() != 3:
         raise ValueError(f"{what}: x must be [tokens, channels] and B [tokens, groups, states]")
-    (T, ch), (G, S) = x.shape, B.shape[1:]
-    _typed(what, x.dtype, dt=dt, B=B, C=C, z=z)
-    _typed(what, torch.float32, A=A, D=D, dt_bias=dt_bias)
-    _shaped(what, (T, ch), dt=dt, z=z)
-    _shaped(what, (T, G, S), B=B, C=C)
-    _shaped(what, (ch, S), A=A)
-    _shaped(what, (ch,), D=D, dt_bias=dt_bias)
-    _dense(what, A=A, D=D, dt_bias=dt_bias)
-    return SsmStruct(_p(x), _p(dt), _p(B), _p(C), _p(z), _p(A), _p(D), _p(dt_bias), _p(cu),
-                     _row_stride(what, "x", x), _row_stride(what, "dt", dt), _row_stride(what, "B", B),
-                     _row_stride(what, "C", C), 0 if z is None else _row_stride(what, "z", z), T, N, ch, G, S,
-                     int(dt_softplus), _dt(x.dtype))
+    T, ch = x.shape
+    _, G, S = B.shape
+    ty = x.dtype
+    ti = _type(what, x)
+    dev = x.get_device()
+    tc, ts, cs = (T, ch), (T, G, S), (ch,)
+    px, lx = _rows(what, "x", x, ty, tc, dev)
+    pd, ld = _rows(what, "dt", dt, ty, tc, dev)
+    pB, lB = _rows(what, "B", B, ty, ts, dev)
+    pC, lC = _rows(what, "C", C, ty, ts, dev)
+    pz, lz = (None, 0) if z is None else _rows(what, "z", z, ty, tc, dev)
+    s = SsmStruct(px, pd, pB, pC, pz, _dense(what, "A", A, _F32, (ch, S), dev), _opt(what, "D", D, _F32, cs, dev),
+                  _opt(what, "dt_bias", dt_bias, _F32, cs, dev), pc, lx, ld, lB, lC, lz, T, N, ch, G, S, dt_softplus, ti)
+    _gpu(what, x)
+    return s
 
 
 def gdn_ssm_num_chunk_states(total_tokens: int, num_seqs: int) -> int:
@@ -621,24 +648,17 @@ def gdn_ssm_forward(x, dt, A, B, C, cu_seqlens=None, *, D=None, z=None, dt_bias=
     Returns (y, state_out, chunk_states).  chunk_states (with ``save_states``; else
     None) is what :func:`gdn_ssm_backward` reads."""
     what = "gdn_ssm_forward"
-    N = _sequences(what, cu_seqlens)
-    s = _ssm_struct(what, x, dt, A, B, C, cu_seqlens, N, D, z, dt_bias, dt_softplus)
-    dev = _where(x, what, dt, A, B, C, cu_seqlens, D, z, dt_bias, state_in, y, state_out, chunk_states, status)
-    T, ch, S, f32 = s.total_tokens, s.channels, s.states, torch.float32
-    lib = load_library()
-    y = torch.empty(T, ch, dtype=x.dtype, device=dev) if y is None else y
-    state_out = torch.empty(N, ch, S, dtype=f32, device=dev) if state_out is None else state_out
+    dev = x.get_device()
+    pc, N = _sequences(what, cu_seqlens, dev)
+    s = _ssm_struct(what, x, dt, A, B, C, pc, N, D, z, dt_bias, dt_softplus)
+    T, ch, S, ty = s.total_tokens, s.channels, s.states, x.dtype
+    y, py = _out(what, "y", y, ty, (T, ch), dev)
+    state_out, ps = _out(what, "state_out", state_out, _F32, (N, ch, S), dev)
+    saved = (T // SSM_CHUNK + N, ch, S)
     if chunk_states is None and save_states:
-        chunk_states = torch.empty(gdn_ssm_num_chunk_states(T, N), ch, S, dtype=f32, device=dev)
-    if chunk_states is not None:
-        _shaped(what, (gdn_ssm_num_chunk_states(T, N), ch, S), chunk_states=chunk_states)
-    _typed(what, x.dtype, y=y)
-    _typed(what, f32, state_in=state_in, state_out=state_out, chunk_states=chunk_states)
-    _typed(what, torch.int32, status=status)
-    _shaped(what, (T, ch), y=y)
-    _shaped(what, (N, ch, S), state_in=state_in, state_out=state_out)
-    _dense(what, y=y, state_in=state_in, state_out=state_out, chunk_states=chunk_states)
-    _call(dev, what, lib.gdn_ssm_forward, s, _p(state_in), _p(y), _p(state_out), _p(chunk_states), _p(status))
+        chunk_states = torch.empty(saved, dtype=_F32, device=dev)
+    _call(dev, what, load_library().gdn_ssm_forward, s, _opt(what, "state_in", state_in, _F32, (N, ch, S), dev),
+          py, ps, _opt(what, "chunk_states", chunk_states, _F32, saved, dev), _opt(what, "status", status, torch.int32, (1,), dev))
     return y, state_out, chunk_states
 
 
@@ -651,37 +671,28 @@ def gdn_ssm_backward(x, dt, A, B, C, dy, chunk_states, cu_seqlens=None, *, D=Non
     dz in x's dtype, the others fp32; dD, dz and ddt_bias are None where the
     forward had no D, z or dt_bias.  ``grads``: an optional tuple of those nine to write into."""
     what = "gdn_ssm_backward"
-    N = _sequences(what, cu_seqlens)
-    s = _ssm_struct(what, x, dt, A, B, C, cu_seqlens, N, D, z, dt_bias, dt_softplus)
-    dev = _where(x, what, dt, A, B, C, dy, chunk_states, cu_seqlens, D, z, dt_bias, dstate_out, workspace, status,
-                 *(grads or ()))
-    T, ch, G, S, f32 = s.total_tokens, s.channels, s.groups, s.states, torch.float32
-    lib = load_library()
+    dev = x.get_device()
+    pc, N = _sequences(what, cu_seqlens, dev)
+    s = _ssm_struct(what, x, dt, A, B, C, pc, N, D, z, dt_bias, dt_softplus)
+    T, ch, G, S, ty = s.total_tokens, s.channels, s.groups, s.states, x.dtype
+    tc, ts, st, cs = (T, ch), (T, G, S), (N, ch, S), (ch,)
     if grads is None:
-        tok = dict(dtype=x.dtype, device=dev)
-        par = dict(dtype=f32, device=dev)
-        grads = (torch.empty(T, ch, **tok), torch.empty(T, ch, **tok), torch.empty(ch, S, **par),
-                 torch.empty(T, G, S, **tok), torch.empty(T, G, S, **tok),
-                 None if D is None else torch.empty(ch, **par), None if z is None else torch.empty(T, ch, **tok),
-                 None if dt_bias is None else torch.empty(ch, **par), torch.empty(N, ch, S, **par))
+        new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
+        grads = (new(tc, ty), new(tc, ty), new((ch, S), _F32), new(ts, ty), new(ts, ty),
+                 None if D is None else new(cs, _F32), None if z is None else new(tc, ty),
+                 None if dt_bias is None else new(cs, _F32), new(st, _F32))
     dx, ddt, dA, dB, dC, dD, dz, dbias, ds = grads
     if z is not None and dz is None:
         raise ValueError(f"{what}: dz is needed with z")
-    _typed(what, x.dtype, dy=dy, dx=dx, ddt=ddt, dB=dB, dC=dC, dz=dz)
-    _typed(what, f32, dA=dA, dD=dD, ddt_bias=dbias, dstate_in=ds, dstate_out=dstate_out, chunk_states=chunk_states)
-    _typed(what, torch.int32, status=status)
-    _shaped(what, (T, ch), dy=dy, dx=dx, ddt=ddt, dz=dz)
-    _shaped(what, (T, G, S), dB=dB, dC=dC)
-    _shaped(what, (ch, S), dA=dA)
-    _shaped(what, (ch,), dD=dD, ddt_bias=dbias)
-    _shaped(what, (N, ch, S), dstate_in=ds, dstate_out=dstate_out)
-    _shaped(what, (gdn_ssm_num_chunk_states(T, N), ch, S), chunk_states=chunk_states)
-    _dense(what, dx=dx, ddt=ddt, dA=dA, dB=dB, dC=dC, dD=dD, dz=dz, ddt_bias=dbias, dstate_in=ds,
-           dstate_out=dstate_out, chunk_states=chunk_states)
-    workspace = _scratch(what, workspace, lib.gdn_ssm_backward_workspace_size(T, N, ch, G, S), dev)
-    _call(dev, what, lib.gdn_ssm_backward, s, _p(dy), _row_stride(what, "dy", dy), _p(chunk_states), _p(dstate_out),
-          _p(dx), _p(ddt), _p(dA), _p(dB), _p(dC), _p(dD), _p(dz), _p(dbias), _p(ds), _p(workspace),
-          workspace.numel() * workspace.element_size(), _p(status))
+    pg, ldg = _rows(what, "dy", dy, ty, tc, dev)
+    keep, ws, nbytes = _scratch(what, workspace, _scratch_size("gdn_ssm_backward_workspace_size", T, N, ch, G, S), dev)
+    _call(dev, what, load_library().gdn_ssm_backward, s, pg, ldg,
+          _dense(what, "chunk_states", chunk_states, _F32, (T // SSM_CHUNK + N, ch, S), dev),
+          _opt(what, "dstate_out", dstate_out, _F32, st, dev), _dense(what, "dx", dx, ty, tc, dev),
+          _dense(what, "ddt", ddt, ty, tc, dev), _dense(what, "dA", dA, _F32, (ch, S), dev),
+          _dense(what, "dB", dB, ty, ts, dev), _dense(what, "dC", dC, ty, ts, dev), _opt(what, "dD", dD, _F32, cs, dev),
+          _opt(what, "dz", dz, ty, tc, dev), _opt(what, "ddt_bias", dbias, _F32, cs, dev),
+          _dense(what, "dstate_in", ds, _F32, st, dev), ws, nbytes, _opt(what, "status", status, torch.int32, (1,), dev))
     return grads
 
 
@@ -691,16 +702,13 @@ def gdn_ssm_step(x, dt, A, B, C, state, *, D=None, z=None, dt_bias=None, dt_soft
     :func:`gdn_ssm_forward`), updated in place or written to ``state_out``.  Returns y [N, channels]."""
     what = "gdn_ssm_step"
     s = _ssm_struct(what, x, dt, A, B, C, None, x.shape[0], D, z, dt_bias, dt_softplus)
-    dev = _where(x, what, dt, A, B, C, state, D, z, dt_bias, y, state_out)
-    N, ch = x.shape
-    y = torch.empty(N, ch, dtype=x.dtype, device=dev) if y is None else y
-    state_out = state if state_out is None else state_out
-    _typed(what, x.dtype, y=y)
-    _typed(what, torch.float32, state=state, state_out=state_out)
-    _shaped(what, (N, ch), y=y)
-    _shaped(what, (N, ch, s.states), state=state, state_out=state_out)
-    _dense(what, y=y, state=state, state_out=state_out)
-    _call(dev, what, load_library().gdn_ssm_step, s, _p(state), _p(state_out), _p(y))
+    dev = x.get_device()
+    shape = (s.num_seqs, s.channels, s.states)
+    y, py = _out(what, "y", y, x.dtype, shape[:2], dev)
+    ps = _dense(what, "state", state, _F32, shape, dev)
+    _call(dev, what, load_library().gdn_ssm_step, s, ps,
+          ps if state_out is None else _dense(what, "state_out", state_out, _F32, shape, dev),
+          py)
     return y
 
 
@@ -710,6 +718,8 @@ def _rows2d(what: str, name: str, t: torch.Tensor) -> torch.Tensor:
         return t
     if t.dim() < 1:
         raise ValueError(f"{what}: {name} must have at least one axis")
+    if t.numel() == 0:
+        return t.reshape(t.numel() // max(1, t.shape[-1]), t.shape[-1])
     try:
         return t.view(-1, t.shape[-1])
     except RuntimeError:
@@ -723,17 +733,15 @@ def gdn_layer_norm_forward(x, weight, *, bias=None, eps: float = 1e-5, y=None):
     what = "gdn_layer_norm_forward"
     x2 = _rows2d(what, "x", x)
     R, D = x2.shape
-    dev = _where(x, what, weight, bias, y)
-    _dense(what, weight=weight, bias=bias, y=y)
-    _typed(what, weight.dtype, bias=bias)
-    _shaped(what, (D,), weight=weight, bias=bias)
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev) if y is None else y
-    _typed(what, x.dtype, y=y)
-    _shaped(what, x.shape, y=y)
-    stats = torch.empty((2,) + x.shape[:-1], dtype=torch.float32, device=dev)
-    mean, rstd = stats[0], stats[1]
-    _call(dev, what, load_library().gdn_layer_norm_forward, _p(x2), _row_stride(what, "x", x2), _p(weight), _p(bias),
-          eps, R, D, _dt(x.dtype), _dt(weight.dtype), _p(y), _p(mean), _p(rstd))
+    dt, wt, shape = x.dtype, weight.dtype, x.shape
+    ti, wi = _type(what, x), _type(what, weight)
+    dev = _gpu(what, x)
+    px, ldx = _rows(what, "x", x2, dt, (R, D), dev)
+    y, py = _out(what, "y", y, dt, shape, dev)
+    mean = torch.empty(shape[:-1], dtype=_F32, device=dev)
+    rstd = torch.empty(shape[:-1], dtype=_F32, device=dev)
+    _call(dev, what, load_library().gdn_layer_norm_forward, px, ldx, _dense(what, "weight", weight, wt, (D,), dev),
+          _opt(what, "bias", bias, wt, (D,), dev), eps, R, D, ti, wi, py, mean.data_ptr(), rstd.data_ptr())
     return y, mean, rstd
 
 
@@ -745,21 +753,20 @@ def gdn_layer_norm_backward(x, weight, dy, mean, rstd, *, workspace=None, grads=
     what = "gdn_layer_norm_backward"
     x2, g2 = _rows2d(what, "x", x), _rows2d(what, "dy", dy)
     R, D = x2.shape
-    f32 = torch.float32
-    dev = _where(x, what, weight, dy, mean, rstd, workspace, *(grads or ()))
+    dt, wt, shape = x.dtype, weight.dtype, x.shape
+    ti, wi = _type(what, x), _type(what, weight)
+    dev = _gpu(what, x)
+    if dy.shape != shape:
+        raise ValueError(f"{what}: dy must have shape {tuple(shape)}, not {tuple(dy.shape)}")
     if grads is None:
-        par = torch.empty(2, D, dtype=f32, device=dev)
-        grads = (torch.empty(x.shape, dtype=x.dtype, device=dev), par[0], par[1])
+        grads = (torch.empty(shape, dtype=dt, device=dev), torch.empty((D,), dtype=_F32, device=dev),
+                 torch.empty((D,), dtype=_F32, device=dev))
     dx, dw, db = grads
-    _typed(what, x.dtype, dy=dy, dx=dx)
-    _typed(what, f32, mean=mean, rstd=rstd, dweight=dw, dbias=db)
-    _shaped(what, x.shape, dy=dy, dx=dx)
-    _shaped(what, x.shape[:-1], mean=mean, rstd=rstd)
-    _shaped(what, (D,), weight=weight, dweight=dw, dbias=db)
-    _dense(what, weight=weight, mean=mean, rstd=rstd, dx=dx, dweight=dw, dbias=db)
-    lib = load_library()
-    workspace = _scratch(what, workspace, lib.gdn_layer_norm_backward_workspace_size(R, D), dev)
-    _call(dev, what, lib.gdn_layer_norm_backward, _p(x2), _row_stride(what, "x", x2), _p(g2),
-          _row_stride(what, "dy", g2), _p(weight), _p(mean), _p(rstd), R, D, _dt(x.dtype), _dt(weight.dtype), _p(dx),
-          _p(dw), _p(db), _p(workspace), workspace.numel() * workspace.element_size())
+    px, ldx = _rows(what, "x", x2, dt, (R, D), dev)
+    pg, ldg = _rows(what, "dy", g2, dt, (R, D), dev)
+    keep, ws, nbytes = _scratch(what, workspace, _scratch_size("gdn_layer_norm_backward_workspace_size", R, D), dev)
+    _call(dev, what, load_library().gdn_layer_norm_backward, px, ldx, pg, ldg,
+          _dense(what, "weight", weight, wt, (D,), dev), _dense(what, "mean", mean, _F32, shape[:-1], dev),
+          _dense(what, "rstd", rstd, _F32, shape[:-1], dev), R, D, ti, wi, _dense(what, "dx", dx, dt, shape, dev),
+          _dense(what, "dweight", dw, _F32, (D,), dev), _opt(what, "dbias", db, _F32, (D,), dev), ws, nbytes)
     return grads
