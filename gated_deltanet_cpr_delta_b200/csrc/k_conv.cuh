@@ -44,12 +44,15 @@ struct ConvTaps {
     float w[W][V], b[V];
     __device__ __forceinline__ void load(const ConvArgs& a, int64_t c)
     {
+float raw[V * W];
+        load_ws<V * W>(a.w, a.w_bf16, c * W, raw);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
+            b[v] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < W; ++i) w[i][v] = load_w(a.w, a.w_bf16, (c + v) * W + i);
-            b[v] = a.bias != nullptr ? load_w(a.bias, a.w_bf16, c + v) : 0.0f;
+            for (int i = 0; i < W; ++i) w[i][v] = raw[v * W + i];
         }
+        if (a.bias != nullptr) load_ws<V>(a.bias, a.w_bf16, c, b);
     }
 };
 
@@ -383,13 +386,16 @@ __global__ void __launch_bounds__(128) k_conv_step(const T* __restrict__ x, int6
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) win[i] = load_vec<T, V>(state + (n * (W - 1) + i) * D + c);
     win[W - 1] = load_vec<T, V>(x + n * ldx + c);
-    float o[V];
+    float o[V], taps[V * W];
+    load_ws<V * W>(w, w_bf16, c * W, taps);
+#pragma unroll
+    for (int k = 0; k < V; ++k) o[k] = 0.0f;
+    if (bias != nullptr) load_ws<V>(bias, w_bf16, c, o);
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-        float p = bias != nullptr ? load_w(bias, w_bf16, c + k) : 0.0f;
 #pragma unroll
-        for (int i = 0; i < W; ++i) p = __fmaf_rn(load_w(w, w_bf16, (c + k) * W + i), to_f<T>(win[i].v[k]), p);
-        o[k] = silu_on ? silu(p) : p;
+        for (int i = 0; i < W; ++i) o[k] = __fmaf_rn(taps[k * W + i], to_f<T>(win[i].v[k]), o[k]);
+        if (silu_on) o[k] = silu(o[k]);
     }
     store_vec<T, V>(y + n * D + c, o);
 #pragma unroll

@@ -285,29 +285,44 @@ template <typename T, int S>
 __global__ void __launch_bounds__(256) k_ssm_step(const SsmArgs a)
 {
     constexpr int LN = S / 4;
-    const int64_t id = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LN;
-    const int q = threadIdx.x & (LN - 1);
-    const bool on = id < a.s.N * (int64_t)a.D;
-    const int64_t i = on ? id : 0;
-    const int64_t n = i / a.D;
-    const int c = (int)(i - n * a.D), e = c / a.Dg;
+    // a grid row per sequence; 256 / LN channels per block
+    const int64_t n = blockIdx.y;
+    const int cc = blockIdx.x * (256 / LN) + threadIdx.x / LN, q = threadIdx.x & (LN - 1);
+    const bool on = cc < a.D;
+    const int c = on ? cc : 0, e = a.G == 1 ? 0 : c / a.Dg;
+    const int64_t i = n * a.D + c;
     const float4 h = *reinterpret_cast<const float4*>(a.state_in + i * S + 4 * q);
     const float4 A = *reinterpret_cast<const float4*>(a.A + (int64_t)c * S + 4 * q);
     const float x = to_f<T>(static_cast<const T*>(a.x)[n * a.ldx + c]);
     const float d = ssm_delta(a, to_f<T>(static_cast<const T*>(a.dt)[n * a.lddt + c]),
                               a.dt_bias != nullptr ? a.dt_bias[c] : 0.0f);
-    const T* B = static_cast<const T*>(a.B) + n * a.ldB + e * S + 4 * q;
-    const T* C = static_cast<const T*>(a.C) + n * a.ldC + e * S + 4 * q;
+    const T* pB = static_cast<const T*>(a.B) + n * a.ldB + e * S + 4 * q;
+    const T* pC = static_cast<const T*>(a.C) + n * a.ldC + e * S + 4 * q;
+    float B[4], C[4];
+    if (a.bc16) {
+        const Vec<T, 4> vb = load_vec<T, 4>(pB), vc = load_vec<T, 4>(pC);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            B[k] = to_f<T>(vb.v[k]);
+            C[k] = to_f<T>(vc.v[k]);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            B[k] = to_f<T>(pB[k]);
+            C[k] = to_f<T>(pC[k]);
+        }
+    }
     const float u = d * x, d2 = d * kLog2e;
     float4 o;
-    o.x = __fmaf_rn(ex2(d2 * A.x), h.x, u * to_f<T>(B[0]));
-    o.y = __fmaf_rn(ex2(d2 * A.y), h.y, u * to_f<T>(B[1]));
-    o.z = __fmaf_rn(ex2(d2 * A.z), h.z, u * to_f<T>(B[2]));
-    o.w = __fmaf_rn(ex2(d2 * A.w), h.w, u * to_f<T>(B[3]));
-    float s = o.x * to_f<T>(C[0]);
-    s = __fmaf_rn(o.y, to_f<T>(C[1]), s);
-    s = __fmaf_rn(o.z, to_f<T>(C[2]), s);
-    s = __fmaf_rn(o.w, to_f<T>(C[3]), s);
+    o.x = __fmaf_rn(ex2(d2 * A.x), h.x, u * B[0]);
+    o.y = __fmaf_rn(ex2(d2 * A.y), h.y, u * B[1]);
+    o.z = __fmaf_rn(ex2(d2 * A.z), h.z, u * B[2]);
+    o.w = __fmaf_rn(ex2(d2 * A.w), h.w, u * B[3]);
+    float s = o.x * C[0];
+    s = __fmaf_rn(o.y, C[1], s);
+    s = __fmaf_rn(o.z, C[2], s);
+    s = __fmaf_rn(o.w, C[3], s);
 #pragma unroll
     for (int w = LN / 2; w > 0; w >>= 1) s += __shfl_xor_sync(kFullMask, s, w);
     if (!on) return;

@@ -10,6 +10,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "schedule.cuh"
 
 namespace gdn {
@@ -131,6 +133,30 @@ __device__ __forceinline__ void pstore(T* p, const typename Lanes<V>::type* x)
 __device__ __forceinline__ float load_w(const void* w, int bf16, int64_t i)
 {
     return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i]) : static_cast<const float*>(w)[i];
+}
+
+// n consecutive weights from element i on, in accesses as wide as n elements and the address allow
+template <int N>
+__device__ __forceinline__ void load_ws(const void* w, int bf16, int64_t i, float (&x)[N])
+{
+    auto run = [&](auto* p) {
+        using WT = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
+        constexpr int B = N * sizeof(WT);  // bytes
+        constexpr int A = B % 16 == 0 ? 16 : B % 8 == 0 ? 8 : B % 4 == 0 ? 4 : (int)sizeof(WT), E = A / (int)sizeof(WT);
+        if ((reinterpret_cast<uintptr_t>(p) & (A - 1)) == 0) {
+#pragma unroll
+            for (int j = 0; j < N / E; ++j) {
+                const Vec<WT, E> v = load_vec<WT, E>(p + j * E);
+#pragma unroll
+                for (int k = 0; k < E; ++k) x[j * E + k] = to_f<WT>(v.v[k]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j) x[j] = to_f<WT>(p[j]);
+        }
+    };
+    if (bf16) run(static_cast<const __nv_bfloat16*>(w) + i);
+    else run(static_cast<const float*>(w) + i);
 }
 
 // The packed batch: sequence n holds rows [lo(n), hi(n)).  Offsets come from

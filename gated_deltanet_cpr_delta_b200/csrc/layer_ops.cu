@@ -385,9 +385,20 @@ gdn_status_t ssm_backward_launch(const gdn::SsmBwdArgs& b, void* dB, void* dC, f
 template <typename T, int S>
 gdn_status_t ssm_step_launch(const gdn::SsmArgs& a, cudaStream_t st)
 {
-    const int64_t blocks = ceil_div((int64_t)a.s.N * a.D * (S / 4), 256);
-    if (blocks > INT32_MAX) return GDN_ERR_INVALID_ARG;
-    gdn::k_ssm_step<T, S><<<(unsigned)blocks, 256, 0, st>>>(a);
+    const unsigned across = (unsigned)ceil_div(a.D, 1024 / S);
+    for (int n = 0; n < a.s.N; n += 65535) {  // a grid has at most 65535 rows
+        gdn::SsmArgs b = a;
+        const int64_t es = sizeof(T), per = (int64_t)a.D * S;
+        b.x = static_cast<const char*>(a.x) + n * a.ldx * es;
+        b.dt = static_cast<const char*>(a.dt) + n * a.lddt * es;
+        b.z = a.z != nullptr ? static_cast<const char*>(a.z) + n * a.ldz * es : nullptr;
+        b.B = static_cast<const char*>(a.B) + n * a.ldB * es;
+        b.C = static_cast<const char*>(a.C) + n * a.ldC * es;
+        b.state_in = a.state_in + n * per;
+        b.state_out = a.state_out + n * per;
+        b.y = static_cast<char*>(a.y) + n * (int64_t)a.D * es;
+        gdn::k_ssm_step<T, S><<<dim3(across, (unsigned)std::min(65535, a.s.N - n)), 256, 0, st>>>(b);
+    }
     return launched() ? GDN_OK : GDN_ERR_CUDA;
 }
 
