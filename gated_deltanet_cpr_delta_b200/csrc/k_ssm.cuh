@@ -66,10 +66,13 @@ struct SsmFwdCfg {
                                     sizeof(float) * 2 * S * CB;
 };
 
-__device__ __forceinline__ void ssm_cp_async16(void* smem, const void* gmem)
+// 16 bytes past L1, or 4 bytes (rows that are not whole 16-byte vectors)
+template <int BYTES>
+__device__ __forceinline__ void ssm_cp_async(void* smem, const void* gmem)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(smem)), "l"(gmem)
-                 : "memory");
+    const unsigned to = (unsigned)__cvta_generic_to_shared(smem);
+    if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(gmem) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(gmem), "n"(BYTES) : "memory");
 }
 
 template <typename T, int S, int V, int SEG>
@@ -122,10 +125,10 @@ __global__ void __launch_bounds__(SsmFwdCfg<T, S, SEG>::THREADS, SEG == 32 ? 2 :
                 const T* px = static_cast<const T*>(a.x) + at(row, a.ldx) + cbase + v;
                 const T* pd = static_cast<const T*>(a.dt) + at(row, a.lddt) + cbase + v;
                 const T* pz = a.z != nullptr ? static_cast<const T*>(a.z) + at(row, a.ldz) + cbase + v : nullptr;
-                if (V * sizeof(T) == 16) {
-                    ssm_cp_async16(d, px);
-                    ssm_cp_async16(d + Cf::TOK, pd);
-                    if (pz != nullptr) ssm_cp_async16(d + 2 * Cf::TOK, pz);
+                if constexpr (V * sizeof(T) >= 4) {
+                    ssm_cp_async<V * sizeof(T)>(d, px);
+                    ssm_cp_async<V * sizeof(T)>(d + Cf::TOK, pd);
+                    if (pz != nullptr) ssm_cp_async<V * sizeof(T)>(d + 2 * Cf::TOK, pz);
                 } else {
 #pragma unroll
                     for (int k = 0; k < V; ++k) {
@@ -143,8 +146,8 @@ __global__ void __launch_bounds__(SsmFwdCfg<T, S, SEG>::THREADS, SEG == 32 ? 2 :
         if (a.bc16) {
             for (int i = tid; i < rows * (S / VB); i += NT) {
                 const int t = i / (S / VB), v = (i % (S / VB)) * VB;
-                ssm_cp_async16(rawB + t * S + v, B + at((int)(lo + p) + t, a.ldB) + v);
-                ssm_cp_async16(rawB + (TT + t) * S + v, C + at((int)(lo + p) + t, a.ldC) + v);
+                ssm_cp_async<16>(rawB + t * S + v, B + at((int)(lo + p) + t, a.ldB) + v);
+                ssm_cp_async<16>(rawB + (TT + t) * S + v, C + at((int)(lo + p) + t, a.ldC) + v);
             }
         } else {
             for (int i = tid; i < rows * S; i += NT) {
