@@ -166,14 +166,16 @@ __global__ void __launch_bounds__(kSsmThreads, 4) k_ssm_rev(const SsmBwdArgs b)
         for (int i = 0; i < NVEC; ++i) {
             const int r = vr + i * RSTEP;
             if (r < TT) {
+                const bool in = vok && r < rows;
+                float vd[V], vu[V];
 #pragma unroll
                 for (int k = 0; k < V; ++k) {
-                    const bool in = vok && r < rows;
-                    float u = to_f<T>(rx[i].v[k]);
-                    if (z != nullptr) u *= silu(to_f<T>(rz[i].v[k]));
-                    sd[r][vc + k] = in ? ssm_delta(a, to_f<T>(rd[i].v[k]), bias != nullptr ? bias[k] : 0.0f) : 0.0f;
-                    su[r][vc + k] = in ? u : 0.0f;
+                    vu[k] = in ? to_f<T>(rx[i].v[k]) : 0.0f;
+                    if (z != nullptr && in) vu[k] *= silu(to_f<T>(rz[i].v[k]));
+                    vd[k] = in ? ssm_delta(a, to_f<T>(rd[i].v[k]), bias != nullptr ? bias[k] : 0.0f) : 0.0f;
                 }
+                put_row<V>(&sd[r][vc], vd);
+                put_row<V>(&su[r][vc], vu);
             }
         }
 #pragma unroll
@@ -333,13 +335,16 @@ __global__ void __launch_bounds__(kSsmThreads, 3) k_ssm_bwd(const SsmBwdArgs b)
 
     const int vc = (tid % PER_ROW) * V, vr = tid / PER_ROW;
     const bool vok = cbase + vc < cend;
-    float bias[V], Dv[V], dbias[V];
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-        bias[k] = vok && a.dt_bias != nullptr ? a.dt_bias[cbase + vc + k] : 0.0f;
-        Dv[k] = vok && a.Dp != nullptr ? a.Dp[cbase + vc + k] : 0.0f;
-        dbias[k] = 0.0f;
+    __shared__ __align__(16) float sbias[CB], sD[CB];
+    if (tid < CB) {
+        const bool ok = cbase + tid < cend;
+        sbias[tid] = ok && a.dt_bias != nullptr ? a.dt_bias[cbase + tid] : 0.0f;
+        sD[tid] = ok && a.Dp != nullptr ? a.Dp[cbase + tid] : 0.0f;
     }
+    __syncthreads();
+    float dbias[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) dbias[k] = 0.0f;
     const T* x = static_cast<const T*>(a.x) + cbase + vc;
     const T* dt = static_cast<const T*>(a.dt) + cbase + vc;
     const T* dy = static_cast<const T*>(b.dy) + cbase + vc;
@@ -385,12 +390,17 @@ __global__ void __launch_bounds__(kSsmThreads, 3) k_ssm_bwd(const SsmBwdArgs b)
                 wg = load_vec<T, V>(dy + row * b.lddy);
                 if (GATE) wz = load_vec<T, V>(z + row * a.ldz);
             }
+            float vb[V], vd[V], vx[V], vg[V];
+            get_row<V>(sbias + vc, vb);
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                sd[r * CB + vc + k] = in ? ssm_delta(a, to_f<T>(wd.v[k]), bias[k]) : 0.0f;
-                sx[r * CB + vc + k] = in ? to_f<T>(wx.v[k]) : 0.0f;
-                sg[r * CB + vc + k] = in ? to_f<T>(wg.v[k]) * (GATE ? silu(to_f<T>(wz.v[k])) : 1.0f) : 0.0f;
+                vd[k] = in ? ssm_delta(a, to_f<T>(wd.v[k]), vb[k]) : 0.0f;
+                vx[k] = in ? to_f<T>(wx.v[k]) : 0.0f;
+                vg[k] = in ? to_f<T>(wg.v[k]) * (GATE ? silu(to_f<T>(wz.v[k])) : 1.0f) : 0.0f;
             }
+            put_row<V>(sd + r * CB + vc, vd);
+            put_row<V>(sx + r * CB + vc, vx);
+            put_row<V>(sg + r * CB + vc, vg);
         }
         for (int i = tid; i < P * S; i += kSsmThreads) {
             const int r = i / S, s = i % S;
@@ -554,13 +564,14 @@ __global__ void __launch_bounds__(kSsmThreads, 3) k_ssm_bwd(const SsmBwdArgs b)
         for (int r = vr; r < rows; r += RSTEP) {
             if (!vok) break;
             const int64_t row = lo + p + r;
-            float o[V], od[V];
+            float o[V], od[V], vb[V];
             const Vec<T, V> wd = load_vec<T, V>(dt + row * a.lddt);
+            get_row<V>(sg + r * CB + vc, o);
+            get_row<V>(sx + r * CB + vc, od);
+            get_row<V>(sbias + vc, vb);
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                o[k] = sg[r * CB + vc + k];
-                od[k] = sx[r * CB + vc + k];
-                if (a.softplus) od[k] *= sigmoid(to_f<T>(wd.v[k]) + bias[k]);
+                if (a.softplus) od[k] *= sigmoid(to_f<T>(wd.v[k]) + vb[k]);
                 dbias[k] += od[k];
             }
             store_vec<T, V>(static_cast<T*>(b.dx) + row * a.D + cbase + vc, o);
@@ -568,10 +579,11 @@ __global__ void __launch_bounds__(kSsmThreads, 3) k_ssm_bwd(const SsmBwdArgs b)
             if (GATE) {
                 const Vec<T, V> wx = load_vec<T, V>(x + row * a.ldx), wz = load_vec<T, V>(z + row * a.ldz);
                 const Vec<T, V> wg = load_vec<T, V>(dy + row * b.lddy);
+                get_row<V>(sy + r * CB + vc, o);
+                get_row<V>(sD + vc, vb);
 #pragma unroll
                 for (int k = 0; k < V; ++k)
-                    o[k] = to_f<T>(wg.v[k]) * silu_grad(to_f<T>(wz.v[k])) *
-                           __fmaf_rn(Dv[k], to_f<T>(wx.v[k]), sy[r * CB + vc + k]);
+                    o[k] = to_f<T>(wg.v[k]) * silu_grad(to_f<T>(wz.v[k])) * __fmaf_rn(vb[k], to_f<T>(wx.v[k]), o[k]);
                 store_vec<T, V>(static_cast<T*>(b.dz) + row * a.D + cbase + vc, o);
             }
         }

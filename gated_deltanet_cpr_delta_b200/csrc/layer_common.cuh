@@ -129,6 +129,33 @@ __device__ __forceinline__ void pstore(T* p, const typename Lanes<V>::type* x)
     store_vec<T, V>(p, o);
 }
 
+// V floats of shared memory, 16 bytes at a time where V allows
+template <int V>
+__device__ __forceinline__ void put_row(float* p, const float (&x)[V])
+{
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) p[i] = x[i];
+    }
+}
+template <int V>
+__device__ __forceinline__ void get_row(const float* p, float (&x)[V])
+{
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(p + i);
+            x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = p[i];
+    }
+}
+
 // Weights and biases may be fp32 or bf16 whatever the tokens are.
 __device__ __forceinline__ float load_w(const void* w, int bf16, int64_t i)
 {
