@@ -20,6 +20,7 @@ namespace {
 using gdn::Seqs;
 
 constexpr size_t kAlign = 256;
+constexpr int64_t kMaxRows = INT32_MAX - 4096;  // the kernels count rows, and a few beyond the end, in 32 bits
 
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -143,7 +144,7 @@ gdn_status_t conv_check(const void* x, int64_t x_stride, const void* weight, con
                         const int32_t* cu, int32_t num_seqs, int64_t T, int32_t D, int32_t W, gdn_dtype_t in,
                         gdn_dtype_t wt)
 {
-    if (num_seqs < 0 || T < 0 || T > INT32_MAX || D <= 0 || W <= 0) return GDN_ERR_INVALID_ARG;
+    if (num_seqs < 0 || T < 0 || T > kMaxRows || D <= 0 || W <= 0) return GDN_ERR_INVALID_ARG;
     if (!dtype_ok(in) || !dtype_ok(wt)) return GDN_ERR_INVALID_ARG;
     if (W < 2 || W > 4) return GDN_ERR_UNSUPPORTED;
     if (cu == nullptr && num_seqs != 1) return GDN_ERR_INVALID_ARG;
@@ -275,7 +276,7 @@ SsmWorkspace ssm_carve(void* base, int64_t T, int32_t N, int32_t D, int32_t G, i
 gdn_status_t ssm_check(const gdn_ssm_t* s, bool step)
 {
     if (s == nullptr) return GDN_ERR_INVALID_ARG;
-    if (s->num_seqs < 0 || s->total_tokens < 0 || s->total_tokens > INT32_MAX || s->channels <= 0 || s->groups <= 0 ||
+    if (s->num_seqs < 0 || s->total_tokens < 0 || s->total_tokens > kMaxRows || s->channels <= 0 || s->groups <= 0 ||
         s->states <= 0 || s->channels % s->groups != 0)
         return GDN_ERR_INVALID_ARG;
     if (!dtype_ok(s->in_dtype)) return GDN_ERR_INVALID_ARG;
@@ -467,7 +468,10 @@ gdn_status_t gdn_conv_backward(const void* x, int64_t x_stride, const void* weig
     const size_t es = esize(in_dtype);
     const Span sx(x, total_tokens, x_stride, channels, es), sg(dy, total_tokens, dy_stride, channels, es);
     const Span sd(dx, total_tokens, channels, channels, es);
-    if (sd.hits(sx) || sd.hits(sg)) return GDN_ERR_INVALID_ARG;
+    const int64_t tail = (int64_t)num_seqs * (width - 1);
+    if (sd.hits(sx) || sd.hits(sg) ||
+        Span(dstate_in, tail, channels, channels, 4).hits(Span(dstate_out, tail, channels, channels, 4)))
+        return GDN_ERR_INVALID_ARG;
     if (workspace == nullptr ||
         workspace_bytes < gdn_conv_backward_workspace_size(total_tokens, num_seqs, channels, width))
         return GDN_ERR_WORKSPACE;
@@ -534,7 +538,7 @@ gdn_status_t gdn_layer_norm_forward(const void* x, int64_t x_stride, const void*
                                     int64_t rows, int32_t width, gdn_dtype_t in_dtype, gdn_dtype_t w_dtype, void* y,
                                     float* mean, float* rstd, void* stream)
 {
-    if (rows < 0 || rows > INT32_MAX || width <= 0 || !(eps >= 0.0f) || !dtype_ok(in_dtype) || !dtype_ok(w_dtype))
+    if (rows < 0 || rows > kMaxRows || width <= 0 || !(eps >= 0.0f) || !dtype_ok(in_dtype) || !dtype_ok(w_dtype))
         return GDN_ERR_INVALID_ARG;
     if (weight == nullptr || !aligned(weight, esize(w_dtype)) || (bias && !aligned(bias, esize(w_dtype))))
         return GDN_ERR_INVALID_ARG;
@@ -576,7 +580,7 @@ gdn_status_t gdn_layer_norm_backward(const void* x, int64_t x_stride, const void
                                      float* dweight, float* dbias, void* workspace, size_t workspace_bytes,
                                      void* stream)
 {
-    if (rows < 0 || rows > INT32_MAX || width <= 0 || !dtype_ok(in_dtype) || !dtype_ok(w_dtype))
+    if (rows < 0 || rows > kMaxRows || width <= 0 || !dtype_ok(in_dtype) || !dtype_ok(w_dtype))
         return GDN_ERR_INVALID_ARG;
     if (weight == nullptr || !aligned(weight, esize(w_dtype)) || dweight == nullptr || !aligned(dweight, 4) ||
         (dbias && !aligned(dbias, 4)))
@@ -633,7 +637,7 @@ gdn_status_t gdn_layer_norm_backward(const void* x, int64_t x_stride, const void
 
 int64_t gdn_ssm_num_chunk_states(int64_t total_tokens, int32_t num_seqs)
 {
-    if (total_tokens < 0 || total_tokens > INT32_MAX || num_seqs < 0) return -1;
+    if (total_tokens < 0 || total_tokens > kMaxRows || num_seqs < 0) return -1;
     return total_tokens / GDN_SSM_CHUNK + num_seqs;
 }
 
@@ -661,7 +665,10 @@ gdn_status_t gdn_ssm_forward(const gdn_ssm_t* args, const float* state_in, void*
     const int64_t T = s.total_tokens, per = (int64_t)s.channels * s.states;
     const Span sy(y, T, s.channels, s.channels, es), so(state_out, s.num_seqs, per, per, 4);
     if (sy.hits(Span(s.x, T, s.x_stride, s.channels, es)) || sy.hits(Span(s.dt, T, s.dt_stride, s.channels, es)) ||
-        sy.hits(Span(s.z, T, s.z_stride, s.channels, es)) || so.hits(Span(state_in, s.num_seqs, per, per, 4)))
+        sy.hits(Span(s.z, T, s.z_stride, s.channels, es)) ||
+        sy.hits(Span(s.B, T, s.B_stride, (int64_t)s.groups * s.states, es)) ||
+        sy.hits(Span(s.C, T, s.C_stride, (int64_t)s.groups * s.states, es)) ||
+        so.hits(Span(state_in, s.num_seqs, per, per, 4)))
         return GDN_ERR_INVALID_ARG;
     gdn::SsmArgs a = ssm_args(args, 1);  // the launch sets the channel blocks
     a.state_in = state_in; a.y = y; a.state_out = state_out; a.saved = chunk_states;
@@ -699,6 +706,9 @@ gdn_status_t gdn_ssm_backward(const gdn_ssm_t* args, const void* dy, int64_t dy_
     for (const Span& i : in)
         for (const Span& o : out)
             if (i.hits(o)) return GDN_ERR_INVALID_ARG;
+    const int64_t per = (int64_t)s.channels * s.states;
+    if (Span(dstate_in, s.num_seqs, per, per, 4).hits(Span(dstate_out, s.num_seqs, per, per, 4)))
+        return GDN_ERR_INVALID_ARG;
     if (workspace == nullptr ||
         workspace_bytes < gdn_ssm_backward_workspace_size(s.total_tokens, s.num_seqs, s.channels, s.groups, s.states))
         return GDN_ERR_WORKSPACE;

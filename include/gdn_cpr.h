@@ -453,7 +453,7 @@ gdn_status_t gdn_cpr_forward_noalloc(const void* q, const void* k, const void* v
  * They take the conventions at the top of this file, with these differences:
  *  - Token tensors ([T, channels], [T, G, S]) may be views of wider rows, such as the slices
  *    of one projection's output: `*_stride` is the distance between tokens in
- *    elements (at least the row's width).  They need the alignment of one
+ *    elements (at least the row's width, below 2^31).  They need the alignment of one
  *    element only; rows whose width, stride and address are multiples of 16 bytes
  *    are read in 16-byte accesses.  Outputs are dense.  States, parameters in fp32 and
  *    gradients of either are 16-byte aligned.
@@ -466,9 +466,10 @@ gdn_status_t gdn_cpr_forward_noalloc(const void* q, const void* k, const void* v
  *    device, or NULL; never cleared by the library) becomes GDN_ERR_DEVICE_INPUT.
  *  - Outputs must not overlap inputs, except where a call says so.
  *  - Every sum is fp32 and in a fixed order, without atomics: repeated calls
- *    give the same bits.  Inputs that are not finite spread as IEEE arithmetic does,
- *    within the rows (norm) or sequences (convolution, scan) and channels they
- *    belong to, and into the gradients of the parameters.
+ *    give the same bits.  Inputs that are not finite spread within the rows (norm)
+ *    or sequences (convolution, scan) and channels they belong to, and into the
+ *    gradients of the parameters; in the scan an infinity may turn into NaN.
+ *  - total_tokens and rows are below 2^31 - 4096; offsets of elements take 64 bits.
  */
 
 /*

@@ -45,7 +45,7 @@ def conv_backward(lib, **kw):
 @pytest.mark.parametrize("kw,want", [
     (dict(W=5), UNSUPPORTED), (dict(dy=None), BAD), (dict(ldg=1), BAD), (dict(dx=None), BAD), (dict(dw=None), BAD),
     (dict(ds=None), BAD), (dict(do=A8 + 4), BAD), (dict(dx=A2), BAD), (dict(dx=A0), BAD), (dict(ws=None), SCRATCH),
-    (dict(wsb=64), SCRATCH), (dict(ws=A7 + 16), BAD)])
+    (dict(wsb=64), SCRATCH), (dict(ws=A7 + 16), BAD), (dict(do=A6), BAD), (dict(T=2 ** 31 - 1), BAD)])
 def test_conv_backward_refuses(lib, kw, want):
     assert conv_backward(lib, **kw) == want
 
@@ -85,7 +85,7 @@ def test_ssm_forward_refuses(lib, kw, want):
 def test_ssm_forward_refuses_buffers(lib):
     f = lambda si=None, y=A7, so=A8, cs=None: lib.gdn_ssm_forward(ssm_struct(), si, y, so, cs, None, None)  # noqa: E731
     assert f(y=None) == BAD and f(so=None) == BAD and f(so=A8 + 8) == BAD and f(cs=A5 + 4) == BAD
-    assert f(y=A0) == BAD and f(y=A1 + 128) == BAD and f(si=A8) == BAD
+    assert f(y=A0) == BAD and f(y=A1 + 128) == BAD and f(si=A8) == BAD and f(y=A2) == BAD and f(y=A3) == BAD
     assert lib.gdn_ssm_forward(None, None, A7, A8, None, None, None) == BAD
 
 
@@ -106,6 +106,7 @@ def test_ssm_backward_refuses_buffers(lib):
         assert f(**{n: None}) == BAD, n
     assert f(z=True) == BAD                                   # dz is needed with z
     assert f(ld=63) == BAD and f(do=A8 + 8) == BAD and f(dx=base["dy"]) == BAD and f(dB=A2) == BAD
+    assert f(do=base["ds"]) == BAD
     assert f(ws=None) == SCRATCH and f(n=256) == SCRATCH and f(ws=base["ws"] + 16) == BAD
 
 
