@@ -332,21 +332,23 @@ __global__ void __launch_bounds__(512) k_norm_bwd(const NormArgs a)
             mean_next = *pm;
             rstd_next = *pr;
         }
-        Vec<T, V> cx[NV], cg[NV];
+        P xc[NV][L::N], gw[NV][L::N];  // x - mean and dy w
         P s0 = pset<V>(0.0f), s1 = pset<V>(0.0f);
         Ring::wait();
         if (on) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 if (col(i) < a.D) {
-                    cx[i] = ringx.get(slot, i, qx + i * a.tpr * V);
-                    cg[i] = ringg.get(slot, i, qg + i * a.tpr * V);
+                    const Vec<T, V> cx = ringx.get(slot, i, qx + i * a.tpr * V);
+                    const Vec<T, V> cg = ringg.get(slot, i, qg + i * a.tpr * V);
 #pragma unroll
                     for (int k = 0; k < L::N; ++k) {
-                        const P n = padd(pget<T, V>(cx[i], k), minus), d = pget<T, V>(cg[i], k);  // n without rstd
+                        const P n = padd(pget<T, V>(cx, k), minus), d = pget<T, V>(cg, k);
+                        xc[i][k] = n;
                         dw[i][k] = pfma(pmul(d, r2), n, dw[i][k]);
                         db[i][k] = padd(db[i][k], d);
                         const P g = pmul(d, pget<WT, V>(w[i], k));
+                        gw[i][k] = g;
                         s0 = padd(s0, g);
                         s1 = pfma(g, n, s1);
                     }
@@ -362,15 +364,12 @@ __global__ void __launch_bounds__(512) k_norm_bwd(const NormArgs a)
             const P c0 = pset<V>(-rstd * s[0] * inv), c1 = pset<V>(-rstd * rstd * rstd * s[1] * inv);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                keep_packed(w[i]);  // widened again, not kept in twice the registers
-                keep_packed(cx[i]);
-                keep_packed(cg[i]);
+                keep_packed(w[i]);  // not kept widened in twice the registers
                 if (col(i) < a.D) {
                     P o[L::N];
 #pragma unroll
                     for (int k = 0; k < L::N; ++k) {
-                        const P n = padd(pget<T, V>(cx[i], k), minus);
-                        o[k] = pfma(pget<T, V>(cg[i], k), pmul(pget<WT, V>(w[i], k), r2), pfma(n, c1, c0));
+                        o[k] = pfma(gw[i][k], r2, pfma(xc[i][k], c1, c0));
                     }
                     pstore<T, V>(pd + i * a.tpr * V, o);
                 }
