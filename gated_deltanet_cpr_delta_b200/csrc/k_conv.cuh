@@ -39,27 +39,56 @@ struct ConvArgs {
     int32_t* status;
 };
 
+// The taps and the window hold pairs of channels (or one channel, V = 1).
 template <typename T, int W, int V>
 struct ConvTaps {
-    float w[W][V], b[V];
+    using P = typename Lanes<V>::type;
+    static constexpr int N = Lanes<V>::N;
+    P w[W][N], b[N];
     __device__ __forceinline__ void load(const ConvArgs& a, int64_t c)
     {
-float raw[V * W];
+        float raw[V * W], rb[V];
         load_ws<V * W>(a.w, a.w_bf16, c * W, raw);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            b[v] = 0.0f;
+        for (int v = 0; v < V; ++v) rb[v] = 0.0f;
+        if (a.bias != nullptr) load_ws<V>(a.bias, a.w_bf16, c, rb);
 #pragma unroll
-            for (int i = 0; i < W; ++i) w[i][v] = raw[v * W + i];
+        for (int n = 0; n < N; ++n) {
+            if constexpr (V == 1) {
+                b[n] = rb[0];
+#pragma unroll
+                for (int i = 0; i < W; ++i) w[i][n] = raw[i];
+            } else {
+                b[n] = pk2(rb[2 * n], rb[2 * n + 1]);
+#pragma unroll
+                for (int i = 0; i < W; ++i) w[i][n] = pk2(raw[2 * n * W + i], raw[(2 * n + 1) * W + i]);
+            }
         }
-        if (a.bias != nullptr) load_ws<V>(a.bias, a.w_bf16, c, b);
+    }
+    __device__ __forceinline__ P pre(const P (&win)[W][N], int n) const
+    {
+        P p = b[n];
+#pragma unroll
+        for (int i = 0; i < W; ++i) p = pfma(w[i][n], win[i][n], p);
+        return p;
     }
 };
+
+// f on every element of a pair
+template <typename F>
+__device__ __forceinline__ f2x peach(f2x a, F f)
+{
+    float x, y;
+    up2(a, x, y);
+    return pk2(f(x), f(y));
+}
+template <typename F>
+__device__ __forceinline__ float peach(float a, F f) { return f(a); }
 
 // The window before row t of sequence n: win[i] = x[t - (W-1) + i] for i < W-1.
 template <typename T, int W, int V>
 __device__ __forceinline__ void conv_window(const ConvArgs& a, int n, int64_t lo, int64_t t, int64_t c,
-                                            float (&win)[W][V])
+                                            typename Lanes<V>::type (&win)[W][Lanes<V>::N])
 {
     const T* x = static_cast<const T*>(a.x);
     const T* st = static_cast<const T*>(a.state_in);
@@ -72,7 +101,7 @@ __device__ __forceinline__ void conv_window(const ConvArgs& a, int n, int64_t lo
         else if (st != nullptr) v = load_vec<T, V>(st + ((int64_t)n * (W - 1) + (W - 1) + (r - lo)) * a.D + c);
         else have = false;
 #pragma unroll
-        for (int k = 0; k < V; ++k) win[i][k] = have ? to_f<T>(v.v[k]) : 0.0f;
+        for (int k = 0; k < Lanes<V>::N; ++k) win[i][k] = have ? pget<T, V>(v, k) : pset<V>(0.0f);
     }
 }
 
@@ -132,21 +161,21 @@ __global__ void __launch_bounds__(128, 5) k_conv_fwd(const ConvArgs a)
     const T* x = static_cast<const T*>(a.x) + c + t * ldx;  // row t
     T* y = static_cast<T*>(a.y) + c + t * ldy;
     int hi = (int)a.s.hi(n);
-    float win[W][V];
+    using P = typename Lanes<V>::type;
+    constexpr int N = Lanes<V>::N;
+    P win[W][N];
     conv_window<T, W, V>(a, n, a.s.lo(n), t, c, win);
     auto row = [&](const Vec<T, V>& r, T* out, bool store) {
-        float o[V];
+        P o[N];
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            win[W - 1][k] = to_f<T>(r.v[k]);
-            float p = taps.b[k];
-#pragma unroll
-            for (int i = 0; i < W; ++i) p = __fmaf_rn(taps.w[i][k], win[i][k], p);
-            o[k] = a.silu ? silu(p) : p;
+        for (int k = 0; k < N; ++k) {
+            win[W - 1][k] = pget<T, V>(r, k);
+            o[k] = taps.pre(win, k);
+            if (a.silu) o[k] = pmul(o[k], peach(o[k], sigmoid));
 #pragma unroll
             for (int i = 0; i < W - 1; ++i) win[i][k] = win[i + 1][k];
         }
-        if (store) store_vec<T, V>(out, o);
+        if (store) pstore<T, V>(out, o);
     };
     Vec<T, V> next[U];
 #pragma unroll
@@ -190,8 +219,11 @@ __global__ void __launch_bounds__(128, 5) k_conv_fwd(const ConvArgs a)
 // the start.
 template <typename T, int W, int V>
 __device__ __forceinline__ void conv_bwd_run(const ConvArgs& a, int64_t t0, int64_t t1, int only_seq, int64_t c,
-                                             const ConvTaps<T, W, V>& taps, float (&dw)[W][V], float (&db)[V])
+                                             const ConvTaps<T, W, V>& taps, typename Lanes<V>::type (&dw)[W][Lanes<V>::N],
+                                             typename Lanes<V>::type (&db)[Lanes<V>::N])
 {
+    using P = typename Lanes<V>::type;
+    constexpr int N = Lanes<V>::N;
     const T* x = static_cast<const T*>(a.x);
     const T* dy = static_cast<const T*>(a.dy);
     T* dx = static_cast<T*>(a.dx);
@@ -206,46 +238,39 @@ __device__ __forceinline__ void conv_bwd_run(const ConvArgs& a, int64_t t0, int6
         const int64_t lo = a.s.lo(n), hi = a.s.hi(n);
         // rows this pass reads, and the last row it may add to a row that it owns
         const int64_t stop = only_seq >= 0 ? min(hi, lo + (W - 1)) : min(hi, t1 + (W - 1));
-        float win[W][V], acc[W][V];
+        P win[W][N], acc[W][N];
         conv_window<T, W, V>(a, n, lo, t, c, win);
 #pragma unroll
         for (int i = 0; i < W; ++i)
 #pragma unroll
-            for (int k = 0; k < V; ++k) acc[i][k] = 0.0f;
-        auto emit = [&](int64_t r, const float (&v)[V]) {
+            for (int k = 0; k < N; ++k) acc[i][k] = pset<V>(0.0f);
+        auto emit = [&](int64_t r, const P (&v)[N]) {
             if (only_seq >= 0) {
-                if (r < lo) {
-                    float* p = a.dstate_in + ((int64_t)n * (W - 1) + (W - 1) + (r - lo)) * a.D + c;
-#pragma unroll
-                    for (int k = 0; k < V; ++k) p[k] = v[k];
-                }
+                if (r < lo) pstore<float, V>(a.dstate_in + ((int64_t)n * (W - 1) + (W - 1) + (r - lo)) * a.D + c, v);
             } else if (r >= lo && r >= t0 && r < t1) {
-                store_vec<T, V>(dx + r * a.D + c, v);
+                pstore<T, V>(dx + r * a.D + c, v);
             }
         };
         // One row.  `inner`: the row and the finished one are the run's own.
         auto row = [&](const Vec<T, V>& rx, const Vec<T, V>& rg, int64_t at, T* out, bool inner) {
             const bool own = inner || at < t1;
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-                win[W - 1][k] = to_f<T>(rx.v[k]);
-                float p = taps.b[k];
-#pragma unroll
-                for (int i = 0; i < W; ++i) p = __fmaf_rn(taps.w[i][k], win[i][k], p);
-                float g = to_f<T>(rg.v[k]);
-                if (a.silu) g *= silu_grad(p);
-                const float go = own ? g : 0.0f;
-                db[k] += go;
+            for (int k = 0; k < N; ++k) {
+                win[W - 1][k] = pget<T, V>(rx, k);
+                P g = pget<T, V>(rg, k);
+                if (a.silu) g = pmul(g, peach(taps.pre(win, k), silu_grad));
+                const P go = own ? g : pset<V>(0.0f);
+                db[k] = padd(db[k], go);
 #pragma unroll
                 for (int i = 0; i < W; ++i) {
-                    acc[i][k] = i < W - 1 ? __fmaf_rn(taps.w[i][k], g, acc[i][k]) : taps.w[i][k] * g;
-                    dw[i][k] = __fmaf_rn(go, win[i][k], dw[i][k]);
+                    acc[i][k] = i < W - 1 ? pfma(taps.w[i][k], g, acc[i][k]) : pmul(taps.w[i][k], g);
+                    dw[i][k] = pfma(go, win[i][k], dw[i][k]);
                 }
             }
-            if (inner) store_vec<T, V>(out, acc[0]);
+            if (inner) pstore<T, V>(out, acc[0]);
             else emit(at - (W - 1), acc[0]);
 #pragma unroll
-            for (int k = 0; k < V; ++k)
+            for (int k = 0; k < N; ++k)
 #pragma unroll
                 for (int i = 0; i < W - 1; ++i) {
                     win[i][k] = win[i + 1][k];
@@ -295,9 +320,10 @@ __device__ __forceinline__ void conv_bwd_run(const ConvArgs& a, int64_t t0, int6
 #pragma unroll
             for (int i = 0; i < W - 1; ++i) {
                 if (a.dstate_out != nullptr) {
-                    const float* p = a.dstate_out + ((int64_t)n * (W - 1) + i) * a.D + c;
+                    const Vec<float, V> v =
+                        load_vec<float, V>(a.dstate_out + ((int64_t)n * (W - 1) + i) * a.D + c);
 #pragma unroll
-                    for (int k = 0; k < V; ++k) acc[i][k] += p[k];
+                    for (int k = 0; k < N; ++k) acc[i][k] = padd(acc[i][k], pget<float, V>(v, k));
                 }
                 emit(hi - (W - 1) + i, acc[i]);
             }
@@ -322,12 +348,14 @@ __global__ void __launch_bounds__(128, 4) k_conv_bwd(const ConvArgs a)
     const int cb = (int)(blockIdx.x - tile * a.ncb);
     const int tx = threadIdx.x % a.cx, ty = threadIdx.x / a.cx, ny = 128 / a.cx;
     const int64_t c = ((int64_t)cb * a.cx + tx) * V;
-    float dw[W][V], db[V];
+    using P = typename Lanes<V>::type;
+    constexpr int N = Lanes<V>::N;
+    P dw[W][N], db[N];
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-        db[k] = 0.0f;
+    for (int k = 0; k < N; ++k) {
+        db[k] = pset<V>(0.0f);
 #pragma unroll
-        for (int i = 0; i < W; ++i) dw[i][k] = 0.0f;
+        for (int i = 0; i < W; ++i) dw[i][k] = pset<V>(0.0f);
     }
     if (c < a.D) {
         ConvTaps<T, W, V> taps;
@@ -343,11 +371,19 @@ __global__ void __launch_bounds__(128, 4) k_conv_bwd(const ConvArgs a)
     }
     if (tile >= a.ntiles) return;
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
+    for (int i = 0; i <= W; ++i)
 #pragma unroll
-        for (int i = 0; i < W; ++i) sh[(i * V + k) * 128 + threadIdx.x] = dw[i][k];
-        sh[(W * V + k) * 128 + threadIdx.x] = db[k];
-    }
+        for (int k = 0; k < N; ++k) {
+            const P v = i < W ? dw[i < W ? i : 0][k] : db[k];
+            if constexpr (V == 1) {
+                sh[i * 128 + threadIdx.x] = v;
+            } else {
+                float x, y;
+                up2(v, x, y);
+                sh[(i * V + 2 * k) * 128 + threadIdx.x] = x;
+                sh[(i * V + 2 * k + 1) * 128 + threadIdx.x] = y;
+            }
+        }
     __syncthreads();
     if (ty == 0 && c < a.D) {
 #pragma unroll

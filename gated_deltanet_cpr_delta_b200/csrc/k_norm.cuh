@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(norm_threads(V)) k_norm_fwd(const NormArgs a)
             if (in) r = ring.get(slot, i, cx + i * a.tpr * V);
 #pragma unroll
             for (int k = 0; k < L::N; ++k) {
-                v[i][k] = in ? pget<T, V>(r, k) : pset<V>(0.0f);
+                v[i][k] = in ? pbits<T, V>(r, k) : pset<V>(0.0f);
                 acc = padd(acc, v[i][k]);
             }
         }
@@ -227,8 +227,8 @@ __global__ void __launch_bounds__(norm_threads(V)) k_norm_fwd(const NormArgs a)
 #pragma unroll
                     for (int k = 0; k < L::N; ++k) {
                         o[k] = pmul(v[i][k], r2);
-                        o[k] = a.b != nullptr ? pfma(o[k], pget<WT, V>(w[i], k), pget<WT, V>(b[i], k))
-                                              : pmul(o[k], pget<WT, V>(w[i], k));
+                        o[k] = a.b != nullptr ? pfma(o[k], pbits<WT, V>(w[i], k), pbits<WT, V>(b[i], k))
+                                              : pmul(o[k], pbits<WT, V>(w[i], k));
                     }
                     pstore<T, V>(py + i * a.tpr * V, o);
                 }
@@ -343,11 +343,11 @@ __global__ void __launch_bounds__(512) k_norm_bwd(const NormArgs a)
                     const Vec<T, V> cg = ringg.get(slot, i, qg + i * a.tpr * V);
 #pragma unroll
                     for (int k = 0; k < L::N; ++k) {
-                        const P n = padd(pget<T, V>(cx, k), minus), d = pget<T, V>(cg, k);
+                        const P n = padd(pbits<T, V>(cx, k), minus), d = pbits<T, V>(cg, k);
                         xc[i][k] = n;
                         dw[i][k] = pfma(pmul(d, r2), n, dw[i][k]);
                         db[i][k] = padd(db[i][k], d);
-                        const P g = pmul(d, pget<WT, V>(w[i], k));
+                        const P g = pmul(d, pbits<WT, V>(w[i], k));
                         gw[i][k] = g;
                         s0 = padd(s0, g);
                         s1 = pfma(g, n, s1);

@@ -110,11 +110,21 @@ __device__ __forceinline__ typename Lanes<V>::type pget(const Vec<T, V>& r, int 
 {
     if constexpr (V == 1) {
         return to_f<T>(r.v[0]);
-    } else if constexpr (sizeof(T) == 2) {
+    } else {
+        return pk2(to_f<T>(r.v[2 * i]), to_f<T>(r.v[2 * i + 1]));
+    }
+}
+// The same by a shift and a mask of the packed word.  Layer norm, which holds rows packed
+// and widens them where they are used, is a fifth faster with it (59 against 75 us), the
+// convolution, which widens what has just arrived, a fifth slower (96 against 77 us).
+template <typename T, int V>
+__device__ __forceinline__ typename Lanes<V>::type pbits(const Vec<T, V>& r, int i)
+{
+    if constexpr (V > 1 && sizeof(T) == 2) {
         const uint32_t u = reinterpret_cast<const uint32_t*>(&r)[i];
         return pk2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
     } else {
-        return pk2(to_f<T>(r.v[2 * i]), to_f<T>(r.v[2 * i + 1]));
+        return pget<T, V>(r, i);
     }
 }
 template <typename T, int V>
