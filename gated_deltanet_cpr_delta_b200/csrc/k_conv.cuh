@@ -105,6 +105,36 @@ __device__ __forceinline__ void conv_window(const ConvArgs& a, int n, int64_t lo
     }
 }
 
+// A thread's own rows ahead, in a ring in shared memory that cp.async fills (4, 8 or 16
+// bytes a row; 2-byte rows are loaded when they are needed).  In registers the rows ahead
+// cost the occupancy that they were to spare: the gradients held 125 registers and 4
+// blocks per SM with 8 rows of 2 channels ahead.
+template <typename T, int V, int DEP>
+struct ConvRing {
+    static constexpr int B = V * sizeof(T);
+    static constexpr bool ON = B >= 4;
+    static constexpr size_t BYTES = ON ? (size_t)DEP * 128 * B : 0;  // per tensor
+    unsigned char* base;
+    __device__ __forceinline__ unsigned char* at(int slot) const { return base + (slot * 128 + threadIdx.x) * B; }
+    __device__ __forceinline__ void copy(int slot, const T* src) const
+    {
+        if constexpr (ON) {
+            const unsigned to = (unsigned)__cvta_generic_to_shared(at(slot));
+            if constexpr (B == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src) : "memory");
+            else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(src), "n"(B) : "memory");
+        }
+    }
+    __device__ __forceinline__ Vec<T, V> get(int slot, const T* src) const
+    {
+        if constexpr (ON) return *reinterpret_cast<const Vec<T, V>*>(at(slot));
+        else return load_vec<T, V>(src);
+    }
+    __device__ static void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    __device__ static void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(DEP - 1) : "memory"); }
+};
+
+constexpr int kConvAhead = 8;  // rows ahead
+
 // state_out of one sequence: its last W-1 inputs, the old state's where it is shorter.
 template <typename T, int W, int V>
 __device__ __forceinline__ void conv_tail(const ConvArgs& a, int n, int64_t c)
@@ -127,13 +157,13 @@ __device__ __forceinline__ void conv_tail(const ConvArgs& a, int n, int64_t c)
     }
 }
 
-// U rows are loaded together and the next U are on their way while they are
-// worked on.  Where these lie in one sequence (almost everywhere) there is no test
-// per row.
+// Where kConvAhead rows lie in one sequence (almost everywhere) there is no test per row.
 template <typename T, int W, int V>
-__global__ void __launch_bounds__(128, 5) k_conv_fwd(const ConvArgs a)
+__global__ void __launch_bounds__(128, 7) k_conv_fwd(const ConvArgs a)
 {
-    constexpr int U = 6;
+    constexpr int U = kConvAhead;
+    extern __shared__ __align__(16) unsigned char conv_smem[];
+    const ConvRing<T, V, U> ring{conv_smem};
     if (blockIdx.x == 0) check_seqs(a.s, a.status);
     const int64_t tile = blockIdx.x / a.ncb;
     const int cb = (int)(blockIdx.x - tile * a.ncb);
@@ -177,21 +207,24 @@ __global__ void __launch_bounds__(128, 5) k_conv_fwd(const ConvArgs a)
         }
         if (store) pstore<T, V>(out, o);
     };
-    Vec<T, V> next[U];
+    const T* px = x;  // the row to copy next
+    auto fetch = [&](int slot, bool in) {
+        if (in) ring.copy(slot, px);
+        px += ldx;
+        ring.commit();
+    };
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (t + u < end) next[u] = load_vec<T, V>(x + u * ldx);
-    for (; t < end; t += U, x += U * ldx, y += U * ldy) {
-        const T* ahead = x + U * ldx;
-        if (t + 2 * U <= min(hi, end)) {  // this group and the next are whole and of one sequence
-            Vec<T, V> raw[U];
+    for (int u = 0; u < U; ++u) fetch(u, t + u < end);
+    for (; t < end; t += U) {
+        if (t + U <= min(hi, end)) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                raw[u] = next[u];
-                next[u] = load_vec<T, V>(ahead + u * ldx);
+                ring.wait();
+                row(ring.get(u, x), y, true);
+                fetch(u, t + U + u < end);  // behind the store that used the slot's last row
+                x += ldx;
+                y += ldy;
             }
-#pragma unroll
-            for (int u = 0; u < U; ++u) row(raw[u], y + u * ldy, true);
         } else {
 #pragma unroll 1
             for (int u = 0; u < U && t + u < end; ++u) {
@@ -200,12 +233,12 @@ __global__ void __launch_bounds__(128, 5) k_conv_fwd(const ConvArgs a)
                     hi = (int)a.s.hi(n);
                     conv_window<T, W, V>(a, n, a.s.lo(n), t + u, c, win);
                 }
-                // rows behind the last sequence stay
-                row(load_vec<T, V>(x + u * ldx), y + u * ldy, t + u < hi);
+                ring.wait();
+                row(ring.get(u, x), y, t + u < hi);  // rows behind the last sequence stay
+                fetch(u, t + U + u < end);
+                x += ldx;
+                y += ldy;
             }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (t + U + u < end) next[u] = load_vec<T, V>(ahead + u * ldx);
         }
     }
 }
@@ -220,8 +253,9 @@ __global__ void __launch_bounds__(128, 5) k_conv_fwd(const ConvArgs a)
 template <typename T, int W, int V>
 __device__ __forceinline__ void conv_bwd_run(const ConvArgs& a, int64_t t0, int64_t t1, int only_seq, int64_t c,
                                              const ConvTaps<T, W, V>& taps, typename Lanes<V>::type (&dw)[W][Lanes<V>::N],
-                                             typename Lanes<V>::type (&db)[Lanes<V>::N])
+                                             typename Lanes<V>::type (&db)[Lanes<V>::N], unsigned char* smem)
 {
+    const ConvRing<T, V, kConvAhead> ringx{smem}, ringg{smem + ConvRing<T, V, kConvAhead>::BYTES};
     using P = typename Lanes<V>::type;
     constexpr int N = Lanes<V>::N;
     const T* x = static_cast<const T*>(a.x);
@@ -277,43 +311,39 @@ __device__ __forceinline__ void conv_bwd_run(const ConvArgs& a, int64_t t0, int6
                     acc[i][k] = acc[i + 1][k];
                 }
         };
-        // U rows are loaded together; the next U are on their way meanwhile
-        constexpr int U = 16 / sizeof(T);
+        constexpr int U = kConvAhead;
         const int64_t ldx = a.ldx, ldg = a.lddy;
         const T* px = x + t * ldx + c;  // row t
         const T* pg = dy + t * ldg + c;
         T* pd = dx + (t - (W - 1)) * (int64_t)a.D + c;  // the row finished at t
-        const int64_t first = max(lo, t0) + (W - 1), last = only_seq >= 0 ? first : min(stop - U, t1);
-        Vec<T, V> nx[U], ng[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (t + u < stop) {
-                nx[u] = load_vec<T, V>(px + u * ldx);
-                ng[u] = load_vec<T, V>(pg + u * ldg);
+        const int64_t first = max(lo, t0) + (W - 1), last = only_seq >= 0 ? first : min(stop, t1);
+        const T *cx = px, *cg = pg;  // the rows to copy next
+        auto fetch = [&](int slot, bool in) {
+            if (in) {
+                ringx.copy(slot, cx);
+                ringg.copy(slot, cg);
             }
-        for (; t < stop; t += U, px += U * ldx, pg += U * ldg, pd += U * (int64_t)a.D) {
-            const T *ax = px + U * ldx, *ag = pg + U * ldg;
+            cx += ldx;
+            cg += ldg;
+            ringx.commit();
+        };
+#pragma unroll
+        for (int u = 0; u < U; ++u) fetch(u, t + u < stop);
+        auto step = [&](int u, bool inner) {
+            ringx.wait();
+            row(ringx.get(u, px), ringg.get(u, pg), t + u, pd, inner);
+            fetch(u, t + U + u < stop);  // behind the use of the slots' last rows
+            px += ldx;
+            pg += ldg;
+            pd += a.D;
+        };
+        for (; t < stop; t += U) {
             if (t >= first && t + U <= last) {
-                Vec<T, V> rx[U], rg[U];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    rx[u] = nx[u];
-                    rg[u] = ng[u];
-                    nx[u] = load_vec<T, V>(ax + u * ldx);
-                    ng[u] = load_vec<T, V>(ag + u * ldg);
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u) row(rx[u], rg[u], t + u, pd + u * (int64_t)a.D, true);
+                for (int u = 0; u < U; ++u) step(u, true);
             } else {
 #pragma unroll 1
-                for (int u = 0; u < U && t + u < stop; ++u)
-                    row(load_vec<T, V>(px + u * ldx), load_vec<T, V>(pg + u * ldg), t + u, nullptr, false);
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (t + U + u < stop) {
-                        nx[u] = load_vec<T, V>(ax + u * ldx);
-                        ng[u] = load_vec<T, V>(ag + u * ldg);
-                    }
+                for (int u = 0; u < U && t + u < stop; ++u) step(u, false);
             }
         }
         if (stop == hi) {  // the sequence's end: the open rows hi - (W-1) + i
@@ -342,7 +372,9 @@ __device__ __forceinline__ void conv_bwd_run(const ConvArgs& a, int64_t t0, int6
 template <typename T, int W, int V>
 __global__ void __launch_bounds__(128, 4) k_conv_bwd(const ConvArgs a)
 {
-    extern __shared__ float sh[];  // [(W + 1) * V][128]: joins the runs of a block
+    extern __shared__ __align__(16) unsigned char conv_smem[];
+    unsigned char* smem = conv_smem;                  // two rings; then
+    float* sh = reinterpret_cast<float*>(conv_smem);  // [(W + 1) * V][128]: joins the runs of a block
     if (blockIdx.x == 0) check_seqs(a.s, a.status);
     const int64_t tile = blockIdx.x / a.ncb;
     const int cb = (int)(blockIdx.x - tile * a.ncb);
@@ -363,13 +395,14 @@ __global__ void __launch_bounds__(128, 4) k_conv_bwd(const ConvArgs a)
         if (tile >= a.ntiles) {
             const int64_t n = (tile - a.ntiles) * ny + ty;
             // no rows are owned: only the state's gradient is written
-            if (n < a.s.N) conv_bwd_run<T, W, V>(a, a.s.lo((int)n), a.s.lo((int)n), (int)n, c, taps, dw, db);
+            if (n < a.s.N) conv_bwd_run<T, W, V>(a, a.s.lo((int)n), a.s.lo((int)n), (int)n, c, taps, dw, db, smem);
         } else {
             const int64_t t0 = (tile * ny + ty) * a.run, t1 = min(t0 + a.run, a.s.T);
-            if (t0 < t1) conv_bwd_run<T, W, V>(a, t0, t1, -1, c, taps, dw, db);
+            if (t0 < t1) conv_bwd_run<T, W, V>(a, t0, t1, -1, c, taps, dw, db, smem);
         }
     }
     if (tile >= a.ntiles) return;
+    __syncthreads();  // every thread is done with its rings
 #pragma unroll
     for (int i = 0; i <= W; ++i)
 #pragma unroll

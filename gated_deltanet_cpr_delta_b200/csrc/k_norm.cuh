@@ -196,10 +196,10 @@ __global__ void __launch_bounds__(norm_threads(V)) k_norm_fwd(const NormArgs a)
                 acc = padd(acc, v[i][k]);
             }
         }
-        fetch(left - DEP * step, slot);
-        slot = slot + 1 == DEP ? 0 : slot + 1;
         float s[1] = {psum(acc)};
         row_sum<1>(s, a.tpr, red);
+        fetch(left - DEP * step, slot);  // behind the sum that used the slot's last row
+        slot = slot + 1 == DEP ? 0 : slot + 1;
         const float mean = s[0] * inv;
         acc = pset<V>(0.0f);
         const P minus = pset<V>(-mean);
@@ -355,10 +355,10 @@ __global__ void __launch_bounds__(512) k_norm_bwd(const NormArgs a)
                 }
             }
         }
-        fetch(left - DEP * step, slot);
-        slot = slot + 1 == DEP ? 0 : slot + 1;
         float s[2] = {psum(s0), psum(s1)};
         row_sum<2>(s, a.tpr, red);
+        fetch(left - DEP * step, slot);  // behind the sums that used the slots' last rows
+        slot = slot + 1 == DEP ? 0 : slot + 1;
         if (on) {
             // dx = rstd g + c1 (x - mean) + c0
             const P c0 = pset<V>(-rstd * s[0] * inv), c1 = pset<V>(-rstd * rstd * rstd * s[1] * inv);

@@ -114,15 +114,16 @@ int64_t conv_tiles_max(int64_t T) { return ceil_div(T, 8); }
 template <typename T, int V>
 void launch_conv_fwd(const gdn::ConvArgs& a, int W, unsigned blocks, cudaStream_t st)
 {
-    if (W == 2) gdn::k_conv_fwd<T, 2, V><<<blocks, 128, 0, st>>>(a);
-    else if (W == 3) gdn::k_conv_fwd<T, 3, V><<<blocks, 128, 0, st>>>(a);
-    else gdn::k_conv_fwd<T, 4, V><<<blocks, 128, 0, st>>>(a);
+    constexpr size_t sm = gdn::ConvRing<T, V, gdn::kConvAhead>::BYTES;
+    if (W == 2) gdn::k_conv_fwd<T, 2, V><<<blocks, 128, sm, st>>>(a);
+    else if (W == 3) gdn::k_conv_fwd<T, 3, V><<<blocks, 128, sm, st>>>(a);
+    else gdn::k_conv_fwd<T, 4, V><<<blocks, 128, sm, st>>>(a);
 }
 
 template <typename T, int V>
 void launch_conv_bwd(const gdn::ConvArgs& a, int W, unsigned blocks, cudaStream_t st)
 {
-    const size_t sm = sizeof(float) * (W + 1) * V * 128;
+    const size_t sm = std::max(2 * gdn::ConvRing<T, V, gdn::kConvAhead>::BYTES, sizeof(float) * (W + 1) * V * 128);
     if (W == 2) gdn::k_conv_bwd<T, 2, V><<<blocks, 128, sm, st>>>(a);
     else if (W == 3) gdn::k_conv_bwd<T, 3, V><<<blocks, 128, sm, st>>>(a);
     else gdn::k_conv_bwd<T, 4, V><<<blocks, 128, sm, st>>>(a);
@@ -432,7 +433,7 @@ gdn_status_t gdn_conv_forward(const void* x, int64_t x_stride, const void* weigh
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool v16 = wide(x, x_stride, channels, in_dtype) && wide(y, channels, channels, in_dtype);
     unsigned blocks = 0;
-    if (!conv_grid(a, v16 ? 4 : 1, 5, &blocks)) return GDN_ERR_INVALID_ARG;
+    if (!conv_grid(a, v16 ? 4 : 1, 7, &blocks)) return GDN_ERR_INVALID_ARG;
     if (in_dtype == GDN_BF16) {
         if (v16) launch_conv_fwd<__nv_bfloat16, 4>(a, width, blocks, st);
         else launch_conv_fwd<__nv_bfloat16, 1>(a, width, blocks, st);
@@ -487,13 +488,13 @@ gdn_status_t gdn_conv_backward(const void* x, int64_t x_stride, const void* weig
     const bool v4 = wide(x, x_stride, channels, in_dtype) && wide(dy, dy_stride, channels, in_dtype) &&
                     wide(dx, channels, channels, in_dtype);
     unsigned blocks = 0;
-    if (!conv_grid(a, v4 ? 2 : 1, 4, &blocks)) return GDN_ERR_INVALID_ARG;
+    if (!conv_grid(a, v4 ? 4 : 1, 4, &blocks)) return GDN_ERR_INVALID_ARG;
     if (blocks > 0) {
         if (in_dtype == GDN_BF16) {
-            if (v4) launch_conv_bwd<__nv_bfloat16, 2>(a, width, blocks, st);
+            if (v4) launch_conv_bwd<__nv_bfloat16, 4>(a, width, blocks, st);
             else launch_conv_bwd<__nv_bfloat16, 1>(a, width, blocks, st);
         } else {
-            if (v4) launch_conv_bwd<float, 2>(a, width, blocks, st);
+            if (v4) launch_conv_bwd<float, 4>(a, width, blocks, st);
             else launch_conv_bwd<float, 1>(a, width, blocks, st);
         }
     }
