@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(SsmFwdCfg<T, S, SEG>::THREADS, SEG == 32 ? 2 :
         stage(0, 0);
         stage_bc(0);
     }
+    const f2x shift = pk2(kEx2Mean, kEx2Mean);
     const f2x later = seg == 0 ? pk2(0.0f, 0.0f) : pk2(1.0f, 1.0f);
     int buf = 0;
     for (int64_t p = 0; p < L; p += TT, buf ^= 1) {
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(SsmFwdCfg<T, S, SEG>::THREADS, SEG == 32 ? 2 :
                 for (int q = 0; q < 2; ++q) {
                     const int k = 2 * k2 + q;
                     float e0, e1;
-                    up2(fmul2(dl[k], A2), e0, e1);
+                    up2(ffma2(dl[k], A2, shift), e0, e1);
                     am[k] = pk2(ex2(e0), ex2(e1));
                     bm[k] = fmul2(u[k], q ? b2.y : b2.x);
                     if (k == 0) {
@@ -318,10 +319,10 @@ __global__ void __launch_bounds__(256) k_ssm_step(const SsmArgs a)
     }
     const float u = d * x, d2 = d * kLog2e;
     float4 o;
-    o.x = __fmaf_rn(ex2(d2 * A.x), h.x, u * B[0]);
-    o.y = __fmaf_rn(ex2(d2 * A.y), h.y, u * B[1]);
-    o.z = __fmaf_rn(ex2(d2 * A.z), h.z, u * B[2]);
-    o.w = __fmaf_rn(ex2(d2 * A.w), h.w, u * B[3]);
+    o.x = __fmaf_rn(ex2(__fmaf_rn(d2, A.x, kEx2Mean)), h.x, u * B[0]);
+    o.y = __fmaf_rn(ex2(__fmaf_rn(d2, A.y, kEx2Mean)), h.y, u * B[1]);
+    o.z = __fmaf_rn(ex2(__fmaf_rn(d2, A.z, kEx2Mean)), h.z, u * B[2]);
+    o.w = __fmaf_rn(ex2(__fmaf_rn(d2, A.w, kEx2Mean)), h.w, u * B[3]);
     float s = o.x * C[0];
     s = __fmaf_rn(o.y, C[1], s);
     s = __fmaf_rn(o.z, C[2], s);

@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(kSsmThreads, 4) k_ssm_rev(const SsmBwdArgs b)
             if (p + r < p1) rc[i] = C[(lo + p + r) * a.ldC + s];
         }
     };
+    const f2x shift = pk2(kEx2Mean, kEx2Mean);
     const int64_t ntile = (p1 - p0 + TT - 1) / TT;
     fetch(p0 + (ntile - 1) * TT);
     for (int64_t it = ntile - 1; it >= 0; --it) {
@@ -192,8 +193,8 @@ __global__ void __launch_bounds__(kSsmThreads, 4) k_ssm_rev(const SsmBwdArgs b)
             for (int i = 0; i < 4; ++i) {
                 const f2x d2 = pk2(d[i], d[i]), u2 = pk2(u[i], u[i]);
                 float e0, e1, e2, e3;
-                up2(fmul2(d2, A2[i][0]), e0, e1);
-                up2(fmul2(d2, A2[i][1]), e2, e3);
+                up2(ffma2(d2, A2[i][0], shift), e0, e1);
+                up2(ffma2(d2, A2[i][1], shift), e2, e3);
                 h[i][0] = fmul2(pk2(ex2(e0), ex2(e1)), ffma2(u2, c4.x, h[i][0]));
                 h[i][1] = fmul2(pk2(ex2(e2), ex2(e3)), ffma2(u2, c4.y, h[i][1]));
                 dsum[i] += d[i];
@@ -360,7 +361,7 @@ __global__ void __launch_bounds__(kSsmThreads, 3) k_ssm_bwd(const SsmBwdArgs b)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 float e0, e1;
-                up2(fmul2(d2, A2[i][k]), e0, e1);
+                up2(ffma2(d2, A2[i][k], pk2(kEx2Mean, kEx2Mean)), e0, e1);
                 o[i][k] = pk2(ex2(e0), ex2(e1));
             }
         }

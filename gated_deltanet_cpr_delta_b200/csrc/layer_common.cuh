@@ -256,9 +256,8 @@ __device__ __forceinline__ void check_seqs(const Seqs& s, int32_t* status)
 }
 
 // 2^x in one instruction.  Measured against the exact value over [-10, -1e-5]:
-// relative error at most 1.5e-7, 3e-8 to 6e-8 rms, and biased by 6e-9 (near 0)
-// to 5e-8, the same size as expf's.  A state that decays slowly multiplies
-// thousands of such factors close to 1, where the bias is the smallest.
+// relative error at most 1.5e-7, 3e-8 to 6e-8 rms, and too small by 6e-9 (near 0), 1.2e-8
+// to 2.6e-8 (from -0.001 to -1) and 5e-8 (below) in the mean.
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
@@ -267,6 +266,12 @@ __device__ __forceinline__ float ex2(float x)
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
+
+// A state that decays slowly multiplies thousands of such factors close to 1, whose mean
+// error then adds up.  The decays take 2^(x + kEx2Mean), which costs nothing as the
+// exponent is a product already: it raises a factor by 1.6e-8, so that the mean error is at most
+// 1e-8 where it matters; x = 0 still gives exactly 1.
+constexpr float kEx2Mean = 2.3e-8f;
 
 // 1 / x in one instruction, off by at most one unit; 0 for x above 2^126
 __device__ __forceinline__ float rcp(float x)
