@@ -343,7 +343,8 @@ __global__ void __launch_bounds__(kSsmThreads, 3) k_ssm_bwd(const SsmBwdArgs b)
         sD[tid] = ok && a.Dp != nullptr ? a.Dp[cbase + tid] : 0.0f;
     }
     __syncthreads();
-    float dbias[V];
+    __shared__ __align__(16) float sdb[kSsmThreads * V];  // each thread's sums of ddt
+    float* dbias = sdb + tid * V;
 #pragma unroll
     for (int k = 0; k < V; ++k) dbias[k] = 0.0f;
     const T* x = static_cast<const T*>(a.x) + cbase + vc;
@@ -565,7 +566,8 @@ __global__ void __launch_bounds__(kSsmThreads, 3) k_ssm_bwd(const SsmBwdArgs b)
         for (int r = vr; r < rows; r += RSTEP) {
             if (!vok) break;
             const int64_t row = lo + p + r;
-            float o[V], od[V], vb[V];
+            float o[V], od[V], vb[V], sum[V];
+            get_row<V>(dbias, sum);
             const Vec<T, V> wd = load_vec<T, V>(dt + row * a.lddt);
             get_row<V>(sg + r * CB + vc, o);
             get_row<V>(sx + r * CB + vc, od);
@@ -573,8 +575,9 @@ __global__ void __launch_bounds__(kSsmThreads, 3) k_ssm_bwd(const SsmBwdArgs b)
 #pragma unroll
             for (int k = 0; k < V; ++k) {
                 if (a.softplus) od[k] *= sigmoid(to_f<T>(wd.v[k]) + vb[k]);
-                dbias[k] += od[k];
+                sum[k] += od[k];
             }
+            put_row<V>(dbias, sum);
             store_vec<T, V>(static_cast<T*>(b.dx) + row * a.D + cbase + vc, o);
             store_vec<T, V>(static_cast<T*>(b.ddt) + row * a.D + cbase + vc, od);
             if (GATE) {
