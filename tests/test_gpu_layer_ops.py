@@ -214,6 +214,20 @@ def test_ssm_long_sequences_are_cut_into_chunks():
         close(name, t, want[name], M[name], K + len(wy))
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("D,S", [(2400, 16), (2401, 16), (2400, 32), (2400, 64)])
+def test_ssm_many_channels(dtype, D, S):
+    # enough channels for the short tiles of the forward
+    lengths = [40, 0, 1, 65, 130, 2, 70]
+    g, h, _, _, cu, cu_h = ssm_case(TYPES[dtype], D, 1, S, lengths)
+    y, last, _ = ssm_run(g, cu)
+    wy, wl, _ = ops.ssm(h, cu_h)
+    My, Ml, _ = ops.ssm(h, cu_h, bound=True)
+    K = 8 * 138 + S + D + 60
+    close("y", y, wy, My, K)
+    close("state_out", last, wl, Ml, K)
+
+
 def test_ssm_zero_and_extreme_steps():
     # steps of exactly 0 (softplus of a very negative input) keep the state; very long ones forget it
     g, h, dy, do, cu, cu_h = ssm_case(torch.float32, 32, 1, 16, [40, 40], bias=False)
@@ -235,7 +249,7 @@ def test_ssm_zero_and_extreme_steps():
 # ------------------------------------------------------------------- layer norm
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("R,D", [(1, 1), (7, 16), (300, 33), (64, 128), (9, 1000), (5, 1003), (3, 4096), (2, 16384),
-                                 (2, 20001), (1025, 64), (700, 2048)])
+                                 (2, 20001), (1025, 64), (700, 2048), (4, 6000), (3, 8200), (2, 3001), (2, 9001)])
 @pytest.mark.parametrize("bias", [True, False])
 def test_layer_norm(dtype, R, D, bias):
     t = TYPES[dtype]
