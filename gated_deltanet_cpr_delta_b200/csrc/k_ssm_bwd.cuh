@@ -245,20 +245,32 @@ __global__ void __launch_bounds__(128) k_ssm_bwd_pass(const SsmBwdArgs b)
         const float4 v = *reinterpret_cast<const float4*>(dstate_out + ((int64_t)n * a.D + c) * S + s);
         e[0] = v.x, e[1] = v.y, e[2] = v.z, e[3] = v.w;
     }
-    for (int64_t k = nch - 1; k >= 0; --k) {
-        const int64_t slot = a.s.first_slot(n, b.Lc) + k;
-        float4* p = reinterpret_cast<float4*>(b.ebuf + (slot * a.D + c) * S + s);
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        float d = 0.0f;
-        if (k > 0) {  // the first chunk's part is made by its own walk
-            v = *p;
-            d = b.dsum[slot * a.D + c];
+    // four chunks' parts are loaded together: the chain alone would wait for each
+    constexpr int U = 4;
+    float4* base = reinterpret_cast<float4*>(b.ebuf + (a.s.first_slot(n, b.Lc) * a.D + c) * S + s);
+    const float* ds = b.dsum + a.s.first_slot(n, b.Lc) * a.D + c;
+    const int64_t per_chunk = (int64_t)a.D * S / 4;
+    for (int64_t k = nch - 1; k >= 0; k -= U) {
+        float4 v[U];
+        float d[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            d[u] = 0.0f;
+            if (k - u > 0) {  // the first chunk's part is made by its own walk
+                v[u] = base[(k - u) * per_chunk];
+                d[u] = ds[(k - u) * a.D];
+            }
         }
-        *p = make_float4(e[0], e[1], e[2], e[3]);
-        e[0] = __fmaf_rn(ex2(d * A2[0]), e[0], v.x);
-        e[1] = __fmaf_rn(ex2(d * A2[1]), e[1], v.y);
-        e[2] = __fmaf_rn(ex2(d * A2[2]), e[2], v.z);
-        e[3] = __fmaf_rn(ex2(d * A2[3]), e[3], v.w);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (k - u < 0) break;
+            base[(k - u) * per_chunk] = make_float4(e[0], e[1], e[2], e[3]);
+            e[0] = __fmaf_rn(ex2(d[u] * A2[0]), e[0], v[u].x);
+            e[1] = __fmaf_rn(ex2(d[u] * A2[1]), e[1], v[u].y);
+            e[2] = __fmaf_rn(ex2(d[u] * A2[2]), e[2], v[u].z);
+            e[3] = __fmaf_rn(ex2(d[u] * A2[3]), e[3], v[u].w);
+        }
     }
 }
 
