@@ -20,9 +20,8 @@
 //
 // A lane holds 4 states of 2 channels, which leaves room for the tile's 64 registers of
 // decays and states.  dB and dC are sums over the
-// channels: 8 values per lane, summed over the lanes that share the states
-// by halving (7 shuffles for S = 16), over the warps in shared memory, and over the
-// channel blocks by k_ssm_dbc, in a fixed order.
+// channels: 8 values per lane, summed over the lanes that share the states and over
+// the warps in shared memory, and over the channel blocks by k_ssm_dbc, in a fixed order.
 //
 // Bound by instructions and their latency: 31 per (token, channel, state) in k_ssm_bwd, at
 // half of the issue slots with 12 warps per SM (168 registers, 70 KB).  Measured on a B200 for
@@ -93,7 +92,10 @@ struct SsmBwdCfg {
     static constexpr int CB = CW * (kSsmThreads / 32);
     static constexpr int SLOT = S > 32 ? 8 * S : 256;  // floats per warp and 4-token tile: states, later dB and dC
     static constexpr int NT = kSsmSave / 4;
-    static constexpr size_t SMEM = sizeof(float) * (4 * kSsmSave * CB + 2 * kSsmSave * S + 4 * NT * SLOT);
+    static constexpr int NG = 32 / LN;                   // lanes that share their states
+    static constexpr int PAIR = 2 * NG * 2 * S;          // floats per warp: dB and dC of 2 tokens and NG channel pairs
+    static constexpr size_t SMEM =
+        sizeof(float) * (3 * kSsmSave * CB + 2 * kSsmSave * S + 4 * NT * SLOT + 4 * PAIR);
 };
 
 // The adjoint of a chunk from zero, tokens in reverse: e = a (C dy' + e), and the chunk's
@@ -274,45 +276,24 @@ __global__ void __launch_bounds__(128) k_ssm_bwd_pass(const SsmBwdArgs b)
     }
 }
 
-// Sums of 8 values over the 32 / LN lanes that share q, by halving: v[0 .. 8 LN / 32)
-// end as the sums of the values 8 / NG * group + 0, 1, ...
-template <int LN>
-__device__ __forceinline__ void sum_groups(float (&v)[8], int lane)
-{
-    int have = 8;
-#pragma unroll
-    for (int o = 16; o >= LN; o >>= 1) {
-        have >>= 1;
-        const bool up = (lane & o) != 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (i < have) {
-                const float give = up ? v[i] : v[i + have];
-                const float keep = up ? v[i + have] : v[i];
-                v[i] = keep + __shfl_xor_sync(kFullMask, give, o);
-            }
-        }
-    }
-}
-
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 template <typename T, int S, int V, bool GATE>
 __global__ void __launch_bounds__(kSsmThreads, 3) k_ssm_bwd(const SsmBwdArgs b)
 {
     using Cf = SsmBwdCfg<S>;
-    constexpr int LN = Cf::LN, CW = Cf::CW, CB = Cf::CB, P = kSsmSave, NT = Cf::NT;
+    constexpr int LN = Cf::LN, CW = Cf::CW, CB = Cf::CB, P = kSsmSave, NT = Cf::NT, NG = Cf::NG;
     constexpr int PER_ROW = CB / V;
     constexpr int RSTEP = kSsmThreads / PER_ROW;
     static_assert(kSsmThreads % PER_ROW == 0, "a thread's vectors share their columns");
     extern __shared__ __align__(16) float smem[];
-    float* sd = smem;              // [P][CB] delta
+    float* sd = smem;              // [P][CB] delta, then sum_s h C
     float* sx = sd + P * CB;       // x, then ddelta
     float* sg = sx + P * CB;       // dy', then dx
-    float* sy = sg + P * CB;       // sum_s h C
-    float* sB = sy + P * CB;       // [P][S]
+    float* sB = sg + P * CB;       // [P][S]
     float* sC = sB + P * S;
     float* sh = sC + P * S;        // [warps][NT][SLOT]
+    float* sp = sh + 4 * NT * Cf::SLOT;  // [warps][PAIR]
 
     const SsmArgs& a = b.f;
     if (blockIdx.x == 0) check_seqs(a.s, a.status);
@@ -330,6 +311,8 @@ __global__ void __launch_bounds__(kSsmThreads, 3) k_ssm_bwd(const SsmBwdArgs b)
     const int q = lane & (LN - 1);
     const int col = warp * CW + (lane / LN) * 2;
     float* tiles = sh + warp * NT * Cf::SLOT;
+    float* pair = sp + warp * Cf::PAIR;
+    const int grp = lane / LN;
     f2x A2[2][2], ev[2][2], dA[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -468,6 +451,7 @@ __global__ void __launch_bounds__(kSsmThreads, 3) k_ssm_bwd(const SsmBwdArgs b)
         }
         for (int k = last; k >= 0; --k) {
             f2x am[4][2][2], qm[4][2][2];
+            float yk[4];  // sum_s h C of channel (q & LN / 2) != 0
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(tiles + k * Cf::SLOT + i * 128 + lane * 4);
@@ -503,7 +487,7 @@ __global__ void __launch_bounds__(kSsmThreads, 3) k_ssm_bwd(const SsmBwdArgs b)
                     float s = (up ? o[1] : o[0]) + __shfl_xor_sync(kFullMask, up ? o[0] : o[1], LN / 2);
 #pragma unroll
                     for (int w = LN / 4; w > 0; w >>= 1) s += __shfl_xor_sync(kFullMask, s, w);
-                    if ((q & (LN / 2 - 1)) == 0) sy[t * CB + col + (up ? 1 : 0)] = s;
+                    yk[j] = s;
                 }
             }
 #pragma unroll
@@ -559,18 +543,31 @@ __global__ void __launch_bounds__(kSsmThreads, 3) k_ssm_bwd(const SsmBwdArgs b)
                 } else if (owner) {
                     sx[t * CB + col + oi] = s;
                 }
-                float v[8];
-                up2(dB[0], v[0], v[1]);
-                up2(dB[1], v[2], v[3]);
-                up2(dC[0], v[4], v[5]);
-                up2(dC[1], v[6], v[7]);
-                sum_groups<LN>(v, lane);
-                constexpr int KEEP = 8 * LN / 32;
-                const int first = (lane / LN);  // bits of the group, the highest one halved first
+                if (GATE && (q & (LN / 2 - 1)) == 0) sd[t * CB + col + ((q & (LN / 2)) != 0 ? 1 : 0)] = yk[j];
+                // dB and dC of this token: [channel pair][dB, dC][S], the halves of odd pairs swapped
+                // (a quarter of the warp then writes to all banks); two tokens at a time are
+                // summed over the channel pairs.  Halving by shuffles took 28 instructions
+                // per token, this takes 12.
+                float* w = pair + ((j & 1) * NG + grp) * 2 * S + 4 * q;
+                *reinterpret_cast<ulonglong2*>(w + (grp & 1) * S) = make_ulonglong2(dB[0], dB[1]);
+                *reinterpret_cast<ulonglong2*>(w + (~grp & 1) * S) = make_ulonglong2(dC[0], dC[1]);
+                if ((j & 1) == 0) {
+                    __syncwarp();
+                    constexpr int OPL = S / 8;  // values per lane: 16 lanes to a token
+                    const int tok = lane >> 4, at = (lane & 15) * OPL;
+                    const float* r = pair + tok * NG * 2 * S;
+                    f2x sum[OPL / 2];
 #pragma unroll
-                for (int w = 0; w < KEEP; ++w) {
-                    const int id = first * KEEP + w;  // 0..3: dB of state 4q + id, 4..7: dC
-                    tiles[k * Cf::SLOT + j * 2 * S + (id >> 2) * S + 4 * q + (id & 3)] = v[w];
+                    for (int g = 0; g < NG; ++g)
+#pragma unroll
+                        for (int k = 0; k < OPL / 2; ++k) {
+                            const f2x x = *reinterpret_cast<const f2x*>(r + g * 2 * S + ((at + 2 * k) ^ ((g & 1) * S)));
+                            sum[k] = g == 0 ? x : fadd2(sum[k], x);
+                        }
+                    float* o = tiles + k * Cf::SLOT + (j + tok) * 2 * S + at;
+#pragma unroll
+                    for (int k = 0; k < OPL / 2; ++k) *reinterpret_cast<f2x*>(o + 2 * k) = sum[k];
+                    __syncwarp();
                 }
             }
         }
@@ -603,7 +600,7 @@ __global__ void __launch_bounds__(kSsmThreads, 3) k_ssm_bwd(const SsmBwdArgs b)
             if (GATE) {
                 const Vec<T, V> wx = load_vec<T, V>(x + row * a.ldx), wz = load_vec<T, V>(z + row * a.ldz);
                 const Vec<T, V> wg = load_vec<T, V>(dy + row * b.lddy);
-                get_row<V>(sy + r * CB + vc, o);
+                get_row<V>(sd + r * CB + vc, o);
                 get_row<V>(sD + vc, vb);
 #pragma unroll
                 for (int k = 0; k < V; ++k)
@@ -632,7 +629,7 @@ __global__ void __launch_bounds__(kSsmThreads, 3) k_ssm_bwd(const SsmBwdArgs b)
     }
     if (own >= 2 && owner && oc < cend) b.partD[slot * 2 * a.D + oc] = dD;
     float* red = sd;  // [RSTEP][CB]
-    static_assert(RSTEP * CB <= 4 * P * CB, "the token rows hold it");
+    static_assert(RSTEP * CB <= 3 * P * CB, "the token rows hold it");
 #pragma unroll
     for (int k = 0; k < V; ++k) red[vr * CB + vc + k] = dbias[k];
     __syncthreads();
