@@ -160,7 +160,8 @@ gdn_status_t conv_check(const void* x, int64_t x_stride, const void* weight, con
 
 struct NormPlan {
     int V, NV, tpr, threads;
-    bool wide;  // one block per row, the row read again
+    bool wide;   // one block per row, the row read again
+    bool shift;  // dense rows that are not whole vectors
 };
 
 // A row's threads: up to a warp with one vector each, then more vectors (up to
@@ -185,7 +186,10 @@ NormPlan norm_plan(int32_t D, int V, int most, int max_threads)
 // Blocks that walk the rows: a full GPU of about `resident` threads per SM.
 int64_t norm_blocks(int64_t rows, const NormPlan& p, int resident)
 {
-    return std::min<int64_t>(ceil_div(rows, p.threads / p.tpr), (int64_t)148 * std::max(1, resident / p.threads));
+    const int64_t all = ceil_div(rows, p.threads / p.tpr);
+    const int64_t most = (int64_t)148 * std::max(1, resident / p.threads);
+    if (all <= most) return all;
+    return p.shift ? most / p.V * p.V : most;  // shifted rows: a stride of whole vectors of rows
 }
 
 template <typename T, typename WT, int V, int NV>
@@ -194,7 +198,9 @@ bool norm_fwd_nv(const gdn::NormArgs& a, const NormPlan& p, cudaStream_t st)
     if (p.NV == NV) {
         const size_t sm = gdn::NormRing<T, V, NV, gdn::norm_depth(NV)>::BYTES * p.threads;
         const int resident = V == 1 ? 2048 : NV == 1 ? 1280 : NV == 2 ? 1024 : 512;
-        auto k = gdn::k_norm_fwd<T, WT, V, NV>;
+        auto k = gdn::k_norm_fwd<T, WT, V, NV, false>;
+        if constexpr (V > 1)
+            if (p.shift) k = gdn::k_norm_fwd<T, WT, V, NV, true>;
         if (!raise_smem(k, sm)) return false;
         k<<<(unsigned)norm_blocks(a.R, p, resident), p.threads, sm, st>>>(a);
     } else if constexpr (NV < (V == 1 ? 16 : 4)) {
@@ -215,7 +221,9 @@ bool norm_bwd_nv(const gdn::NormArgs& a, const NormPlan& p, int64_t* blocks, cud
     if (p.NV == NV) {
         const size_t sm = std::max(2 * gdn::NormRing<T, V, NV, gdn::norm_depth(NV)>::BYTES * p.threads,
                                    p.threads > p.tpr ? sizeof(float) * 2 * (size_t)a.D : 0);
-        auto k = gdn::k_norm_bwd<T, WT, V, NV>;
+        auto k = gdn::k_norm_bwd<T, WT, V, NV, false>;
+        if constexpr (V > 1)
+            if (p.shift) k = gdn::k_norm_bwd<T, WT, V, NV, true>;
         if (!raise_smem(k, sm)) return false;
         *blocks = norm_blocks(a.R, p, NV == 1 && V > 1 ? 1024 : 512);
         k<<<(unsigned)*blocks, p.threads, sm, st>>>(a);
@@ -556,10 +564,15 @@ gdn_status_t gdn_layer_norm_forward(const void* x, int64_t x_stride, const void*
     a.x = x; a.ldx = x_stride; a.w = weight; a.b = bias; a.w_bf16 = w_dtype == GDN_BF16;
     a.eps = eps; a.R = rows; a.D = width; a.y = y; a.mean = mean; a.rstd = rstd;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bool v16 = wide(x, x_stride, width, in_dtype) && wide(y, width, width, in_dtype);
+    bool v16 = wide(x, x_stride, width, in_dtype) && wide(y, width, width, in_dtype);
+    const int vec = (int)(16 / es);
+    const bool shift = !v16 && x_stride == width && aligned(x, 16) && aligned(y, 16) && width >= 4 * vec;
+    v16 = v16 || shift;
+    const int32_t span = shift ? width + vec - 1 : width;  // what the vectors of a row may cover
     // two vectors per thread measured best at 4096 x 16384 rows (63 us; four: 79, one: 101)
-    NormPlan p = v16 ? norm_plan(width, (int)(16 / es), 2, 512) : norm_plan(width, 1, 16, 1024);
-    if (p.wide && v16) p = norm_plan(width, (int)(16 / es), 4, 512);
+    NormPlan p = v16 ? norm_plan(span, vec, 2, 512) : norm_plan(width, 1, 16, 1024);
+    if (p.wide && v16) p = norm_plan(span, vec, 4, 512);
+    p.shift = shift;
     a.tpr = p.tpr;
     if (p.wide) {
         if (in_dtype == GDN_BF16) gdn::k_norm_fwd_wide<__nv_bfloat16><<<(unsigned)rows, 1024, 0, st>>>(a);
@@ -605,11 +618,17 @@ gdn_status_t gdn_layer_norm_backward(const void* x, int64_t x_stride, const void
     a.mean = const_cast<float*>(mean); a.rstd = const_cast<float*>(rstd);
     a.part = static_cast<float*>(workspace);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bool v16 = wide(x, x_stride, width, in_dtype) && wide(dy, dy_stride, width, in_dtype) &&
-                     wide(dx, width, width, in_dtype);
-    NormPlan p = v16 ? norm_plan(width, (int)(16 / es), 2, 256) : norm_plan(width, 1, 16, 256);
-    if (p.wide && v16) p = norm_plan(width, (int)(16 / es), 2, 512);
-    if (p.wide && v16) p = norm_plan(width, (int)(16 / es), 4, 512);
+    bool v16 = wide(x, x_stride, width, in_dtype) && wide(dy, dy_stride, width, in_dtype) &&
+               wide(dx, width, width, in_dtype);
+    const int vec = (int)(16 / es);
+    const bool shift = !v16 && x_stride == width && dy_stride == width && aligned(x, 16) && aligned(dy, 16) &&
+                       aligned(dx, 16) && width >= 4 * vec;
+    v16 = v16 || shift;
+    const int32_t span = shift ? width + vec - 1 : width;
+    NormPlan p = v16 ? norm_plan(span, vec, 2, 256) : norm_plan(width, 1, 16, 256);
+    if (p.wide && v16) p = norm_plan(span, vec, 2, 512);
+    if (p.wide && v16) p = norm_plan(span, vec, 4, 512);
+    p.shift = shift;
     a.tpr = p.tpr;
     int64_t parts = 0;
     if (rows > 0 && p.wide) {

@@ -249,7 +249,8 @@ def test_ssm_zero_and_extreme_steps():
 # ------------------------------------------------------------------- layer norm
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("R,D", [(1, 1), (7, 16), (300, 33), (64, 128), (9, 1000), (5, 1003), (3, 4096), (2, 16384),
-                                 (2, 20001), (1025, 64), (700, 2048), (4, 6000), (3, 8200), (2, 3001), (2, 9001)])
+                                 (2, 20001), (1025, 64), (700, 2048), (4, 6000), (3, 8200), (2, 3001), (2, 9001),
+                                 (50000, 35), (3000, 1003), (2000, 4098)])
 @pytest.mark.parametrize("bias", [True, False])
 def test_layer_norm(dtype, R, D, bias):
     t = TYPES[dtype]
