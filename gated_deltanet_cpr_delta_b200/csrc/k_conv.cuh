@@ -220,7 +220,17 @@ __global__ void __launch_bounds__(128, 7) k_conv_fwd(const ConvArgs a)
 #pragma unroll
     for (int u = 0; u < U; ++u) fetch(u, t + u < end);
     for (; t < end; t += U) {
-        if (t + U <= min(hi, end)) {
+        if (!ring.ON && t + U <= min(hi, end)) {  // 2-byte rows: all loads before the first use
+            Vec<T, V> raw[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) raw[u] = load_vec<T, V>(x + u * ldx);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                row(raw[u], y, true);
+                y += ldy;
+            }
+            x += U * ldx;
+        } else if (t + U <= min(hi, end)) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 ring.wait();
@@ -342,7 +352,19 @@ __device__ __forceinline__ void conv_bwd_run(const ConvArgs& a, int64_t t0, int6
             pd += a.D;
         };
         for (; t < stop; t += U) {
-            if (t >= first && t + U <= last) {
+            if (!ringx.ON && t >= first && t + U <= last) {  // 2-byte rows: all loads before the first use
+                Vec<T, V> rx[U], rg[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    rx[u] = load_vec<T, V>(px + u * ldx);
+                    rg[u] = load_vec<T, V>(pg + u * ldg);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) row(rx[u], rg[u], t + u, pd + u * (int64_t)a.D, true);
+                px += U * ldx;
+                pg += U * ldg;
+                pd += U * (int64_t)a.D;
+            } else if (t >= first && t + U <= last) {
 #pragma unroll
                 for (int u = 0; u < U; ++u) step(u, true);
             } else {

@@ -64,6 +64,12 @@ bool wide(const void* p, int64_t stride, int64_t width, gdn_dtype_t t)
     return p == nullptr || (aligned(p, 16) && stride % v == 0 && width % v == 0);
 }
 
+// Whether every row starts at, and consists of, whole groups of v elements.
+bool groups(const void* p, int64_t stride, int64_t width, gdn_dtype_t t, int64_t v)
+{
+    return aligned(p, v * esize(t)) && stride % v == 0 && width % v == 0;
+}
+
 bool rows_ok(const void* p, int64_t stride, int64_t width, gdn_dtype_t t)
 {
     return p != nullptr && stride >= width && stride <= INT32_MAX && aligned(p, esize(t));
@@ -442,14 +448,19 @@ gdn_status_t gdn_conv_forward(const void* x, int64_t x_stride, const void* weigh
     a.D = channels; a.silu = silu != 0; a.w_bf16 = w_dtype == GDN_BF16;
     a.y = y; a.state_out = state_out; a.status = status;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bool v16 = wide(x, x_stride, channels, in_dtype) && wide(y, channels, channels, in_dtype);
+    auto can = [&](int64_t v) {
+        return groups(x, x_stride, channels, in_dtype, v) && groups(y, channels, channels, in_dtype, v);
+    };
+    const int V = can(4) ? 4 : can(2) ? 2 : 1;  // channels per thread
     unsigned blocks = 0;
-    if (!conv_grid(a, v16 ? 4 : 1, 7, &blocks)) return GDN_ERR_INVALID_ARG;
+    if (!conv_grid(a, V, V == 4 ? 7 : 8, &blocks)) return GDN_ERR_INVALID_ARG;
     if (in_dtype == GDN_BF16) {
-        if (v16) launch_conv_fwd<__nv_bfloat16, 4>(a, width, blocks, st);
+        if (V == 4) launch_conv_fwd<__nv_bfloat16, 4>(a, width, blocks, st);
+        else if (V == 2) launch_conv_fwd<__nv_bfloat16, 2>(a, width, blocks, st);
         else launch_conv_fwd<__nv_bfloat16, 1>(a, width, blocks, st);
     } else {
-        if (v16) launch_conv_fwd<float, 4>(a, width, blocks, st);
+        if (V == 4) launch_conv_fwd<float, 4>(a, width, blocks, st);
+        else if (V == 2) launch_conv_fwd<float, 2>(a, width, blocks, st);
         else launch_conv_fwd<float, 1>(a, width, blocks, st);
     }
     return launched() ? GDN_OK : GDN_ERR_CUDA;
@@ -496,16 +507,21 @@ gdn_status_t gdn_conv_backward(const void* x, int64_t x_stride, const void* weig
     a.part = static_cast<float*>(workspace);
     a.status = status;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bool v4 = wide(x, x_stride, channels, in_dtype) && wide(dy, dy_stride, channels, in_dtype) &&
-                    wide(dx, channels, channels, in_dtype);
+    auto can = [&](int64_t v) {
+        return groups(x, x_stride, channels, in_dtype, v) && groups(dy, dy_stride, channels, in_dtype, v) &&
+               groups(dx, channels, channels, in_dtype, v);
+    };
+    const int V = can(4) ? 4 : can(2) ? 2 : 1;  // channels per thread
     unsigned blocks = 0;
-    if (!conv_grid(a, v4 ? 4 : 1, 4, &blocks)) return GDN_ERR_INVALID_ARG;
+    if (!conv_grid(a, V, 4, &blocks)) return GDN_ERR_INVALID_ARG;
     if (blocks > 0) {
         if (in_dtype == GDN_BF16) {
-            if (v4) launch_conv_bwd<__nv_bfloat16, 4>(a, width, blocks, st);
+            if (V == 4) launch_conv_bwd<__nv_bfloat16, 4>(a, width, blocks, st);
+            else if (V == 2) launch_conv_bwd<__nv_bfloat16, 2>(a, width, blocks, st);
             else launch_conv_bwd<__nv_bfloat16, 1>(a, width, blocks, st);
         } else {
-            if (v4) launch_conv_bwd<float, 4>(a, width, blocks, st);
+            if (V == 4) launch_conv_bwd<float, 4>(a, width, blocks, st);
+            else if (V == 2) launch_conv_bwd<float, 2>(a, width, blocks, st);
             else launch_conv_bwd<float, 1>(a, width, blocks, st);
         }
     }

@@ -68,7 +68,7 @@ def conv_case(dtype, D, W, lengths, bias, state, seed=0, wtype=None):
 
 @pytest.mark.parametrize("lengths", list(LENGTHS))
 @pytest.mark.parametrize("dtype", list(TYPES))
-@pytest.mark.parametrize("D,W,bias,state,act", [(64, 4, True, True, True), (33, 3, False, True, True),
+@pytest.mark.parametrize("D,W,bias,state,act", [(64, 4, True, True, True), (36, 4, True, True, True), (22, 3, True, True, True), (33, 3, False, True, True),
                                                 (1, 2, True, False, False), (2056, 4, False, False, True),
                                                 (130, 2, True, True, True)])
 def test_conv(dtype, D, W, bias, state, act, lengths):
