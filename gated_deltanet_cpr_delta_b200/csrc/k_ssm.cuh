@@ -124,25 +124,40 @@ __global__ void __launch_bounds__(SsmFwdCfg<T, S, SEG>::THREADS, 4) k_ssm_fwd(co
     auto stage = [&](int64_t p, int buf) {
         T* dst = raw + buf * 3 * Cf::TOK;
         const int rows = (int)min((int64_t)TT, L - p);
-        for (int i = tid; i < TT * (CB / V); i += NT) {
-            const int t = i / (CB / V), v = (i % (CB / V)) * V;
-            if (t < rows && cbase + v < cend) {
-                const int row = (int)(lo + p) + t;
-                T* d = dst + (t / K) * Cf::SEGROW + (t % K) * CB + v;
-                const T* px = static_cast<const T*>(a.x) + at(row, a.ldx) + cbase + v;
-                const T* pd = static_cast<const T*>(a.dt) + at(row, a.lddt) + cbase + v;
-                const T* pz = a.z != nullptr ? static_cast<const T*>(a.z) + at(row, a.ldz) + cbase + v : nullptr;
-                if constexpr (V * sizeof(T) >= 4) {
-                    ssm_cp_async<V * sizeof(T)>(d, px);
-                    ssm_cp_async<V * sizeof(T)>(d + Cf::TOK, pd);
-                    if (pz != nullptr) ssm_cp_async<V * sizeof(T)>(d + 2 * Cf::TOK, pz);
-                } else {
+        if constexpr (V * sizeof(T) >= 4) {
+            for (int i = tid; i < TT * (CB / V); i += NT) {
+                const int t = i / (CB / V), v = (i % (CB / V)) * V;
+                if (t < rows && cbase + v < cend) {
+                    const int row = (int)(lo + p) + t;
+                    T* d = dst + (t / K) * Cf::SEGROW + (t % K) * CB + v;
+                    ssm_cp_async<V * sizeof(T)>(d, static_cast<const T*>(a.x) + at(row, a.ldx) + cbase + v);
+                    ssm_cp_async<V * sizeof(T)>(d + Cf::TOK, static_cast<const T*>(a.dt) + at(row, a.lddt) + cbase + v);
+                    if (a.z != nullptr)
+                        ssm_cp_async<V * sizeof(T)>(d + 2 * Cf::TOK,
+                                                    static_cast<const T*>(a.z) + at(row, a.ldz) + cbase + v);
+                }
+            }
+        } else {  // 2 bytes: all loads before the first store
+            constexpr int E = TT * CB / NT;
+            T rx[E], rd[E], rz[E];
 #pragma unroll
-                    for (int k = 0; k < V; ++k) {
-                        d[k] = px[k];
-                        d[Cf::TOK + k] = pd[k];
-                        if (pz != nullptr) d[2 * Cf::TOK + k] = pz[k];
-                    }
+            for (int i = 0; i < E; ++i) {
+                const int t = (i * NT + tid) / CB, v = (i * NT + tid) % CB;
+                if (t < rows && cbase + v < cend) {
+                    const int row = (int)(lo + p) + t;
+                    rx[i] = static_cast<const T*>(a.x)[at(row, a.ldx) + cbase + v];
+                    rd[i] = static_cast<const T*>(a.dt)[at(row, a.lddt) + cbase + v];
+                    if (a.z != nullptr) rz[i] = static_cast<const T*>(a.z)[at(row, a.ldz) + cbase + v];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const int t = (i * NT + tid) / CB, v = (i * NT + tid) % CB;
+                if (t < rows && cbase + v < cend) {
+                    T* d = dst + (t / K) * Cf::SEGROW + (t % K) * CB + v;
+                    d[0] = rx[i];
+                    d[Cf::TOK] = rd[i];
+                    if (a.z != nullptr) d[2 * Cf::TOK] = rz[i];
                 }
             }
         }
