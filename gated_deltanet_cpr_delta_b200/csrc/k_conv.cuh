@@ -13,7 +13,8 @@
 // blocks allows.  Measured on a B200 (bf16, W = 4, silu): forward of 16384 x 6144
 // 73 us, 5.5 TB/s, 85% of the copy rate, with two special-function instructions per element
 // (48 us) next to it; gradients of 16384 x 2048 56 us + 4 us for the
-// sums of dw, 3.6 TB/s; the step of 64 x 12288 3.9 us.
+// sums of dw, 3.6 TB/s; the step of 64 x 12288 3.9 us.  Rows that are not whole 8 bytes
+// go in groups of 2 channels or singly: 8192 x 4097 39 us, gradients 105 us (x 4096: 27, 56).
 #pragma once
 
 #include "layer_common.cuh"

@@ -11,7 +11,9 @@
 // is large, without a second read.  Measured on a B200 (bf16): 16384 x 4096 forward
 // 59 us, 4.5 TB/s, gradients 78 us, 5.2 TB/s, + 5 us for the sums of dw and db;
 // 262144 rows of 128 30 us, 4.5 TB/s (there a row's two sums over 16 lanes
-// bind it as much as the memory); 64 x 4096 3.1 us.
+// bind it as much as the memory); 64 x 4096 3.5 us.  Dense rows of odd widths are read
+// in 16-byte vectors that start off the row (SHIFT): 8192 x 4097 forward 60 us, gradients 84 us
+// (8192 x 4096: 31 and 51 us; element by element 164 and 154 us).
 #pragma once
 
 #include "layer_common.cuh"

@@ -23,13 +23,14 @@
 // channels: 8 values per lane, summed over the lanes that share the states and over
 // the warps in shared memory, and over the channel blocks by k_ssm_dbc, in a fixed order.
 //
-// Bound by instructions and their latency: 31 per (token, channel, state) in k_ssm_bwd, at
-// half of the issue slots with 12 warps per SM (168 registers, 70 KB).  Measured on a B200 for
+// Bound by instructions and their latency: 30 per (token, channel, state) in k_ssm_bwd, at
+// half of the issue slots with 12 warps per SM (168 registers, 72 KB).  Measured on a B200 for
 // 2 x 4096 tokens x 2048 channels x 16 states (bf16): k_ssm_rev 106 us, k_ssm_bwd_pass
-// 14 us, k_ssm_bwd 480 us, the sums 24 us; the exponentials (three per element) take
+// 8 us, k_ssm_bwd 444 us, the sums 24 us; the exponentials (three per element) take
 // 173 us of that.  The forward's form (time segments in lanes, each exponential made
 // once, the channels in a loop) took 718 us in place of the three: as many instructions,
-// and half the warps.
+// and half the warps.  Rows that are not whole 16 bytes load element by element:
+// 8192 tokens x 4096 channels 1170 us in all, x 4097 1620 us.
 #pragma once
 
 #include "k_ssm.cuh"
