@@ -447,8 +447,9 @@ __global__ void __launch_bounds__(512) k_norm_bwd(const NormArgs a)
         fetch(left - DEP * step, slot);  // behind the sums that used the slots' last rows
         slot = slot + 1 == DEP ? 0 : slot + 1;
         if (on) {
-            // dx = rstd g + c1 (x - mean) + c0
-            const P c0 = pset<V>(-rstd * s[0] * inv), c1 = pset<V>(-rstd * rstd * rstd * s[1] * inv);
+            // dx = rstd g + c1 n + c0 with n = (x - mean) rstd formed again: a factor for x - mean would be
+            // rstd^3 s1 / D, and powers of rstd leave fp32 for rows of spread 1e13 or 1e-13
+            const P c0 = pset<V>(-rstd * (s[0] * inv)), c1 = pset<V>(-rstd * (s[1] * inv * rstd));
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 keep_packed(w[i]);  // not kept widened in twice the registers
@@ -456,7 +457,7 @@ __global__ void __launch_bounds__(512) k_norm_bwd(const NormArgs a)
                     P o[L::N];
 #pragma unroll
                     for (int k = 0; k < L::N; ++k) {
-                        o[k] = pfma(gw[i][k], r2, pfma(xc[i][k], c1, c0));
+                        o[k] = pfma(gw[i][k], r2, pfma(pmul(xc[i][k], r2), c1, c0));
                     }
                     if constexpr (SHIFT) cols.store(i, pd + i * a.tpr * V, o);
                     else pstore<T, V>(pd + i * a.tpr * V, o);

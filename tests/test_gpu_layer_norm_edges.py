@@ -1,0 +1,78 @@
+"""Layer norm on the GPU where its arithmetic is under strain: rows of extreme spread, constant rows,
+large means, strided rows, and gradients summed over many rows.
+
+Tolerances, in units of 2^-24 on the magnitude sum M of a value's terms.  A sum over a row passes
+d = 28 + D / 1024 additions at most (16 elements of a thread, or D / 1024 of the widest form, then the
+lanes and the warps).  In first order
+    mean   d + 4
+    rstd   (d + 4) / 2 + 4: the variance's sum, halved by the root, and the root
+    n      mean and rstd together: 2 d + 8
+    y      n, and two roundings: 2 d + 12
+    dx     rstd, n twice, a sum and a few products: 6 d + 32
+    dw     n, and the depth of the sum over the rows: R / 64 of a thread, 16 rows of a
+           block, 156 blocks of a column: 2 d + 12 + min(R, R / 64 + 172)
+    db     that depth
+and half a step of the output's type.  An error that is common to a whole column would pass the bounds of dw and
+db at many rows, so they are held to 1e-5 in the norm as well: independent roundings add like a random walk.
+"""
+import numpy as np
+import pytest
+import torch
+
+from gated_deltanet_cpr_delta_b200 import gdn
+from oracle import layer_ops as ops
+from test_gpu_layer_ops import TYPES, close, make
+
+pytestmark = pytest.mark.gpu
+
+
+def depth(D):
+    return 28 + D // 1024
+
+
+def rows_of(form, t, R, D):
+    """An uninitialised [R, D] whose rows are dense, or one element off within wider ones."""
+    if form == "dense":
+        return torch.empty(R, D, dtype=t, device="cuda")
+    return torch.empty(R, D + 9, dtype=t, device="cuda")[:, 1:1 + D]
+
+
+def fill(view, values):
+    view.copy_(values)
+    return view, view.double().cpu().numpy()
+
+
+def check(x, x64, w, w64, dy, dy64, eps, b=None, b64=None):
+    R, D = x64.shape
+    d = depth(D)
+    y, mean, rstd = gdn.gdn_layer_norm_forward(x, w, bias=b, eps=eps)
+    wy, wm, wr = ops.layer_norm(x64, w64, b64, eps)
+    My, Mx, Mw, Mb = ops.layer_norm_bounds(x64, w64, dy64, eps)
+    close("mean", mean, wm, np.abs(x64).mean(1), d + 4)
+    close("rstd", rstd, wr, wr, (d + 4) / 2 + 4)
+    close("y", y, wy, My + (0 if b64 is None else np.abs(b64)), 2 * d + 12)
+    dx, dw, db = gdn.gdn_layer_norm_backward(x, w, dy, mean, rstd)
+    wx, ww, wb = ops.layer_norm_backward(x64, w64, dy64, eps)
+    K = min(R, R // 64 + 172)
+    close("dx", dx, wx, Mx, 6 * d + 32)
+    close("dw", dw, ww, Mw, 2 * d + 12 + K)
+    close("db", db, wb, Mb, K)
+    for name, got, want in (("dw", dw, ww), ("db", db, wb)):
+        err = np.linalg.norm(got.double().cpu().numpy() - want)
+        assert err <= 1e-5 * np.linalg.norm(want), (name, err / np.linalg.norm(want))
+
+
+# columns and rows of the forms: vectors, shifted vectors, single elements, wider than the registers
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("form,D", [("dense", 64), ("dense", 1024), ("dense", 1003), ("off", 1003), ("off", 64),
+                                    ("dense", 20001)])
+@pytest.mark.parametrize("eps", [0.0, 1e-5])
+def test_rows_of_extreme_spread(dtype, form, D, eps):
+    """Rows scaled from 1e-16 to 1e16 (with eps = 1e-5, from 1): rstd is as small and as large, its cube out of range."""
+    t = TYPES[dtype]
+    rng = np.random.default_rng([5, D])
+    scales = [1.0, 1e15, 1e16, 1e12] + ([1e-14, 1e-16, 1e-12] if eps == 0 else [])
+    x = make(rng, t, len(scales), D)[0].float() * torch.tensor(scales, device="cuda")[:, None]
+    x, x64 = fill(rows_of(form, t, len(scales), D), x)
+    dy, dy64 = fill(rows_of(form, t, len(scales), D), make(rng, t, len(scales), D)[0])
+    check(x, x64, *make(rng, t, D), dy, dy64, eps)
