@@ -76,3 +76,59 @@ def test_rows_of_extreme_spread(dtype, form, D, eps):
     x, x64 = fill(rows_of(form, t, len(scales), D), x)
     dy, dy64 = fill(rows_of(form, t, len(scales), D), make(rng, t, len(scales), D)[0])
     check(x, x64, *make(rng, t, D), dy, dy64, eps)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("form,R,D", [("dense", 50000, 35), ("off", 50000, 33), ("dense", 30000, 64), ("dense", 9000, 128),
+                                      ("dense", 3000, 1003), ("off", 1500, 1000), ("dense", 2000, 4098),
+                                      ("dense", 1000, 2560), ("dense", 7, 16), ("off", 5, 3), ("dense", 150, 1),
+                                      ("dense", 300, 12001), ("dense", 90, 20001)])
+@pytest.mark.parametrize("bias", [True, False])
+def test_many_rows(dtype, form, R, D, bias):
+    """Blocks that walk several groups of rows, and join them: every row counts in dw and db."""
+    t = TYPES[dtype]
+    rng = np.random.default_rng([6, R, D])
+    x, x64 = fill(rows_of(form, t, R, D), make(rng, t, R, D)[0])
+    dy, dy64 = fill(rows_of(form, t, R, D), make(rng, t, R, D)[0])
+    check(x, x64, *make(rng, t, D), dy, dy64, 1e-5, *(make(rng, t, D) if bias else (None, None)))
+
+
+@pytest.mark.parametrize("form,R,D", [("dense", 60, 64), ("dense", 60, 1003), ("off", 60, 130), ("dense", 60, 9001)])
+def test_rows_of_large_mean(form, R, D):
+    """Mean 1000 and spread 1: the values and the gradients, not their shapes alone."""
+    rng = np.random.default_rng([7, D])
+    x, x64 = fill(rows_of(form, torch.float32, R, D), make(rng, torch.float32, R, D)[0] + 1000)
+    dy, dy64 = fill(rows_of(form, torch.float32, R, D), make(rng, torch.float32, R, D)[0])
+    w, w64 = make(rng, torch.float32, D)
+    d, eps = depth(D), 1e-5
+    y, mean, rstd = gdn.gdn_layer_norm_forward(x, w, eps=eps)
+    wy, wm, _ = ops.layer_norm(x64, w64, None, eps)
+    My, Mx, Mw, Mb = ops.layer_norm_bounds(x64, w64, dy64, eps)
+    close("mean", mean, wm, np.abs(x64).mean(1), d + 4)
+    close("y", y, wy, My, 2 * d + 12)
+    got = gdn.gdn_layer_norm_backward(x, w, dy, mean, rstd)
+    K = (6 * d + 32, 2 * d + 12 + R, R)
+    for name, g, want, m, k in zip(("dx", "dw", "db"), got, ops.layer_norm_backward(x64, w64, dy64, eps), (Mx, Mw, Mb), K):
+        close(name, g, want, m, k)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("form,D", [("dense", 64), ("dense", 1003), ("off", 77), ("dense", 20001)])
+def test_constant_rows(dtype, form, D):
+    """With eps a constant row gives y = bias; with eps = 0 it is not a number, and its neighbours are."""
+    t = TYPES[dtype]
+    rng = np.random.default_rng([8, D])
+    x = make(rng, t, 5, D)[0]
+    x[1], x[3] = 0.0, 1.5
+    x, x64 = fill(rows_of(form, t, 5, D), x)
+    dy, dy64 = fill(rows_of(form, t, 5, D), make(rng, t, 5, D)[0])
+    (w, w64), (b, b64) = make(rng, t, D), make(rng, t, D)
+    check(x, x64, w, w64, dy, dy64, 1e-5, b, b64)
+    y, mean, rstd = gdn.gdn_layer_norm_forward(x, w, bias=b, eps=0.0)
+    assert torch.equal(y[[1, 3]].isnan(), torch.ones_like(y[[1, 3]], dtype=torch.bool)) and torch.isinf(rstd[[1, 3]]).all()
+    dx = gdn.gdn_layer_norm_backward(x, w, dy, mean, rstd)[0]
+    keep = [0, 2, 4]
+    wy = ops.layer_norm(x64[keep], w64, b64, 0.0)[0]
+    My, Mx, _, _ = ops.layer_norm_bounds(x64[keep], w64, dy64[keep], 0.0)
+    close("y", y[keep], wy, My + np.abs(b64), 2 * depth(D) + 12)
+    close("dx", dx[keep], ops.layer_norm_backward(x64[keep], w64, dy64[keep], 0.0)[0], Mx, 6 * depth(D) + 32)
