@@ -96,11 +96,11 @@ int conv_run(int64_t T, int64_t nvec, int sms, int resident)
     return (int)std::max<int64_t>(8, std::min<int64_t>(512, ceil_div(run, 8) * 8));
 }
 
-// Grid of the convolution kernels for V channels per thread; false if it does not fit.
-bool conv_grid(gdn::ConvArgs& a, int V, int resident, unsigned* blocks)
+// Grid of the convolution kernels for V channels per thread.
+gdn_status_t conv_grid(gdn::ConvArgs& a, int V, int resident, unsigned* blocks)
 {
     const int sms = sm_count();
-    if (sms == 0) return false;
+    if (sms == 0) return GDN_ERR_CUDA;
     const int64_t nvec = ceil_div(a.D, V);
     a.cx = conv_cx(nvec);
     a.ncb = (int32_t)ceil_div(nvec, a.cx);
@@ -108,9 +108,9 @@ bool conv_grid(gdn::ConvArgs& a, int V, int resident, unsigned* blocks)
     const int ny = 128 / a.cx;
     a.ntiles = ceil_div(a.s.T, (int64_t)a.run * ny);
     const int64_t n = (a.ntiles + ceil_div(a.s.N, ny)) * a.ncb;
-    if (n > INT32_MAX) return false;
+    if (n > INT32_MAX) return GDN_ERR_INVALID_ARG;
     *blocks = (unsigned)n;
-    return true;
+    return GDN_OK;
 }
 
 // Rows of partial weight gradients for any vector width and any number of SMs:
@@ -453,7 +453,8 @@ gdn_status_t gdn_conv_forward(const void* x, int64_t x_stride, const void* weigh
     };
     const int V = can(4) ? 4 : can(2) ? 2 : 1;  // channels per thread
     unsigned blocks = 0;
-    if (!conv_grid(a, V, V == 4 ? 7 : 8, &blocks)) return GDN_ERR_INVALID_ARG;
+    const gdn_status_t grid = conv_grid(a, V, V == 4 ? 7 : 8, &blocks);
+    if (grid != GDN_OK) return grid;
     if (in_dtype == GDN_BF16) {
         if (V == 4) launch_conv_fwd<__nv_bfloat16, 4>(a, width, blocks, st);
         else if (V == 2) launch_conv_fwd<__nv_bfloat16, 2>(a, width, blocks, st);
@@ -513,7 +514,8 @@ gdn_status_t gdn_conv_backward(const void* x, int64_t x_stride, const void* weig
     };
     const int V = can(4) ? 4 : can(2) ? 2 : 1;  // channels per thread
     unsigned blocks = 0;
-    if (!conv_grid(a, V, 4, &blocks)) return GDN_ERR_INVALID_ARG;
+    const gdn_status_t grid = conv_grid(a, V, 4, &blocks);
+    if (grid != GDN_OK) return grid;
     if (blocks > 0) {
         if (in_dtype == GDN_BF16) {
             if (V == 4) launch_conv_bwd<__nv_bfloat16, 4>(a, width, blocks, st);
