@@ -14,6 +14,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <initializer_list>
 
 namespace {
 
@@ -46,16 +47,40 @@ int sm_count()
     return sms;
 }
 
-// A [rows, width] tensor with rows `stride` elements apart, as a byte range.
+// The bytes of a [rows, width] tensor whose rows are `stride` elements apart.
 struct Span {
-    uintptr_t lo, hi;
-    Span(const void* p, int64_t rows, int64_t stride, int64_t width, size_t esz)
-        : lo(reinterpret_cast<uintptr_t>(p)),
-          hi(p == nullptr || rows <= 0 ? lo : lo + (size_t)((rows - 1) * stride + width) * esz)
+    uintptr_t lo = 0, hi = 0;      // from the first row's start to the last row's end; empty: lo == hi
+    size_t step = 0, width = 0;    // bytes between rows, and of a row
+    Span(const void* p, int64_t rows, int64_t stride, int64_t row, size_t esz)
     {
+        if (p == nullptr || rows <= 0 || row <= 0) return;
+        lo = reinterpret_cast<uintptr_t>(p);
+        step = (size_t)stride * esz;
+        width = (size_t)row * esz;
+        hi = lo + (size_t)(rows - 1) * step + width;
     }
-    bool hits(const Span& o) const { return lo < o.hi && o.lo < hi; }
+    Span(const void* p, int64_t n, size_t esz) : Span(p, 1, n, n, esz) {}
+    // Whether a dense tensor o shares bytes with it: its rows, not the room between them.
+    bool hits(const Span& o) const
+    {
+        if (lo == hi || o.lo == o.hi || lo >= o.hi || o.lo >= hi) return false;
+        // the first row that ends behind o's start
+        const size_t k = o.lo < lo + width ? 0 : (o.lo - lo - width) / step + 1;
+        return lo + k * step < o.hi;
+    }
 };
+
+// Whether an output (all dense) shares bytes with an input or with another output.
+bool overlap(std::initializer_list<Span> outs, std::initializer_list<Span> ins)
+{
+    for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+        for (const Span& i : ins)
+            if (i.hits(*o)) return true;
+        for (const Span* q = o + 1; q != outs.end(); ++q)
+            if (o->hits(*q)) return true;
+    }
+    return false;
+}
 
 // 16-byte accesses: the row's address, stride and width are multiples of 16 bytes.
 bool wide(const void* p, int64_t stride, int64_t width, gdn_dtype_t t)
@@ -438,10 +463,11 @@ gdn_status_t gdn_conv_forward(const void* x, int64_t x_stride, const void* weigh
     if (state_out == nullptr || !aligned(state_out, 16)) return GDN_ERR_INVALID_ARG;
     if (total_tokens > 0 && !rows_ok(y, channels, channels, in_dtype)) return GDN_ERR_INVALID_ARG;
     const size_t es = esize(in_dtype);
-    const Span sx(x, total_tokens, x_stride, channels, es), sy(y, total_tokens, channels, channels, es);
-    const Span si(state_in, (int64_t)num_seqs * (width - 1), channels, channels, es);
-    const Span so(state_out, (int64_t)num_seqs * (width - 1), channels, channels, es);
-    if (sx.hits(sy) || sx.hits(so) || si.hits(sy) || si.hits(so) || sy.hits(so)) return GDN_ERR_INVALID_ARG;
+    const int64_t tail = (int64_t)num_seqs * (width - 1) * channels;
+    if (overlap({{y, total_tokens * channels, es}, {state_out, tail, es}, {status, 1, 4}},
+                {{x, total_tokens, x_stride, channels, es}, {state_in, tail, es}, {cu_seqlens, num_seqs + 1LL, 4},
+                 {weight, (int64_t)channels * width, esize(w_dtype)}, {bias, channels, esize(w_dtype)}}))
+        return GDN_ERR_INVALID_ARG;
     gdn::ConvArgs a{};
     a.s = Seqs{cu_seqlens, num_seqs, total_tokens};
     a.x = x; a.ldx = x_stride; a.w = weight; a.bias = bias; a.state_in = state_in;
@@ -490,15 +516,15 @@ gdn_status_t gdn_conv_backward(const void* x, int64_t x_stride, const void* weig
     if (total_tokens > 0 && (!rows_ok(dy, dy_stride, channels, in_dtype) || !rows_ok(dx, channels, channels, in_dtype)))
         return GDN_ERR_INVALID_ARG;
     const size_t es = esize(in_dtype);
-    const Span sx(x, total_tokens, x_stride, channels, es), sg(dy, total_tokens, dy_stride, channels, es);
-    const Span sd(dx, total_tokens, channels, channels, es);
-    const int64_t tail = (int64_t)num_seqs * (width - 1);
-    if (sd.hits(sx) || sd.hits(sg) ||
-        Span(dstate_in, tail, channels, channels, 4).hits(Span(dstate_out, tail, channels, channels, 4)))
+    const int64_t tail = (int64_t)num_seqs * (width - 1) * channels;
+    const size_t need = gdn_conv_backward_workspace_size(total_tokens, num_seqs, channels, width);
+    if (overlap({{dx, total_tokens * channels, es}, {dweight, (int64_t)channels * width, 4}, {dbias, channels, 4},
+                 {dstate_in, tail, 4}, {workspace, (int64_t)need, 1}, {status, 1, 4}},
+                {{x, total_tokens, x_stride, channels, es}, {dy, total_tokens, dy_stride, channels, es},
+                 {state_in, tail, es}, {dstate_out, tail, 4}, {cu_seqlens, num_seqs + 1LL, 4},
+                 {weight, (int64_t)channels * width, esize(w_dtype)}, {bias, channels, esize(w_dtype)}}))
         return GDN_ERR_INVALID_ARG;
-    if (workspace == nullptr ||
-        workspace_bytes < gdn_conv_backward_workspace_size(total_tokens, num_seqs, channels, width))
-        return GDN_ERR_WORKSPACE;
+    if (workspace == nullptr || workspace_bytes < need) return GDN_ERR_WORKSPACE;
     if (!aligned(workspace, kAlign)) return GDN_ERR_INVALID_ARG;
     gdn::ConvArgs a{};
     a.s = Seqs{cu_seqlens, num_seqs, num_seqs > 0 ? total_tokens : 0};
@@ -545,10 +571,10 @@ gdn_status_t gdn_conv_step(const void* x, int64_t x_stride, const void* weight, 
     if (state == nullptr || state_out == nullptr || !aligned(state_out, 16) || !rows_ok(y, channels, channels, in_dtype))
         return GDN_ERR_INVALID_ARG;
     const size_t es = esize(in_dtype);
-    const Span sx(x, num_seqs, x_stride, channels, es), sy(y, num_seqs, channels, channels, es);
-    const Span si(state, (int64_t)num_seqs * (width - 1), channels, channels, es);
-    const Span so(state_out, (int64_t)num_seqs * (width - 1), channels, channels, es);
-    if (sx.hits(sy) || sx.hits(so) || sy.hits(si) || sy.hits(so) || (state != state_out && si.hits(so)))
+    const int64_t tail = (int64_t)num_seqs * (width - 1) * channels;
+    if (overlap({{y, (int64_t)num_seqs * channels, es}, {state_out, tail, es}},
+                {{x, num_seqs, x_stride, channels, es}, {state != state_out ? state : nullptr, tail, es},
+                 {weight, (int64_t)channels * width, esize(w_dtype)}, {bias, channels, esize(w_dtype)}}))
         return GDN_ERR_INVALID_ARG;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool v16 = wide(x, x_stride, channels, in_dtype) && wide(y, channels, channels, in_dtype);
@@ -577,7 +603,9 @@ gdn_status_t gdn_layer_norm_forward(const void* x, int64_t x_stride, const void*
         rstd == nullptr || !aligned(mean, 4) || !aligned(rstd, 4))
         return GDN_ERR_INVALID_ARG;
     const size_t es = esize(in_dtype);
-    if (Span(x, rows, x_stride, width, es).hits(Span(y, rows, width, width, es))) return GDN_ERR_INVALID_ARG;
+    if (overlap({{y, rows * width, es}, {mean, rows, 4}, {rstd, rows, 4}},
+                {{x, rows, x_stride, width, es}, {weight, width, esize(w_dtype)}, {bias, width, esize(w_dtype)}}))
+        return GDN_ERR_INVALID_ARG;
     gdn::NormArgs a{};
     a.x = x; a.ldx = x_stride; a.w = weight; a.b = bias; a.w_bf16 = w_dtype == GDN_BF16;
     a.eps = eps; a.R = rows; a.D = width; a.y = y; a.mean = mean; a.rstd = rstd;
@@ -624,11 +652,12 @@ gdn_status_t gdn_layer_norm_backward(const void* x, int64_t x_stride, const void
                      !rows_ok(dx, width, width, in_dtype) || mean == nullptr || rstd == nullptr))
         return GDN_ERR_INVALID_ARG;
     const size_t es = esize(in_dtype);
-    const Span sd(dx, rows, width, width, es);
-    if (sd.hits(Span(x, rows, x_stride, width, es)) || sd.hits(Span(dy, rows, dy_stride, width, es)))
+    const size_t need = gdn_layer_norm_backward_workspace_size(rows, width);
+    if (overlap({{dx, rows * width, es}, {dweight, width, 4}, {dbias, width, 4}, {workspace, (int64_t)need, 1}},
+                {{x, rows, x_stride, width, es}, {dy, rows, dy_stride, width, es}, {mean, rows, 4}, {rstd, rows, 4},
+                 {weight, width, esize(w_dtype)}}))
         return GDN_ERR_INVALID_ARG;
-    if (workspace == nullptr || workspace_bytes < gdn_layer_norm_backward_workspace_size(rows, width))
-        return GDN_ERR_WORKSPACE;
+    if (workspace == nullptr || workspace_bytes < need) return GDN_ERR_WORKSPACE;
     if (!aligned(workspace, kAlign)) return GDN_ERR_INVALID_ARG;
     gdn::NormArgs a{};
     a.x = x; a.ldx = x_stride; a.dy = dy; a.lddy = dy_stride; a.w = weight; a.w_bf16 = w_dtype == GDN_BF16;
@@ -703,13 +732,13 @@ gdn_status_t gdn_ssm_forward(const gdn_ssm_t* args, const float* state_in, void*
         return GDN_ERR_INVALID_ARG;
     if (s.total_tokens > 0 && !rows_ok(y, s.channels, s.channels, s.in_dtype)) return GDN_ERR_INVALID_ARG;
     const size_t es = esize(s.in_dtype);
-    const int64_t T = s.total_tokens, per = (int64_t)s.channels * s.states;
-    const Span sy(y, T, s.channels, s.channels, es), so(state_out, s.num_seqs, per, per, 4);
-    if (sy.hits(Span(s.x, T, s.x_stride, s.channels, es)) || sy.hits(Span(s.dt, T, s.dt_stride, s.channels, es)) ||
-        sy.hits(Span(s.z, T, s.z_stride, s.channels, es)) ||
-        sy.hits(Span(s.B, T, s.B_stride, (int64_t)s.groups * s.states, es)) ||
-        sy.hits(Span(s.C, T, s.C_stride, (int64_t)s.groups * s.states, es)) ||
-        so.hits(Span(state_in, s.num_seqs, per, per, 4)))
+    const int64_t T = s.total_tokens, per = (int64_t)s.channels * s.states, bc = (int64_t)s.groups * s.states;
+    if (overlap({{y, T * s.channels, es}, {state_out, s.num_seqs * per, 4}, {status, 1, 4},
+                 {chunk_states, gdn_ssm_num_chunk_states(T, s.num_seqs) * per, 4}},
+                {{s.x, T, s.x_stride, s.channels, es}, {s.dt, T, s.dt_stride, s.channels, es},
+                 {s.z, T, s.z_stride, s.channels, es}, {s.B, T, s.B_stride, bc, es}, {s.C, T, s.C_stride, bc, es},
+                 {s.A, per, 4}, {s.D, s.channels, 4}, {s.dt_bias, s.channels, 4},
+                 {s.cu_seqlens, s.num_seqs + 1LL, 4}, {state_in, s.num_seqs * per, 4}}))
         return GDN_ERR_INVALID_ARG;
     gdn::SsmArgs a = ssm_args(args, 1);  // the launch sets the channel blocks
     a.state_in = state_in; a.y = y; a.state_out = state_out; a.saved = chunk_states;
@@ -738,21 +767,19 @@ gdn_status_t gdn_ssm_backward(const gdn_ssm_t* args, const void* dy, int64_t dy_
         return GDN_ERR_INVALID_ARG;
     const size_t es = esize(s.in_dtype);
     const int64_t bc = (int64_t)s.groups * s.states;
-    const Span in[] = {Span(s.x, T, s.x_stride, s.channels, es), Span(s.dt, T, s.dt_stride, s.channels, es),
-                       Span(s.z, T, s.z_stride, s.channels, es), Span(dy, T, dy_stride, s.channels, es),
-                       Span(s.B, T, s.B_stride, bc, es), Span(s.C, T, s.C_stride, bc, es)};
-    const Span out[] = {Span(dx, T, s.channels, s.channels, es), Span(ddt, T, s.channels, s.channels, es),
-                        Span(s.z ? dz : nullptr, T, s.channels, s.channels, es), Span(dB, T, bc, bc, es),
-                        Span(dC, T, bc, bc, es)};
-    for (const Span& i : in)
-        for (const Span& o : out)
-            if (i.hits(o)) return GDN_ERR_INVALID_ARG;
-    const int64_t per = (int64_t)s.channels * s.states;
-    if (Span(dstate_in, s.num_seqs, per, per, 4).hits(Span(dstate_out, s.num_seqs, per, per, 4)))
+    const int64_t per = (int64_t)s.channels * s.states, states = s.num_seqs * per;
+    const size_t need =
+        gdn_ssm_backward_workspace_size(s.total_tokens, s.num_seqs, s.channels, s.groups, s.states);
+    if (overlap({{dx, T * s.channels, es}, {ddt, T * s.channels, es}, {s.z ? dz : nullptr, T * s.channels, es},
+                 {dB, T * bc, es}, {dC, T * bc, es}, {dA, per, 4}, {dD, s.channels, 4}, {ddt_bias, s.channels, 4},
+                 {dstate_in, states, 4}, {workspace, (int64_t)need, 1}, {status, 1, 4}},
+                {{s.x, T, s.x_stride, s.channels, es}, {s.dt, T, s.dt_stride, s.channels, es},
+                 {s.z, T, s.z_stride, s.channels, es}, {s.B, T, s.B_stride, bc, es}, {s.C, T, s.C_stride, bc, es},
+                 {s.A, per, 4}, {s.D, s.channels, 4}, {s.dt_bias, s.channels, 4},
+                 {s.cu_seqlens, s.num_seqs + 1LL, 4}, {dy, T, dy_stride, s.channels, es}, {dstate_out, states, 4},
+                 {chunk_states, gdn_ssm_num_chunk_states(T, s.num_seqs) * per, 4}}))
         return GDN_ERR_INVALID_ARG;
-    if (workspace == nullptr ||
-        workspace_bytes < gdn_ssm_backward_workspace_size(s.total_tokens, s.num_seqs, s.channels, s.groups, s.states))
-        return GDN_ERR_WORKSPACE;
+    if (workspace == nullptr || workspace_bytes < need) return GDN_ERR_WORKSPACE;
     if (!aligned(workspace, kAlign)) return GDN_ERR_INVALID_ARG;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (s.num_seqs == 0) {  // no token, no state: the parameters' gradients are zero
@@ -787,9 +814,12 @@ gdn_status_t gdn_ssm_step(const gdn_ssm_t* args, const float* state, float* stat
         return GDN_ERR_INVALID_ARG;
     const size_t es = esize(s.in_dtype);
     const int64_t N = s.num_seqs, per = (int64_t)s.channels * s.states;
-    const Span sy(y, N, s.channels, s.channels, es), si(state, N, per, per, 4), so(state_out, N, per, per, 4);
-    if (sy.hits(Span(s.x, N, s.x_stride, s.channels, es)) || sy.hits(Span(s.dt, N, s.dt_stride, s.channels, es)) ||
-        sy.hits(Span(s.z, N, s.z_stride, s.channels, es)) || (state != state_out && si.hits(so)))
+    const int64_t bc = (int64_t)s.groups * s.states;
+    if (overlap({{y, N * s.channels, es}, {state_out, N * per, 4}},
+                {{s.x, N, s.x_stride, s.channels, es}, {s.dt, N, s.dt_stride, s.channels, es},
+                 {s.z, N, s.z_stride, s.channels, es}, {s.B, N, s.B_stride, bc, es}, {s.C, N, s.C_stride, bc, es},
+                 {s.A, per, 4}, {s.D, s.channels, 4}, {s.dt_bias, s.channels, 4},
+                 {state != state_out ? state : nullptr, N * per, 4}}))
         return GDN_ERR_INVALID_ARG;
     gdn::SsmArgs a = ssm_args(args, 1);
     a.state_in = state; a.state_out = state_out; a.y = y;

@@ -464,7 +464,9 @@ gdn_status_t gdn_cpr_forward_noalloc(const void* q, const void* k, const void* v
  *    are in every output.  An offset that breaks this is clamped, so no access
  *    leaves the tensors, the results are unspecified, and *status (one int32 on the
  *    device, or NULL; never cleared by the library) becomes GDN_ERR_DEVICE_INPUT.
- *  - Outputs must not overlap inputs, except where a call says so.
+ *  - An output shares no byte with an input (a parameter, a state, the offsets), with another
+ *    output or with the part of the workspace that the call asks for, except where a
+ *    call says so: GDN_ERR_INVALID_ARG.  The room between the rows of a strided view is free.
  *  - Every sum is fp32 and in a fixed order, without atomics: repeated calls
  *    give the same bits.  Inputs that are not finite spread within the rows (norm)
  *    or sequences (convolution, scan) and channels they belong to, and into the

@@ -80,3 +80,72 @@ CALLS = [conv_forward, conv_backward, conv_step, norm_forward, norm_backward, ss
 @pytest.mark.parametrize("call", CALLS)
 def test_a_valid_call_without_a_gpu_is_a_cuda_error(lib, call):
     assert call(lib) == CUDA
+
+
+# bytes of each tensor of the calls above (bf16 tokens, parameters as the call has them)
+TOK, BC = 10 * 64 * 2, 10 * 2 * 16 * 2
+OVERLAPS = {
+    conv_forward: (dict(x=TOK, w=64 * 4 * 2, b=128, s=2 * 3 * 64 * 2, cu=12), dict(y=TOK, so=2 * 3 * 64 * 2, st=4)),
+    conv_backward: (dict(x=TOK, w=64 * 4 * 2, b=128, s=2 * 3 * 64 * 2, cu=12, dy=TOK, do=2 * 3 * 64 * 4),
+                    dict(dx=TOK, dw=64 * 4 * 4, db=256, ds=2 * 3 * 64 * 4, ws=2 * 5 * 64 * 4, st=4)),
+    conv_step: (dict(x=2 * 64 * 2, w=64 * 4 * 2, b=128), dict(y=2 * 64 * 2, so=2 * 3 * 64 * 2)),
+    norm_forward: (dict(x=4 * 64 * 2, w=128, b=128), dict(y=4 * 64 * 2, m=16, r=16)),
+    norm_backward: (dict(x=4 * 64 * 2, dy=4 * 64 * 2, w=128, m=16, r=16), dict(dx=4 * 64 * 2, dw=256, db=256, ws=4 * 2 * 64 * 4)),
+    ssm_forward: (dict(x=TOK, dt=TOK, B=BC, C=BC, z=TOK, A=4096, D=256, dt_bias=256, cu=12, si=8192),
+                  dict(y=TOK, so=8192, cs=2 * 4096, st=4)),
+    ssm_backward: (dict(x=TOK, dt=TOK, B=BC, C=BC, z=TOK, A=4096, D=256, dt_bias=256, cu=12, dy=TOK, cs=8192, do=8192),
+                   dict(dx=TOK, ddt=TOK, dA=4096, dB=BC, dC=BC, dD=256, dz=TOK, db=256, ds=8192, ws=8192 + 1024 + 2560, st=4)),
+    ssm_step: (dict(x=256, dt=256, B=128, C=128, z=256, A=4096, D=256, dt_bias=256), dict(y=256, so=8192)),
+}
+PAIRS = [(call, o, i) for call, (ins, outs) in OVERLAPS.items() for n, o in enumerate(outs)
+         for i in list(ins) + list(outs)[n + 1:]]
+BIG = A[60]
+
+
+def place(call, name):
+    """(the tensor's bytes, the alignment that it needs)"""
+    ins, outs = OVERLAPS[call]
+    return dict(ins, **outs)[name]
+
+
+@pytest.mark.parametrize("call,out,other", PAIRS, ids=[f"{c.__name__}-{o}-{i}" for c, o, i in PAIRS])
+def test_outputs_that_overlap_are_refused(lib, call, out, other):
+    """The last 16 bytes (4 of a short tensor) of either inside the other; just behind it is accepted."""
+    step = 256 if "ws" in (out, other) else 16 if place(call, out) >= 16 and place(call, other) >= 16 else 4
+    kw = {"s": BIG + (1 << 30)} if call is conv_step else {"s": BIG + (2 << 30)} if call is ssm_step else {}
+    n = place(call, other) // step * step
+    assert call(lib, **dict(kw, **{other: BIG, out: BIG + max(0, n - step)})) == BAD
+    n = place(call, out) // step * step
+    assert call(lib, **dict(kw, **{out: BIG, other: BIG + max(0, n - step)})) == BAD
+    n = -(-place(call, other) // 256) * 256
+    assert call(lib, **dict(kw, **{other: BIG, out: BIG + n})) == CUDA
+
+
+def test_states_of_the_steps(lib):
+    for call, n in ((conv_step, 2 * 3 * 64 * 2), (ssm_step, 8192)):
+        assert call(lib, s=BIG, so=BIG) == CUDA and call(lib, s=BIG, so=BIG + n) == CUDA
+        assert call(lib, s=BIG, so=BIG + n - 16) == BAD and call(lib, s=BIG + n - 16, so=BIG) == BAD
+        assert call(lib, s=BIG, so=BIG, y=BIG) == BAD and call(lib, s=BIG, so=A[40], y=BIG + n - 16) == BAD
+        assert call(lib, s=BIG, so=A[40], y=A[40] + n - 16) == BAD
+
+
+def test_outputs_between_the_rows_of_an_input(lib):
+    """Rows 4096 elements apart leave room for another tensor; a row's own bytes do not."""
+    wide = dict(x=BIG, ldx=4096)
+    assert conv_forward(lib, so=BIG + 128, **wide) == CUDA and conv_forward(lib, y=BIG + 8192 + 128, **wide) == CUDA
+    assert conv_forward(lib, y=BIG + 8192 - 16, **wide) == BAD and conv_forward(lib, y=BIG + 8192 * 9 + 112, **wide) == BAD
+    assert conv_forward(lib, y=BIG + 8192 * 9 + 128, **wide) == CUDA
+    assert conv_forward(lib, y=BIG + 8192 - TOK, **wide) == CUDA and conv_forward(lib, y=BIG - TOK, **wide) == CUDA
+
+
+def test_the_workspace_is_what_the_call_needs(lib):
+    """A workspace with bytes to spare may hold other tensors behind the bytes that the call asks for."""
+    n = lib.gdn_conv_backward_workspace_size(10, 2, 64, 4)
+    assert conv_backward(lib, ws=BIG, wsb=1 << 30, dx=BIG + n) == CUDA
+    assert conv_backward(lib, ws=BIG, wsb=1 << 30, dx=BIG + n - 256) == BAD
+    n = lib.gdn_ssm_backward_workspace_size(10, 2, 64, 2, 16)
+    assert ssm_backward(lib, ws=BIG, wsb=1 << 30, ds=BIG + n) == CUDA
+    assert ssm_backward(lib, ws=BIG, wsb=1 << 30, ds=BIG + n - 256) == BAD
+    n = lib.gdn_layer_norm_backward_workspace_size(4, 64)
+    assert norm_backward(lib, ws=BIG, wsb=1 << 30, dx=BIG + n) == CUDA
+    assert norm_backward(lib, ws=BIG, wsb=1 << 30, dx=BIG + n - 256) == BAD
