@@ -173,13 +173,13 @@ void launch_conv_step(const void* x, int64_t ldx, const void* w, const void* b, 
 }
 
 gdn_status_t conv_check(const void* x, int64_t x_stride, const void* weight, const void* bias, const void* state,
-                        const int32_t* cu, int32_t num_seqs, int64_t T, int32_t D, int32_t W, gdn_dtype_t in,
-                        gdn_dtype_t wt)
+                        const int32_t* cu, const int32_t* status, int32_t num_seqs, int64_t T, int32_t D, int32_t W,
+                        gdn_dtype_t in, gdn_dtype_t wt)
 {
     if (num_seqs < 0 || T < 0 || T > kMaxRows || D <= 0 || W <= 0) return GDN_ERR_INVALID_ARG;
     if (!dtype_ok(in) || !dtype_ok(wt)) return GDN_ERR_INVALID_ARG;
     if (W < 2 || W > 4) return GDN_ERR_UNSUPPORTED;
-    if (cu == nullptr && num_seqs != 1) return GDN_ERR_INVALID_ARG;
+    if ((cu == nullptr && num_seqs != 1) || !aligned(cu, 4) || !aligned(status, 4)) return GDN_ERR_INVALID_ARG;
     if (T > 0 && !rows_ok(x, x_stride, D, in)) return GDN_ERR_INVALID_ARG;
     if (weight == nullptr || !aligned(weight, esize(wt)) || (bias && !aligned(bias, esize(wt))))
         return GDN_ERR_INVALID_ARG;
@@ -313,9 +313,9 @@ SsmWorkspace ssm_carve(void* base, int64_t T, int32_t N, int32_t D, int32_t G, i
     return w;
 }
 
-gdn_status_t ssm_check(const gdn_ssm_t* s, bool step)
+gdn_status_t ssm_check(const gdn_ssm_t* s, const int32_t* status, bool step)
 {
-    if (s == nullptr) return GDN_ERR_INVALID_ARG;
+    if (s == nullptr || !aligned(status, 4)) return GDN_ERR_INVALID_ARG;
     if (s->num_seqs < 0 || s->total_tokens < 0 || s->total_tokens > kMaxRows || s->channels <= 0 || s->groups <= 0 ||
         s->states <= 0 || s->channels % s->groups != 0)
         return GDN_ERR_INVALID_ARG;
@@ -323,7 +323,8 @@ gdn_status_t ssm_check(const gdn_ssm_t* s, bool step)
     if (s->states != 16 && s->states != 32 && s->states != 64) return GDN_ERR_UNSUPPORTED;
     if (s->A == nullptr || !aligned(s->A, 16)) return GDN_ERR_INVALID_ARG;
     if ((s->D && !aligned(s->D, 4)) || (s->dt_bias && !aligned(s->dt_bias, 4))) return GDN_ERR_INVALID_ARG;
-    if (step ? s->total_tokens != s->num_seqs : (s->cu_seqlens == nullptr && s->num_seqs != 1))
+    if (step ? s->total_tokens != s->num_seqs
+             : (s->cu_seqlens == nullptr && s->num_seqs != 1) || !aligned(s->cu_seqlens, 4))
         return GDN_ERR_INVALID_ARG;
     if (s->total_tokens > 0) {
         const int64_t bc = (int64_t)s->groups * s->states;
@@ -456,7 +457,7 @@ gdn_status_t gdn_conv_forward(const void* x, int64_t x_stride, const void* weigh
                               gdn_dtype_t in_dtype, gdn_dtype_t w_dtype, void* y, void* state_out, int32_t* status,
                               void* stream)
 {
-    const gdn_status_t bad = conv_check(x, x_stride, weight, bias, state_in, cu_seqlens, num_seqs, total_tokens,
+    const gdn_status_t bad = conv_check(x, x_stride, weight, bias, state_in, cu_seqlens, status, num_seqs, total_tokens,
                                         channels, width, in_dtype, w_dtype);
     if (bad != GDN_OK) return bad;
     if (num_seqs == 0) return GDN_OK;
@@ -507,7 +508,7 @@ gdn_status_t gdn_conv_backward(const void* x, int64_t x_stride, const void* weig
                                float* dweight, float* dbias, float* dstate_in, void* workspace,
                                size_t workspace_bytes, int32_t* status, void* stream)
 {
-    const gdn_status_t bad = conv_check(x, x_stride, weight, bias, state_in, cu_seqlens, num_seqs, total_tokens,
+    const gdn_status_t bad = conv_check(x, x_stride, weight, bias, state_in, cu_seqlens, status, num_seqs, total_tokens,
                                         channels, width, in_dtype, w_dtype);
     if (bad != GDN_OK) return bad;
     if (dweight == nullptr || !aligned(dweight, 16) || (dbias && !aligned(dbias, 16))) return GDN_ERR_INVALID_ARG;
@@ -565,7 +566,7 @@ gdn_status_t gdn_conv_step(const void* x, int64_t x_stride, const void* weight, 
 {
     static const int32_t none = 0;  // conv_check wants offsets for num_seqs != 1; the step reads none
     const gdn_status_t bad =
-        conv_check(x, x_stride, weight, bias, state, &none, num_seqs, num_seqs, channels, width, in_dtype, w_dtype);
+        conv_check(x, x_stride, weight, bias, state, &none, nullptr, num_seqs, num_seqs, channels, width, in_dtype, w_dtype);
     if (bad != GDN_OK) return bad;
     if (num_seqs == 0) return GDN_OK;
     if (state == nullptr || state_out == nullptr || !aligned(state_out, 16) || !rows_ok(y, channels, channels, in_dtype))
@@ -649,7 +650,8 @@ gdn_status_t gdn_layer_norm_backward(const void* x, int64_t x_stride, const void
         (dbias && !aligned(dbias, 4)))
         return GDN_ERR_INVALID_ARG;
     if (rows > 0 && (!rows_ok(x, x_stride, width, in_dtype) || !rows_ok(dy, dy_stride, width, in_dtype) ||
-                     !rows_ok(dx, width, width, in_dtype) || mean == nullptr || rstd == nullptr))
+                     !rows_ok(dx, width, width, in_dtype) || mean == nullptr || rstd == nullptr || !aligned(mean, 4) ||
+                     !aligned(rstd, 4)))
         return GDN_ERR_INVALID_ARG;
     const size_t es = esize(in_dtype);
     const size_t need = gdn_layer_norm_backward_workspace_size(rows, width);
@@ -723,7 +725,7 @@ size_t gdn_ssm_backward_workspace_size(int64_t total_tokens, int32_t num_seqs, i
 gdn_status_t gdn_ssm_forward(const gdn_ssm_t* args, const float* state_in, void* y, float* state_out,
                              float* chunk_states, int32_t* status, void* stream)
 {
-    const gdn_status_t bad = ssm_check(args, false);
+    const gdn_status_t bad = ssm_check(args, status, false);
     if (bad != GDN_OK) return bad;
     const gdn_ssm_t& s = *args;
     if (s.num_seqs == 0) return GDN_OK;
@@ -752,7 +754,7 @@ gdn_status_t gdn_ssm_backward(const gdn_ssm_t* args, const void* dy, int64_t dy_
                               void* dz, float* ddt_bias, float* dstate_in, void* workspace, size_t workspace_bytes,
                               int32_t* status, void* stream)
 {
-    const gdn_status_t bad = ssm_check(args, false);
+    const gdn_status_t bad = ssm_check(args, status, false);
     if (bad != GDN_OK) return bad;
     const gdn_ssm_t& s = *args;
     const int64_t T = s.num_seqs > 0 ? s.total_tokens : 0;
@@ -763,6 +765,7 @@ gdn_status_t gdn_ssm_backward(const gdn_ssm_t* args, const void* dy, int64_t dy_
         return GDN_ERR_INVALID_ARG;
     if (T > 0 && (!rows_ok(dy, dy_stride, s.channels, s.in_dtype) || !rows_ok(dx, s.channels, s.channels, s.in_dtype) ||
                   !rows_ok(ddt, s.channels, s.channels, s.in_dtype) || dB == nullptr || dC == nullptr ||
+                  !aligned(dB, esize(s.in_dtype)) || !aligned(dC, esize(s.in_dtype)) ||
                   (s.z != nullptr && !rows_ok(dz, s.channels, s.channels, s.in_dtype))))
         return GDN_ERR_INVALID_ARG;
     const size_t es = esize(s.in_dtype);
@@ -805,7 +808,7 @@ gdn_status_t gdn_ssm_backward(const gdn_ssm_t* args, const void* dy, int64_t dy_
 
 gdn_status_t gdn_ssm_step(const gdn_ssm_t* args, const float* state, float* state_out, void* y, void* stream)
 {
-    const gdn_status_t bad = ssm_check(args, true);
+    const gdn_status_t bad = ssm_check(args, nullptr, true);
     if (bad != GDN_OK) return bad;
     const gdn_ssm_t& s = *args;
     if (s.num_seqs == 0) return GDN_OK;

@@ -149,3 +149,22 @@ def test_the_workspace_is_what_the_call_needs(lib):
     n = lib.gdn_layer_norm_backward_workspace_size(4, 64)
     assert norm_backward(lib, ws=BIG, wsb=1 << 30, dx=BIG + n) == CUDA
     assert norm_backward(lib, ws=BIG, wsb=1 << 30, dx=BIG + n - 256) == BAD
+
+
+# alignment that each address needs (bf16 tokens and weights): what the kernels read in one access
+ALIGNMENT = [(conv_forward, dict(cu=4, st=4, x=2, w=2, b=2, y=2, s=16, so=16)),
+             (conv_backward, dict(cu=4, st=4, x=2, dy=2, w=2, b=2, dx=2, s=16, do=16, dw=16, db=16, ds=16, ws=256)),
+             (conv_step, dict(x=2, w=2, b=2, y=2, so=16)),
+             (norm_forward, dict(x=2, w=2, b=2, y=2, m=4, r=4)),
+             (norm_backward, dict(x=2, dy=2, w=2, m=4, r=4, dx=2, dw=4, db=4, ws=256)),
+             (ssm_forward, dict(x=2, dt=2, B=2, C=2, z=2, A=16, D=4, dt_bias=4, cu=4, si=16, y=2, so=16, cs=16, st=4)),
+             (ssm_backward, dict(x=2, dt=2, B=2, C=2, z=2, A=16, D=4, dt_bias=4, cu=4, dy=2, cs=16, do=16, dx=2, ddt=2, dA=4,
+                                 dB=2, dC=2, dD=4, dz=2, db=4, ds=16, ws=256, st=4)),
+             (ssm_step, dict(x=2, dt=2, B=2, C=2, z=2, A=16, D=4, dt_bias=4, y=2, so=16))]
+
+
+@pytest.mark.parametrize("call,name,n", [(c, k, n) for c, a in ALIGNMENT for k, n in a.items()],
+                         ids=[f"{c.__name__}-{k}" for c, a in ALIGNMENT for k in a])
+def test_misaligned_addresses_are_refused(lib, call, name, n):
+    assert call(lib, **{name: BIG + n // 2}) == BAD
+    assert call(lib, **{name: BIG + n}) == CUDA
