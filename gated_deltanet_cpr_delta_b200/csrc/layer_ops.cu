@@ -21,7 +21,9 @@ namespace {
 using gdn::Seqs;
 
 constexpr size_t kAlign = 256;
-constexpr int64_t kMaxRows = INT32_MAX - 4096;  // the kernels count rows, and a few beyond the end, in 32 bits
+// The kernels count rows, the columns of the norm and the channels of the scan, and a block's worth beyond
+// the end, in 32 bits.
+constexpr int64_t kMaxRows = INT32_MAX - 4096;
 
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -316,8 +318,8 @@ SsmWorkspace ssm_carve(void* base, int64_t T, int32_t N, int32_t D, int32_t G, i
 gdn_status_t ssm_check(const gdn_ssm_t* s, const int32_t* status, bool step)
 {
     if (s == nullptr || !aligned(status, 4)) return GDN_ERR_INVALID_ARG;
-    if (s->num_seqs < 0 || s->total_tokens < 0 || s->total_tokens > kMaxRows || s->channels <= 0 || s->groups <= 0 ||
-        s->states <= 0 || s->channels % s->groups != 0)
+    if (s->num_seqs < 0 || s->total_tokens < 0 || s->total_tokens > kMaxRows || s->channels <= 0 ||
+        s->channels > kMaxRows || s->groups <= 0 || s->states <= 0 || s->channels % s->groups != 0)
         return GDN_ERR_INVALID_ARG;
     if (!dtype_ok(s->in_dtype)) return GDN_ERR_INVALID_ARG;
     if (s->states != 16 && s->states != 32 && s->states != 64) return GDN_ERR_UNSUPPORTED;
@@ -431,7 +433,7 @@ template <typename T, int S>
 gdn_status_t ssm_step_launch(const gdn::SsmArgs& a, cudaStream_t st)
 {
     const unsigned across = (unsigned)ceil_div(a.D, 1024 / S);
-    for (int n = 0; n < a.s.N; n += 65535) {  // a grid has at most 65535 rows
+    for (int64_t n = 0; n < a.s.N; n += 65535) {  // a grid has at most 65535 rows
         gdn::SsmArgs b = a;
         const int64_t es = sizeof(T), per = (int64_t)a.D * S;
         b.x = static_cast<const char*>(a.x) + n * a.ldx * es;
@@ -442,7 +444,7 @@ gdn_status_t ssm_step_launch(const gdn::SsmArgs& a, cudaStream_t st)
         b.state_in = a.state_in + n * per;
         b.state_out = a.state_out + n * per;
         b.y = static_cast<char*>(a.y) + n * (int64_t)a.D * es;
-        gdn::k_ssm_step<T, S><<<dim3(across, (unsigned)std::min(65535, a.s.N - n)), 256, 0, st>>>(b);
+        gdn::k_ssm_step<T, S><<<dim3(across, (unsigned)std::min<int64_t>(65535, a.s.N - n)), 256, 0, st>>>(b);
     }
     return launched() ? GDN_OK : GDN_ERR_CUDA;
 }
@@ -595,7 +597,7 @@ gdn_status_t gdn_layer_norm_forward(const void* x, int64_t x_stride, const void*
                                     int64_t rows, int32_t width, gdn_dtype_t in_dtype, gdn_dtype_t w_dtype, void* y,
                                     float* mean, float* rstd, void* stream)
 {
-    if (rows < 0 || rows > kMaxRows || width <= 0 || !(eps >= 0.0f) || !dtype_ok(in_dtype) || !dtype_ok(w_dtype))
+    if (rows < 0 || rows > kMaxRows || width <= 0 || width > kMaxRows || !(eps >= 0.0f) || !dtype_ok(in_dtype) || !dtype_ok(w_dtype))
         return GDN_ERR_INVALID_ARG;
     if (weight == nullptr || !aligned(weight, esize(w_dtype)) || (bias && !aligned(bias, esize(w_dtype))))
         return GDN_ERR_INVALID_ARG;
@@ -644,7 +646,7 @@ gdn_status_t gdn_layer_norm_backward(const void* x, int64_t x_stride, const void
                                      float* dweight, float* dbias, void* workspace, size_t workspace_bytes,
                                      void* stream)
 {
-    if (rows < 0 || rows > kMaxRows || width <= 0 || !dtype_ok(in_dtype) || !dtype_ok(w_dtype))
+    if (rows < 0 || rows > kMaxRows || width <= 0 || width > kMaxRows || !dtype_ok(in_dtype) || !dtype_ok(w_dtype))
         return GDN_ERR_INVALID_ARG;
     if (weight == nullptr || !aligned(weight, esize(w_dtype)) || dweight == nullptr || !aligned(dweight, 4) ||
         (dbias && !aligned(dbias, 4)))

@@ -471,7 +471,8 @@ gdn_status_t gdn_cpr_forward_noalloc(const void* q, const void* k, const void* v
  *    give the same bits.  Inputs that are not finite spread within the rows (norm)
  *    or sequences (convolution, scan) and channels they belong to, and into the
  *    gradients of the parameters; in the scan an infinity may turn into NaN.
- *  - total_tokens and rows are below 2^31 - 4096; offsets of elements take 64 bits.
+ *  - total_tokens, rows, the norm's width and the scan's channels are below 2^31 - 4096; offsets of
+ *    elements take 64 bits.
  */
 
 /*

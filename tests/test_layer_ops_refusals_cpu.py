@@ -168,3 +168,14 @@ ALIGNMENT = [(conv_forward, dict(cu=4, st=4, x=2, w=2, b=2, y=2, s=16, so=16)),
 def test_misaligned_addresses_are_refused(lib, call, name, n):
     assert call(lib, **{name: BIG + n // 2}) == BAD
     assert call(lib, **{name: BIG + n}) == CUDA
+
+
+@pytest.mark.parametrize("call,name,ld", [(norm_forward, "D", ("ldx",)), (norm_backward, "D", ("ldx", "ldg")),
+                                          (ssm_forward, "D_", ("ldx", "lddt", "ldz")), (ssm_backward, "D_", ("ldx", "lddt", "ldz", "ldg")),
+                                          (ssm_step, "D_", ("ldx", "lddt", "ldz"))])
+def test_widths_beyond_the_counters_are_refused(lib, call, name, ld):
+    """The kernels count columns, and a block's worth beyond the last, in 32 bits."""
+    far = {k: (i + 1) << 50 for i, k in enumerate(dict(OVERLAPS[call][0], **OVERLAPS[call][1]))}
+    far.update({"s": 60 << 50} if call is ssm_step else {}, **({"wsb": 1 << 50} if "ws" in far else {}))
+    for width, want in ((2 ** 31 - 4098, CUDA), (2 ** 31 - 4096, BAD), (2 ** 31 - 2, BAD)):
+        assert call(lib, **dict(far, **{name: width, **{k: width for k in ld}})) == want, width
