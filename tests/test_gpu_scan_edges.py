@@ -50,3 +50,37 @@ def test_saved_states_and_gradients_of_wide_batches(dtype, S, D, G):
     for name, t in zip(SSM_GRADS, got):
         close(name, t, want[name], M[name], K + (D // G if name in ("dB", "dC") else len(wy)))
         near(name, t, want[name])
+
+
+def softplus_case(dt):
+    """States of single tokens from zero with x = B = 1: the state is the step width itself."""
+    N, D = dt.shape
+    one = lambda *s: torch.ones(*s, device="cuda")  # noqa: E731
+    A, B = -one(D, 16), one(N, 1, 16)
+    state = torch.zeros(N, D, 16, device="cuda")
+    gdn.gdn_ssm_step(one(N, D), dt, A, B, B, state)
+    cu = torch.arange(N + 1, dtype=torch.int32, device="cuda")
+    return state, gdn.gdn_ssm_forward(one(N, D), dt, A, B, B, cu)[1]
+
+
+@pytest.mark.parametrize("D", [4096, 96])
+def test_step_widths_are_accurate_relative_to_their_value(D):
+    """softplus over [-20, 5], where step widths lie.  In units of 2^-24: e^-|v| is off by 2.5 (2^x in one
+    instruction), 0.9 (ln 2 rounded, times |v|) and 1; log1p's polynomial by 0.6 and, relative to its smallest
+    value ln 2, 3 of its roundings; the result by 1: 9 in all."""
+    dt = torch.linspace(-20, 5, 64 * D, device="cuda").view(64, D)
+    v = dt.double().cpu().numpy()
+    want = np.maximum(v, 0) + np.log1p(np.exp(-np.abs(v)))
+    for got in softplus_case(dt):
+        got = got.double().cpu().numpy()
+        assert (got == got[:, :, :1]).all()
+        assert np.abs(got[:, :, 0] / want - 1).max() <= 9 * 2.0 ** -24
+
+
+def test_step_widths_at_the_ends():
+    inf, nan = float("inf"), float("nan")
+    dt = torch.tensor([[-inf, -3e38, -1e5, -200, -104, -88, 0, 88, 104, 200, 1e5, 3e38, inf, nan]], device="cuda")
+    got = softplus_case(dt)[0][0, :, 0].cpu()
+    want = torch.tensor([0, 0, 0, 0, 0, 0, np.log(2), 88, 104, 200, 1e5, 3e38, inf, nan], dtype=torch.float32)
+    assert torch.equal(got[7:13], want[7:13]) and got[13].isnan()
+    assert (got[:6].abs() <= 2.0 ** -126).all() and abs(got[6] - want[6]) <= 9 * 2.0 ** -24
