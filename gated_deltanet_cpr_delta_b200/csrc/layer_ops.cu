@@ -379,9 +379,19 @@ template <typename T, int S, int V>
 gdn_status_t ssm_forward_launch(const gdn::SsmArgs& a, cudaStream_t st)
 {
     // Tiles of 64 tokens (8 segments, 4 channels per warp) or of 128 (16 segments, 2 channels per
-    // warp, twice the warps).  Measured at 16 states: N D = 8192: 337 against 344 us; 7000: 173
-    // against 122; 4096: 271 against 234; 1024 (32 states): 27 against 19.
-    if ((int64_t)a.s.N * a.D >= 16 * 1024) return ssm_forward_seg<T, S, V, 8>(a, st);
+    // warp: twice the blocks, half the steps of a sequence, more shared memory).  16 where its
+    // blocks take at most three rounds of those that are resident.  Measured, 8 against 16 segments, bf16:
+    //   1 sequence x 2048 tokens x 1024 channels (0.2, 0.3 and 0.9 rounds at 16, 32 and 64 states):
+    //     96 against 57, 160 against 94, 293 against 176 us
+    //   4 x 2048 x 2048 (1.7, 2.3, 6.9): 176 against 181, 307 against 358, 733 against 1180 us
+    //   8 x 2048 x 2048 (3.5, 4.6, 13.8): 303 against 344, 528 against 657, 1356 against 2348 us
+    // The lengths are not known here.  In ragged batches the longest sequence counts, which 16 segments walk faster: 9
+    // sequences of 1 to 1500 tokens x 777 channels (1.5, 2.0, 6.0): 152 against 99, 287 against 160, 434 against 447 us.
+    const int sms = sm_count();
+    if (sms == 0) return GDN_ERR_CUDA;
+    using Cf = gdn::SsmFwdCfg<T, S, 16>;
+    constexpr int64_t per_sm = std::min<int64_t>(4, 228 * 1024 / (Cf::BYTES + 1024));  // 4: launch bounds
+    if ((int64_t)a.s.N * a.G * ceil_div(a.Dg, Cf::CB) > 3 * per_sm * sms) return ssm_forward_seg<T, S, V, 8>(a, st);
     return ssm_forward_seg<T, S, V, 16>(a, st);
 }
 
