@@ -132,3 +132,17 @@ def test_constant_rows(dtype, form, D):
     My, Mx, _, _ = ops.layer_norm_bounds(x64[keep], w64, dy64[keep], 0.0)
     close("y", y[keep], wy, My + np.abs(b64), 2 * depth(D) + 12)
     close("dx", dx[keep], ops.layer_norm_backward(x64[keep], w64, dy64[keep], 0.0)[0], Mx, 6 * depth(D) + 32)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_gradients_per_head(dtype):
+    """[tokens, heads, d]: the values of dx, and dw and db summed over tokens and heads."""
+    t = TYPES[dtype]
+    rng = np.random.default_rng(9)
+    (x, x64), (dy, dy64), (w, w64) = make(rng, t, 50, 6, 32), make(rng, t, 50, 6, 32), make(rng, t, 32)
+    _, mean, rstd = gdn.gdn_layer_norm_forward(x, w)
+    got = gdn.gdn_layer_norm_backward(x, w, dy, mean, rstd)
+    assert got[0].shape == x.shape
+    a = (x64.reshape(300, 32), w64, dy64.reshape(300, 32))
+    for name, g, want, m in zip(("dx", "dw", "db"), got, ops.layer_norm_backward(*a), ops.layer_norm_bounds(*a)[1:]):
+        close(name, g.view(want.shape), want, m, 6 * 28 + 32 + (176 if name != "dx" else 0))
