@@ -5,15 +5,16 @@
 // and with g = dy w:
 //     dx = rstd (g - sum g / D - n sum(g n) / D),  dw = sum_rows dy n,  db = sum_rows dy
 //
-// Bound by memory: one read of x (and dy), one write.  A row stays in the
+// One read of x (and dy), one write; bound by the latency of memory and of the rows' sums, with DRAM at
+// 43% (forward) and 58% of its peak.  A row stays in the
 // registers of `tpr` threads (NV vectors of V elements each), so the variance
 // is the second moment about the mean, exact to fp32 also for rows whose mean
 // is large, without a second read.  Measured on a B200 (bf16): 16384 x 4096 forward
 // 59 us, 4.5 TB/s, gradients 78 us, 5.2 TB/s, + 5 us for the sums of dw and db;
 // 262144 rows of 128 30 us, 4.5 TB/s (there a row's two sums over 16 lanes
 // bind it as much as the memory); 64 x 4096 3.5 us.  Dense rows of odd widths are read
-// in 16-byte vectors that start off the row (SHIFT): 8192 x 4097 forward 60 us, gradients 84 us
-// (8192 x 4096: 31 and 51 us; element by element 164 and 154 us).
+// in 16-byte vectors that start off the row (SHIFT): 8192 x 4097 forward 60 us, gradients 85 us,
+// 82 of them in k_norm_bwd (8192 x 4096: 30, 52 and 47 us; element by element 164 and 154 us).
 #pragma once
 
 #include "layer_common.cuh"
@@ -151,8 +152,7 @@ struct NormRing {
 // within a vector, but rows V apart start alike: with a stride of a multiple of V
 // rows, a thread's vectors cover the same columns in every row.  They start m columns before the row, so
 // that they are aligned; the first may hold the end of the row before (cleared), the
-// last stops at the row's end.  (Element by element the forward took 164 us, not 32, at
-// 8192 x 4097 bf16.)
+// last stops at the row's end.  (8192 x 4097 bf16: 60 us forward, element by element 164.)
 template <typename T, int V>
 struct NormCols {
     int c0, step, D;  // vector i covers the columns c0 + i step ..

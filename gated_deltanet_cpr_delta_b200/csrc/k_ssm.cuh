@@ -13,11 +13,13 @@
 // written once: 64 x 4096 x 16 in 8.9 us, 4.0 TB/s).  Measured on a B200 for 4 x 4096
 // tokens x 2048 channels x 16 states (bf16): 345 us, where the exponentials alone
 // take 115 us and the bytes 42 us.  It issues 13 instructions per (token, channel,
-// state) at 55% of the issue slots: 8 in the loop over the states, the rest for the
+// state) at 56% of the issue slots: 8 in the loop over the states, the rest for the
 // step width, the gate, the staging and the joining of the segments.  Before it: two passes
 // over chunks of time, every exponential made twice, 1022 us; this form with two
 // channels per lane (168 registers, 12 warps per SM) 450 us.  Rows that are not whole 16
-// bytes are staged element by element: 8192 tokens x 4096 channels 390 us, x 4097 512 us.
+// bytes are staged element by element: 8192 tokens x 4096 channels 390 us, x 4097 517 us.
+// 4 x 2048 tokens x 2048 channels: 175, 353 and 729 us at 16, 32 and 64 states.  A block walks its
+// sequence alone: one of 32768 tokens takes 780 us at 64 channels as at 1024.
 #pragma once
 
 #include "layer_common.cuh"

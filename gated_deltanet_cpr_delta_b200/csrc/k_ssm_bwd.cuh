@@ -25,12 +25,13 @@
 //
 // Bound by instructions and their latency: 30 per (token, channel, state) in k_ssm_bwd, at
 // half of the issue slots with 12 warps per SM (168 registers, 72 KB).  Measured on a B200 for
-// 2 x 4096 tokens x 2048 channels x 16 states (bf16): k_ssm_rev 106 us, k_ssm_bwd_pass
-// 8 us, k_ssm_bwd 444 us, the sums 24 us; the exponentials (three per element) take
+// 2 x 4096 tokens x 2048 channels x 16 states (bf16): k_ssm_rev 107 us, k_ssm_bwd_pass
+// 7 us, k_ssm_bwd 449 us, the sums 24 us; the exponentials (three per element) take
 // 173 us of that.  The forward's form (time segments in lanes, each exponential made
 // once, the channels in a loop) took 718 us in place of the three: as many instructions,
 // and half the warps.  Rows that are not whole 16 bytes load element by element:
-// 8192 tokens x 4096 channels 1170 us in all, x 4097 1620 us.
+// 8192 tokens x 4096 channels 1190 us in all, x 4097 1620 us.  4 x 2048 x 2048: 584, 1198 and 3051 us at 16, 32
+// and 64 states.
 #pragma once
 
 #include "k_ssm.cuh"

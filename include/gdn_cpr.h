@@ -455,8 +455,9 @@ gdn_status_t gdn_cpr_forward_noalloc(const void* q, const void* k, const void* v
  *    of one projection's output: `*_stride` is the distance between tokens in
  *    elements (at least the row's width, below 2^31).  They need the alignment of one
  *    element only; rows whose width, stride and address are multiples of 16 bytes
- *    are read in 16-byte accesses.  Outputs are dense.  States, parameters in fp32 and
- *    gradients of either are 16-byte aligned.
+ *    are read in 16-byte accesses.  Outputs are dense.  States, their gradients, the scan's A and
+ *    chunk states and the gradients of the convolution's parameters are 16-byte aligned; every
+ *    other address needs the alignment of its element.
  *  - cu_seqlens is read on the device only, so that a captured graph can be
  *    replayed with other lengths: 0 <= cu[0], non-decreasing, cu[num_seqs] <=
  *    total_tokens.  NULL stands for one sequence of total_tokens rows (num_seqs = 1).
@@ -577,6 +578,9 @@ gdn_status_t gdn_ssm_step(const gdn_ssm_t* args, const float* state, float* stat
  * Layer norm of each row of x [rows, width]:
  *   y = (x - mean) rstd weight + bias,  rstd = (mean((x - mean)^2) + eps)^(-1/2)
  * weight and bias (NULL: none) [width] in w_dtype; y in in_dtype; mean, rstd [rows] fp32.
+ * The squares of x - mean are summed in fp32: sums above 3e38 (a spread of 1e18 at a width of 100) give
+ * rstd = 0, and without an eps that covers them spreads below 1e-18 lose digits.  A constant row with
+ * eps = 0 is not a number.
  * The backward gives the gradients of sum(dy y): dx in in_dtype, dweight and dbias (NULL: not
  * wanted) fp32, summed over the rows.
  */
