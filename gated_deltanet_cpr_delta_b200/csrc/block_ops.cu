@@ -1,0 +1,297 @@
+// block_ops.cu -- host side of the norm of queries and keys with the position rotation, and of
+// the clipped policy loss (gdn_cpr.h).
+//
+// As layer_ops.cu: it validates on the host, carves the caller's workspace and
+// enqueues on the caller's stream; it allocates nothing, keeps no state and
+// never synchronises.
+#include "layer_host.cuh"
+#include "k_policy.cuh"
+#include "k_qknorm.cuh"
+
+#include <cmath>
+
+namespace {
+
+// ------------------------------------------------------------- norm of queries and keys
+
+gdn_status_t qk_check(const gdn_qk_norm_t* s)
+{
+    if (s == nullptr || s->tokens < 0 || s->tokens > kMaxRows || s->q_heads <= 0 || s->k_heads <= 0 || s->head_dim <= 0 ||
+        s->rot_dim < 0 || s->rot_dim > s->head_dim || !(s->eps >= 0.0f) || !dtype_ok(s->in_dtype) || !dtype_ok(s->w_dtype))
+        return GDN_ERR_INVALID_ARG;
+    if (s->head_dim % 2 != 0 || s->rot_dim % 2 != 0 || s->head_dim > 256) return GDN_ERR_UNSUPPORTED;
+    const size_t ws = esize(s->w_dtype);
+    if ((s->q_weight && !aligned(s->q_weight, ws)) || (s->k_weight && !aligned(s->k_weight, ws))) return GDN_ERR_INVALID_ARG;
+    if (s->rot_dim > 0 && (s->inv_freq == nullptr || !aligned(s->inv_freq, 4))) return GDN_ERR_INVALID_ARG;
+    const int64_t heads = (int64_t)s->q_heads + s->k_heads;
+    if (heads * s->head_dim > INT32_MAX) return GDN_ERR_INVALID_ARG;
+    if (s->tokens == 0) return GDN_OK;
+    if (s->rot_dim > 0 && (s->positions == nullptr || !aligned(s->positions, 4))) return GDN_ERR_INVALID_ARG;
+    if (!rows_ok(s->q, s->q_stride, (int64_t)s->q_heads * s->head_dim, s->in_dtype) ||
+        !rows_ok(s->k, s->k_stride, (int64_t)s->k_heads * s->head_dim, s->in_dtype))
+        return GDN_ERR_INVALID_ARG;
+    return GDN_OK;
+}
+
+// Whether a thread's four pairs of a row are two accesses of four elements.
+bool qk_vectors(const gdn_qk_norm_t* s, const void* p, int64_t stride)
+{
+    const size_t bytes = 4 * esize(s->in_dtype);
+    return aligned(p, bytes) && stride % 4 == 0 && s->head_dim % 8 == 0 && (s->interleaved || s->rot_dim % 8 == 0);
+}
+
+// Lanes of a row: a power of two that covers its pairs, four per lane.
+int qk_lanes(int32_t d)
+{
+    int n = 1;
+    while (n * 8 < d) n *= 2;
+    return n;
+}
+
+// Tokens that a block takes at a time: enough rows for each of its threads to have several in flight, few
+// enough that every SM has blocks, and with angles that fit 24 KB.
+int qk_tokens(const gdn_qk_norm_t* s, int tpr, int sms)
+{
+    const int64_t rows = (int64_t)(gdn::kQkThreads / tpr) * gdn::qk_rows(false) * 2, heads = (int64_t)s->q_heads + s->k_heads;
+    int64_t n = ceil_div(rows, heads);
+    n = std::min(n, ceil_div(s->tokens, (int64_t)sms * 4));
+    if (s->rot_dim > 0) n = std::min<int64_t>(n, 24 * 1024 / (4 * s->rot_dim));
+    return (int)std::max<int64_t>(1, n);
+}
+
+constexpr int kQkParts = 1024;  // most blocks of the backward
+
+size_t qk_smem(const gdn::QkArgs& a, bool bwd)
+{
+    return sizeof(float2) * (size_t)a.tokens * (a.rot / 2) + sizeof(float) * (bwd ? gdn::kQkThreads / 32 : 2) * a.d;
+}
+
+template <typename T, bool VEC, bool BWD>
+gdn_status_t qk_launch(const gdn::QkArgs& a, unsigned blocks, cudaStream_t st)
+{
+    gdn::k_qk_norm<T, VEC, BWD><<<blocks, gdn::kQkThreads, qk_smem(a, BWD), st>>>(a);
+    return launched() ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn::QkArgs qk_args(const gdn_qk_norm_t* s, int sms)
+{
+    gdn::QkArgs a{};
+    a.x[0] = s->q; a.x[1] = s->k; a.ldx[0] = s->q_stride; a.ldx[1] = s->k_stride;
+    a.w[0] = s->q_weight; a.w[1] = s->k_weight; a.H[0] = s->q_heads; a.H[1] = s->k_heads;
+    a.w_bf16 = s->w_dtype == GDN_BF16; a.interleaved = s->interleaved != 0;
+    a.pos = s->positions; a.freq = s->inv_freq; a.eps = s->eps;
+    a.inv_n = s->unit ? 1.0f : 1.0f / (float)s->head_dim;
+    a.T = s->tokens; a.d = s->head_dim; a.rot = s->rot_dim; a.tpr = qk_lanes(s->head_dim);
+    a.tokens = qk_tokens(s, a.tpr, sms);
+    return a;
+}
+
+// ------------------------------------------------------------- policy loss
+
+gdn_status_t policy_check(const gdn_policy_t* s, const int32_t* status)
+{
+    if (s == nullptr || s->rows < 0 || s->rows > kMaxRows || s->vocab <= 0 || !dtype_ok(s->in_dtype) || !aligned(status, 4))
+        return GDN_ERR_INVALID_ARG;
+    if (!(s->temperature > 0.0f) || std::isinf(s->temperature)) return GDN_ERR_INVALID_ARG;
+    if ((s->old_logprob == nullptr) != (s->advantages == nullptr) || (s->ref_logprob && !s->old_logprob))
+        return GDN_ERR_INVALID_ARG;
+    if (s->old_logprob && (!(s->clip_low >= 0.0f) || !(s->clip_low <= 1.0f) || !(s->clip_high >= 0.0f) || std::isnan(s->kl_coef)))
+        return GDN_ERR_INVALID_ARG;
+    if ((int64_t)s->vocab * (int64_t)esize(s->in_dtype) > gdn::kPolicyMaxBytes) return GDN_ERR_UNSUPPORTED;
+    if (!aligned(s->old_logprob, 4) || !aligned(s->ref_logprob, 4) || !aligned(s->advantages, 4)) return GDN_ERR_INVALID_ARG;
+    if (s->rows == 0) return GDN_OK;
+    if (!rows_ok(s->logits, s->logits_stride, s->vocab, s->in_dtype) || s->targets == nullptr || !aligned(s->targets, 8))
+        return GDN_ERR_INVALID_ARG;
+    return GDN_OK;
+}
+
+struct PolicyPlan {
+    int cluster, threads;
+    size_t smem;
+};
+
+// How a row is cut, by its bytes alone (the log-probabilities' bits follow from it): one block up to
+// 32 KB, then a cluster of 2, 4 or 8 blocks, each with a slice of whole 16-byte vectors,
+// kPolicyVecs of them per thread.
+PolicyPlan policy_plan(gdn::PolicyArgs& a, gdn_dtype_t t)
+{
+    const int64_t bytes = (int64_t)a.V * (int64_t)esize(t);
+    const int E = 16 / (int)esize(t);
+    PolicyPlan p;
+    p.cluster = 1;
+    while (p.cluster < gdn::kPolicyMaxCluster && bytes > (int64_t)p.cluster * 32 * 1024) p.cluster *= 2;
+    const int64_t vecs = ceil_div(ceil_div(a.V, E), p.cluster);  // of a slice
+    a.slice = (int32_t)(vecs * E);
+    p.threads = (int)std::max<int64_t>(64, ceil_div(ceil_div(vecs, gdn::kPolicyVecs), 32) * 32);
+    p.smem = 16 * (size_t)(vecs + 2);
+    return p;
+}
+
+template <typename T, bool BWD>
+gdn_status_t policy_launch(gdn::PolicyArgs& a, gdn_dtype_t t, cudaStream_t st)
+{
+    const PolicyPlan p = policy_plan(a, t);
+    const int sms = sm_count();
+    if (sms == 0) return GDN_ERR_CUDA;
+    auto k = gdn::k_policy<T, BWD>;
+    if (!raise_smem(k, p.smem)) return GDN_ERR_CUDA;
+    const int per_sm = (int)std::min<size_t>(1024 / p.threads, (size_t)(220 * 1024) / (p.smem + 2048));
+    const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(a.T, (int64_t)sms * std::max(1, per_sm) / p.cluster));
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(clusters * p.cluster));
+    cfg.blockDim = dim3((unsigned)p.threads);
+    cfg.dynamicSmemBytes = p.smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)p.cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, (const gdn::PolicyArgs&)a) == cudaSuccess && launched() ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn::PolicyArgs policy_args(const gdn_policy_t* s, int32_t* status)
+{
+    gdn::PolicyArgs a{};
+    a.z = s->logits; a.ldz = s->logits_stride; a.y = s->targets;
+    a.old = s->old_logprob; a.ref = s->ref_logprob; a.adv = s->advantages;
+    a.lo = 1.0f - s->clip_low; a.hi = 1.0f + s->clip_high; a.kl = s->kl_coef;
+    a.c = (float)(1.4426950408889634 / (double)s->temperature); a.inv_tau = (float)(1.0 / (double)s->temperature);
+    a.T = s->rows; a.V = s->vocab; a.status = status;
+    return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+gdn_status_t gdn_qk_norm_forward(const gdn_qk_norm_t* args, void* q_out, void* k_out, void* stream)
+{
+    const gdn_status_t bad = qk_check(args);
+    if (bad != GDN_OK) return bad;
+    const gdn_qk_norm_t& s = *args;
+    if (s.tokens == 0) return GDN_OK;
+    const int64_t T = s.tokens, wq = (int64_t)s.q_heads * s.head_dim, wk = (int64_t)s.k_heads * s.head_dim;
+    if (!rows_ok(q_out, wq, wq, s.in_dtype) || !rows_ok(k_out, wk, wk, s.in_dtype)) return GDN_ERR_INVALID_ARG;
+    const size_t es = esize(s.in_dtype), ws = esize(s.w_dtype);
+    if (overlap({{q_out, T * wq, es}, {k_out, T * wk, es}},
+                {{s.q, T, s.q_stride, wq, es}, {s.k, T, s.k_stride, wk, es}, {s.q_weight, s.head_dim, ws},
+                 {s.k_weight, s.head_dim, ws}, {s.rot_dim ? s.positions : nullptr, T, 4},
+                 {s.rot_dim ? s.inv_freq : nullptr, s.rot_dim / 2, 4}}))
+        return GDN_ERR_INVALID_ARG;
+    const int sms = sm_count();
+    if (sms == 0) return GDN_ERR_CUDA;
+    gdn::QkArgs a = qk_args(args, sms);
+    a.out[0] = q_out; a.out[1] = k_out;
+    const unsigned blocks = (unsigned)ceil_div(T, a.tokens);
+    const bool vec = qk_vectors(args, s.q, s.q_stride) && qk_vectors(args, s.k, s.k_stride) &&
+                     qk_vectors(args, q_out, wq) && qk_vectors(args, k_out, wk);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (s.in_dtype == GDN_BF16)
+        return vec ? qk_launch<__nv_bfloat16, true, false>(a, blocks, st) : qk_launch<__nv_bfloat16, false, false>(a, blocks, st);
+    return vec ? qk_launch<float, true, false>(a, blocks, st) : qk_launch<float, false, false>(a, blocks, st);
+}
+
+size_t gdn_qk_norm_backward_workspace_size(int64_t tokens, int32_t head_dim)
+{
+    if (tokens < 0 || head_dim <= 0) return 0;
+    return align_up(sizeof(float) * 2 * (size_t)std::max<int64_t>(1, std::min<int64_t>(tokens, kQkParts)) * head_dim);
+}
+
+gdn_status_t gdn_qk_norm_backward(const gdn_qk_norm_t* args, const void* dq_out, int64_t dq_out_stride, const void* dk_out,
+                                  int64_t dk_out_stride, void* dq, void* dk, float* dq_weight, float* dk_weight,
+                                  void* workspace, size_t workspace_bytes, void* stream)
+{
+    const gdn_status_t bad = qk_check(args);
+    if (bad != GDN_OK) return bad;
+    const gdn_qk_norm_t& s = *args;
+    const int64_t T = s.tokens, wq = (int64_t)s.q_heads * s.head_dim, wk = (int64_t)s.k_heads * s.head_dim;
+    const bool weights = dq_weight != nullptr || dk_weight != nullptr;
+    if (!aligned(dq_weight, 4) || !aligned(dk_weight, 4) || (dq_weight && !s.q_weight) || (dk_weight && !s.k_weight))
+        return GDN_ERR_INVALID_ARG;
+    if (T > 0 && (!rows_ok(dq_out, dq_out_stride, wq, s.in_dtype) || !rows_ok(dk_out, dk_out_stride, wk, s.in_dtype) ||
+                  !rows_ok(dq, wq, wq, s.in_dtype) || !rows_ok(dk, wk, wk, s.in_dtype)))
+        return GDN_ERR_INVALID_ARG;
+    const size_t es = esize(s.in_dtype), ws = esize(s.w_dtype);
+    const size_t need = weights ? gdn_qk_norm_backward_workspace_size(T, s.head_dim) : 0;
+    if (overlap({{dq, T * wq, es}, {dk, T * wk, es}, {dq_weight, s.head_dim, 4}, {dk_weight, s.head_dim, 4},
+                 {workspace, (int64_t)need, 1}},
+                {{s.q, T, s.q_stride, wq, es}, {s.k, T, s.k_stride, wk, es}, {dq_out, T, dq_out_stride, wq, es},
+                 {dk_out, T, dk_out_stride, wk, es}, {s.q_weight, s.head_dim, ws}, {s.k_weight, s.head_dim, ws},
+                 {s.rot_dim ? s.positions : nullptr, T, 4}, {s.rot_dim ? s.inv_freq : nullptr, s.rot_dim / 2, 4}}))
+        return GDN_ERR_INVALID_ARG;
+    if (weights && (workspace == nullptr || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
+    if (weights && !aligned(workspace, kAlign)) return GDN_ERR_INVALID_ARG;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int64_t parts = 0;
+    float* part = weights ? static_cast<float*>(workspace) : nullptr;
+    if (T > 0) {
+        const int sms = sm_count();
+        if (sms == 0) return GDN_ERR_CUDA;
+        gdn::QkArgs a = qk_args(args, sms);
+        a.dy[0] = dq_out; a.dy[1] = dk_out; a.lddy[0] = dq_out_stride; a.lddy[1] = dk_out_stride;
+        a.out[0] = dq; a.out[1] = dk; a.part = part;
+        parts = std::min<int64_t>(ceil_div(T, a.tokens), std::min<int64_t>(kQkParts, (int64_t)sms * 4));
+        const bool vec = qk_vectors(args, s.q, s.q_stride) && qk_vectors(args, s.k, s.k_stride) &&
+                         qk_vectors(args, dq_out, dq_out_stride) && qk_vectors(args, dk_out, dk_out_stride) &&
+                         qk_vectors(args, dq, wq) && qk_vectors(args, dk, wk);
+        gdn_status_t r;
+        if (s.in_dtype == GDN_BF16)
+            r = vec ? qk_launch<__nv_bfloat16, true, true>(a, (unsigned)parts, st)
+                    : qk_launch<__nv_bfloat16, false, true>(a, (unsigned)parts, st);
+        else
+            r = vec ? qk_launch<float, true, true>(a, (unsigned)parts, st) : qk_launch<float, false, true>(a, (unsigned)parts, st);
+        if (r != GDN_OK) return r;
+    }
+    if (!weights) return GDN_OK;
+    const int64_t M = 2 * (int64_t)s.head_dim;
+    gdn::k_colsum<<<(unsigned)ceil_div(M, 32), dim3(32, 8), 0, st>>>(part, parts, M,
+                                                                     gdn::QkGradMap{dq_weight, dk_weight, s.head_dim});
+    return launched() ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn_status_t gdn_policy_loss_forward(const gdn_policy_t* args, float* loss, float* logprob, int32_t* status, void* stream)
+{
+    const gdn_status_t bad = policy_check(args, status);
+    if (bad != GDN_OK) return bad;
+    const gdn_policy_t& s = *args;
+    if ((loss == nullptr) != (s.old_logprob == nullptr) || !aligned(loss, 4) || !aligned(logprob, 4)) return GDN_ERR_INVALID_ARG;
+    if (s.rows == 0) return GDN_OK;
+    if (logprob == nullptr) return GDN_ERR_INVALID_ARG;
+    const size_t es = esize(s.in_dtype);
+    if (overlap({{loss, s.rows, 4}, {logprob, s.rows, 4}, {status, 1, 4}},
+                {{s.logits, s.rows, s.logits_stride, s.vocab, es}, {s.targets, s.rows, 8}, {s.old_logprob, s.rows, 4},
+                 {s.ref_logprob, s.rows, 4}, {s.advantages, s.rows, 4}}))
+        return GDN_ERR_INVALID_ARG;
+    gdn::PolicyArgs a = policy_args(args, status);
+    a.loss = loss; a.lp = logprob;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return s.in_dtype == GDN_BF16 ? policy_launch<__nv_bfloat16, false>(a, s.in_dtype, st)
+                                  : policy_launch<float, false>(a, s.in_dtype, st);
+}
+
+gdn_status_t gdn_policy_loss_backward(const gdn_policy_t* args, const float* dloss, void* dlogits, float* loss,
+                                      float* logprob, int32_t* status, void* stream)
+{
+    const gdn_status_t bad = policy_check(args, status);
+    if (bad != GDN_OK) return bad;
+    const gdn_policy_t& s = *args;
+    if (s.old_logprob == nullptr || !aligned(loss, 4) || !aligned(logprob, 4) || !aligned(dloss, 4)) return GDN_ERR_INVALID_ARG;
+    if (s.rows == 0) return GDN_OK;
+    if (dloss == nullptr || !rows_ok(dlogits, s.vocab, s.vocab, s.in_dtype)) return GDN_ERR_INVALID_ARG;
+    const size_t es = esize(s.in_dtype);
+    // the gradient may take the place of dense logits: a row is on the chip before it is written
+    const bool in_place = dlogits == s.logits && (s.logits_stride == s.vocab || s.rows == 1);
+    if (overlap({{dlogits, s.rows * s.vocab, es}, {loss, s.rows, 4}, {logprob, s.rows, 4}, {status, 1, 4}},
+                {{in_place ? nullptr : s.logits, s.rows, s.logits_stride, s.vocab, es}, {s.targets, s.rows, 8},
+                 {s.old_logprob, s.rows, 4}, {s.ref_logprob, s.rows, 4}, {s.advantages, s.rows, 4}, {dloss, s.rows, 4}}))
+        return GDN_ERR_INVALID_ARG;
+    gdn::PolicyArgs a = policy_args(args, status);
+    a.loss = loss; a.lp = logprob; a.dloss = dloss; a.dz = dlogits;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return s.in_dtype == GDN_BF16 ? policy_launch<__nv_bfloat16, true>(a, s.in_dtype, st)
+                                  : policy_launch<float, true>(a, s.in_dtype, st);
+}
+
+}  // extern "C"

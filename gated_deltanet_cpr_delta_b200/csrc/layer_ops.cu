@@ -5,102 +5,15 @@
 // enqueues on the caller's stream; it allocates nothing, keeps no state and
 // never synchronises.
 #include "gdn_cpr.h"
+#include "layer_host.cuh"
 #include "k_conv.cuh"
 #include "k_norm.cuh"
 #include "k_ssm.cuh"
 #include "k_ssm_bwd.cuh"
 
-#include <cuda_runtime.h>
-
-#include <algorithm>
-#include <cstdint>
-#include <initializer_list>
-
 namespace {
 
 using gdn::Seqs;
-
-constexpr size_t kAlign = 256;
-// The kernels count rows, the columns of the norm and the channels of the scan, and a block's worth beyond
-// the end, in 32 bits.
-constexpr int64_t kMaxRows = INT32_MAX - 4096;
-
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-bool dtype_ok(gdn_dtype_t t) { return t == GDN_F32 || t == GDN_BF16; }
-size_t esize(gdn_dtype_t t) { return t == GDN_BF16 ? 2 : 4; }
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-bool launched() { return cudaGetLastError() == cudaSuccess; }
-
-// Shared memory beyond the 48 KB that every launch may have
-template <typename K>
-bool raise_smem(K* kernel, size_t bytes)
-{
-    return bytes <= 48 * 1024 ||
-           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
-}
-
-int sm_count()
-{
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
-        return 0;
-    return sms;
-}
-
-// The bytes of a [rows, width] tensor whose rows are `stride` elements apart.
-struct Span {
-    uintptr_t lo = 0, hi = 0;      // from the first row's start to the last row's end; empty: lo == hi
-    size_t step = 0, width = 0;    // bytes between rows, and of a row
-    Span(const void* p, int64_t rows, int64_t stride, int64_t row, size_t esz)
-    {
-        if (p == nullptr || rows <= 0 || row <= 0) return;
-        lo = reinterpret_cast<uintptr_t>(p);
-        step = (size_t)stride * esz;
-        width = (size_t)row * esz;
-        hi = lo + (size_t)(rows - 1) * step + width;
-    }
-    Span(const void* p, int64_t n, size_t esz) : Span(p, 1, n, n, esz) {}
-    // Whether a dense tensor o shares bytes with it: its rows, not the room between them.
-    bool hits(const Span& o) const
-    {
-        if (lo == hi || o.lo == o.hi || lo >= o.hi || o.lo >= hi) return false;
-        // the first row that ends behind o's start
-        const size_t k = o.lo < lo + width ? 0 : (o.lo - lo - width) / step + 1;
-        return lo + k * step < o.hi;
-    }
-};
-
-// Whether an output (all dense) shares bytes with an input or with another output.
-bool overlap(std::initializer_list<Span> outs, std::initializer_list<Span> ins)
-{
-    for (const Span* o = outs.begin(); o != outs.end(); ++o) {
-        for (const Span& i : ins)
-            if (i.hits(*o)) return true;
-        for (const Span* q = o + 1; q != outs.end(); ++q)
-            if (o->hits(*q)) return true;
-    }
-    return false;
-}
-
-// 16-byte accesses: the row's address, stride and width are multiples of 16 bytes.
-bool wide(const void* p, int64_t stride, int64_t width, gdn_dtype_t t)
-{
-    const int64_t v = 16 / (int64_t)esize(t);
-    return p == nullptr || (aligned(p, 16) && stride % v == 0 && width % v == 0);
-}
-
-// Whether every row starts at, and consists of, whole groups of v elements.
-bool groups(const void* p, int64_t stride, int64_t width, gdn_dtype_t t, int64_t v)
-{
-    return aligned(p, v * esize(t)) && stride % v == 0 && width % v == 0;
-}
-
-bool rows_ok(const void* p, int64_t stride, int64_t width, gdn_dtype_t t)
-{
-    return p != nullptr && stride >= width && stride <= INT32_MAX && aligned(p, esize(t));
-}
 
 // ------------------------------------------------------------------- convolution
 

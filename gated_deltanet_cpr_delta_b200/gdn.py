@@ -34,7 +34,9 @@ SYMBOLS = ("gdn_contract_id", "gdn_status_string", "gdn_num_chunk_states", "gdn_
            "gdn_conv_forward", "gdn_conv_backward_workspace_size", "gdn_conv_backward", "gdn_conv_step",
            "gdn_ssm_num_chunk_states", "gdn_ssm_forward",
            "gdn_ssm_backward_workspace_size", "gdn_ssm_backward", "gdn_ssm_step",
-           "gdn_layer_norm_forward", "gdn_layer_norm_backward_workspace_size", "gdn_layer_norm_backward")
+           "gdn_layer_norm_forward", "gdn_layer_norm_backward_workspace_size", "gdn_layer_norm_backward",
+           "gdn_qk_norm_forward", "gdn_qk_norm_backward_workspace_size", "gdn_qk_norm_backward",
+           "gdn_policy_loss_forward", "gdn_policy_loss_backward")
 
 #: gdn_identity_kind_t
 ID_SEMANTIC, ID_NUMERICAL_POLICY, ID_DEPLOYMENT = 0, 1, 2
@@ -64,6 +66,20 @@ class SsmStruct(ctypes.Structure):
                                               "total_tokens")] + \
                [(n, ctypes.c_int32) for n in ("num_seqs", "channels", "groups", "states", "delta_softplus",
                                               "in_dtype")]
+
+
+class QkNormStruct(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "q_weight", "k_weight", "positions", "inv_freq")] + \
+               [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "tokens")] + \
+               [(n, ctypes.c_int32) for n in ("q_heads", "k_heads", "head_dim", "rot_dim", "interleaved", "unit")] + \
+               [("eps", ctypes.c_float)] + [(n, ctypes.c_int32) for n in ("in_dtype", "w_dtype")]
+
+
+class PolicyStruct(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("logits", "targets", "old_logprob", "ref_logprob", "advantages")] + \
+               [(n, ctypes.c_int64) for n in ("logits_stride", "rows")] + [("vocab", ctypes.c_int32)] + \
+               [(n, ctypes.c_float) for n in ("clip_low", "clip_high", "kl_coef", "temperature")] + \
+               [("in_dtype", ctypes.c_int32)]
 
 
 _lib = None
@@ -145,6 +161,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.gdn_layer_norm_backward_workspace_size.argtypes = [i64, i32]
     lib.gdn_layer_norm_backward.restype = e
     lib.gdn_layer_norm_backward.argtypes = [P, i64, P, i64, P, P, P, i64, i32, e, e, P, P, P, P, sz, P]
+    qk, pol = ctypes.POINTER(QkNormStruct), ctypes.POINTER(PolicyStruct)
+    lib.gdn_qk_norm_forward.restype = e
+    lib.gdn_qk_norm_forward.argtypes = [qk, P, P, P]
+    lib.gdn_qk_norm_backward_workspace_size.restype = sz
+    lib.gdn_qk_norm_backward_workspace_size.argtypes = [i64, i32]
+    lib.gdn_qk_norm_backward.restype = e
+    lib.gdn_qk_norm_backward.argtypes = [qk, P, i64, P, i64, P, P, P, P, P, sz, P]
+    lib.gdn_policy_loss_forward.restype = e
+    lib.gdn_policy_loss_forward.argtypes = [pol, P, P, P, P]
+    lib.gdn_policy_loss_backward.restype = e
+    lib.gdn_policy_loss_backward.argtypes = [pol, P, P, P, P, P, P]
     _lib = lib
     return lib
 
@@ -772,3 +799,133 @@ def gdn_layer_norm_backward(x, weight, dy, mean, rstd, *, workspace=None, grads=
           _dense(what, "rstd", rstd, _F32, shape[:-1], dev), R, D, ti, wi, _dense(what, "dx", dx, dt, shape, dev),
           _dense(what, "dweight", dw, _F32, (D,), dev), _opt(what, "dbias", db, _F32, (D,), dev), ws, nbytes)
     return grads
+
+
+def _qk_struct(what, q, k, q_weight, k_weight, positions, inv_freq, interleaved, l2, eps, dev):
+    if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+        raise ValueError(f"{what}: q must be [tokens, q_heads, head_dim] and k [tokens, k_heads, head_dim]")
+    if (positions is None) != (inv_freq is None):
+        raise ValueError(f"{what}: positions and inv_freq go together")
+    T, Hq, d = q.shape
+    Hk, ty = k.shape[1], q.dtype
+    weight = q_weight if q_weight is not None else k_weight
+    wt = ty if weight is None else weight.dtype
+    ti = _type(what, q)
+    pq, lq = _rows(what, "q", q, ty, (T, Hq, d), dev)
+    pk, lk = _rows(what, "k", k, ty, (T, Hk, d), dev)
+    rot, pp, pf = 0, None, None
+    if positions is not None:
+        if inv_freq.dim() != 1:
+            raise ValueError(f"{what}: inv_freq must be a vector")
+        rot = 2 * inv_freq.shape[0]
+        pp = _dense(what, "positions", positions, torch.int32, (T,), dev)
+        pf = _dense(what, "inv_freq", inv_freq, _F32, inv_freq.shape, dev)
+    return QkNormStruct(pq, pk, _opt(what, "q_weight", q_weight, wt, (d,), dev), _opt(what, "k_weight", k_weight, wt, (d,), dev),
+                        pp, pf, lq, lk, T, Hq, Hk, d, rot, interleaved, l2, eps, ti, _DT.get(wt, -1))
+
+
+def gdn_qk_norm_forward(q, k, *, q_weight=None, k_weight=None, positions=None, inv_freq=None, interleaved: bool = False,
+                        l2: bool = False, eps: float = 1e-6, q_out=None, k_out=None):
+    """Norm of every query's and key's head with the position rotation in the same pass (gdn_qk_norm_forward).
+
+    q [T, q_heads, d], k [T, k_heads, d] (bf16 or fp32; tokens may be strided, so slices of one projection's output
+    do), d even and at most 256; q_weight, k_weight [d] or None (bf16 or fp32, one type); positions int32 [T] and inv_freq
+    fp32 [rot / 2] turn the first rot dimensions in pairs (i, i + rot / 2), or (2 i, 2 i + 1) with
+    ``interleaved``; both None: no rotation.  ``l2``: rows of unit length (as the recurrence takes
+    them) instead of unit mean square.  A decode step's tokens are rows like any other.  Returns
+    (q_out, k_out), dense, in the inputs' shapes and type."""
+    what = "gdn_qk_norm_forward"
+    dev = _gpu(what, q)
+    s = _qk_struct(what, q, k, q_weight, k_weight, positions, inv_freq, interleaved, l2, eps, dev)
+    q_out, pq = _out(what, "q_out", q_out, q.dtype, q.shape, dev, q)
+    k_out, pk = _out(what, "k_out", k_out, q.dtype, k.shape, dev, k)
+    _call(dev, what, load_library().gdn_qk_norm_forward, s, pq, pk)
+    return q_out, k_out
+
+
+def gdn_qk_norm_backward(q, k, dq_out, dk_out, *, q_weight=None, k_weight=None, positions=None, inv_freq=None,
+                         interleaved: bool = False, l2: bool = False, eps: float = 1e-6, workspace=None, grads=None):
+    """Gradients of sum(dq_out q_out) + sum(dk_out k_out) for :func:`gdn_qk_norm_forward` of the same inputs.
+
+    dq_out, dk_out in q's and k's shapes and type (tokens may be strided).  Returns (dq, dk, dq_weight, dk_weight): the
+    first two in the inputs' type, the others fp32, summed over tokens and heads, None without the
+    weight.  ``grads``: an optional tuple of those four to write into."""
+    what = "gdn_qk_norm_backward"
+    dev = _gpu(what, q)
+    s = _qk_struct(what, q, k, q_weight, k_weight, positions, inv_freq, interleaved, l2, eps, dev)
+    T, d, ty = s.tokens, s.head_dim, q.dtype
+    pgq, lgq = _rows(what, "dq_out", dq_out, ty, q.shape, dev)
+    pgk, lgk = _rows(what, "dk_out", dk_out, ty, k.shape, dev)
+    if grads is None:
+        grads = (torch.empty(q.shape, dtype=ty, device=dev), torch.empty(k.shape, dtype=ty, device=dev),
+                 None if q_weight is None else torch.empty((d,), dtype=_F32, device=dev),
+                 None if k_weight is None else torch.empty((d,), dtype=_F32, device=dev))
+    dq, dk, dqw, dkw = grads
+    keep, ws, nbytes = None, None, 0
+    if dqw is not None or dkw is not None:
+        keep, ws, nbytes = _scratch(what, workspace, _scratch_size("gdn_qk_norm_backward_workspace_size", T, d), dev)
+    _call(dev, what, load_library().gdn_qk_norm_backward, s, pgq, lgq, pgk, lgk, _dense(what, "dq", dq, ty, q.shape, dev),
+          _dense(what, "dk", dk, ty, k.shape, dev), _opt(what, "dq_weight", dqw, _F32, (d,), dev),
+          _opt(what, "dk_weight", dkw, _F32, (d,), dev), ws, nbytes)
+    return grads
+
+
+def _policy_struct(what, logits, targets, old_logprob, advantages, ref_logprob, clip_low, clip_high, kl_coef, temperature, dev):
+    if logits.dim() != 2:
+        raise ValueError(f"{what}: logits must be [rows, vocab]")
+    if (old_logprob is None) != (advantages is None) or (ref_logprob is not None and old_logprob is None):
+        raise ValueError(f"{what}: old_logprob and advantages go together, and with ref_logprob")
+    R, V = logits.shape
+    ti = _type(what, logits)
+    pz, lz = _rows(what, "logits", logits, logits.dtype, (R, V), dev)
+    return PolicyStruct(pz, _dense(what, "targets", targets, torch.int64, (R,), dev),
+                        _opt(what, "old_logprob", old_logprob, _F32, (R,), dev),
+                        _opt(what, "ref_logprob", ref_logprob, _F32, (R,), dev),
+                        _opt(what, "advantages", advantages, _F32, (R,), dev), lz, R, V, clip_low, clip_high, kl_coef,
+                        temperature, ti)
+
+
+def gdn_policy_loss_forward(logits, targets, *, old_logprob=None, advantages=None, ref_logprob=None, clip_low: float = 0.2,
+                            clip_high: float = 0.2, kl_coef: float = 0.0, temperature: float = 1.0, loss=None, logprob=None,
+                            status=None):
+    """Clipped policy loss with a KL term for each row of logits [rows, vocab] (gdn_policy_loss_forward):
+        logprob = log_softmax(logits / temperature)[target],  ratio = exp(logprob - old_logprob)
+        loss = -min(ratio A, clip(ratio, 1 - clip_low, 1 + clip_high) A) + kl_coef (e^g - g - 1),  g = ref_logprob - logprob
+
+    logits bf16 or fp32 (rows may be strided); targets int64 [rows], negative: the row takes no part (its results are 0);
+    old_logprob, advantages, ref_logprob fp32 [rows].  ref_logprob None: no KL term; old_logprob and advantages None: the
+    log-probabilities alone, as a rollout records them.  Returns (loss or None, logprob), fp32 [rows].  A row's
+    log-probability has the same bits in every batch and in :func:`gdn_policy_loss_backward`.
+    ``status``: an optional int32 that records a target outside the vocabulary."""
+    what = "gdn_policy_loss_forward"
+    dev = _gpu(what, logits)
+    s = _policy_struct(what, logits, targets, old_logprob, advantages, ref_logprob, clip_low, clip_high, kl_coef, temperature, dev)
+    shape = (s.rows,)
+    logprob, pl = _out(what, "logprob", logprob, _F32, shape, dev)
+    po = None
+    if old_logprob is not None:
+        loss, po = _out(what, "loss", loss, _F32, shape, dev)
+    elif loss is not None:
+        raise ValueError(f"{what}: a loss needs old_logprob and advantages")
+    _call(dev, what, load_library().gdn_policy_loss_forward, s, po, pl, _opt(what, "status", status, torch.int32, (1,), dev))
+    return loss, logprob
+
+
+def gdn_policy_loss_backward(logits, targets, dloss, *, old_logprob, advantages, ref_logprob=None, clip_low: float = 0.2,
+                             clip_high: float = 0.2, kl_coef: float = 0.0, temperature: float = 1.0, dlogits=None, loss=None,
+                             logprob=None, status=None):
+    """The logits' gradient of sum(dloss loss) for :func:`gdn_policy_loss_forward` of the same inputs, and that call's
+    results: a training step whose weights ``dloss`` (fp32 [rows]) are known is this call alone.
+
+    Returns (dlogits [rows, vocab] in the logits' type, loss, logprob).  ``dlogits`` may be the (dense) logits
+    themselves: the gradient then takes their place."""
+    what = "gdn_policy_loss_backward"
+    dev = _gpu(what, logits)
+    s = _policy_struct(what, logits, targets, old_logprob, advantages, ref_logprob, clip_low, clip_high, kl_coef, temperature, dev)
+    shape = (s.rows,)
+    dlogits, pd = _out(what, "dlogits", dlogits, logits.dtype, logits.shape, dev, logits)
+    loss, po = _out(what, "loss", loss, _F32, shape, dev)
+    logprob, pl = _out(what, "logprob", logprob, _F32, shape, dev)
+    _call(dev, what, load_library().gdn_policy_loss_backward, s, _dense(what, "dloss", dloss, _F32, shape, dev), pd, po, pl,
+          _opt(what, "status", status, torch.int32, (1,), dev))
+    return dlogits, loss, logprob

@@ -449,7 +449,8 @@ gdn_status_t gdn_cpr_forward_noalloc(const void* q, const void* k, const void* v
  * ------------------------------------------------------------------ layer operators
  * The operators around the recurrence, for prefill, training and decode: the short causal
  * convolution in front of a recurrent mixer, the selective state space scan (a mixer of
- * its own kind, with a diagonal decay per channel and state), and layer norm.
+ * its own kind, with a diagonal decay per channel and state), layer norm, the norm of queries and
+ * keys with the position rotation, and the clipped policy loss.
  * They take the conventions at the top of this file, with these differences:
  *  - Token tensors ([T, channels], [T, G, S]) may be views of wider rows, such as the slices
  *    of one projection's output: `*_stride` is the distance between tokens in
@@ -593,6 +594,84 @@ gdn_status_t gdn_layer_norm_backward(const void* x, int64_t x_stride, const void
                                      int32_t width, gdn_dtype_t in_dtype, gdn_dtype_t w_dtype, void* dx,
                                      float* dweight, float* dbias, void* workspace, size_t workspace_bytes,
                                      void* stream);
+
+/*
+ * Norms of the queries' and keys' heads, with the position rotation in the same pass.  For each row x (one
+ * head of one token) of q and of k:
+ *   u = x (sum(x^2) / n + eps)^(-1/2) weight,  n = head_dim, or 1 with `unit` (rows of unit length, as
+ *       the recurrence takes its q and k)
+ * and the first rot_dim dimensions of u turn in pairs (a, b) by the angle positions[t] inv_freq[i]:
+ *   a' = a cos - b sin,  b' = b cos + a sin
+ * Pair i is (i, i + rot_dim / 2), or (2 i, 2 i + 1) with `interleaved`; rot_dim = 0: no rotation.
+ *   q [tokens, q_heads, head_dim], k [tokens, k_heads, head_dim] in in_dtype, tokens *_stride apart
+ *   q_weight, k_weight [head_dim] in w_dtype, or NULL for ones
+ *   positions [tokens] int32 (any value) and inv_freq [rot_dim / 2] fp32, read with rot_dim > 0 only; the
+ *     angle is the exact product, reduced in 64 bits
+ * head_dim is even and at most 256, rot_dim even: GDN_ERR_UNSUPPORTED else.  Single tokens of a decode step are rows like any
+ * other.  Squares are summed in fp32 (as in layer norm: values above 1e18 give 0, and without an eps
+ * that covers them values below 1e-18 lose digits); a row of zeros with eps = 0 is not a number.
+ */
+typedef struct {
+    const void *q, *k, *q_weight, *k_weight;
+    const int32_t* positions;
+    const float* inv_freq;
+    int64_t q_stride, k_stride, tokens;
+    int32_t q_heads, k_heads, head_dim, rot_dim;
+    int32_t interleaved, unit;
+    float eps;
+    gdn_dtype_t in_dtype, w_dtype;
+} gdn_qk_norm_t;
+
+/* q_out and k_out: dense, in q's and k's shapes and type. */
+gdn_status_t gdn_qk_norm_forward(const gdn_qk_norm_t* args, void* q_out, void* k_out, void* stream);
+
+/*
+ * Gradients of sum(dq_out q_out) + sum(dk_out k_out), from the forward's inputs: dq, dk in in_dtype;
+ * dq_weight, dk_weight [head_dim] fp32, summed over tokens and heads (NULL: not wanted; only where the weight is
+ * given).  Without either no workspace is needed.
+ */
+size_t gdn_qk_norm_backward_workspace_size(int64_t tokens, int32_t head_dim);
+gdn_status_t gdn_qk_norm_backward(const gdn_qk_norm_t* args, const void* dq_out, int64_t dq_out_stride, const void* dk_out,
+                                  int64_t dk_out_stride, void* dq, void* dk, float* dq_weight, float* dk_weight,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Clipped policy loss with a KL term, for each row (token) of logits z [rows, vocab] in in_dtype, rows
+ * logits_stride apart, with the sampled token y = targets[row] (int64):
+ *   logprob = z_y / temperature - log(sum_v e^(z_v / temperature)),  ratio = e^(logprob - old_logprob)
+ *   loss    = -min(ratio A, clip(ratio, 1 - clip_low, 1 + clip_high) A)
+ *             + kl_coef (e^(ref_logprob - logprob) - (ref_logprob - logprob) - 1),   A = advantages[row]
+ * old_logprob, ref_logprob, advantages [rows] fp32.  ref_logprob NULL: no KL term.  old_logprob and advantages NULL (both):
+ * log-probabilities only, as a rollout records them.  A row with a negative target takes
+ * no part: nothing of it is read, its loss, log-probability and gradient are 0.  A target of vocab or above is
+ * treated so too, and *status (may be NULL) becomes GDN_ERR_DEVICE_INPUT.
+ * Logits of -inf have probability 0; a row whose logits are all -inf, or that holds +inf or a NaN, is not a number in its
+ * own results.  An advantage of 0 adds 0, whatever the ratio.
+ * A row's log-probability has the same bits in every call on the same values, type and
+ * vocabulary: whatever the batch, the row's place, its stride, and whether the gradient is made.
+ * Rows of more than 1 MiB (524288 bf16, 262144 fp32): GDN_ERR_UNSUPPORTED.
+ */
+typedef struct {
+    const void* logits;
+    const int64_t* targets;
+    const float *old_logprob, *ref_logprob, *advantages;
+    int64_t logits_stride, rows;
+    int32_t vocab;
+    float clip_low, clip_high, kl_coef, temperature;
+    gdn_dtype_t in_dtype;
+} gdn_policy_t;
+
+/* loss [rows] fp32 (NULL exactly where old_logprob is) and logprob [rows] fp32. */
+gdn_status_t gdn_policy_loss_forward(const gdn_policy_t* args, float* loss, float* logprob, int32_t* status, void* stream);
+
+/*
+ * The logits' gradient of sum(dloss loss), dloss [rows] fp32: dlogits [rows, vocab] in in_dtype, dense; and the
+ * forward's results again where loss and logprob are given, so that a training step whose weights dloss are
+ * known is this call alone: the logits are read once.  dlogits may be the logits' own memory (dense).  The clipped
+ * branch has the gradient 0; on the border the unclipped one counts.
+ */
+gdn_status_t gdn_policy_loss_backward(const gdn_policy_t* args, const float* dloss, void* dlogits, float* loss,
+                                      float* logprob, int32_t* status, void* stream);
 
 #ifdef __cplusplus
 }
