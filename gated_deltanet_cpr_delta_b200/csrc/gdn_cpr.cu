@@ -7,6 +7,7 @@
 // per-device address cache of gdn_cpr_forward_noalloc (end of file).
 #include "gdn_cpr.h"
 #include "kernels.cuh"
+#include "tensor_map.cuh"
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -121,22 +122,6 @@ Workspace carve(void* base, int64_t max_full, int32_t N, int32_t H, int32_t dk, 
         ws.dC = reinterpret_cast<float*>(b + o_dc);
     }
     return ws;
-}
-
-// cuTensorMapEncodeTiled from the driver, looked up once through the runtime
-// (the library does not link libcuda itself).
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
-{
-    static std::once_flag once;
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    std::call_once(once, [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    });
-    return fn;
 }
 
 // Tensor map of a [T, H, D] token tensor for TMA boxes of D x 1 x `box`

@@ -1,0 +1,298 @@
+// glu_ops.cu -- host side of the gated feed-forward block (gdn_cpr.h).
+//
+// As layer_ops.cu: it validates on the host, carves the caller's workspace and
+// enqueues on the caller's stream; it allocates nothing, keeps no state and
+// never synchronises.
+#include "layer_host.cuh"
+#include "tensor_map.cuh"
+#include "k_glu.cuh"
+
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+// Tensor map of a [rows, cols] bf16 matrix, rows ld elements apart, for boxes of 64 columns with 128-byte swizzle.  Boxes
+// that reach past the end are filled with zeros.
+bool matrix_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (enc == nullptr) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {64u, (cuuint32_t)box_rows};
+    const cuuint32_t estr[2] = {1u, 1u};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A matrix that TMA can read: whole 16-byte rows at a 16-byte address.
+bool tma_rows(const void* p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
+int64_t pad8(int64_t n) { return (n + 7) / 8 * 8; }
+
+// x and the weights, or their aligned copies in the workspace
+struct GluOperands {
+    const void *x, *wg, *wu;
+    int64_t ldx, ldg, ldu;
+    size_t bytes;  // of the copies
+};
+
+// Carves the copies from p (which may be null: sizes only).
+GluOperands glu_operands(const gdn_glu_t& s, unsigned char* p)
+{
+    GluOperands o{s.x, s.w_gate, s.w_up, s.x_stride, s.gate_stride, s.up_stride, 0};
+    const int64_t ld = pad8(s.width);
+    auto copy = [&](const void*& q, int64_t& l, int64_t rows) {
+        if (rows == 0 || tma_rows(q, l)) return;
+        q = p + o.bytes;
+        l = ld;
+        o.bytes += align_up((size_t)rows * ld * 2);
+    };
+    copy(o.x, o.ldx, s.rows);
+    copy(o.wg, o.ldg, s.inner);
+    copy(o.wu, o.ldu, s.inner);
+    return o;
+}
+
+bool glu_align(const void* src, int64_t lds, const void* dst, int64_t ldd, int64_t rows, int64_t cols, cudaStream_t st)
+{
+    if (src == dst || rows == 0) return true;
+    const int64_t n = rows * (ldd / 8);
+    gdn::k_glu_align<<<(unsigned)std::min<int64_t>(ceil_div(n, 256), 148 * 16), 256, 0, st>>>(
+        static_cast<const uint16_t*>(src), lds, rows, cols, static_cast<uint16_t*>(const_cast<void*>(dst)), ldd);
+    return launched();
+}
+
+bool glu_align_all(const gdn_glu_t& s, const GluOperands& o, cudaStream_t st)
+{
+    return glu_align(s.x, s.x_stride, o.x, o.ldx, s.rows, s.width, st) &&
+           glu_align(s.w_gate, s.gate_stride, o.wg, o.ldg, s.inner, s.width, st) &&
+           glu_align(s.w_up, s.up_stride, o.wu, o.ldu, s.inner, s.width, st);
+}
+
+gdn_status_t glu_check(const gdn_glu_t* s, const int32_t* status)
+{
+    if (s == nullptr || s->rows < 0 || s->rows > kMaxRows || s->width <= 0 || s->inner <= 0 || s->width > kMaxRows ||
+        s->inner > kMaxRows || !dtype_ok(s->in_dtype) || (s->act != GDN_ACT_SILU && s->act != GDN_ACT_GELU) ||
+        !aligned(status, 4))
+        return GDN_ERR_INVALID_ARG;
+    if (s->in_dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED;
+    if (!rows_ok(s->w_gate, s->gate_stride, s->width, s->in_dtype) || !rows_ok(s->w_up, s->up_stride, s->width, s->in_dtype))
+        return GDN_ERR_INVALID_ARG;
+    if (s->rows > 0 && !rows_ok(s->x, s->x_stride, s->width, s->in_dtype)) return GDN_ERR_INVALID_ARG;
+    return GDN_OK;
+}
+
+template <int MODE>
+gdn_status_t glu_gemm(gdn::GluMaps& maps, gdn::GluGemmArgs& a, int sms, cudaStream_t st)
+{
+    a.tiles_m = (int32_t)ceil_div(a.M, 256);
+    a.tiles_n = (int32_t)ceil_div(a.N, MODE == gdn::kGluFwd ? 128 : 256);
+    a.tiles = (int64_t)a.tiles_m * a.tiles_n * a.problems * a.splits;
+    auto k = gdn::k_glu_gemm<MODE>;
+    if (!raise_smem(k, gdn::kGluSmem)) return GDN_ERR_CUDA;
+    const unsigned pairs = (unsigned)std::min<int64_t>(a.tiles, std::max(1, sms / 2));
+    k<<<2 * pairs, gdn::kGluThreads, gdn::kGluSmem, st>>>(maps, a);
+    return launched() ? GDN_OK : GDN_ERR_CUDA;
+}
+
+// Parts of the K axis of a product with few tiles: enough for every pair of SMs, each of at least 8 stages.
+int glu_splits(int64_t tiles, int64_t ksteps, int sms)
+{
+    const int64_t want = std::max<int64_t>(1, (sms / 2) / tiles);
+    return (int)std::max<int64_t>(1, std::min<int64_t>({want, ksteps / 8, 64}));
+}
+
+template <int NB>
+gdn_status_t glu_few(const GluOperands& o, const gdn_glu_t& s, const gdn::GluFewArgs& a, int sms, cudaStream_t st)
+{
+    gdn::GluFewMaps maps;
+    if (!matrix_map(&maps.x, o.x, s.rows, s.width, o.ldx, NB) || !matrix_map(&maps.wg, o.wg, s.inner, s.width, o.ldg, 128) ||
+        !matrix_map(&maps.wu, o.wu, s.inner, s.width, o.ldu, 128))
+        return GDN_ERR_CUDA;
+    using G = gdn::GluFew<NB>;
+    const int tiles = (int)ceil_div(s.inner, 128);
+    // blocks for every SM, two of them where they fit, each with 4 stages at least
+    const int room = sms * (G::SMEM <= 113 * 1024 ? 2 : 1);
+    int S = 1;
+    while (S < 8 && tiles * S * 2 <= room && a.ksteps >= 4 * S * 2) S *= 2;
+    auto k = gdn::k_glu_few<NB>;
+    if (!raise_smem(k, G::SMEM)) return GDN_ERR_CUDA;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(tiles * S));
+    cfg.blockDim = dim3(gdn::kGluThreads);
+    cfg.dynamicSmemBytes = G::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)S;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, maps, a) == cudaSuccess && launched() ? GDN_OK : GDN_ERR_CUDA;
+}
+
+// The backward's workspace: dg and du, rows ld apart; aligned copies; the splits' partial products.
+struct GluBackwardPlan {
+    int64_t ld;
+    int splits_x, splits_w;
+    size_t copies, part, bytes;  // offsets
+};
+
+GluBackwardPlan glu_backward_plan(const gdn_glu_t& s, int sms)
+{
+    GluBackwardPlan p;
+    p.ld = pad8(s.inner);
+    const int64_t tx = ceil_div(s.rows, 256) * ceil_div(s.width, 256);
+    const int64_t tw = 2 * ceil_div(s.inner, 256) * ceil_div(s.width, 256);
+    p.splits_x = s.rows > 0 ? glu_splits(tx, 2 * ceil_div(s.inner, gdn::kGluK), sms) : 1;
+    p.splits_w = s.rows > 0 ? glu_splits(tw, ceil_div(s.rows, gdn::kGluK), sms) : 1;
+    p.copies = 2 * align_up((size_t)s.rows * p.ld * 2);
+    p.part = p.copies + glu_operands(s, nullptr).bytes;
+    const size_t px = p.splits_x > 1 ? sizeof(float) * (size_t)p.splits_x * s.rows * s.width : 0;
+    const size_t pw = p.splits_w > 1 ? sizeof(float) * 2 * (size_t)p.splits_w * s.inner * s.width : 0;
+    p.bytes = p.part + align_up(std::max(px, pw));
+    return p;
+}
+
+template <typename OT>
+bool glu_join(const float* part, int splits, int64_t n, void* o0, void* o1, int problems, cudaStream_t st)
+{
+    gdn::k_glu_join<OT><<<(unsigned)std::min<int64_t>(ceil_div(n * problems, 256), 148 * 16), 256, 0, st>>>(
+        part, splits, n, static_cast<OT*>(o0), static_cast<OT*>(o1), problems);
+    return launched();
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t gdn_glu_saved_size(int64_t rows, int32_t inner)
+{
+    return rows < 0 || inner <= 0 ? -1 : 6 * rows * (int64_t)inner;
+}
+
+size_t gdn_glu_forward_workspace_size(const gdn_glu_t* args)
+{
+    return glu_check(args, nullptr) == GDN_OK ? glu_operands(*args, nullptr).bytes : 0;
+}
+
+gdn_status_t gdn_glu_forward(const gdn_glu_t* args, void* h, void* saved, void* workspace, size_t workspace_bytes,
+                             int32_t* status, void* stream)
+{
+    const gdn_status_t bad = glu_check(args, status);
+    if (bad != GDN_OK) return bad;
+    const gdn_glu_t& s = *args;
+    if (s.rows == 0) return GDN_OK;
+    if (!rows_ok(h, s.inner, s.inner, s.in_dtype) || !aligned(saved, 16)) return GDN_ERR_INVALID_ARG;
+    const size_t need = gdn_glu_forward_workspace_size(args);
+    const int64_t R = s.rows, F = s.inner, D = s.width;
+    if (overlap({{h, R * F, 2}, {saved, gdn_glu_saved_size(R, s.inner), 1}, {workspace, (int64_t)need, 1}, {status, 1, 4}},
+                {{s.x, R, s.x_stride, D, 2}, {s.w_gate, F, s.gate_stride, D, 2}, {s.w_up, F, s.up_stride, D, 2}}))
+        return GDN_ERR_INVALID_ARG;
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
+    if (need > 0 && !aligned(workspace, kAlign)) return GDN_ERR_INVALID_ARG;
+    const int sms = sm_count();
+    if (sms == 0) return GDN_ERR_CUDA;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const GluOperands o = glu_operands(s, static_cast<unsigned char*>(workspace));
+    if (!glu_align_all(s, o, st)) return GDN_ERR_CUDA;
+    const int32_t ksteps = (int32_t)ceil_div(D, gdn::kGluK);
+    if (R <= 256) {
+        gdn::GluFewArgs a{(int32_t)R, s.inner, ksteps, h, static_cast<uint16_t*>(saved), s.act, status};
+        if (R <= 16) return glu_few<16>(o, s, a, sms, st);
+        if (R <= 32) return glu_few<32>(o, s, a, sms, st);
+        if (R <= 64) return glu_few<64>(o, s, a, sms, st);
+        if (R <= 128) return glu_few<128>(o, s, a, sms, st);
+        return glu_few<256>(o, s, a, sms, st);
+    }
+    gdn::GluMaps maps;
+    if (!matrix_map(&maps.a[0], o.x, R, D, o.ldx, 128) || !matrix_map(&maps.b[0], o.wg, F, D, o.ldg, 128) ||
+        !matrix_map(&maps.b[1], o.wu, F, D, o.ldu, 128))
+        return GDN_ERR_CUDA;
+    maps.a[1] = maps.a[0];
+    gdn::GluGemmArgs a{};
+    a.M = R; a.N = F; a.ksteps = ksteps; a.parts = 1; a.problems = 1; a.splits = 1;
+    a.out[0] = h; a.vec = F % 8 == 0 && aligned(h, 16);
+    a.saved = static_cast<uint16_t*>(saved); a.act = s.act; a.status = status;
+    return glu_gemm<gdn::kGluFwd>(maps, a, sms, st);
+}
+
+size_t gdn_glu_backward_workspace_size(const gdn_glu_t* args)
+{
+    const int sms = sm_count();
+    return glu_check(args, nullptr) == GDN_OK && sms > 0 ? glu_backward_plan(*args, sms).bytes : 0;
+}
+
+gdn_status_t gdn_glu_backward(const gdn_glu_t* args, const void* dh, int64_t dh_stride, const void* saved, void* dx,
+                              void* dw_gate, void* dw_up, gdn_dtype_t dw_dtype, void* workspace, size_t workspace_bytes,
+                              int32_t* status, void* stream)
+{
+    const gdn_status_t bad = glu_check(args, status);
+    if (bad != GDN_OK) return bad;
+    const gdn_glu_t& s = *args;
+    const int64_t R = s.rows, F = s.inner, D = s.width;
+    if (!dtype_ok(dw_dtype)) return GDN_ERR_INVALID_ARG;
+    const size_t ws = esize(dw_dtype);
+    if (dw_gate == nullptr || dw_up == nullptr || !aligned(dw_gate, ws) || !aligned(dw_up, ws)) return GDN_ERR_INVALID_ARG;
+    if (R > 0 && (!rows_ok(dh, dh_stride, F, s.in_dtype) || !rows_ok(dx, D, D, s.in_dtype) || saved == nullptr ||
+                  !aligned(saved, 16)))
+        return GDN_ERR_INVALID_ARG;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    auto shared = [&](const void* w, size_t n) {
+        return overlap({{R > 0 ? dx : nullptr, R * D, 2}, {dw_gate, F * D, ws}, {dw_up, F * D, ws}, {w, (int64_t)n, 1}, {status, 1, 4}},
+                       {{s.x, R, s.x_stride, D, 2}, {s.w_gate, F, s.gate_stride, D, 2}, {s.w_up, F, s.up_stride, D, 2},
+                        {dh, R, dh_stride, F, 2}, {saved, gdn_glu_saved_size(R, s.inner), 1}});
+    };
+    if (shared(nullptr, 0)) return GDN_ERR_INVALID_ARG;
+    const int sms = sm_count();
+    if (sms == 0) return GDN_ERR_CUDA;
+    const GluBackwardPlan p = glu_backward_plan(s, sms);
+    if (R > 0 && shared(workspace, p.bytes)) return GDN_ERR_INVALID_ARG;
+    if (R == 0)  // no token: the weights' gradients are zero
+        return cudaMemsetAsync(dw_gate, 0, ws * (size_t)F * D, st) == cudaSuccess &&
+                       cudaMemsetAsync(dw_up, 0, ws * (size_t)F * D, st) == cudaSuccess
+                   ? GDN_OK : GDN_ERR_CUDA;
+    if (workspace == nullptr || workspace_bytes < p.bytes) return GDN_ERR_WORKSPACE;
+    if (!aligned(workspace, kAlign)) return GDN_ERR_INVALID_ARG;
+    unsigned char* base = static_cast<unsigned char*>(workspace);
+    bf16 *dg = reinterpret_cast<bf16*>(base), *du = reinterpret_cast<bf16*>(base + p.copies / 2);
+    float* part = reinterpret_cast<float*>(base + p.part);
+    const GluOperands o = glu_operands(s, base + p.copies);
+    if (!glu_align_all(s, o, st)) return GDN_ERR_CUDA;
+
+    const bool v8 = F % 8 == 0 && wide(dh, dh_stride, F, s.in_dtype);
+    const unsigned blocks = (unsigned)std::min<int64_t>(ceil_div(R * ceil_div(F, v8 ? 8 : 1), 256), (int64_t)sms * 32);
+    const bf16* g = static_cast<const bf16*>(dh);
+    const uint16_t* sv = static_cast<const uint16_t*>(saved);
+    if (v8) gdn::k_glu_grad<8><<<blocks, 256, 0, st>>>(g, dh_stride, sv, R, F, s.act, dg, du, p.ld);
+    else gdn::k_glu_grad<1><<<blocks, 256, 0, st>>>(g, dh_stride, sv, R, F, s.act, dg, du, p.ld);
+    if (!launched()) return GDN_ERR_CUDA;
+
+    gdn::GluMaps mx, mw;
+    if (!matrix_map(&mx.a[0], dg, R, F, p.ld, 128) || !matrix_map(&mx.a[1], du, R, F, p.ld, 128) ||
+        !matrix_map(&mx.b[0], o.wg, F, D, o.ldg, 64) || !matrix_map(&mx.b[1], o.wu, F, D, o.ldu, 64) ||
+        !matrix_map(&mw.a[0], dg, R, F, p.ld, 64) || !matrix_map(&mw.a[1], du, R, F, p.ld, 64) ||
+        !matrix_map(&mw.b[0], o.x, R, D, o.ldx, 64))
+        return GDN_ERR_CUDA;
+    mw.b[1] = mw.b[0];
+    gdn::GluGemmArgs a{};
+    a.M = R; a.N = D; a.ksteps = (int32_t)ceil_div(F, gdn::kGluK); a.parts = 2; a.problems = 1; a.splits = p.splits_x;
+    a.out[0] = dx; a.vec = D % 8 == 0 && aligned(dx, 16); a.partial = part; a.status = status;
+    gdn_status_t r = glu_gemm<gdn::kGluDx>(mx, a, sms, st);
+    if (r != GDN_OK) return r;
+    if (p.splits_x > 1 && !glu_join<bf16>(part, p.splits_x, R * D, dx, nullptr, 1, st)) return GDN_ERR_CUDA;
+    a.M = F; a.N = D; a.ksteps = (int32_t)ceil_div(R, gdn::kGluK); a.parts = 1; a.problems = 2; a.splits = p.splits_w;
+    a.out[0] = dw_gate; a.out[1] = dw_up; a.out_f32 = dw_dtype == GDN_F32;
+    a.vec = D % (16 / (int)ws) == 0 && aligned(dw_gate, 16) && aligned(dw_up, 16);
+    r = glu_gemm<gdn::kGluDw>(mw, a, sms, st);
+    if (r != GDN_OK) return r;
+    if (p.splits_w > 1) {
+        const bool ok = dw_dtype == GDN_F32 ? glu_join<float>(part, p.splits_w, F * D, dw_gate, dw_up, 2, st)
+                                            : glu_join<bf16>(part, p.splits_w, F * D, dw_gate, dw_up, 2, st);
+        if (!ok) return GDN_ERR_CUDA;
+    }
+    return GDN_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,622 @@
+// k_glu.cuh -- the gated feed-forward block's projections, activation and product, forward and backward, on the
+// 5th-generation tensor cores (sm_100a).
+//
+//     g = x Wg^T,  u = x Wu^T,  h = act(g) u
+//     dg = dh u act'(g),  du = dh act(g)
+//     dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x
+//
+// k_glu_gemm is the product of all three: a pair of CTAs on neighbouring SMs makes a tile of 256 x 256
+// with tcgen05.mma.cta_group::2 (bf16 operands, fp32 accumulators in tensor memory), so that each SM fetches
+// half of either operand: 32 KB per 128 x 256 x 64 products, 64 bytes per cycle at the
+// tensor cores' rate.  TMA fills a ring of shared memory stages, one thread issues the products, and four
+// warps empty one accumulator (256 of 512 columns) while the next tile fills the other.
+//   forward   A = x, B = 128 rows of Wg (from the first CTA) and the same rows of Wu (from the second): a row of the
+//             accumulator holds g and u of the same 128 units, so act(g) u is made where it is read
+//   dx        A = dg, then du; B = Wg, then Wu, with the output's columns contiguous (read as K x N)
+//   dW        A = dg or du as K x M, B = x as K x N; the two gradients are the two halves of the tiles
+//
+// k_glu_few serves up to 256 tokens, where the weights' bytes bound it: 128 rows of Wg and of Wu are the M side, the
+// tokens the N side (16 to 256), and the K axis is split over a cluster whose partial sums meet in
+// distributed shared memory in a fixed order.
+#pragma once
+
+#include "k_tc.cuh"
+#include "layer_common.cuh"
+#include "tma.cuh"
+
+namespace gdn {
+
+constexpr int kGluSilu = 0, kGluGelu = 1;
+
+// ------------------------------------------------------------- the activation
+// act(g) and act'(g).  gelu: 0.5 g (1 + tanh t) = g sigmoid(2 t), 2 t = sqrt(8 / pi) (g + 0.044715 g^3)
+__device__ __forceinline__ float glu_act(float g, int act)
+{
+    if (act == kGluSilu) return silu(g);
+    const float t = 1.5957691216057308f * __fmaf_rn(0.044715f * g * g, g, g);
+    return g * sigmoid(t);
+}
+__device__ __forceinline__ void glu_act2(float g, int act, float& a, float& slope)
+{
+    if (act == kGluSilu) {
+        const float s = sigmoid(g);
+        a = g * s;
+        slope = s * __fmaf_rn(g, 1.0f - s, 1.0f);
+        return;
+    }
+    const float g2 = g * g, s = sigmoid(1.5957691216057308f * __fmaf_rn(0.044715f * g2, g, g));
+    a = g * s;
+    slope = __fmaf_rn(a * (1.0f - s), 1.5957691216057308f * __fmaf_rn(0.134145f, g2, 1.0f), s);
+}
+
+// What the backward reads of the forward: g and u to 24 bits (15 of mantissa), as planes of 16-bit words
+// [3][rows][inner]: their upper halves, and the next bytes of both in one word.  In bf16 alone the
+// rounding of g and u would add to dg, du and the weights' gradients as much again as the rounding of the
+// products' operands; 24 bits leave 2^-15, for 6 bytes in place of 4 (fp32: 8).
+__device__ __forceinline__ void glu_pack(float g, float u, uint16_t& gh, uint16_t& uh, uint16_t& low)
+{
+    const uint32_t a = __float_as_uint(g), b = __float_as_uint(u);
+    gh = (uint16_t)(a >> 16);
+    uh = (uint16_t)(b >> 16);
+    low = (uint16_t)(((a >> 8) & 0xff) | (b & 0xff00));
+}
+__device__ __forceinline__ void glu_unpack(uint16_t gh, uint16_t uh, uint16_t low, float& g, float& u)
+{
+    g = __uint_as_float(((uint32_t)gh << 16) | ((uint32_t)(low & 0xff) << 8));
+    u = __uint_as_float(((uint32_t)uh << 16) | (low & 0xff00u));
+}
+
+// ------------------------------------------------------------- primitives
+__device__ __forceinline__ uint32_t cta_rank()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the address of this CTA's shared object in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank)
+{
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void mbar_arrive_peer(uint32_t cluster_addr)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// A tile of a matrix into this CTA's shared memory; its bytes count on the barrier at cluster address `mbar`, which
+// may be the pair's other CTA's.
+__device__ __forceinline__ void tma_pair_2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t mbar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(mbar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* mbar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(mbar))
+        : "memory");
+}
+template <int GROUP>
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    if constexpr (GROUP == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
+}
+// One arrival at the barrier of both CTAs of the pair when every product issued before is complete.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* mbar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_addr(mbar)), "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t a, float (&x)[16])
+{
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(a)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// Operand tiles lie as TMA leaves them with 128-byte swizzle.  K-major: rows of 64 k; the next 8 rows are
+// 1024 bytes on.  Otherwise (k by k rows of 64 columns): the next 8 k are 1024 bytes on, the next 64
+// columns a box of 64 k on.
+constexpr int kGluK = 64;                       // k per stage
+constexpr uint32_t kGluBox = kGluK * 128;       // bytes of a box of 64 columns by 64 k
+__device__ __forceinline__ uint64_t swizzled_desc(uint32_t addr, bool kmajor)
+{
+    const uint64_t lbo = kmajor ? 1 : kGluBox >> 4, sbo = 1024 >> 4;
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | (lbo << 16) | (sbo << 32) | (1ull << 46) | (2ull << 61);
+}
+// bytes from one step of 16 k to the next
+__device__ __forceinline__ uint32_t k16_bytes(bool kmajor) { return kmajor ? 32 : 2048; }
+// fp32 accumulators, bf16 operands
+__host__ __device__ constexpr uint32_t bf16_idesc(int m, int n, bool a_kmajor, bool b_kmajor)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((a_kmajor ? 0u : 1u) << 15) | ((b_kmajor ? 0u : 1u) << 16) |
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// ------------------------------------------------------------- the pair's product
+enum GluMode { kGluFwd = 0, kGluDx = 1, kGluDw = 2 };
+
+struct GluMaps {
+    CUtensorMap a[2], b[2];
+};
+
+struct GluGemmArgs {
+    int64_t M, N;        // of the output (forward: tokens and units)
+    int32_t ksteps;      // stages of one part of K
+    int32_t parts;       // dx: 2 (dg, then du)
+    int32_t tiles_m, tiles_n, problems, splits;
+    int64_t tiles;       // tiles_m tiles_n problems splits
+    void* out[2];
+    int32_t vec;         // rows of the outputs start at 16-byte boundaries
+    uint16_t* saved;     // forward: planes [3][M][N], or null
+    float* partial;      // splits > 1: [problems][splits][M][N]
+    int32_t act, out_f32;
+    int32_t* status;
+};
+
+struct GluTile {
+    int64_t m, n;  // first row (of the pair) and first column
+    int problem, split, k0, k1;
+};
+
+constexpr int kGluStages = 6;
+constexpr uint32_t kGluOperand = 128 * kGluK * 2;  // bytes of one operand of one CTA in a stage
+constexpr int kGluThreads = 256;
+constexpr size_t kGluSmem = (size_t)kGluStages * 2 * kGluOperand + 1024 + 256;
+
+// Tiles in groups of 8 rows of tiles, down the rows first: what is on the chip at a time shares few rows and columns.
+template <int MODE>
+__device__ __forceinline__ GluTile glu_tile(const GluGemmArgs& a, int64_t id)
+{
+    GluTile t;
+    const int64_t per = (int64_t)a.tiles_m * a.tiles_n;
+    const int64_t ps = id / per;
+    int64_t i = id - ps * per;
+    t.problem = (int)(ps / a.splits);
+    t.split = (int)(ps - (int64_t)t.problem * a.splits);
+    const int64_t group = i / (8 * (int64_t)a.tiles_n);
+    const int64_t rows = min((int64_t)8, a.tiles_m - group * 8);
+    i -= group * 8 * a.tiles_n;
+    t.m = (group * 8 + i % rows) * 256;
+    t.n = (i / rows) * (MODE == kGluFwd ? 128 : 256);
+    const int64_t all = (int64_t)a.ksteps * a.parts;
+    t.k0 = (int)(all * t.split / a.splits);
+    t.k1 = (int)(all * (t.split + 1) / a.splits);
+    return t;
+}
+
+// 16 values of a row as bf16, or fp32, from column c of a row of n
+template <typename OT>
+__device__ __forceinline__ void glu_store16(OT* row, const float (&x)[16], int64_t c, int64_t n, bool vec)
+{
+    constexpr int V = 16 / (int)sizeof(OT);
+    if (vec && c + 16 <= n) {
+#pragma unroll
+        for (int i = 0; i < 16; i += V) store_vec<OT, V>(row + c + i, x + i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (c + i < n) row[c + i] = from_f<OT>(x[i]);
+    }
+}
+__device__ __forceinline__ void glu_save16(uint16_t* row, const uint16_t (&x)[16], int64_t c, int64_t n, bool vec)
+{
+    if (vec && c + 16 <= n) {
+        const uint4* v = reinterpret_cast<const uint4*>(x);
+        *reinterpret_cast<uint4*>(row + c) = v[0];
+        *reinterpret_cast<uint4*>(row + c + 8) = v[1];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (c + i < n) row[c + i] = x[i];
+    }
+}
+
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGluThreads, 1)
+    k_glu_gemm(const __grid_constant__ GluMaps maps, const GluGemmArgs a)
+{
+    constexpr bool AK = MODE != kGluDw, BK = MODE == kGluFwd;  // which operands are K-major
+    constexpr int ST = kGluStages;
+    constexpr uint32_t IDESC = bf16_idesc(256, 256, AK, BK);
+    extern __shared__ unsigned char glu_smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(glu_smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + ST * 2 * kGluOperand);  // [ST] used in the first CTA
+    uint64_t* empty = full + ST;      // [ST] one per CTA
+    uint64_t* done = empty + ST;      // [2] the accumulators are complete
+    uint64_t* drained = done + 2;     // [2] used in the first CTA: both CTAs have read an accumulator
+    uint32_t* slot = reinterpret_cast<uint32_t*>(drained + 2);
+    const uint32_t rank = cta_rank();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(done + i, 1);
+            mbar_init(drained + i, 8);
+        }
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)), "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    cluster_barrier();
+    tc_fence_after();
+    const uint32_t tmem = *slot;
+    const int64_t step = gridDim.x / 2, first = blockIdx.x / 2;
+    bool ok = true;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---- both CTAs: their halves of the operands
+            int s = 0;
+            uint32_t ph = 1;  // the stages start empty
+            for (int64_t id = first; id < a.tiles && ok; id += step) {
+                const GluTile t = glu_tile<MODE>(a, id);
+                for (int k = t.k0; k < t.k1; ++k) {
+                    if (!(ok = mbar_wait(empty + s, ph))) break;
+                    unsigned char* sa = smem + s * 2 * kGluOperand;
+                    unsigned char* sb = sa + kGluOperand;
+                    const int part = k / a.ksteps, kk = (k - part * a.ksteps) * kGluK;
+                    const uint32_t bar = peer_addr(full + s, 0);
+                    if (rank == 0) mbar_arrive_expect_tx(full + s, 4 * kGluOperand);
+                    const int m = (int)t.m + (int)rank * 128;
+                    if constexpr (AK) {
+                        tma_pair_2d(sa, &maps.a[part], kk, m, bar);
+                    } else {
+                        tma_pair_2d(sa, &maps.a[t.problem], m, kk, bar);
+                        tma_pair_2d(sa + kGluBox, &maps.a[t.problem], m + 64, kk, bar);
+                    }
+                    if constexpr (MODE == kGluFwd) {
+                        tma_pair_2d(sb, &maps.b[rank], kk, (int)t.n, bar);
+                    } else {
+                        const int n = (int)t.n + (int)rank * 128, which = MODE == kGluDx ? part : 0;
+                        tma_pair_2d(sb, &maps.b[which], n, kk, bar);
+                        tma_pair_2d(sb + kGluBox, &maps.b[which], n + 64, kk, bar);
+                    }
+                    if (++s == ST) s = 0, ph ^= 1;
+                }
+            }
+            // every stage has been released: no arrival is under way to a CTA that has ended
+            for (int i = 0; i < ST && ok; ++i) {
+                ok = mbar_wait(empty + s, ph);
+                if (++s == ST) s = 0, ph ^= 1;
+            }
+        }
+    } else if (warp == 1 && rank == 0) {
+        if (lane == 0) {
+            // ---- the first CTA: the products of both
+            int s = 0;
+            uint32_t ph = 0, acc = 0, acc_ph = 1;
+            for (int64_t id = first; id < a.tiles && ok; id += step) {
+                const GluTile t = glu_tile<MODE>(a, id);
+                if (!(ok = mbar_wait(drained + acc, acc_ph))) break;
+                tc_fence_after();
+                const uint32_t d = tmem + acc * 256;
+                for (int k = t.k0; k < t.k1; ++k) {
+                    if (!(ok = mbar_wait(full + s, ph))) break;
+                    tc_fence_after();
+                    const uint32_t sa = smem_addr(smem + s * 2 * kGluOperand);
+                    const uint64_t da = swizzled_desc(sa, AK), db = swizzled_desc(sa + kGluOperand, BK);
+#pragma unroll
+                    for (int j = 0; j < kGluK / 16; ++j)
+                        mma_bf16<2>(d, da + j * (k16_bytes(AK) >> 4), db + j * (k16_bytes(BK) >> 4), IDESC, k > t.k0 || j > 0);
+                    mma_commit_pair(empty + s);
+                    if (++s == ST) s = 0, ph ^= 1;
+                }
+                if (!ok) break;
+                mma_commit_pair(done + acc);
+                if (++acc == 2) acc = 0, acc_ph ^= 1;
+            }
+        }
+    } else if (warp >= 4) {
+        // ---- both CTAs: accumulators to memory.  Thread: row 32 (warp % 4) + lane of this CTA's 128.
+        uint32_t acc = 0, ph = 0;
+        const int64_t r0 = (int64_t)rank * 128 + 32 * (warp - 4) + lane;
+        for (int64_t id = first; id < a.tiles; id += step) {
+            const GluTile t = glu_tile<MODE>(a, id);
+            ok = mbar_wait(done + acc, ph);
+            if (!(ok = __all_sync(kFullMask, ok))) break;
+            tc_fence_after();
+            const uint32_t col = tmem + ((uint32_t)(32 * (warp - 4)) << 16) + acc * 256;
+            const int64_t row = t.m + r0;
+            const bool on = row < a.M;
+            if constexpr (MODE == kGluFwd) {
+                __nv_bfloat16* h = static_cast<__nv_bfloat16*>(a.out[0]) + row * a.N;
+                for (int c = 0; c < 128; c += 16) {
+                    float g[16], u[16];
+                    tmem_ld16(col + c, g);
+                    tmem_ld16(col + 128 + c, u);
+                    tmem_wait_ld();
+                    if (on && t.n + c < a.N) {
+                        if (a.saved != nullptr) {
+                            alignas(16) uint16_t gh[16], uh[16], low[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) glu_pack(g[i], u[i], gh[i], uh[i], low[i]);
+                            glu_save16(a.saved + row * a.N, gh, t.n + c, a.N, a.vec);
+                            glu_save16(a.saved + (a.M + row) * a.N, uh, t.n + c, a.N, a.vec);
+                            glu_save16(a.saved + (2 * a.M + row) * a.N, low, t.n + c, a.N, a.vec);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) g[i] = glu_act(g[i], a.act) * u[i];
+                        glu_store16(h, g, t.n + c, a.N, a.vec);
+                    }
+                    __syncwarp();  // the next read of tensor memory is the whole warp's
+                }
+            } else {
+                const int64_t at = row * a.N;
+                void* out = t.problem ? a.out[1] : a.out[0];
+                float* part = a.partial + ((int64_t)t.problem * a.splits + t.split) * a.M * a.N + at;
+                for (int c = 0; c < 256; c += 16) {
+                    float x[16];
+                    tmem_ld16(col + c, x);
+                    tmem_wait_ld();
+                    if (on && t.n + c < a.N) {
+                        if (a.splits > 1) glu_store16(part, x, t.n + c, a.N, a.N % 4 == 0);
+                        else if (a.out_f32) glu_store16(static_cast<float*>(out) + at, x, t.n + c, a.N, a.vec);
+                        else glu_store16(static_cast<__nv_bfloat16*>(out) + at, x, t.n + c, a.N, a.vec);
+                    }
+                    __syncwarp();
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_peer(peer_addr(drained + acc, 0));
+            if (++acc == 2) acc = 0, ph ^= 1;
+        }
+    }
+    if (!ok && lane == 0 && a.status != nullptr) atomicCAS(a.status, GDN_OK, GDN_ERR_TIMEOUT);
+    __syncwarp();
+    cluster_barrier();
+    if (warp == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+}
+
+// ------------------------------------------------------------- few tokens
+struct GluFewArgs {
+    int32_t T, F, ksteps;
+    void* h;
+    uint16_t* saved;
+    int32_t act;
+    int32_t* status;
+};
+
+struct GluFewMaps {
+    CUtensorMap x, wg, wu;
+};
+
+template <int NB>
+struct GluFew {
+    static constexpr uint32_t STAGE = 2 * kGluOperand + NB * 128;
+    // two CTAs per SM up to 128 tokens
+    static constexpr int STAGES = NB <= 32 ? 3 : NB <= 128 ? 2 : 3;
+    static constexpr int CHUNK = NB < 32 ? NB : 32;                        // tokens that meet at a time
+    static constexpr uint32_t COLS = 2 * NB < 32 ? 32 : 2 * NB;            // of tensor memory
+    static constexpr size_t SMEM = (size_t)STAGES * STAGE + 1024 + 128;
+    static_assert((size_t)2 * CHUNK * 128 * 4 <= (size_t)STAGES * STAGE, "the partial sums lie where the operands were");
+};
+
+template <int NB>
+__global__ void __launch_bounds__(kGluThreads, 1) k_glu_few(const __grid_constant__ GluFewMaps maps, const GluFewArgs a)
+{
+    using G = GluFew<NB>;
+    constexpr int ST = G::STAGES, CH = G::CHUNK;
+    constexpr uint32_t IDESC = bf16_idesc(128, NB, true, true);
+    extern __shared__ unsigned char glu_smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(glu_smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + ST * G::STAGE);
+    uint64_t* empty = full + ST;
+    uint64_t* done = empty + ST;
+    uint32_t* slot = reinterpret_cast<uint32_t*>(done + 1);
+    uint32_t S;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(S));
+    const uint32_t rank = cta_rank();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int f0 = (int)(blockIdx.x / S) * 128;
+    const int k0 = (int)((int64_t)a.ksteps * rank / S), k1 = (int)((int64_t)a.ksteps * (rank + 1) / S);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, 1);
+        }
+        mbar_init(done, 1);
+    }
+    if (warp == 2) tmem_alloc(slot, G::COLS);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *slot;
+    bool ok = true;
+    if (warp == 0) {
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 1;
+            for (int k = k0; k < k1; ++k) {
+                if (!(ok = mbar_wait(empty + s, ph))) break;
+                unsigned char* p = smem + s * G::STAGE;
+                mbar_arrive_expect_tx(full + s, G::STAGE);
+                tma_2d(p, &maps.wg, k * kGluK, f0, full + s);
+                tma_2d(p + kGluOperand, &maps.wu, k * kGluK, f0, full + s);
+                tma_2d(p + 2 * kGluOperand, &maps.x, k * kGluK, 0, full + s);
+                if (++s == ST) s = 0, ph ^= 1;
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 0;
+            for (int k = k0; k < k1; ++k) {
+                if (!(ok = mbar_wait(full + s, ph))) break;
+                tc_fence_after();
+                const uint32_t p = smem_addr(smem + s * G::STAGE);
+                const uint64_t dg = swizzled_desc(p, true), du = swizzled_desc(p + kGluOperand, true),
+                               dx = swizzled_desc(p + 2 * kGluOperand, true);
+#pragma unroll
+                for (int j = 0; j < kGluK / 16; ++j) {
+                    mma_bf16<1>(tmem, dg + 2 * j, dx + 2 * j, IDESC, k > k0 || j > 0);
+                    mma_bf16<1>(tmem + NB, du + 2 * j, dx + 2 * j, IDESC, k > k0 || j > 0);
+                }
+                mma_commit(empty + s);
+                if (++s == ST) s = 0, ph ^= 1;
+            }
+            mma_commit(done);
+        }
+    }
+    __syncwarp();
+    // every thread: the operands are no longer read once the accumulators are complete
+    if (!mbar_wait(done, 0)) ok = false;
+    tc_fence_after();
+    ok = __syncthreads_and(ok);
+    const bool none = k0 >= k1;
+    const int r = 32 * (warp & 3) + lane, f = f0 + r;  // this thread's unit
+    const uint32_t col = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    auto finish = [&](int t, float g, float u) {
+        if (t >= a.T || f >= a.F) return;
+        const int64_t at = (int64_t)t * a.F + f;
+        if (a.saved != nullptr) {
+            const int64_t plane = (int64_t)a.T * a.F;
+            glu_pack(g, u, a.saved[at], a.saved[plane + at], a.saved[2 * plane + at]);
+        }
+        static_cast<__nv_bfloat16*>(a.h)[at] = __float2bfloat16_rn(glu_act(g, a.act) * u);
+    };
+    // a wait that ran out leaves the outputs as they are; the cluster's barriers are passed all the same
+    float* part = reinterpret_cast<float*>(smem);  // [2][CH][128]
+    for (int c = 0; c < NB && c < a.T; c += CH) {
+        if (warp < 4) {
+#pragma unroll 1
+            for (int i = 0; i < CH; i += 16) {
+                float g[16], u[16];
+                tmem_ld16(col + c + i, g);
+                tmem_ld16(col + NB + c + i, u);
+                tmem_wait_ld();
+                if (none) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) g[j] = u[j] = 0.0f;
+                }
+                if (S == 1) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (ok) finish(c + i + j, g[j], u[j]);
+                    __syncwarp();
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        part[(i + j) * 128 + r] = g[j];
+                        part[(CH + i + j) * 128 + r] = u[j];
+                    }
+                }
+            }
+        }
+        if (S > 1) {
+            cluster_barrier();
+            // token by token round the cluster; two of them at a time in a block
+            for (int t = (int)rank * 2 + (warp >> 2); t < CH; t += (int)S * 2) {
+                float g = 0.0f, u = 0.0f;
+                for (uint32_t q = 0; q < S; ++q) {
+                    const uint32_t p = peer_addr(part + t * 128 + r, q);
+                    float x, y;
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(p) : "memory");
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(y) : "r"(p + CH * 128 * 4) : "memory");
+                    g += x;
+                    u += y;
+                }
+                if (ok) finish(c + t, g, u);
+            }
+            cluster_barrier();
+        }
+    }
+    if (!ok && threadIdx.x == 0 && a.status != nullptr) atomicCAS(a.status, GDN_OK, GDN_ERR_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) tmem_dealloc(tmem, G::COLS);
+}
+
+// ------------------------------------------------------------- elementwise parts
+// dg and du, rows ld apart, from dh and what the forward saved; columns from F to ld are not read by anyone.
+template <int V>
+__global__ void __launch_bounds__(256) k_glu_grad(const __nv_bfloat16* __restrict__ dh, int64_t lddh,
+                                                  const uint16_t* __restrict__ saved, int64_t T, int64_t F, int act,
+                                                  __nv_bfloat16* __restrict__ dg, __nv_bfloat16* __restrict__ du, int64_t ld)
+{
+    const int64_t per = (F + V - 1) / V, n = T * per, plane = T * F;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t t = i / per, c = (i - t * per) * V;
+        const Vec<__nv_bfloat16, V> d = load_vec<__nv_bfloat16, V>(dh + t * lddh + c);
+        const uint16_t* s = saved + t * F + c;
+        const Vec<uint16_t, V> gh = load_vec<uint16_t, V>(s), uh = load_vec<uint16_t, V>(s + plane),
+                               low = load_vec<uint16_t, V>(s + 2 * plane);
+        float x[V], y[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            float g, u, f, slope;
+            glu_unpack(gh.v[k], uh.v[k], low.v[k], g, u);
+            glu_act2(g, act, f, slope);
+            const float e = to_f<__nv_bfloat16>(d.v[k]);
+            x[k] = e * u * slope;
+            y[k] = e * f;
+        }
+        store_vec<__nv_bfloat16, V>(dg + t * ld + c, x);
+        store_vec<__nv_bfloat16, V>(du + t * ld + c, y);
+    }
+}
+
+// A matrix whose rows are not whole 16 bytes, into rows that are (ldd: a multiple of 8).
+__global__ void __launch_bounds__(256) k_glu_align(const uint16_t* __restrict__ src, int64_t lds, int64_t rows, int64_t cols,
+                                                   uint16_t* __restrict__ dst, int64_t ldd)
+{
+    const int64_t per = ldd / 8, n = rows * per;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / per, c = (i - r * per) * 8;
+        Vec<uint16_t, 8> v;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v.v[k] = c + k < cols ? src[r * lds + c + k] : (uint16_t)0;
+        *reinterpret_cast<Vec<uint16_t, 8>*>(dst + r * ldd + c) = v;
+    }
+}
+
+// The sums of the splits' partial products, in ascending order.
+template <typename OT>
+__global__ void __launch_bounds__(256) k_glu_join(const float* __restrict__ part, int splits, int64_t n, OT* __restrict__ out0,
+                                                  OT* __restrict__ out1, int problems)
+{
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n * problems; i += (int64_t)gridDim.x * 256) {
+        const int64_t p = i / n, e = i - p * n;
+        const float* s = part + p * splits * n + e;
+        float x = 0.0f;
+        for (int k = 0; k < splits; ++k) x += s[k * n];
+        (p ? out1 : out0)[e] = from_f<OT>(x);
+    }
+}
+
+}  // namespace gdn

@@ -36,6 +36,8 @@ SYMBOLS = ("gdn_contract_id", "gdn_status_string", "gdn_num_chunk_states", "gdn_
            "gdn_ssm_backward_workspace_size", "gdn_ssm_backward", "gdn_ssm_step",
            "gdn_layer_norm_forward", "gdn_layer_norm_backward_workspace_size", "gdn_layer_norm_backward",
            "gdn_qk_norm_forward", "gdn_qk_norm_backward_workspace_size", "gdn_qk_norm_backward",
+           "gdn_glu_saved_size", "gdn_glu_forward_workspace_size", "gdn_glu_forward",
+           "gdn_glu_backward_workspace_size", "gdn_glu_backward",
            "gdn_policy_loss_forward", "gdn_policy_loss_backward")
 
 #: gdn_identity_kind_t
@@ -73,6 +75,12 @@ class QkNormStruct(ctypes.Structure):
                [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "tokens")] + \
                [(n, ctypes.c_int32) for n in ("q_heads", "k_heads", "head_dim", "rot_dim", "interleaved", "unit")] + \
                [("eps", ctypes.c_float)] + [(n, ctypes.c_int32) for n in ("in_dtype", "w_dtype")]
+
+
+class GluStruct(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "w_gate", "w_up")] + \
+               [(n, ctypes.c_int64) for n in ("x_stride", "gate_stride", "up_stride", "rows")] + \
+               [(n, ctypes.c_int32) for n in ("width", "inner", "act", "in_dtype")]
 
 
 class PolicyStruct(ctypes.Structure):
@@ -168,6 +176,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.gdn_qk_norm_backward_workspace_size.argtypes = [i64, i32]
     lib.gdn_qk_norm_backward.restype = e
     lib.gdn_qk_norm_backward.argtypes = [qk, P, i64, P, i64, P, P, P, P, P, sz, P]
+    glu = ctypes.POINTER(GluStruct)
+    lib.gdn_glu_saved_size.restype = i64
+    lib.gdn_glu_saved_size.argtypes = [i64, i32]
+    lib.gdn_glu_forward_workspace_size.restype = sz
+    lib.gdn_glu_forward_workspace_size.argtypes = [glu]
+    lib.gdn_glu_forward.restype = e
+    lib.gdn_glu_forward.argtypes = [glu, P, P, P, sz, P, P]
+    lib.gdn_glu_backward_workspace_size.restype = sz
+    lib.gdn_glu_backward_workspace_size.argtypes = [glu]
+    lib.gdn_glu_backward.restype = e
+    lib.gdn_glu_backward.argtypes = [glu, P, i64, P, P, P, P, e, P, sz, P, P]
     lib.gdn_policy_loss_forward.restype = e
     lib.gdn_policy_loss_forward.argtypes = [pol, P, P, P, P]
     lib.gdn_policy_loss_backward.restype = e
@@ -867,6 +886,82 @@ def gdn_qk_norm_backward(q, k, dq_out, dk_out, *, q_weight=None, k_weight=None, 
     _call(dev, what, load_library().gdn_qk_norm_backward, s, pgq, lgq, pgk, lgk, _dense(what, "dq", dq, ty, q.shape, dev),
           _dense(what, "dk", dk, ty, k.shape, dev), _opt(what, "dq_weight", dqw, _F32, (d,), dev),
           _opt(what, "dk_weight", dkw, _F32, (d,), dev), ws, nbytes)
+    return grads
+
+
+#: gdn_glu_t.act
+ACTS = {"silu": 0, "gelu": 1}
+
+
+def _glu_struct(what, x, w_gate, w_up, act, dev):
+    x2 = _rows2d(what, "x", x)
+    if w_gate.dim() != 2 or w_gate.shape[1] != x2.shape[1]:
+        raise ValueError(f"{what}: x must be [.., width] and w_gate, w_up [inner, width]")
+    if act not in ACTS:
+        raise ValueError(f"{what}: act must be one of {sorted(ACTS)}, not {act!r}")
+    R, D = x2.shape
+    F, ty = w_gate.shape[0], x.dtype
+    ti = _type(what, x)
+    px, lx = _rows(what, "x", x2, ty, (R, D), dev)
+    pg, lg = _rows(what, "w_gate", w_gate, ty, (F, D), dev)
+    pu, lu = _rows(what, "w_up", w_up, ty, (F, D), dev)
+    return GluStruct(px, pg, pu, lx, lg, lu, R, D, F, ACTS[act], ti)
+
+
+def _glu_scratch(what, workspace, size, s, dev):
+    """As _scratch, for sizes that follow from the addresses; nothing is allocated where nothing is needed."""
+    if torch.cuda.current_device() == dev:
+        n = size(s)
+    else:
+        with torch.cuda.device(dev):
+            n = size(s)
+    return _scratch(what, workspace, n, dev) if n else (None, None, 0)
+
+
+def gdn_glu_forward(x, w_gate, w_up, *, act: str = "silu", save: bool = False, h=None, saved=None, workspace=None, status=None):
+    """The gated feed-forward block's projections, activation and product (gdn_glu_forward):
+        h = act(x w_gate^T) (x w_up^T)
+
+    x [.., width], w_gate, w_up [inner, width], bf16 (rows may be strided: the weights may be halves of one matrix); ``act``
+    "silu" or "gelu" (tanh form).  Returns (h [.., inner], saved): saved (with ``save``; else None) is what
+    :func:`gdn_glu_backward` reads, 6 bytes per element of h.  Single tokens of a decode step are rows like any
+    other.  ``status``: an optional int32 that records a wait that ran out."""
+    what = "gdn_glu_forward"
+    dev = _gpu(what, x)
+    s = _glu_struct(what, x, w_gate, w_up, act, dev)
+    R, F = s.rows, s.inner
+    h, ph = _out(what, "h", h, x.dtype, x.shape[:-1] + (F,), dev)
+    if saved is None and save:
+        saved = torch.empty((6 * R * F,), dtype=torch.uint8, device=dev)
+    lib = load_library()
+    keep, ws, nbytes = _glu_scratch(what, workspace, lib.gdn_glu_forward_workspace_size, s, dev)
+    _call(dev, what, lib.gdn_glu_forward, s, ph, _opt(what, "saved", saved, torch.uint8, (6 * R * F,), dev), ws, nbytes,
+          _opt(what, "status", status, torch.int32, (1,), dev))
+    return h, saved
+
+
+def gdn_glu_backward(x, w_gate, w_up, dh, saved, *, act: str = "silu", workspace=None, grads=None, status=None):
+    """Gradients of sum(dh h) for :func:`gdn_glu_forward` of the same inputs with ``save``.
+
+    dh [.., inner] in x's type (rows may be strided).  Returns (dx in x's shape, dw_gate, dw_up), in x's type.
+    ``grads``: an optional tuple of those three to write into; the weights' gradients may then be fp32 (both)."""
+    what = "gdn_glu_backward"
+    dev = _gpu(what, x)
+    s = _glu_struct(what, x, w_gate, w_up, act, dev)
+    R, D, F, ty = s.rows, s.width, s.inner, x.dtype
+    if dh.shape != x.shape[:-1] + (F,):
+        raise ValueError(f"{what}: dh must have shape {tuple(x.shape[:-1]) + (F,)}, not {tuple(dh.shape)}")
+    pd, ld = _rows(what, "dh", _rows2d(what, "dh", dh), ty, (R, F), dev)
+    if grads is None:
+        grads = tuple(torch.empty(n, dtype=ty, device=dev) for n in (x.shape, (F, D), (F, D)))
+    dx, dwg, dwu = grads
+    wt = dwg.dtype
+    lib = load_library()
+    keep, ws, nbytes = _glu_scratch(what, workspace, lib.gdn_glu_backward_workspace_size, s, dev)
+    _call(dev, what, lib.gdn_glu_backward, s, pd, ld, _dense(what, "saved", saved, torch.uint8, (6 * R * F,), dev),
+          _dense(what, "dx", dx, ty, x.shape, dev), _dense(what, "dw_gate", dwg, wt, (F, D), dev),
+          _dense(what, "dw_up", dwu, wt, (F, D), dev), _type(what, dwg), ws, nbytes,
+          _opt(what, "status", status, torch.int32, (1,), dev))
     return grads
 
 

@@ -450,7 +450,7 @@ gdn_status_t gdn_cpr_forward_noalloc(const void* q, const void* k, const void* v
  * The operators around the recurrence, for prefill, training and decode: the short causal
  * convolution in front of a recurrent mixer, the selective state space scan (a mixer of
  * its own kind, with a diagonal decay per channel and state), layer norm, the norm of queries and
- * keys with the position rotation, and the clipped policy loss.
+ * keys with the position rotation, the gated feed-forward block, and the clipped policy loss.
  * They take the conventions at the top of this file, with these differences:
  *  - Token tensors ([T, channels], [T, G, S]) may be views of wider rows, such as the slices
  *    of one projection's output: `*_stride` is the distance between tokens in
@@ -634,6 +634,49 @@ size_t gdn_qk_norm_backward_workspace_size(int64_t tokens, int32_t head_dim);
 gdn_status_t gdn_qk_norm_backward(const gdn_qk_norm_t* args, const void* dq_out, int64_t dq_out_stride, const void* dk_out,
                                   int64_t dk_out_stride, void* dq, void* dk, float* dq_weight, float* dk_weight,
                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The gated feed-forward block's projections, activation and product:
+ *   h = act(x Wg^T) (x Wu^T),  act = silu, or gelu in its tanh form
+ *   x [rows, width], w_gate and w_up [inner, width] in in_dtype, rows *_stride apart (the two weights may be halves of
+ *     one [2 inner, width] matrix); in_dtype bf16 (fp32: GDN_ERR_UNSUPPORTED: the products are the tensor cores')
+ *   h [rows, inner] in in_dtype, dense
+ *   saved: what gdn_glu_backward reads, gdn_glu_saved_size() = 6 rows inner bytes (both projections to 24
+ *     bits), 16-byte aligned; NULL where no backward follows
+ *   workspace: gdn_glu_forward_workspace_size(args) bytes, 0 where every row of x and of the weights starts at a
+ *     multiple of 16 bytes: other ones are copied first
+ * Products of bf16 values are summed in fp32, act and the product are fp32, h is rounded once.  A single token of each of
+ * up to 256 sequences is bound by the weights' bytes and takes a path of its own.
+ * *status (one int32 on the device, or NULL) becomes GDN_ERR_TIMEOUT when a wait inside the kernel runs
+ * out (about a second): the outputs are then unspecified.
+ */
+#define GDN_ACT_SILU 0
+#define GDN_ACT_GELU 1
+typedef struct {
+    const void *x, *w_gate, *w_up;
+    int64_t x_stride, gate_stride, up_stride, rows;
+    int32_t width, inner;
+    int32_t act;
+    gdn_dtype_t in_dtype;
+} gdn_glu_t;
+
+/* Bytes of `saved`; -1 for invalid sizes. */
+int64_t gdn_glu_saved_size(int64_t rows, int32_t inner);
+size_t gdn_glu_forward_workspace_size(const gdn_glu_t* args);
+gdn_status_t gdn_glu_forward(const gdn_glu_t* args, void* h, void* saved, void* workspace, size_t workspace_bytes,
+                             int32_t* status, void* stream);
+
+/*
+ * Gradients of sum(dh h): dx [rows, width] in in_dtype, dw_gate and dw_up [inner, width] in dw_dtype (bf16 or
+ * fp32), all dense.  dh [rows, inner] in in_dtype, rows dh_stride apart; saved: as the forward of these
+ * inputs wrote it.  The gradients of the two projections are rounded to bf16, as the tensor cores'
+ * operands.  The workspace's size (at least 4 rows inner bytes) depends on the addresses' alignment and the
+ * current device.
+ */
+size_t gdn_glu_backward_workspace_size(const gdn_glu_t* args);
+gdn_status_t gdn_glu_backward(const gdn_glu_t* args, const void* dh, int64_t dh_stride, const void* saved, void* dx,
+                              void* dw_gate, void* dw_up, gdn_dtype_t dw_dtype, void* workspace, size_t workspace_bytes,
+                              int32_t* status, void* stream);
 
 /*
  * Clipped policy loss with a KL term, for each row (token) of logits z [rows, vocab] in in_dtype, rows
