@@ -127,18 +127,14 @@ PolicyPlan policy_plan(gdn::PolicyArgs& a, gdn_dtype_t t)
     return p;
 }
 
-template <typename T, bool BWD>
-gdn_status_t policy_launch(gdn::PolicyArgs& a, gdn_dtype_t t, cudaStream_t st)
+template <typename T, bool BWD, bool ALIGNED>
+gdn_status_t policy_run(const gdn::PolicyArgs& a, const PolicyPlan& p, cudaStream_t st)
 {
-    const PolicyPlan p = policy_plan(a, t);
     const int sms = sm_count();
     if (sms == 0) return GDN_ERR_CUDA;
-    auto k = gdn::k_policy<T, BWD>;
+    auto k = gdn::k_policy<T, BWD, ALIGNED>;
     if (!raise_smem(k, p.smem)) return GDN_ERR_CUDA;
-    const int per_sm = (int)std::min<size_t>(1024 / p.threads, (size_t)(220 * 1024) / (p.smem + 2048));
-    const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(a.T, (int64_t)sms * std::max(1, per_sm) / p.cluster));
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(clusters * p.cluster));
     cfg.blockDim = dim3((unsigned)p.threads);
     cfg.dynamicSmemBytes = p.smem;
     cfg.stream = st;
@@ -148,7 +144,28 @@ gdn_status_t policy_launch(gdn::PolicyArgs& a, gdn_dtype_t t, cudaStream_t st)
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k, (const gdn::PolicyArgs&)a) == cudaSuccess && launched() ? GDN_OK : GDN_ERR_CUDA;
+    // As many clusters as are resident at a time, each with its share of the rows.  Clusters keep to a
+    // group of SMs, so that fewer fit than the SMs' sum suggests, and one that waits for another's end doubles the time.
+    const int per_sm = (int)std::min<size_t>(1024 / p.threads, (size_t)(220 * 1024) / (p.smem + 2048));
+    int64_t clusters = std::max<int64_t>(1, (int64_t)sms * std::max(1, per_sm) / p.cluster);
+    if (a.T * 2 <= clusters) {
+        clusters = a.T;
+    } else {
+        cfg.gridDim = dim3((unsigned)(clusters * p.cluster));
+        int fit = 0;
+        if (cudaOccupancyMaxActiveClusters(&fit, k, &cfg) != cudaSuccess || fit <= 0) return GDN_ERR_CUDA;
+        clusters = std::min<int64_t>(fit, a.T);
+    }
+    cfg.gridDim = dim3((unsigned)(clusters * p.cluster));
+    return cudaLaunchKernelEx(&cfg, k, a) == cudaSuccess && launched() ? GDN_OK : GDN_ERR_CUDA;
+}
+
+template <typename T, bool BWD>
+gdn_status_t policy_launch(gdn::PolicyArgs& a, gdn_dtype_t t, cudaStream_t st)
+{
+    const PolicyPlan p = policy_plan(a, t);
+    return wide(a.z, a.ldz, a.V, t) && wide(a.dz, a.V, a.V, t) ? policy_run<T, BWD, true>(a, p, st)
+                                                               : policy_run<T, BWD, false>(a, p, st);
 }
 
 gdn::PolicyArgs policy_args(const gdn_policy_t* s, int32_t* status)

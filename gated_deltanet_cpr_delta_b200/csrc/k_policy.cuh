@@ -85,17 +85,53 @@ __device__ __forceinline__ uint4 bytes_at(const uint4& a, const uint4& b, int s)
                       __funnelshift_r(v[2], v[3], sh), __funnelshift_r(v[3], v[4], sh));
 }
 
-// a sum s of 2^(x - m) taken over to the maximum M; maxima of -inf (nothing yet) count as 0
+// maxima of -inf (nothing yet, or nothing but -inf) count as 0 where they are taken off an exponent
 __device__ __forceinline__ float policy_base(float m) { return m == -INFINITY ? 0.0f : m; }
 
-template <typename T, bool BWD>
+// The largest of a thread's packed values.
+template <typename T, int E>
+struct PolicyMax;
+template <>
+struct PolicyMax<__nv_bfloat16, 8> {
+    __nv_bfloat162 m = __float2bfloat162_rn(-INFINITY);
+    __device__ __forceinline__ void add(const Vec<__nv_bfloat16, 8>& v)
+    {
+        const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&v);
+        m = __hmax2(m, __hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3])));
+    }
+    __device__ __forceinline__ float get() const { return fmaxf(__low2float(m), __high2float(m)); }
+};
+template <>
+struct PolicyMax<float, 4> {
+    float m = -INFINITY;
+    __device__ __forceinline__ void add(const Vec<float, 4>& v)
+    {
+        m = fmaxf(m, fmaxf(fmaxf(v.v[0], v.v[1]), fmaxf(v.v[2], v.v[3])));
+    }
+    __device__ __forceinline__ float get() const { return m; }
+};
+
+// The maximum and the sum of 2^(x - maximum) over a warp, from each lane's own; the same in every lane.
+__device__ __forceinline__ void policy_warp(float& m, float& sum)
+{
+    float M = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
+    sum *= ex2(m - policy_base(M));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFullMask, sum, o);
+    m = M;
+}
+
+// ALIGNED: every row of the logits and of the gradient is whole 16-byte vectors.
+template <typename T, bool BWD, bool ALIGNED>
 __global__ void __launch_bounds__(kPolicyMaxThreads, 1) k_policy(const PolicyArgs a)
 {
     constexpr int E = 16 / (int)sizeof(T);  // elements of a vector
     constexpr int NV = kPolicyVecs;
     extern __shared__ __align__(128) unsigned char policy_smem[];  // the slice at its global address mod 16
     __shared__ __align__(8) uint64_t bar;
-    __shared__ float wm[32], ws[32];                    // maxima and sums of the warps
+    __shared__ float wm[32], ws[32], target_logit;      // maxima and sums of the warps
     __shared__ float peer[2][kPolicyMaxCluster][3];     // of the cluster's blocks, and the target's logit; by row parity
     const uint32_t rank = cluster_rank(), blocks = cluster_size();
     const int64_t first = blockIdx.x / blocks, step = gridDim.x / blocks;
@@ -114,21 +150,24 @@ __global__ void __launch_bounds__(kPolicyMaxThreads, 1) k_policy(const PolicyArg
     // The slice's 16-byte granules in one copy; the up to 2 (E - 1) elements around them by threads 0 .. 2 E - 1.
     auto place = [&](int64_t row, int& s, int& head, int& body) {
         const uintptr_t p = reinterpret_cast<uintptr_t>(static_cast<const T*>(a.z) + row * a.ldz + lo);
-        s = (int)(p & 15);
+        s = ALIGNED ? 0 : (int)(p & 15);
         head = s ? min(len, (16 - s) / (int)sizeof(T)) : 0;
         body = (len - head) / E * E;
     };
     T edge{};  // an element that the copy does not cover
+    const int issuer = NT - 32;  // a thread of the last warp
     auto issue = [&](int64_t row) {
         int s, head, body;
         place(row, s, head, body);
         const T* src = static_cast<const T*>(a.z) + row * a.ldz + lo;
-        if (tid < E) {
-            if (tid < head) edge = src[tid];
-        } else if (tid < 2 * E) {
-            if (head + body + tid - E < len) edge = src[head + body + tid - E];
+        if constexpr (!ALIGNED) {
+            if (tid < E) {
+                if (tid < head) edge = src[tid];
+            } else if (tid < 2 * E) {
+                if (head + body + tid - E < len) edge = src[head + body + tid - E];
+            }
         }
-        if (tid == 0) {
+        if (tid == issuer) {
             mbar_arrive_expect_tx(&bar, (uint32_t)(body * sizeof(T)));
             if (body > 0) bulk_load(policy_smem + s + head * sizeof(T), src + head, (uint32_t)(body * sizeof(T)), &bar);
         }
@@ -139,106 +178,113 @@ __global__ void __launch_bounds__(kPolicyMaxThreads, 1) k_policy(const PolicyArg
     uint32_t parity = 0;
     int turn = 0;
     bool lost = false;
-    for (int64_t row = first; row < a.T; row += step, turn ^= 1) {
+    for (int64_t row = first; row < a.T; row += step) {
         const int64_t y_after = target(row + 2 * step);
-        if (y < 0) {  // nothing read; the same in every block of the cluster
+        if (y < 0) {  // nothing read, no exchange; the same in every block of the cluster
             if (rank == 0 && tid == 0) {
                 if (a.loss != nullptr) a.loss[row] = 0.0f;
                 if (a.lp != nullptr) a.lp[row] = 0.0f;
             }
             if constexpr (BWD) {
                 T* out = static_cast<T*>(a.dz) + row * a.V + lo;
-                for (int i = tid; i < len; i += NT) out[i] = from_f<T>(0.0f);
+                if constexpr (ALIGNED) {
+                    for (int i = tid; i < nvec; i += NT) *reinterpret_cast<uint4*>(out + i * E) = make_uint4(0, 0, 0, 0);
+                } else {
+                    for (int i = tid; i < len; i += NT) out[i] = from_f<T>(0.0f);
+                }
             }
             if (y_next >= 0 && !lost) issue(row + step);
             y = y_next, y_next = y_after;
-            turn ^= 1;  // no exchange in this row
             continue;
         }
-        int s, head, body;
-        place(row, s, head, body);
-        if (tid < 2 * E) {
+        // what the row's end needs, on its way from here on
+        const float old = a.old != nullptr ? a.old[row] : 0.0f, adv = a.old != nullptr ? a.adv[row] : 0.0f;
+        const float ref = a.ref != nullptr ? a.ref[row] : 0.0f, dloss = BWD ? a.dloss[row] : 0.0f;
+        int s = 0;
+        if constexpr (!ALIGNED) {
+            int head, body;
+            place(row, s, head, body);
             T* at = reinterpret_cast<T*>(policy_smem + s);
-            if (tid < head) at[tid] = edge;
-            else if (tid >= E && head + body + tid - E < len) at[head + body + tid - E] = edge;
+            if (tid < E) {
+                if (tid < head) at[tid] = edge;
+            } else if (tid < 2 * E) {
+                if (head + body + tid - E < len) at[head + body + tid - E] = edge;
+            } else if (tid < 3 * E) {  // the last vector is filled up with -inf
+                if (len + tid - 2 * E < nvec * E) at[len + tid - 2 * E] = from_f<T>(-INFINITY);
+            }
+            __syncthreads();
         }
         if (!lost && !mbar_wait_bounded(&bar, parity, 1ll << 31)) lost = true;
         parity ^= 1;
-        lost = __syncthreads_or(lost);
-        if (lost && tid == 0 && a.status != nullptr) atomicCAS(a.status, GDN_OK, GDN_ERR_TIMEOUT);
 
-        // this thread's vectors, packed; elements behind the row's end are -inf
+        // this thread's vectors, packed
         Vec<T, E> v[NV];
-        float m = -INFINITY;
+        PolicyMax<T, E> top;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int i = tid + j * NT;
             if (i < nvec) {
                 const uint4* p = reinterpret_cast<const uint4*>(policy_smem) + i;
                 uint4 r = p[0];
-                if (s != 0) r = bytes_at(r, p[1], s);
+                if (!ALIGNED && s != 0) r = bytes_at(r, p[1], s);
                 v[j] = *reinterpret_cast<const Vec<T, E>*>(&r);
-                if (i == nvec - 1) {
-#pragma unroll
-                    for (int k = 0; k < E; ++k)
-                        if (i * E + k >= len) v[j].v[k] = from_f<T>(-INFINITY);
-                }
-#pragma unroll
-                for (int k = 0; k < E; ++k) m = fmaxf(m, to_f<T>(v[j].v[k]));
+                top.add(v[j]);
             }
         }
-        float zy = 0.0f;
-        if (tid == 0 && y >= lo && y < lo + len) zy = to_f<T>(reinterpret_cast<const T*>(policy_smem + s)[y - lo]);
-        fence_proxy_async_smem();
-        __syncthreads();  // the slice is in registers
-        if (y_next >= 0 && !lost) issue(row + step);
-
-        m *= a.c;  // in units of log2 from here on
-        const float base = -policy_base(m);
-        float sum = 0.0f;
+        if (tid == 0 && y >= lo && y < lo + len) target_logit = to_f<T>(reinterpret_cast<const T*>(policy_smem + s)[y - lo]);
+        const f2x c2 = pk2(a.c, a.c);
+        float m = top.get() * a.c, sum;  // in units of log2 from here on
+        {
+            const float base = -policy_base(m);
+            const f2x b2 = pk2(base, base);
+            f2x s0 = pk2(0.0f, 0.0f), s1 = s0;
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if (tid + j * NT < nvec) {
+            for (int j = 0; j < NV; ++j)
+                if (tid + j * NT < nvec) {
 #pragma unroll
-                for (int k = 0; k < E; ++k) sum += ex2(__fmaf_rn(to_f<T>(v[j].v[k]), a.c, base));
-            }
-        auto join = [](float& m, float& s, float m2, float s2) {
-            const float M = fmaxf(m, m2), b = policy_base(M);
-            s = s * ex2(m - b) + s2 * ex2(m2 - b);
-            m = M;
-        };
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) join(m, sum, __shfl_xor_sync(kFullMask, m, o), __shfl_xor_sync(kFullMask, sum, o));
+                    for (int k = 0; k < E / 2; ++k) {
+                        float x0, x1;
+                        up2(pfma(pbits<T, E>(v[j], k), c2, b2), x0, x1);
+                        f2x& acc = k & 1 ? s1 : s0;
+                        acc = padd(acc, pk2(ex2(x0), ex2(x1)));
+                    }
+                }
+            sum = psum(padd(s0, s1));
+        }
+        policy_warp(m, sum);
         if (lane == 0) wm[warp] = m, ws[warp] = sum;
-        __syncthreads();
+        fence_proxy_async_smem();
+        __syncthreads();  // also: the slice is in registers
+        if (y_next >= 0 && !lost) issue(row + step);
         if (warp == 0) {
             m = lane < NT / 32 ? wm[lane] : -INFINITY;
             sum = lane < NT / 32 ? ws[lane] : 0.0f;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) join(m, sum, __shfl_xor_sync(kFullMask, m, o), __shfl_xor_sync(kFullMask, sum, o));
-            zy = __shfl_sync(kFullMask, zy, 0);
+            policy_warp(m, sum);
             if (lane < (int)blocks) {
                 st_cluster(&peer[turn][rank][0], lane, m);
                 st_cluster(&peer[turn][rank][1], lane, sum);
-                st_cluster(&peer[turn][rank][2], lane, zy);
+                st_cluster(&peer[turn][rank][2], lane, target_logit);
             }
         }
         cluster_sync();  // also this block's barrier: a slot of this parity is written again two exchanges later
-        m = peer[turn][0][0], sum = peer[turn][0][1];
-        for (uint32_t b = 1; b < blocks; ++b) join(m, sum, peer[turn][b][0], peer[turn][b][1]);
-        zy = peer[turn][y / a.slice][2];
+        m = peer[turn][0][0];
+        for (uint32_t b = 1; b < blocks; ++b) m = fmaxf(m, peer[turn][b][0]);
         const float bm = policy_base(m);
+        sum = 0.0f;
+        for (uint32_t b = 0; b < blocks; ++b) sum = __fmaf_rn(peer[turn][b][1], ex2(peer[turn][b][0] - bm), sum);
+        const float zy = peer[turn][(uint32_t)y / (uint32_t)a.slice][2];
+        turn ^= 1;
         const float lp = (__fmaf_rn(zy, a.c, -bm) - log2f(sum)) * 0.69314718055994530942f;
         float loss = 0.0f, d = 0.0f;
         if (a.old != nullptr) {
-            const float adv = a.adv[row], ratio = ex2((lp - a.old[row]) * kLog2e);
+            const float ratio = ex2((lp - old) * kLog2e);
             if (adv != 0.0f) {  // a zero takes no part, whatever the ratio
                 const float free = -adv * ratio, held = -adv * fminf(fmaxf(ratio, a.lo), a.hi);
                 loss = free < held ? held : free;  // not a number where the ratio is not
                 d = free < held ? 0.0f : free;
             }
             if (a.ref != nullptr) {
-                const float gap = a.ref[row] - lp, e = ex2(gap * kLog2e);
+                const float gap = ref - lp, e = ex2(gap * kLog2e);
                 loss = __fmaf_rn(a.kl, e - gap - 1.0f, loss);
                 d = __fmaf_rn(a.kl, 1.0f - e, d);
             }
@@ -248,34 +294,62 @@ __global__ void __launch_bounds__(kPolicyMaxThreads, 1) k_policy(const PolicyArg
             if (a.lp != nullptr) a.lp[row] = lp;
         }
         if constexpr (BWD) {
-            d *= a.dloss[row] * a.inv_tau;
+            d *= dloss * a.inv_tau;
             const float scale = -d / sum;
+            const f2x b2 = pk2(-bm, -bm), scale2 = pk2(scale, scale);
             T* out = static_cast<T*>(a.dz) + row * a.V + lo;
-            const bool whole = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+            const int so = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(out) & 15);
             const int yl = (int)y - lo;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int i = tid + j * NT;
-                if (i < nvec && !lost) {
-                    float o[E];
+                if (i - lane < nvec && !lost) {  // the whole warp: it exchanges below
+                    f2x o[E / 2];
 #pragma unroll
-                    for (int k = 0; k < E; ++k) {
-                        o[k] = ex2(__fmaf_rn(to_f<T>(v[j].v[k]), a.c, -bm)) * scale;
-                        if (i * E + k == yl) o[k] += d;
+                    for (int k = 0; k < E / 2; ++k) {
+                        float x0, x1;
+                        up2(pfma(pbits<T, E>(v[j], k), c2, b2), x0, x1);
+                        o[k] = pmul(pk2(ex2(x0), ex2(x1)), scale2);
                     }
-                    if (whole && i * E + E <= len) {
-                        store_vec<T, E>(out + i * E, o);
-                    } else {
+                    if ((unsigned)(yl - i * E) < (unsigned)E) {
 #pragma unroll
-                        for (int k = 0; k < E; ++k)
-                            if (i * E + k < len) out[i * E + k] = from_f<T>(o[k]);
+                        for (int k = 0; k < E / 2; ++k) {
+                            const int q = yl - i * E - 2 * k;
+                            o[k] = padd(o[k], pk2(q == 0 ? d : 0.0f, q == 1 ? d : 0.0f));
+                        }
+                    }
+                    if constexpr (ALIGNED) {
+                        if (i < nvec) pstore<T, E>(out + i * E, o);
+                    } else {
+                        // The rows start anywhere: a thread stores the 16 bytes of memory that begin in its
+                        // neighbour's vector and end in its own.  The warp's first and last bytes, and the row's, go one by one.
+                        Vec<T, E> r;
+                        pstore<T, E>(r.v, o);
+                        const uint4 own = *reinterpret_cast<const uint4*>(&r);
+                        uint4 left;
+                        left.x = __shfl_up_sync(kFullMask, own.x, 1);
+                        left.y = __shfl_up_sync(kFullMask, own.y, 1);
+                        left.z = __shfl_up_sync(kFullMask, own.z, 1);
+                        left.w = __shfl_up_sync(kFullMask, own.w, 1);
+                        const int cut = so / (int)sizeof(T);  // elements of a vector that belong to the next 16 bytes
+                        auto fits = [&](int i) { return i < nvec && i * E + E - cut <= len; };
+                        const bool joined = fits(i) && (lane > 0 || cut == 0);
+                        if (joined) *reinterpret_cast<uint4*>(out + i * E - cut) = cut == 0 ? own : bytes_at(left, own, 16 - so);
+#pragma unroll
+                        for (int k = 0; k < E; ++k) {
+                            const bool mine = k < E - cut ? !joined : lane == 31 || !fits(i + 1);
+                            if (i < nvec && mine && i * E + k < len) out[i * E + k] = r.v[k];
+                        }
                     }
                 }
             }
         }
         y = y_next, y_next = y_after;
     }
-    if (lost) mbar_wait_bounded(&bar, parity ^ 1, 1ll << 31);  // the copy that was late
+    if (lost) {
+        if (a.status != nullptr) atomicCAS(a.status, GDN_OK, GDN_ERR_TIMEOUT);
+        mbar_wait_bounded(&bar, parity ^ 1, 1ll << 31);  // the copy that was late
+    }
 }
 
 }  // namespace gdn
