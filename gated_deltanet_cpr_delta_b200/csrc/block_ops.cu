@@ -97,7 +97,7 @@ gdn_status_t policy_check(const gdn_policy_t* s, const int32_t* status)
         return GDN_ERR_INVALID_ARG;
     if (s->old_logprob && (!(s->clip_low >= 0.0f) || !(s->clip_low <= 1.0f) || !(s->clip_high >= 0.0f) || std::isnan(s->kl_coef)))
         return GDN_ERR_INVALID_ARG;
-    if ((int64_t)s->vocab * (int64_t)esize(s->in_dtype) > gdn::kPolicyMaxBytes) return GDN_ERR_UNSUPPORTED;
+    if (s->vocab > kMaxRows) return GDN_ERR_INVALID_ARG;
     if (!aligned(s->old_logprob, 4) || !aligned(s->ref_logprob, 4) || !aligned(s->advantages, 4)) return GDN_ERR_INVALID_ARG;
     if (s->rows == 0) return GDN_OK;
     if (!rows_ok(s->logits, s->logits_stride, s->vocab, s->in_dtype) || s->targets == nullptr || !aligned(s->targets, 8))
@@ -105,67 +105,28 @@ gdn_status_t policy_check(const gdn_policy_t* s, const int32_t* status)
     return GDN_OK;
 }
 
-struct PolicyPlan {
-    int cluster, threads;
-    size_t smem;
-};
-
-// How a row is cut, by its bytes alone (the log-probabilities' bits follow from it): one block up to
-// 32 KB, then a cluster of 2, 4 or 8 blocks, each with a slice of whole 16-byte vectors,
-// kPolicyVecs of them per thread.
-PolicyPlan policy_plan(gdn::PolicyArgs& a, gdn_dtype_t t)
-{
-    const int64_t bytes = (int64_t)a.V * (int64_t)esize(t);
-    const int E = 16 / (int)esize(t);
-    PolicyPlan p;
-    p.cluster = 1;
-    while (p.cluster < gdn::kPolicyMaxCluster && bytes > (int64_t)p.cluster * 32 * 1024) p.cluster *= 2;
-    const int64_t vecs = ceil_div(ceil_div(a.V, E), p.cluster);  // of a slice
-    a.slice = (int32_t)(vecs * E);
-    p.threads = (int)std::max<int64_t>(64, ceil_div(ceil_div(vecs, gdn::kPolicyVecs), 32) * 32);
-    p.smem = 16 * (size_t)(vecs + 2);
-    return p;
-}
-
-template <typename T, bool BWD, bool ALIGNED>
-gdn_status_t policy_run(const gdn::PolicyArgs& a, const PolicyPlan& p, cudaStream_t st)
+template <typename T, bool BWD, bool ALIGNED, int NT>
+gdn_status_t policy_run(const gdn::PolicyArgs& a, cudaStream_t st)
 {
     const int sms = sm_count();
     if (sms == 0) return GDN_ERR_CUDA;
-    auto k = gdn::k_policy<T, BWD, ALIGNED>;
-    if (!raise_smem(k, p.smem)) return GDN_ERR_CUDA;
-    cudaLaunchConfig_t cfg{};
-    cfg.blockDim = dim3((unsigned)p.threads);
-    cfg.dynamicSmemBytes = p.smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)p.cluster;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    // As many clusters as are resident at a time, each with its share of the rows.  Clusters keep to a
-    // group of SMs, so that fewer fit than the SMs' sum suggests, and one that waits for another's end doubles the time.
-    const int per_sm = (int)std::min<size_t>(1024 / p.threads, (size_t)(220 * 1024) / (p.smem + 2048));
-    int64_t clusters = std::max<int64_t>(1, (int64_t)sms * std::max(1, per_sm) / p.cluster);
-    if (a.T * 2 <= clusters) {
-        clusters = a.T;
-    } else {
-        cfg.gridDim = dim3((unsigned)(clusters * p.cluster));
-        int fit = 0;
-        if (cudaOccupancyMaxActiveClusters(&fit, k, &cfg) != cudaSuccess || fit <= 0) return GDN_ERR_CUDA;
-        clusters = std::min<int64_t>(fit, a.T);
-    }
-    cfg.gridDim = dim3((unsigned)(clusters * p.cluster));
-    return cudaLaunchKernelEx(&cfg, k, a) == cudaSuccess && launched() ? GDN_OK : GDN_ERR_CUDA;
+    auto k = gdn::k_policy<T, BWD, ALIGNED, NT>;
+    constexpr size_t smem = (size_t)gdn::kPolicySlots * gdn::policy_slot_bytes(NT);
+    if (!raise_smem(k, smem)) return GDN_ERR_CUDA;
+    constexpr int resident = NT == 64 ? 6 : 2;
+    k<<<(unsigned)std::min<int64_t>(a.T, (int64_t)sms * resident), NT + 32, smem, st>>>(a);
+    return launched() ? GDN_OK : GDN_ERR_CUDA;
 }
 
+// Rows of up to two tiles of 4 KB by 64 threads, longer ones by 256 (the log-probabilities' bits
+// follow from the vocabulary and the type).
 template <typename T, bool BWD>
-gdn_status_t policy_launch(gdn::PolicyArgs& a, gdn_dtype_t t, cudaStream_t st)
+gdn_status_t policy_launch(const gdn::PolicyArgs& a, gdn_dtype_t t, cudaStream_t st)
 {
-    const PolicyPlan p = policy_plan(a, t);
-    return wide(a.z, a.ldz, a.V, t) && wide(a.dz, a.V, a.V, t) ? policy_run<T, BWD, true>(a, p, st)
-                                                               : policy_run<T, BWD, false>(a, p, st);
+    const bool whole = wide(a.z, a.ldz, a.V, t) && wide(a.dz, a.V, a.V, t);
+    if ((int64_t)a.V * (int64_t)sizeof(T) <= 2 * gdn::policy_tile_bytes(64))
+        return whole ? policy_run<T, BWD, true, 64>(a, st) : policy_run<T, BWD, false, 64>(a, st);
+    return whole ? policy_run<T, BWD, true, 256>(a, st) : policy_run<T, BWD, false, 256>(a, st);
 }
 
 gdn::PolicyArgs policy_args(const gdn_policy_t* s, int32_t* status)
