@@ -105,28 +105,34 @@ gdn_status_t policy_check(const gdn_policy_t* s, const int32_t* status)
     return GDN_OK;
 }
 
-template <typename T, bool BWD, bool ALIGNED, int NT>
+template <typename T, bool BWD, bool ALIGNED, int NT, int RES>
 gdn_status_t policy_run(const gdn::PolicyArgs& a, cudaStream_t st)
 {
     const int sms = sm_count();
     if (sms == 0) return GDN_ERR_CUDA;
-    auto k = gdn::k_policy<T, BWD, ALIGNED, NT>;
-    constexpr size_t smem = (size_t)gdn::kPolicySlots * gdn::policy_slot_bytes(NT);
+    auto k = gdn::k_policy<T, BWD, ALIGNED, NT, RES>;
+    constexpr size_t smem = (size_t)gdn::policy_slots(RES) * gdn::policy_slot_bytes(NT);
     if (!raise_smem(k, smem)) return GDN_ERR_CUDA;
-    constexpr int resident = NT == 64 ? 6 : 2;
-    k<<<(unsigned)std::min<int64_t>(a.T, (int64_t)sms * resident), NT + 32, smem, st>>>(a);
+    k<<<(unsigned)std::min<int64_t>(a.T, (int64_t)sms * RES), NT + 32, smem, st>>>(a);
     return launched() ? GDN_OK : GDN_ERR_CUDA;
 }
 
 // Rows of up to two tiles of 4 KB by 64 threads, longer ones by 256 (the log-probabilities' bits
-// follow from the vocabulary and the type).
+// follow from the vocabulary and the type).  Three blocks per SM, but two with larger rings where the rows that are walked at
+// a time, of which a part is fetched again for the gradient, would not stay in L2: 4096 x 131072 bf16 (256 KB
+// a row) 401 us with two, 459 with three; 4096 x 50021 199 and 180; 16384 x 32768 401 and 367.
 template <typename T, bool BWD>
 gdn_status_t policy_launch(const gdn::PolicyArgs& a, gdn_dtype_t t, cudaStream_t st)
 {
     const bool whole = wide(a.z, a.ldz, a.V, t) && wide(a.dz, a.V, a.V, t);
-    if ((int64_t)a.V * (int64_t)sizeof(T) <= 2 * gdn::policy_tile_bytes(64))
-        return whole ? policy_run<T, BWD, true, 64>(a, st) : policy_run<T, BWD, false, 64>(a, st);
-    return whole ? policy_run<T, BWD, true, 256>(a, st) : policy_run<T, BWD, false, 256>(a, st);
+    const int64_t bytes = (int64_t)a.V * (int64_t)sizeof(T);
+    if (bytes <= 2 * gdn::policy_tile_bytes(64))
+        return whole ? policy_run<T, BWD, true, 64, 8>(a, st) : policy_run<T, BWD, false, 64, 8>(a, st);
+    if constexpr (BWD) {
+        if (bytes > 160 * 1024)
+            return whole ? policy_run<T, BWD, true, 256, 2>(a, st) : policy_run<T, BWD, false, 256, 2>(a, st);
+    }
+    return whole ? policy_run<T, BWD, true, 256, 3>(a, st) : policy_run<T, BWD, false, 256, 3>(a, st);
 }
 
 gdn::PolicyArgs policy_args(const gdn_policy_t* s, int32_t* status)

@@ -7,7 +7,7 @@
 //
 // One block walks a row twice: running maximum and sum, then the gradient.  A warp of its own streams the row's tiles
 // into a ring in shared memory with bulk copies; the tiles of a row's end are still there when the second walk
-// begins with them, and only what the ring does not hold is fetched again (from L2: 96 KB of a row stay).  The copies run
+// begins with them, and only what the ring does not hold is fetched again (from L2).  The copies run
 // ahead over the end of the walks and of the rows, so that memory does not wait for the two block-wide sums per row.
 // (Rows cut over a cluster of up to 8 blocks, wholly in shared memory, waited for each other: 495 us at
 // 4096 x 131072 bf16, whether with the cluster's barrier or with exchanges a row ahead.)
@@ -24,8 +24,6 @@
 namespace gdn {
 
 constexpr int kPolicyVecs = 4;    // 16-byte vectors of a tile per thread
-constexpr int kPolicySlots = 6;   // tiles in the ring
-constexpr int kPolicyStay = 4;    // of them, the row's last ones that stay for the second walk
 
 struct PolicyArgs {
     const void* z;
@@ -42,10 +40,10 @@ struct PolicyArgs {
 };
 
 // n bytes, a multiple of 16, both addresses 16-byte aligned
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t n, uint64_t* mbar)
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t n, uint64_t* mbar, uint64_t policy)
 {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     smem_addr(dst)), "l"(src), "r"(n), "r"(smem_addr(mbar))
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+                     smem_addr(dst)), "l"(src), "r"(n), "r"(smem_addr(mbar)), "l"(policy)
                  : "memory");
 }
 
@@ -53,10 +51,11 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t n
 __device__ __forceinline__ uint4 bytes_at(const uint4& a, const uint4& b, int s)
 {
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    uint32_t v[5];
-    const int n = s >> 2;
+    uint32_t t[6], v[5];
 #pragma unroll
-    for (int i = 0; i < 5; ++i) v[i] = n == 0 ? w[i] : n == 1 ? w[i + 1] : n == 2 ? w[i + 2] : w[i + 3];
+    for (int i = 0; i < 6; ++i) t[i] = s & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) v[i] = s & 4 ? t[i + 1] : t[i];
     const int sh = (s & 3) * 8;
     return make_uint4(__funnelshift_r(v[0], v[1], sh), __funnelshift_r(v[1], v[2], sh),
                       __funnelshift_r(v[2], v[3], sh), __funnelshift_r(v[3], v[4], sh));
@@ -101,16 +100,30 @@ __device__ __forceinline__ void policy_join(float& m, float& sum)
     m = M;
 }
 
+// E elements that are written once and not read here: first to leave L2
+template <typename T, int E>
+__device__ __forceinline__ void store_once(T* p, const f2x (&x)[E / 2])
+{
+    Vec<T, E> r;
+    pstore<T, E>(r.v, x);
+    const uint4 u = *reinterpret_cast<const uint4*>(&r);
+    asm volatile("st.global.cs.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w) : "memory");
+}
+
 __host__ __device__ constexpr int policy_tile_bytes(int NT) { return NT * kPolicyVecs * 16; }
 // a tile that starts s bytes into its first 16, and as many behind its last
 __host__ __device__ constexpr int policy_slot_bytes(int NT) { return policy_tile_bytes(NT) + 32; }
 
-// NT threads walk, 32 more fetch.  ALIGNED: every row of the logits and of the gradient is whole 16-byte vectors.
-template <typename T, bool BWD, bool ALIGNED, int NT>
-__global__ void __launch_bounds__(NT + 32, NT == 64 ? 6 : 2) k_policy(const PolicyArgs a)
+// Tiles in the ring with so many blocks per SM; all but two of them stay for the second walk.
+__host__ __device__ constexpr int policy_slots(int resident) { return resident == 2 ? 6 : 4; }
+
+// NT threads walk, 32 more fetch; `RES` blocks per SM.  ALIGNED: every row of the logits and of the gradient is whole
+// 16-byte vectors.
+template <typename T, bool BWD, bool ALIGNED, int NT, int RES>
+__global__ void __launch_bounds__(NT + 32, RES) k_policy(const PolicyArgs a)
 {
     constexpr int E = 16 / (int)sizeof(T);  // elements of a vector
-    constexpr int NV = kPolicyVecs, K = kPolicySlots, TILE = NT * NV * E, SLOT = policy_slot_bytes(NT), WARPS = NT / 32;
+    constexpr int NV = kPolicyVecs, K = policy_slots(RES), TILE = NT * NV * E, SLOT = policy_slot_bytes(NT), WARPS = NT / 32;
     constexpr long long LIMIT = 1ll << 31;
     extern __shared__ __align__(128) unsigned char policy_smem[];  // tiles, each at its global address mod 16
     __shared__ __align__(8) uint64_t full[K], empty[K];
@@ -118,7 +131,7 @@ __global__ void __launch_bounds__(NT + 32, NT == 64 ? 6 : 2) k_policy(const Poli
     __shared__ volatile int lost;           // a wait that ran out: nothing is written from then on
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = (int)(((int64_t)a.V + TILE - 1) / TILE);        // tiles of a row
-    const int stay = BWD ? min(n, kPolicyStay) : 0, again = BWD ? n - stay : 0;
+    const int stay = BWD ? min(n, K - 2) : 0, again = BWD ? n - stay : 0;
     if (tid == 0) {
         for (int i = 0; i < K; ++i) {
             mbar_init_cta(full + i, 1);
@@ -141,6 +154,10 @@ __global__ void __launch_bounds__(NT + 32, NT == 64 ? 6 : 2) k_policy(const Poli
     if (warp == WARPS) {
         // ---- the copies: a row's tiles in order, then those that did not stay
         phase = 1;  // the slots start empty
+        // what is fetched again stays in L2 until then, before what is read or written once
+        uint64_t keep, once;
+        asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
+        asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
         int y_next = target(blockIdx.x);
         for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
             const int y = y_next;
@@ -168,10 +185,11 @@ __global__ void __launch_bounds__(NT + 32, NT == 64 ? 6 : 2) k_policy(const Poli
                         if (lane * (int)sizeof(T) < from) at[lane] = src[lane];
                     }
                     int end = ((s + to + 15) & ~15) - s;
-                    if (end > (a.V - tile * TILE) * (int)sizeof(T)) {
+                    const int rest = a.V - tile * TILE;  // to the row's end
+                    if (end > rest * (int)sizeof(T)) {
                         end = max(from, ((s + to) & ~15) - s);
                         const int i = max(end, 0) / (int)sizeof(T) + lane;
-                        if (i < len) at[i] = src[i];
+                        if (lane < E && i < rest) at[i] = src[i];
                     }
                     if (len + lane < (len + E - 1) / E * E) at[len + lane] = from_f<T>(-INFINITY);  // fills the row's last vector
                     to = end;
@@ -181,7 +199,7 @@ __global__ void __launch_bounds__(NT + 32, NT == 64 ? 6 : 2) k_policy(const Poli
                 if (lane == 0) {
                     mbar_arrive_expect_tx(full + slot, (uint32_t)(to - from));
                     if (to > from)
-                        bulk_load(dst + s + from, reinterpret_cast<const unsigned char*>(src) + from, (uint32_t)(to - from), full + slot);
+                        bulk_load(dst + s + from, reinterpret_cast<const unsigned char*>(src) + from, (uint32_t)(to - from), full + slot, t < again ? keep : once);
                 }
                 if (++slot == K) slot = 0, phase ^= 1;
             }
@@ -316,56 +334,67 @@ __global__ void __launch_bounds__(NT + 32, NT == 64 ? 6 : 2) k_policy(const Poli
                 if (t == stay) slot = end_slot, phase = end_phase;
                 if (t >= stay) wait();
                 T* dst = out + (int64_t)tile * TILE;
-                const int len = min(TILE, a.V - tile * TILE), nvec = (len + E - 1) / E, yl = y - tile * TILE;
-                const int here = lost ? 0 : nvec;
-                auto turn = [&](auto whole) {
-                    constexpr bool WHOLE = decltype(whole)::value;
+                const int rest = a.V - tile * TILE, len = min(TILE, rest), yl = y - tile * TILE;  // rest: to the row's end
+                const int here = lost ? 0 : (len + E - 1) / E;
+                auto gradient = [&](const Vec<T, E>& v, int first, f2x (&o)[E / 2]) {  // of the elements from `first` on
 #pragma unroll
-                    for (int j = 0; j < NV; ++j) {
-                        const int i = tid + j * NT;
-                        if (!WHOLE && i - lane >= nvec) break;  // the whole warp: it exchanges below
-                        f2x o[E / 2];
-                        const Vec<T, E> v = vec(i);
+                    for (int k = 0; k < E / 2; ++k) {
+                        float x0, x1;
+                        up2(pfma(pbits<T, E>(v, k), c2, b2), x0, x1);
+                        o[k] = pmul(pk2(ex2(x0), ex2(x1)), scale2);
+                    }
+                    if ((unsigned)(yl - first) < (unsigned)E) {
 #pragma unroll
                         for (int k = 0; k < E / 2; ++k) {
-                            float x0, x1;
-                            up2(pfma(pbits<T, E>(v, k), c2, b2), x0, x1);
-                            o[k] = pmul(pk2(ex2(x0), ex2(x1)), scale2);
-                        }
-                        if ((unsigned)(yl - i * E) < (unsigned)E) {
-#pragma unroll
-                            for (int k = 0; k < E / 2; ++k) {
-                                const int q = yl - i * E - 2 * k;
-                                o[k] = padd(o[k], pk2(q == 0 ? d : 0.0f, q == 1 ? d : 0.0f));
-                            }
-                        }
-                        if constexpr (ALIGNED) {
-                            if (i < here) pstore<T, E>(dst + i * E, o);
-                        } else {
-                            // The rows start anywhere: a thread stores the 16 bytes of memory that begin in its
-                            // neighbour's vector and end in its own.  The warp's first and last bytes, and the row's, go one by one.
-                            Vec<T, E> r;
-                            pstore<T, E>(r.v, o);
-                            const uint4 own = *reinterpret_cast<const uint4*>(&r);
-                            uint4 left;
-                            left.x = __shfl_up_sync(kFullMask, own.x, 1);
-                            left.y = __shfl_up_sync(kFullMask, own.y, 1);
-                            left.z = __shfl_up_sync(kFullMask, own.z, 1);
-                            left.w = __shfl_up_sync(kFullMask, own.w, 1);
-                            const int cut = so / (int)sizeof(T);  // elements of a vector that belong to the next 16 bytes
-                            auto fits = [&](int i) { return i < here && i * E + E - cut <= len; };
-                            const bool joined = fits(i) && (lane > 0 || cut == 0);
-                            if (joined) *reinterpret_cast<uint4*>(dst + i * E - cut) = cut == 0 ? own : bytes_at(left, own, 16 - so);
-#pragma unroll
-                            for (int k = 0; k < E; ++k) {
-                                const bool mine = k < E - cut ? !joined : lane == 31 || !fits(i + 1);
-                                if (i < here && mine && i * E + k < len) dst[i * E + k] = r.v[k];
-                            }
+                            const int q = yl - first - 2 * k;
+                            o[k] = padd(o[k], pk2(q == 0 ? d : 0.0f, q == 1 ? d : 0.0f));
                         }
                     }
                 };
-                if (len == TILE) turn(std::true_type{});
-                else turn(std::false_type{});
+                if (ALIGNED || so == s) {
+                    // The gradient's 16-byte granules are the logits': the tile's are those that start in it; of the row's
+                    // first and last the elements that belong to the row.
+                    const int skip = s ? E - s / (int)sizeof(T) : 0;  // elements before the first of them
+                    auto granules = [&](auto whole) {
+                        constexpr bool WHOLE = decltype(whole)::value;
+#pragma unroll
+                        for (int j = 0; j < NV; ++j) {
+                            const int i = tid + j * NT, e = skip + i * E;
+                            if (WHOLE || e + E <= rest) {
+                                const uint4 r = reinterpret_cast<const uint4*>(policy_smem + slot * SLOT)[i + (s != 0)];
+                                f2x o[E / 2];
+                                gradient(*reinterpret_cast<const Vec<T, E>*>(&r), e, o);
+                                store_once<T, E>(dst + e, o);
+                            }
+                        }
+                    };
+                    if (here > 0) {
+                        if (rest >= TILE + skip) granules(std::true_type{});
+                        else granules(std::false_type{});
+                        if (!ALIGNED) {
+                            const int last = rest >= TILE + skip ? 0 : max(0, (rest - skip) / E);  // granules of the row's end
+                            const int e = tid < E ? (tile == 0 && tid < min(skip, rest) ? tid : -1)
+                                                  : tid < 2 * E && rest < TILE + skip && skip + last * E + tid - E < rest ? skip + last * E + tid - E : -1;
+                            if (e >= 0) {
+                                const float x = to_f<T>(reinterpret_cast<const T*>(policy_smem + slot * SLOT + s)[e]);
+                                dst[e] = from_f<T>(__fmaf_rn(ex2(__fmaf_rn(x, a.c, -bm)), scale, e == yl ? d : 0.0f));
+                            }
+                        }
+                    }
+                } else {
+                    for (int j = 0; j < NV; ++j) {
+                        const int i = tid + j * NT;
+                        if (i < here) {
+                            f2x o[E / 2];
+                            gradient(vec(i), i * E, o);
+                            Vec<T, E> r;
+                            pstore<T, E>(r.v, o);
+#pragma unroll
+                            for (int k = 0; k < E; ++k)
+                                if (i * E + k < len) dst[i * E + k] = r.v[k];
+                        }
+                    }
+                }
                 release(slot);
                 advance();
             }

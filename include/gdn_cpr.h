@@ -692,7 +692,8 @@ gdn_status_t gdn_glu_backward(const gdn_glu_t* args, const void* dh, int64_t dh_
  * own results.  An advantage of 0 adds 0, whatever the ratio.
  * A row's log-probability has the same bits in every call on the same values, type and
  * vocabulary: whatever the batch, the row's place, its stride, and whether the gradient is made.
- * Rows of more than 1 MiB (524288 bf16, 262144 fp32): GDN_ERR_UNSUPPORTED.
+ * *status becomes GDN_ERR_TIMEOUT when a wait inside the kernel runs out (about a second): the outputs are then
+ * unspecified.
  */
 typedef struct {
     const void* logits;

@@ -76,7 +76,7 @@ def check(c, z64, kw, z=None):
 
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("R,V,tau,kl", [
-    (1, 1, 1.0, 0.1), (5, 2, 1.0, 0.0), (3, 7, 0.5, 0.1), (2, 8, 1.0, 0.1), (70, 100, 1.0, 0.05), (9, 1000, 2.0, 0.1), (4, 4099, 1.0, 0.1),
+    (1, 1, 1.0, 0.1), (5, 2, 1.0, 0.0), (3, 7, 0.5, 0.1), (2, 8, 1.0, 0.1), (70, 100, 1.0, 0.05), (9, 1000, 2.0, 0.1), (9, 4097, 1.0, 0.1), (9, 4099, 1.0, 0.1), (9, 8193, 1.0, 0.1), (9, 8199, 1.0, 0.0), (9, 2047, 1.0, 0.1),
     (3, 16384, 1.0, 0.0), (3, 16391, 0.7, 0.1), (5, 32768, 1.0, 0.1), (2, 50021, 1.0, 0.1), (2, 65537, 1.0, 0.1), (3, 131072, 0.7, 0.05)])
 def test_sizes(dtype, R, V, tau, kl):
     check(*case(TYPES[dtype], R, V, tau, kl))
