@@ -48,32 +48,42 @@ int qk_lanes(int32_t d)
     return n;
 }
 
-// Tokens that a block takes at a time: enough rows for each of its threads to have several in flight, few
-// enough that every SM has blocks, and with angles that fit 24 KB.
-int qk_tokens(const gdn_qk_norm_t* s, int tpr, int sms)
+// Tokens that a block takes at a time: the same number of tiles for every block, as large as 16 KB of angles (or
+// 1024 rows) allow.  Each tile costs its setup and two barriers: 4 tokens at a time took 65 us where these take 63, the gradients 217 and 192
+// (16384 tokens, 16 + 16 heads of 128).
+int qk_tokens(const gdn_qk_norm_t* s, int tpr, int blocks)
 {
-    const int64_t rows = (int64_t)(gdn::kQkThreads / tpr) * gdn::qk_rows(false) * 2, heads = (int64_t)s->q_heads + s->k_heads;
-    int64_t n = ceil_div(rows, heads);
-    n = std::min(n, ceil_div(s->tokens, (int64_t)sms * 4));
-    if (s->rot_dim > 0) n = std::min<int64_t>(n, 24 * 1024 / (4 * s->rot_dim));
-    return (int)std::max<int64_t>(1, n);
+    const int64_t heads = (int64_t)s->q_heads + s->k_heads;
+    int64_t most = std::max<int64_t>(1, 1024 / heads);
+    if (s->rot_dim > 0) most = std::min<int64_t>(most, 16 * 1024 / (32 * tpr));
+    const int64_t rounds = std::max<int64_t>(1, ceil_div(s->tokens, most * blocks));
+    return (int)std::max<int64_t>(1, ceil_div(s->tokens, rounds * blocks));
 }
 
 constexpr int kQkParts = 1024;  // most blocks of the backward
 
-size_t qk_smem(const gdn::QkArgs& a, bool bwd)
-{
-    return sizeof(float2) * (size_t)a.tokens * (a.rot / 2) + sizeof(float) * (bwd ? gdn::kQkThreads / 32 : 2) * a.d;
-}
-
-template <typename T, bool VEC, bool BWD>
+template <typename T, bool VEC, bool INTER, bool BWD>
 gdn_status_t qk_launch(const gdn::QkArgs& a, unsigned blocks, cudaStream_t st)
 {
-    gdn::k_qk_norm<T, VEC, BWD><<<blocks, gdn::kQkThreads, qk_smem(a, BWD), st>>>(a);
+    const size_t angles = a.rot > 0 ? sizeof(float) * 8 * (size_t)a.tokens * a.tpr : 0, weights = sizeof(float) * 16 * a.tpr;
+    const size_t smem = std::max(angles + weights, BWD ? sizeof(float) * (gdn::kQkThreads / 32) * a.d : 0);
+    gdn::k_qk_norm<T, VEC, INTER, BWD><<<blocks, gdn::kQkThreads, smem, st>>>(a);
     return launched() ? GDN_OK : GDN_ERR_CUDA;
 }
 
-gdn::QkArgs qk_args(const gdn_qk_norm_t* s, int sms)
+template <bool BWD>
+gdn_status_t qk_dispatch(const gdn::QkArgs& a, gdn_dtype_t t, bool vec, unsigned blocks, cudaStream_t st)
+{
+    const bool in = a.interleaved;
+    if (t == GDN_BF16) {
+        if (vec) return in ? qk_launch<__nv_bfloat16, true, true, BWD>(a, blocks, st) : qk_launch<__nv_bfloat16, true, false, BWD>(a, blocks, st);
+        return in ? qk_launch<__nv_bfloat16, false, true, BWD>(a, blocks, st) : qk_launch<__nv_bfloat16, false, false, BWD>(a, blocks, st);
+    }
+    if (vec) return in ? qk_launch<float, true, true, BWD>(a, blocks, st) : qk_launch<float, true, false, BWD>(a, blocks, st);
+    return in ? qk_launch<float, false, true, BWD>(a, blocks, st) : qk_launch<float, false, false, BWD>(a, blocks, st);
+}
+
+gdn::QkArgs qk_args(const gdn_qk_norm_t* s, int blocks)
 {
     gdn::QkArgs a{};
     a.x[0] = s->q; a.x[1] = s->k; a.ldx[0] = s->q_stride; a.ldx[1] = s->k_stride;
@@ -82,7 +92,7 @@ gdn::QkArgs qk_args(const gdn_qk_norm_t* s, int sms)
     a.pos = s->positions; a.freq = s->inv_freq; a.eps = s->eps;
     a.inv_n = s->unit ? 1.0f : 1.0f / (float)s->head_dim;
     a.T = s->tokens; a.d = s->head_dim; a.rot = s->rot_dim; a.tpr = qk_lanes(s->head_dim);
-    a.tokens = qk_tokens(s, a.tpr, sms);
+    a.tokens = qk_tokens(s, a.tpr, blocks);
     return a;
 }
 
@@ -166,15 +176,12 @@ gdn_status_t gdn_qk_norm_forward(const gdn_qk_norm_t* args, void* q_out, void* k
         return GDN_ERR_INVALID_ARG;
     const int sms = sm_count();
     if (sms == 0) return GDN_ERR_CUDA;
-    gdn::QkArgs a = qk_args(args, sms);
+    gdn::QkArgs a = qk_args(args, sms * gdn::qk_resident(false));
     a.out[0] = q_out; a.out[1] = k_out;
-    const unsigned blocks = (unsigned)ceil_div(T, a.tokens);
+    const unsigned blocks = (unsigned)std::min<int64_t>(ceil_div(T, a.tokens), (int64_t)sms * gdn::qk_resident(false));
     const bool vec = qk_vectors(args, s.q, s.q_stride) && qk_vectors(args, s.k, s.k_stride) &&
                      qk_vectors(args, q_out, wq) && qk_vectors(args, k_out, wk);
-    const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (s.in_dtype == GDN_BF16)
-        return vec ? qk_launch<__nv_bfloat16, true, false>(a, blocks, st) : qk_launch<__nv_bfloat16, false, false>(a, blocks, st);
-    return vec ? qk_launch<float, true, false>(a, blocks, st) : qk_launch<float, false, false>(a, blocks, st);
+    return qk_dispatch<false>(a, s.in_dtype, vec, blocks, static_cast<cudaStream_t>(stream));
 }
 
 size_t gdn_qk_norm_backward_workspace_size(int64_t tokens, int32_t head_dim)
@@ -213,19 +220,14 @@ gdn_status_t gdn_qk_norm_backward(const gdn_qk_norm_t* args, const void* dq_out,
     if (T > 0) {
         const int sms = sm_count();
         if (sms == 0) return GDN_ERR_CUDA;
-        gdn::QkArgs a = qk_args(args, sms);
+        gdn::QkArgs a = qk_args(args, (int)std::min<int64_t>(kQkParts, (int64_t)sms * gdn::qk_resident(true)));
         a.dy[0] = dq_out; a.dy[1] = dk_out; a.lddy[0] = dq_out_stride; a.lddy[1] = dk_out_stride;
         a.out[0] = dq; a.out[1] = dk; a.part = part;
-        parts = std::min<int64_t>(ceil_div(T, a.tokens), std::min<int64_t>(kQkParts, (int64_t)sms * 4));
+        parts = std::min<int64_t>(ceil_div(T, a.tokens), std::min<int64_t>(kQkParts, (int64_t)sms * gdn::qk_resident(true)));
         const bool vec = qk_vectors(args, s.q, s.q_stride) && qk_vectors(args, s.k, s.k_stride) &&
                          qk_vectors(args, dq_out, dq_out_stride) && qk_vectors(args, dk_out, dk_out_stride) &&
                          qk_vectors(args, dq, wq) && qk_vectors(args, dk, wk);
-        gdn_status_t r;
-        if (s.in_dtype == GDN_BF16)
-            r = vec ? qk_launch<__nv_bfloat16, true, true>(a, (unsigned)parts, st)
-                    : qk_launch<__nv_bfloat16, false, true>(a, (unsigned)parts, st);
-        else
-            r = vec ? qk_launch<float, true, true>(a, (unsigned)parts, st) : qk_launch<float, false, true>(a, (unsigned)parts, st);
+        const gdn_status_t r = qk_dispatch<true>(a, s.in_dtype, vec, (unsigned)parts, st);
         if (r != GDN_OK) return r;
     }
     if (!weights) return GDN_OK;

@@ -39,125 +39,120 @@ struct QkArgs {
 };
 
 constexpr int kQkThreads = 256;
-__host__ __device__ constexpr int qk_rows(bool bwd) { return bwd ? 2 : 4; }  // rows of a thread in flight
+__host__ __device__ constexpr int qk_rows(bool bwd, int esize) { return bwd || esize == 4 ? 2 : 4; }  // rows of a thread in flight
+__host__ __device__ constexpr int qk_resident(bool bwd) { return bwd ? 2 : 3; }    // blocks per SM
 
-// The elements of a thread's pair i (of 4 neighbouring ones).
-template <bool VEC>
+// A thread's four neighbouring pairs of a row: the elements a(i) and b(i), i < 4.  INTER: (2 p, 2 p + 1), else
+// (p, p + R / 2), and behind the rotated ones any two that are left.
+template <bool INTER>
 struct QkPairs {
-    int first, n, R2, inter;
-    __device__ __forceinline__ QkPairs(const QkArgs& a, int lane)
-        : first(lane * 4), n(a.d / 2), R2(a.rot / 2), inter(a.interleaved) {}
-    __device__ __forceinline__ int pair(int i) const { return first + i; }
-    __device__ __forceinline__ bool has(int i) const { return (VEC ? first : first + i) < n; }  // VEC: all four or none
-    // the pair's two elements; behind the rotated ones any two that are left
+    int first, n, R2;
+    __device__ __forceinline__ QkPairs(const QkArgs& a, int lane) : first(lane * 4), n(a.d / 2), R2(a.rot / 2) {}
+    __device__ __forceinline__ bool has(int i) const { return first + i < n; }
     __device__ __forceinline__ int a(int i) const
     {
-        const int p = pair(i);
-        return inter ? 2 * p : (p < R2 ? p : p + R2);
+        const int p = first + i;
+        return INTER ? 2 * p : (p < R2 ? p : p + R2);
     }
     __device__ __forceinline__ int b(int i) const
     {
-        const int p = pair(i);
-        return inter ? 2 * p + 1 : (p < R2 ? p + R2 : p + n);
+        const int p = first + i;
+        return INTER ? 2 * p + 1 : (p < R2 ? p + R2 : p + n);
     }
 };
 
-// A thread's share of a row: va and vb hold the elements a and b of its four pairs.  VEC: two accesses of
-// four elements, else one element at a time; the sums, and with them the bits, are the same.
-template <typename T, bool VEC>
+// A thread's share of a row, as it lies in memory: two accesses of four elements (VEC: all of its pairs or none are
+// there), or one element at a time.  The sums, and with them the bits, are the same.
+template <typename T, bool VEC, bool INTER>
 struct QkRow {
     Vec<T, 4> lo, hi;
-    __device__ __forceinline__ void load(const T* row, const QkPairs<VEC>& q)
+    __device__ __forceinline__ void load(const T* row, const QkPairs<INTER>& q, int ea, int eb)
     {
         if constexpr (VEC) {
-            if (q.has(0)) {
-                lo = load_vec<T, 4>(row + q.a(0));
-                hi = load_vec<T, 4>(row + (q.inter ? q.a(2) : q.b(0)));
+            lo = load_vec<T, 4>(row + ea);
+            hi = load_vec<T, 4>(row + eb);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                T& x = INTER ? (i < 2 ? lo.v[2 * i] : hi.v[2 * i - 4]) : lo.v[i];
+                T& y = INTER ? (i < 2 ? lo.v[2 * i + 1] : hi.v[2 * i - 3]) : hi.v[i];
+                x = q.has(i) ? row[q.a(i)] : from_f<T>(0.0f);
+                y = q.has(i) ? row[q.b(i)] : from_f<T>(0.0f);
+            }
+        }
+    }
+    // (a0, a1), (a2, a3) and (b0, b1), (b2, b3), widened
+    __device__ __forceinline__ void get(f2x (&va)[2], f2x (&vb)[2]) const
+    {
+        if constexpr (INTER) {
+            va[0] = pk2(to_f<T>(lo.v[0]), to_f<T>(lo.v[2])), va[1] = pk2(to_f<T>(hi.v[0]), to_f<T>(hi.v[2]));
+            vb[0] = pk2(to_f<T>(lo.v[1]), to_f<T>(lo.v[3])), vb[1] = pk2(to_f<T>(hi.v[1]), to_f<T>(hi.v[3]));
+        } else {
+            va[0] = pbits<T, 4>(lo, 0), va[1] = pbits<T, 4>(lo, 1);
+            vb[0] = pbits<T, 4>(hi, 0), vb[1] = pbits<T, 4>(hi, 1);
+        }
+    }
+    __device__ static __forceinline__ void store(T* row, const QkPairs<INTER>& q, int ea, int eb, const f2x (&va)[2], const f2x (&vb)[2])
+    {
+        float x[4], y[4];
+        up2(va[0], x[0], x[1]), up2(va[1], x[2], x[3]);
+        up2(vb[0], y[0], y[1]), up2(vb[1], y[2], y[3]);
+        if constexpr (VEC) {
+            if constexpr (INTER) {
+                const float l[4] = {x[0], y[0], x[1], y[1]}, h[4] = {x[2], y[2], x[3], y[3]};
+                store_vec<T, 4>(row + ea, l);
+                store_vec<T, 4>(row + eb, h);
+            } else {
+                store_vec<T, 4>(row + ea, x);
+                store_vec<T, 4>(row + eb, y);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (q.has(i)) {
-                    lo.v[i] = row[q.a(i)];
-                    hi.v[i] = row[q.b(i)];
-                }
-        }
-    }
-    __device__ __forceinline__ void get(const QkPairs<VEC>& q, float (&va)[4], float (&vb)[4]) const
-    {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            va[i] = q.has(i) ? to_f<T>(lo.v[i]) : 0.0f;
-            vb[i] = q.has(i) ? to_f<T>(hi.v[i]) : 0.0f;
-        }
-        if (VEC && q.inter) swap(va, vb);
-    }
-    // neighbouring pairs: (a0 b0 a1 b1), (a2 b2 a3 b3) <-> (a0 a1 a2 a3), (b0 b1 b2 b3)
-    __device__ static __forceinline__ void swap(float (&va)[4], float (&vb)[4])
-    {
-        const float x1 = va[1], x2 = va[2], x3 = va[3], y0 = vb[0], y1 = vb[1], y2 = vb[2];
-        va[1] = x2, va[2] = y0, va[3] = y2;
-        vb[0] = x1, vb[1] = x3, vb[2] = y1;
-    }
-    __device__ static __forceinline__ void join(float (&va)[4], float (&vb)[4])
-    {
-        const float a1 = va[1], a2 = va[2], a3 = va[3], b0 = vb[0], b1 = vb[1], b2 = vb[2];
-        va[1] = b0, va[2] = a1, va[3] = b1;
-        vb[0] = a2, vb[1] = b2, vb[2] = a3;
-    }
-    __device__ static __forceinline__ void store(T* row, const QkPairs<VEC>& q, float (&va)[4], float (&vb)[4])
-    {
-        if constexpr (VEC) {
-            if (q.has(0)) {
-                if (q.inter) join(va, vb);
-                store_vec<T, 4>(row + q.a(0), va);
-                store_vec<T, 4>(row + (q.inter ? q.a(2) : q.b(0)), vb);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (q.has(i)) {
-                    row[q.a(i)] = from_f<T>(va[i]);
-                    row[q.b(i)] = from_f<T>(vb[i]);
+                    row[q.a(i)] = from_f<T>(x[i]);
+                    row[q.b(i)] = from_f<T>(y[i]);
                 }
         }
     }
 };
 
-// Turns the pairs by the token's angles (sign = -1: back).
-template <bool VEC>
-__device__ __forceinline__ void qk_turn(const float2* cs, const QkPairs<VEC>& q, float sign, float (&va)[4], float (&vb)[4])
+// Four consecutive floats as two pairs; the address is 16-byte aligned.
+__device__ __forceinline__ void qk_four(const float* p, f2x (&v)[2])
 {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (q.pair(i) < q.R2) {
-            const float2 c = cs[q.pair(i)];
-            const float s = c.y * sign, x = va[i], y = vb[i];
-            va[i] = __fmaf_rn(x, c.x, -(y * s));
-            vb[i] = __fmaf_rn(y, c.x, x * s);
-        }
+    const float4 f = *reinterpret_cast<const float4*>(p);
+    v[0] = pk2(f.x, f.y), v[1] = pk2(f.z, f.w);
 }
 
-// BWD: the gradients.  T tokens, VEC as QkPairs.
-template <typename T, bool VEC, bool BWD>
-__global__ void __launch_bounds__(kQkThreads, BWD ? 2 : 3) k_qk_norm(const QkArgs a)
+// BWD: the gradients.
+template <typename T, bool VEC, bool INTER, bool BWD>
+__global__ void __launch_bounds__(kQkThreads, qk_resident(BWD)) k_qk_norm(const QkArgs a)
 {
-    constexpr int U = qk_rows(BWD);
+    constexpr int U = qk_rows(BWD, sizeof(T));
+    using Row = QkRow<T, VEC, INTER>;
     extern __shared__ __align__(16) unsigned char qk_smem[];
-    float2* cs = reinterpret_cast<float2*>(qk_smem);                         // [tokens][rot / 2]
-    float* ws = reinterpret_cast<float*>(cs + (int64_t)a.tokens * (a.rot / 2));  // [2][d]: the a's of all pairs, then the b's
+    // cosines [tokens][span] and sines, 1 and 0 behind the rotated pairs; span: the pairs of all lanes
+    float* cs = reinterpret_cast<float*>(qk_smem);
     const int tpr = a.tpr, lane = threadIdx.x & (tpr - 1), slot = threadIdx.x / tpr, slots = kQkThreads / tpr;
-    const int n = a.d / 2, R2 = a.rot / 2;
-    const QkPairs<VEC> pairs(a, lane);
-    for (int i = threadIdx.x; i < 2 * a.d; i += kQkThreads) {
-        const int kind = i / a.d, e = i % a.d, p = e < n ? e : e - n;
-        const int at = a.interleaved ? 2 * p + (e >= n) : (e < n ? (p < R2 ? p : p + R2) : (p < R2 ? p + R2 : p + n));
-        ws[i] = a.w[kind] != nullptr ? load_w(a.w[kind], a.w_bf16, at) : 1.0f;
+    const int R2 = a.rot / 2, span = tpr * 4, half = a.tokens * span;
+    const QkPairs<INTER> pairs(a, lane);
+    float* ws = cs + (R2 > 0 ? 2 * half : 0);  // weights [2][2][span]: those of the a's, then of the b's
+    const bool mine = pairs.has(0);
+    // VEC: where the two accesses start; lanes without a pair read the row's first elements, which count for nothing
+    const int ea = !mine ? 0 : INTER ? 2 * pairs.first : pairs.a(0), eb = !mine ? 0 : INTER ? 2 * pairs.first + 4 : pairs.b(0);
+    for (int i = threadIdx.x; i < 2 * span; i += kQkThreads) {
+        const int kind = i / span, p = i - kind * span;
+        const QkPairs<INTER> q(a, p / 4);
+        const bool in = a.w[kind] != nullptr && q.has(p % 4);
+        ws[(2 * kind) * span + p] = in ? load_w(a.w[kind], a.w_bf16, q.a(p % 4)) : 1.0f;
+        ws[(2 * kind + 1) * span + p] = in ? load_w(a.w[kind], a.w_bf16, q.b(p % 4)) : 1.0f;
     }
     __syncthreads();
-    float da[2][4], db[2][4];  // backward: this thread's columns of dw, of q and k
+    const bool weighted = a.w[0] != nullptr || a.w[1] != nullptr;
+    // this thread's columns of dw: of the kind that is worked on, and of the other one
+    f2x da[2], db[2], oa[2], ob[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) da[0][i] = da[1][i] = db[0][i] = db[1][i] = 0.0f;
+    for (int i = 0; i < 2; ++i) da[i] = db[i] = oa[i] = ob[i] = pk2(0.0f, 0.0f);
 
     const int64_t tiles = (a.T + a.tokens - 1) / a.tokens;
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
@@ -165,125 +160,201 @@ __global__ void __launch_bounds__(kQkThreads, BWD ? 2 : 3) k_qk_norm(const QkArg
         const int nt = (int)min((int64_t)a.tokens, a.T - t0);
         if (R2 > 0) {
             __syncthreads();  // the last tile's angles have been read
-            for (int i = threadIdx.x; i < nt * R2; i += kQkThreads) {
-                const int t = i / R2, p = i - t * R2;
-                const double turns = (double)a.pos[t0 + t] * ((double)a.freq[p] * 0.15915494309189533577);
-                float s, c;
-                sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
-                cs[i] = make_float2(c, s);
+            for (int i = threadIdx.x; i < nt * span; i += kQkThreads) {
+                const int t = i / span, p = i - t * span;
+                float s = 0.0f, c = 1.0f;
+                if (p < R2) {
+                    const double turns = (double)a.pos[t0 + t] * ((double)a.freq[p] * 0.15915494309189533577);
+                    sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
+                }
+                cs[i] = c;
+                cs[half + i] = s;
             }
             __syncthreads();
         }
-#pragma unroll
+#pragma unroll 1
         for (int kind = 0; kind < 2; ++kind) {
-            const int H = a.H[kind], rows = nt * H;
-            const T* x0 = static_cast<const T*>(a.x[kind]) + t0 * a.ldx[kind];
-            const T* g0 = BWD ? static_cast<const T*>(a.dy[kind]) + t0 * a.lddy[kind] : nullptr;
-            T* o0 = static_cast<T*>(a.out[kind]) + t0 * H * a.d;
-            float wa[4], wb[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                wa[i] = pairs.has(i) ? ws[kind * a.d + pairs.pair(i)] : 0.0f;
-                wb[i] = pairs.has(i) ? ws[kind * a.d + n + pairs.pair(i)] : 0.0f;
-            }
-            for (int r0 = 0; r0 < rows; r0 += slots * U) {  // the same turns for every thread: the sums are shuffles
-                QkRow<T, VEC> x[U], g[BWD ? U : 1];
-                int tok[U];
+            f2x wa[2], wb[2];
+            qk_four(ws + 2 * kind * span + pairs.first, wa);
+            qk_four(ws + (2 * kind + 1) * span + pairs.first, wb);
+            const int H = a.H[kind], rows = nt * H, dt = slots / H, dh = slots - dt * H;
+            const int64_t ldx = a.ldx[kind], ldg = BWD ? a.lddy[kind] : 0;
+            // this thread's next row: its head, its angles, and where it lies; from there to the next one, `slots` rows
+            // on, dt tokens and dh heads, or one token more and H heads less
+            const int tok0 = slot / H;
+            int h = slot - tok0 * H, at = tok0 * span + pairs.first;
+            const T* px = static_cast<const T*>(a.x[kind]) + (t0 + tok0) * ldx + h * a.d;
+            const T* pg = BWD ? static_cast<const T*>(a.dy[kind]) + (t0 + tok0) * ldg + h * a.d : nullptr;
+            T* po = static_cast<T*>(a.out[kind]) + (t0 * H + slot) * (int64_t)a.d;
+            const int64_t stepx = dt * ldx + dh * a.d, wrapx = ldx - (int64_t)H * a.d;
+            const int64_t stepg = dt * ldg + dh * a.d, wrapg = ldg - (int64_t)H * a.d;
+            const int64_t stepo = (int64_t)slots * a.d;
+            auto some = [&](auto count, int r0) {  // so many rows of every thread; more than one: all of them are there
+                constexpr int U = decltype(count)::value;
+                constexpr bool WHOLE = U > 1;
+                Row x[U];
+                [[maybe_unused]] Row g[BWD ? U : 1];
+                int ang[U];
+                bool on[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const int r = r0 + u * slots + slot;
-                    tok[u] = r / H;
-                    if (r < rows) {
-                        x[u].load(x0 + tok[u] * a.ldx[kind] + (r - tok[u] * H) * a.d, pairs);
-                        if constexpr (BWD) g[u].load(g0 + tok[u] * a.lddy[kind] + (r - tok[u] * H) * a.d, pairs);
+                    on[u] = WHOLE || r0 + slot < rows;
+                    ang[u] = at;
+                    if (on[u]) {
+                        x[u].load(px, pairs, ea, eb);
+                        if constexpr (BWD) g[u].load(pg, pairs, ea, eb);
+                    }
+                    px += stepx;
+                    if constexpr (BWD) pg += stepg;
+                    at += dt * span;
+                    h += dh;
+                    if (dh != 0 && h >= H) {
+                        h -= H;
+                        at += span;
+                        px += wrapx;
+                        if constexpr (BWD) pg += wrapg;
                     }
                 }
-                float ss[U], sg[BWD ? U : 1];
-                float ga[BWD ? U : 1][4], gb[BWD ? U : 1][4];
+                float ss[U];
+                [[maybe_unused]] float sg[BWD ? U : 1];
+                [[maybe_unused]] f2x ga[BWD ? U : 1][2], gb[BWD ? U : 1][2];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const bool on = r0 + u * slots + slot < rows;
-                    float va[4], vb[4];
-                    x[u].get(pairs, va, vb);
                     ss[u] = 0.0f;
+                    if constexpr (BWD) sg[u] = 0.0f;
+                    if (on[u]) {
+                        f2x va[2], vb[2];
+                        x[u].get(va, vb);
+                        ss[u] = psum(pfma(va[0], va[0], pfma(va[1], va[1], pfma(vb[0], vb[0], pmul(vb[1], vb[1])))));
+                        if constexpr (BWD) {
+                            g[u].get(ga[u], gb[u]);
+                            if (R2 > 0) {  // turned back
+                                f2x c[2], s[2];
+                                qk_four(cs + ang[u], c);
+                                qk_four(cs + half + ang[u], s);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) ss[u] = __fmaf_rn(va[i], va[i], __fmaf_rn(vb[i], vb[i], ss[u]));
-                    if constexpr (BWD) {
-                        sg[u] = 0.0f;
-                        if (on) {
-                            g[u].get(pairs, ga[u], gb[u]);
-                            qk_turn<VEC>(cs + tok[u] * R2, pairs, -1.0f, ga[u], gb[u]);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                sg[u] = __fmaf_rn(ga[u][i] * wa[i], va[i], __fmaf_rn(gb[u][i] * wb[i], vb[i], sg[u]));
+                                for (int i = 0; i < 2; ++i) {
+                                    const f2x p = ga[u][i], q = gb[u][i];
+                                    ga[u][i] = pfma(p, c[i], pmul(q, s[i]));
+                                    gb[u][i] = pfma(pmul(p, pk2(-1.0f, -1.0f)), s[i], pmul(q, c[i]));
+                                }
+                            }
+                            f2x acc = pmul(pmul(ga[u][0], wa[0]), va[0]);
+                            acc = pfma(pmul(ga[u][1], wa[1]), va[1], acc);
+                            acc = pfma(pmul(gb[u][0], wb[0]), vb[0], acc);
+                            sg[u] = psum(pfma(pmul(gb[u][1], wb[1]), vb[1], acc));
+                            if (!mine) sg[u] = 0.0f;
                         }
+                        if (!mine) ss[u] = 0.0f;
                     }
                 }
-                for (int o = tpr >> 1; o > 0; o >>= 1) {
+                auto fold = [&](int o) {
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
                         ss[u] += __shfl_xor_sync(kFullMask, ss[u], o);
                         if constexpr (BWD) sg[u] += __shfl_xor_sync(kFullMask, sg[u], o);
                     }
-                }
+                };
+                if (tpr > 16) fold(16);
+                if (tpr > 8) fold(8);
+                if (tpr > 4) fold(4);
+                if (tpr > 2) fold(2);
+                if (tpr > 1) fold(1);
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const int r = r0 + u * slots + slot;
-                    if (r >= rows) continue;
-                    const float rr = inv_sqrt(__fmaf_rn(ss[u], a.inv_n, a.eps));
-                    float va[4], vb[4];
-                    x[u].get(pairs, va, vb);
-                    if constexpr (BWD) {
-                        // as in layer norm, no power of r is formed: x r is again about 1
-                        const float c = sg[u] * rr * a.inv_n;
+                    if (on[u]) {
+                        const float rr = inv_sqrt(__fmaf_rn(ss[u], a.inv_n, a.eps));
+                        const f2x r2 = pk2(rr, rr);
+                        f2x va[2], vb[2];
+                        keep_packed(x[u].lo);
+                        keep_packed(x[u].hi);
+                        x[u].get(va, vb);
+                        if constexpr (BWD) {
+                            // as in layer norm, no power of r is formed: x r is again about 1
+                            const float c = -(sg[u] * rr * a.inv_n);
+                            const f2x c2 = pk2(c, c);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float na = va[i] * rr, nb = vb[i] * rr;
-                            da[kind][i] = __fmaf_rn(ga[u][i], na, da[kind][i]);
-                            db[kind][i] = __fmaf_rn(gb[u][i], nb, db[kind][i]);
-                            va[i] = rr * __fmaf_rn(-na, c, ga[u][i] * wa[i]);
-                            vb[i] = rr * __fmaf_rn(-nb, c, gb[u][i] * wb[i]);
-                        }
-                    } else {
+                            for (int i = 0; i < 2; ++i) {
+                                const f2x na = pmul(va[i], r2), nb = pmul(vb[i], r2);
+                                da[i] = pfma(ga[u][i], na, da[i]);
+                                db[i] = pfma(gb[u][i], nb, db[i]);
+                                va[i] = pmul(r2, pfma(na, c2, pmul(ga[u][i], wa[i])));
+                                vb[i] = pmul(r2, pfma(nb, c2, pmul(gb[u][i], wb[i])));
+                            }
+                        } else {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            va[i] = va[i] * rr * wa[i];
-                            vb[i] = vb[i] * rr * wb[i];
+                            for (int i = 0; i < 2; ++i) {
+                                va[i] = pmul(va[i], r2);
+                                vb[i] = pmul(vb[i], r2);
+                                if (weighted) {
+                                    va[i] = pmul(va[i], wa[i]);
+                                    vb[i] = pmul(vb[i], wb[i]);
+                                }
+                            }
+                            if (R2 > 0) {
+                                f2x c[2], s[2];
+                                qk_four(cs + ang[u], c);
+                                qk_four(cs + half + ang[u], s);
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    const f2x p = va[i], q = vb[i];
+                                    va[i] = pfma(pmul(q, pk2(-1.0f, -1.0f)), s[i], pmul(p, c[i]));
+                                    vb[i] = pfma(p, s[i], pmul(q, c[i]));
+                                }
+                            }
                         }
-                        qk_turn<VEC>(cs + tok[u] * R2, pairs, 1.0f, va, vb);
+                        if (mine) Row::store(po + u * stepo, pairs, ea, eb, va, vb);
                     }
-                    QkRow<T, VEC>::store(o0 + (int64_t)r * a.d, pairs, va, vb);
+                }
+                po += U * stepo;
+            };
+            // the same turns for every thread: the sums are shuffles
+            int r0 = 0;
+            for (; r0 + slots * U <= rows; r0 += slots * U) some(std::integral_constant<int, U>{}, r0);
+            for (; r0 < rows; r0 += slots) some(std::integral_constant<int, 1>{}, r0);
+            if constexpr (BWD) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    f2x t = da[i];
+                    da[i] = oa[i], oa[i] = t;
+                    t = db[i];
+                    db[i] = ob[i], ob[i] = t;
                 }
             }
         }
     }
-    if (!BWD || a.part == nullptr) return;
-    // dw: the rows of a warp by shuffles, then the warps in order
-    float* red = ws;  // [8][d], behind the angles; the weights are in registers
-    float* part = a.part + (int64_t)blockIdx.x * 2 * a.d;
+    if constexpr (BWD) {
+        if (a.part == nullptr) return;
+        // dw: the rows of a warp by shuffles, then the warps in order
+        float* red = cs;  // [8][d]
+        float* part = a.part + (int64_t)blockIdx.x * 2 * a.d;
 #pragma unroll
-    for (int kind = 0; kind < 2; ++kind) {
-        for (int o = 16; o >= tpr; o >>= 1)
+        for (int kind = 0; kind < 2; ++kind) {
+            float x[4], y[4];
+            up2(kind ? oa[0] : da[0], x[0], x[1]), up2(kind ? oa[1] : da[1], x[2], x[3]);
+            up2(kind ? ob[0] : db[0], y[0], y[1]), up2(kind ? ob[1] : db[1], y[2], y[3]);
+            for (int o = 16; o >= tpr; o >>= 1)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                da[kind][i] += __shfl_xor_sync(kFullMask, da[kind][i], o);
-                db[kind][i] += __shfl_xor_sync(kFullMask, db[kind][i], o);
-            }
-        __syncthreads();
-        if ((threadIdx.x & 31) < tpr) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (pairs.has(i)) {
-                    red[(threadIdx.x >> 5) * a.d + pairs.a(i)] = da[kind][i];
-                    red[(threadIdx.x >> 5) * a.d + pairs.b(i)] = db[kind][i];
+                for (int i = 0; i < 4; ++i) {
+                    x[i] += __shfl_xor_sync(kFullMask, x[i], o);
+                    y[i] += __shfl_xor_sync(kFullMask, y[i], o);
                 }
-        }
-        __syncthreads();
-        for (int c = threadIdx.x; c < a.d; c += kQkThreads) {
-            float s = 0.0f;
+            __syncthreads();
+            if ((threadIdx.x & 31) < tpr) {
 #pragma unroll
-            for (int w = 0; w < kQkThreads / 32; ++w) s += red[w * a.d + c];
-            part[kind * a.d + c] = s;
+                for (int i = 0; i < 4; ++i)
+                    if (pairs.has(i)) {
+                        red[(threadIdx.x >> 5) * a.d + pairs.a(i)] = x[i];
+                        red[(threadIdx.x >> 5) * a.d + pairs.b(i)] = y[i];
+                    }
+            }
+            __syncthreads();
+            for (int c = threadIdx.x; c < a.d; c += kQkThreads) {
+                float s = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kQkThreads / 32; ++w) s += red[w * a.d + c];
+                part[kind * a.d + c] = s;
+            }
         }
     }
 }
