@@ -96,6 +96,8 @@ gdn_status_t glu_gemm(gdn::GluMaps& maps, gdn::GluGemmArgs& a, int sms, cudaStre
     return launched() ? GDN_OK : GDN_ERR_CUDA;
 }
 
+constexpr int64_t kGluFewRows = 256;  // up to so many tokens the weights are streamed past them
+
 // Parts of the K axis of a product with few tiles: enough for every pair of SMs, each of at least 8 stages.
 int glu_splits(int64_t tiles, int64_t ksteps, int sms)
 {
@@ -103,25 +105,32 @@ int glu_splits(int64_t tiles, int64_t ksteps, int sms)
     return (int)std::max<int64_t>(1, std::min<int64_t>({want, ksteps / 8, 64}));
 }
 
+// Blocks take equal shares of the units, in multiples of 8 up to 64: one block per SM, with all of its shared memory, or
+// two where 64 units for each SM are not enough.  With fewer units than 32 for each SM, clusters of 2, 4 or 8 blocks
+// share the K axis.
 template <int NB>
-gdn_status_t glu_few(const GluOperands& o, const gdn_glu_t& s, const gdn::GluFewArgs& a, int sms, cudaStream_t st)
+gdn_status_t glu_few(const GluOperands& o, const gdn_glu_t& s, gdn::GluFewArgs& a, int sms, cudaStream_t st)
 {
-    gdn::GluFewMaps maps;
-    if (!matrix_map(&maps.x, o.x, s.rows, s.width, o.ldx, NB) || !matrix_map(&maps.wg, o.wg, s.inner, s.width, o.ldg, 128) ||
-        !matrix_map(&maps.wu, o.wu, s.inner, s.width, o.ldu, 128))
-        return GDN_ERR_CUDA;
-    using G = gdn::GluFew<NB>;
-    const int tiles = (int)ceil_div(s.inner, 128);
-    // blocks for every SM, two of them where they fit, each with 4 stages at least
-    const int room = sms * (G::SMEM <= 113 * 1024 ? 2 : 1);
+    // a cluster's blocks lie in one group of SMs, of which a few are left over: a full house would come in two waves
+    const auto slots = [&](int S) { return S > 1 ? sms * 7 / 8 : sms; };
     int S = 1;
-    while (S < 8 && tiles * S * 2 <= room && a.ksteps >= 4 * S * 2) S *= 2;
+    while (S < 4 && ceil_div((int64_t)s.inner * S * 2, slots(2)) <= 64 && a.ksteps >= 8 * S) S *= 2;
+    const int resident = ceil_div((int64_t)s.inner * S, slots(S)) <= 64 ? 1 : 2;
+    a.rows = (int)std::min<int64_t>(64, ceil_div(ceil_div((int64_t)s.inner * S, (int64_t)slots(S) * resident), 8) * 8);
+    a.chunks = NB > 128 ? 1 : NB > 16 ? 2 : 4;
+    const size_t room = (size_t)(resident == 1 ? 224 : 110) * 1024 - gdn::kGluOperand;
+    a.stages = (int)std::min<size_t>(gdn::kGluFewStages, room / (a.chunks * gdn::glu_few_chunk(NB, a.rows)));
+    const size_t smem = gdn::glu_few_tiles(NB, a.rows, a.stages, a.chunks) + 1024 + 512;
+    gdn::GluFewMaps maps;
+    if (!matrix_map(&maps.x, o.x, s.rows, s.width, o.ldx, NB) || !matrix_map(&maps.wg, o.wg, s.inner, s.width, o.ldg, a.rows) ||
+        !matrix_map(&maps.wu, o.wu, s.inner, s.width, o.ldu, a.rows))
+        return GDN_ERR_CUDA;
     auto k = gdn::k_glu_few<NB>;
-    if (!raise_smem(k, G::SMEM)) return GDN_ERR_CUDA;
+    if (!raise_smem(k, smem)) return GDN_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(tiles * S));
+    cfg.gridDim = dim3((unsigned)ceil_div(s.inner, a.rows) * S, (unsigned)ceil_div(s.rows, NB));
     cfg.blockDim = dim3(gdn::kGluThreads);
-    cfg.dynamicSmemBytes = G::SMEM;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -198,8 +207,9 @@ gdn_status_t gdn_glu_forward(const gdn_glu_t* args, void* h, void* saved, void* 
     const GluOperands o = glu_operands(s, static_cast<unsigned char*>(workspace));
     if (!glu_align_all(s, o, st)) return GDN_ERR_CUDA;
     const int32_t ksteps = (int32_t)ceil_div(D, gdn::kGluK);
-    if (R <= 256) {
-        gdn::GluFewArgs a{(int32_t)R, s.inner, ksteps, h, static_cast<uint16_t*>(saved), s.act, status};
+    if (R <= kGluFewRows) {
+        gdn::GluFewArgs a{};
+        a.T = (int32_t)R; a.F = s.inner; a.ksteps = ksteps; a.h = h; a.saved = static_cast<uint16_t*>(saved); a.act = s.act; a.status = status;
         if (R <= 16) return glu_few<16>(o, s, a, sms, st);
         if (R <= 32) return glu_few<32>(o, s, a, sms, st);
         if (R <= 64) return glu_few<64>(o, s, a, sms, st);

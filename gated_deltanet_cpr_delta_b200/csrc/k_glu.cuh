@@ -15,9 +15,10 @@
 //   dx        A = dg, then du; B = Wg, then Wu, with the output's columns contiguous (read as K x N)
 //   dW        A = dg or du as K x M, B = x as K x N; the two gradients are the two halves of the tiles
 //
-// k_glu_few serves up to 256 tokens, where the weights' bytes bound it: 128 rows of Wg and of Wu are the M side, the
-// tokens the N side (16 to 256), and the K axis is split over a cluster whose partial sums meet in
-// distributed shared memory in a fixed order.
+// k_glu_few serves few tokens, where the weights' bytes bound it: a block holds up to 64 rows of Wg and the same ones of Wu
+// as the M side of one product, as many as give every SM the same share of them, and streams them past the
+// tokens (the N side, 16 to 256).  Where that would leave few rows, a cluster of blocks shares the K axis,
+// and its partial sums meet in distributed shared memory, in a fixed order.
 #pragma once
 
 #include "k_tc.cuh"
@@ -104,6 +105,10 @@ __device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x,
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
         ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(mbar))
         : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 template <int GROUP>
 __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
@@ -404,8 +409,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGluThreads, 1)
 }
 
 // ------------------------------------------------------------- few tokens
+constexpr int kGluFewStages = 24;  // most stages
+
 struct GluFewArgs {
-    int32_t T, F, ksteps;
+    int32_t T, F, ksteps;          // ksteps: of 64 columns
+    int32_t rows, stages, chunks;  // units of a block (a multiple of 8, at most 64); stages; 64 columns in each
     void* h;
     uint16_t* saved;
     int32_t act;
@@ -416,35 +424,38 @@ struct GluFewMaps {
     CUtensorMap x, wg, wu;
 };
 
-template <int NB>
-struct GluFew {
-    static constexpr uint32_t STAGE = 2 * kGluOperand + NB * 128;
-    // two CTAs per SM up to 128 tokens
-    static constexpr int STAGES = NB <= 32 ? 3 : NB <= 128 ? 2 : 3;
-    static constexpr int CHUNK = NB < 32 ? NB : 32;                        // tokens that meet at a time
-    static constexpr uint32_t COLS = 2 * NB < 32 ? 32 : 2 * NB;            // of tensor memory
-    static constexpr size_t SMEM = (size_t)STAGES * STAGE + 1024 + 128;
-    static_assert((size_t)2 * CHUNK * 128 * 4 <= (size_t)STAGES * STAGE, "the partial sums lie where the operands were");
-};
+// Shared memory of 64 columns: the units of Wg, the same of Wu, NB tokens
+__host__ __device__ constexpr uint32_t glu_few_chunk(int NB, int rows) { return (uint32_t)(2 * rows + NB) * 128; }
+// The stages; the product reads 128 rows from each one's start on, whose rows behind the weights' count for
+// nothing; the results lie where the stages were.
+__host__ __device__ inline uint32_t glu_few_tiles(int NB, int rows, int stages, int chunks)
+{
+    const uint32_t tiles = stages * chunks * glu_few_chunk(NB, rows) + kGluOperand, results = 2 * NB * 64 * 4;
+    return tiles > results ? tiles : results;
+}
 
 template <int NB>
 __global__ void __launch_bounds__(kGluThreads, 1) k_glu_few(const __grid_constant__ GluFewMaps maps, const GluFewArgs a)
 {
-    using G = GluFew<NB>;
-    constexpr int ST = G::STAGES, CH = G::CHUNK;
+    constexpr uint32_t COLS = NB < 32 ? 32 : NB;
     constexpr uint32_t IDESC = bf16_idesc(128, NB, true, true);
     extern __shared__ unsigned char glu_smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(glu_smem_raw) + 1023) & ~(uintptr_t)1023);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + ST * G::STAGE);
-    uint64_t* empty = full + ST;
-    uint64_t* done = empty + ST;
+    const int ST = a.stages, C = a.chunks;
+    const uint32_t chunk = glu_few_chunk(NB, a.rows);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + glu_few_tiles(NB, a.rows, ST, C));
+    uint64_t* empty = full + kGluFewStages;
+    uint64_t* done = empty + kGluFewStages;
     uint32_t* slot = reinterpret_cast<uint32_t*>(done + 1);
-    uint32_t S;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t S;  // blocks that share the K axis
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(S));
     const uint32_t rank = cta_rank();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int f0 = (int)(blockIdx.x / S) * 128;
-    const int k0 = (int)((int64_t)a.ksteps * rank / S), k1 = (int)((int64_t)a.ksteps * (rank + 1) / S);
+    const int f0 = blockIdx.x / S * a.rows, t0 = blockIdx.y * NB;
+    const int all = (a.ksteps + C - 1) / C, first = (int)((int64_t)all * rank / S);
+    const int turns = (int)((int64_t)all * (rank + 1) / S) - first;  // at least one: the host sees to it
+    if (lane == 0 && (warp == 0 || warp == 2 || warp == 3))
+        prefetch_map(warp == 0 ? &maps.wg : warp == 2 ? &maps.wu : &maps.x);
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(full + i, 1);
@@ -452,23 +463,25 @@ __global__ void __launch_bounds__(kGluThreads, 1) k_glu_few(const __grid_constan
         }
         mbar_init(done, 1);
     }
-    if (warp == 2) tmem_alloc(slot, G::COLS);
+    if (warp == 2) tmem_alloc(slot, COLS);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *slot;
     bool ok = true;
-    if (warp == 0) {
+    if (warp == 0 || warp == 2 || warp == 3) {
         if (lane == 0) {
+            // one warp for each operand; the first announces the bytes of all
+            const CUtensorMap* map = warp == 0 ? &maps.wg : warp == 2 ? &maps.wu : &maps.x;
+            const uint32_t at = warp == 0 ? 0 : warp == 2 ? a.rows * 128 : 2 * a.rows * 128;
+            const int y = warp == 3 ? t0 : f0;
             int s = 0;
             uint32_t ph = 1;
-            for (int k = k0; k < k1; ++k) {
+            for (int k = 0; k < turns; ++k) {
                 if (!(ok = mbar_wait(empty + s, ph))) break;
-                unsigned char* p = smem + s * G::STAGE;
-                mbar_arrive_expect_tx(full + s, G::STAGE);
-                tma_2d(p, &maps.wg, k * kGluK, f0, full + s);
-                tma_2d(p + kGluOperand, &maps.wu, k * kGluK, f0, full + s);
-                tma_2d(p + 2 * kGluOperand, &maps.x, k * kGluK, 0, full + s);
+                if (warp == 0) mbar_arrive_expect_tx(full + s, C * chunk);
+                for (int c = 0; c < C; ++c)
+                    tma_2d(smem + (s * C + c) * chunk + at, map, ((first + k) * C + c) * kGluK, y, full + s);
                 if (++s == ST) s = 0, ph ^= 1;
             }
         }
@@ -476,16 +489,14 @@ __global__ void __launch_bounds__(kGluThreads, 1) k_glu_few(const __grid_constan
         if (lane == 0) {
             int s = 0;
             uint32_t ph = 0;
-            for (int k = k0; k < k1; ++k) {
+            for (int k = 0; k < turns; ++k) {
                 if (!(ok = mbar_wait(full + s, ph))) break;
                 tc_fence_after();
-                const uint32_t p = smem_addr(smem + s * G::STAGE);
-                const uint64_t dg = swizzled_desc(p, true), du = swizzled_desc(p + kGluOperand, true),
-                               dx = swizzled_desc(p + 2 * kGluOperand, true);
+                for (int c = 0; c < C; ++c) {
+                    const uint32_t p = smem_addr(smem + (s * C + c) * chunk);
+                    const uint64_t dw = swizzled_desc(p, true), dx = swizzled_desc(p + 2 * a.rows * 128, true);
 #pragma unroll
-                for (int j = 0; j < kGluK / 16; ++j) {
-                    mma_bf16<1>(tmem, dg + 2 * j, dx + 2 * j, IDESC, k > k0 || j > 0);
-                    mma_bf16<1>(tmem + NB, du + 2 * j, dx + 2 * j, IDESC, k > k0 || j > 0);
+                    for (int j = 0; j < kGluK / 16; ++j) mma_bf16<1>(tmem, dw + 2 * j, dx + 2 * j, IDESC, k > 0 || c > 0 || j > 0);
                 }
                 mma_commit(empty + s);
                 if (++s == ST) s = 0, ph ^= 1;
@@ -494,72 +505,75 @@ __global__ void __launch_bounds__(kGluThreads, 1) k_glu_few(const __grid_constan
         }
     }
     __syncwarp();
-    // every thread: the operands are no longer read once the accumulators are complete
     if (!mbar_wait(done, 0)) ok = false;
     tc_fence_after();
     ok = __syncthreads_and(ok);
-    const bool none = k0 >= k1;
-    const int r = 32 * (warp & 3) + lane, f = f0 + r;  // this thread's unit
-    const uint32_t col = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    auto finish = [&](int t, float g, float u) {
-        if (t >= a.T || f >= a.F) return;
-        const int64_t at = (int64_t)t * a.F + f;
-        if (a.saved != nullptr) {
-            const int64_t plane = (int64_t)a.T * a.F;
-            glu_pack(g, u, a.saved[at], a.saved[plane + at], a.saved[2 * plane + at]);
+    // accumulators to shared memory: [2][tokens][64 units], half of the tokens by either four warps
+    float* out = reinterpret_cast<float*>(smem);
+    {
+        const int r = 32 * (warp & 3) + lane;
+        const uint32_t col = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const int up = r >= a.rows;  // rows behind both are written nowhere
+        float* to = out + up * NB * 64 + (r - up * a.rows);
+        for (int c = (warp >> 2) * 16; c < NB && t0 + c < a.T; c += 32) {
+            float x[16];
+            tmem_ld16(col + c, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (r < 2 * a.rows) to[(c + j) * 64] = x[j];
+            __syncwarp();
         }
-        static_cast<__nv_bfloat16*>(a.h)[at] = __float2bfloat16_rn(glu_act(g, a.act) * u);
-    };
-    // a wait that ran out leaves the outputs as they are; the cluster's barriers are passed all the same
-    float* part = reinterpret_cast<float*>(smem);  // [2][CH][128]
-    for (int c = 0; c < NB && c < a.T; c += CH) {
-        if (warp < 4) {
-#pragma unroll 1
-            for (int i = 0; i < CH; i += 16) {
-                float g[16], u[16];
-                tmem_ld16(col + c + i, g);
-                tmem_ld16(col + NB + c + i, u);
-                tmem_wait_ld();
-                if (none) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) g[j] = u[j] = 0.0f;
-                }
-                if (S == 1) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (ok) finish(c + i + j, g[j], u[j]);
-                    __syncwarp();
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        part[(i + j) * 128 + r] = g[j];
-                        part[(CH + i + j) * 128 + r] = u[j];
-                    }
-                }
-            }
-        }
-        if (S > 1) {
-            cluster_barrier();
-            // token by token round the cluster; two of them at a time in a block
-            for (int t = (int)rank * 2 + (warp >> 2); t < CH; t += (int)S * 2) {
-                float g = 0.0f, u = 0.0f;
-                for (uint32_t q = 0; q < S; ++q) {
-                    const uint32_t p = peer_addr(part + t * 128 + r, q);
-                    float x, y;
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(p) : "memory");
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(y) : "r"(p + CH * 128 * 4) : "memory");
-                    g += x;
-                    u += y;
-                }
-                if (ok) finish(c + t, g, u);
-            }
-            cluster_barrier();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) tmem_dealloc(tmem, COLS);
+    if (S > 1) {
+        // a wait that ran out counts for the whole cluster
+        if (threadIdx.x == 0) *slot = ok;
+        cluster_barrier();
+        for (uint32_t q = 0; q < S; ++q) {
+            uint32_t good;
+            asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(good) : "r"(peer_addr(slot, q)) : "memory");
+            ok = ok && good;
         }
     }
     if (!ok && threadIdx.x == 0 && a.status != nullptr) atomicCAS(a.status, GDN_OK, GDN_ERR_TIMEOUT);
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 2) tmem_dealloc(tmem, G::COLS);
+    const int r = threadIdx.x & 63, f = f0 + r;
+    const int64_t plane = (int64_t)a.T * a.F;
+    if (ok && r < a.rows && f < a.F) {  // else the outputs are left as they are
+        auto finish = [&](int t, float g, float u) {
+            const int64_t at = (int64_t)(t0 + t) * a.F + f;
+            if (a.saved != nullptr) glu_pack(g, u, a.saved[at], a.saved[plane + at], a.saved[2 * plane + at]);
+            static_cast<__nv_bfloat16*>(a.h)[at] = __float2bfloat16_rn(glu_act(g, a.act) * u);
+        };
+        const int last = min(NB, a.T - t0), group = threadIdx.x >> 6;
+        if (S == 1) {
+#pragma unroll 4
+            for (int t = group; t < last; t += kGluThreads / 64) finish(t, out[t * 64 + r], out[(NB + t) * 64 + r]);
+        } else {
+            // tokens round the cluster
+            for (int t = (int)rank + (int)S * group; t < last; t += (int)S * (kGluThreads / 64)) {
+                float g = 0.0f, u = 0.0f;
+#pragma unroll
+                for (uint32_t q = 0; q < 8; ++q) {
+                    if (q < S) {
+                        const uint32_t p = peer_addr(out + t * 64 + r, q);
+                        float x, y;
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(p) : "memory");
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(y) : "r"(p + NB * 64 * 4) : "memory");
+                        g += x;
+                        u += y;
+                    }
+                }
+                finish(t, g, u);
+            }
+        }
+    }
+    if (S > 1) {
+        __syncwarp();
+        cluster_barrier();  // no block ends while another reads it
+    }
 }
 
 // ------------------------------------------------------------- elementwise parts
