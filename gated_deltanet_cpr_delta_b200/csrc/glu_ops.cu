@@ -54,20 +54,28 @@ GluOperands glu_operands(const gdn_glu_t& s, unsigned char* p)
     return o;
 }
 
-bool glu_align(const void* src, int64_t lds, const void* dst, int64_t ldd, int64_t rows, int64_t cols, cudaStream_t st)
+bool glu_align(const gdn_glu_t& s, const GluOperands& o, int sms, cudaStream_t st)
 {
-    if (src == dst || rows == 0) return true;
-    const int64_t n = rows * (ldd / 8);
-    gdn::k_glu_align<<<(unsigned)std::min<int64_t>(ceil_div(n, 256), 148 * 16), 256, 0, st>>>(
-        static_cast<const uint16_t*>(src), lds, rows, cols, static_cast<uint16_t*>(const_cast<void*>(dst)), ldd);
+    gdn::GluAlign a{};
+    a.cols = s.width;
+    a.ldd = pad8(s.width);
+    int m = 0;
+    int64_t most = 0;
+    auto add = [&](const void* src, int64_t lds, const void* dst, int64_t rows) {
+        if (src == dst || rows == 0) return;
+        a.src[m] = static_cast<const uint16_t*>(src);
+        a.dst[m] = static_cast<uint16_t*>(const_cast<void*>(dst));
+        a.lds[m] = lds;
+        a.rows[m++] = rows;
+        most = std::max(most, rows);
+    };
+    add(s.x, s.x_stride, o.x, s.rows);
+    add(s.w_gate, s.gate_stride, o.wg, s.inner);
+    add(s.w_up, s.up_stride, o.wu, s.inner);
+    if (m == 0) return true;
+    const dim3 grid((unsigned)std::min<int64_t>(ceil_div(most * (a.ldd / 8), 256), (int64_t)sms * 8), (unsigned)m);
+    gdn::k_glu_align<<<grid, 256, 0, st>>>(a);
     return launched();
-}
-
-bool glu_align_all(const gdn_glu_t& s, const GluOperands& o, cudaStream_t st)
-{
-    return glu_align(s.x, s.x_stride, o.x, o.ldx, s.rows, s.width, st) &&
-           glu_align(s.w_gate, s.gate_stride, o.wg, o.ldg, s.inner, s.width, st) &&
-           glu_align(s.w_up, s.up_stride, o.wu, o.ldu, s.inner, s.width, st);
 }
 
 gdn_status_t glu_check(const gdn_glu_t* s, const int32_t* status)
@@ -205,7 +213,7 @@ gdn_status_t gdn_glu_forward(const gdn_glu_t* args, void* h, void* saved, void* 
     if (sms == 0) return GDN_ERR_CUDA;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const GluOperands o = glu_operands(s, static_cast<unsigned char*>(workspace));
-    if (!glu_align_all(s, o, st)) return GDN_ERR_CUDA;
+    if (!glu_align(s, o, sms, st)) return GDN_ERR_CUDA;
     const int32_t ksteps = (int32_t)ceil_div(D, gdn::kGluK);
     if (R <= kGluFewRows) {
         gdn::GluFewArgs a{};
@@ -223,7 +231,7 @@ gdn_status_t gdn_glu_forward(const gdn_glu_t* args, void* h, void* saved, void* 
     maps.a[1] = maps.a[0];
     gdn::GluGemmArgs a{};
     a.M = R; a.N = F; a.ksteps = ksteps; a.parts = 1; a.problems = 1; a.splits = 1;
-    a.out[0] = h; a.vec = F % 8 == 0 && aligned(h, 16);
+    a.out[0] = h;
     a.saved = static_cast<uint16_t*>(saved); a.act = s.act; a.status = status;
     return glu_gemm<gdn::kGluFwd>(maps, a, sms, st);
 }
@@ -269,14 +277,14 @@ gdn_status_t gdn_glu_backward(const gdn_glu_t* args, const void* dh, int64_t dh_
     bf16 *dg = reinterpret_cast<bf16*>(base), *du = reinterpret_cast<bf16*>(base + p.copies / 2);
     float* part = reinterpret_cast<float*>(base + p.part);
     const GluOperands o = glu_operands(s, base + p.copies);
-    if (!glu_align_all(s, o, st)) return GDN_ERR_CUDA;
+    if (!glu_align(s, o, sms, st)) return GDN_ERR_CUDA;
 
-    const bool v8 = F % 8 == 0 && wide(dh, dh_stride, F, s.in_dtype);
-    const unsigned blocks = (unsigned)std::min<int64_t>(ceil_div(R * ceil_div(F, v8 ? 8 : 1), 256), (int64_t)sms * 32);
-    const bf16* g = static_cast<const bf16*>(dh);
-    const uint16_t* sv = static_cast<const uint16_t*>(saved);
-    if (v8) gdn::k_glu_grad<8><<<blocks, 256, 0, st>>>(g, dh_stride, sv, R, F, s.act, dg, du, p.ld);
-    else gdn::k_glu_grad<1><<<blocks, 256, 0, st>>>(g, dh_stride, sv, R, F, s.act, dg, du, p.ld);
+    const unsigned blocks = (unsigned)std::min<int64_t>(ceil_div(R * (p.ld / 8), 256), (int64_t)sms * 32);
+    const uint16_t *g = static_cast<const uint16_t*>(dh), *sv = static_cast<const uint16_t*>(saved);
+    if (F % 8 == 0 && wide(dh, dh_stride, F, s.in_dtype))
+        gdn::k_glu_grad<true><<<blocks, 256, 0, st>>>(g, dh_stride, sv, R, F, s.act, dg, du, p.ld);
+    else
+        gdn::k_glu_grad<false><<<blocks, 256, 0, st>>>(g, dh_stride, sv, R, F, s.act, dg, du, p.ld);
     if (!launched()) return GDN_ERR_CUDA;
 
     gdn::GluMaps mx, mw;
@@ -288,13 +296,13 @@ gdn_status_t gdn_glu_backward(const gdn_glu_t* args, const void* dh, int64_t dh_
     mw.b[1] = mw.b[0];
     gdn::GluGemmArgs a{};
     a.M = R; a.N = D; a.ksteps = (int32_t)ceil_div(F, gdn::kGluK); a.parts = 2; a.problems = 1; a.splits = p.splits_x;
-    a.out[0] = dx; a.vec = D % 8 == 0 && aligned(dx, 16); a.partial = part; a.status = status;
+    a.out[0] = dx; a.partial = part; a.status = status;
     gdn_status_t r = glu_gemm<gdn::kGluDx>(mx, a, sms, st);
     if (r != GDN_OK) return r;
     if (p.splits_x > 1 && !glu_join<bf16>(part, p.splits_x, R * D, dx, nullptr, 1, st)) return GDN_ERR_CUDA;
     a.M = F; a.N = D; a.ksteps = (int32_t)ceil_div(R, gdn::kGluK); a.parts = 1; a.problems = 2; a.splits = p.splits_w;
     a.out[0] = dw_gate; a.out[1] = dw_up; a.out_f32 = dw_dtype == GDN_F32;
-    a.vec = D % (16 / (int)ws) == 0 && aligned(dw_gate, 16) && aligned(dw_up, 16);
+    a.vec = D % 4 == 0 && aligned(dw_gate, 16) && aligned(dw_up, 16);
     r = glu_gemm<gdn::kGluDw>(mw, a, sms, st);
     if (r != GDN_OK) return r;
     if (p.splits_w > 1) {

@@ -179,7 +179,7 @@ struct GluGemmArgs {
     int32_t tiles_m, tiles_n, problems, splits;
     int64_t tiles;       // tiles_m tiles_n problems splits
     void* out[2];
-    int32_t vec;         // rows of the outputs start at 16-byte boundaries
+    int32_t vec;         // fp32 rows start at 16-byte boundaries
     uint16_t* saved;     // forward: planes [3][M][N], or null
     float* partial;      // splits > 1: [problems][splits][M][N]
     int32_t act, out_f32;
@@ -217,26 +217,66 @@ __device__ __forceinline__ GluTile glu_tile(const GluGemmArgs& a, int64_t id)
     return t;
 }
 
-// 16 values of a row as bf16, or fp32, from column c of a row of n
-template <typename OT>
-__device__ __forceinline__ void glu_store16(OT* row, const float (&x)[16], int64_t c, int64_t n, bool vec)
-{
-    constexpr int V = 16 / (int)sizeof(OT);
-    if (vec && c + 16 <= n) {
+// A thread's part of a row of n 2-byte elements, written eight at a time from column c0 (a multiple of 8) on.  Rows of
+// odd widths start anywhere: the thread then stores the 16 bytes of memory that begin in one eight and end in the next, and
+// its first and last bytes one by one (333 x 1003 x 2777: 30 us element by element, 13 so).
+struct GluRow {
+    uint16_t* row;
+    int64_t n;
+    int s;      // bytes from a 16-byte boundary to the row's eights
+    bool open;  // `prev`, the eight before column `next`, has been written only in part
+    int64_t next;
+    uint4 prev;
+    __device__ __forceinline__ GluRow(void* base, int64_t at, int64_t n, int64_t c0)
+        : row(static_cast<uint16_t*>(base) + at), n(n), s((int)(reinterpret_cast<uintptr_t>(row + c0) & 15)), open(false), next(0) {}
+    __device__ __forceinline__ void ones(const uint4& v, int64_t c, int from, int to)
+    {
+        const uint16_t* e = reinterpret_cast<const uint16_t*>(&v);
 #pragma unroll
-        for (int i = 0; i < 16; i += V) store_vec<OT, V>(row + c + i, x + i);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (c + i < n) row[c + i] = from_f<OT>(x[i]);
+        for (int k = 0; k < 8; ++k)
+            if (k >= from && k < to) row[c + k] = e[k];
     }
-}
-__device__ __forceinline__ void glu_save16(uint16_t* row, const uint16_t (&x)[16], int64_t c, int64_t n, bool vec)
+    __device__ __forceinline__ void put(const uint4& v, int64_t c)
+    {
+        if (c + 8 > n) {
+            close();
+            ones(v, c, 0, (int)(n - c));
+        } else if (s == 0) {
+            *reinterpret_cast<uint4*>(row + c) = v;
+        } else {
+            if (open) *reinterpret_cast<uint4*>(row + c - s / 2) = bytes_at(prev, v, 16 - s);
+            else ones(v, c, 0, 8 - s / 2);
+            open = true;
+            next = c + 8;
+            prev = v;
+        }
+    }
+    __device__ __forceinline__ void close()
+    {
+        if (open) ones(prev, next - 8, 8 - s / 2, 8);
+        open = false;
+    }
+    __device__ __forceinline__ void put16(const float (&x)[16], int64_t c)
+    {
+        uint4 v[2];
+        uint32_t* u = reinterpret_cast<uint32_t*>(v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = bf16_pair(x[2 * i], x[2 * i + 1]);
+        put(v[0], c);
+        if (c + 8 < n) put(v[1], c + 8);
+    }
+    __device__ __forceinline__ void put16(const uint16_t (&x)[16], int64_t c)
+    {
+        const uint4* v = reinterpret_cast<const uint4*>(x);
+        put(v[0], c);
+        if (c + 8 < n) put(v[1], c + 8);
+    }
+};
+__device__ __forceinline__ void glu_store16(float* row, const float (&x)[16], int64_t c, int64_t n, bool vec)
 {
     if (vec && c + 16 <= n) {
-        const uint4* v = reinterpret_cast<const uint4*>(x);
-        *reinterpret_cast<uint4*>(row + c) = v[0];
-        *reinterpret_cast<uint4*>(row + c + 8) = v[1];
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) store_vec<float, 4>(row + c + i, x + i);
     } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
@@ -358,42 +398,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGluThreads, 1)
             const int64_t row = t.m + r0;
             const bool on = row < a.M;
             if constexpr (MODE == kGluFwd) {
-                __nv_bfloat16* h = static_cast<__nv_bfloat16*>(a.out[0]) + row * a.N;
-                for (int c = 0; c < 128; c += 16) {
-                    float g[16], u[16];
-                    tmem_ld16(col + c, g);
-                    tmem_ld16(col + 128 + c, u);
-                    tmem_wait_ld();
-                    if (on && t.n + c < a.N) {
-                        if (a.saved != nullptr) {
-                            alignas(16) uint16_t gh[16], uh[16], low[16];
+                const int64_t plane = a.M * a.N, at = row * a.N;
+                GluRow h(a.out[0], at, a.N, t.n);
+                if (a.saved != nullptr) {
+                    GluRow gh(a.saved, at, a.N, t.n), uh(a.saved, plane + at, a.N, t.n), low(a.saved, 2 * plane + at, a.N, t.n);
+                    for (int c = 0; c < 128; c += 16) {
+                        float g[16], u[16];
+                        tmem_ld16(col + c, g);
+                        tmem_ld16(col + 128 + c, u);
+                        tmem_wait_ld();
+                        if (on && t.n + c < a.N) {
+                            alignas(16) uint16_t x[16], y[16], z[16];
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) glu_pack(g[i], u[i], gh[i], uh[i], low[i]);
-                            glu_save16(a.saved + row * a.N, gh, t.n + c, a.N, a.vec);
-                            glu_save16(a.saved + (a.M + row) * a.N, uh, t.n + c, a.N, a.vec);
-                            glu_save16(a.saved + (2 * a.M + row) * a.N, low, t.n + c, a.N, a.vec);
+                            for (int i = 0; i < 16; ++i) glu_pack(g[i], u[i], x[i], y[i], z[i]);
+                            gh.put16(x, t.n + c);
+                            uh.put16(y, t.n + c);
+                            low.put16(z, t.n + c);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) g[i] = glu_act(g[i], a.act) * u[i];
+                            h.put16(g, t.n + c);
                         }
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) g[i] = glu_act(g[i], a.act) * u[i];
-                        glu_store16(h, g, t.n + c, a.N, a.vec);
+                        __syncwarp();  // the next read of tensor memory is the whole warp's
                     }
-                    __syncwarp();  // the next read of tensor memory is the whole warp's
+                    gh.close();
+                    uh.close();
+                    low.close();
+                } else {
+                    for (int c = 0; c < 128; c += 16) {
+                        float g[16], u[16];
+                        tmem_ld16(col + c, g);
+                        tmem_ld16(col + 128 + c, u);
+                        tmem_wait_ld();
+                        if (on && t.n + c < a.N) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) g[i] = glu_act(g[i], a.act) * u[i];
+                            h.put16(g, t.n + c);
+                        }
+                        __syncwarp();
+                    }
                 }
+                h.close();
             } else {
                 const int64_t at = row * a.N;
                 void* out = t.problem ? a.out[1] : a.out[0];
                 float* part = a.partial + ((int64_t)t.problem * a.splits + t.split) * a.M * a.N + at;
+                GluRow to(out, at, a.N, t.n);
+                const bool whole = a.splits == 1 && !a.out_f32;
                 for (int c = 0; c < 256; c += 16) {
                     float x[16];
                     tmem_ld16(col + c, x);
                     tmem_wait_ld();
                     if (on && t.n + c < a.N) {
-                        if (a.splits > 1) glu_store16(part, x, t.n + c, a.N, a.N % 4 == 0);
-                        else if (a.out_f32) glu_store16(static_cast<float*>(out) + at, x, t.n + c, a.N, a.vec);
-                        else glu_store16(static_cast<__nv_bfloat16*>(out) + at, x, t.n + c, a.N, a.vec);
+                        if (whole) to.put16(x, t.n + c);
+                        else if (a.splits > 1) glu_store16(part, x, t.n + c, a.N, a.N % 4 == 0);
+                        else glu_store16(static_cast<float*>(out) + at, x, t.n + c, a.N, a.vec);
                     }
                     __syncwarp();
                 }
+                to.close();
             }
             tc_fence_before();
             __syncwarp();
@@ -577,45 +639,75 @@ __global__ void __launch_bounds__(kGluThreads, 1) k_glu_few(const __grid_constan
 }
 
 // ------------------------------------------------------------- elementwise parts
-// dg and du, rows ld apart, from dh and what the forward saved; columns from F to ld are not read by anyone.
-template <int V>
-__global__ void __launch_bounds__(256) k_glu_grad(const __nv_bfloat16* __restrict__ dh, int64_t lddh,
+// Eight 2-byte elements at p, of the tensor [base, end): two aligned accesses where they lie within it
+__device__ __forceinline__ uint4 glu_load8(const uint16_t* p, const uint16_t* base, const uint16_t* end, int64_t count)
+{
+    const int s = (int)(reinterpret_cast<uintptr_t>(p) & 15);
+    const uint16_t* q = p - s / 2;
+    if (s == 0 && count >= 8) return *reinterpret_cast<const uint4*>(p);
+    if (q >= base && q + 16 <= end) {
+        const uint4* v = reinterpret_cast<const uint4*>(q);
+        return s == 0 ? v[0] : bytes_at(v[0], v[1], s);
+    }
+    Vec<uint16_t, 8> v;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v.v[k] = k < count ? p[k] : (uint16_t)0;
+    return *reinterpret_cast<const uint4*>(&v);
+}
+
+// dg and du, rows ld (a multiple of 8) apart, from dh and what the forward saved; columns from F on are read by nobody.
+// WHOLE: every row of dh and of the planes is whole 16-byte vectors (121 us at 8192 x 8192, the copy rate; else 131).
+template <bool WHOLE>
+__global__ void __launch_bounds__(256) k_glu_grad(const uint16_t* __restrict__ dh, int64_t lddh,
                                                   const uint16_t* __restrict__ saved, int64_t T, int64_t F, int act,
                                                   __nv_bfloat16* __restrict__ dg, __nv_bfloat16* __restrict__ du, int64_t ld)
 {
-    const int64_t per = (F + V - 1) / V, n = T * per, plane = T * F;
+    const int64_t per = ld / 8, n = T * per, plane = T * F;
+    const uint16_t *dend = dh + (T - 1) * lddh + F, *send = saved + 3 * plane;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t t = i / per, c = (i - t * per) * V;
-        const Vec<__nv_bfloat16, V> d = load_vec<__nv_bfloat16, V>(dh + t * lddh + c);
+        const int64_t t = i / per, c = (i - t * per) * 8, left = F - c;
         const uint16_t* s = saved + t * F + c;
-        const Vec<uint16_t, V> gh = load_vec<uint16_t, V>(s), uh = load_vec<uint16_t, V>(s + plane),
-                               low = load_vec<uint16_t, V>(s + 2 * plane);
-        float x[V], y[V];
+        auto load = [&](const uint16_t* p, const uint16_t* base, const uint16_t* end) {
+            return WHOLE ? *reinterpret_cast<const uint4*>(p) : glu_load8(p, base, end, left);
+        };
+        const uint4 d4 = load(dh + t * lddh + c, dh, dend), g4 = load(s, saved, send), u4 = load(s + plane, saved, send),
+                    l4 = load(s + 2 * plane, saved, send);
+        const __nv_bfloat16* d = reinterpret_cast<const __nv_bfloat16*>(&d4);
+        const uint16_t *gh = reinterpret_cast<const uint16_t*>(&g4), *uh = reinterpret_cast<const uint16_t*>(&u4),
+                       *low = reinterpret_cast<const uint16_t*>(&l4);
+        float x[8], y[8];
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
+        for (int k = 0; k < 8; ++k) {
             float g, u, f, slope;
-            glu_unpack(gh.v[k], uh.v[k], low.v[k], g, u);
+            glu_unpack(gh[k], uh[k], low[k], g, u);
             glu_act2(g, act, f, slope);
-            const float e = to_f<__nv_bfloat16>(d.v[k]);
+            const float e = to_f<__nv_bfloat16>(d[k]);
             x[k] = e * u * slope;
             y[k] = e * f;
         }
-        store_vec<__nv_bfloat16, V>(dg + t * ld + c, x);
-        store_vec<__nv_bfloat16, V>(du + t * ld + c, y);
+        store_vec<__nv_bfloat16, 8>(dg + t * ld + c, x);
+        store_vec<__nv_bfloat16, 8>(du + t * ld + c, y);
     }
 }
 
-// A matrix whose rows are not whole 16 bytes, into rows that are (ldd: a multiple of 8).
-__global__ void __launch_bounds__(256) k_glu_align(const uint16_t* __restrict__ src, int64_t lds, int64_t rows, int64_t cols,
-                                                   uint16_t* __restrict__ dst, int64_t ldd)
+// Matrices whose rows are not whole 16 bytes, into rows that are (ldd: a multiple of 8); one by blockIdx.y.
+struct GluAlign {
+    const uint16_t* src[3];
+    uint16_t* dst[3];
+    int64_t lds[3], rows[3];
+    int64_t cols, ldd;
+};
+__global__ void __launch_bounds__(256) k_glu_align(const GluAlign a)
 {
-    const int64_t per = ldd / 8, n = rows * per;
+    const int m = blockIdx.y;
+    const uint16_t* src = m == 0 ? a.src[0] : m == 1 ? a.src[1] : a.src[2];
+    uint16_t* dst = m == 0 ? a.dst[0] : m == 1 ? a.dst[1] : a.dst[2];
+    const int64_t lds = m == 0 ? a.lds[0] : m == 1 ? a.lds[1] : a.lds[2], rows = m == 0 ? a.rows[0] : m == 1 ? a.rows[1] : a.rows[2];
+    const int64_t per = a.ldd / 8, n = rows * per;
+    const uint16_t* end = src + (rows - 1) * lds + a.cols;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         const int64_t r = i / per, c = (i - r * per) * 8;
-        Vec<uint16_t, 8> v;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v.v[k] = c + k < cols ? src[r * lds + c + k] : (uint16_t)0;
-        *reinterpret_cast<Vec<uint16_t, 8>*>(dst + r * ldd + c) = v;
+        *reinterpret_cast<uint4*>(dst + r * a.ldd + c) = glu_load8(src + r * lds + c, src, end, a.cols - c);
     }
 }
 

@@ -47,20 +47,6 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t n
                  : "memory");
 }
 
-// The 16 bytes that start s bytes into the 32 bytes a, b (s below 16, the same for the whole block).
-__device__ __forceinline__ uint4 bytes_at(const uint4& a, const uint4& b, int s)
-{
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    uint32_t t[6], v[5];
-#pragma unroll
-    for (int i = 0; i < 6; ++i) t[i] = s & 8 ? w[i + 2] : w[i];
-#pragma unroll
-    for (int i = 0; i < 5; ++i) v[i] = s & 4 ? t[i + 1] : t[i];
-    const int sh = (s & 3) * 8;
-    return make_uint4(__funnelshift_r(v[0], v[1], sh), __funnelshift_r(v[1], v[2], sh),
-                      __funnelshift_r(v[2], v[3], sh), __funnelshift_r(v[3], v[4], sh));
-}
-
 // maxima of -inf (nothing yet, or nothing but -inf) count as 0 where they are taken off an exponent
 __device__ __forceinline__ float policy_base(float m) { return m == -INFINITY ? 0.0f : m; }
 

@@ -325,6 +325,20 @@ __device__ __forceinline__ float softplus(float v)
     return __fmaf_rn(p, e, fmaxf(v, 0.0f));
 }
 
+// The 16 bytes that start s bytes into the 32 bytes a, b (s below 16).
+__device__ __forceinline__ uint4 bytes_at(const uint4& a, const uint4& b, int s)
+{
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t t[6], v[5];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) t[i] = s & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) v[i] = s & 4 ? t[i + 1] : t[i];
+    const int sh = (s & 3) * 8;
+    return make_uint4(__funnelshift_r(v[0], v[1], sh), __funnelshift_r(v[1], v[2], sh),
+                      __funnelshift_r(v[2], v[3], sh), __funnelshift_r(v[3], v[4], sh));
+}
+
 // Column sums out[map(m)] = sum_r in[r][m], r < R, m < M, in a fixed order: 8
 // row slices per block, each summed in ascending rows, then joined in order.
 // OutMap: m -> pointer to write (may be nullptr: not wanted).

@@ -107,6 +107,27 @@ def test_views(T, shift):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("T", [5, 300])
+@pytest.mark.parametrize("D,F", [(64, 136), (72, 264), (250, 131)])
+def test_outputs_at_odd_addresses_get_the_same(T, D, F):
+    """Outputs need the alignment of one element; what lies around them stays as it is."""
+    c = case(T, D, F)
+
+    def odd(*shape):
+        n = int(np.prod(shape))
+        b = torch.full((n + 24,), 7.0, dtype=BF, device="cuda")
+        return b, b[11:11 + n].view(shape)
+
+    h, saved = gdn.gdn_glu_forward(c["x"][0], c["wg"][0], c["wu"][0], save=True)
+    one = gdn.gdn_glu_backward(c["x"][0], c["wg"][0], c["wu"][0], c["dh"][0], saved)
+    bh, vh = odd(T, F)
+    gdn.gdn_glu_forward(c["x"][0], c["wg"][0], c["wu"][0], h=vh)
+    buffers = [odd(*g.shape) for g in one]
+    gdn.gdn_glu_backward(c["x"][0], c["wg"][0], c["wu"][0], c["dh"][0], saved, grads=tuple(v for _, v in buffers))
+    for (b, v), want in zip([(bh, vh)] + buffers, (h,) + tuple(one)):
+        assert torch.equal(v, want) and (b[:11] == 7).all() and (b[11 + v.numel():] == 7).all()
+
+
 @pytest.mark.parametrize("T", [7, 400])
 def test_weight_gradients_in_fp32(T):
     c = case(T, 200, 72)
