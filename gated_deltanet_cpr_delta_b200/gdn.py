@@ -820,6 +820,15 @@ def gdn_layer_norm_backward(x, weight, dy, mean, rstd, *, workspace=None, grads=
     return grads
 
 
+def _heads(what: str, name: str, t: torch.Tensor, dtype: torch.dtype, shape, dev: int):
+    """As _rows, for [tokens, heads, head_dim]; the usual views of a projection without a walk over the strides."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        a, b, c = t.stride()
+        if c == 1 and b == shape[2] and a >= b * shape[1] and shape[0] > 1:
+            return t.data_ptr(), a
+    return _rows(what, name, t, dtype, shape, dev)
+
+
 def _qk_struct(what, q, k, q_weight, k_weight, positions, inv_freq, interleaved, l2, eps, dev):
     if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
         raise ValueError(f"{what}: q must be [tokens, q_heads, head_dim] and k [tokens, k_heads, head_dim]")
@@ -830,8 +839,8 @@ def _qk_struct(what, q, k, q_weight, k_weight, positions, inv_freq, interleaved,
     weight = q_weight if q_weight is not None else k_weight
     wt = ty if weight is None else weight.dtype
     ti = _type(what, q)
-    pq, lq = _rows(what, "q", q, ty, (T, Hq, d), dev)
-    pk, lk = _rows(what, "k", k, ty, (T, Hk, d), dev)
+    pq, lq = _heads(what, "q", q, ty, (T, Hq, d), dev)
+    pk, lk = _heads(what, "k", k, ty, (T, Hk, d), dev)
     rot, pp, pf = 0, None, None
     if positions is not None:
         if inv_freq.dim() != 1:
@@ -856,8 +865,11 @@ def gdn_qk_norm_forward(q, k, *, q_weight=None, k_weight=None, positions=None, i
     what = "gdn_qk_norm_forward"
     dev = _gpu(what, q)
     s = _qk_struct(what, q, k, q_weight, k_weight, positions, inv_freq, interleaved, l2, eps, dev)
-    q_out, pq = _out(what, "q_out", q_out, q.dtype, q.shape, dev, q)
-    k_out, pk = _out(what, "k_out", k_out, q.dtype, k.shape, dev, k)
+    if q_out is None:
+        q_out = q.new_empty(q.shape)
+    if k_out is None:
+        k_out = k.new_empty(k.shape)
+    pq, pk = _dense(what, "q_out", q_out, q.dtype, q.shape, dev), _dense(what, "k_out", k_out, q.dtype, k.shape, dev)
     _call(dev, what, load_library().gdn_qk_norm_forward, s, pq, pk)
     return q_out, k_out
 
@@ -873,12 +885,17 @@ def gdn_qk_norm_backward(q, k, dq_out, dk_out, *, q_weight=None, k_weight=None, 
     dev = _gpu(what, q)
     s = _qk_struct(what, q, k, q_weight, k_weight, positions, inv_freq, interleaved, l2, eps, dev)
     T, d, ty = s.tokens, s.head_dim, q.dtype
-    pgq, lgq = _rows(what, "dq_out", dq_out, ty, q.shape, dev)
-    pgk, lgk = _rows(what, "dk_out", dk_out, ty, k.shape, dev)
+    pgq, lgq = _heads(what, "dq_out", dq_out, ty, q.shape, dev)
+    pgk, lgk = _heads(what, "dk_out", dk_out, ty, k.shape, dev)
     if grads is None:
-        grads = (torch.empty(q.shape, dtype=ty, device=dev), torch.empty(k.shape, dtype=ty, device=dev),
-                 None if q_weight is None else torch.empty((d,), dtype=_F32, device=dev),
-                 None if k_weight is None else torch.empty((d,), dtype=_F32, device=dev))
+        dqw = dkw = None
+        if q_weight is not None and k_weight is not None:
+            dqw, dkw = torch.empty((2, d), dtype=_F32, device=dev).unbind(0)
+        elif q_weight is not None:
+            dqw = torch.empty((d,), dtype=_F32, device=dev)
+        elif k_weight is not None:
+            dkw = torch.empty((d,), dtype=_F32, device=dev)
+        grads = (q.new_empty(q.shape), k.new_empty(k.shape), dqw, dkw)
     dq, dk, dqw, dkw = grads
     keep, ws, nbytes = None, None, 0
     if dqw is not None or dkw is not None:
@@ -930,7 +947,10 @@ def gdn_glu_forward(x, w_gate, w_up, *, act: str = "silu", save: bool = False, h
     dev = _gpu(what, x)
     s = _glu_struct(what, x, w_gate, w_up, act, dev)
     R, F = s.rows, s.inner
-    h, ph = _out(what, "h", h, x.dtype, x.shape[:-1] + (F,), dev)
+    shape = x.shape[:-1] + (F,)
+    if h is None:
+        h = x.new_empty(shape)
+    ph = _dense(what, "h", h, x.dtype, shape, dev)
     if saved is None and save:
         saved = torch.empty((6 * R * F,), dtype=torch.uint8, device=dev)
     lib = load_library()
@@ -953,7 +973,7 @@ def gdn_glu_backward(x, w_gate, w_up, dh, saved, *, act: str = "silu", workspace
         raise ValueError(f"{what}: dh must have shape {tuple(x.shape[:-1]) + (F,)}, not {tuple(dh.shape)}")
     pd, ld = _rows(what, "dh", _rows2d(what, "dh", dh), ty, (R, F), dev)
     if grads is None:
-        grads = tuple(torch.empty(n, dtype=ty, device=dev) for n in (x.shape, (F, D), (F, D)))
+        grads = tuple(x.new_empty(n) for n in (x.shape, (F, D), (F, D)))
     dx, dwg, dwu = grads
     wt = dwg.dtype
     lib = load_library()
