@@ -91,16 +91,17 @@ gdn_status_t glu_check(const gdn_glu_t* s, const int32_t* status)
     return GDN_OK;
 }
 
-template <int MODE>
+template <int MODE, bool SAVE = false, int ACT = gdn::kGluSilu>
 gdn_status_t glu_gemm(gdn::GluMaps& maps, gdn::GluGemmArgs& a, int sms, cudaStream_t st)
 {
     a.tiles_m = (int32_t)ceil_div(a.M, 256);
     a.tiles_n = (int32_t)ceil_div(a.N, MODE == gdn::kGluFwd ? 128 : 256);
     a.tiles = (int64_t)a.tiles_m * a.tiles_n * a.problems * a.splits;
-    auto k = gdn::k_glu_gemm<MODE>;
-    if (!raise_smem(k, gdn::kGluSmem)) return GDN_ERR_CUDA;
+    auto k = gdn::k_glu_gemm<MODE, SAVE, ACT>;
+    constexpr size_t smem = gdn::glu_gemm_smem(SAVE);
+    if (!raise_smem(k, smem)) return GDN_ERR_CUDA;
     const unsigned pairs = (unsigned)std::min<int64_t>(a.tiles, std::max(1, sms / 2));
-    k<<<2 * pairs, gdn::kGluThreads, gdn::kGluSmem, st>>>(maps, a);
+    k<<<2 * pairs, gdn::kGluGemmThreads, smem, st>>>(maps, a);
     return launched() ? GDN_OK : GDN_ERR_CUDA;
 }
 
@@ -133,7 +134,7 @@ gdn_status_t glu_few(const GluOperands& o, const gdn_glu_t& s, gdn::GluFewArgs& 
     if (!matrix_map(&maps.x, o.x, s.rows, s.width, o.ldx, NB) || !matrix_map(&maps.wg, o.wg, s.inner, s.width, o.ldg, a.rows) ||
         !matrix_map(&maps.wu, o.wu, s.inner, s.width, o.ldu, a.rows))
         return GDN_ERR_CUDA;
-    auto k = gdn::k_glu_few<NB>;
+    auto k = s.act == GDN_ACT_SILU ? gdn::k_glu_few<NB, gdn::kGluSilu> : gdn::k_glu_few<NB, gdn::kGluGelu>;
     if (!raise_smem(k, smem)) return GDN_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)ceil_div(s.inner, a.rows) * S, (unsigned)ceil_div(s.rows, NB));
@@ -217,7 +218,7 @@ gdn_status_t gdn_glu_forward(const gdn_glu_t* args, void* h, void* saved, void* 
     const int32_t ksteps = (int32_t)ceil_div(D, gdn::kGluK);
     if (R <= kGluFewRows) {
         gdn::GluFewArgs a{};
-        a.T = (int32_t)R; a.F = s.inner; a.ksteps = ksteps; a.h = h; a.saved = static_cast<uint16_t*>(saved); a.act = s.act; a.status = status;
+        a.T = (int32_t)R; a.F = s.inner; a.ksteps = ksteps; a.h = h; a.saved = static_cast<uint16_t*>(saved); a.status = status;
         if (R <= 16) return glu_few<16>(o, s, a, sms, st);
         if (R <= 32) return glu_few<32>(o, s, a, sms, st);
         if (R <= 64) return glu_few<64>(o, s, a, sms, st);
@@ -232,8 +233,12 @@ gdn_status_t gdn_glu_forward(const gdn_glu_t* args, void* h, void* saved, void* 
     gdn::GluGemmArgs a{};
     a.M = R; a.N = F; a.ksteps = ksteps; a.parts = 1; a.problems = 1; a.splits = 1;
     a.out[0] = h;
-    a.saved = static_cast<uint16_t*>(saved); a.act = s.act; a.status = status;
-    return glu_gemm<gdn::kGluFwd>(maps, a, sms, st);
+    a.saved = static_cast<uint16_t*>(saved); a.status = status;
+    if (s.act == GDN_ACT_SILU)
+        return saved ? glu_gemm<gdn::kGluFwd, true, gdn::kGluSilu>(maps, a, sms, st)
+                     : glu_gemm<gdn::kGluFwd, false, gdn::kGluSilu>(maps, a, sms, st);
+    return saved ? glu_gemm<gdn::kGluFwd, true, gdn::kGluGelu>(maps, a, sms, st)
+                 : glu_gemm<gdn::kGluFwd, false, gdn::kGluGelu>(maps, a, sms, st);
 }
 
 size_t gdn_glu_backward_workspace_size(const gdn_glu_t* args)
@@ -281,10 +286,10 @@ gdn_status_t gdn_glu_backward(const gdn_glu_t* args, const void* dh, int64_t dh_
 
     const unsigned blocks = (unsigned)std::min<int64_t>(ceil_div(R * (p.ld / 8), 256), (int64_t)sms * 32);
     const uint16_t *g = static_cast<const uint16_t*>(dh), *sv = static_cast<const uint16_t*>(saved);
-    if (F % 8 == 0 && wide(dh, dh_stride, F, s.in_dtype))
-        gdn::k_glu_grad<true><<<blocks, 256, 0, st>>>(g, dh_stride, sv, R, F, s.act, dg, du, p.ld);
-    else
-        gdn::k_glu_grad<false><<<blocks, 256, 0, st>>>(g, dh_stride, sv, R, F, s.act, dg, du, p.ld);
+    const bool whole = F % 8 == 0 && wide(dh, dh_stride, F, s.in_dtype);
+    auto k = s.act == GDN_ACT_SILU ? (whole ? gdn::k_glu_grad<true, gdn::kGluSilu> : gdn::k_glu_grad<false, gdn::kGluSilu>)
+                                   : (whole ? gdn::k_glu_grad<true, gdn::kGluGelu> : gdn::k_glu_grad<false, gdn::kGluGelu>);
+    k<<<blocks, 256, 0, st>>>(g, dh_stride, sv, R, F, dg, du, p.ld);
     if (!launched()) return GDN_ERR_CUDA;
 
     gdn::GluMaps mx, mw;
@@ -302,7 +307,6 @@ gdn_status_t gdn_glu_backward(const gdn_glu_t* args, const void* dh, int64_t dh_
     if (p.splits_x > 1 && !glu_join<bf16>(part, p.splits_x, R * D, dx, nullptr, 1, st)) return GDN_ERR_CUDA;
     a.M = F; a.N = D; a.ksteps = (int32_t)ceil_div(R, gdn::kGluK); a.parts = 1; a.problems = 2; a.splits = p.splits_w;
     a.out[0] = dw_gate; a.out[1] = dw_up; a.out_f32 = dw_dtype == GDN_F32;
-    a.vec = D % 4 == 0 && aligned(dw_gate, 16) && aligned(dw_up, 16);
     r = glu_gemm<gdn::kGluDw>(mw, a, sms, st);
     if (r != GDN_OK) return r;
     if (p.splits_w > 1) {

@@ -8,7 +8,7 @@
 // k_glu_gemm is the product of all three: a pair of CTAs on neighbouring SMs makes a tile of 256 x 256
 // with tcgen05.mma.cta_group::2 (bf16 operands, fp32 accumulators in tensor memory), so that each SM fetches
 // half of either operand: 32 KB per 128 x 256 x 64 products, 64 bytes per cycle at the
-// tensor cores' rate.  TMA fills a ring of shared memory stages, one thread issues the products, and four
+// tensor cores' rate.  TMA fills a ring of shared memory stages, one thread issues the products, and eight
 // warps empty one accumulator (256 of 512 columns) while the next tile fills the other.
 //   forward   A = x, B = 128 rows of Wg (from the first CTA) and the same rows of Wu (from the second): a row of the
 //             accumulator holds g and u of the same 128 units, so act(g) u is made where it is read
@@ -31,23 +31,26 @@ constexpr int kGluSilu = 0, kGluGelu = 1;
 
 // ------------------------------------------------------------- the activation
 // act(g) and act'(g).  gelu: 0.5 g (1 + tanh t) = g sigmoid(2 t), 2 t = sqrt(8 / pi) (g + 0.044715 g^3)
-__device__ __forceinline__ float glu_act(float g, int act)
+// (ACT is a template's: a branch for each element would keep them from overlapping.)
+template <int ACT>
+__device__ __forceinline__ float glu_act(float g)
 {
-    if (act == kGluSilu) return silu(g);
+    if constexpr (ACT == kGluSilu) return silu(g);
     const float t = 1.5957691216057308f * __fmaf_rn(0.044715f * g * g, g, g);
     return g * sigmoid(t);
 }
-__device__ __forceinline__ void glu_act2(float g, int act, float& a, float& slope)
+template <int ACT>
+__device__ __forceinline__ void glu_act2(float g, float& a, float& slope)
 {
-    if (act == kGluSilu) {
+    if constexpr (ACT == kGluSilu) {
         const float s = sigmoid(g);
         a = g * s;
         slope = s * __fmaf_rn(g, 1.0f - s, 1.0f);
-        return;
+    } else {
+        const float g2 = g * g, s = sigmoid(1.5957691216057308f * __fmaf_rn(0.044715f * g2, g, g));
+        a = g * s;
+        slope = __fmaf_rn(a * (1.0f - s), 1.5957691216057308f * __fmaf_rn(0.134145f, g2, 1.0f), s);
     }
-    const float g2 = g * g, s = sigmoid(1.5957691216057308f * __fmaf_rn(0.044715f * g2, g, g));
-    a = g * s;
-    slope = __fmaf_rn(a * (1.0f - s), 1.5957691216057308f * __fmaf_rn(0.134145f, g2, 1.0f), s);
 }
 
 // What the backward reads of the forward: g and u to 24 bits (15 of mantissa), as planes of 16-bit words
@@ -179,10 +182,9 @@ struct GluGemmArgs {
     int32_t tiles_m, tiles_n, problems, splits;
     int64_t tiles;       // tiles_m tiles_n problems splits
     void* out[2];
-    int32_t vec;         // fp32 rows start at 16-byte boundaries
     uint16_t* saved;     // forward: planes [3][M][N], or null
     float* partial;      // splits > 1: [problems][splits][M][N]
-    int32_t act, out_f32;
+    int32_t out_f32;
     int32_t* status;
 };
 
@@ -191,10 +193,16 @@ struct GluTile {
     int problem, split, k0, k1;
 };
 
-constexpr int kGluStages = 6;
+constexpr int kGluStages = 6;                      // 5 where the forward saves: three more planes are staged
 constexpr uint32_t kGluOperand = 128 * kGluK * 2;  // bytes of one operand of one CTA in a stage
-constexpr int kGluThreads = 256;
-constexpr size_t kGluSmem = (size_t)kGluStages * 2 * kGluOperand + 1024 + 256;
+constexpr int kGluThreads = 256;                   // of k_glu_few
+constexpr int kGluOutWarps = 8, kGluGemmThreads = 128 + 32 * kGluOutWarps;
+__host__ __device__ constexpr int glu_stages(bool save) { return kGluStages - (save ? 1 : 0); }
+__host__ __device__ constexpr uint32_t glu_staging(bool save) { return kGluOutWarps * (save ? 4 : 1) * 2048; }
+__host__ __device__ constexpr size_t glu_gemm_smem(bool save)
+{
+    return (size_t)glu_stages(save) * 2 * kGluOperand + glu_staging(save) + 1024 + 256;
+}
 
 // Tiles in groups of 8 rows of tiles, down the rows first: what is on the chip at a time shares few rows and columns.
 template <int MODE>
@@ -217,83 +225,61 @@ __device__ __forceinline__ GluTile glu_tile(const GluGemmArgs& a, int64_t id)
     return t;
 }
 
-// A thread's part of a row of n 2-byte elements, written eight at a time from column c0 (a multiple of 8) on.  Rows of
-// odd widths start anywhere: the thread then stores the 16 bytes of memory that begin in one eight and end in the next, and
-// its first and last bytes one by one (333 x 1003 x 2777: 30 us element by element, 13 so).
-struct GluRow {
-    uint16_t* row;
-    int64_t n;
-    int s;      // bytes from a 16-byte boundary to the row's eights
-    bool open;  // `prev`, the eight before column `next`, has been written only in part
-    int64_t next;
-    uint4 prev;
-    __device__ __forceinline__ GluRow(void* base, int64_t at, int64_t n, int64_t c0)
-        : row(static_cast<uint16_t*>(base) + at), n(n), s((int)(reinterpret_cast<uintptr_t>(row + c0) & 15)), open(false), next(0) {}
-    __device__ __forceinline__ void ones(const uint4& v, int64_t c, int from, int to)
-    {
-        const uint16_t* e = reinterpret_cast<const uint16_t*>(&v);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (k >= from && k < to) row[c + k] = e[k];
-    }
-    __device__ __forceinline__ void put(const uint4& v, int64_t c)
-    {
-        if (c + 8 > n) {
-            close();
-            ones(v, c, 0, (int)(n - c));
-        } else if (s == 0) {
-            *reinterpret_cast<uint4*>(row + c) = v;
-        } else {
-            if (open) *reinterpret_cast<uint4*>(row + c - s / 2) = bytes_at(prev, v, 16 - s);
-            else ones(v, c, 0, 8 - s / 2);
-            open = true;
-            next = c + 8;
-            prev = v;
-        }
-    }
-    __device__ __forceinline__ void close()
-    {
-        if (open) ones(prev, next - 8, 8 - s / 2, 8);
-        open = false;
-    }
-    __device__ __forceinline__ void put16(const float (&x)[16], int64_t c)
-    {
-        uint4 v[2];
-        uint32_t* u = reinterpret_cast<uint32_t*>(v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] = bf16_pair(x[2 * i], x[2 * i + 1]);
-        put(v[0], c);
-        if (c + 8 < n) put(v[1], c + 8);
-    }
-    __device__ __forceinline__ void put16(const uint16_t (&x)[16], int64_t c)
-    {
-        const uint4* v = reinterpret_cast<const uint4*>(x);
-        put(v[0], c);
-        if (c + 8 < n) put(v[1], c + 8);
-    }
-};
-__device__ __forceinline__ void glu_store16(float* row, const float (&x)[16], int64_t c, int64_t n, bool vec)
+// A warp's 32 rows of 64 bytes on their way to memory, where a row lies across threads: each thread puts its row's 16-byte
+// pieces, then the warp stores whole rows of them, eight at a time.  Straight from the threads' rows every store would
+// touch 32 lines, which bound the products of few columns (20110 x 128 x 11712 with what the backward
+// reads: 1138 us).
+__device__ __forceinline__ uint4* glu_piece(unsigned char* st, int row, int piece)
 {
-    if (vec && c + 16 <= n) {
+    return reinterpret_cast<uint4*>(st + row * 64 + ((piece ^ (row >> 1)) & 3) * 16);  // no two of 8 threads in one bank
+}
+// `bytes` of the first `rows` rows to `to`, ld bytes apart.  Rows of odd widths start anywhere: 16 bytes of memory then begin in
+// one piece and end in the next, and of a row's 64 bytes the 16 at its ends go in twos.
+__device__ __forceinline__ void glu_rows_out(unsigned char* st, unsigned char* to, int64_t ld, int rows, int bytes, int lane)
+{
+    const uintptr_t any = reinterpret_cast<uintptr_t>(to) | (uintptr_t)ld | (uintptr_t)bytes;
+    if ((any & 15) == 0) {
 #pragma unroll
-        for (int i = 0; i < 16; i += 4) store_vec<float, 4>(row + c + i, x + i);
+        for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + (lane >> 2), p = lane & 3;
+            if (r < rows && p * 16 < bytes) *reinterpret_cast<uint4*>(to + r * ld + p * 16) = *glu_piece(st, r, p);
+        }
+    } else if (bytes == 64) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const int at = i * 32 + lane, r = at / 3, k = at - r * 3 + 1;
+            unsigned char* row = to + r * ld;
+            const int s = (int)(reinterpret_cast<uintptr_t>(row) & 15);
+            const uint4 v = *glu_piece(st, r, k);
+            if (r < rows) *reinterpret_cast<uint4*>(row + 16 * k - s) = s == 0 ? v : bytes_at(*glu_piece(st, r, k - 1), v, 16 - s);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (lane >> 3), j = lane & 7;
+            uint16_t* row = reinterpret_cast<uint16_t*>(to + r * ld);
+            const int s = (int)(reinterpret_cast<uintptr_t>(row) & 15), e = 2 * j < 16 - s ? j : 24 + j;
+            if (r < rows) row[e] = reinterpret_cast<const uint16_t*>(glu_piece(st, r, e >> 3))[e & 7];
+        }
     } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (c + i < n) row[c + i] = x[i];
+#pragma unroll 4
+        for (int r = 0; r < 32; ++r)
+            if (r < rows && lane * 2 < bytes)
+                *reinterpret_cast<uint16_t*>(to + r * ld + lane * 2) = reinterpret_cast<const uint16_t*>(glu_piece(st, r, lane >> 3))[lane & 7];
     }
 }
 
-template <int MODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGluThreads, 1)
+// SAVE: the forward leaves what the backward reads.
+template <int MODE, bool SAVE, int ACT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGluGemmThreads, 1)
     k_glu_gemm(const __grid_constant__ GluMaps maps, const GluGemmArgs a)
 {
     constexpr bool AK = MODE != kGluDw, BK = MODE == kGluFwd;  // which operands are K-major
-    constexpr int ST = kGluStages;
+    constexpr int ST = glu_stages(SAVE);
     constexpr uint32_t IDESC = bf16_idesc(256, 256, AK, BK);
     extern __shared__ unsigned char glu_smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(glu_smem_raw) + 1023) & ~(uintptr_t)1023);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + ST * 2 * kGluOperand);  // [ST] used in the first CTA
+    unsigned char* staging = smem + ST * 2 * kGluOperand;
+    uint64_t* full = reinterpret_cast<uint64_t*>(staging + glu_staging(SAVE));  // [ST] used in the first CTA
     uint64_t* empty = full + ST;      // [ST] one per CTA
     uint64_t* done = empty + ST;      // [2] the accumulators are complete
     uint64_t* drained = done + 2;     // [2] used in the first CTA: both CTAs have read an accumulator
@@ -307,7 +293,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGluThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(done + i, 1);
-            mbar_init(drained + i, 8);
+            mbar_init(drained + i, 2 * kGluOutWarps);
         }
     }
     if (warp == 2) {
@@ -386,76 +372,87 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGluThreads, 1)
             }
         }
     } else if (warp >= 4) {
-        // ---- both CTAs: accumulators to memory.  Thread: row 32 (warp % 4) + lane of this CTA's 128.
+        // ---- both CTAs: accumulators to memory.  A warp: 32 of this CTA's 128 rows, a thread each, and half of the columns.
         uint32_t acc = 0, ph = 0;
-        const int64_t r0 = (int64_t)rank * 128 + 32 * (warp - 4) + lane;
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
+        unsigned char* st = staging + (warp - 4) * (SAVE ? 4 : 1) * 2048;
         for (int64_t id = first; id < a.tiles; id += step) {
             const GluTile t = glu_tile<MODE>(a, id);
             ok = mbar_wait(done + acc, ph);
             if (!(ok = __all_sync(kFullMask, ok))) break;
             tc_fence_after();
-            const uint32_t col = tmem + ((uint32_t)(32 * (warp - 4)) << 16) + acc * 256;
-            const int64_t row = t.m + r0;
-            const bool on = row < a.M;
+            const uint32_t col = tmem + ((uint32_t)(32 * quarter) << 16) + acc * 256;
+            const int64_t row = t.m + (int64_t)rank * 128 + 32 * quarter;  // the warp's first
+            const int rows = (int)max((int64_t)0, min((int64_t)32, a.M - row));
+            // 64 bytes of the warp's rows, staged, to column c of an output of `esize`-byte elements
+            auto out = [&](unsigned char* from, void* to, int64_t c, int esize) {
+                glu_rows_out(from, static_cast<unsigned char*>(to) + (row * a.N + c) * esize, a.N * esize, rows,
+                             (int)min((int64_t)64, (a.N - c) * esize), lane);
+            };
             if constexpr (MODE == kGluFwd) {
-                const int64_t plane = a.M * a.N, at = row * a.N;
-                GluRow h(a.out[0], at, a.N, t.n);
-                if (a.saved != nullptr) {
-                    GluRow gh(a.saved, at, a.N, t.n), uh(a.saved, plane + at, a.N, t.n), low(a.saved, 2 * plane + at, a.N, t.n);
-                    for (int c = 0; c < 128; c += 16) {
+                for (int c0 = half * 64; c0 < half * 64 + 64 && t.n + c0 < a.N; c0 += 32) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 16) {
                         float g[16], u[16];
-                        tmem_ld16(col + c, g);
-                        tmem_ld16(col + 128 + c, u);
+                        tmem_ld16(col + c0 + i, g);
+                        tmem_ld16(col + 128 + c0 + i, u);
                         tmem_wait_ld();
-                        if (on && t.n + c < a.N) {
-                            alignas(16) uint16_t x[16], y[16], z[16];
+                        if constexpr (SAVE) {
+                            alignas(16) uint16_t x[3][16];
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) glu_pack(g[i], u[i], x[i], y[i], z[i]);
-                            gh.put16(x, t.n + c);
-                            uh.put16(y, t.n + c);
-                            low.put16(z, t.n + c);
+                            for (int k = 0; k < 16; ++k) glu_pack(g[k], u[k], x[0][k], x[1][k], x[2][k]);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) g[i] = glu_act(g[i], a.act) * u[i];
-                            h.put16(g, t.n + c);
+                            for (int p = 0; p < 3; ++p) {
+                                *glu_piece(st + (p + 1) * 2048, lane, i / 8) = reinterpret_cast<const uint4*>(x[p])[0];
+                                *glu_piece(st + (p + 1) * 2048, lane, i / 8 + 1) = reinterpret_cast<const uint4*>(x[p])[1];
+                            }
                         }
-                        __syncwarp();  // the next read of tensor memory is the whole warp's
-                    }
-                    gh.close();
-                    uh.close();
-                    low.close();
-                } else {
-                    for (int c = 0; c < 128; c += 16) {
-                        float g[16], u[16];
-                        tmem_ld16(col + c, g);
-                        tmem_ld16(col + 128 + c, u);
-                        tmem_wait_ld();
-                        if (on && t.n + c < a.N) {
+                        uint4 v[2];
+                        uint32_t* w = reinterpret_cast<uint32_t*>(v);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) g[i] = glu_act(g[i], a.act) * u[i];
-                            h.put16(g, t.n + c);
-                        }
-                        __syncwarp();
+                        for (int k = 0; k < 8; ++k)
+                            w[k] = bf16_pair(glu_act<ACT>(g[2 * k]) * u[2 * k], glu_act<ACT>(g[2 * k + 1]) * u[2 * k + 1]);
+                        *glu_piece(st, lane, i / 8) = v[0];
+                        *glu_piece(st, lane, i / 8 + 1) = v[1];
                     }
-                }
-                h.close();
-            } else {
-                const int64_t at = row * a.N;
-                void* out = t.problem ? a.out[1] : a.out[0];
-                float* part = a.partial + ((int64_t)t.problem * a.splits + t.split) * a.M * a.N + at;
-                GluRow to(out, at, a.N, t.n);
-                const bool whole = a.splits == 1 && !a.out_f32;
-                for (int c = 0; c < 256; c += 16) {
-                    float x[16];
-                    tmem_ld16(col + c, x);
-                    tmem_wait_ld();
-                    if (on && t.n + c < a.N) {
-                        if (whole) to.put16(x, t.n + c);
-                        else if (a.splits > 1) glu_store16(part, x, t.n + c, a.N, a.N % 4 == 0);
-                        else glu_store16(static_cast<float*>(out) + at, x, t.n + c, a.N, a.vec);
+                    __syncwarp();
+                    out(st, a.out[0], t.n + c0, 2);
+                    if constexpr (SAVE) {
+#pragma unroll
+                        for (int p = 0; p < 3; ++p) out(st + (p + 1) * 2048, a.saved + p * a.M * a.N, t.n + c0, 2);
                     }
                     __syncwarp();
                 }
-                to.close();
+            } else {
+                void* to = t.problem ? a.out[1] : a.out[0];
+                float* part = a.partial + ((int64_t)t.problem * a.splits + t.split) * a.M * a.N;
+                const bool narrow = a.splits == 1 && !a.out_f32;
+                for (int c0 = half * 128; c0 < half * 128 + 128 && t.n + c0 < a.N; c0 += 32) {
+                    float x[2][16];
+                    tmem_ld16(col + c0, x[0]);
+                    tmem_ld16(col + c0 + 16, x[1]);
+                    tmem_wait_ld();
+                    if (narrow) {
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) {
+                            const float* y = x[p >> 1] + (p & 1) * 8;
+                            *glu_piece(st, lane, p) = make_uint4(bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3]), bf16_pair(y[4], y[5]),
+                                                                 bf16_pair(y[6], y[7]));
+                        }
+                        __syncwarp();
+                        out(st, to, t.n + c0, 2);
+                        __syncwarp();
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                            for (int p = 0; p < 4; ++p) *glu_piece(st, lane, p) = reinterpret_cast<const uint4*>(x[i])[p];
+                            __syncwarp();
+                            if (t.n + c0 + 16 * i < a.N) out(st, a.splits > 1 ? static_cast<void*>(part) : to, t.n + c0 + 16 * i, 4);
+                            __syncwarp();
+                        }
+                    }
+                }
             }
             tc_fence_before();
             __syncwarp();
@@ -478,7 +475,6 @@ struct GluFewArgs {
     int32_t rows, stages, chunks;  // units of a block (a multiple of 8, at most 64); stages; 64 columns in each
     void* h;
     uint16_t* saved;
-    int32_t act;
     int32_t* status;
 };
 
@@ -496,7 +492,7 @@ __host__ __device__ inline uint32_t glu_few_tiles(int NB, int rows, int stages, 
     return tiles > results ? tiles : results;
 }
 
-template <int NB>
+template <int NB, int ACT>
 __global__ void __launch_bounds__(kGluThreads, 1) k_glu_few(const __grid_constant__ GluFewMaps maps, const GluFewArgs a)
 {
     constexpr uint32_t COLS = NB < 32 ? 32 : NB;
@@ -607,7 +603,7 @@ __global__ void __launch_bounds__(kGluThreads, 1) k_glu_few(const __grid_constan
         auto finish = [&](int t, float g, float u) {
             const int64_t at = (int64_t)(t0 + t) * a.F + f;
             if (a.saved != nullptr) glu_pack(g, u, a.saved[at], a.saved[plane + at], a.saved[2 * plane + at]);
-            static_cast<__nv_bfloat16*>(a.h)[at] = __float2bfloat16_rn(glu_act(g, a.act) * u);
+            static_cast<__nv_bfloat16*>(a.h)[at] = __float2bfloat16_rn(glu_act<ACT>(g) * u);
         };
         const int last = min(NB, a.T - t0), group = threadIdx.x >> 6;
         if (S == 1) {
@@ -657,9 +653,9 @@ __device__ __forceinline__ uint4 glu_load8(const uint16_t* p, const uint16_t* ba
 
 // dg and du, rows ld (a multiple of 8) apart, from dh and what the forward saved; columns from F on are read by nobody.
 // WHOLE: every row of dh and of the planes is whole 16-byte vectors (121 us at 8192 x 8192, the copy rate; else 131).
-template <bool WHOLE>
+template <bool WHOLE, int ACT>
 __global__ void __launch_bounds__(256) k_glu_grad(const uint16_t* __restrict__ dh, int64_t lddh,
-                                                  const uint16_t* __restrict__ saved, int64_t T, int64_t F, int act,
+                                                  const uint16_t* __restrict__ saved, int64_t T, int64_t F,
                                                   __nv_bfloat16* __restrict__ dg, __nv_bfloat16* __restrict__ du, int64_t ld)
 {
     const int64_t per = ld / 8, n = T * per, plane = T * F;
@@ -680,7 +676,7 @@ __global__ void __launch_bounds__(256) k_glu_grad(const uint16_t* __restrict__ d
         for (int k = 0; k < 8; ++k) {
             float g, u, f, slope;
             glu_unpack(gh[k], uh[k], low[k], g, u);
-            glu_act2(g, act, f, slope);
+            glu_act2<ACT>(g, f, slope);
             const float e = to_f<__nv_bfloat16>(d[k]);
             x[k] = e * u * slope;
             y[k] = e * f;
