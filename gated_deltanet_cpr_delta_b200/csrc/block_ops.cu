@@ -60,10 +60,17 @@ int qk_tokens(const gdn_qk_norm_t* s, int tpr, int blocks)
     return (int)std::max<int64_t>(1, ceil_div(s->tokens, rounds * blocks));
 }
 
-constexpr int kQkParts = 1024;  // most blocks of the backward
+constexpr int kQkParts = 1024;  // most blocks of the backward (fewer than SMs where they share tiles)
+
+// Blocks that share a tile's rows: where there are fewer tiles than SMs, as many as have two rows per thread.
+unsigned qk_shares(const gdn::QkArgs& a, int64_t tiles, int sms)
+{
+    const int64_t rows = (int64_t)a.tokens * std::max(a.H[0], a.H[1]), slots = gdn::kQkThreads / a.tpr;
+    return (unsigned)std::max<int64_t>(1, std::min<int64_t>(sms / std::max<int64_t>(1, tiles), rows / (2 * slots)));
+}
 
 template <typename T, bool VEC, bool INTER, bool BWD>
-gdn_status_t qk_launch(const gdn::QkArgs& a, unsigned blocks, cudaStream_t st)
+gdn_status_t qk_launch(const gdn::QkArgs& a, dim3 blocks, cudaStream_t st)
 {
     const size_t angles = a.rot > 0 ? sizeof(float) * 8 * (size_t)a.tokens * a.tpr : 0, weights = sizeof(float) * 16 * a.tpr;
     const size_t smem = std::max(angles + weights, BWD ? sizeof(float) * (gdn::kQkThreads / 32) * a.d : 0);
@@ -72,7 +79,7 @@ gdn_status_t qk_launch(const gdn::QkArgs& a, unsigned blocks, cudaStream_t st)
 }
 
 template <bool BWD>
-gdn_status_t qk_dispatch(const gdn::QkArgs& a, gdn_dtype_t t, bool vec, unsigned blocks, cudaStream_t st)
+gdn_status_t qk_dispatch(const gdn::QkArgs& a, gdn_dtype_t t, bool vec, dim3 blocks, cudaStream_t st)
 {
     const bool in = a.interleaved;
     if (t == GDN_BF16) {
@@ -178,7 +185,8 @@ gdn_status_t gdn_qk_norm_forward(const gdn_qk_norm_t* args, void* q_out, void* k
     if (sms == 0) return GDN_ERR_CUDA;
     gdn::QkArgs a = qk_args(args, sms * gdn::qk_resident(false));
     a.out[0] = q_out; a.out[1] = k_out;
-    const unsigned blocks = (unsigned)std::min<int64_t>(ceil_div(T, a.tokens), (int64_t)sms * gdn::qk_resident(false));
+    const int64_t tiles = ceil_div(T, a.tokens);
+    const dim3 blocks((unsigned)std::min<int64_t>(tiles, (int64_t)sms * gdn::qk_resident(false)), qk_shares(a, tiles, sms));
     const bool vec = qk_vectors(args, s.q, s.q_stride) && qk_vectors(args, s.k, s.k_stride) &&
                      qk_vectors(args, q_out, wq) && qk_vectors(args, k_out, wk);
     return qk_dispatch<false>(a, s.in_dtype, vec, blocks, static_cast<cudaStream_t>(stream));
@@ -187,7 +195,7 @@ gdn_status_t gdn_qk_norm_forward(const gdn_qk_norm_t* args, void* q_out, void* k
 size_t gdn_qk_norm_backward_workspace_size(int64_t tokens, int32_t head_dim)
 {
     if (tokens < 0 || head_dim <= 0) return 0;
-    return align_up(sizeof(float) * 2 * (size_t)std::max<int64_t>(1, std::min<int64_t>(tokens, kQkParts)) * head_dim);
+    return align_up(sizeof(float) * 2 * (size_t)kQkParts * head_dim);
 }
 
 gdn_status_t gdn_qk_norm_backward(const gdn_qk_norm_t* args, const void* dq_out, int64_t dq_out_stride, const void* dk_out,
@@ -223,11 +231,14 @@ gdn_status_t gdn_qk_norm_backward(const gdn_qk_norm_t* args, const void* dq_out,
         gdn::QkArgs a = qk_args(args, (int)std::min<int64_t>(kQkParts, (int64_t)sms * gdn::qk_resident(true)));
         a.dy[0] = dq_out; a.dy[1] = dk_out; a.lddy[0] = dq_out_stride; a.lddy[1] = dk_out_stride;
         a.out[0] = dq; a.out[1] = dk; a.part = part;
-        parts = std::min<int64_t>(ceil_div(T, a.tokens), std::min<int64_t>(kQkParts, (int64_t)sms * gdn::qk_resident(true)));
+        const int64_t tiles = ceil_div(T, a.tokens);
+        const dim3 blocks((unsigned)std::min<int64_t>(tiles, std::min<int64_t>(kQkParts, (int64_t)sms * gdn::qk_resident(true))),
+                          qk_shares(a, tiles, sms));
+        parts = (int64_t)blocks.x * blocks.y;
         const bool vec = qk_vectors(args, s.q, s.q_stride) && qk_vectors(args, s.k, s.k_stride) &&
                          qk_vectors(args, dq_out, dq_out_stride) && qk_vectors(args, dk_out, dk_out_stride) &&
                          qk_vectors(args, dq, wq) && qk_vectors(args, dk, wk);
-        const gdn_status_t r = qk_dispatch<true>(a, s.in_dtype, vec, (unsigned)parts, st);
+        const gdn_status_t r = qk_dispatch<true>(a, s.in_dtype, vec, blocks, st);
         if (r != GDN_OK) return r;
     }
     if (!weights) return GDN_OK;

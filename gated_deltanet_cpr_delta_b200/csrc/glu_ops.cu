@@ -105,7 +105,9 @@ gdn_status_t glu_gemm(gdn::GluMaps& maps, gdn::GluGemmArgs& a, int sms, cudaStre
     return launched() ? GDN_OK : GDN_ERR_CUDA;
 }
 
-constexpr int64_t kGluFewRows = 256;  // up to so many tokens the weights are streamed past them
+// Whether the weights are streamed past the tokens: up to 256 tokens, and where the pairs of SMs would have at most 16 tiles
+// (300 x 4096 x 1024 18 us, in tiles 27; 1024 x 2048 x 512 15 and 17; with 32 tiles, 1024 x 1024 x 1024, 17 and 13).
+bool glu_is_few(int64_t rows, int64_t inner) { return rows <= 256 || ceil_div(rows, 256) * ceil_div(inner, 128) <= 16; }
 
 // Parts of the K axis of a product with few tiles: enough for every pair of SMs, each of at least 8 stages.
 int glu_splits(int64_t tiles, int64_t ksteps, int sms)
@@ -121,7 +123,8 @@ template <int NB>
 gdn_status_t glu_few(const GluOperands& o, const gdn_glu_t& s, gdn::GluFewArgs& a, int sms, cudaStream_t st)
 {
     // a cluster's blocks lie in one group of SMs, of which a few are left over: a full house would come in two waves
-    const auto slots = [&](int S) { return S > 1 ? sms * 7 / 8 : sms; };
+    const int groups = (int)ceil_div(s.rows, NB);  // of tokens
+    const auto slots = [&](int S) { return std::max(1, (S > 1 ? sms * 7 / 8 : sms) / groups); };
     int S = 1;
     while (S < 4 && ceil_div((int64_t)s.inner * S * 2, slots(2)) <= 64 && a.ksteps >= 8 * S) S *= 2;
     const int resident = ceil_div((int64_t)s.inner * S, slots(S)) <= 64 ? 1 : 2;
@@ -216,7 +219,7 @@ gdn_status_t gdn_glu_forward(const gdn_glu_t* args, void* h, void* saved, void* 
     const GluOperands o = glu_operands(s, static_cast<unsigned char*>(workspace));
     if (!glu_align(s, o, sms, st)) return GDN_ERR_CUDA;
     const int32_t ksteps = (int32_t)ceil_div(D, gdn::kGluK);
-    if (R <= kGluFewRows) {
+    if (glu_is_few(R, F)) {
         gdn::GluFewArgs a{};
         a.T = (int32_t)R; a.F = s.inner; a.ksteps = ksteps; a.h = h; a.saved = static_cast<uint16_t*>(saved); a.status = status;
         if (R <= 16) return glu_few<16>(o, s, a, sms, st);

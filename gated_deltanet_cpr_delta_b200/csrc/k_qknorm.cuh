@@ -7,7 +7,7 @@
 // and, with g = the gradient turned back and h = g w:
 //     dx = r (h - x r sum(h x) r / n),  dw = sum_rows g x r
 //
-// One read of x (and dy), one write, q and k in one launch.  A row (one head of one token) lies in the
+// One read of x (and dy), one write, q and k in one launch; with few tokens several blocks share the heads of each.  A row (one head of one token) lies in the
 // registers of tpr neighbouring lanes, each with four pairs, so that a pair's two elements meet in one
 // thread and turn without an exchange.  A block takes `tokens` tokens at a time and
 // makes their angles once, for all heads, in shared memory: position times frequency in turns
@@ -177,15 +177,18 @@ __global__ void __launch_bounds__(kQkThreads, qk_resident(BWD)) k_qk_norm(const 
             f2x wa[2], wb[2];
             qk_four(ws + 2 * kind * span + pairs.first, wa);
             qk_four(ws + (2 * kind + 1) * span + pairs.first, wb);
-            const int H = a.H[kind], rows = nt * H, dt = slots / H, dh = slots - dt * H;
+            const int H = a.H[kind], all = nt * H, dt = slots / H, dh = slots - dt * H;
+            // this block's share of the tile's rows, in whole rounds of the slots
+            const int share = (int)(((int64_t)all + slots * gridDim.y - 1) / (slots * gridDim.y)) * slots;
+            const int begin = min(all, share * (int)blockIdx.y), rows = min(all, begin + share);
             const int64_t ldx = a.ldx[kind], ldg = BWD ? a.lddy[kind] : 0;
             // this thread's next row: its head, its angles, and where it lies; from there to the next one, `slots` rows
             // on, dt tokens and dh heads, or one token more and H heads less
-            const int tok0 = slot / H;
-            int h = slot - tok0 * H, at = tok0 * span + pairs.first;
+            const int tok0 = (begin + slot) / H;
+            int h = begin + slot - tok0 * H, at = tok0 * span + pairs.first;
             const T* px = static_cast<const T*>(a.x[kind]) + (t0 + tok0) * ldx + h * a.d;
             const T* pg = BWD ? static_cast<const T*>(a.dy[kind]) + (t0 + tok0) * ldg + h * a.d : nullptr;
-            T* po = static_cast<T*>(a.out[kind]) + (t0 * H + slot) * (int64_t)a.d;
+            T* po = static_cast<T*>(a.out[kind]) + (t0 * H + begin + slot) * (int64_t)a.d;
             const int64_t stepx = dt * ldx + dh * a.d, wrapx = ldx - (int64_t)H * a.d;
             const int64_t stepg = dt * ldg + dh * a.d, wrapg = ldg - (int64_t)H * a.d;
             const int64_t stepo = (int64_t)slots * a.d;
@@ -309,7 +312,7 @@ __global__ void __launch_bounds__(kQkThreads, qk_resident(BWD)) k_qk_norm(const 
                 po += U * stepo;
             };
             // the same turns for every thread: the sums are shuffles
-            int r0 = 0;
+            int r0 = begin;
             for (; r0 + slots * U <= rows; r0 += slots * U) some(std::integral_constant<int, U>{}, r0);
             for (; r0 < rows; r0 += slots) some(std::integral_constant<int, 1>{}, r0);
             if constexpr (BWD) {
@@ -327,7 +330,7 @@ __global__ void __launch_bounds__(kQkThreads, qk_resident(BWD)) k_qk_norm(const 
         if (a.part == nullptr) return;
         // dw: the rows of a warp by shuffles, then the warps in order
         float* red = cs;  // [8][d]
-        float* part = a.part + (int64_t)blockIdx.x * 2 * a.d;
+        float* part = a.part + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 2 * a.d;
 #pragma unroll
         for (int kind = 0; kind < 2; ++kind) {
             float x[4], y[4];
