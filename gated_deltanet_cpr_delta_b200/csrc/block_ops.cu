@@ -70,16 +70,21 @@ unsigned qk_shares(const gdn::QkArgs& a, int64_t tiles, int sms)
 }
 
 template <typename T, bool VEC, bool INTER, bool BWD>
-gdn_status_t qk_launch(const gdn::QkArgs& a, dim3 blocks, cudaStream_t st)
+gdn_status_t qk_launch(gdn::QkArgs& a, dim3 blocks, cudaStream_t st)
 {
     const size_t angles = a.rot > 0 ? sizeof(float) * 8 * (size_t)a.tokens * a.tpr : 0, weights = sizeof(float) * 16 * a.tpr;
-    const size_t smem = std::max(angles + weights, BWD ? sizeof(float) * (gdn::kQkThreads / 32) * a.d : 0);
-    gdn::k_qk_norm<T, VEC, INTER, BWD><<<blocks, gdn::kQkThreads, smem, st>>>(a);
+    const size_t own = (angles + weights + 127) / 128 * 128;
+    const size_t ring = VEC ? gdn::QkRing<T, gdn::qk_rows(BWD, sizeof(T)), BWD>::BYTES : 0;
+    const size_t smem = std::max(own + ring, BWD ? sizeof(float) * (gdn::kQkThreads / 32) * a.d : 0);
+    a.ring = (int32_t)own;
+    auto k = gdn::k_qk_norm<T, VEC, INTER, BWD>;
+    if (!raise_smem(k, smem)) return GDN_ERR_CUDA;
+    k<<<blocks, gdn::kQkThreads, smem, st>>>(a);
     return launched() ? GDN_OK : GDN_ERR_CUDA;
 }
 
 template <bool BWD>
-gdn_status_t qk_dispatch(const gdn::QkArgs& a, gdn_dtype_t t, bool vec, dim3 blocks, cudaStream_t st)
+gdn_status_t qk_dispatch(gdn::QkArgs& a, gdn_dtype_t t, bool vec, dim3 blocks, cudaStream_t st)
 {
     const bool in = a.interleaved;
     if (t == GDN_BF16) {
@@ -183,12 +188,13 @@ gdn_status_t gdn_qk_norm_forward(const gdn_qk_norm_t* args, void* q_out, void* k
         return GDN_ERR_INVALID_ARG;
     const int sms = sm_count();
     if (sms == 0) return GDN_ERR_CUDA;
-    gdn::QkArgs a = qk_args(args, sms * gdn::qk_resident(false));
-    a.out[0] = q_out; a.out[1] = k_out;
-    const int64_t tiles = ceil_div(T, a.tokens);
-    const dim3 blocks((unsigned)std::min<int64_t>(tiles, (int64_t)sms * gdn::qk_resident(false)), qk_shares(a, tiles, sms));
     const bool vec = qk_vectors(args, s.q, s.q_stride) && qk_vectors(args, s.k, s.k_stride) &&
                      qk_vectors(args, q_out, wq) && qk_vectors(args, k_out, wk);
+    const int most = sms * gdn::qk_resident(false, vec);
+    gdn::QkArgs a = qk_args(args, most);
+    a.out[0] = q_out; a.out[1] = k_out;
+    const int64_t tiles = ceil_div(T, a.tokens);
+    const dim3 blocks((unsigned)std::min<int64_t>(tiles, most), qk_shares(a, tiles, sms));
     return qk_dispatch<false>(a, s.in_dtype, vec, blocks, static_cast<cudaStream_t>(stream));
 }
 
@@ -228,11 +234,11 @@ gdn_status_t gdn_qk_norm_backward(const gdn_qk_norm_t* args, const void* dq_out,
     if (T > 0) {
         const int sms = sm_count();
         if (sms == 0) return GDN_ERR_CUDA;
-        gdn::QkArgs a = qk_args(args, (int)std::min<int64_t>(kQkParts, (int64_t)sms * gdn::qk_resident(true)));
+        gdn::QkArgs a = qk_args(args, (int)std::min<int64_t>(kQkParts, (int64_t)sms * gdn::qk_resident(true, true)));
         a.dy[0] = dq_out; a.dy[1] = dk_out; a.lddy[0] = dq_out_stride; a.lddy[1] = dk_out_stride;
         a.out[0] = dq; a.out[1] = dk; a.part = part;
         const int64_t tiles = ceil_div(T, a.tokens);
-        const dim3 blocks((unsigned)std::min<int64_t>(tiles, std::min<int64_t>(kQkParts, (int64_t)sms * gdn::qk_resident(true))),
+        const dim3 blocks((unsigned)std::min<int64_t>(tiles, std::min<int64_t>(kQkParts, (int64_t)sms * gdn::qk_resident(true, true))),
                           qk_shares(a, tiles, sms));
         parts = (int64_t)blocks.x * blocks.y;
         const bool vec = qk_vectors(args, s.q, s.q_stride) && qk_vectors(args, s.k, s.k_stride) &&

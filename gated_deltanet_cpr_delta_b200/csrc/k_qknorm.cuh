@@ -35,12 +35,13 @@ struct QkArgs {
     int64_t T;
     int32_t d, rot, tpr;
     int32_t tokens;     // per tile
+    int32_t ring;       // where the ring starts in shared memory
     float* part;        // backward: [grid][2][d] sums of dw, or null
 };
 
 constexpr int kQkThreads = 256;
 __host__ __device__ constexpr int qk_rows(bool bwd, int esize) { return bwd || esize == 4 ? 2 : 4; }  // rows of a thread in flight
-__host__ __device__ constexpr int qk_resident(bool bwd) { return bwd ? 2 : 3; }    // blocks per SM
+__host__ __device__ constexpr int qk_resident(bool bwd, bool vec) { return bwd || !vec ? 2 : 3; }  // blocks per SM
 
 // A thread's four neighbouring pairs of a row: the elements a(i) and b(i), i < 4.  INTER: (2 p, 2 p + 1), else
 // (p, p + R / 2), and behind the rotated ones any two that are left.
@@ -124,9 +125,34 @@ __device__ __forceinline__ void qk_four(const float* p, f2x (&v)[2])
     v[0] = pk2(f.x, f.y), v[1] = pk2(f.z, f.w);
 }
 
+// A thread's own pieces of the rows that it will work on next, in a ring in shared memory that cp.async fills, as
+// NormRing: the next rows are under way through the sums of these, without registers or barriers.
+constexpr int kQkAhead = 2;  // turns ahead
+template <typename T, int U, bool BWD>
+struct QkRing {
+    static constexpr int P = 4 * (int)sizeof(T), TENSORS = BWD ? 2 : 1;       // bytes of a piece
+    static constexpr size_t BYTES = (size_t)kQkAhead * U * TENSORS * 2 * P * kQkThreads;
+    unsigned char* base;
+    __device__ __forceinline__ unsigned char* at(int turn, int u, int tensor, int piece) const
+    {
+        return base + ((((turn * U + u) * TENSORS + tensor) * 2 + piece) * kQkThreads + threadIdx.x) * P;
+    }
+    __device__ __forceinline__ void copy(int turn, int u, int tensor, int piece, const T* src) const
+    {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((unsigned)__cvta_generic_to_shared(at(turn, u, tensor, piece))),
+                     "l"(src), "n"(P) : "memory");
+    }
+    template <typename ROW>
+    __device__ __forceinline__ void get(int turn, int u, int tensor, ROW& row) const
+    {
+        row.lo = *reinterpret_cast<const Vec<T, 4>*>(at(turn, u, tensor, 0));
+        row.hi = *reinterpret_cast<const Vec<T, 4>*>(at(turn, u, tensor, 1));
+    }
+};
+
 // BWD: the gradients.
 template <typename T, bool VEC, bool INTER, bool BWD>
-__global__ void __launch_bounds__(kQkThreads, qk_resident(BWD)) k_qk_norm(const QkArgs a)
+__global__ void __launch_bounds__(kQkThreads, qk_resident(BWD, VEC)) k_qk_norm(const QkArgs a)
 {
     constexpr int U = qk_rows(BWD, sizeof(T));
     using Row = QkRow<T, VEC, INTER>;
@@ -155,6 +181,88 @@ __global__ void __launch_bounds__(kQkThreads, qk_resident(BWD)) k_qk_norm(const 
     for (int i = 0; i < 2; ++i) da[i] = db[i] = oa[i] = ob[i] = pk2(0.0f, 0.0f);
 
     const int64_t tiles = (a.T + a.tokens - 1) / a.tokens;
+    // this block's share of a tile's rows, in whole rounds of the slots
+    auto share = [&](int all, int& begin, int& end) {
+        const int n = (int)(((int64_t)all + slots * gridDim.y - 1) / (slots * gridDim.y)) * slots;
+        begin = min(all, n * (int)blockIdx.y);
+        end = min(all, begin + n);
+    };
+    // Where the thread's next rows to fetch lie: from one to the next, `slots` rows on, dt tokens and dh heads, or one token
+    // more and H heads less.
+    struct {
+        int64_t tile, stepx, wrapx, stepg, wrapg;
+        const T *px, *pg;
+        int kind, r, end, h, H, dh;
+    } next{};
+    auto aim = [&] {  // at the first row of next.kind in next.tile
+        const int64_t t0 = next.tile * a.tokens;
+        const bool k = next.kind;  // (no indexed arguments: they would be copied to local memory)
+        const int H = k ? a.H[1] : a.H[0], dt = slots / H;
+        int begin;
+        share((int)min((int64_t)a.tokens, a.T - t0) * H, begin, next.end);
+        const int64_t ldx = k ? a.ldx[1] : a.ldx[0], ldg = BWD ? (k ? a.lddy[1] : a.lddy[0]) : 0;
+        const int tok = (begin + slot) / H;
+        next.H = H;
+        next.dh = slots - dt * H;
+        next.h = begin + slot - tok * H;
+        next.r = begin;
+        next.px = static_cast<const T*>(k ? a.x[1] : a.x[0]) + (t0 + tok) * ldx + next.h * a.d;
+        next.stepx = dt * ldx + next.dh * a.d, next.wrapx = ldx - (int64_t)H * a.d;
+        if constexpr (BWD) {
+            next.pg = static_cast<const T*>(k ? a.dy[1] : a.dy[0]) + (t0 + tok) * ldg + next.h * a.d;
+            next.stepg = dt * ldg + next.dh * a.d, next.wrapg = ldg - (int64_t)H * a.d;
+        }
+    };
+    auto advance = [&] {
+        next.px += next.stepx;
+        if constexpr (BWD) next.pg += next.stepg;
+        if (next.dh != 0) {
+            next.h += next.dh;
+            if (next.h >= next.H) {
+                next.h -= next.H;
+                next.px += next.wrapx;
+                if constexpr (BWD) next.pg += next.wrapg;
+            }
+        }
+    };
+    auto skip = [&] {  // over what has no rows (left)
+        while (next.tile < tiles && next.r >= next.end) {
+            if (next.kind) next.tile += gridDim.x;
+            next.kind ^= 1;
+            if (next.tile < tiles) aim();
+        }
+    };
+    const QkRing<T, U, BWD> ring{qk_smem + a.ring};
+    int turn = 0;  // of the ring
+    auto fetch = [&](int turn) {
+        if (next.tile < tiles) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (next.r + u * slots + slot < next.end) {
+                    ring.copy(turn, u, 0, 0, next.px + ea);
+                    ring.copy(turn, u, 0, 1, next.px + eb);
+                    if constexpr (BWD) {
+                        ring.copy(turn, u, 1, 0, next.pg + ea);
+                        ring.copy(turn, u, 1, 1, next.pg + eb);
+                    }
+                }
+                advance();
+            }
+            next.r += U * slots;
+            skip();
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    next.tile = blockIdx.x;
+    next.kind = 0;
+    if (next.tile < tiles) {
+        aim();
+        skip();
+    }
+    if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < kQkAhead; ++i) fetch(i);
+    }
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         const int64_t t0 = tile * a.tokens;
         const int nt = (int)min((int64_t)a.tokens, a.T - t0);
@@ -177,46 +285,40 @@ __global__ void __launch_bounds__(kQkThreads, qk_resident(BWD)) k_qk_norm(const 
             f2x wa[2], wb[2];
             qk_four(ws + 2 * kind * span + pairs.first, wa);
             qk_four(ws + (2 * kind + 1) * span + pairs.first, wb);
-            const int H = a.H[kind], all = nt * H, dt = slots / H, dh = slots - dt * H;
-            // this block's share of the tile's rows, in whole rounds of the slots
-            const int share = (int)(((int64_t)all + slots * gridDim.y - 1) / (slots * gridDim.y)) * slots;
-            const int begin = min(all, share * (int)blockIdx.y), rows = min(all, begin + share);
-            const int64_t ldx = a.ldx[kind], ldg = BWD ? a.lddy[kind] : 0;
-            // this thread's next row: its head, its angles, and where it lies; from there to the next one, `slots` rows
-            // on, dt tokens and dh heads, or one token more and H heads less
+            const int H = kind ? a.H[1] : a.H[0], dt = slots / H, dh = slots - dt * H;
+            int begin, rows;
+            share(nt * H, begin, rows);
             const int tok0 = (begin + slot) / H;
-            int h = begin + slot - tok0 * H, at = tok0 * span + pairs.first;
-            const T* px = static_cast<const T*>(a.x[kind]) + (t0 + tok0) * ldx + h * a.d;
-            const T* pg = BWD ? static_cast<const T*>(a.dy[kind]) + (t0 + tok0) * ldg + h * a.d : nullptr;
-            T* po = static_cast<T*>(a.out[kind]) + (t0 * H + begin + slot) * (int64_t)a.d;
-            const int64_t stepx = dt * ldx + dh * a.d, wrapx = ldx - (int64_t)H * a.d;
-            const int64_t stepg = dt * ldg + dh * a.d, wrapg = ldg - (int64_t)H * a.d;
+            int h = begin + slot - tok0 * H, at = tok0 * span + pairs.first;  // the head and the angles of this thread's next row
+            T* po = static_cast<T*>(kind ? a.out[1] : a.out[0]) + (t0 * H + begin + slot) * (int64_t)a.d;
             const int64_t stepo = (int64_t)slots * a.d;
-            auto some = [&](auto count, int r0) {  // so many rows of every thread; more than one: all of them are there
-                constexpr int U = decltype(count)::value;
-                constexpr bool WHOLE = U > 1;
+            auto some = [&](auto all, int r0) {  // U rows of every thread; WHOLE: all of them are there
+                constexpr bool WHOLE = decltype(all)::value;
                 Row x[U];
                 [[maybe_unused]] Row g[BWD ? U : 1];
                 int ang[U];
                 bool on[U];
+                if constexpr (VEC) asm volatile("cp.async.wait_group %0;" ::"n"(kQkAhead - 1) : "memory");
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    on[u] = WHOLE || r0 + slot < rows;
+                    on[u] = WHOLE || r0 + u * slots + slot < rows;
                     ang[u] = at;
-                    if (on[u]) {
-                        x[u].load(px, pairs, ea, eb);
-                        if constexpr (BWD) g[u].load(pg, pairs, ea, eb);
+                    if constexpr (!VEC) {
+                        if (on[u]) {
+                            x[u].load(next.px, pairs, ea, eb);
+                            if constexpr (BWD) g[u].load(next.pg, pairs, ea, eb);
+                        }
+                        advance();
                     }
-                    px += stepx;
-                    if constexpr (BWD) pg += stepg;
                     at += dt * span;
-                    h += dh;
-                    if (dh != 0 && h >= H) {
-                        h -= H;
-                        at += span;
-                        px += wrapx;
-                        if constexpr (BWD) pg += wrapg;
+                    if (dh != 0) {
+                        h += dh;
+                        if (h >= H) h -= H, at += span;
                     }
+                }
+                if constexpr (!VEC) {
+                    next.r += U * slots;
+                    skip();
                 }
                 float ss[U];
                 [[maybe_unused]] float sg[BWD ? U : 1];
@@ -227,9 +329,11 @@ __global__ void __launch_bounds__(kQkThreads, qk_resident(BWD)) k_qk_norm(const 
                     if constexpr (BWD) sg[u] = 0.0f;
                     if (on[u]) {
                         f2x va[2], vb[2];
+                        if constexpr (VEC) ring.get(turn, u, 0, x[u]);
                         x[u].get(va, vb);
                         ss[u] = psum(pfma(va[0], va[0], pfma(va[1], va[1], pfma(vb[0], vb[0], pmul(vb[1], vb[1])))));
                         if constexpr (BWD) {
+                            if constexpr (VEC) ring.get(turn, u, 1, g[u]);
                             g[u].get(ga[u], gb[u]);
                             if (R2 > 0) {  // turned back
                                 f2x c[2], s[2];
@@ -269,8 +373,13 @@ __global__ void __launch_bounds__(kQkThreads, qk_resident(BWD)) k_qk_norm(const 
                         const float rr = inv_sqrt(__fmaf_rn(ss[u], a.inv_n, a.eps));
                         const f2x r2 = pk2(rr, rr);
                         f2x va[2], vb[2];
-                        keep_packed(x[u].lo);
-                        keep_packed(x[u].hi);
+                        if constexpr (VEC) {
+                            asm volatile("" ::: "memory");  // read again: it need not wait in registers
+                            ring.get(turn, u, 0, x[u]);
+                        } else {
+                            keep_packed(x[u].lo);
+                            keep_packed(x[u].hi);
+                        }
                         x[u].get(va, vb);
                         if constexpr (BWD) {
                             // as in layer norm, no power of r is formed: x r is again about 1
@@ -310,11 +419,15 @@ __global__ void __launch_bounds__(kQkThreads, qk_resident(BWD)) k_qk_norm(const 
                     }
                 }
                 po += U * stepo;
+                if constexpr (VEC) {
+                    fetch(turn);  // behind the last use of what lies there
+                    turn = turn + 1 == kQkAhead ? 0 : turn + 1;
+                }
             };
             // the same turns for every thread: the sums are shuffles
             int r0 = begin;
-            for (; r0 + slots * U <= rows; r0 += slots * U) some(std::integral_constant<int, U>{}, r0);
-            for (; r0 < rows; r0 += slots) some(std::integral_constant<int, 1>{}, r0);
+            for (; r0 + slots * U <= rows; r0 += slots * U) some(std::true_type{}, r0);
+            if (r0 < rows) some(std::false_type{}, r0);
             if constexpr (BWD) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
