@@ -98,7 +98,7 @@ gdn_status_t glu_gemm(gdn::GluMaps& maps, gdn::GluGemmArgs& a, int sms, cudaStre
     a.tiles_n = (int32_t)ceil_div(a.N, MODE == gdn::kGluFwd ? 128 : 256);
     a.tiles = (int64_t)a.tiles_m * a.tiles_n * a.problems * a.splits;
     auto k = gdn::k_glu_gemm<MODE, SAVE, ACT>;
-    constexpr size_t smem = gdn::glu_gemm_smem(SAVE);
+    constexpr size_t smem = gdn::glu_gemm_smem(MODE, SAVE);
     if (!raise_smem(k, smem)) return GDN_ERR_CUDA;
     const unsigned pairs = (unsigned)std::min<int64_t>(a.tiles, std::max(1, sms / 2));
     k<<<2 * pairs, gdn::kGluGemmThreads, smem, st>>>(maps, a);
@@ -109,11 +109,14 @@ gdn_status_t glu_gemm(gdn::GluMaps& maps, gdn::GluGemmArgs& a, int sms, cudaStre
 // (300 x 4096 x 1024 18 us, in tiles 27; 1024 x 2048 x 512 15 and 17; with 32 tiles, 1024 x 1024 x 1024, 17 and 13).
 bool glu_is_few(int64_t rows, int64_t inner) { return rows <= 256 || ceil_div(rows, 256) * ceil_div(inner, 128) <= 16; }
 
-// Parts of the K axis of a product with few tiles: enough for every pair of SMs, each of at least 8 stages.
+// k of a stage of the gradients' products
+constexpr int64_t kDxK = gdn::kGluK * gdn::glu_chunks(gdn::kGluDx), kDwK = gdn::kGluK * gdn::glu_chunks(gdn::kGluDw);
+
+// Parts of the K axis of a product with few tiles: enough for every pair of SMs, each of at least 4 stages.
 int glu_splits(int64_t tiles, int64_t ksteps, int sms)
 {
     const int64_t want = std::max<int64_t>(1, (sms / 2) / tiles);
-    return (int)std::max<int64_t>(1, std::min<int64_t>({want, ksteps / 8, 64}));
+    return (int)std::max<int64_t>(1, std::min<int64_t>({want, ksteps / 4, 64}));
 }
 
 // Blocks take equal shares of the units, in multiples of 8 up to 64: one block per SM, with all of its shared memory, or
@@ -166,8 +169,8 @@ GluBackwardPlan glu_backward_plan(const gdn_glu_t& s, int sms)
     p.ld = pad8(s.inner);
     const int64_t tx = ceil_div(s.rows, 256) * ceil_div(s.width, 256);
     const int64_t tw = 2 * ceil_div(s.inner, 256) * ceil_div(s.width, 256);
-    p.splits_x = s.rows > 0 ? glu_splits(tx, 2 * ceil_div(s.inner, gdn::kGluK), sms) : 1;
-    p.splits_w = s.rows > 0 ? glu_splits(tw, ceil_div(s.rows, gdn::kGluK), sms) : 1;
+    p.splits_x = s.rows > 0 ? glu_splits(tx, 2 * ceil_div(s.inner, kDxK), sms) : 1;
+    p.splits_w = s.rows > 0 ? glu_splits(tw, ceil_div(s.rows, kDwK), sms) : 1;
     p.copies = 2 * align_up((size_t)s.rows * p.ld * 2);
     p.part = p.copies + glu_operands(s, nullptr).bytes;
     const size_t px = p.splits_x > 1 ? sizeof(float) * (size_t)p.splits_x * s.rows * s.width : 0;
@@ -297,18 +300,18 @@ gdn_status_t gdn_glu_backward(const gdn_glu_t* args, const void* dh, int64_t dh_
 
     gdn::GluMaps mx, mw;
     if (!matrix_map(&mx.a[0], dg, R, F, p.ld, 128) || !matrix_map(&mx.a[1], du, R, F, p.ld, 128) ||
-        !matrix_map(&mx.b[0], o.wg, F, D, o.ldg, 64) || !matrix_map(&mx.b[1], o.wu, F, D, o.ldu, 64) ||
-        !matrix_map(&mw.a[0], dg, R, F, p.ld, 64) || !matrix_map(&mw.a[1], du, R, F, p.ld, 64) ||
-        !matrix_map(&mw.b[0], o.x, R, D, o.ldx, 64))
+        !matrix_map(&mx.b[0], o.wg, F, D, o.ldg, 128) || !matrix_map(&mx.b[1], o.wu, F, D, o.ldu, 128) ||
+        !matrix_map(&mw.a[0], dg, R, F, p.ld, 128) || !matrix_map(&mw.a[1], du, R, F, p.ld, 128) ||
+        !matrix_map(&mw.b[0], o.x, R, D, o.ldx, 128))
         return GDN_ERR_CUDA;
     mw.b[1] = mw.b[0];
     gdn::GluGemmArgs a{};
-    a.M = R; a.N = D; a.ksteps = (int32_t)ceil_div(F, gdn::kGluK); a.parts = 2; a.problems = 1; a.splits = p.splits_x;
+    a.M = R; a.N = D; a.ksteps = (int32_t)ceil_div(F, kDxK); a.parts = 2; a.problems = 1; a.splits = p.splits_x;
     a.out[0] = dx; a.partial = part; a.status = status;
     gdn_status_t r = glu_gemm<gdn::kGluDx>(mx, a, sms, st);
     if (r != GDN_OK) return r;
     if (p.splits_x > 1 && !glu_join<bf16>(part, p.splits_x, R * D, dx, nullptr, 1, st)) return GDN_ERR_CUDA;
-    a.M = F; a.N = D; a.ksteps = (int32_t)ceil_div(R, gdn::kGluK); a.parts = 1; a.problems = 2; a.splits = p.splits_w;
+    a.M = F; a.N = D; a.ksteps = (int32_t)ceil_div(R, kDwK); a.parts = 1; a.problems = 2; a.splits = p.splits_w;
     a.out[0] = dw_gate; a.out[1] = dw_up; a.out_f32 = dw_dtype == GDN_F32;
     r = glu_gemm<gdn::kGluDw>(mw, a, sms, st);
     if (r != GDN_OK) return r;

@@ -151,16 +151,14 @@ __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.
 
 // Operand tiles lie as TMA leaves them with 128-byte swizzle.  K-major: rows of 64 k; the next 8 rows are
 // 1024 bytes on.  Otherwise (k by k rows of 64 columns): the next 8 k are 1024 bytes on, the next 64
-// columns a box of 64 k on.
-constexpr int kGluK = 64;                       // k per stage
-constexpr uint32_t kGluBox = kGluK * 128;       // bytes of a box of 64 columns by 64 k
-__device__ __forceinline__ uint64_t swizzled_desc(uint32_t addr, bool kmajor)
+// columns a box on.
+constexpr int kGluK = 64;  // k of a box of a K-major operand
+// `box`: the bytes of 64 columns by the stage's k, for operands that are not K-major
+__device__ __forceinline__ uint64_t swizzled_desc(uint32_t addr, bool kmajor, uint32_t box = 0)
 {
-    const uint64_t lbo = kmajor ? 1 : kGluBox >> 4, sbo = 1024 >> 4;
+    const uint64_t lbo = kmajor ? 1 : box >> 4, sbo = 1024 >> 4;
     return (uint64_t)((addr >> 4) & 0x3FFFu) | (lbo << 16) | (sbo << 32) | (1ull << 46) | (2ull << 61);
 }
-// bytes from one step of 16 k to the next
-__device__ __forceinline__ uint32_t k16_bytes(bool kmajor) { return kmajor ? 32 : 2048; }
 // fp32 accumulators, bf16 operands
 __host__ __device__ constexpr uint32_t bf16_idesc(int m, int n, bool a_kmajor, bool b_kmajor)
 {
@@ -193,15 +191,18 @@ struct GluTile {
     int problem, split, k0, k1;
 };
 
-constexpr int kGluStages = 6;                      // 5 where the forward saves: three more planes are staged
-constexpr uint32_t kGluOperand = 128 * kGluK * 2;  // bytes of one operand of one CTA in a stage
+constexpr uint32_t kGluOperand = 128 * kGluK * 2;  // bytes of 128 rows by 64 k of an operand
+// What a stage holds of either operand, in 64 k.  A box is 16 KB in every mode, 128 rows by 64 k, or 64 columns by
+// 128 k: with half of that a product takes an eighth longer (forward 705 and 792 us at 8192 x 4096 x 8192).
+__host__ __device__ constexpr int glu_chunks(int mode) { return mode == 0 ? 1 : 2; }
+// 192 KB of stages; 160 where the forward saves: three more planes are staged on their way out
+__host__ __device__ constexpr int glu_stages(int mode, bool save) { return mode != 0 ? 3 : save ? 5 : 6; }
 constexpr int kGluThreads = 256;                   // of k_glu_few
 constexpr int kGluOutWarps = 8, kGluGemmThreads = 128 + 32 * kGluOutWarps;
-__host__ __device__ constexpr int glu_stages(bool save) { return kGluStages - (save ? 1 : 0); }
 __host__ __device__ constexpr uint32_t glu_staging(bool save) { return kGluOutWarps * (save ? 4 : 1) * 2048; }
-__host__ __device__ constexpr size_t glu_gemm_smem(bool save)
+__host__ __device__ constexpr size_t glu_gemm_smem(int mode, bool save)
 {
-    return (size_t)glu_stages(save) * 2 * kGluOperand + glu_staging(save) + 1024 + 256;
+    return (size_t)glu_stages(mode, save) * 2 * glu_chunks(mode) * kGluOperand + glu_staging(save) + 1024 + 256;
 }
 
 // Tiles in groups of 8 rows of tiles, down the rows first: what is on the chip at a time shares few rows and columns.
@@ -274,11 +275,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGluGemmThreads, 1)
     k_glu_gemm(const __grid_constant__ GluMaps maps, const GluGemmArgs a)
 {
     constexpr bool AK = MODE != kGluDw, BK = MODE == kGluFwd;  // which operands are K-major
-    constexpr int ST = glu_stages(SAVE);
+    constexpr int ST = glu_stages(MODE, SAVE), KC = glu_chunks(MODE);
+    constexpr uint32_t OPERAND = KC * kGluOperand;  // bytes of one operand in a stage
     constexpr uint32_t IDESC = bf16_idesc(256, 256, AK, BK);
     extern __shared__ unsigned char glu_smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(glu_smem_raw) + 1023) & ~(uintptr_t)1023);
-    unsigned char* staging = smem + ST * 2 * kGluOperand;
+    unsigned char* staging = smem + ST * 2 * OPERAND;
     uint64_t* full = reinterpret_cast<uint64_t*>(staging + glu_staging(SAVE));  // [ST] used in the first CTA
     uint64_t* empty = full + ST;      // [ST] one per CTA
     uint64_t* done = empty + ST;      // [2] the accumulators are complete
@@ -317,24 +319,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGluGemmThreads, 1)
                 const GluTile t = glu_tile<MODE>(a, id);
                 for (int k = t.k0; k < t.k1; ++k) {
                     if (!(ok = mbar_wait(empty + s, ph))) break;
-                    unsigned char* sa = smem + s * 2 * kGluOperand;
-                    unsigned char* sb = sa + kGluOperand;
-                    const int part = k / a.ksteps, kk = (k - part * a.ksteps) * kGluK;
+                    unsigned char* sa = smem + s * 2 * OPERAND;
+                    unsigned char* sb = sa + OPERAND;
+                    const int part = k / a.ksteps, kk = (k - part * a.ksteps) * (KC * kGluK);
                     const uint32_t bar = peer_addr(full + s, 0);
-                    if (rank == 0) mbar_arrive_expect_tx(full + s, 4 * kGluOperand);
+                    if (rank == 0) mbar_arrive_expect_tx(full + s, 4 * OPERAND);
                     const int m = (int)t.m + (int)rank * 128;
-                    if constexpr (AK) {
-                        tma_pair_2d(sa, &maps.a[part], kk, m, bar);
-                    } else {
-                        tma_pair_2d(sa, &maps.a[t.problem], m, kk, bar);
-                        tma_pair_2d(sa + kGluBox, &maps.a[t.problem], m + 64, kk, bar);
-                    }
                     if constexpr (MODE == kGluFwd) {
+                        tma_pair_2d(sa, &maps.a[0], kk, m, bar);
                         tma_pair_2d(sb, &maps.b[rank], kk, (int)t.n, bar);
                     } else {
                         const int n = (int)t.n + (int)rank * 128, which = MODE == kGluDx ? part : 0;
-                        tma_pair_2d(sb, &maps.b[which], n, kk, bar);
-                        tma_pair_2d(sb + kGluBox, &maps.b[which], n + 64, kk, bar);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if constexpr (AK) tma_pair_2d(sa + i * kGluOperand, &maps.a[part], kk + i * kGluK, m, bar);
+                            else tma_pair_2d(sa + i * kGluOperand, &maps.a[t.problem], m + i * 64, kk, bar);
+                            tma_pair_2d(sb + i * kGluOperand, &maps.b[which], n + i * 64, kk, bar);
+                        }
                     }
                     if (++s == ST) s = 0, ph ^= 1;
                 }
@@ -358,11 +359,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGluGemmThreads, 1)
                 for (int k = t.k0; k < t.k1; ++k) {
                     if (!(ok = mbar_wait(full + s, ph))) break;
                     tc_fence_after();
-                    const uint32_t sa = smem_addr(smem + s * 2 * kGluOperand);
-                    const uint64_t da = swizzled_desc(sa, AK), db = swizzled_desc(sa + kGluOperand, BK);
+                    const uint32_t sa = smem_addr(smem + s * 2 * OPERAND);
+                    const uint64_t da = swizzled_desc(sa, AK, kGluOperand), db = swizzled_desc(sa + OPERAND, BK, kGluOperand);
 #pragma unroll
-                    for (int j = 0; j < kGluK / 16; ++j)
-                        mma_bf16<2>(d, da + j * (k16_bytes(AK) >> 4), db + j * (k16_bytes(BK) >> 4), IDESC, k > t.k0 || j > 0);
+                    for (int j = 0; j < KC * kGluK / 16; ++j) {
+                        // the next 64 k of a K-major operand are a box on
+                        const uint32_t ka = AK ? j / 4 * kGluOperand + j % 4 * 32 : j * 2048, kb = BK ? j * 32 : j * 2048;
+                        mma_bf16<2>(d, da + (ka >> 4), db + (kb >> 4), IDESC, k > t.k0 || j > 0);
+                    }
                     mma_commit_pair(empty + s);
                     if (++s == ST) s = 0, ph ^= 1;
                 }
