@@ -98,7 +98,7 @@ gdn_status_t glu_gemm(gdn::GluMaps& maps, gdn::GluGemmArgs& a, int sms, cudaStre
     a.tiles_n = (int32_t)ceil_div(a.N, MODE == gdn::kGluFwd ? 128 : 256);
     a.tiles = (int64_t)a.tiles_m * a.tiles_n * a.problems * a.splits;
     auto k = gdn::k_glu_gemm<MODE, SAVE, ACT>;
-    constexpr size_t smem = gdn::glu_gemm_smem(MODE, SAVE);
+    constexpr size_t smem = gdn::glu_gemm_smem(SAVE);
     if (!raise_smem(k, smem)) return GDN_ERR_CUDA;
     const unsigned pairs = (unsigned)std::min<int64_t>(a.tiles, std::max(1, sms / 2));
     k<<<2 * pairs, gdn::kGluGemmThreads, smem, st>>>(maps, a);
@@ -109,8 +109,23 @@ gdn_status_t glu_gemm(gdn::GluMaps& maps, gdn::GluGemmArgs& a, int sms, cudaStre
 // (300 x 4096 x 1024 18 us, in tiles 27; 1024 x 2048 x 512 15 and 17; with 32 tiles, 1024 x 1024 x 1024, 17 and 13).
 bool glu_is_few(int64_t rows, int64_t inner) { return rows <= 256 || ceil_div(rows, 256) * ceil_div(inner, 128) <= 16; }
 
-// k of a stage of the gradients' products
-constexpr int64_t kDxK = gdn::kGluK * gdn::glu_chunks(gdn::kGluDx), kDwK = gdn::kGluK * gdn::glu_chunks(gdn::kGluDw);
+constexpr int64_t kStageK = 2 * gdn::kGluK;  // k of a stage of the pair's product
+
+// Tensor map of an operand of the pair's product: boxes of 64 columns by 128 rows, or (wide: whole 64 columns) of two such runs
+// side by side.
+bool operand_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, bool wide_boxes)
+{
+    if (!wide_boxes) return matrix_map(map, base, rows, cols, ld, 128);
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (enc == nullptr) return false;
+    const cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)(cols / 64)};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, 128};
+    const cuuint32_t box[3] = {64u, 128u, 2u};
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 // Parts of the K axis of a product with few tiles: enough for every pair of SMs, each of at least 4 stages.
 int glu_splits(int64_t tiles, int64_t ksteps, int sms)
@@ -133,7 +148,7 @@ gdn_status_t glu_few(const GluOperands& o, const gdn_glu_t& s, gdn::GluFewArgs& 
     const int resident = ceil_div((int64_t)s.inner * S, slots(S)) <= 64 ? 1 : 2;
     a.rows = (int)std::min<int64_t>(64, ceil_div(ceil_div((int64_t)s.inner * S, (int64_t)slots(S) * resident), 8) * 8);
     a.chunks = NB > 128 ? 1 : NB > 16 ? 2 : 4;
-    const size_t room = (size_t)(resident == 1 ? 224 : 110) * 1024 - gdn::kGluOperand;
+    const size_t room = (size_t)(resident == 1 ? 224 : 110) * 1024 - gdn::kGluHalf;
     a.stages = (int)std::min<size_t>(gdn::kGluFewStages, room / (a.chunks * gdn::glu_few_chunk(NB, a.rows)));
     const size_t smem = gdn::glu_few_tiles(NB, a.rows, a.stages, a.chunks) + 1024 + 512;
     gdn::GluFewMaps maps;
@@ -169,8 +184,8 @@ GluBackwardPlan glu_backward_plan(const gdn_glu_t& s, int sms)
     p.ld = pad8(s.inner);
     const int64_t tx = ceil_div(s.rows, 256) * ceil_div(s.width, 256);
     const int64_t tw = 2 * ceil_div(s.inner, 256) * ceil_div(s.width, 256);
-    p.splits_x = s.rows > 0 ? glu_splits(tx, 2 * ceil_div(s.inner, kDxK), sms) : 1;
-    p.splits_w = s.rows > 0 ? glu_splits(tw, ceil_div(s.rows, kDwK), sms) : 1;
+    p.splits_x = s.rows > 0 ? glu_splits(tx, 2 * ceil_div(s.inner, kStageK), sms) : 1;
+    p.splits_w = s.rows > 0 ? glu_splits(tw, ceil_div(s.rows, kStageK), sms) : 1;
     p.copies = 2 * align_up((size_t)s.rows * p.ld * 2);
     p.part = p.copies + glu_operands(s, nullptr).bytes;
     const size_t px = p.splits_x > 1 ? sizeof(float) * (size_t)p.splits_x * s.rows * s.width : 0;
@@ -232,12 +247,13 @@ gdn_status_t gdn_glu_forward(const gdn_glu_t* args, void* h, void* saved, void* 
         return glu_few<256>(o, s, a, sms, st);
     }
     gdn::GluMaps maps;
-    if (!matrix_map(&maps.a[0], o.x, R, D, o.ldx, 128) || !matrix_map(&maps.b[0], o.wg, F, D, o.ldg, 128) ||
-        !matrix_map(&maps.b[1], o.wu, F, D, o.ldu, 128))
+    const bool wide_boxes = D % 64 == 0;
+    if (!operand_map(&maps.a[0], o.x, R, D, o.ldx, wide_boxes) || !operand_map(&maps.b[0], o.wg, F, D, o.ldg, wide_boxes) ||
+        !operand_map(&maps.b[1], o.wu, F, D, o.ldu, wide_boxes))
         return GDN_ERR_CUDA;
     maps.a[1] = maps.a[0];
     gdn::GluGemmArgs a{};
-    a.M = R; a.N = F; a.ksteps = ksteps; a.parts = 1; a.problems = 1; a.splits = 1;
+    a.M = R; a.N = F; a.ksteps = (int32_t)ceil_div(D, kStageK); a.parts = 1; a.problems = 1; a.splits = 1; a.wide = wide_boxes;
     a.out[0] = h;
     a.saved = static_cast<uint16_t*>(saved); a.status = status;
     if (s.act == GDN_ACT_SILU)
@@ -299,19 +315,20 @@ gdn_status_t gdn_glu_backward(const gdn_glu_t* args, const void* dh, int64_t dh_
     if (!launched()) return GDN_ERR_CUDA;
 
     gdn::GluMaps mx, mw;
-    if (!matrix_map(&mx.a[0], dg, R, F, p.ld, 128) || !matrix_map(&mx.a[1], du, R, F, p.ld, 128) ||
-        !matrix_map(&mx.b[0], o.wg, F, D, o.ldg, 128) || !matrix_map(&mx.b[1], o.wu, F, D, o.ldu, 128) ||
-        !matrix_map(&mw.a[0], dg, R, F, p.ld, 128) || !matrix_map(&mw.a[1], du, R, F, p.ld, 128) ||
-        !matrix_map(&mw.b[0], o.x, R, D, o.ldx, 128))
+    const bool wide_boxes = D % 64 == 0 && F % 64 == 0;
+    if (!operand_map(&mx.a[0], dg, R, F, p.ld, wide_boxes) || !operand_map(&mx.a[1], du, R, F, p.ld, wide_boxes) ||
+        !operand_map(&mx.b[0], o.wg, F, D, o.ldg, wide_boxes) || !operand_map(&mx.b[1], o.wu, F, D, o.ldu, wide_boxes) ||
+        !operand_map(&mw.b[0], o.x, R, D, o.ldx, wide_boxes))
         return GDN_ERR_CUDA;
-    mw.b[1] = mw.b[0];
+    mw.a[0] = mx.a[0]; mw.a[1] = mx.a[1]; mw.b[1] = mw.b[0];
     gdn::GluGemmArgs a{};
-    a.M = R; a.N = D; a.ksteps = (int32_t)ceil_div(F, kDxK); a.parts = 2; a.problems = 1; a.splits = p.splits_x;
+    a.wide = wide_boxes;
+    a.M = R; a.N = D; a.ksteps = (int32_t)ceil_div(F, kStageK); a.parts = 2; a.problems = 1; a.splits = p.splits_x;
     a.out[0] = dx; a.partial = part; a.status = status;
     gdn_status_t r = glu_gemm<gdn::kGluDx>(mx, a, sms, st);
     if (r != GDN_OK) return r;
     if (p.splits_x > 1 && !glu_join<bf16>(part, p.splits_x, R * D, dx, nullptr, 1, st)) return GDN_ERR_CUDA;
-    a.M = F; a.N = D; a.ksteps = (int32_t)ceil_div(R, kDwK); a.parts = 1; a.problems = 2; a.splits = p.splits_w;
+    a.M = F; a.N = D; a.ksteps = (int32_t)ceil_div(R, kStageK); a.parts = 1; a.problems = 2; a.splits = p.splits_w;
     a.out[0] = dw_gate; a.out[1] = dw_up; a.out_f32 = dw_dtype == GDN_F32;
     r = glu_gemm<gdn::kGluDw>(mw, a, sms, st);
     if (r != GDN_OK) return r;

@@ -102,6 +102,14 @@ __device__ __forceinline__ void tma_pair_2d(void* dst, const CUtensorMap* map, i
         ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(mbar)
         : "memory");
 }
+// The same of 64 columns, a second run of them, and rows in between: two boxes of a matrix side by side
+__device__ __forceinline__ void tma_pair_3d(void* dst, const CUtensorMap* map, int y, int chunk, uint32_t mbar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(chunk), "r"(mbar)
+        : "memory");
+}
 __device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* mbar)
 {
     asm volatile(
@@ -176,6 +184,7 @@ struct GluMaps {
 struct GluGemmArgs {
     int64_t M, N;        // of the output (forward: tokens and units)
     int32_t ksteps;      // stages of one part of K
+    int32_t wide;        // the maps' boxes are whole operands of a stage: rows of whole 64 columns
     int32_t parts;       // dx: 2 (dg, then du)
     int32_t tiles_m, tiles_n, problems, splits;
     int64_t tiles;       // tiles_m tiles_n problems splits
@@ -191,18 +200,17 @@ struct GluTile {
     int problem, split, k0, k1;
 };
 
-constexpr uint32_t kGluOperand = 128 * kGluK * 2;  // bytes of 128 rows by 64 k of an operand
-// What a stage holds of either operand, in 64 k.  A box is 16 KB in every mode, 128 rows by 64 k, or 64 columns by
-// 128 k: with half of that a product takes an eighth longer (forward 705 and 792 us at 8192 x 4096 x 8192).
-__host__ __device__ constexpr int glu_chunks(int mode) { return mode == 0 ? 1 : 2; }
-// 192 KB of stages; 160 where the forward saves: three more planes are staged on their way out
-__host__ __device__ constexpr int glu_stages(int mode, bool save) { return mode != 0 ? 3 : save ? 5 : 6; }
+// A stage holds 128 k of either operand.  The larger the boxes that fetch it the better: 8192 x 4096 x 8192 takes the
+// forward 792 us with boxes of 8 KB, 705 with 16 KB and 674 with 32 KB, the weights' gradients 829, 735 and 712.
+constexpr uint32_t kGluHalf = 128 * kGluK * 2;     // 128 rows by 64 k, or 64 columns by 128 k
+constexpr uint32_t kGluOperand = 2 * kGluHalf;     // bytes of one operand of one CTA in a stage
+constexpr int kGluStages = 3;
 constexpr int kGluThreads = 256;                   // of k_glu_few
 constexpr int kGluOutWarps = 8, kGluGemmThreads = 128 + 32 * kGluOutWarps;
-__host__ __device__ constexpr uint32_t glu_staging(bool save) { return kGluOutWarps * (save ? 4 : 1) * 2048; }
-__host__ __device__ constexpr size_t glu_gemm_smem(int mode, bool save)
+__host__ __device__ constexpr uint32_t glu_staging(bool save) { return kGluOutWarps * (save ? 2 : 1) * 2048; }
+__host__ __device__ constexpr size_t glu_gemm_smem(bool save)
 {
-    return (size_t)glu_stages(mode, save) * 2 * glu_chunks(mode) * kGluOperand + glu_staging(save) + 1024 + 256;
+    return (size_t)kGluStages * 2 * kGluOperand + glu_staging(save) + 1024 + 256;
 }
 
 // Tiles in groups of 8 rows of tiles, down the rows first: what is on the chip at a time shares few rows and columns.
@@ -275,12 +283,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGluGemmThreads, 1)
     k_glu_gemm(const __grid_constant__ GluMaps maps, const GluGemmArgs a)
 {
     constexpr bool AK = MODE != kGluDw, BK = MODE == kGluFwd;  // which operands are K-major
-    constexpr int ST = glu_stages(MODE, SAVE), KC = glu_chunks(MODE);
-    constexpr uint32_t OPERAND = KC * kGluOperand;  // bytes of one operand in a stage
+    constexpr int ST = kGluStages;
     constexpr uint32_t IDESC = bf16_idesc(256, 256, AK, BK);
     extern __shared__ unsigned char glu_smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(glu_smem_raw) + 1023) & ~(uintptr_t)1023);
-    unsigned char* staging = smem + ST * 2 * OPERAND;
+    unsigned char* staging = smem + ST * 2 * kGluOperand;
     uint64_t* full = reinterpret_cast<uint64_t*>(staging + glu_staging(SAVE));  // [ST] used in the first CTA
     uint64_t* empty = full + ST;      // [ST] one per CTA
     uint64_t* done = empty + ST;      // [2] the accumulators are complete
@@ -319,24 +326,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGluGemmThreads, 1)
                 const GluTile t = glu_tile<MODE>(a, id);
                 for (int k = t.k0; k < t.k1; ++k) {
                     if (!(ok = mbar_wait(empty + s, ph))) break;
-                    unsigned char* sa = smem + s * 2 * OPERAND;
-                    unsigned char* sb = sa + OPERAND;
-                    const int part = k / a.ksteps, kk = (k - part * a.ksteps) * (KC * kGluK);
+                    unsigned char* sa = smem + s * 2 * kGluOperand;
+                    unsigned char* sb = sa + kGluOperand;
+                    const int part = k / a.ksteps, kk = (k - part * a.ksteps) * 2 * kGluK;
                     const uint32_t bar = peer_addr(full + s, 0);
-                    if (rank == 0) mbar_arrive_expect_tx(full + s, 4 * OPERAND);
-                    const int m = (int)t.m + (int)rank * 128;
-                    if constexpr (MODE == kGluFwd) {
-                        tma_pair_2d(sa, &maps.a[0], kk, m, bar);
-                        tma_pair_2d(sb, &maps.b[rank], kk, (int)t.n, bar);
-                    } else {
-                        const int n = (int)t.n + (int)rank * 128, which = MODE == kGluDx ? part : 0;
+                    if (rank == 0) mbar_arrive_expect_tx(full + s, 4 * kGluOperand);
+                    auto fetch = [&](unsigned char* to, const CUtensorMap* map, bool kmajor, int row) {
+                        if (a.wide) {
+                            tma_pair_3d(to, map, kmajor ? row : kk, (kmajor ? kk : row) / 64, bar);
+                        } else {
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            if constexpr (AK) tma_pair_2d(sa + i * kGluOperand, &maps.a[part], kk + i * kGluK, m, bar);
-                            else tma_pair_2d(sa + i * kGluOperand, &maps.a[t.problem], m + i * 64, kk, bar);
-                            tma_pair_2d(sb + i * kGluOperand, &maps.b[which], n + i * 64, kk, bar);
+                            for (int i = 0; i < 2; ++i)
+                                tma_pair_2d(to + i * kGluHalf, map, kmajor ? kk + i * 64 : row + i * 64, kmajor ? row : kk, bar);
                         }
-                    }
+                    };
+                    const int half = (int)rank * 128;
+                    fetch(sa, &maps.a[MODE == kGluFwd ? 0 : MODE == kGluDx ? part : t.problem], AK, (int)t.m + half);
+                    fetch(sb, &maps.b[MODE == kGluFwd ? rank : MODE == kGluDx ? part : 0], BK, (int)t.n + (MODE == kGluFwd ? 0 : half));
                     if (++s == ST) s = 0, ph ^= 1;
                 }
             }
@@ -359,12 +365,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGluGemmThreads, 1)
                 for (int k = t.k0; k < t.k1; ++k) {
                     if (!(ok = mbar_wait(full + s, ph))) break;
                     tc_fence_after();
-                    const uint32_t sa = smem_addr(smem + s * 2 * OPERAND);
-                    const uint64_t da = swizzled_desc(sa, AK, kGluOperand), db = swizzled_desc(sa + OPERAND, BK, kGluOperand);
+                    const uint32_t sa = smem_addr(smem + s * 2 * kGluOperand);
+                    const uint64_t da = swizzled_desc(sa, AK, kGluHalf), db = swizzled_desc(sa + kGluOperand, BK, kGluHalf);
 #pragma unroll
-                    for (int j = 0; j < KC * kGluK / 16; ++j) {
-                        // the next 64 k of a K-major operand are a box on
-                        const uint32_t ka = AK ? j / 4 * kGluOperand + j % 4 * 32 : j * 2048, kb = BK ? j * 32 : j * 2048;
+                    for (int j = 0; j < 2 * kGluK / 16; ++j) {
+                        // the next 64 k of a K-major operand are a half on
+                        const uint32_t split = j / 4 * kGluHalf + j % 4 * 32, ka = AK ? split : j * 2048, kb = BK ? split : j * 2048;
                         mma_bf16<2>(d, da + (ka >> 4), db + (kb >> 4), IDESC, k > t.k0 || j > 0);
                     }
                     mma_commit_pair(empty + s);
@@ -379,7 +385,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGluGemmThreads, 1)
         // ---- both CTAs: accumulators to memory.  A warp: 32 of this CTA's 128 rows, a thread each, and half of the columns.
         uint32_t acc = 0, ph = 0;
         const int quarter = warp & 3, half = (warp - 4) >> 2;
-        unsigned char* st = staging + (warp - 4) * (SAVE ? 4 : 1) * 2048;
+        unsigned char* st = staging + (warp - 4) * (SAVE ? 2 : 1) * 2048;
         for (int64_t id = first; id < a.tiles; id += step) {
             const GluTile t = glu_tile<MODE>(a, id);
             ok = mbar_wait(done + acc, ph);
@@ -395,36 +401,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGluGemmThreads, 1)
             };
             if constexpr (MODE == kGluFwd) {
                 for (int c0 = half * 64; c0 < half * 64 + 64 && t.n + c0 < a.N; c0 += 32) {
+                    float g[32], u[32];
+                    tmem_ld16(col + c0, *reinterpret_cast<float(*)[16]>(g));
+                    tmem_ld16(col + c0 + 16, *reinterpret_cast<float(*)[16]>(g + 16));
+                    tmem_ld16(col + 128 + c0, *reinterpret_cast<float(*)[16]>(u));
+                    tmem_ld16(col + 128 + c0 + 16, *reinterpret_cast<float(*)[16]>(u + 16));
+                    tmem_wait_ld();
+                    if constexpr (SAVE) {
+                        // the upper halves, then h and the next bytes
 #pragma unroll
-                    for (int i = 0; i < 32; i += 16) {
-                        float g[16], u[16];
-                        tmem_ld16(col + c0 + i, g);
-                        tmem_ld16(col + 128 + c0 + i, u);
-                        tmem_wait_ld();
-                        if constexpr (SAVE) {
-                            alignas(16) uint16_t x[3][16];
+                        for (int p = 0; p < 4; ++p) {
+                            alignas(16) uint32_t x[4], y[4];
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) glu_pack(g[k], u[k], x[0][k], x[1][k], x[2][k]);
-#pragma unroll
-                            for (int p = 0; p < 3; ++p) {
-                                *glu_piece(st + (p + 1) * 2048, lane, i / 8) = reinterpret_cast<const uint4*>(x[p])[0];
-                                *glu_piece(st + (p + 1) * 2048, lane, i / 8 + 1) = reinterpret_cast<const uint4*>(x[p])[1];
+                            for (int k = 0; k < 4; ++k) {
+                                const int e = p * 8 + 2 * k;
+                                x[k] = __byte_perm(__float_as_uint(g[e]), __float_as_uint(g[e + 1]), 0x7632);
+                                y[k] = __byte_perm(__float_as_uint(u[e]), __float_as_uint(u[e + 1]), 0x7632);
                             }
+                            *glu_piece(st, lane, p) = *reinterpret_cast<const uint4*>(x);
+                            *glu_piece(st + 2048, lane, p) = *reinterpret_cast<const uint4*>(y);
                         }
-                        uint4 v[2];
-                        uint32_t* w = reinterpret_cast<uint32_t*>(v);
+                        __syncwarp();
+                        out(st, a.saved, t.n + c0, 2);
+                        out(st + 2048, a.saved + a.M * a.N, t.n + c0, 2);
+                        __syncwarp();
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            w[k] = bf16_pair(glu_act<ACT>(g[2 * k]) * u[2 * k], glu_act<ACT>(g[2 * k + 1]) * u[2 * k + 1]);
-                        *glu_piece(st, lane, i / 8) = v[0];
-                        *glu_piece(st, lane, i / 8 + 1) = v[1];
+                        for (int p = 0; p < 4; ++p) {
+                            alignas(16) uint32_t x[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const int e = p * 8 + 2 * k;  // bytes 1 of g, u, g, u
+                                const uint32_t lo = __byte_perm(__float_as_uint(g[e]), __float_as_uint(u[e]), 0x0051);
+                                const uint32_t hi = __byte_perm(__float_as_uint(g[e + 1]), __float_as_uint(u[e + 1]), 0x0051);
+                                x[k] = __byte_perm(lo, hi, 0x5410);
+                            }
+                            *glu_piece(st + 2048, lane, p) = *reinterpret_cast<const uint4*>(x);
+                        }
+                    }
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        alignas(16) uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int e = p * 8 + 2 * k;
+                            w[k] = bf16_pair(glu_act<ACT>(g[e]) * u[e], glu_act<ACT>(g[e + 1]) * u[e + 1]);
+                        }
+                        *glu_piece(st, lane, p) = *reinterpret_cast<const uint4*>(w);
                     }
                     __syncwarp();
                     out(st, a.out[0], t.n + c0, 2);
-                    if constexpr (SAVE) {
-#pragma unroll
-                        for (int p = 0; p < 3; ++p) out(st + (p + 1) * 2048, a.saved + p * a.M * a.N, t.n + c0, 2);
-                    }
+                    if constexpr (SAVE) out(st + 2048, a.saved + 2 * a.M * a.N, t.n + c0, 2);
                     __syncwarp();
                 }
             } else {
@@ -492,7 +518,7 @@ __host__ __device__ constexpr uint32_t glu_few_chunk(int NB, int rows) { return 
 // nothing; the results lie where the stages were.
 __host__ __device__ inline uint32_t glu_few_tiles(int NB, int rows, int stages, int chunks)
 {
-    const uint32_t tiles = stages * chunks * glu_few_chunk(NB, rows) + kGluOperand, results = 2 * NB * 64 * 4;
+    const uint32_t tiles = stages * chunks * glu_few_chunk(NB, rows) + kGluHalf, results = 2 * NB * 64 * 4;
     return tiles > results ? tiles : results;
 }
 
