@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(NT + 32, RES) k_policy(const PolicyArgs a)
                 unsigned char* dst = policy_smem + slot * SLOT;
                 if (lost || !mbar_wait_bounded(empty + slot, phase, LIMIT)) {
                     lost = 1;
-                    return;
+                    break;
                 }
                 // Whole 16-byte granules, those that the tile shares with its neighbours too; what shares one with
                 // the bytes before or behind the row comes element by element.
@@ -189,7 +189,10 @@ __global__ void __launch_bounds__(NT + 32, RES) k_policy(const PolicyArgs a)
                 }
                 if (++slot == K) slot = 0, phase ^= 1;
             }
+            if (lost) break;
         }
+        // every copy has landed before the block ends, whether the walks wait for it or have given up
+        for (int i = 0; i < K && mbar_wait_bounded(full + i, i < slot ? phase ^ 1 : phase, LIMIT); ++i) {}
         return;
     }
 
