@@ -47,7 +47,8 @@ __device__ __forceinline__ void glu_act2(float g, float& a, float& slope)
         a = g * s;
         slope = s * __fmaf_rn(g, 1.0f - s, 1.0f);
     } else {
-        const float g2 = g * g, s = sigmoid(1.5957691216057308f * __fmaf_rn(0.044715f * g2, g, g));
+        // a square that overflowed would make the slope of the far ends 0 times infinity
+        const float g2 = fminf(g * g, 1e30f), s = sigmoid(1.5957691216057308f * __fmaf_rn(0.044715f * g2, g, g));
         a = g * s;
         slope = __fmaf_rn(a * (1.0f - s), 1.5957691216057308f * __fmaf_rn(0.134145f, g2, 1.0f), s);
     }
@@ -347,10 +348,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGluGemmThreads, 1)
                 }
             }
             // every stage has been released: no arrival is under way to a CTA that has ended
+            const int end = s;
+            const uint32_t end_ph = ph;
             for (int i = 0; i < ST && ok; ++i) {
                 ok = mbar_wait(empty + s, ph);
                 if (++s == ST) s = 0, ph ^= 1;
             }
+            // a wait that ran out: both CTAs' copies land before the pair ends
+            for (int i = 0; i < ST && !ok && rank == 0 && mbar_wait(full + i, i < end ? end_ph ^ 1 : end_ph); ++i) {}
         }
     } else if (warp == 1 && rank == 0) {
         if (lane == 0) {
@@ -572,6 +577,8 @@ __global__ void __launch_bounds__(kGluThreads, 1) k_glu_few(const __grid_constan
                     tma_2d(smem + (s * C + c) * chunk + at, map, ((first + k) * C + c) * kGluK, y, full + s);
                 if (++s == ST) s = 0, ph ^= 1;
             }
+            // a wait that ran out: the copies land before the block ends
+            for (int i = 0; i < ST && !ok && mbar_wait(full + i, i < s ? ph ^ 1 : ph); ++i) {}
         }
     } else if (warp == 1) {
         if (lane == 0) {

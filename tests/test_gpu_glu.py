@@ -29,11 +29,12 @@ def e_dot(n, M):
     return (n / 4 + 8) * U * M
 
 
-def near(name, got, want, tol):
+def near(name, got, want, tol, M=0.0):
+    """M: the magnitudes' sum; a sum of which it passes fp32's range may overflow, and is not held to its value."""
     half = HALF[got.dtype] * np.abs(want) * (1 + 2.0 ** -7)
     got = got.detach().double().cpu().numpy()
     assert got.shape == want.shape, name
-    bad = ~(np.abs(got - want) <= tol + half + 1e-37)
+    bad = ~(np.abs(got - want) <= tol + half + 1e-37) & (M + np.zeros_like(want) < 3.3e38)
     assert not bad.any(), (name, int(bad.sum()), np.argwhere(bad)[:4], np.abs(got - want)[bad][:4], (tol + half)[bad][:4])
 
 
@@ -62,8 +63,8 @@ def check(c, act="silu", views=None, backward=True, **kw):
     n = np.abs
     want = ops.glu_backward(x, wg, wu, dh, act)
     near("dx", grads[0], want[0], edg @ n(wg) + edu @ n(wu) + e_dot(2 * F, n(dg) @ n(wg) + n(du) @ n(wu)) * 1.01)
-    near("dwg", grads[1], want[1], edg.T @ n(x) + e_dot(T, n(dg).T @ n(x)) * 1.01)
-    near("dwu", grads[2], want[2], edu.T @ n(x) + e_dot(T, n(du).T @ n(x)) * 1.01)
+    near("dwg", grads[1], want[1], edg.T @ n(x) + e_dot(T, n(dg).T @ n(x)) * 1.01, n(dg).T @ n(x))
+    near("dwu", grads[2], want[2], edu.T @ n(x) + e_dot(T, n(du).T @ n(x)) * 1.01, n(du).T @ n(x))
     assert status.item() == gdn.GDN_OK
     return h, grads
 
@@ -79,6 +80,22 @@ def test_few_tokens(T, D, F, act):
                                        (1024, 512, 640, "silu"), (333, 1, 5, "silu"), (2100, 264, 136, "gelu"), (600, 2048, 1032, "silu")])
 def test_many_tokens(T, D, F, act):
     check(case(T, D, F), act)
+
+
+@pytest.mark.parametrize("T", [5, 300])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_far_ends(T, act):
+    """Activations whose squares overflow fp32 keep their slopes, 1 and 0 (dw_up's first column, 1e20 * 1e20 dh, is out of
+    range)."""
+    c = case(T, 2, 40)
+    ends = torch.tensor([1e20, -1e20, 30.0, -30.0, 0.0], dtype=BF).repeat(T // 5).cuda()
+    x, wg, wu = (c[n][0].clone() for n in ("x", "wg", "wu"))
+    x[:, 0], x[:, 1] = ends, 1.0
+    wg[:, 0], wg[:, 1] = 1.0, 0.0
+    wu[:, 0] = 0.0
+    for n, t in dict(x=x, wg=wg, wu=wu).items():
+        c[n] = (t, t.double().cpu().numpy())
+    check(c, act)
 
 
 def test_more_tiles_than_pairs_of_sms():
