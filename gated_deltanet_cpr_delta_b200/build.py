@@ -25,7 +25,7 @@ SOURCES = ["gdn_cpr.cu", "identity.cu", "layer_ops.cu", "block_ops.cu", "glu_ops
 DEPS = ["gdn_cpr.cu", "identity.cu", "kernels.cuh", "schedule.cuh", "tma.cuh", "k_tables.cuh", "k_ptok.cuh",
         "k_tc.cuh", "k_prep.cuh", "k_pchunk.cuh", "k_decode.cuh", "k_bwd.cuh", "k_bgrad.cuh",
         "layer_ops.cu", "layer_common.cuh", "k_conv.cuh", "k_norm.cuh", "k_ssm.cuh", "k_ssm_bwd.cuh",
-        "layer_host.cuh", "block_ops.cu", "k_qknorm.cuh", "k_policy.cuh", "tensor_map.cuh",
+        "layer_host.cuh", "cluster.cuh", "block_ops.cu", "k_qknorm.cuh", "k_policy.cuh", "tensor_map.cuh",
         "glu_ops.cu", "k_glu.cuh"]
 HEADERS = [os.path.join(ROOT, "include", "gdn_cpr.h")]
 

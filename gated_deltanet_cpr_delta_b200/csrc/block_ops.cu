@@ -49,8 +49,8 @@ int qk_lanes(int32_t d)
 }
 
 // Tokens that a block takes at a time: the same number of tiles for every block, as large as 16 KB of angles (or
-// 1024 rows) allow.  Each tile costs its setup and two barriers: 4 tokens at a time took 65 us where these take 63, the gradients 217 and 192
-// (16384 tokens, 16 + 16 heads of 128).
+// 1024 rows) allow.  Each tile costs its setup and two barriers: 4 tokens at a time took 65 us where these took 63 (16384
+// tokens, 16 + 16 heads of 128), the gradients 217 and 192 (32 + 32 heads).
 int qk_tokens(const gdn_qk_norm_t* s, int tpr, int blocks)
 {
     const int64_t heads = (int64_t)s->q_heads + s->k_heads;
@@ -127,12 +127,39 @@ gdn_status_t policy_check(const gdn_policy_t* s, const int32_t* status)
     return GDN_OK;
 }
 
+// A cluster of S blocks for each row, two blocks per SM.
+template <typename T, bool BWD, bool ALIGNED>
+gdn_status_t policy_split(const gdn::PolicyArgs& a, int S, cudaStream_t st)
+{
+    auto k = gdn::k_policy<T, BWD, ALIGNED, 256, 2, true>;
+    const size_t smem = (size_t)gdn::policy_slots(2) * gdn::policy_slot_bytes(256) + sizeof(float2) * 256 * (gdn::kPolicyParts / 2);
+    if (!raise_smem(k, smem)) return GDN_ERR_CUDA;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(a.T * S));
+    cfg.blockDim = dim3(256 + 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)S;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, a) == cudaSuccess && launched() ? GDN_OK : GDN_ERR_CUDA;
+}
+
 template <typename T, bool BWD, bool ALIGNED, int NT, int RES>
 gdn_status_t policy_run(const gdn::PolicyArgs& a, cudaStream_t st)
 {
     const int sms = sm_count();
     if (sms == 0) return GDN_ERR_CUDA;
-    auto k = gdn::k_policy<T, BWD, ALIGNED, NT, RES>;
+    if constexpr (NT == 256) {
+        const int64_t tile = gdn::policy_tile_bytes(NT) / (int64_t)sizeof(T);
+        int S = 1 << gdn::policy_parts_log((int)ceil_div(a.V, tile));
+        while (S > 1 && a.T * S > sms * 7 / 4) S /= 2;
+        if (S > 1) return policy_split<T, BWD, ALIGNED>(a, S, st);
+    }
+    auto k = gdn::k_policy<T, BWD, ALIGNED, NT, RES, false>;
     constexpr size_t smem = (size_t)gdn::policy_slots(RES) * gdn::policy_slot_bytes(NT);
     if (!raise_smem(k, smem)) return GDN_ERR_CUDA;
     k<<<(unsigned)std::min<int64_t>(a.T, (int64_t)sms * RES), NT + 32, smem, st>>>(a);

@@ -9,15 +9,24 @@
 // into a ring in shared memory with bulk copies; the tiles of a row's end are still there when the second walk
 // begins with them, and only what the ring does not hold is fetched again (from L2).  The copies run
 // ahead over the end of the walks and of the rows, so that memory does not wait for the two block-wide sums per row.
+// Bound by the bytes (the logits once, with their gradient twice) next to 2^x: one per logit, with the gradient two, which
+// alone would take 235 us of the 395 to 400 us for 4096 x 131072 bf16 (5.4 TB/s; the special-function unit at 16 per cycle
+// and SM).  777 x 50021 fp32, losses alone: 35 us (4.4 TB/s).  64 x 131072 bf16, log-probabilities: 12 us, one row per
+// block on 64 of the SMs.
 // (Rows cut over a cluster of up to 8 blocks, wholly in shared memory, waited for each other: 495 us at
 // 4096 x 131072 bf16, whether with the cluster's barrier or with exchanges a row ahead.)
 //
-// The partition of a row follows from the vocabulary and the type alone: a thread's elements are the same
-// whatever the row's address and stride, so a row's log-probability has the same bits in every
+// Where there are few rows, a cluster of blocks shares each (64 x 131072: 4): a block walks its part of the tiles, then all
+// read the others' maxima and sums in distributed shared memory.
+//
+// The partition of a row, up to 8 parts, follows from the vocabulary and the type alone: a thread's elements are the same
+// whatever the row's address and stride, and their parts' sums are joined one after the other, whether they lie in one
+// block or in several.  So a row's log-probability has the same bits in every
 // batch, in a strided view or a dense tensor, in the forward and with the gradient.  A ratio between
 // a rollout and a trainer that saw the same logits is then exactly 1.
 #pragma once
 
+#include "cluster.cuh"
 #include "layer_common.cuh"
 #include "tma.cuh"
 
@@ -103,29 +112,52 @@ __host__ __device__ constexpr int policy_slot_bytes(int NT) { return policy_tile
 // Tiles in the ring with so many blocks per SM; all but two of them stay for the second walk.
 __host__ __device__ constexpr int policy_slots(int resident) { return resident == 2 ? 6 : 4; }
 
+// Parts of a row of n tiles: a power of two (its logarithm), of at least 4 tiles each
+constexpr int kPolicyParts = 8;
+__host__ __device__ constexpr int policy_parts_log(int n) { return n >= 32 ? 3 : n >= 16 ? 2 : n >= 8 ? 1 : 0; }
+
+// The maximum and sum of what lies behind, joined to those of what lies before
+__device__ __forceinline__ void policy_add(float& m, float& sum, float m1, float sum1)
+{
+    const float M = fmaxf(m, m1), base = policy_base(M);
+    sum = __fmaf_rn(sum1, ex2(m1 - base), sum * ex2(m - base));
+    m = M;
+}
+
 // NT threads walk, 32 more fetch; `RES` blocks per SM.  ALIGNED: every row of the logits and of the gradient is whole
-// 16-byte vectors.
-template <typename T, bool BWD, bool ALIGNED, int NT, int RES>
+// 16-byte vectors.  SPLIT: a cluster of blocks per row, each with the same number of the row's parts.
+template <typename T, bool BWD, bool ALIGNED, int NT, int RES, bool SPLIT>
 __global__ void __launch_bounds__(NT + 32, RES) k_policy(const PolicyArgs a)
 {
     constexpr int E = 16 / (int)sizeof(T);  // elements of a vector
     constexpr int NV = kPolicyVecs, K = policy_slots(RES), TILE = NT * NV * E, SLOT = policy_slot_bytes(NT), WARPS = NT / 32;
     constexpr long long LIMIT = 1ll << 31;
     extern __shared__ __align__(128) unsigned char policy_smem[];  // tiles, each at its global address mod 16
-    __shared__ __align__(8) uint64_t full[K], empty[K];
+    __shared__ __align__(8) uint64_t full[K], empty[K], joined;
     __shared__ float wm[WARPS], ws[WARPS], target_logit;
     __shared__ volatile int lost;           // a wait that ran out: nothing is written from then on
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int n = (int)(((int64_t)a.V + TILE - 1) / TILE);        // tiles of a row
+    const int tiles = (int)(((unsigned)a.V + TILE - 1) / TILE), lg = NT == 256 ? policy_parts_log(tiles) : 0, parts = 1 << lg;  // of a row
+    int S = 1, rank = 0;  // blocks of a row, and which of them this is
+    if constexpr (SPLIT) {
+        asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(S));
+        rank = (int)cta_rank();
+    }
+    const int mine = parts / S, part0 = mine * rank;  // this block's parts, and its tiles
+    const int first = SPLIT ? tiles * part0 >> lg : 0, last = SPLIT ? tiles * (part0 + mine) >> lg : tiles, n = last - first;
+    const int64_t row0 = SPLIT ? blockIdx.x / S : blockIdx.x, rows = SPLIT ? a.T : gridDim.x;  // the block's first row and its step
     const int stay = BWD ? min(n, K - 2) : 0, again = BWD ? n - stay : 0;
+    float2* found = reinterpret_cast<float2*>(policy_smem + K * SLOT);  // SPLIT: [mine][NT] maxima and sums, for the cluster
     if (tid == 0) {
         for (int i = 0; i < K; ++i) {
             mbar_init_cta(full + i, 1);
             mbar_init_cta(empty + i, WARPS);
         }
+        if constexpr (SPLIT) mbar_init_cta(&joined, S);
         lost = 0;
     }
-    __syncthreads();
+    if constexpr (SPLIT) cluster_barrier();
+    else __syncthreads();
     auto target = [&](int64_t row) -> int {  // -1: a row that takes no part
         if (row >= a.T) return -1;
         const int64_t y = a.y[row];
@@ -144,16 +176,16 @@ __global__ void __launch_bounds__(NT + 32, RES) k_policy(const PolicyArgs a)
         uint64_t keep, once;
         asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
         asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
-        int y_next = target(blockIdx.x);
-        for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
+        int y_next = target(row0);
+        for (int64_t row = row0; row < a.T; row += rows) {
             const int y = y_next;
-            y_next = target(row + gridDim.x);
+            y_next = target(row + rows);
             if (a.status != nullptr && lane == 0 && a.y[row] >= a.V) atomicCAS(a.status, GDN_OK, GDN_ERR_DEVICE_INPUT);
             if (y < 0) continue;
             const T* z = static_cast<const T*>(a.z) + row * a.ldz;
             const int s = misplaced(row);
             for (int t = 0; t < n + again; ++t) {
-                const int tile = t < n ? t : t - n;
+                const int tile = first + (t < n ? t : t - n);
                 const int len = min(TILE, a.V - tile * TILE);
                 const T* src = z + (int64_t)tile * TILE;
                 unsigned char* dst = policy_smem + slot * SLOT;
@@ -193,6 +225,10 @@ __global__ void __launch_bounds__(NT + 32, RES) k_policy(const PolicyArgs a)
         }
         // every copy has landed before the block ends, whether the walks wait for it or have given up
         for (int i = 0; i < K && mbar_wait_bounded(full + i, i < slot ? phase ^ 1 : phase, LIMIT); ++i) {}
+        if constexpr (SPLIT) {
+            __syncwarp();
+            cluster_barrier();
+        }
         return;
     }
 
@@ -209,21 +245,22 @@ __global__ void __launch_bounds__(NT + 32, RES) k_policy(const PolicyArgs a)
         if (++slot == K) slot = 0, phase ^= 1;
     };
     auto together = [] { asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory"); };  // the walking threads
-    int y_next = target(blockIdx.x);
-    for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
+    int y_next = target(row0);
+    for (int64_t row = row0; row < a.T; row += rows) {
         const int y = y_next;
-        y_next = target(row + gridDim.x);
+        y_next = target(row + rows);
         T* out = static_cast<T*>(a.dz) + row * a.V;
         if (y < 0) {  // nothing is read
-            if (tid == 0) {
+            if (tid == 0 && rank == 0) {
                 if (a.loss != nullptr) a.loss[row] = 0.0f;
                 if (a.lp != nullptr) a.lp[row] = 0.0f;
             }
             if constexpr (BWD) {
+                const int64_t begin = (int64_t)first * TILE, end = min((int64_t)last * TILE, (int64_t)a.V);
                 if constexpr (ALIGNED) {
-                    for (int i = tid; i < a.V / E; i += NT) reinterpret_cast<uint4*>(out)[i] = make_uint4(0, 0, 0, 0);
+                    for (int64_t i = begin / E + tid; i < end / E; i += NT) reinterpret_cast<uint4*>(out)[i] = make_uint4(0, 0, 0, 0);
                 } else {
-                    for (int i = tid; i < a.V; i += NT) out[i] = from_f<T>(0.0f);
+                    for (int64_t i = begin + tid; i < end; i += NT) out[i] = from_f<T>(0.0f);
                 }
             }
             continue;
@@ -232,6 +269,8 @@ __global__ void __launch_bounds__(NT + 32, RES) k_policy(const PolicyArgs a)
         const float old = a.old != nullptr ? a.old[row] : 0.0f, adv = a.old != nullptr ? a.adv[row] : 0.0f;
         const float ref = a.ref != nullptr ? a.ref[row] : 0.0f, dloss = BWD ? a.dloss[row] : 0.0f;
         const int s = misplaced(row);
+        // (the tile that holds it may be another block's, which may put the gradient in its place)
+        [[maybe_unused]] const float split_target = SPLIT ? to_f<T>((static_cast<const T*>(a.z) + row * a.ldz)[y]) : 0.0f;
         auto vec = [&](int i) {
             const uint4* p = reinterpret_cast<const uint4*>(policy_smem + slot * SLOT) + i;
             uint4 r = p[0];
@@ -239,10 +278,17 @@ __global__ void __launch_bounds__(NT + 32, RES) k_policy(const PolicyArgs a)
             return *reinterpret_cast<const Vec<T, E>*>(&r);
         };
         // ---- the first walk: running maximum (in units of log2) and sum
-        float m = -INFINITY, sum = 0.0f;
+        float m = -INFINITY, sum = 0.0f, before = -INFINITY, before_sum = 0.0f;
         const int slot0 = slot;
         const uint32_t phase0 = phase;
-        for (int t = 0; t < n; ++t) {
+        int part = part0, part_end = tiles * (part + 1) >> lg;
+        for (int t = first; t < last; ++t) {
+            if (t == part_end) {
+                if constexpr (SPLIT) found[(part - part0) * NT + tid] = make_float2(m, sum);
+                else policy_add(before, before_sum, m, sum);
+                m = -INFINITY, sum = 0.0f;
+                part_end = tiles * (++part + 1) >> lg;
+            }
             wait();
             auto add = [&](auto whole, int nvec) {
                 constexpr bool WHOLE = decltype(whole)::value;
@@ -273,13 +319,28 @@ __global__ void __launch_bounds__(NT + 32, RES) k_policy(const PolicyArgs a)
                 sum += psum(padd(s0, s1));
             };
             const int len = a.V - t * TILE;
-            if (tid == 0 && y - t * TILE >= 0 && y - t * TILE < TILE)
+            if (!SPLIT && tid == 0 && y - t * TILE >= 0 && y - t * TILE < TILE)
                 target_logit = to_f<T>(reinterpret_cast<const T*>(policy_smem + slot * SLOT + s)[y - t * TILE]);
             if (len >= TILE) add(std::true_type{}, 0);
             else add(std::false_type{}, (len + E - 1) / E);
-            if (t < n - stay) release(slot);
+            if (t - first < n - stay) release(slot);
             advance();
         }
+        if constexpr (SPLIT) {
+            found[(part - part0) * NT + tid] = make_float2(m, sum);
+            together();
+            if (tid < S && !lost) mbar_arrive_peer(peer_addr(&joined, tid));
+            if (!mbar_wait_cluster(&joined, 0, LIMIT)) lost = 1;  // (one row per cluster)
+            for (int p = 0; p < parts; ++p) {
+                float m1, sum1;
+                asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(m1), "=f"(sum1)
+                             : "r"(peer_addr(found + p % mine * NT + tid, p / mine)) : "memory");
+                policy_add(before, before_sum, m1, sum1);
+            }
+        } else {
+            policy_add(before, before_sum, m, sum);
+        }
+        m = before, sum = before_sum;
         policy_join<32>(m, sum);
         if (lane == 0) wm[warp] = m, ws[warp] = sum;
         together();
@@ -288,7 +349,7 @@ __global__ void __launch_bounds__(NT + 32, RES) k_policy(const PolicyArgs a)
         sum = lane < WARPS ? ws[lane] : 0.0f;
         policy_join<32>(m, sum);
         const float bm = policy_base(m);
-        const float lp = (__fmaf_rn(target_logit, a.c, -bm) - log2f(sum)) * 0.69314718055994530942f;
+        const float lp = (__fmaf_rn(SPLIT ? split_target : target_logit, a.c, -bm) - log2f(sum)) * 0.69314718055994530942f;
         float loss = 0.0f, d = 0.0f;
         if (a.old != nullptr) {
             const float ratio = ex2((lp - old) * kLog2e);
@@ -303,7 +364,7 @@ __global__ void __launch_bounds__(NT + 32, RES) k_policy(const PolicyArgs a)
                 d = __fmaf_rn(a.kl, 1.0f - e, d);
             }
         }
-        if (tid == 0 && !lost) {
+        if (tid == 0 && rank == 0 && !lost) {
             if (a.loss != nullptr) a.loss[row] = loss;
             if (a.lp != nullptr) a.lp[row] = lp;
         }
@@ -319,7 +380,7 @@ __global__ void __launch_bounds__(NT + 32, RES) k_policy(const PolicyArgs a)
             slot = slot0, phase = phase0;
             for (int i = 0; i < n - stay; ++i) advance();
             for (int t = 0; t < n; ++t) {
-                const int tile = t < stay ? n - stay + t : t - stay;
+                const int tile = t < stay ? last - stay + t : first + t - stay;
                 if (t == stay) slot = end_slot, phase = end_phase;
                 if (t >= stay) wait();
                 T* dst = out + (int64_t)tile * TILE;
@@ -391,6 +452,10 @@ __global__ void __launch_bounds__(NT + 32, RES) k_policy(const PolicyArgs a)
         }
     }
     if (lost && tid == 0 && a.status != nullptr) atomicCAS(a.status, GDN_OK, GDN_ERR_TIMEOUT);
+    if constexpr (SPLIT) {
+        __syncwarp();
+        cluster_barrier();  // no block ends while another reads it
+    }
 }
 
 }  // namespace gdn

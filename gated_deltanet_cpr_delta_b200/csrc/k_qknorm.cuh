@@ -7,12 +7,17 @@
 // and, with g = the gradient turned back and h = g w:
 //     dx = r (h - x r sum(h x) r / n),  dw = sum_rows g x r
 //
-// One read of x (and dy), one write, q and k in one launch; with few tokens several blocks share the heads of each.  A row (one head of one token) lies in the
-// registers of tpr neighbouring lanes, each with four pairs, so that a pair's two elements meet in one
-// thread and turn without an exchange.  A block takes `tokens` tokens at a time and
+// One read of x (and dy), one write, q and k in one launch; with few tokens several blocks share the heads of
+// each.  A row (one head of one token) lies in the registers of tpr neighbouring lanes, each with four pairs, so that a
+// pair's two elements meet in one thread and turn without an exchange.  A block takes `tokens` tokens at a time and
 // makes their angles once, for all heads, in shared memory: position times frequency in turns
 // and in 64 bits, so that far positions keep their angle (at 10^6 tokens fp32 is off by 0.06), with the whole turns
 // taken off before sincospi in fp32.
+//
+// Bound by the bytes, 4 (forward) and 6 (gradients) per bf16 element, and close behind by instructions: 164 warp
+// instructions per two rows of 128.  16384 tokens x (16 + 16) heads of 128 bf16 with rotation take 58 us (4.6 TB/s);
+// x (32 + 32) heads forward 112 and gradients 168 + 5 us (4.8 TB/s).  64 tokens x (32 + 32) take 6 us, 3001 x (7 + 3)
+// heads of 90 fp32 12 us: latency.
 #pragma once
 
 #include "layer_common.cuh"

@@ -131,6 +131,44 @@ def test_the_same_bits_in_every_place(dtype, V, shift):
             assert torch.equal(a[0], b[i])
 
 
+@pytest.mark.parametrize("dtype,V,shift", [("bf16", 65536, 0), ("bf16", 65537, 0), ("bf16", 131072, 3), ("bf16", 150001, 1), ("bf16", 262144, 0),
+                                           ("f32", 32768, 0), ("f32", 40003, 2), ("f32", 131071, 0), ("f32", 140000, 0)])
+def test_few_rows_share_the_blocks(dtype, V, shift):
+    """Rows cut over 8, 4, 2 and 1 blocks: the same bits, and the definition's values.  (The up to 8 joins of the
+    parts, 4 units each, stand for less than half of what the tolerance counts per tile and does not come up: 8 tiles and more,
+    each of 11 units in place of 21.)"""
+    t, R = TYPES[dtype], 280
+    c, z64, kw = case(t, 9, V)
+    c["y"][3] = -1
+    c["z"][4, V // 3:] = -float("inf")  # parts of nothing but masked logits
+    c["y"][4], c["y"][5], c["y"][6] = 5, 0, V - 1
+    z64 = n64(c["z"])
+    o = ops.policy(z64, c["y"].cpu().numpy(), tau=kw["temperature"])[1]
+    c["old"], c["ref"] = (torch.from_numpy(np.where(np.isfinite(o), o, 0) + d).float().cuda() for d in (0.05, -0.1))
+    wide = torch.full((R, V + shift), float("nan"), dtype=t, device="cuda")
+    view = wide[:, shift:shift + V]
+    view[:9].copy_(c["z"])
+    results = check(c, z64, kw, view[:9])
+    big = {k: v[:1].repeat((R,) + (1,) * (v.dim() - 1)) if v.dim() == 1 else view for k, v in c.items()}
+    for k in ("y", "old", "adv", "ref", "w"):
+        big[k][:9] = c[k]
+    view[9:].copy_(c["z"][:1].expand(R - 9, V))
+    for n in (1, 2, 9, 33, 64, 70, 129, R):
+        part = {k: v[:n] for k, v in big.items()}
+        args = dict(advantages=part["adv"], old_logprob=part["old"], ref_logprob=part["ref"], **kw)
+        loss, lp = gdn.gdn_policy_loss_forward(part["z"], part["y"], **args)
+        dz, loss2, lp2 = gdn.gdn_policy_loss_backward(part["z"], part["y"], part["w"], **args)
+        assert torch.equal(loss, loss2) and torch.equal(lp, lp2)
+        k = min(n, 9)
+        for got, want in zip((loss, lp, dz), results):
+            assert torch.equal(got[:k], want[:k]), n
+            assert n <= 9 or torch.equal(got[9:], want[:1].expand(got[9:].shape)), n
+        if shift == 0:
+            place = part["z"].clone()
+            gdn.gdn_policy_loss_backward(place, part["y"], part["w"], dlogits=place, **args)
+            assert torch.equal(place, dz), n
+
+
 @pytest.mark.parametrize("dtype", list(TYPES))
 def test_masked_logits_and_rows_that_are_not_finite(dtype):
     t, V, inf = TYPES[dtype], 5000, float("inf")
