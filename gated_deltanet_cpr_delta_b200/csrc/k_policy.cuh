@@ -11,9 +11,9 @@
 // ahead over the end of the walks and of the rows, so that memory does not wait for the two block-wide sums per row.
 // Bound by the bytes (the logits once, with their gradient twice) next to 2^x: one per logit, with the gradient two, which
 // alone would take 235 us of the 395 to 400 us for 4096 x 131072 bf16 (5.4 TB/s; the special-function unit at 16 per cycle
-// and SM).  777 x 50021 fp32, losses alone: 35 us (4.4 TB/s).  64 x 131072 bf16, log-probabilities: 12 us, one row per
-// block on 64 of the SMs.
-// (Rows cut over a cluster of up to 8 blocks, wholly in shared memory, waited for each other: 495 us at
+// and SM).  777 x 50021 fp32, losses alone: 34 us (4.6 TB/s).  Log-probabilities of 64 x 131072 bf16 take 10 us, of one
+// row 8: latency.
+// (Many rows cut over clusters of up to 8 blocks, wholly in shared memory, waited for each other: 495 us at
 // 4096 x 131072 bf16, whether with the cluster's barrier or with exchanges a row ahead.)
 //
 // Where there are few rows, a cluster of blocks shares each (64 x 131072: 4): a block walks its part of the tiles, then all
@@ -112,9 +112,10 @@ __host__ __device__ constexpr int policy_slot_bytes(int NT) { return policy_tile
 // Tiles in the ring with so many blocks per SM; all but two of them stay for the second walk.
 __host__ __device__ constexpr int policy_slots(int resident) { return resident == 2 ? 6 : 4; }
 
-// Parts of a row of n tiles: a power of two (its logarithm), of at least 4 tiles each
+// Parts of a row of n tiles: a power of two (its logarithm), of at least 4 tiles each, or 2 where there are two parts.  (Parts of
+// 2 tiles throughout: 64 x 131072 bf16 10.9 us in place of 9.9, 1 x 131072 7.6 and 7.8; 32 x 50021, 7 tiles, 7.6 and 9.1.)
 constexpr int kPolicyParts = 8;
-__host__ __device__ constexpr int policy_parts_log(int n) { return n >= 32 ? 3 : n >= 16 ? 2 : n >= 8 ? 1 : 0; }
+__host__ __device__ constexpr int policy_parts_log(int n) { return n >= 32 ? 3 : n >= 16 ? 2 : n >= 4 ? 1 : 0; }
 
 // The maximum and sum of what lies behind, joined to those of what lies before
 __device__ __forceinline__ void policy_add(float& m, float& sum, float m1, float sum1)
