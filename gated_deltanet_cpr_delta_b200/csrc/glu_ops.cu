@@ -173,7 +173,7 @@ gdn_status_t glu_few(const GluOperands& o, const gdn_glu_t& s, gdn::GluFewArgs& 
 
 // The backward's workspace: dg and du, rows ld apart; aligned copies; the splits' partial products.
 struct GluBackwardPlan {
-    int64_t ld;
+    int64_t ld, grad_rows;  // rows of dg and du: with those of what their rounding left, twice the tokens
     int splits_x, splits_w;
     size_t copies, part, bytes;  // offsets
 };
@@ -182,16 +182,25 @@ GluBackwardPlan glu_backward_plan(const gdn_glu_t& s, int sms)
 {
     GluBackwardPlan p;
     p.ld = pad8(s.inner);
+    p.grad_rows = s.rows <= 128 ? 2 * s.rows : s.rows;
     const int64_t tx = ceil_div(s.rows, 256) * ceil_div(s.width, 256);
     const int64_t tw = 2 * ceil_div(s.inner, 256) * ceil_div(s.width, 256);
     p.splits_x = s.rows > 0 ? glu_splits(tx, 2 * ceil_div(s.inner, kStageK), sms) : 1;
     p.splits_w = s.rows > 0 ? glu_splits(tw, ceil_div(s.rows, kStageK), sms) : 1;
-    p.copies = 2 * align_up((size_t)s.rows * p.ld * 2);
+    p.copies = 2 * align_up((size_t)p.grad_rows * p.ld * 2);
     p.part = p.copies + glu_operands(s, nullptr).bytes;
-    const size_t px = p.splits_x > 1 ? sizeof(float) * (size_t)p.splits_x * s.rows * s.width : 0;
+    const bool joined = p.splits_x > 1 || p.grad_rows > s.rows;
+    const size_t px = joined ? sizeof(float) * (size_t)p.splits_x * p.grad_rows * s.width : 0;
     const size_t pw = p.splits_w > 1 ? sizeof(float) * 2 * (size_t)p.splits_w * s.inner * s.width : 0;
     p.bytes = p.part + align_up(std::max(px, pw));
     return p;
+}
+
+template <bool LO>
+auto glu_grad(int32_t act, bool whole)
+{
+    return act == GDN_ACT_SILU ? (whole ? gdn::k_glu_grad<true, gdn::kGluSilu, LO> : gdn::k_glu_grad<false, gdn::kGluSilu, LO>)
+                               : (whole ? gdn::k_glu_grad<true, gdn::kGluGelu, LO> : gdn::k_glu_grad<false, gdn::kGluGelu, LO>);
 }
 
 template <typename OT>
@@ -309,26 +318,28 @@ gdn_status_t gdn_glu_backward(const gdn_glu_t* args, const void* dh, int64_t dh_
     const unsigned blocks = (unsigned)std::min<int64_t>(ceil_div(R * (p.ld / 8), 256), (int64_t)sms * 32);
     const uint16_t *g = static_cast<const uint16_t*>(dh), *sv = static_cast<const uint16_t*>(saved);
     const bool whole = F % 8 == 0 && wide(dh, dh_stride, F, s.in_dtype);
-    auto k = s.act == GDN_ACT_SILU ? (whole ? gdn::k_glu_grad<true, gdn::kGluSilu> : gdn::k_glu_grad<false, gdn::kGluSilu>)
-                                   : (whole ? gdn::k_glu_grad<true, gdn::kGluGelu> : gdn::k_glu_grad<false, gdn::kGluGelu>);
+    const bool few = p.grad_rows > R;
+    auto k = few ? glu_grad<true>(s.act, whole) : glu_grad<false>(s.act, whole);
     k<<<blocks, 256, 0, st>>>(g, dh_stride, sv, R, F, dg, du, p.ld);
     if (!launched()) return GDN_ERR_CUDA;
 
     gdn::GluMaps mx, mw;
     const bool wide_boxes = D % 64 == 0 && F % 64 == 0;
-    if (!operand_map(&mx.a[0], dg, R, F, p.ld, wide_boxes) || !operand_map(&mx.a[1], du, R, F, p.ld, wide_boxes) ||
+    if (!operand_map(&mx.a[0], dg, p.grad_rows, F, p.ld, wide_boxes) || !operand_map(&mx.a[1], du, p.grad_rows, F, p.ld, wide_boxes) ||
         !operand_map(&mx.b[0], o.wg, F, D, o.ldg, wide_boxes) || !operand_map(&mx.b[1], o.wu, F, D, o.ldu, wide_boxes) ||
         !operand_map(&mw.b[0], o.x, R, D, o.ldx, wide_boxes))
         return GDN_ERR_CUDA;
     mw.a[0] = mx.a[0]; mw.a[1] = mx.a[1]; mw.b[1] = mw.b[0];
     gdn::GluGemmArgs a{};
     a.wide = wide_boxes;
-    a.M = R; a.N = D; a.ksteps = (int32_t)ceil_div(F, kStageK); a.parts = 2; a.problems = 1; a.splits = p.splits_x;
-    a.out[0] = dx; a.partial = part; a.status = status;
+    a.M = p.grad_rows; a.N = D; a.ksteps = (int32_t)ceil_div(F, kStageK); a.parts = 2; a.problems = 1; a.splits = p.splits_x;
+    const int sums = few ? 2 * p.splits_x : p.splits_x;  // [splits][grad_rows][D]
+    a.out[0] = dx; a.partial = sums > 1 ? part : nullptr; a.status = status;
     gdn_status_t r = glu_gemm<gdn::kGluDx>(mx, a, sms, st);
     if (r != GDN_OK) return r;
-    if (p.splits_x > 1 && !glu_join<bf16>(part, p.splits_x, R * D, dx, nullptr, 1, st)) return GDN_ERR_CUDA;
-    a.M = F; a.N = D; a.ksteps = (int32_t)ceil_div(R, kStageK); a.parts = 1; a.problems = 2; a.splits = p.splits_w;
+    if (sums > 1 && !glu_join<bf16>(part, sums, R * D, dx, nullptr, 1, st)) return GDN_ERR_CUDA;
+    a.M = F; a.N = D; a.ksteps = (int32_t)ceil_div(R, kStageK); a.parts = few ? 2 : 1; a.problems = 2; a.splits = p.splits_w;
+    a.lo = (int32_t)R; a.partial = p.splits_w > 1 ? part : nullptr;
     a.out[0] = dw_gate; a.out[1] = dw_up; a.out_f32 = dw_dtype == GDN_F32;
     r = glu_gemm<gdn::kGluDw>(mw, a, sms, st);
     if (r != GDN_OK) return r;

@@ -14,6 +14,10 @@
 //             accumulator holds g and u of the same 128 units, so act(g) u is made where it is read
 //   dx        A = dg, then du; B = Wg, then Wu, with the output's columns contiguous (read as K x N)
 //   dW        A = dg or du as K x M, B = x as K x N; the two gradients are the two halves of the tiles
+// dg and du are rounded to bf16, which adds to the gradients about what the rounding of a bf16 result adds, where sums
+// of many tokens and units level it out.  Up to 128 tokens, where a few of them can dominate, what the rounding left
+// goes through the products as well, in room that the tiles have anyway: as more rows of dx, joined with
+// the splits of K, and as more rows of K for dW.
 //
 // k_glu_few serves few tokens, where the weights' bytes bound it: a block holds up to 64 rows of Wg and the same ones of Wu
 // as the M side of one product, as many as give every SM the same share of them, and streams them past the
@@ -169,12 +173,13 @@ struct GluGemmArgs {
     int64_t M, N;        // of the output (forward: tokens and units)
     int32_t ksteps;      // stages of one part of K
     int32_t wide;        // the maps' boxes are whole operands of a stage: rows of whole 64 columns
-    int32_t parts;       // dx: 2 (dg, then du)
+    int32_t parts;       // dx: 2 (dg, then du); dW of few tokens: 2 (dg or du, then what its rounding left, `lo` rows on)
+    int32_t lo;
     int32_t tiles_m, tiles_n, problems, splits;
     int64_t tiles;       // tiles_m tiles_n problems splits
     void* out[2];
     uint16_t* saved;     // forward: planes [3][M][N], or null
-    float* partial;      // splits > 1: [problems][splits][M][N]
+    float* partial;      // [problems][splits][M][N], to be joined, or null
     int32_t out_f32;
     int32_t* status;
 };
@@ -315,7 +320,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGluGemmThreads, 1)
                     const int part = k / a.ksteps, kk = (k - part * a.ksteps) * 2 * kGluK;
                     const uint32_t bar = peer_addr(full + s, 0);
                     if (rank == 0) mbar_arrive_expect_tx(full + s, 4 * kGluOperand);
-                    auto fetch = [&](unsigned char* to, const CUtensorMap* map, bool kmajor, int row) {
+                    auto fetch = [&](unsigned char* to, const CUtensorMap* map, bool kmajor, int row, int kk) {
                         if (a.wide) {
                             tma_pair_3d(to, map, kmajor ? row : kk, (kmajor ? kk : row) / 64, bar);
                         } else {
@@ -325,8 +330,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGluGemmThreads, 1)
                         }
                     };
                     const int half = (int)rank * 128;
-                    fetch(sa, &maps.a[MODE == kGluFwd ? 0 : MODE == kGluDx ? part : t.problem], AK, (int)t.m + half);
-                    fetch(sb, &maps.b[MODE == kGluFwd ? rank : MODE == kGluDx ? part : 0], BK, (int)t.n + (MODE == kGluFwd ? 0 : half));
+                    fetch(sa, &maps.a[MODE == kGluFwd ? 0 : MODE == kGluDx ? part : t.problem], AK, (int)t.m + half,
+                          MODE == kGluDw ? kk + part * a.lo : kk);
+                    fetch(sb, &maps.b[MODE == kGluFwd ? rank : MODE == kGluDx ? part : 0], BK, (int)t.n + (MODE == kGluFwd ? 0 : half), kk);
                     if (++s == ST) s = 0, ph ^= 1;
                 }
             }
@@ -444,7 +450,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGluGemmThreads, 1)
             } else {
                 void* to = t.problem ? a.out[1] : a.out[0];
                 float* part = a.partial + ((int64_t)t.problem * a.splits + t.split) * a.M * a.N;
-                const bool narrow = a.splits == 1 && !a.out_f32;
+                const bool joined = a.partial != nullptr, narrow = !joined && !a.out_f32;
                 for (int c0 = half * 128; c0 < half * 128 + 128 && t.n + c0 < a.N; c0 += 32) {
                     float x[2][16];
                     tmem_ld16(col + c0, x[0]);
@@ -466,7 +472,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGluGemmThreads, 1)
 #pragma unroll
                             for (int p = 0; p < 4; ++p) *glu_piece(st, lane, p) = reinterpret_cast<const uint4*>(x[i])[p];
                             __syncwarp();
-                            if (t.n + c0 + 16 * i < a.N) out(st, a.splits > 1 ? static_cast<void*>(part) : to, t.n + c0 + 16 * i, 4);
+                            if (t.n + c0 + 16 * i < a.N) out(st, joined ? static_cast<void*>(part) : to, t.n + c0 + 16 * i, 4);
                             __syncwarp();
                         }
                     }
@@ -672,8 +678,9 @@ __device__ __forceinline__ uint4 glu_load8(const uint16_t* p, const uint16_t* ba
 }
 
 // dg and du, rows ld (a multiple of 8) apart, from dh and what the forward saved; columns from F on are read by nobody.
+// LO: what their rounding to bf16 leaves goes into T more rows behind.
 // WHOLE: every row of dh and of the planes is whole 16-byte vectors (121 us at 8192 x 8192, the copy rate; else 131).
-template <bool WHOLE, int ACT>
+template <bool WHOLE, int ACT, bool LO>
 __global__ void __launch_bounds__(256) k_glu_grad(const uint16_t* __restrict__ dh, int64_t lddh,
                                                   const uint16_t* __restrict__ saved, int64_t T, int64_t F,
                                                   __nv_bfloat16* __restrict__ dg, __nv_bfloat16* __restrict__ du, int64_t ld)
@@ -703,6 +710,16 @@ __global__ void __launch_bounds__(256) k_glu_grad(const uint16_t* __restrict__ d
         }
         store_vec<__nv_bfloat16, 8>(dg + t * ld + c, x);
         store_vec<__nv_bfloat16, 8>(du + t * ld + c, y);
+        if constexpr (LO) {
+            auto left_over = [](float v) {
+                const float r = to_f<__nv_bfloat16>(__float2bfloat16_rn(v));
+                return isfinite(r) ? v - r : 0.0f;
+            };
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = left_over(x[k]), y[k] = left_over(y[k]);
+            store_vec<__nv_bfloat16, 8>(dg + (T + t) * ld + c, x);
+            store_vec<__nv_bfloat16, 8>(du + (T + t) * ld + c, y);
+        }
     }
 }
 

@@ -497,9 +497,13 @@ def _opt(what: str, name: str, t: Optional[torch.Tensor], dtype: torch.dtype, sh
 def _out(what: str, name: str, t: Optional[torch.Tensor], dtype: torch.dtype, shape, dev: int, like=None):
     """(tensor, address) of an output: the caller's, or a new one (``like``: a tensor of its type and shape)."""
     if t is None:
-        # empty_like takes half the time of empty with a type and a device
-        t = torch.empty_like(like) if like is not None and like.is_contiguous() else \
-            torch.empty(shape, dtype=dtype, device=dev)
+        # empty_like takes half the time of empty with a type and a device; views of a wider tensor come out dense, but for
+        # unusual orders of their axes
+        if like is not None:
+            t = torch.empty_like(like)
+            if t.is_contiguous():
+                return t, t.data_ptr()
+        t = torch.empty(shape, dtype=dtype, device=dev)
         return t, t.data_ptr()
     return t, _dense(what, name, t, dtype, shape, dev)
 
@@ -865,11 +869,8 @@ def gdn_qk_norm_forward(q, k, *, q_weight=None, k_weight=None, positions=None, i
     what = "gdn_qk_norm_forward"
     dev = _gpu(what, q)
     s = _qk_struct(what, q, k, q_weight, k_weight, positions, inv_freq, interleaved, l2, eps, dev)
-    if q_out is None:
-        q_out = q.new_empty(q.shape)
-    if k_out is None:
-        k_out = k.new_empty(k.shape)
-    pq, pk = _dense(what, "q_out", q_out, q.dtype, q.shape, dev), _dense(what, "k_out", k_out, q.dtype, k.shape, dev)
+    q_out, pq = _out(what, "q_out", q_out, q.dtype, q.shape, dev, q)
+    k_out, pk = _out(what, "k_out", k_out, q.dtype, k.shape, dev, k)
     _call(dev, what, load_library().gdn_qk_norm_forward, s, pq, pk)
     return q_out, k_out
 
@@ -895,15 +896,16 @@ def gdn_qk_norm_backward(q, k, dq_out, dk_out, *, q_weight=None, k_weight=None, 
             dqw = torch.empty((d,), dtype=_F32, device=dev)
         elif k_weight is not None:
             dkw = torch.empty((d,), dtype=_F32, device=dev)
-        grads = (q.new_empty(q.shape), k.new_empty(k.shape), dqw, dkw)
+        grads = (None, None, dqw, dkw)
     dq, dk, dqw, dkw = grads
+    dq, pdq = _out(what, "dq", dq, ty, q.shape, dev, q)
+    dk, pdk = _out(what, "dk", dk, ty, k.shape, dev, k)
     keep, ws, nbytes = None, None, 0
     if dqw is not None or dkw is not None:
         keep, ws, nbytes = _scratch(what, workspace, _scratch_size("gdn_qk_norm_backward_workspace_size", T, d), dev)
-    _call(dev, what, load_library().gdn_qk_norm_backward, s, pgq, lgq, pgk, lgk, _dense(what, "dq", dq, ty, q.shape, dev),
-          _dense(what, "dk", dk, ty, k.shape, dev), _opt(what, "dq_weight", dqw, _F32, (d,), dev),
+    _call(dev, what, load_library().gdn_qk_norm_backward, s, pgq, lgq, pgk, lgk, pdq, pdk, _opt(what, "dq_weight", dqw, _F32, (d,), dev),
           _opt(what, "dk_weight", dkw, _F32, (d,), dev), ws, nbytes)
-    return grads
+    return dq, dk, dqw, dkw
 
 
 #: gdn_glu_t.act
@@ -972,17 +974,16 @@ def gdn_glu_backward(x, w_gate, w_up, dh, saved, *, act: str = "silu", workspace
     if dh.shape != x.shape[:-1] + (F,):
         raise ValueError(f"{what}: dh must have shape {tuple(x.shape[:-1]) + (F,)}, not {tuple(dh.shape)}")
     pd, ld = _rows(what, "dh", _rows2d(what, "dh", dh), ty, (R, F), dev)
-    if grads is None:
-        grads = tuple(x.new_empty(n) for n in (x.shape, (F, D), (F, D)))
-    dx, dwg, dwu = grads
-    wt = dwg.dtype
+    dx, dwg, dwu = grads if grads is not None else (None, None, None)
+    wt = ty if dwg is None else dwg.dtype
+    dx, pdx = _out(what, "dx", dx, ty, x.shape, dev, x)
+    dwg, pdg = _out(what, "dw_gate", dwg, wt, (F, D), dev, w_gate)
+    dwu, pdu = _out(what, "dw_up", dwu, wt, (F, D), dev, w_up)
     lib = load_library()
     keep, ws, nbytes = _glu_scratch(what, workspace, lib.gdn_glu_backward_workspace_size, s, dev)
     _call(dev, what, lib.gdn_glu_backward, s, pd, ld, _dense(what, "saved", saved, torch.uint8, (6 * R * F,), dev),
-          _dense(what, "dx", dx, ty, x.shape, dev), _dense(what, "dw_gate", dwg, wt, (F, D), dev),
-          _dense(what, "dw_up", dwu, wt, (F, D), dev), _type(what, dwg), ws, nbytes,
-          _opt(what, "status", status, torch.int32, (1,), dev))
-    return grads
+          pdx, pdg, pdu, _type(what, dwg), ws, nbytes, _opt(what, "status", status, torch.int32, (1,), dev))
+    return dx, dwg, dwu
 
 
 def _policy_struct(what, logits, targets, old_logprob, advantages, ref_logprob, clip_low, clip_high, kl_coef, temperature, dev):
@@ -1016,10 +1017,12 @@ def gdn_policy_loss_forward(logits, targets, *, old_logprob=None, advantages=Non
     dev = _gpu(what, logits)
     s = _policy_struct(what, logits, targets, old_logprob, advantages, ref_logprob, clip_low, clip_high, kl_coef, temperature, dev)
     shape = (s.rows,)
-    logprob, pl = _out(what, "logprob", logprob, _F32, shape, dev)
+    if logprob is None and old_logprob is None:
+        logprob = torch.empty_like(targets, dtype=_F32)
+    logprob, pl = _out(what, "logprob", logprob, _F32, shape, dev, old_logprob)
     po = None
     if old_logprob is not None:
-        loss, po = _out(what, "loss", loss, _F32, shape, dev)
+        loss, po = _out(what, "loss", loss, _F32, shape, dev, old_logprob)
     elif loss is not None:
         raise ValueError(f"{what}: a loss needs old_logprob and advantages")
     _call(dev, what, load_library().gdn_policy_loss_forward, s, po, pl, _opt(what, "status", status, torch.int32, (1,), dev))
@@ -1039,8 +1042,8 @@ def gdn_policy_loss_backward(logits, targets, dloss, *, old_logprob, advantages,
     s = _policy_struct(what, logits, targets, old_logprob, advantages, ref_logprob, clip_low, clip_high, kl_coef, temperature, dev)
     shape = (s.rows,)
     dlogits, pd = _out(what, "dlogits", dlogits, logits.dtype, logits.shape, dev, logits)
-    loss, po = _out(what, "loss", loss, _F32, shape, dev)
-    logprob, pl = _out(what, "logprob", logprob, _F32, shape, dev)
+    loss, po = _out(what, "loss", loss, _F32, shape, dev, old_logprob)
+    logprob, pl = _out(what, "logprob", logprob, _F32, shape, dev, old_logprob)
     _call(dev, what, load_library().gdn_policy_loss_backward, s, _dense(what, "dloss", dloss, _F32, shape, dev), pd, po, pl,
           _opt(what, "status", status, torch.int32, (1,), dev))
     return dlogits, loss, logprob
