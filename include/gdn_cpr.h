@@ -670,8 +670,8 @@ gdn_status_t gdn_glu_forward(const gdn_glu_t* args, void* h, void* saved, void* 
  * Gradients of sum(dh h): dx [rows, width] in in_dtype, dw_gate and dw_up [inner, width] in dw_dtype (bf16 or
  * fp32), all dense.  dh [rows, inner] in in_dtype, rows dh_stride apart; saved: as the forward of these
  * inputs wrote it.  The gradients of the two projections are rounded to bf16, as the tensor cores'
- * operands.  The workspace's size (at least 4 rows inner bytes) depends on the addresses' alignment and the
- * current device.
+ * operands; for up to 128 rows to two bf16 terms (16 bits).  The workspace's size (at least 4 rows inner bytes)
+ * depends on the addresses' alignment and the current device.
  */
 size_t gdn_glu_backward_workspace_size(const gdn_glu_t* args);
 gdn_status_t gdn_glu_backward(const gdn_glu_t* args, const void* dh, int64_t dh_stride, const void* saved, void* dx,
