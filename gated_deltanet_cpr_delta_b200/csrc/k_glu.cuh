@@ -24,8 +24,8 @@
 // tokens (the N side, 16 to 256).  Where that would leave few rows, a cluster of blocks shares the K axis,
 // and its partial sums meet in distributed shared memory, in a fixed order.
 //
-// Bound by the tensor cores: 8192 x 4096 x 8192 takes the forward 674 us (1631 TFLOP/s; 720 with what the backward reads), dx
-// 682 (1612) and the weights' gradients 712 us (1544); a second under load, with the clock held down by the power limit, about
+// Bound by the tensor cores: 8192 x 4096 x 8192 takes the forward 655 us (1679 TFLOP/s; 708 with what the backward reads), dx
+// 680 (1617) and the weights' gradients 712 us (1544); a second under load, with the clock held down by the power limit, about
 // 1300.  k_glu_grad between them 123 us.  64 x 4096 x 8192 takes k_glu_few 27 us, 1 x 2048 x 8192 15 us (5.0 and 4.5 TB/s).
 #pragma once
 
@@ -190,7 +190,7 @@ struct GluTile {
 };
 
 // A stage holds 128 k of either operand.  The larger the boxes that fetch it the better: 8192 x 4096 x 8192 takes the
-// forward 792 us with boxes of 8 KB, 705 with 16 KB and 674 with 32 KB, the weights' gradients 829, 735 and 712.
+// forward 792 us with boxes of 8 KB, 705 with 16 KB and 674 with 32 KB (655 since), the weights' gradients 829, 735 and 712.
 constexpr uint32_t kGluHalf = 128 * kGluK * 2;     // 128 rows by 64 k, or 64 columns by 128 k
 constexpr uint32_t kGluOperand = 2 * kGluHalf;     // bytes of one operand of one CTA in a stage
 constexpr int kGluStages = 3;
@@ -202,7 +202,9 @@ __host__ __device__ constexpr size_t glu_gemm_smem(bool save)
     return (size_t)kGluStages * 2 * kGluOperand + glu_staging(save) + 1024 + 256;
 }
 
-// Tiles in groups of 8 rows of tiles, down the rows first: what is on the chip at a time shares few rows and columns.
+// Tiles in groups of 8 or 16 rows of tiles, down the rows first: what is on the chip at a time shares few rows and columns.
+// The forward by 16: 16384 x 2048 x 8192 takes 668 us and by 8 688 (8192 x 4096 x 8192: 655 and 673; only few K with what the
+// backward reads lose, 32768 x 1024 x 2048 218 and 213); dx of the first 687 and 679, the weights' gradients 716 and 712.
 template <int MODE>
 __device__ __forceinline__ GluTile glu_tile(const GluGemmArgs& a, int64_t id)
 {
@@ -212,10 +214,11 @@ __device__ __forceinline__ GluTile glu_tile(const GluGemmArgs& a, int64_t id)
     int64_t i = id - ps * per;
     t.problem = (int)(ps / a.splits);
     t.split = (int)(ps - (int64_t)t.problem * a.splits);
-    const int64_t group = i / (8 * (int64_t)a.tiles_n);
-    const int64_t rows = min((int64_t)8, a.tiles_m - group * 8);
-    i -= group * 8 * a.tiles_n;
-    t.m = (group * 8 + i % rows) * 256;
+    constexpr int64_t GROUP = MODE == kGluFwd ? 16 : 8;
+    const int64_t group = i / (GROUP * a.tiles_n);
+    const int64_t rows = min(GROUP, a.tiles_m - group * GROUP);
+    i -= group * GROUP * a.tiles_n;
+    t.m = (group * GROUP + i % rows) * 256;
     t.n = (i / rows) * (MODE == kGluFwd ? 128 : 256);
     const int64_t all = (int64_t)a.ksteps * a.parts;
     t.k0 = (int)(all * t.split / a.splits);
