@@ -216,3 +216,18 @@ def test_fp32_is_refused():
     with pytest.raises(gdn.GdnError) as e:
         gdn.gdn_glu_forward(x, x, x)
     assert e.value.status == gdn.GDN_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("T,D,F,shift", [(1, 1003, 777, 0), (5, 64, 100, 1), (16, 257, 2000, 0), (17, 510, 300, 3), (33, 1, 9, 0), (64, 4097, 72, 0),
+                                         (64, 2048, 640, 5), (3, 8, 8, 7), (4, 63, 20000, 0), (40, 127, 10000, 0), (9, 8190, 64, 0)])
+def test_few_tokens_of_rows_that_start_anywhere(T, D, F, shift):
+    """Neighbours of the operands' rows that are not numbers do not reach the results."""
+    c = case(T, D, F)
+    views = {}
+    for n in ("x", "wg", "wu"):
+        rows = c[n][0].shape[0]
+        wide = torch.full((rows * (D + shift) + 2 * shift,), float("nan"), dtype=BF, device="cuda")
+        views[n] = wide[shift:shift + rows * (D + shift)].view(rows, D + shift)[:, :D]
+        views[n].copy_(c[n][0])
+    one, two = check(c, views=views, backward=T <= 17), check(c, backward=T <= 17)
+    assert torch.equal(one[0], two[0])
