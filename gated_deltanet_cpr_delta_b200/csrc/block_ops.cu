@@ -278,9 +278,8 @@ gdn_status_t gdn_qk_norm_backward(const gdn_qk_norm_t* args, const void* dq_out,
     }
     if (!weights) return GDN_OK;
     const int64_t M = 2 * (int64_t)s.head_dim;
-    gdn::k_colsum<<<(unsigned)ceil_div(M, 32), dim3(32, 8), 0, st>>>(part, parts, M,
-                                                                     gdn::QkGradMap{dq_weight, dk_weight, s.head_dim});
-    return launched() ? GDN_OK : GDN_ERR_CUDA;
+    return launch_next(gdn::k_colsum<gdn::QkGradMap>, dim3((unsigned)ceil_div(M, 32)), dim3(32, 8), 0, 0, st, part, parts, M,
+                       gdn::QkGradMap{dq_weight, dk_weight, s.head_dim}) ? GDN_OK : GDN_ERR_CUDA;
 }
 
 gdn_status_t gdn_policy_loss_forward(const gdn_policy_t* args, float* loss, float* logprob, int32_t* status, void* stream)

@@ -101,8 +101,7 @@ gdn_status_t glu_gemm(gdn::GluMaps& maps, gdn::GluGemmArgs& a, int sms, cudaStre
     constexpr size_t smem = gdn::glu_gemm_smem(SAVE);
     if (!raise_smem(k, smem)) return GDN_ERR_CUDA;
     const unsigned pairs = (unsigned)std::min<int64_t>(a.tiles, std::max(1, sms / 2));
-    k<<<2 * pairs, gdn::kGluGemmThreads, smem, st>>>(maps, a);
-    return launched() ? GDN_OK : GDN_ERR_CUDA;
+    return launch_next(k, dim3(2 * pairs), dim3(gdn::kGluGemmThreads), smem, 0, st, maps, a) ? GDN_OK : GDN_ERR_CUDA;
 }
 
 // Whether the weights are streamed past the tokens: up to 256 tokens, and where the pairs of SMs would have at most 16 tiles
@@ -157,18 +156,8 @@ gdn_status_t glu_few(const GluOperands& o, const gdn_glu_t& s, gdn::GluFewArgs& 
         return GDN_ERR_CUDA;
     auto k = s.act == GDN_ACT_SILU ? gdn::k_glu_few<NB, gdn::kGluSilu> : gdn::k_glu_few<NB, gdn::kGluGelu>;
     if (!raise_smem(k, smem)) return GDN_ERR_CUDA;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)ceil_div(s.inner, a.rows) * S, (unsigned)ceil_div(s.rows, NB));
-    cfg.blockDim = dim3(gdn::kGluThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)S;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k, maps, a) == cudaSuccess && launched() ? GDN_OK : GDN_ERR_CUDA;
+    const dim3 grid((unsigned)ceil_div(s.inner, a.rows) * S, (unsigned)ceil_div(s.rows, NB));
+    return launch_next(k, grid, dim3(gdn::kGluThreads), smem, S, st, maps, a) ? GDN_OK : GDN_ERR_CUDA;
 }
 
 // The backward's workspace: dg and du, rows ld apart; aligned copies; the splits' partial products.
@@ -206,9 +195,8 @@ auto glu_grad(int32_t act, bool whole)
 template <typename OT>
 bool glu_join(const float* part, int splits, int64_t n, void* o0, void* o1, int problems, cudaStream_t st)
 {
-    gdn::k_glu_join<OT><<<(unsigned)std::min<int64_t>(ceil_div(n * problems, 256), 148 * 16), 256, 0, st>>>(
-        part, splits, n, static_cast<OT*>(o0), static_cast<OT*>(o1), problems);
-    return launched();
+    return launch_next(gdn::k_glu_join<OT>, dim3((unsigned)std::min<int64_t>(ceil_div(n * problems, 256), 148 * 16)), dim3(256), 0, 0, st,
+                       part, splits, n, static_cast<OT*>(o0), static_cast<OT*>(o1), problems);
 }
 
 }  // namespace
@@ -320,8 +308,7 @@ gdn_status_t gdn_glu_backward(const gdn_glu_t* args, const void* dh, int64_t dh_
     const bool whole = F % 8 == 0 && wide(dh, dh_stride, F, s.in_dtype);
     const bool few = p.grad_rows > R;
     auto k = few ? glu_grad<true>(s.act, whole) : glu_grad<false>(s.act, whole);
-    k<<<blocks, 256, 0, st>>>(g, dh_stride, sv, R, F, dg, du, p.ld);
-    if (!launched()) return GDN_ERR_CUDA;
+    if (!launch_next(k, dim3(blocks), dim3(256), 0, 0, st, g, dh_stride, sv, R, F, dg, du, p.ld)) return GDN_ERR_CUDA;
 
     gdn::GluMaps mx, mw;
     const bool wide_boxes = D % 64 == 0 && F % 64 == 0;

@@ -305,6 +305,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGluGemmThreads, 1)
     tc_fence_before();
     cluster_barrier();
     tc_fence_after();
+    let_next_start();
+    after_previous();
     const uint32_t tmem = *slot;
     const int64_t step = gridDim.x / 2, first = blockIdx.x / 2;
     bool ok = true;
@@ -552,6 +554,8 @@ __global__ void __launch_bounds__(kGluThreads, 1) k_glu_few(const __grid_constan
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    let_next_start();
+    after_previous();
     const uint32_t tmem = *slot;
     bool ok = true;
     if (warp == 0 || warp == 2 || warp == 3) {
@@ -688,6 +692,8 @@ __global__ void __launch_bounds__(256) k_glu_grad(const uint16_t* __restrict__ d
                                                   const uint16_t* __restrict__ saved, int64_t T, int64_t F,
                                                   __nv_bfloat16* __restrict__ dg, __nv_bfloat16* __restrict__ du, int64_t ld)
 {
+    let_next_start();
+    after_previous();
     const int64_t per = ld / 8, n = T * per, plane = T * F;
     const uint16_t *dend = dh + (T - 1) * lddh + F, *send = saved + 3 * plane;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
@@ -735,6 +741,7 @@ struct GluAlign {
 };
 __global__ void __launch_bounds__(256) k_glu_align(const GluAlign a)
 {
+    let_next_start();
     const int m = blockIdx.y;
     const uint16_t* src = m == 0 ? a.src[0] : m == 1 ? a.src[1] : a.src[2];
     uint16_t* dst = m == 0 ? a.dst[0] : m == 1 ? a.dst[1] : a.dst[2];
@@ -752,6 +759,8 @@ template <typename OT>
 __global__ void __launch_bounds__(256) k_glu_join(const float* __restrict__ part, int splits, int64_t n, OT* __restrict__ out0,
                                                   OT* __restrict__ out1, int problems)
 {
+    let_next_start();
+    after_previous();
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n * problems; i += (int64_t)gridDim.x * 256) {
         const int64_t p = i / n, e = i - p * n;
         const float* s = part + p * splits * n + e;

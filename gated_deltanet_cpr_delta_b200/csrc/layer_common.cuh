@@ -325,6 +325,11 @@ __device__ __forceinline__ float softplus(float v)
     return __fmaf_rn(p, e, fmaxf(v, 0.0f));
 }
 
+// A kernel that starts while the one before it in the stream still runs (launch_next) waits here, before it reads or writes
+// memory; the one before it lets it start from here on.
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // The 16 bytes that start s bytes into the 32 bytes a, b (s below 16).
 __device__ __forceinline__ uint4 bytes_at(const uint4& a, const uint4& b, int s)
 {
@@ -345,6 +350,7 @@ __device__ __forceinline__ uint4 bytes_at(const uint4& a, const uint4& b, int s)
 template <typename OutMap>
 __global__ void __launch_bounds__(256) k_colsum(const float* __restrict__ in, int64_t R, int64_t M, OutMap out)
 {
+    after_previous();
     __shared__ float part[8][32];
     const int64_t m = (int64_t)blockIdx.x * 32 + threadIdx.x;
     float s = 0.0f;

@@ -225,15 +225,16 @@ def test_the_gradient_in_the_logits_place(dtype, V):
         assert torch.equal(a, b)
 
 
-def test_a_graph_replays_other_values():
-    c, z64, kw = case(torch.bfloat16, 40, 9000)
+@pytest.mark.parametrize("R,V", [(40, 9000), (5, 131072)])
+def test_a_graph_replays_other_values(R, V):
+    c, z64, kw = case(torch.bfloat16, R, V)
     args = dict(old_logprob=c["old"], advantages=c["adv"], ref_logprob=c["ref"], **kw)
-    out = dict(dlogits=torch.empty_like(c["z"]), loss=torch.empty(40, device="cuda"), logprob=torch.empty(40, device="cuda"))
+    out = dict(dlogits=torch.empty_like(c["z"]), loss=torch.empty(R, device="cuda"), logprob=torch.empty(R, device="cuda"))
     gdn.gdn_policy_loss_backward(c["z"], c["y"], c["w"], **args, **out)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         gdn.gdn_policy_loss_backward(c["z"], c["y"], c["w"], **args, **out)
-    d, _, _ = case(torch.bfloat16, 40, 9000, seed=9)
+    d, _, _ = case(torch.bfloat16, R, V, seed=9)
     d["y"][3] = -100
     for k in c:
         c[k].copy_(d[k])
