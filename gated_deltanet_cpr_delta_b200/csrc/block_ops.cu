@@ -79,8 +79,7 @@ gdn_status_t qk_launch(gdn::QkArgs& a, dim3 blocks, cudaStream_t st)
     a.ring = (int32_t)own;
     auto k = gdn::k_qk_norm<T, VEC, INTER, BWD>;
     if (!raise_smem(k, smem)) return GDN_ERR_CUDA;
-    k<<<blocks, gdn::kQkThreads, smem, st>>>(a);
-    return launched() ? GDN_OK : GDN_ERR_CUDA;
+    return launch_next(k, blocks, dim3(gdn::kQkThreads), smem, 0, st, a) ? GDN_OK : GDN_ERR_CUDA;
 }
 
 template <bool BWD>
@@ -134,18 +133,7 @@ gdn_status_t policy_split(const gdn::PolicyArgs& a, int S, cudaStream_t st)
     auto k = gdn::k_policy<T, BWD, ALIGNED, 256, 2, true>;
     const size_t smem = (size_t)gdn::policy_slots(2) * gdn::policy_slot_bytes(256) + sizeof(float2) * 256 * (gdn::kPolicyParts / 2);
     if (!raise_smem(k, smem)) return GDN_ERR_CUDA;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(a.T * S));
-    cfg.blockDim = dim3(256 + 32);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)S;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k, a) == cudaSuccess && launched() ? GDN_OK : GDN_ERR_CUDA;
+    return launch_next(k, dim3((unsigned)(a.T * S)), dim3(256 + 32), smem, S, st, a) ? GDN_OK : GDN_ERR_CUDA;
 }
 
 template <typename T, bool BWD, bool ALIGNED, int NT, int RES>
@@ -164,8 +152,8 @@ gdn_status_t policy_run(const gdn::PolicyArgs& a, cudaStream_t st)
     auto k = gdn::k_policy<T, BWD, ALIGNED, NT, RES, false>;
     constexpr size_t smem = (size_t)gdn::policy_slots(RES) * gdn::policy_slot_bytes(NT);
     if (!raise_smem(k, smem)) return GDN_ERR_CUDA;
-    k<<<(unsigned)std::min<int64_t>(a.T, (int64_t)sms * RES), NT + 32, smem, st>>>(a);
-    return launched() ? GDN_OK : GDN_ERR_CUDA;
+    const dim3 grid((unsigned)std::min<int64_t>(a.T, (int64_t)sms * RES));
+    return launch_next(k, grid, dim3(NT + 32), smem, 0, st, a) ? GDN_OK : GDN_ERR_CUDA;
 }
 
 // Rows of up to two tiles of 4 KB by 64 threads, longer ones by 256 (the log-probabilities' bits

@@ -159,6 +159,8 @@ __global__ void __launch_bounds__(NT + 32, RES) k_policy(const PolicyArgs a)
     }
     if constexpr (SPLIT) cluster_barrier();
     else __syncthreads();
+    let_next_start();
+    after_previous();
     auto target = [&](int64_t row) -> int {  // -1: a row that takes no part
         if (row >= a.T) return -1;
         const int64_t y = a.y[row];

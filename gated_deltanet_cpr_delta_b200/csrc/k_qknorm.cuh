@@ -162,7 +162,8 @@ __global__ void __launch_bounds__(kQkThreads, qk_resident(BWD, VEC)) k_qk_norm(c
     constexpr int U = qk_rows(BWD, sizeof(T));
     using Row = QkRow<T, VEC, INTER>;
     extern __shared__ __align__(16) unsigned char qk_smem[];
-    let_next_start();  // the sums of the weights' gradients
+    let_next_start();
+    after_previous();
     // cosines [tokens][span] and sines, 1 and 0 behind the rotated pairs; span: the pairs of all lanes
     float* cs = reinterpret_cast<float*>(qk_smem);
     const int tpr = a.tpr, lane = threadIdx.x & (tpr - 1), slot = threadIdx.x / tpr, slots = kQkThreads / tpr;
