@@ -317,3 +317,48 @@ def test_glu_gradients_against_differences():
     size = float((h.double() * dh.double()).abs().sum())
     want = float((dx * (up.double() - down.double())).sum())
     assert abs(run(up) - run(down) - want) <= 2 * 2 ** -8 * size * 1.5 + 2 ** -7 * abs(want) + e ** 3 / 3 * 4 * size
+
+
+def test_a_graph_of_copies_branches_and_calls():
+    """Calls behind copies, fills, other kernels and a join of two streams in one captured graph."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    r = lambda *n, t=torch.bfloat16: torch.randn(*n, generator=g, device="cuda").to(t)  # noqa: E731
+    T, H, d, D, F, V = 300, 4, 64, 256, 512, 40000
+    fresh = dict(q=r(T, H, d), k=r(T, H, d), x=r(T, D), xs=r(5, D), z=r(6, V), w=r(d), dh=r(T, F))
+    wg, wu, w = r(F, D), r(F, D), r(d)
+    y = torch.arange(6, device="cuda") * 7
+    adv = r(6, t=torch.float32)
+    kept = {n: torch.zeros_like(v) for n, v in fresh.items()}
+
+    def calls(v, side=None):
+        main = torch.cuda.current_stream()
+        q, k = gdn.gdn_qk_norm_forward(v["q"], v["k"], q_weight=v["w"])
+        grads = gdn.gdn_qk_norm_backward(v["q"], v["k"], q, k, q_weight=v["w"])
+        h, saved = gdn.gdn_glu_forward(v["x"], wg, wu, save=True)
+        few, _ = gdn.gdn_glu_forward(v["xs"], wg, wu)
+        if side is not None:
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                _, lp = gdn.gdn_policy_loss_forward(v["z"], y)
+            main.wait_stream(side)
+        else:
+            _, lp = gdn.gdn_policy_loss_forward(v["z"], y)
+        dx, dwg, dwu = gdn.gdn_glu_backward(v["x"], wg, wu, v["dh"], saved)
+        dz, loss, _ = gdn.gdn_policy_loss_backward(v["z"], y, adv, old_logprob=lp, advantages=adv)
+        return [q, k, *grads[:3], h, few, lp, dx, dwg, dwu, dz, loss]
+
+    want = calls(fresh)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for n, v in kept.items():
+            v.copy_(fresh[n])
+        got = calls(kept, side)
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(got, want)):
+            assert torch.equal(a, b), i
