@@ -495,11 +495,11 @@ def _opt(what: str, name: str, t: Optional[torch.Tensor], dtype: torch.dtype, sh
 
 
 def _out(what: str, name: str, t: Optional[torch.Tensor], dtype: torch.dtype, shape, dev: int, like=None):
-    """(tensor, address) of an output: the caller's, or a new one (``like``: a tensor of its type and shape)."""
+    """(tensor, address) of an output: the caller's, or a new one (``like``: a tensor of its shape, and perhaps type)."""
     if t is None:
         # empty_like takes half the time of empty with a type and a device; views of a wider tensor come out dense, but for
         # unusual orders of their axes
-        if like is not None:
+        if like is not None and like.dtype is dtype and like.shape == shape:
             t = torch.empty_like(like)
             if t.is_contiguous():
                 return t, t.data_ptr()
@@ -966,7 +966,8 @@ def gdn_glu_backward(x, w_gate, w_up, dh, saved, *, act: str = "silu", workspace
     """Gradients of sum(dh h) for :func:`gdn_glu_forward` of the same inputs with ``save``.
 
     dh [.., inner] in x's type (rows may be strided).  Returns (dx in x's shape, dw_gate, dw_up), in x's type.
-    ``grads``: an optional tuple of those three to write into; the weights' gradients may then be fp32 (both)."""
+    ``grads``: an optional tuple of those three to write into; what is None in it is allocated.  The weights' gradients
+    may then be fp32, both: the one that is given decides."""
     what = "gdn_glu_backward"
     dev = _gpu(what, x)
     s = _glu_struct(what, x, w_gate, w_up, act, dev)
@@ -975,7 +976,7 @@ def gdn_glu_backward(x, w_gate, w_up, dh, saved, *, act: str = "silu", workspace
         raise ValueError(f"{what}: dh must have shape {tuple(x.shape[:-1]) + (F,)}, not {tuple(dh.shape)}")
     pd, ld = _rows(what, "dh", _rows2d(what, "dh", dh), ty, (R, F), dev)
     dx, dwg, dwu = grads if grads is not None else (None, None, None)
-    wt = ty if dwg is None else dwg.dtype
+    wt = dwg.dtype if dwg is not None else dwu.dtype if dwu is not None else ty
     dx, pdx = _out(what, "dx", dx, ty, x.shape, dev, x)
     dwg, pdg = _out(what, "dw_gate", dwg, wt, (F, D), dev, w_gate)
     dwu, pdu = _out(what, "dw_up", dwu, wt, (F, D), dev, w_up)

@@ -1,0 +1,71 @@
+"""What the binding hands to the library for the norm of queries and keys, the gated block and the policy loss, with the library
+replaced by a recorder: no GPU is needed, and no address is read."""
+import itertools
+
+import pytest
+import torch
+
+from gated_deltanet_cpr_delta_b200 import gdn
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+class Recorder:
+    """Stands for the library: sizes are 256, calls are recorded and return GDN_OK."""
+
+    def __init__(self):
+        self.calls = {}
+
+    def __getattr__(self, name):
+        if name.endswith("_size"):
+            return lambda *a: 256
+        return lambda *a: self.calls.__setitem__(name, a) or 0
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    """CPU tensors pass for tensors on the device that `cpu` names."""
+    rec, cpu = Recorder(), torch.device("cpu")
+    monkeypatch.setattr(gdn, "load_library", lambda: rec)
+    monkeypatch.setattr(gdn, "_gpu", lambda what, t: cpu)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: t.device)
+    monkeypatch.setattr(gdn, "_call", lambda dev, what, fn, *args: fn(*args))
+    monkeypatch.setattr(gdn, "_glu_scratch", lambda *a: (None, None, 0))
+    return rec
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("given", list(itertools.product([0, 1], repeat=3)))
+def test_gated_block_gradients_partly_given(lib, dtype, given):
+    """Every buffer that the library writes has the type that it is told, whichever of the three the caller brings."""
+    x, w, dh = torch.zeros(5, 8, dtype=BF), torch.zeros(6, 8, dtype=BF), torch.zeros(5, 6, dtype=BF)
+    mine = (torch.empty(5, 8, dtype=BF), torch.empty(6, 8, dtype=dtype), torch.empty(6, 8, dtype=dtype))
+    grads = tuple(g if on else None for g, on in zip(mine, given))
+    out = gdn.gdn_glu_backward(x, w, w, dh, torch.zeros(6 * 30, dtype=torch.uint8), grads=grads)
+    args = lib.calls["gdn_glu_backward"]
+    want = dtype if given[1] or given[2] else BF
+    assert args[7] == (gdn.GDN_F32 if want is F32 else gdn.GDN_BF16)
+    assert [g.dtype for g in out] == [BF, want, want] and [g.shape for g in out] == [x.shape, w.shape, w.shape]
+    assert list(args[4:7]) == [g.data_ptr() for g in out]
+    for g, m, on in zip(out, mine, given):
+        assert not on or g is m
+
+
+def test_gated_block_gradients_of_two_types_are_refused(lib):
+    x, w, dh = torch.zeros(5, 8, dtype=BF), torch.zeros(6, 8, dtype=BF), torch.zeros(5, 6, dtype=BF)
+    for a, b in ((F32, BF), (BF, F32)):
+        with pytest.raises(ValueError, match="dw_up"):
+            gdn.gdn_glu_backward(x, w, w, dh, torch.zeros(180, dtype=torch.uint8),
+                                 grads=(None, torch.empty(6, 8, dtype=a), torch.empty(6, 8, dtype=b)))
+
+
+def test_a_new_output_has_the_type_and_shape_that_are_asked_for():
+    cpu = torch.device("cpu")
+    like = torch.zeros(4, 8, dtype=BF)
+    for dtype, shape in ((BF, (4, 8)), (F32, (4, 8)), (BF, (4, 9)), (F32, (3,))):
+        t, p = gdn._out("f", "y", None, dtype, shape, cpu, like)
+        assert t.dtype is dtype and t.shape == shape and t.is_contiguous() and p == t.data_ptr()
+    # views and other orders of the axes come out dense
+    for view in (torch.zeros(4, 16, dtype=BF)[:, :8], torch.zeros(8, 4, dtype=BF).t(), torch.zeros(1, 8, dtype=BF).expand(4, 8)):
+        t, _ = gdn._out("f", "y", None, BF, (4, 8), cpu, view)
+        assert t.is_contiguous() and t.shape == (4, 8)
