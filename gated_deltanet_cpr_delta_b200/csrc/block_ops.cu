@@ -131,8 +131,8 @@ template <typename T, bool BWD, bool ALIGNED>
 gdn_status_t policy_split(const gdn::PolicyArgs& a, int S, cudaStream_t st)
 {
     auto k = gdn::k_policy<T, BWD, ALIGNED, 256, 2, true>;
-    const size_t smem = (size_t)gdn::policy_slots(2) * gdn::policy_slot_bytes(256) + sizeof(float2) * 256 * (gdn::kPolicyParts / 2);
-    if (!raise_smem(k, smem)) return GDN_ERR_CUDA;
+    constexpr size_t smem = (size_t)gdn::policy_slots(2) * gdn::policy_slot_bytes(256) + sizeof(float2) * 256 * (gdn::kPolicyParts / 2);
+    if (!raise_smem<smem>(k)) return GDN_ERR_CUDA;
     return launch_next(k, dim3((unsigned)(a.T * S)), dim3(256 + 32), smem, S, st, a) ? GDN_OK : GDN_ERR_CUDA;
 }
 
@@ -151,7 +151,7 @@ gdn_status_t policy_run(const gdn::PolicyArgs& a, cudaStream_t st)
     }
     auto k = gdn::k_policy<T, BWD, ALIGNED, NT, RES, false>;
     constexpr size_t smem = (size_t)gdn::policy_slots(RES) * gdn::policy_slot_bytes(NT);
-    if (!raise_smem(k, smem)) return GDN_ERR_CUDA;
+    if (!raise_smem<smem>(k)) return GDN_ERR_CUDA;
     const dim3 grid((unsigned)std::min<int64_t>(a.T, (int64_t)sms * RES));
     return launch_next(k, grid, dim3(NT + 32), smem, 0, st, a) ? GDN_OK : GDN_ERR_CUDA;
 }

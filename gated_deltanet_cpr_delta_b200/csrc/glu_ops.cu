@@ -99,7 +99,7 @@ gdn_status_t glu_gemm(gdn::GluMaps& maps, gdn::GluGemmArgs& a, int sms, cudaStre
     a.tiles = (int64_t)a.tiles_m * a.tiles_n * a.problems * a.splits;
     auto k = gdn::k_glu_gemm<MODE, SAVE, ACT>;
     constexpr size_t smem = gdn::glu_gemm_smem(SAVE);
-    if (!raise_smem(k, smem)) return GDN_ERR_CUDA;
+    if (!raise_smem<smem>(k)) return GDN_ERR_CUDA;
     const unsigned pairs = (unsigned)std::min<int64_t>(a.tiles, std::max(1, sms / 2));
     return launch_next(k, dim3(2 * pairs), dim3(gdn::kGluGemmThreads), smem, 0, st, maps, a) ? GDN_OK : GDN_ERR_CUDA;
 }

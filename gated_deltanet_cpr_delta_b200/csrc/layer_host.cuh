@@ -24,12 +24,22 @@ size_t esize(gdn_dtype_t t) { return t == GDN_BF16 ? 2 : 4; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 bool launched() { return cudaGetLastError() == cudaSuccess; }
 
-// Shared memory beyond the 48 KB that every launch may have
+// Shared memory beyond the 48 KB that every launch may have.  The limit is the kernel's, not the launch's: another thread's call of
+// the same kernel may set it between this call's setting and its launch, so every call of a kernel sets the same value: all that the
+// device gives, but for 1 KB of static shared memory, which no kernel here that varies its size passes.
+constexpr int kMostSmem = 226 * 1024;
 template <typename K>
 bool raise_smem(K* kernel, size_t bytes)
 {
-    return bytes <= 48 * 1024 ||
-           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+    return bytes <= 48 * 1024 || (bytes <= kMostSmem &&
+           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem) == cudaSuccess);
+}
+// For a kernel that takes the same number of bytes in every launch (and may hold more static shared memory).
+template <size_t BYTES, typename K>
+bool raise_smem(K* kernel)
+{
+    return BYTES <= 48 * 1024 ||
+           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)BYTES) == cudaSuccess;
 }
 
 // Launches a kernel that calls after_previous(): its blocks may start, and get ready, while the kernel before it still runs

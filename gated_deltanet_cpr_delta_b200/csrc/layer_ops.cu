@@ -283,7 +283,7 @@ gdn_status_t ssm_forward_seg(gdn::SsmArgs a, cudaStream_t st)
     const int64_t blocks = (int64_t)a.s.N * a.G * a.cpg;
     if (blocks > INT32_MAX) return GDN_ERR_INVALID_ARG;
     auto k = gdn::k_ssm_fwd<T, S, V, SEG>;
-    if (!raise_smem(k, Cf::BYTES)) return GDN_ERR_CUDA;
+    if (!raise_smem<Cf::BYTES>(k)) return GDN_ERR_CUDA;
     k<<<(unsigned)blocks, Cf::THREADS, Cf::BYTES, st>>>(a);
     return launched() ? GDN_OK : GDN_ERR_CUDA;
 }
@@ -323,7 +323,7 @@ gdn_status_t ssm_backward_launch(const gdn::SsmBwdArgs& b, void* dB, void* dC, f
     }
     constexpr size_t sm = gdn::SsmBwdCfg<S>::SMEM;
     auto k = a.z != nullptr ? gdn::k_ssm_bwd<T, S, V, true> : gdn::k_ssm_bwd<T, S, V, false>;
-    if (!raise_smem(k, sm)) return GDN_ERR_CUDA;
+    if (!raise_smem<sm>(k)) return GDN_ERR_CUDA;
     k<<<(unsigned)(slots * a.G * a.cpg), gdn::kSsmThreads, sm, st>>>(b);
     if (a.s.T > 0) {
         const int64_t ids = a.s.T * a.G * 2 * S;

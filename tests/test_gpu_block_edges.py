@@ -1,5 +1,6 @@
 """The norm of queries and keys, the gated block and the policy loss where a call's form, sizes or values are at an edge."""
 import itertools
+import threading
 
 import pytest
 import torch
@@ -30,3 +31,63 @@ def test_gated_block_gradients_partly_given(T, dtype):
         got = gdn.gdn_glu_backward(x, wg, wu, dh, saved, grads=tuple(b if on else None for b, on in zip(full(), given)))
         for a, b in zip(got, want):
             assert a.dtype is b.dtype and torch.equal(a, b), given
+
+
+def test_threads_with_calls_of_different_sizes(monkeypatch):
+    """Threads call the same kernels with different amounts of shared memory, each on its own stream: every call launches, and
+    the results are those of one thread.  The library's entries are called with arguments that are ready, so that the calls
+    meet."""
+    def norm(seed, d, rot):
+        x, dy = rand(seed, 12, 4, d, t=F32), rand(seed + 1, 12, 4, d, t=F32)
+        kw = dict(positions=torch.arange(12, dtype=torch.int32, device="cuda"), inv_freq=torch.ones(rot // 2, device="cuda")) if rot else {}
+        out = torch.empty_like(x), torch.empty_like(x), None, None
+        return out[:2], lambda: gdn.gdn_qk_norm_backward(x, x, dy, dy, grads=out, **kw)
+
+    def block(seed, D, F):
+        x, w, h = rand(seed, 4, D), rand(seed + 1, F, D, scale=D ** -0.5), torch.empty(4, F, dtype=BF, device="cuda")
+        return (h,), lambda: gdn.gdn_glu_forward(x, w, w, h=h)
+
+    def layer_norm(seed, D):
+        x, w, y = rand(seed, 8, D, t=F32), rand(seed + 1, D, t=F32), torch.empty(8, D, device="cuda")
+        return (y,), lambda: gdn.gdn_layer_norm_forward(x, w, y=y)
+
+    ready = []  # the entry and its arguments, but for the stream
+    call = gdn._call
+
+    def record(dev, what, fn, *args):
+        ready.append((fn, args))
+        call(dev, what, fn, *args)
+
+    pairs = [(norm(1, 128, 0), norm(7, 128, 128)), (block(3, 1024, 640), block(9, 256, 4096)), (layer_norm(5, 6000), layer_norm(11, 8192))]
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    for pair in pairs:
+        want, entries = [], []
+        with monkeypatch.context() as m:
+            m.setattr(gdn, "_call", record)
+            for out, f in pair:
+                keep = f()
+                want.append([t.clone() for t in out])
+                entries.append(ready[-1] + (keep,))
+                for t in out:
+                    t.zero_()
+        torch.cuda.synchronize()
+        bad, start = [], threading.Barrier(4)
+
+        def work(i):
+            fn, args, _ = entries[i % 2]
+            torch.zeros(1, device="cuda")
+            start.wait()
+            for _ in range(4000):
+                st = fn(*args, streams[i].cuda_stream)
+                if st != gdn.GDN_OK:
+                    bad.append((i, st))
+
+        threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        torch.cuda.synchronize()
+        assert not bad, (len(bad), bad[:4])
+        for (out, _), w in zip(pair, want):
+            assert all(torch.equal(a, b) for a, b in zip(out, w))
