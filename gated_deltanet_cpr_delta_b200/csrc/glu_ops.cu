@@ -229,7 +229,7 @@ gdn_status_t gdn_glu_forward(const gdn_glu_t* args, void* h, void* saved, void* 
     if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
     if (need > 0 && !aligned(workspace, kAlign)) return GDN_ERR_INVALID_ARG;
     const int sms = sm_count();
-    if (sms == 0) return GDN_ERR_CUDA;
+    if (sms == 0 || !bind_context()) return GDN_ERR_CUDA;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const GluOperands o = glu_operands(s, static_cast<unsigned char*>(workspace));
     if (!glu_align(s, o, sms, st)) return GDN_ERR_CUDA;

@@ -25,4 +25,12 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
     return fn;
 }
 
+// The encoder needs a current context.  A thread that has not called the runtime yet has none: this makes the current device's
+// the thread's own, as a kernel's launch would.
+[[maybe_unused]] bool bind_context()
+{
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
+}
+
 }  // namespace

@@ -33,6 +33,50 @@ def test_gated_block_gradients_partly_given(T, dtype):
             assert a.dtype is b.dtype and torch.equal(a, b), given
 
 
+def entry(monkeypatch, f):
+    """f(), and the library's last entry that it called with its arguments, as a function of the stream."""
+    ready, call = [], gdn._call
+
+    def record(dev, what, fn, *args):
+        ready.append((fn, args))
+        call(dev, what, fn, *args)
+
+    with monkeypatch.context() as m:
+        m.setattr(gdn, "_call", record)
+        keep = f()
+    fn, args = ready[-1]
+    return keep, lambda stream: fn(*args, stream.cuda_stream)
+
+
+def test_a_thread_whose_first_call_this_is(monkeypatch):
+    """Each entry, as the first that a thread calls of CUDA."""
+    x, w, dh, q = rand(1, 300, 64), rand(2, 200, 64), rand(3, 300, 200), rand(4, 20, 2, 64)
+    z, y, adv = rand(5, 9, 1000), torch.arange(9, device="cuda"), rand(6, 9, t=F32)
+    _, saved = gdn.gdn_glu_forward(x, w, w, save=True)
+    calls = [lambda: gdn.gdn_glu_forward(x, w, w), lambda: gdn.gdn_glu_forward(x[:5], w, w),
+             lambda: gdn.gdn_glu_backward(x, w, w, dh, saved), lambda: gdn.gdn_qk_norm_forward(q, q),
+             lambda: gdn.gdn_qk_norm_backward(q, q, q, q), lambda: gdn.gdn_policy_loss_forward(z, y),
+             lambda: gdn.gdn_policy_loss_backward(z, y, adv, old_logprob=adv, advantages=adv)]
+    stream = torch.cuda.Stream()
+    for f in calls:
+        workspaces, scratch = [], gdn._scratch
+        with monkeypatch.context() as m:  # kept for the second call
+            m.setattr(gdn, "_scratch", lambda *a: workspaces.append(scratch(*a)) or workspaces[-1])
+            outs, again = entry(monkeypatch, f)
+        outs = [t for t in outs if t is not None]
+        want = [t.clone() for t in outs]
+        for t in outs:
+            t.zero_()
+        torch.cuda.synchronize()
+        got = []
+        t = threading.Thread(target=lambda: got.append(again(stream)))
+        t.start()
+        t.join()
+        torch.cuda.synchronize()
+        assert got == [gdn.GDN_OK]
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
 def test_threads_with_calls_of_different_sizes(monkeypatch):
     """Threads call the same kernels with different amounts of shared memory, each on its own stream: every call launches, and
     the results are those of one thread.  The library's entries are called with arguments that are ready, so that the calls
@@ -51,34 +95,24 @@ def test_threads_with_calls_of_different_sizes(monkeypatch):
         x, w, y = rand(seed, 8, D, t=F32), rand(seed + 1, D, t=F32), torch.empty(8, D, device="cuda")
         return (y,), lambda: gdn.gdn_layer_norm_forward(x, w, y=y)
 
-    ready = []  # the entry and its arguments, but for the stream
-    call = gdn._call
-
-    def record(dev, what, fn, *args):
-        ready.append((fn, args))
-        call(dev, what, fn, *args)
-
     pairs = [(norm(1, 128, 0), norm(7, 128, 128)), (block(3, 1024, 640), block(9, 256, 4096)), (layer_norm(5, 6000), layer_norm(11, 8192))]
     streams = [torch.cuda.Stream() for _ in range(4)]
     for pair in pairs:
         want, entries = [], []
-        with monkeypatch.context() as m:
-            m.setattr(gdn, "_call", record)
-            for out, f in pair:
-                keep = f()
-                want.append([t.clone() for t in out])
-                entries.append(ready[-1] + (keep,))
-                for t in out:
-                    t.zero_()
+        for out, f in pair:
+            entries.append(entry(monkeypatch, f))
+            want.append([t.clone() for t in out])
+            for t in out:
+                t.zero_()
         torch.cuda.synchronize()
         bad, start = [], threading.Barrier(4)
 
         def work(i):
-            fn, args, _ = entries[i % 2]
+            again = entries[i % 2][1]
             torch.zeros(1, device="cuda")
             start.wait()
             for _ in range(4000):
-                st = fn(*args, streams[i].cuda_stream)
+                st = again(streams[i])
                 if st != gdn.GDN_OK:
                     bad.append((i, st))
 
