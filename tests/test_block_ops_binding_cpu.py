@@ -5,7 +5,7 @@ import itertools
 import pytest
 import torch
 
-from gated_deltanet_cpr_delta_b200 import gdn
+from gated_deltanet_cpr_delta_b200 import build, gdn
 
 BF, F32 = torch.bfloat16, torch.float32
 
@@ -69,3 +69,20 @@ def test_a_new_output_has_the_type_and_shape_that_are_asked_for():
     for view in (torch.zeros(4, 16, dtype=BF)[:, :8], torch.zeros(8, 4, dtype=BF).t(), torch.zeros(1, 8, dtype=BF).expand(4, 8)):
         t, _ = gdn._out("f", "y", None, BF, (4, 8), cpu, view)
         assert t.is_contiguous() and t.shape == (4, 8)
+
+
+BIG = 1 << 36
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are not memory")
+def test_temperatures_whose_reciprocal_leaves_the_range_are_refused():
+    """2^-100 is the smallest that is taken: a call that passes every check ends with GDN_ERR_CUDA here."""
+    build.build()
+    lib = gdn.load_library()
+
+    def forward(tau):
+        s = gdn.PolicyStruct(BIG, 2 * BIG, 3 * BIG, None, 4 * BIG, 64, 10, 64, 0.2, 0.2, 0.0, tau, gdn.GDN_BF16)
+        return lib.gdn_policy_loss_forward(s, 5 * BIG, 6 * BIG, None, None)
+
+    assert [forward(t) for t in (1e-45, 1e-40, 1e-38, 2.0 ** -101, 0.0)] == [gdn.GDN_ERR_INVALID_ARG] * 5
+    assert [forward(t) for t in (2.0 ** -100, 1e-6, 1.0, 1e30)] == [gdn.GDN_ERR_CUDA] * 4
