@@ -113,7 +113,7 @@ gdn_status_t policy_check(const gdn_policy_t* s, const int32_t* status)
 {
     if (s == nullptr || s->rows < 0 || s->rows > kMaxRows || s->vocab <= 0 || !dtype_ok(s->in_dtype) || !aligned(status, 4))
         return GDN_ERR_INVALID_ARG;
-    // (2^-100: log2(e) / temperature and its products with logits of ordinary size stay in range)
+    // (2^-100: the kernel's power of two for far logits stays in range)
     if (!(s->temperature >= 0x1p-100f) || std::isinf(s->temperature)) return GDN_ERR_INVALID_ARG;
     if ((s->old_logprob == nullptr) != (s->advantages == nullptr) || (s->ref_logprob && !s->old_logprob))
         return GDN_ERR_INVALID_ARG;

@@ -56,8 +56,11 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t n
                  : "memory");
 }
 
-// maxima of -inf (nothing yet, or nothing but -inf) count as 0 where they are taken off an exponent
-__device__ __forceinline__ float policy_base(float m) { return m == -INFINITY ? 0.0f : m; }
+// The running maximum m is in units of log2, max(z) c with c = log2(e) / tau, and a row's exponents are fma(z, c, -m): they share the
+// rounding of m, at most 32 where |m| is below 2^30, which the sum takes out again.  Beyond, it would leave the range of 2^x.
+// Maxima start at -2^30, below which nothing is told apart, and a row whose maximum ends there or at 2^30 and above (one that a mask
+// of -1e10 or of the type's lowest value fills) is walked once more (policy_far).
+constexpr float kPolicyFar = 1073741824.0f;
 
 // The largest of a thread's packed values.
 template <typename T, int E>
@@ -89,7 +92,7 @@ __device__ __forceinline__ void policy_join(float& m, float& sum)
     float M = m;
 #pragma unroll
     for (int o = N / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
-    sum *= ex2(m - policy_base(M));
+    sum *= ex2(m - M);
 #pragma unroll
     for (int o = N / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFullMask, sum, o);
     m = M;
@@ -120,9 +123,44 @@ __host__ __device__ constexpr int policy_parts_log(int n) { return n >= 32 ? 3 :
 // The maximum and sum of what lies behind, joined to those of what lies before
 __device__ __forceinline__ void policy_add(float& m, float& sum, float m1, float sum1)
 {
-    const float M = fmaxf(m, m1), base = policy_base(M);
-    sum = __fmaf_rn(sum1, ex2(m1 - base), sum * ex2(m - base));
+    const float M = fmaxf(m, m1);
+    sum = __fmaf_rn(sum1, ex2(m1 - M), sum * ex2(m - M));
     m = M;
+}
+
+// A row whose maximum is far off, by NT threads: the maximum M itself and how many logits equal it, which are all that count: logits that
+// differ there differ by 64 or more in units of log2.  n: as a sum relative to M, not a number where a logit is not or M is infinite.
+// (As a call of its own it cost every row: 2048 x 32000 losses 36.3 us in place of 34.8.)
+template <typename T, int NT>
+__device__ __forceinline__ float2 policy_far(const T* z, int V, float* wm, float* ws)
+{
+    const int tid = threadIdx.x, lane = tid & 31;
+    auto together = [] { asm volatile("bar.sync 1, %0;" ::"n"(NT) : "memory"); };
+    float M = -INFINITY, bad = 0.0f;
+#pragma unroll 1
+    for (int i = tid; i < V; i += NT) {
+        const float x = to_f<T>(z[i]);
+        M = fmaxf(M, x);
+        if (x != x) bad = x;
+    }
+    auto warps = [&](float x, float* w, auto join) {  // over all threads, the same in each
+        for (int o = 16; o > 0; o >>= 1) x = join(x, __shfl_xor_sync(kFullMask, x, o));
+        together();
+        if (lane == 0) w[tid >> 5] = x;
+        together();
+        x = w[0];
+        for (int i = 1; i < NT / 32; ++i) x = join(x, w[i]);
+        return x;
+    };
+    M = warps(M, wm, [](float x, float y) { return fmaxf(x, y); });
+    int count = 0;
+#pragma unroll 1
+    for (int i = tid; i < V; i += NT) count += to_f<T>(z[i]) == M;
+    // (the counts are whole: in two halves of 16 bits exact in fp32, whatever the order)
+    float n = warps((float)(count >> 16) * 65536.0f, ws, [](float x, float y) { return x + y; }) +
+        warps((float)(count & 0xffff), wm, [](float x, float y) { return x + y; });
+    n += warps(bad, ws, [](float x, float y) { return x + y; });
+    return make_float2(M, isinf(M) ? M - M : n);
 }
 
 // NT threads walk, 32 more fetch; `RES` blocks per SM.  ALIGNED: every row of the logits and of the gradient is whole
@@ -281,7 +319,7 @@ __global__ void __launch_bounds__(NT + 32, RES) k_policy(const PolicyArgs a)
             return *reinterpret_cast<const Vec<T, E>*>(&r);
         };
         // ---- the first walk: running maximum (in units of log2) and sum
-        float m = -INFINITY, sum = 0.0f, before = -INFINITY, before_sum = 0.0f;
+        float m = -kPolicyFar, sum = 0.0f, before = -kPolicyFar, before_sum = 0.0f;
         const int slot0 = slot;
         const uint32_t phase0 = phase;
         int part = part0, part_end = tiles * (part + 1) >> lg;
@@ -289,7 +327,7 @@ __global__ void __launch_bounds__(NT + 32, RES) k_policy(const PolicyArgs a)
             if (t == part_end) {
                 if constexpr (SPLIT) found[(part - part0) * NT + tid] = make_float2(m, sum);
                 else policy_add(before, before_sum, m, sum);
-                m = -INFINITY, sum = 0.0f;
+                m = -kPolicyFar, sum = 0.0f;
                 part_end = tiles * (++part + 1) >> lg;
             }
             wait();
@@ -303,10 +341,10 @@ __global__ void __launch_bounds__(NT + 32, RES) k_policy(const PolicyArgs a)
                         v[j] = vec(tid + j * NT);
                         top.add(v[j]);
                     }
-                const float M = fmaxf(m, top.get() * a.c), base = policy_base(M);
-                sum *= ex2(m - base);
+                const float M = fmaxf(m, top.get() * a.c);
+                sum *= ex2(m - M);
                 m = M;
-                const f2x b2 = pk2(-base, -base);
+                const f2x b2 = pk2(-M, -M);
                 f2x s0 = pk2(0.0f, 0.0f), s1 = s0;
 #pragma unroll
                 for (int j = 0; j < NV; ++j)
@@ -348,11 +386,28 @@ __global__ void __launch_bounds__(NT + 32, RES) k_policy(const PolicyArgs a)
         if (lane == 0) wm[warp] = m, ws[warp] = sum;
         together();
         // every warp joins the warps itself
-        m = lane < WARPS ? wm[lane] : -INFINITY;
+        m = lane < WARPS ? wm[lane] : -kPolicyFar;
         sum = lane < WARPS ? ws[lane] : 0.0f;
         policy_join<32>(m, sum);
-        const float bm = policy_base(m);
-        const float lp = (__fmaf_rn(SPLIT ? split_target : target_logit, a.c, -bm) - log2f(sum)) * 0.69314718055994530942f;
+        float C = a.c, bm = m;  // exponents are fma(z, C, -bm)
+        const float zt = SPLIT ? split_target : target_logit, at = __fmaf_rn(zt, a.c, -m), log_sum = log2f(sum);
+        float lp = (at - log_sum) * 0.69314718055994530942f;
+        if (fabsf(m) >= kPolicyFar) {
+            const float2 far = policy_far<T, NT>(static_cast<const T*>(a.z) + row * a.ldz, a.V, wm, ws);
+            m = far.x, sum = far.y;
+            // the power of two that puts m C, exact, into 2^40..2^41: equal logits differ by 0, others by 2^16 or more
+            C = __uint_as_float((294u - (__float_as_uint(m) >> 23 & 0xffu)) << 23);
+            bm = m * C;
+            // (by halves: the difference may be out of range where its quotient is not)
+            lp = (zt == m ? 0.0f : (0.5f * zt - 0.5f * m) * a.inv_tau * 2.0f) - log2f(sum) * 0.69314718055994530942f;
+            if constexpr (SPLIT && BWD) {  // the gradient may take the place of what another block still walks
+                together();
+                if (tid < S && !lost) mbar_arrive_peer(peer_addr(&joined, tid));
+                if (!mbar_wait_cluster(&joined, 1, LIMIT)) lost = 1;
+            }
+        } else if (isinf(at)) {  // a target far below: out of range times log2(e), perhaps not by itself
+            lp = zt * a.inv_tau - (m + log_sum) * 0.69314718055994530942f;
+        }
         float loss = 0.0f, d = 0.0f;
         if (a.old != nullptr) {
             const float ratio = ex2((lp - old) * kLog2e);
@@ -376,7 +431,7 @@ __global__ void __launch_bounds__(NT + 32, RES) k_policy(const PolicyArgs a)
             // ---- the second walk: first the tiles that have stayed, then the others
             d *= dloss * a.inv_tau;
             const float scale = -d * rcp(sum);
-            const f2x b2 = pk2(-bm, -bm), scale2 = pk2(scale, scale);
+            const f2x c2 = pk2(C, C), b2 = pk2(-bm, -bm), scale2 = pk2(scale, scale);
             const int so = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(out) & 15);
             const int end_slot = slot;
             const uint32_t end_phase = phase;
@@ -430,7 +485,7 @@ __global__ void __launch_bounds__(NT + 32, RES) k_policy(const PolicyArgs a)
                                                   : tid < 2 * E && rest < TILE + skip && skip + last * E + tid - E < rest ? skip + last * E + tid - E : -1;
                             if (e >= 0) {
                                 const float x = to_f<T>(reinterpret_cast<const T*>(policy_smem + slot * SLOT + s)[e]);
-                                dst[e] = from_f<T>(__fmaf_rn(ex2(__fmaf_rn(x, a.c, -bm)), scale, e == yl ? d : 0.0f));
+                                dst[e] = from_f<T>(__fmaf_rn(ex2(__fmaf_rn(x, C, -bm)), scale, e == yl ? d : 0.0f));
                             }
                         }
                     }

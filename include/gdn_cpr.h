@@ -689,7 +689,8 @@ gdn_status_t gdn_glu_backward(const gdn_glu_t* args, const void* dh, int64_t dh_
  * no part: nothing of it is read, its loss, log-probability and gradient are 0.  A target of vocab or above is
  * treated so too, and *status (may be NULL) becomes GDN_ERR_DEVICE_INPUT.
  * Logits of -inf have probability 0; a row whose logits are all -inf, or that holds +inf or a NaN, is not a number in its
- * own results.  An advantage of 0 adds 0, whatever the ratio.  temperature: at least 2^-100.
+ * own results.  Every finite logit counts as what it is, the type's lowest value in a whole row too; a log-probability below fp32's
+ * range is -inf.  An advantage of 0 adds 0, whatever the ratio.  temperature: at least 2^-100.
  * A row's log-probability has the same bits in every call on the same values, type and
  * vocabulary: whatever the batch, the row's place, its stride, and whether the gradient is made.
  * *status becomes GDN_ERR_TIMEOUT when a wait inside the kernel runs out (about a second): the outputs are then

@@ -2,10 +2,13 @@
 import itertools
 import threading
 
+import numpy as np
 import pytest
 import torch
 
 from gated_deltanet_cpr_delta_b200 import gdn
+from oracle import block_ops as ops
+from test_gpu_layer_ops import HALF, TYPES, U
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -125,3 +128,62 @@ def test_threads_with_calls_of_different_sizes(monkeypatch):
         assert not bad, (len(bad), bad[:4])
         for (out, _), w in zip(pair, want):
             assert all(torch.equal(a, b) for a, b in zip(out, w))
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("V", [40, 3001, 60000, 140001])
+@pytest.mark.parametrize("tau", [1.0, 0.5, 4.0])
+def test_finite_logits_at_the_ends_of_the_range(dtype, V, tau):
+    """Rows that a mask of the type's lowest value fills, wholly or in part, and values beyond fp32's range times log2(e) / tau: a
+    finite logit counts as what it is.  Tolerances: as in the policy loss's tests, e_lp = 2^-24 (101 + 21 (V / 4096) + 4 range +
+    2 |lp|) with the range of the logits whose probability is not 0 (at most 20 / tau here); log-probabilities beyond fp32's range are
+    infinite.  Below 2^30 a row's maximum times log2(e) / tau is rounded by up to 32, which adds four roundings of 32."""
+    t, inf = TYPES[dtype], float("inf")
+    low, top = torch.finfo(t).min, torch.finfo(t).max
+    near = float(torch.tensor(low, dtype=t).view({BF: torch.int16, F32: torch.int32}[t]).sub(1).view(t))  # the next value
+    R = 15
+    z = rand(V, R, V, t=t, scale=2.0).clamp_(-10, 10)
+    y = torch.tensor([3, 5, 7, 9, 11, 13, 15, 17, 19, 20, 21, 22, 23, 24, 25], device="cuda") + (V - 30) // 2
+    y[14] = V - 1
+    z[0] = low                                  # all masked
+    z[1], z[1, 1::2] = -inf, low                # all masked, one half by each kind
+    z[1, y[1]] = low
+    z[2, y[2]] = low                            # the target alone masked
+    z[3, 2], z[3, y[3]] = top, 1.0              # one beyond all
+    z[4, y[4]] = top                            # which is the target
+    z[5], z[5, : V // 2] = low, near            # two values beyond the range
+    z[6] = top
+    z[7], z[7, y[7]] = low, 2.0                 # all but the target masked
+    z[8], z[8, y[8]:] = low, -1e38              # masked, and beyond the range for small temperatures only
+    z[9, V // 3:] = low
+    z[10], z[11], z[12] = -1e9, -1e10, 1e30     # other values that masks take, and rows far off as a whole
+    z[13] -= 3e4
+    z[14, : V // 2] = -1e10
+    n64 = lambda v: v.double().cpu().numpy()  # noqa: E731
+    z64, y_, tau64 = n64(z), y.cpu().numpy(), float(np.float32(tau))
+    with np.errstate(over="ignore"):
+        lp = ops.policy(z64, y_, tau=tau64)[1]
+        assert np.isfinite(lp).all()
+    old = torch.from_numpy(np.clip(lp, -1e30, None).astype(np.float32)).cuda() - 0.05
+    adv, w = rand(V + 1, R, t=F32), rand(V + 2, R, t=F32)
+    dz, loss, got = gdn.gdn_policy_loss_backward(z, y, w, old_logprob=old, advantages=adv, temperature=tau)
+    loss2, got2 = gdn.gdn_policy_loss_forward(z, y, old_logprob=old, advantages=adv, temperature=tau)
+    place = z.clone()
+    third = gdn.gdn_policy_loss_backward(place, y, w, old_logprob=old, advantages=adv, temperature=tau, dlogits=place)
+    assert torch.equal(got, got2) and torch.equal(loss, loss2) and all(torch.equal(a, b) for a, b in zip(third, (dz, loss, got)))
+    o = dict(old=n64(old), adv=n64(adv), lo=float(np.float32(0.2)), hi=float(np.float32(0.2)), tau=tau64)
+    wl, _, wd, p = ops.policy(z64, y_, **o)
+    wz = ops.policy_backward(z64, y_, n64(w), **o)
+    e = U * (101 + 21 * (V // 4096) + 4 * 32 + 4 * 20 / tau + 2 * np.abs(lp))
+    got, loss, dz = n64(got), n64(loss), n64(dz)
+    far = lp < -torch.finfo(F32).max * (1 + 2.0 ** -25)  # rounds to -inf
+    assert (got[far] == -inf).all() and (np.abs(got - lp) <= e)[~far].all(), (got, lp)
+    e = np.where(lp < -1e30, 0, e)  # their ratio is 0, and stays it
+    ratio = np.exp(lp - o["old"])
+    e1 = np.abs(o["adv"]) * ratio * (e + 8 * U) + 4 * U * np.abs(wl)
+    assert (np.abs(loss - wl) <= e1).all(), (loss, wl)
+    hot = np.zeros_like(p)
+    hot[np.arange(R), y_] = 1
+    tol = e1[:, None] * (hot + p) + np.abs(wd)[:, None] * (p * (e + 8 * U)[:, None] + 4 * U * hot)
+    bad = ~(np.abs(dz - wz) <= tol * np.abs(n64(w))[:, None] / tau64 + HALF[t] * np.abs(wz) * 1.01 + 1e-37)
+    assert not bad.any(), (np.argwhere(bad)[:4], dz[bad][:4], wz[bad][:4])
