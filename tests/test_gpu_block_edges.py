@@ -187,3 +187,29 @@ def test_finite_logits_at_the_ends_of_the_range(dtype, V, tau):
     tol = e1[:, None] * (hot + p) + np.abs(wd)[:, None] * (p * (e + 8 * U)[:, None] + 4 * U * hot)
     bad = ~(np.abs(dz - wz) <= tol * np.abs(n64(w))[:, None] / tau64 + HALF[t] * np.abs(wz) * 1.01 + 1e-37)
     assert not bad.any(), (np.argwhere(bad)[:4], dz[bad][:4], wz[bad][:4])
+
+
+@pytest.mark.parametrize("scale", [1e-4, 1e-3, 1e-2, 0.3, 0.6, 3.0])
+def test_the_kl_term_of_policies_that_are_close(scale):
+    """e^g - g - 1 for given gaps g: its own rounding is 3 units of 2^-24 of its value up to 1/2, beyond it e^g - 1 is off by 2 units, up
+    to 4.4 times the difference's size; with the product and the sum's rounding at most 16 units of the value, however small the gap is.
+    The slope 1 - e^g: 2 units, products 4; a probability by e_lp + 8 units."""
+    R, V, kl = 64, 50, 0.3
+    z, y = rand(1, R, V, t=F32), torch.arange(R, device="cuda") % V
+    _, lp = gdn.gdn_policy_loss_forward(z, y)
+    ref = lp + rand(2, R, t=F32).clamp_(-3, 3) * scale
+    w, zero = rand(3, R, t=F32), torch.zeros(R, device="cuda")
+    dz, loss, _ = gdn.gdn_policy_loss_backward(z, y, w, old_logprob=lp, advantages=zero, ref_logprob=ref, kl_coef=kl)
+    n64 = lambda v: v.double().cpu().numpy()  # noqa: E731
+    g = n64(ref - lp)
+    series = sum(g ** n / float(np.prod(np.arange(1.0, n + 1))) for n in range(2, 40))
+    want = float(np.float32(kl)) * np.where(np.abs(g) < 2, series, np.expm1(g) - g)
+    loss = n64(loss)
+    assert (loss >= 0).all() and (np.abs(loss - want) <= 16 * U * want).all(), np.max(np.abs(loss - want) / want) / U
+    z64, y_ = n64(z), y.cpu().numpy()
+    wp, p = ops.policy(z64, y_)[1], ops.policy(z64, y_)[3]
+    d = -float(np.float32(kl)) * np.expm1(g)
+    hot = np.eye(V)[y_]
+    wz = (n64(w) * d)[:, None] * (hot - p)
+    e = U * (101 + 4 * np.ptp(z64, 1) + 2 * np.abs(wp))
+    assert (np.abs(n64(dz) - wz) <= np.abs(n64(w) * d)[:, None] * (p * (e[:, None] + 8 * U) + 8 * U * hot) + U * np.abs(wz) + 1e-37).all()
