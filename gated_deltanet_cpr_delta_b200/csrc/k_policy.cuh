@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(NT + 32, RES) k_policy(const PolicyArgs a)
                 loss = free < held ? held : free;  // not a number where the ratio is not
                 d = free < held ? 0.0f : free;
             }
-            if (a.ref != nullptr) {
+            if (a.ref != nullptr && a.kl != 0.0f) {  // (0 times a term that overflowed is not a number)
                 float slope;
                 loss = __fmaf_rn(a.kl, policy_kl(ref - lp, slope), loss);
                 d = __fmaf_rn(a.kl, slope, d);

@@ -684,7 +684,7 @@ gdn_status_t gdn_glu_backward(const gdn_glu_t* args, const void* dh, int64_t dh_
  *   logprob = z_y / temperature - log(sum_v e^(z_v / temperature)),  ratio = e^(logprob - old_logprob)
  *   loss    = -min(ratio A, clip(ratio, 1 - clip_low, 1 + clip_high) A)
  *             + kl_coef (e^(ref_logprob - logprob) - (ref_logprob - logprob) - 1),   A = advantages[row]
- * old_logprob, ref_logprob, advantages [rows] fp32.  ref_logprob NULL: no KL term.  old_logprob and advantages NULL (both):
+ * old_logprob, ref_logprob, advantages [rows] fp32.  ref_logprob NULL or kl_coef 0: no KL term.  old_logprob and advantages NULL (both):
  * log-probabilities only, as a rollout records them.  A row with a negative target takes
  * no part: nothing of it is read, its loss, log-probability and gradient are 0.  A target of vocab or above is
  * treated so too, and *status (may be NULL) becomes GDN_ERR_DEVICE_INPUT.

@@ -213,3 +213,16 @@ def test_the_kl_term_of_policies_that_are_close(scale):
     wz = (n64(w) * d)[:, None] * (hot - p)
     e = U * (101 + 4 * np.ptp(z64, 1) + 2 * np.abs(wp))
     assert (np.abs(n64(dz) - wz) <= np.abs(n64(w) * d)[:, None] * (p * (e[:, None] + 8 * U) + 8 * U * hot) + U * np.abs(wz) + 1e-37).all()
+
+
+def test_without_a_kl_weight_the_reference_takes_no_part():
+    """However far the reference is."""
+    R, V = 20, 300
+    z, y = rand(1, R, V), torch.arange(R, device="cuda")
+    _, lp = gdn.gdn_policy_loss_forward(z, y)
+    adv, w = rand(2, R, t=F32), rand(3, R, t=F32)
+    for ref in (lp + 200, lp - 200, torch.full_like(lp, float("inf"))):
+        args = dict(old_logprob=lp - 0.1, advantages=adv)
+        want = gdn.gdn_policy_loss_backward(z, y, w, **args)
+        got = gdn.gdn_policy_loss_backward(z, y, w, ref_logprob=ref, kl_coef=0.0, **args)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
