@@ -34,9 +34,9 @@ gdn_status_t qk_check(const gdn_qk_norm_t* s)
 }
 
 // Whether a thread's four pairs of a row are two accesses of four elements.
-bool qk_vectors(const gdn_qk_norm_t* s, const void* p, int64_t stride)
+bool qk_vectors(const gdn_qk_norm_t* s, const void* p, int64_t stride, gdn_dtype_t t)
 {
-    const size_t bytes = 4 * esize(s->in_dtype);
+    const size_t bytes = 4 * esize(t);
     return aligned(p, bytes) && stride % 4 == 0 && s->head_dim % 8 == 0 && (s->interleaved || s->rot_dim % 8 == 0);
 }
 
@@ -69,29 +69,24 @@ unsigned qk_shares(const gdn::QkArgs& a, int64_t tiles, int sms)
     return (unsigned)std::max<int64_t>(1, std::min<int64_t>(sms / std::max<int64_t>(1, tiles), rows / (2 * slots)));
 }
 
-template <typename T, bool VEC, bool INTER, bool BWD>
+template <typename T, typename G, bool BWD, bool VEC, bool INTER>
 gdn_status_t qk_launch(gdn::QkArgs& a, dim3 blocks, cudaStream_t st)
 {
     const size_t angles = a.rot > 0 ? sizeof(float) * 8 * (size_t)a.tokens * a.tpr : 0, weights = sizeof(float) * 16 * a.tpr;
     const size_t own = (angles + weights + 127) / 128 * 128;
-    const size_t ring = VEC ? gdn::QkRing<T, gdn::qk_rows(BWD, sizeof(T)), BWD>::BYTES : 0;
+    const size_t ring = VEC ? gdn::QkRing<T, G, gdn::qk_rows(BWD, sizeof(T)), BWD>::BYTES : 0;
     const size_t smem = std::max(own + ring, BWD ? sizeof(float) * (gdn::kQkThreads / 32) * a.d : 0);
     a.ring = (int32_t)own;
-    auto k = gdn::k_qk_norm<T, VEC, INTER, BWD>;
+    auto k = gdn::k_qk_norm<T, G, VEC, INTER, BWD>;
     if (!raise_smem(k, smem)) return GDN_ERR_CUDA;
     return launch_next(k, blocks, dim3(gdn::kQkThreads), smem, 0, st, a) ? GDN_OK : GDN_ERR_CUDA;
 }
 
-template <bool BWD>
-gdn_status_t qk_dispatch(gdn::QkArgs& a, gdn_dtype_t t, bool vec, dim3 blocks, cudaStream_t st)
+template <typename T, typename G, bool BWD>
+gdn_status_t qk_dispatch(gdn::QkArgs& a, bool vec, dim3 blocks, cudaStream_t st)
 {
-    const bool in = a.interleaved;
-    if (t == GDN_BF16) {
-        if (vec) return in ? qk_launch<__nv_bfloat16, true, true, BWD>(a, blocks, st) : qk_launch<__nv_bfloat16, true, false, BWD>(a, blocks, st);
-        return in ? qk_launch<__nv_bfloat16, false, true, BWD>(a, blocks, st) : qk_launch<__nv_bfloat16, false, false, BWD>(a, blocks, st);
-    }
-    if (vec) return in ? qk_launch<float, true, true, BWD>(a, blocks, st) : qk_launch<float, true, false, BWD>(a, blocks, st);
-    return in ? qk_launch<float, false, true, BWD>(a, blocks, st) : qk_launch<float, false, false, BWD>(a, blocks, st);
+    if (vec) return a.interleaved ? qk_launch<T, G, BWD, true, true>(a, blocks, st) : qk_launch<T, G, BWD, true, false>(a, blocks, st);
+    return a.interleaved ? qk_launch<T, G, BWD, false, true>(a, blocks, st) : qk_launch<T, G, BWD, false, false>(a, blocks, st);
 }
 
 gdn::QkArgs qk_args(const gdn_qk_norm_t* s, int blocks)
@@ -206,14 +201,17 @@ gdn_status_t gdn_qk_norm_forward(const gdn_qk_norm_t* args, void* q_out, void* k
         return GDN_ERR_INVALID_ARG;
     const int sms = sm_count();
     if (sms == 0) return GDN_ERR_CUDA;
-    const bool vec = qk_vectors(args, s.q, s.q_stride) && qk_vectors(args, s.k, s.k_stride) &&
-                     qk_vectors(args, q_out, wq) && qk_vectors(args, k_out, wk);
+    const gdn_dtype_t t = s.in_dtype;
+    const bool vec = qk_vectors(args, s.q, s.q_stride, t) && qk_vectors(args, s.k, s.k_stride, t) &&
+                     qk_vectors(args, q_out, wq, t) && qk_vectors(args, k_out, wk, t);
     const int most = sms * gdn::qk_resident(false, vec);
     gdn::QkArgs a = qk_args(args, most);
     a.out[0] = q_out; a.out[1] = k_out;
     const int64_t tiles = ceil_div(T, a.tokens);
     const dim3 blocks((unsigned)std::min<int64_t>(tiles, most), qk_shares(a, tiles, sms));
-    return qk_dispatch<false>(a, s.in_dtype, vec, blocks, static_cast<cudaStream_t>(stream));
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return t == GDN_BF16 ? qk_dispatch<__nv_bfloat16, __nv_bfloat16, false>(a, vec, blocks, st)
+                         : qk_dispatch<float, float, false>(a, vec, blocks, st);
 }
 
 size_t gdn_qk_norm_backward_workspace_size(int64_t tokens, int32_t head_dim)
@@ -226,22 +224,32 @@ gdn_status_t gdn_qk_norm_backward(const gdn_qk_norm_t* args, const void* dq_out,
                                   int64_t dk_out_stride, void* dq, void* dk, float* dq_weight, float* dk_weight,
                                   void* workspace, size_t workspace_bytes, void* stream)
 {
+    return gdn_qk_norm_backward_ex(args, args != nullptr ? args->in_dtype : GDN_F32, dq_out, dq_out_stride, dk_out, dk_out_stride, dq, dk,
+                                   dq_weight, dk_weight, workspace, workspace_bytes, stream);
+}
+
+gdn_status_t gdn_qk_norm_backward_ex(const gdn_qk_norm_t* args, gdn_dtype_t grad_dtype, const void* dq_out, int64_t dq_out_stride,
+                                     const void* dk_out, int64_t dk_out_stride, void* dq, void* dk, float* dq_weight,
+                                     float* dk_weight, void* workspace, size_t workspace_bytes, void* stream)
+{
     const gdn_status_t bad = qk_check(args);
     if (bad != GDN_OK) return bad;
+    if (!dtype_ok(grad_dtype)) return GDN_ERR_INVALID_ARG;
+    if (grad_dtype != args->in_dtype && grad_dtype != GDN_F32) return GDN_ERR_UNSUPPORTED;
     const gdn_qk_norm_t& s = *args;
     const int64_t T = s.tokens, wq = (int64_t)s.q_heads * s.head_dim, wk = (int64_t)s.k_heads * s.head_dim;
     const bool weights = dq_weight != nullptr || dk_weight != nullptr;
     if (!aligned(dq_weight, 4) || !aligned(dk_weight, 4) || (dq_weight && !s.q_weight) || (dk_weight && !s.k_weight))
         return GDN_ERR_INVALID_ARG;
-    if (T > 0 && (!rows_ok(dq_out, dq_out_stride, wq, s.in_dtype) || !rows_ok(dk_out, dk_out_stride, wk, s.in_dtype) ||
+    if (T > 0 && (!rows_ok(dq_out, dq_out_stride, wq, grad_dtype) || !rows_ok(dk_out, dk_out_stride, wk, grad_dtype) ||
                   !rows_ok(dq, wq, wq, s.in_dtype) || !rows_ok(dk, wk, wk, s.in_dtype)))
         return GDN_ERR_INVALID_ARG;
-    const size_t es = esize(s.in_dtype), ws = esize(s.w_dtype);
+    const size_t es = esize(s.in_dtype), ges = esize(grad_dtype), ws = esize(s.w_dtype);
     const size_t need = weights ? gdn_qk_norm_backward_workspace_size(T, s.head_dim) : 0;
     if (overlap({{dq, T * wq, es}, {dk, T * wk, es}, {dq_weight, s.head_dim, 4}, {dk_weight, s.head_dim, 4},
                  {workspace, (int64_t)need, 1}},
-                {{s.q, T, s.q_stride, wq, es}, {s.k, T, s.k_stride, wk, es}, {dq_out, T, dq_out_stride, wq, es},
-                 {dk_out, T, dk_out_stride, wk, es}, {s.q_weight, s.head_dim, ws}, {s.k_weight, s.head_dim, ws},
+                {{s.q, T, s.q_stride, wq, es}, {s.k, T, s.k_stride, wk, es}, {dq_out, T, dq_out_stride, wq, ges},
+                 {dk_out, T, dk_out_stride, wk, ges}, {s.q_weight, s.head_dim, ws}, {s.k_weight, s.head_dim, ws},
                  {s.rot_dim ? s.positions : nullptr, T, 4}, {s.rot_dim ? s.inv_freq : nullptr, s.rot_dim / 2, 4}}))
         return GDN_ERR_INVALID_ARG;
     if (weights && (workspace == nullptr || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
@@ -259,10 +267,13 @@ gdn_status_t gdn_qk_norm_backward(const gdn_qk_norm_t* args, const void* dq_out,
         const dim3 blocks((unsigned)std::min<int64_t>(tiles, std::min<int64_t>(kQkParts, (int64_t)sms * gdn::qk_resident(true, true))),
                           qk_shares(a, tiles, sms));
         parts = (int64_t)blocks.x * blocks.y;
-        const bool vec = qk_vectors(args, s.q, s.q_stride) && qk_vectors(args, s.k, s.k_stride) &&
-                         qk_vectors(args, dq_out, dq_out_stride) && qk_vectors(args, dk_out, dk_out_stride) &&
-                         qk_vectors(args, dq, wq) && qk_vectors(args, dk, wk);
-        const gdn_status_t r = qk_dispatch<true>(a, s.in_dtype, vec, blocks, st);
+        const gdn_dtype_t t = s.in_dtype;
+        const bool vec = qk_vectors(args, s.q, s.q_stride, t) && qk_vectors(args, s.k, s.k_stride, t) &&
+                         qk_vectors(args, dq_out, dq_out_stride, grad_dtype) && qk_vectors(args, dk_out, dk_out_stride, grad_dtype) &&
+                         qk_vectors(args, dq, wq, t) && qk_vectors(args, dk, wk, t);
+        const gdn_status_t r = t == GDN_F32 ? qk_dispatch<float, float, true>(a, vec, blocks, st)
+                               : grad_dtype == GDN_F32 ? qk_dispatch<__nv_bfloat16, float, true>(a, vec, blocks, st)
+                                                       : qk_dispatch<__nv_bfloat16, __nv_bfloat16, true>(a, vec, blocks, st);
         if (r != GDN_OK) return r;
     }
     if (!weights) return GDN_OK;

@@ -133,34 +133,44 @@ __device__ __forceinline__ void qk_four(const float* p, f2x (&v)[2])
 // A thread's own pieces of the rows that it will work on next, in a ring in shared memory that cp.async fills, as
 // NormRing: the next rows are under way through the sums of these, without registers or barriers.
 constexpr int kQkAhead = 2;  // turns ahead
-template <typename T, int U, bool BWD>
+template <typename T, typename G, int U, bool BWD>
 struct QkRing {
-    static constexpr int P = 4 * (int)sizeof(T), TENSORS = BWD ? 2 : 1;       // bytes of a piece
-    static constexpr size_t BYTES = (size_t)kQkAhead * U * TENSORS * 2 * P * kQkThreads;
+    static constexpr int PX = 4 * (int)sizeof(T), PG = 4 * (int)sizeof(G);     // bytes of a piece of x, and of its gradient
+    static constexpr int ROW = 2 * (PX + (BWD ? PG : 0)) * kQkThreads;
+    static constexpr size_t BYTES = (size_t)kQkAhead * U * ROW;
     unsigned char* base;
-    __device__ __forceinline__ unsigned char* at(int turn, int u, int tensor, int piece) const
+    template <int TENSOR>
+    __device__ __forceinline__ unsigned char* at(int turn, int u, int piece) const
     {
-        return base + ((((turn * U + u) * TENSORS + tensor) * 2 + piece) * kQkThreads + threadIdx.x) * P;
+        constexpr int P = TENSOR ? PG : PX;
+        // (one product for a thread's place where the pieces are alike: the gradients' registers are all taken)
+        if constexpr (PX == PG) return base + ((((turn * U + u) * (BWD ? 2 : 1) + TENSOR) * 2 + piece) * kQkThreads + threadIdx.x) * P;
+        return base + (turn * U + u) * ROW + (TENSOR * 2 * PX + piece * P) * kQkThreads + threadIdx.x * P;
     }
-    __device__ __forceinline__ void copy(int turn, int u, int tensor, int piece, const T* src) const
+    template <int TENSOR>
+    __device__ __forceinline__ void copy(int turn, int u, int piece, const void* src) const
     {
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((unsigned)__cvta_generic_to_shared(at(turn, u, tensor, piece))),
-                     "l"(src), "n"(P) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((unsigned)__cvta_generic_to_shared(at<TENSOR>(turn, u, piece))),
+                     "l"(src), "n"(TENSOR ? PG : PX) : "memory");
     }
-    template <typename ROW>
-    __device__ __forceinline__ void get(int turn, int u, int tensor, ROW& row) const
+    template <int TENSOR, typename R>
+    __device__ __forceinline__ void get(int turn, int u, R& row) const
     {
-        row.lo = *reinterpret_cast<const Vec<T, 4>*>(at(turn, u, tensor, 0));
-        row.hi = *reinterpret_cast<const Vec<T, 4>*>(at(turn, u, tensor, 1));
+        row.lo = *reinterpret_cast<const decltype(row.lo)*>(at<TENSOR>(turn, u, 0));
+        row.hi = *reinterpret_cast<const decltype(row.hi)*>(at<TENSOR>(turn, u, 1));
     }
 };
 
-// BWD: the gradients.
-template <typename T, bool VEC, bool INTER, bool BWD>
+// BWD: the gradients, from those of the outputs in type G: the recurrence's own gradients are fp32, whatever its inputs, and a pass
+// of their own to bf16 would cost more than their bytes here (16384 tokens x (32 + 32) heads of 128: 197 us, with the casts 293).
+// Registers: 128 for the gradients, which bf16 rows on their alignment just fit; fp32 rows or fp32 gradients spill 4 to 24 bytes per
+// thread and rows off their alignment 160 to 284 (16384 x (16 + 16) heads of 128: 207 us in place of about 90).
+template <typename T, typename G, bool VEC, bool INTER, bool BWD>
 __global__ void __launch_bounds__(kQkThreads, qk_resident(BWD, VEC)) k_qk_norm(const QkArgs a)
 {
     constexpr int U = qk_rows(BWD, sizeof(T));
     using Row = QkRow<T, VEC, INTER>;
+    using Grad = QkRow<G, VEC, INTER>;
     extern __shared__ __align__(16) unsigned char qk_smem[];
     let_next_start();
     after_previous();
@@ -198,7 +208,8 @@ __global__ void __launch_bounds__(kQkThreads, qk_resident(BWD, VEC)) k_qk_norm(c
     // more and H heads less.
     struct {
         int64_t tile, stepx, wrapx, stepg, wrapg;
-        const T *px, *pg;
+        const T* px;
+        const G* pg;
         int kind, r, end, h, H, dh;
     } next{};
     auto aim = [&] {  // at the first row of next.kind in next.tile
@@ -216,7 +227,7 @@ __global__ void __launch_bounds__(kQkThreads, qk_resident(BWD, VEC)) k_qk_norm(c
         next.px = static_cast<const T*>(k ? a.x[1] : a.x[0]) + (t0 + tok) * ldx + next.h * a.d;
         next.stepx = dt * ldx + next.dh * a.d, next.wrapx = ldx - (int64_t)H * a.d;
         if constexpr (BWD) {
-            next.pg = static_cast<const T*>(k ? a.dy[1] : a.dy[0]) + (t0 + tok) * ldg + next.h * a.d;
+            next.pg = static_cast<const G*>(k ? a.dy[1] : a.dy[0]) + (t0 + tok) * ldg + next.h * a.d;
             next.stepg = dt * ldg + next.dh * a.d, next.wrapg = ldg - (int64_t)H * a.d;
         }
     };
@@ -239,18 +250,18 @@ __global__ void __launch_bounds__(kQkThreads, qk_resident(BWD, VEC)) k_qk_norm(c
             if (next.tile < tiles) aim();
         }
     };
-    const QkRing<T, U, BWD> ring{qk_smem + a.ring};
+    const QkRing<T, G, U, BWD> ring{qk_smem + a.ring};
     int turn = 0;  // of the ring
     auto fetch = [&](int turn) {
         if (next.tile < tiles) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (next.r + u * slots + slot < next.end) {
-                    ring.copy(turn, u, 0, 0, next.px + ea);
-                    ring.copy(turn, u, 0, 1, next.px + eb);
+                    ring.template copy<0>(turn, u, 0, next.px + ea);
+                    ring.template copy<0>(turn, u, 1, next.px + eb);
                     if constexpr (BWD) {
-                        ring.copy(turn, u, 1, 0, next.pg + ea);
-                        ring.copy(turn, u, 1, 1, next.pg + eb);
+                        ring.template copy<1>(turn, u, 0, next.pg + ea);
+                        ring.template copy<1>(turn, u, 1, next.pg + eb);
                     }
                 }
                 advance();
@@ -302,7 +313,7 @@ __global__ void __launch_bounds__(kQkThreads, qk_resident(BWD, VEC)) k_qk_norm(c
             auto some = [&](auto all, int r0) {  // U rows of every thread; WHOLE: all of them are there
                 constexpr bool WHOLE = decltype(all)::value;
                 Row x[U];
-                [[maybe_unused]] Row g[BWD ? U : 1];
+                [[maybe_unused]] Grad g[BWD ? U : 1];
                 int ang[U];
                 bool on[U];
                 if constexpr (VEC) asm volatile("cp.async.wait_group %0;" ::"n"(kQkAhead - 1) : "memory");
@@ -336,11 +347,11 @@ __global__ void __launch_bounds__(kQkThreads, qk_resident(BWD, VEC)) k_qk_norm(c
                     if constexpr (BWD) sg[u] = 0.0f;
                     if (on[u]) {
                         f2x va[2], vb[2];
-                        if constexpr (VEC) ring.get(turn, u, 0, x[u]);
+                        if constexpr (VEC) ring.template get<0>(turn, u, x[u]);
                         x[u].get(va, vb);
                         ss[u] = psum(pfma(va[0], va[0], pfma(va[1], va[1], pfma(vb[0], vb[0], pmul(vb[1], vb[1])))));
                         if constexpr (BWD) {
-                            if constexpr (VEC) ring.get(turn, u, 1, g[u]);
+                            if constexpr (VEC) ring.template get<1>(turn, u, g[u]);
                             g[u].get(ga[u], gb[u]);
                             if (R2 > 0) {  // turned back
                                 f2x c[2], s[2];
@@ -382,7 +393,7 @@ __global__ void __launch_bounds__(kQkThreads, qk_resident(BWD, VEC)) k_qk_norm(c
                         f2x va[2], vb[2];
                         if constexpr (VEC) {
                             asm volatile("" ::: "memory");  // read again: it need not wait in registers
-                            ring.get(turn, u, 0, x[u]);
+                            ring.template get<0>(turn, u, x[u]);
                         } else {
                             keep_packed(x[u].lo);
                             keep_packed(x[u].hi);

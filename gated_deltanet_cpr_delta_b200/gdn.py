@@ -36,6 +36,7 @@ SYMBOLS = ("gdn_contract_id", "gdn_status_string", "gdn_num_chunk_states", "gdn_
            "gdn_ssm_backward_workspace_size", "gdn_ssm_backward", "gdn_ssm_step",
            "gdn_layer_norm_forward", "gdn_layer_norm_backward_workspace_size", "gdn_layer_norm_backward",
            "gdn_qk_norm_forward", "gdn_qk_norm_backward_workspace_size", "gdn_qk_norm_backward",
+           "gdn_qk_norm_backward_ex",
            "gdn_glu_saved_size", "gdn_glu_forward_workspace_size", "gdn_glu_forward",
            "gdn_glu_backward_workspace_size", "gdn_glu_backward",
            "gdn_policy_loss_forward", "gdn_policy_loss_backward")
@@ -176,6 +177,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.gdn_qk_norm_backward_workspace_size.argtypes = [i64, i32]
     lib.gdn_qk_norm_backward.restype = e
     lib.gdn_qk_norm_backward.argtypes = [qk, P, i64, P, i64, P, P, P, P, P, sz, P]
+    lib.gdn_qk_norm_backward_ex.restype = e
+    lib.gdn_qk_norm_backward_ex.argtypes = [qk, e, P, i64, P, i64, P, P, P, P, P, sz, P]
     glu = ctypes.POINTER(GluStruct)
     lib.gdn_glu_saved_size.restype = i64
     lib.gdn_glu_saved_size.argtypes = [i64, i32]
@@ -879,15 +882,16 @@ def gdn_qk_norm_backward(q, k, dq_out, dk_out, *, q_weight=None, k_weight=None, 
                          interleaved: bool = False, l2: bool = False, eps: float = 1e-6, workspace=None, grads=None):
     """Gradients of sum(dq_out q_out) + sum(dk_out k_out) for :func:`gdn_qk_norm_forward` of the same inputs.
 
-    dq_out, dk_out in q's and k's shapes and type (tokens may be strided).  Returns (dq, dk, dq_weight, dk_weight): the
-    first two in the inputs' type, the others fp32, summed over tokens and heads, None without the
+    dq_out, dk_out in q's and k's shapes, in their type or both fp32, as :func:`gdn_cpr_backward` returns them (tokens may
+    be strided).  Returns (dq, dk, dq_weight, dk_weight): the first two in the inputs' type, the others fp32, summed over tokens and heads, None without the
     weight.  ``grads``: an optional tuple of those four to write into."""
     what = "gdn_qk_norm_backward"
     dev = _gpu(what, q)
     s = _qk_struct(what, q, k, q_weight, k_weight, positions, inv_freq, interleaved, l2, eps, dev)
     T, d, ty = s.tokens, s.head_dim, q.dtype
-    pgq, lgq = _heads(what, "dq_out", dq_out, ty, q.shape, dev)
-    pgk, lgk = _heads(what, "dk_out", dk_out, ty, k.shape, dev)
+    gt = _F32 if dq_out.dtype is _F32 else ty
+    pgq, lgq = _heads(what, "dq_out", dq_out, gt, q.shape, dev)
+    pgk, lgk = _heads(what, "dk_out", dk_out, gt, k.shape, dev)
     if grads is None:
         dqw = dkw = None
         if q_weight is not None and k_weight is not None:
@@ -903,7 +907,7 @@ def gdn_qk_norm_backward(q, k, dq_out, dk_out, *, q_weight=None, k_weight=None, 
     keep, ws, nbytes = None, None, 0
     if dqw is not None or dkw is not None:
         keep, ws, nbytes = _scratch(what, workspace, _scratch_size("gdn_qk_norm_backward_workspace_size", T, d), dev)
-    _call(dev, what, load_library().gdn_qk_norm_backward, s, pgq, lgq, pgk, lgk, pdq, pdk, _opt(what, "dq_weight", dqw, _F32, (d,), dev),
+    _call(dev, what, load_library().gdn_qk_norm_backward_ex, s, _DT[gt], pgq, lgq, pgk, lgk, pdq, pdk, _opt(what, "dq_weight", dqw, _F32, (d,), dev),
           _opt(what, "dk_weight", dkw, _F32, (d,), dev), ws, nbytes)
     return dq, dk, dqw, dkw
 

@@ -626,7 +626,7 @@ typedef struct {
 gdn_status_t gdn_qk_norm_forward(const gdn_qk_norm_t* args, void* q_out, void* k_out, void* stream);
 
 /*
- * Gradients of sum(dq_out q_out) + sum(dk_out k_out), from the forward's inputs: dq, dk in in_dtype;
+ * Gradients of sum(dq_out q_out) + sum(dk_out k_out), from the forward's inputs and dq_out, dk_out in in_dtype: dq, dk in in_dtype;
  * dq_weight, dk_weight [head_dim] fp32, summed over tokens and heads (NULL: not wanted; only where the weight is
  * given).  Without either no workspace is needed.
  */
@@ -634,6 +634,11 @@ size_t gdn_qk_norm_backward_workspace_size(int64_t tokens, int32_t head_dim);
 gdn_status_t gdn_qk_norm_backward(const gdn_qk_norm_t* args, const void* dq_out, int64_t dq_out_stride, const void* dk_out,
                                   int64_t dk_out_stride, void* dq, void* dk, float* dq_weight, float* dk_weight,
                                   void* workspace, size_t workspace_bytes, void* stream);
+/* The same with dq_out and dk_out in grad_dtype: in_dtype, or fp32 as gdn_cpr_backward returns them (bf16 gradients of fp32 inputs:
+ * GDN_ERR_UNSUPPORTED).  dq and dk are in in_dtype. */
+gdn_status_t gdn_qk_norm_backward_ex(const gdn_qk_norm_t* args, gdn_dtype_t grad_dtype, const void* dq_out, int64_t dq_out_stride,
+                                     const void* dk_out, int64_t dk_out_stride, void* dq, void* dk, float* dq_weight,
+                                     float* dk_weight, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * The gated feed-forward block's projections, activation and product:

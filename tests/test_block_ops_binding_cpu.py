@@ -86,3 +86,27 @@ def test_temperatures_whose_reciprocal_leaves_the_range_are_refused():
 
     assert [forward(t) for t in (1e-45, 1e-40, 1e-38, 2.0 ** -101, 0.0)] == [gdn.GDN_ERR_INVALID_ARG] * 5
     assert [forward(t) for t in (2.0 ** -100, 1e-6, 1.0, 1e30)] == [gdn.GDN_ERR_CUDA] * 4
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are not memory")
+def test_gradients_of_the_norms_outputs_in_fp32():
+    """Which types the entry takes, and that the checks go by them: strides, alignment and overlap of 4-byte elements."""
+    build.build()
+    lib = gdn.load_library()
+    A = [(i + 1) << 36 for i in range(12)]
+
+    def call(t=gdn.GDN_BF16, g=gdn.GDN_F32, gq=A[2], ldgq=128, gk=A[3], ldgk=64, dq=A[4], dk=A[5]):
+        s = gdn.QkNormStruct(A[0], A[1], None, None, None, None, 128, 64, 10, 4, 2, 32, 0, 0, 0, 1e-6, t, t)
+        return lib.gdn_qk_norm_backward_ex(s, g, gq, ldgq, gk, ldgk, dq, dk, None, None, None, 0, None)
+
+    bad, cuda = gdn.GDN_ERR_INVALID_ARG, gdn.GDN_ERR_CUDA
+    assert call() == cuda and call(g=gdn.GDN_BF16) == cuda and call(gdn.GDN_F32, gdn.GDN_F32) == cuda
+    assert call(gdn.GDN_F32, gdn.GDN_BF16) == gdn.GDN_ERR_UNSUPPORTED
+    assert call(g=2) == bad and call(g=-1) == bad
+    assert call(gq=A[2] + 2) == bad and call(gq=A[2] + 2, g=gdn.GDN_BF16) == cuda and call(gq=A[2] + 4) == cuda
+    assert call(ldgq=127) == bad and call(ldgk=63) == bad and call(gq=None) == bad
+    size = 10 * 128 * 4
+    assert call(dq=A[2] + size - 16) == bad and call(dq=A[2] + size) == cuda
+    assert call(dq=A[2] + size // 2, g=gdn.GDN_BF16) == cuda
+    assert lib.gdn_qk_norm_backward_ex(None, 0, A[2], 128, A[3], 64, A[4], A[5], None, None, None, 0, None) == bad
+    assert lib.gdn_qk_norm_backward(None, A[2], 128, A[3], 64, A[4], A[5], None, None, None, 0, None) == bad

@@ -226,3 +226,68 @@ def test_without_a_kl_weight_the_reference_takes_no_part():
         want = gdn.gdn_policy_loss_backward(z, y, w, **args)
         got = gdn.gdn_policy_loss_backward(z, y, w, ref_logprob=ref, kl_coef=0.0, **args)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("T,Hq,Hk,d,rot,inter,shift", [
+    (1, 1, 1, 16, 0, False, 0), (70, 4, 4, 128, 128, False, 0), (33, 7, 3, 90, 40, True, 0), (65, 1, 2, 64, 32, True, 4), (300, 3, 3, 8, 8, False, 0),
+    (40, 4, 2, 64, 64, False, 1), (9, 2, 2, 256, 256, False, 2), (2000, 16, 4, 128, 64, False, 0), (17, 5, 1, 34, 22, False, 0)])
+@pytest.mark.parametrize("weight", [False, True])
+def test_the_norms_gradients_from_those_of_the_recurrence(T, Hq, Hk, d, rot, inter, shift, weight):
+    """Gradients of the outputs in fp32 beside bf16 inputs: values that bf16 holds give the bits of a call in bf16, others the definition's
+    values (tolerances as in the norm's tests: dx half a step and 64 units, dw 24 and one for each row, with its fp32 result's own)."""
+    q, k, qw = rand(1, T, Hq, d), rand(2, T, Hk, d, scale=3.0), rand(3, d) if weight else None
+    pos, freq = torch.arange(T, dtype=torch.int32, device="cuda") * 7, 1e2 ** (-torch.arange(rot // 2, device="cuda", dtype=F32) / max(1, rot // 2))
+    args = dict(q_weight=qw, k_weight=qw, interleaved=inter, l2=True)
+    if rot:
+        args.update(positions=pos, inv_freq=freq)
+    wide = torch.full((T, (Hq + Hk) * d + 2 * shift), float("nan"), device="cuda")  # both in one tensor's rows
+    dq, dk = (wide[:, a:a + H * d].unflatten(1, (H, d)) for a, H in ((shift, Hq), (shift + Hq * d, Hk)))
+    dq.copy_(rand(4, T, Hq, d)), dk.copy_(rand(5, T, Hk, d))
+    got = gdn.gdn_qk_norm_backward(q, k, dq, dk, **args)
+    want = gdn.gdn_qk_norm_backward(q, k, dq.to(BF), dk.to(BF), **args)
+    assert got[0].dtype is BF and got[1].dtype is BF
+    for a, b in zip(got, want):
+        assert (a is None and b is None) or torch.equal(a, b)
+    dq.copy_(rand(6, T, Hq, d, t=F32)), dk.copy_(rand(7, T, Hk, d, t=F32))
+    got = gdn.gdn_qk_norm_backward(q, k, dq, dk, **args)
+    n64 = lambda v: v.double().cpu().numpy()  # noqa: E731
+    kw = dict(inter=inter, l2=True, pos=pos.cpu().numpy() if rot else None, freq=n64(freq) if rot else None)
+    for i, (x, dy) in enumerate(((q, dq), (k, dk))):
+        w = n64(qw) if weight else None
+        dx, dw = ops.head_norm_backward(n64(x), n64(dy), w, **kw)
+        Mx, Mw = ops.head_norm_backward(n64(x), n64(dy), w, bound=True, **kw)
+        assert (np.abs(n64(got[i]) - dx) <= HALF[BF] * np.abs(dx) * 1.01 + 64 * U * Mx).all()
+        assert not weight or (np.abs(n64(got[2 + i]) - dw) <= U * np.abs(dw) + (24 + x.shape[0] * x.shape[1]) * U * Mw).all()
+
+
+def test_the_norms_gradients_of_mixed_types_are_refused():
+    x, g = rand(1, 5, 2, 16), rand(2, 5, 2, 16, t=F32)
+    for a, b in ((x, g), (g, x)):
+        with pytest.raises(ValueError, match="dk_out"):
+            gdn.gdn_qk_norm_backward(x, x, a, b)
+    with pytest.raises(ValueError, match="dq_out"):
+        gdn.gdn_qk_norm_backward(g, g, x, x)
+
+
+def test_the_recurrences_gradients_go_to_the_norm_as_they_are():
+    """Norm, recurrence and back: dq and dk of gdn_cpr_backward are the norm's gradients without a cast; dx as the definition has it
+    for them (tolerance as above)."""
+    T, H, D, C = 70, 2, 32, 16
+    qk, v = rand(1, T, 2 * H, D), rand(2, T, H, D)
+    q, k = qk[:, :H], qk[:, H:]
+    pos, freq = torch.arange(T, dtype=torch.int32, device="cuda"), 1e2 ** (-torch.arange(D // 2, device="cuda", dtype=F32) / (D // 2))
+    g = torch.Generator(device="cuda").manual_seed(3)
+    alpha, beta = torch.rand(T, H, generator=g, device="cuda") * 0.4 + 0.6, torch.rand(T, H, generator=g, device="cuda")
+    cu_h = [0, 30, 70]
+    cu = torch.tensor(cu_h, dtype=torch.int32, device="cuda")
+    args = dict(positions=pos, inv_freq=freq, l2=True)
+    qn, kn = gdn.gdn_qk_norm_forward(q, k, **args)
+    o, states = gdn.gdn_cpr_forward(qn, kn, v, alpha, beta, cu, C, cu_seqlens_host=cu_h)
+    dqn, dkn, *_ = gdn.gdn_cpr_backward(qn, kn, v, alpha, beta, rand(4, T, H, D), states, cu, C, cu_seqlens_host=cu_h)
+    assert dqn.dtype is F32
+    got = gdn.gdn_qk_norm_backward(q, k, dqn, dkn, **args)
+    n64 = lambda t: t.double().cpu().numpy()  # noqa: E731
+    kw = dict(l2=True, pos=n64(pos).astype(np.int64), freq=n64(freq))
+    for x, dy, dx in ((q, dqn, got[0]), (k, dkn, got[1])):
+        want, M = (ops.head_norm_backward(n64(x), n64(dy), bound=b, **kw)[0] for b in (False, True))
+        assert dx.dtype is BF and (np.abs(n64(dx) - want) <= HALF[BF] * np.abs(want) * 1.01 + 64 * U * M).all()
