@@ -104,9 +104,14 @@ gdn_status_t glu_gemm(gdn::GluMaps& maps, gdn::GluGemmArgs& a, int sms, cudaStre
     return launch_next(k, dim3(2 * pairs), dim3(gdn::kGluGemmThreads), smem, 0, st, maps, a) ? GDN_OK : GDN_ERR_CUDA;
 }
 
-// Whether the weights are streamed past the tokens: up to 256 tokens, and where the pairs of SMs would have at most 16 tiles
-// (300 x 4096 x 1024 18 us, in tiles 27; 1024 x 2048 x 512 15 and 17; with 32 tiles, 1024 x 1024 x 1024, 17 and 13).
-bool glu_is_few(int64_t rows, int64_t inner) { return rows <= 256 || ceil_div(rows, 256) * ceil_div(inner, 128) <= 16; }
+// Whether the weights are streamed past the tokens: up to 128 tokens, and where the pairs of SMs would have at most 16 tiles, or 32
+// for up to 256 tokens, whose results leave room for one block per SM only (300 x 4096 x 1024 18 us, in tiles 27; 1024 x 2048 x 512 15
+// and 17; with 32 tiles, 1024 x 1024 x 1024, 17 and 13.  A graph's replay, 4 us of it the launch: 256 x 4096 x 4096 37 and 39, x 6144
+// 49 and 43, x 28672 160 and 125; 128 x 4096 x 8192 43 and 47).
+bool glu_is_few(int64_t rows, int64_t inner)
+{
+    return rows <= 128 || ceil_div(rows, 256) * ceil_div(inner, 128) <= (rows <= 256 ? 32 : 16);
+}
 
 constexpr int64_t kStageK = 2 * gdn::kGluK;  // k of a stage of the pair's product
 
@@ -133,9 +138,11 @@ int glu_splits(int64_t tiles, int64_t ksteps, int sms)
     return (int)std::max<int64_t>(1, std::min<int64_t>({want, ksteps / 4, 64}));
 }
 
-// Blocks take equal shares of the units, in multiples of 8 up to 64: one block per SM, with all of its shared memory, or
-// two where 64 units for each SM are not enough.  With fewer units than 32 for each SM, clusters of 2, 4 or 8 blocks
-// share the K axis.
+// Blocks take equal shares of the units, in multiples of 8 up to 64: one block per SM, with all of its shared memory, where 64 units
+// for each SM are enough, or two, or three where all blocks then run at once (replays: 100 x 4096 x 20480 82 us with three, 117 with two;
+// 28672, a block too many for three, 176 and 125; 11008 55 with two, 72 in two rounds of one).  With fewer units than 32 for each SM,
+// clusters of 2 or 4 blocks share the K axis.  A stage holds 4, 2 or 1 times 64 columns, so that there are at least three where
+// there is room (1 x 4096 x 28672 94 us, with one stage 104).
 template <int NB>
 gdn_status_t glu_few(const GluOperands& o, const gdn_glu_t& s, gdn::GluFewArgs& a, int sms, cudaStream_t st)
 {
@@ -144,11 +151,13 @@ gdn_status_t glu_few(const GluOperands& o, const gdn_glu_t& s, gdn::GluFewArgs& 
     const auto slots = [&](int S) { return std::max(1, (S > 1 ? sms * 7 / 8 : sms) / groups); };
     int S = 1;
     while (S < 4 && ceil_div((int64_t)s.inner * S * 2, slots(2)) <= 64 && a.ksteps >= 8 * S) S *= 2;
-    const int resident = ceil_div((int64_t)s.inner * S, slots(S)) <= 64 ? 1 : 2;
+    const int64_t per = ceil_div((int64_t)s.inner * S, slots(S));  // units of an SM
+    const int resident = per <= 64 ? 1 : per <= 128 || per > 192 ? 2 : 3;
     a.rows = (int)std::min<int64_t>(64, ceil_div(ceil_div((int64_t)s.inner * S, (int64_t)slots(S) * resident), 8) * 8);
+    const size_t room = (size_t)(resident == 1 ? 224 : resident == 2 ? 110 : 72) * 1024 - gdn::kGluHalf, chunk = gdn::glu_few_chunk(NB, a.rows);
     a.chunks = NB > 128 ? 1 : NB > 16 ? 2 : 4;
-    const size_t room = (size_t)(resident == 1 ? 224 : 110) * 1024 - gdn::kGluHalf;
-    a.stages = (int)std::min<size_t>(gdn::kGluFewStages, room / (a.chunks * gdn::glu_few_chunk(NB, a.rows)));
+    while (a.chunks > 1 && room / (a.chunks * chunk) < 3) a.chunks /= 2;
+    a.stages = (int)std::min<size_t>(gdn::kGluFewStages, room / (a.chunks * chunk));
     const size_t smem = gdn::glu_few_tiles(NB, a.rows, a.stages, a.chunks) + 1024 + 512;
     gdn::GluFewMaps maps;
     if (!matrix_map(&maps.x, o.x, s.rows, s.width, o.ldx, NB) || !matrix_map(&maps.wg, o.wg, s.inner, s.width, o.ldg, a.rows) ||

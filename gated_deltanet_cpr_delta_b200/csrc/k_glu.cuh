@@ -647,7 +647,7 @@ __global__ void __launch_bounds__(kGluThreads, 1) k_glu_few(const __grid_constan
             for (int t = (int)rank + (int)S * group; t < last; t += (int)S * (kGluThreads / 64)) {
                 float g = 0.0f, u = 0.0f;
 #pragma unroll
-                for (uint32_t q = 0; q < 8; ++q) {
+                for (uint32_t q = 0; q < 4; ++q) {
                     if (q < S) {
                         const uint32_t p = peer_addr(out + t * 64 + r, q);
                         float x, y;

@@ -651,7 +651,7 @@ gdn_status_t gdn_qk_norm_backward_ex(const gdn_qk_norm_t* args, gdn_dtype_t grad
  *   workspace: gdn_glu_forward_workspace_size(args) bytes, 0 where every row of x and of the weights starts at a
  *     multiple of 16 bytes: other ones are copied first
  * Products of bf16 values are summed in fp32, act and the product are fp32, h is rounded once.  A single token of each of
- * up to 256 sequences is bound by the weights' bytes and takes a path of its own.
+ * up to 128 sequences (256 for narrow blocks) is bound by the weights' bytes and takes a path of its own.
  * *status (one int32 on the device, or NULL) becomes GDN_ERR_TIMEOUT when a wait inside the kernel runs
  * out (about a second): the outputs are then unspecified.
  */

@@ -8,6 +8,7 @@ import torch
 
 from gated_deltanet_cpr_delta_b200 import gdn
 from oracle import block_ops as ops
+from test_gpu_glu import case as glu_case, check as glu_check
 from test_gpu_layer_ops import HALF, TYPES, U
 
 pytestmark = pytest.mark.gpu
@@ -291,3 +292,10 @@ def test_the_recurrences_gradients_go_to_the_norm_as_they_are():
     for x, dy, dx in ((q, dqn, got[0]), (k, dkn, got[1])):
         want, M = (ops.head_norm_backward(n64(x), n64(dy), bound=b, **kw)[0] for b in (False, True))
         assert dx.dtype is BF and (np.abs(n64(dx) - want) <= HALF[BF] * np.abs(want) * 1.01 + 64 * U * M).all()
+
+
+@pytest.mark.parametrize("T", [1, 16, 33, 128, 129, 200, 256])
+@pytest.mark.parametrize("D,F", [(72, 4097), (200, 9473), (64, 11008), (136, 20480), (8, 28672), (72, 40001)])
+def test_wide_gated_blocks_of_few_tokens(T, D, F):
+    """Inner widths for which an SM holds one, two and three blocks at a time, and more than run at once."""
+    glu_check(glu_case(T, D, F), "gelu" if T & 1 else "silu", backward=F < 10000)
