@@ -66,7 +66,10 @@ __device__ __forceinline__ void glu_act2(float g, float& a, float& slope)
 // What the backward reads of the forward: g and u to 24 bits (15 of mantissa), as planes of 16-bit words
 // [3][rows][inner]: their upper halves, and the next bytes of both in one word.  In bf16 alone the
 // rounding of g and u would add to dg, du and the weights' gradients as much again as the rounding of the
-// products' operands; 24 bits leave 2^-15, for 6 bytes in place of 4 (fp32: 8).
+// products' operands; 24 bits leave about 2^-16, for 6 bytes in place of 4 (fp32: 8): cut off here, which takes 2^-16
+// ln 2 of a value on average, and given that back when they are read, so that nothing is drawn towards zero (1.35 2^-16 at most; 0 and
+// infinities stay what they are).  (Rounded here, the products of few columns waited for their epilogue: 20110 x
+// 128 x 11712 610 us in place of 498.)
 __device__ __forceinline__ void glu_pack(float g, float u, uint16_t& gh, uint16_t& uh, uint16_t& low)
 {
     const uint32_t a = __float_as_uint(g), b = __float_as_uint(u);
@@ -76,8 +79,9 @@ __device__ __forceinline__ void glu_pack(float g, float u, uint16_t& gh, uint16_
 }
 __device__ __forceinline__ void glu_unpack(uint16_t gh, uint16_t uh, uint16_t low, float& g, float& u)
 {
-    g = __uint_as_float(((uint32_t)gh << 16) | ((uint32_t)(low & 0xff) << 8));
-    u = __uint_as_float(((uint32_t)uh << 16) | (low & 0xff00u));
+    constexpr float back = 1.0000106096f;  // 1 + 2^-16 ln 2
+    g = __uint_as_float(((uint32_t)gh << 16) | ((uint32_t)(low & 0xff) << 8)) * back;
+    u = __uint_as_float(((uint32_t)uh << 16) | (low & 0xff00u)) * back;
 }
 
 // ------------------------------------------------------------- primitives

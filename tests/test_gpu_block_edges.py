@@ -299,3 +299,51 @@ def test_the_recurrences_gradients_go_to_the_norm_as_they_are():
 def test_wide_gated_blocks_of_few_tokens(T, D, F):
     """Inner widths for which an SM holds one, two and three blocks at a time, and more than run at once."""
     glu_check(glu_case(T, D, F), "gelu" if T & 1 else "silu", backward=F < 10000)
+
+
+@pytest.mark.parametrize("T", [64, 640])
+def test_what_the_gated_blocks_backward_reads_is_not_drawn_towards_zero(T):
+    """The forward saves g cut off to 24 bits, by up to 2^-15, and the backward multiplies it with 1 + 2^-16 ln 2: off by at most 2^-15 -
+    2^-16 ln 2 = 1.31 2^-16, and 2^-24 of either rounding.  dw_up = (act(g) dh)^T x with one token for each column of x: each element is
+    one product, within two bf16 terms (2^-16) of act of that.  (Here g = w + 2^-8 w' in [1, 2) has few bits: w' in [2^-k, 2^-k+1) is
+    a multiple of 2^-8-k, and the cut takes 2^-15 (1 - 2^-k) / 2, 2^-15 / 3 on average; so what is read is 2^-16 ln 2 / 3 of the
+    value too large, and was twice that too small.)"""
+    F = 20480 // 64 if T == 640 else 320
+    D = 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.zeros(T, D, device="cuda")
+    rows = torch.arange(T, device="cuda")
+    x[rows, rows % (D // 2)], x[rows, D // 2 + rows % (D // 2)] = 1.0, 2.0 ** -8
+    x = x.to(BF)
+    wg = torch.rand(F, D, generator=g, device="cuda")
+    wg[:, : D // 2] += 1.0
+    wg = wg.to(BF)
+    wu = torch.zeros(F, D, dtype=BF, device="cuda")
+    dh = torch.zeros(T, F, dtype=BF, device="cuda")
+    keep = rows < D // 2
+    dh[keep] = 1.0
+    _, saved = gdn.gdn_glu_forward(x, wg, wu, save=True)
+    words = saved.view(torch.int16).view(3, T, F).to(torch.int32) & 0xffff
+    G = (x.double() @ wg.double().t())[keep]
+    cut = ((words[0] << 16) | ((words[2] & 0xff) << 8)).view(F32)[keep]
+    read = (cut * (1 + 89 * 2.0 ** -23)).double()
+    ln2 = float(np.log(2))
+    assert ((read - G).abs() <= 1.35 * 2.0 ** -16 * G).all()
+    assert abs(float(((read - G) / G).mean()) - 2.0 ** -16 * ln2 / 3) <= 2.0 ** -20
+    assert abs(float(((cut.double() - G) / G).mean()) + 2.0 ** -16 * ln2 * 2 / 3) <= 2.0 ** -20
+    f32 = torch.empty(F, D, device="cuda")
+    grads = gdn.gdn_glu_backward(x, wg, wu, dh, saved, grads=(None, f32, torch.empty_like(f32)))
+    got = grads[2][:, : D // 2].t().double()  # [token, unit]
+    want = torch.nn.functional.silu(read)
+    step = 2.0 ** -8 if T > 128 else 2.0 ** -16
+    assert ((got - want).abs() <= (step + 16 * U) * want).all()
+    # 10240 roundings of at most `step`, as often up as down: within 6 standard errors, and the arithmetic's own 16 units
+    assert abs(float(((got - want) / want).mean())) <= 6 * step / 3 ** 0.5 / got.numel() ** 0.5 + 16 * U
+    # what stands for 0 or for an infinity is read as it is
+    _, zeros = gdn.gdn_glu_forward(torch.zeros_like(x), wg, torch.ones_like(wu), save=True)
+    for out in gdn.gdn_glu_backward(torch.zeros_like(x), wg, torch.ones_like(wu), torch.full_like(dh, 1e4), zeros):
+        assert not out.any()
+    planes = saved.view(torch.int16).view(3, T, F)
+    planes[1, 0, 0], planes[2, 0, 0] = 0x7f80, planes[2, 0, 0] & 0xff  # u = inf
+    dx = gdn.gdn_glu_backward(x, wg, wu, dh, saved)[0]
+    assert (dx[0] == float("inf")).all() and torch.isfinite(dx[1:]).all()
