@@ -202,9 +202,9 @@ auto glu_grad(int32_t act, bool whole)
 }
 
 template <typename OT>
-bool glu_join(const float* part, int splits, int64_t n, void* o0, void* o1, int problems, cudaStream_t st)
+bool glu_join(const float* part, int splits, int64_t n, void* o0, void* o1, int problems, int sms, cudaStream_t st)
 {
-    return launch_next(gdn::k_glu_join<OT>, dim3((unsigned)std::min<int64_t>(ceil_div(n * problems, 256), 148 * 16)), dim3(256), 0, 0, st,
+    return launch_next(gdn::k_glu_join<OT>, dim3((unsigned)std::min<int64_t>(ceil_div(n * problems, 256), (int64_t)sms * 16)), dim3(256), 0, 0, st,
                        part, splits, n, static_cast<OT*>(o0), static_cast<OT*>(o1), problems);
 }
 
@@ -333,15 +333,15 @@ gdn_status_t gdn_glu_backward(const gdn_glu_t* args, const void* dh, int64_t dh_
     a.out[0] = dx; a.partial = sums > 1 ? part : nullptr; a.status = status;
     gdn_status_t r = glu_gemm<gdn::kGluDx>(mx, a, sms, st);
     if (r != GDN_OK) return r;
-    if (sums > 1 && !glu_join<bf16>(part, sums, R * D, dx, nullptr, 1, st)) return GDN_ERR_CUDA;
+    if (sums > 1 && !glu_join<bf16>(part, sums, R * D, dx, nullptr, 1, sms, st)) return GDN_ERR_CUDA;
     a.M = F; a.N = D; a.ksteps = (int32_t)ceil_div(R, kStageK); a.parts = few ? 2 : 1; a.problems = 2; a.splits = p.splits_w;
     a.lo = (int32_t)R; a.partial = p.splits_w > 1 ? part : nullptr;
     a.out[0] = dw_gate; a.out[1] = dw_up; a.out_f32 = dw_dtype == GDN_F32;
     r = glu_gemm<gdn::kGluDw>(mw, a, sms, st);
     if (r != GDN_OK) return r;
     if (p.splits_w > 1) {
-        const bool ok = dw_dtype == GDN_F32 ? glu_join<float>(part, p.splits_w, F * D, dw_gate, dw_up, 2, st)
-                                            : glu_join<bf16>(part, p.splits_w, F * D, dw_gate, dw_up, 2, st);
+        const bool ok = dw_dtype == GDN_F32 ? glu_join<float>(part, p.splits_w, F * D, dw_gate, dw_up, 2, sms, st)
+                                            : glu_join<bf16>(part, p.splits_w, F * D, dw_gate, dw_up, 2, sms, st);
         if (!ok) return GDN_ERR_CUDA;
     }
     return GDN_OK;
