@@ -347,3 +347,46 @@ def test_what_the_gated_blocks_backward_reads_is_not_drawn_towards_zero(T):
     planes[1, 0, 0], planes[2, 0, 0] = 0x7f80, planes[2, 0, 0] & 0xff  # u = inf
     dx = gdn.gdn_glu_backward(x, wg, wu, dh, saved)[0]
     assert (dx[0] == float("inf")).all() and torch.isfinite(dx[1:]).all()
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("T,Hq,Hk,d,shift", [(30000, 2, 2, 16, 0), (16384, 16, 4, 128, 0), (5000, 3, 1, 90, 0), (5000, 4, 2, 64, 1), (9, 145, 3, 256, 0), (1, 1, 1, 2, 0),
+                                            (700, 32, 32, 64, 0)])
+def test_the_norms_weight_gradients_count_every_row(dtype, T, Hq, Hk, d, shift):
+    """Rows of unit length with one element that is not 0, and gradients of 1 to 3: every product and every partial sum is a whole
+    number below 2^24, so the sums over tokens and heads are exact in any order, and a row that is missed or counted twice shows."""
+    t = TYPES[dtype]
+
+    def part(H, seed):
+        row = torch.arange(T * H, device="cuda")
+        at, value = (row * 7 + seed + row // d) % d, 1.0 + (row + seed) % 3
+        wide = torch.full((T, H * d + 2 * shift), float("nan"), dtype=t, device="cuda")
+        x = wide[:, shift:shift + H * d].unflatten(1, (H, d))
+        x.copy_(torch.zeros(T * H, d, device="cuda").scatter_(1, at[:, None], 1.0).view(T, H, d))
+        g = torch.full((T, H, d), 2.0, dtype=t, device="cuda")
+        g.view(T * H, d).scatter_(1, at[:, None], value.to(t)[:, None])
+        return x, g, torch.zeros(d, device="cuda", dtype=torch.float64).index_add_(0, at, value.double())
+
+    (q, dq, wq), (k, dk, wk) = part(Hq, 1), part(Hk, 2)
+    w = torch.ones(d, dtype=t, device="cuda")
+    args = dict(q_weight=w, k_weight=w, l2=True, eps=0.0)
+    for gq, gk in ((dq, dk), (dq.float(), dk.float())):
+        got = gdn.gdn_qk_norm_backward(q, k, gq, gk, **args)
+        assert torch.equal(got[2].double(), wq) and torch.equal(got[3].double(), wk)
+
+
+@pytest.mark.parametrize("D,F", [(200, 300), (512, 1024), (264, 5000)])
+def test_a_rows_bits_in_the_gated_block(D, F):
+    """The same in every call of the same sizes, wherever the row is and whatever stands beside it; in batches of other sizes the
+    sums' order may differ, within e = (D / 4 + 8) 2^-24 of the magnitudes' sum on either side and half a step of the result."""
+    x, wg, wu = rand(1, 600, D), rand(2, F, D, scale=D ** -0.5), rand(3, F, D, scale=D ** -0.5)
+    X, G, V = x.double(), x.double() @ wg.double().t(), x.double() @ wu.double().t()
+    eg, eu = ((D / 4 + 8) * U * (X.abs() @ w.double().abs().t()) for w in (wg, wu))
+    act = torch.nn.functional.silu(G)
+    tol = 2 * (1.13 * V.abs() * eg + (act.abs() + 1.13 * eg) * eu + 16 * U * (act * V).abs()) + 2 * HALF[BF] * (act * V).abs() * 1.02
+    full = gdn.gdn_glu_forward(x, wg, wu)[0]
+    for T in (1, 16, 17, 128, 129, 256, 257, 600):
+        h = gdn.gdn_glu_forward(x[:T], wg, wu)[0]
+        assert ((h.double() - full[:T].double()).abs() <= tol[:T]).all()
+        turned = x[:T].roll(T // 2, 0).contiguous()
+        assert torch.equal(gdn.gdn_glu_forward(turned, wg, wu)[0], h.roll(T // 2, 0)), T
