@@ -14,10 +14,12 @@
 //             accumulator holds g and u of the same 128 units, so act(g) u is made where it is read
 //   dx        A = dg, then du; B = Wg, then Wu, with the output's columns contiguous (read as K x N)
 //   dW        A = dg or du as K x M, B = x as K x N; the two gradients are the two halves of the tiles
-// dg and du are rounded to bf16, which adds to the gradients about what the rounding of a bf16 result adds, where sums
-// of many tokens and units level it out.  Up to 128 tokens, where a few of them can dominate, what the rounding left
-// goes through the products as well, in room that the tiles have anyway: as more rows of dx, joined with
-// the splits of K, and as more rows of K for dW.
+// dg and du are rounded to bf16, which adds to the gradients about what the rounding of a bf16 result adds: their error is 1.41 to 1.45
+// times that of a result rounded once, from 129 to 4096 tokens alike (72 x 80 and 512 x 1024), and 1.7e-3 of the norm in the
+// weights' gradients in fp32 (bf16 results: 2.3e-3).  Up to 128 tokens, where a few of them can dominate (2.2 at 1 x 72 x 80), what
+// the rounding left goes through the products as well, 1.00 and 1e-5, in room that the tiles have anyway: as more rows of dx, of
+// which a tile has 256, joined with the splits of K, and as more rows of K for dW, of which a stage has 128.  Beyond it would double the
+// tiles.
 //
 // k_glu_few serves few tokens, where the weights' bytes bound it: a block holds up to 64 rows of Wg and the same ones of Wu
 // as the M side of one product, as many as give every SM the same share of them, and streams them past the

@@ -650,7 +650,8 @@ gdn_status_t gdn_qk_norm_backward_ex(const gdn_qk_norm_t* args, gdn_dtype_t grad
  *     bits), 16-byte aligned; NULL where no backward follows
  *   workspace: gdn_glu_forward_workspace_size(args) bytes, 0 where every row of x and of the weights starts at a
  *     multiple of 16 bytes: other ones are copied first
- * Products of bf16 values are summed in fp32, act and the product are fp32, h is rounded once.  A single token of each of
+ * Products of bf16 values are summed in fp32, act and the product are fp32, h is rounded once.  The order of a sum goes by the
+ * number of rows and by inner: a row has the same bits in every call of the same sizes, not in every batch.  A single token of each of
  * up to 128 sequences (256 for narrow blocks) is bound by the weights' bytes and takes a path of its own.
  * *status (one int32 on the device, or NULL) becomes GDN_ERR_TIMEOUT when a wait inside the kernel runs
  * out (about a second): the outputs are then unspecified.
@@ -675,7 +676,8 @@ gdn_status_t gdn_glu_forward(const gdn_glu_t* args, void* h, void* saved, void* 
  * Gradients of sum(dh h): dx [rows, width] in in_dtype, dw_gate and dw_up [inner, width] in dw_dtype (bf16 or
  * fp32), all dense.  dh [rows, inner] in in_dtype, rows dh_stride apart; saved: as the forward of these
  * inputs wrote it.  The gradients of the two projections are rounded to bf16, as the tensor cores'
- * operands; for up to 128 rows to two bf16 terms (16 bits).  The workspace's size (at least 4 rows inner bytes)
+ * operands, also where dw_dtype is fp32, which then holds the sums (1.7e-3 of their norm); for up to 128 rows to two bf16 terms (16
+ * bits, 1e-5).  The workspace's size (at least 4 rows inner bytes)
  * depends on the addresses' alignment and the current device.
  */
 size_t gdn_glu_backward_workspace_size(const gdn_glu_t* args);
