@@ -502,7 +502,7 @@ def _out(what: str, name: str, t: Optional[torch.Tensor], dtype: torch.dtype, sh
     if t is None:
         # empty_like takes half the time of empty with a type and a device; views of a wider tensor come out dense, but for
         # unusual orders of their axes
-        if like is not None and like.dtype is dtype and like.shape == shape:
+        if like is not None and like.dtype is dtype:
             t = torch.empty_like(like)
             if t.is_contiguous():
                 return t, t.data_ptr()
