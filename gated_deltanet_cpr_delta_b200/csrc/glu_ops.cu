@@ -106,7 +106,7 @@ gdn_status_t glu_gemm(gdn::GluMaps& maps, gdn::GluGemmArgs& a, int sms, cudaStre
 
 // Whether the weights are streamed past the tokens: up to 128 tokens, and where the pairs of SMs would have at most 16 tiles, or 32
 // for up to 256 tokens, whose results leave room for one block per SM only (300 x 4096 x 1024 18 us, in tiles 27; 1024 x 2048 x 512 15
-// and 17; with 32 tiles, 1024 x 1024 x 1024, 17 and 13.  A graph's replay, 4 us of it the launch: 256 x 4096 x 4096 37 and 39, x 6144
+// and 17; with 32 tiles, 1024 x 1024 x 1024, 17 and 13.  Behind an L2 full of written lines: 256 x 4096 x 4096 37 and 39, x 6144
 // 49 and 43, x 28672 160 and 125; 128 x 4096 x 8192 43 and 47).
 bool glu_is_few(int64_t rows, int64_t inner)
 {
@@ -139,10 +139,10 @@ int glu_splits(int64_t tiles, int64_t ksteps, int sms)
 }
 
 // Blocks take equal shares of the units, in multiples of 8 up to 64: one block per SM, with all of its shared memory, where 64 units
-// for each SM are enough, or two, or three where all blocks then run at once (replays: 100 x 4096 x 20480 82 us with three, 117 with two;
-// 28672, a block too many for three, 176 and 125; 11008 55 with two, 72 in two rounds of one).  With fewer units than 32 for each SM,
-// clusters of 2 or 4 blocks share the K axis.  A stage holds 4, 2 or 1 times 64 columns, so that there are at least three where
-// there is room (1 x 4096 x 28672 94 us, with one stage 104).
+// for each SM are enough, or two, or three where all blocks then run at once (behind an L2 full of written lines: 100 x 4096 x 20480
+// 82 us with three, 117 with two; 28672, a block too many for three, 176 and 125).  With fewer units than 32 for each SM, clusters of
+// 2 or 4 blocks share the K axis.  A stage holds 4, 2 or 1 times 64 columns, so that there are at least three where there is
+// room (100 x 4096 x 11008 55 us, with one stage 72; 1 x 4096 x 28672 94 and 104).
 template <int NB>
 gdn_status_t glu_few(const GluOperands& o, const gdn_glu_t& s, gdn::GluFewArgs& a, int sms, cudaStream_t st)
 {
