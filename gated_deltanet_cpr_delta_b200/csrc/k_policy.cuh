@@ -506,7 +506,8 @@ __global__ void __launch_bounds__(NT + 32, RES) k_policy(const PolicyArgs a)
                                                   : tid < 2 * E && rest < TILE + skip && skip + last * E + tid - E < rest ? skip + last * E + tid - E : -1;
                             if (e >= 0) {
                                 const float x = to_f<T>(reinterpret_cast<const T*>(policy_smem + slot * SLOT + s)[e]);
-                                dst[e] = from_f<T>(__fmaf_rn(ex2(__fmaf_rn(x, C, -bm)), scale, e == yl ? d : 0.0f));
+                                const float g = ex2(__fmaf_rn(x, C, -bm)) * scale;
+                                dst[e] = from_f<T>(e == yl ? g + d : g);  // as in `gradient`: the same bits at every address
                             }
                         }
                     }

@@ -390,3 +390,24 @@ def test_a_rows_bits_in_the_gated_block(D, F):
         assert ((h.double() - full[:T].double()).abs() <= tol[:T]).all()
         turned = x[:T].roll(T // 2, 0).contiguous()
         assert torch.equal(gdn.gdn_glu_forward(turned, wg, wu)[0], h.roll(T // 2, 0)), T
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("V", [1, 4, 13, 1003, 20001])
+def test_the_logits_gradient_has_the_same_bits_at_every_address(dtype, V):
+    """Targets at the rows' ends among them, which come element by element where a row starts or ends inside 16 bytes."""
+    t, R = TYPES[dtype], 60
+    z, w, adv = rand(1, R, V, t=t, scale=3.0), rand(2, R, t=F32), rand(3, R, t=F32)
+    y = torch.tensor([0, 1, 2, V - 1, V - 2, V - 3, V // 2, 5, 7, V - 8] * (R // 10), device="cuda").clamp(0, V - 1)
+    kw = dict(old_logprob=gdn.gdn_policy_loss_forward(z, y)[1] + 0.1, advantages=adv)
+    want = gdn.gdn_policy_loss_backward(z, y, w, **kw)
+    for at in range(9):
+        place = torch.full((R * V + 24,), 7.0, dtype=t, device="cuda")
+        view = place[at:at + R * V].view(R, V)
+        view.copy_(z)
+        apart = torch.full((R * V + 24,), 7.0, dtype=t, device="cuda")
+        for got in (gdn.gdn_policy_loss_backward(view, y, w, dlogits=apart[3:3 + R * V].view(R, V), **kw),
+                    gdn.gdn_policy_loss_backward(view, y, w, dlogits=view, **kw)):
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), at
+        for b, o in ((place, at), (apart, 3)):
+            assert (b[:o] == 7).all() and (b[o + R * V:] == 7).all()
