@@ -91,17 +91,22 @@ gdn_status_t glu_check(const gdn_glu_t* s, const int32_t* status)
     return GDN_OK;
 }
 
+// Before the product's maps are made
+template <int MODE, bool SAVE = false, int ACT = gdn::kGluSilu>
+bool glu_ready()
+{
+    return raise_smem<gdn::glu_gemm_smem(SAVE)>(gdn::k_glu_gemm<MODE, SAVE, ACT>);
+}
+
 template <int MODE, bool SAVE = false, int ACT = gdn::kGluSilu>
 gdn_status_t glu_gemm(gdn::GluMaps& maps, gdn::GluGemmArgs& a, int sms, cudaStream_t st)
 {
     a.tiles_m = (int32_t)ceil_div(a.M, 256);
     a.tiles_n = (int32_t)ceil_div(a.N, MODE == gdn::kGluFwd ? 128 : 256);
     a.tiles = (int64_t)a.tiles_m * a.tiles_n * a.problems * a.splits;
-    auto k = gdn::k_glu_gemm<MODE, SAVE, ACT>;
-    constexpr size_t smem = gdn::glu_gemm_smem(SAVE);
-    if (!raise_smem<smem>(k)) return GDN_ERR_CUDA;
     const unsigned pairs = (unsigned)std::min<int64_t>(a.tiles, std::max(1, sms / 2));
-    return launch_next(k, dim3(2 * pairs), dim3(gdn::kGluGemmThreads), smem, 0, st, maps, a) ? GDN_OK : GDN_ERR_CUDA;
+    return launch_next(gdn::k_glu_gemm<MODE, SAVE, ACT>, dim3(2 * pairs), dim3(gdn::kGluGemmThreads), gdn::glu_gemm_smem(SAVE), 0, st, maps, a)
+               ? GDN_OK : GDN_ERR_CUDA;
 }
 
 // Whether the weights are streamed past the tokens: up to 128 tokens, and where the pairs of SMs would have at most 16 tiles, or 32
@@ -159,12 +164,12 @@ gdn_status_t glu_few(const GluOperands& o, const gdn_glu_t& s, gdn::GluFewArgs& 
     while (a.chunks > 1 && room / (a.chunks * chunk) < 3) a.chunks /= 2;
     a.stages = (int)std::min<size_t>(gdn::kGluFewStages, room / (a.chunks * chunk));
     const size_t smem = gdn::glu_few_tiles(NB, a.rows, a.stages, a.chunks) + 1024 + 512;
+    auto k = s.act == GDN_ACT_SILU ? gdn::k_glu_few<NB, gdn::kGluSilu> : gdn::k_glu_few<NB, gdn::kGluGelu>;
+    if (!raise_smem(k, smem)) return GDN_ERR_CUDA;
     gdn::GluFewMaps maps;
     if (!matrix_map(&maps.x, o.x, s.rows, s.width, o.ldx, NB) || !matrix_map(&maps.wg, o.wg, s.inner, s.width, o.ldg, a.rows) ||
         !matrix_map(&maps.wu, o.wu, s.inner, s.width, o.ldu, a.rows))
         return GDN_ERR_CUDA;
-    auto k = s.act == GDN_ACT_SILU ? gdn::k_glu_few<NB, gdn::kGluSilu> : gdn::k_glu_few<NB, gdn::kGluGelu>;
-    if (!raise_smem(k, smem)) return GDN_ERR_CUDA;
     const dim3 grid((unsigned)ceil_div(s.inner, a.rows) * S, (unsigned)ceil_div(s.rows, NB));
     return launch_next(k, grid, dim3(gdn::kGluThreads), smem, S, st, maps, a) ? GDN_OK : GDN_ERR_CUDA;
 }
@@ -238,7 +243,7 @@ gdn_status_t gdn_glu_forward(const gdn_glu_t* args, void* h, void* saved, void* 
     if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
     if (need > 0 && !aligned(workspace, kAlign)) return GDN_ERR_INVALID_ARG;
     const int sms = sm_count();
-    if (sms == 0 || !bind_context()) return GDN_ERR_CUDA;
+    if (sms == 0) return GDN_ERR_CUDA;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const GluOperands o = glu_operands(s, static_cast<unsigned char*>(workspace));
     if (!glu_align(s, o, sms, st)) return GDN_ERR_CUDA;
@@ -252,6 +257,10 @@ gdn_status_t gdn_glu_forward(const gdn_glu_t* args, void* h, void* saved, void* 
         if (R <= 128) return glu_few<128>(o, s, a, sms, st);
         return glu_few<256>(o, s, a, sms, st);
     }
+    const bool silu = s.act == GDN_ACT_SILU;
+    if (!(silu ? (saved ? glu_ready<gdn::kGluFwd, true, gdn::kGluSilu>() : glu_ready<gdn::kGluFwd, false, gdn::kGluSilu>())
+               : (saved ? glu_ready<gdn::kGluFwd, true, gdn::kGluGelu>() : glu_ready<gdn::kGluFwd, false, gdn::kGluGelu>())))
+        return GDN_ERR_CUDA;
     gdn::GluMaps maps;
     const bool wide_boxes = D % 64 == 0;
     if (!operand_map(&maps.a[0], o.x, R, D, o.ldx, wide_boxes) || !operand_map(&maps.b[0], o.wg, F, D, o.ldg, wide_boxes) ||
@@ -262,7 +271,7 @@ gdn_status_t gdn_glu_forward(const gdn_glu_t* args, void* h, void* saved, void* 
     a.M = R; a.N = F; a.ksteps = (int32_t)ceil_div(D, kStageK); a.parts = 1; a.problems = 1; a.splits = 1; a.wide = wide_boxes;
     a.out[0] = h;
     a.saved = static_cast<uint16_t*>(saved); a.status = status;
-    if (s.act == GDN_ACT_SILU)
+    if (silu)
         return saved ? glu_gemm<gdn::kGluFwd, true, gdn::kGluSilu>(maps, a, sms, st)
                      : glu_gemm<gdn::kGluFwd, false, gdn::kGluSilu>(maps, a, sms, st);
     return saved ? glu_gemm<gdn::kGluFwd, true, gdn::kGluGelu>(maps, a, sms, st)
@@ -319,6 +328,7 @@ gdn_status_t gdn_glu_backward(const gdn_glu_t* args, const void* dh, int64_t dh_
     auto k = few ? glu_grad<true>(s.act, whole) : glu_grad<false>(s.act, whole);
     if (!launch_next(k, dim3(blocks), dim3(256), 0, 0, st, g, dh_stride, sv, R, F, dg, du, p.ld)) return GDN_ERR_CUDA;
 
+    if (!glu_ready<gdn::kGluDx>() || !glu_ready<gdn::kGluDw>()) return GDN_ERR_CUDA;
     gdn::GluMaps mx, mw;
     const bool wide_boxes = D % 64 == 0 && F % 64 == 0;
     if (!operand_map(&mx.a[0], dg, p.grad_rows, F, p.ld, wide_boxes) || !operand_map(&mx.a[1], du, p.grad_rows, F, p.ld, wide_boxes) ||

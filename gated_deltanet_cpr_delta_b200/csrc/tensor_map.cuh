@@ -10,7 +10,8 @@
 namespace {
 
 // cuTensorMapEncodeTiled from the driver, looked up once through the runtime
-// (the library does not link libcuda itself).
+// (the library does not link libcuda itself).  It needs a current context, which a thread has from its first call of the runtime
+// that needs one: a launch, or the setting of a kernel's attribute, comes before the first map.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
 {
     static std::once_flag once;
@@ -23,14 +24,6 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
             fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
     });
     return fn;
-}
-
-// The encoder needs a current context.  A thread that has not called the runtime yet has none: this makes the current device's
-// the thread's own, as a kernel's launch would.
-[[maybe_unused]] bool bind_context()
-{
-    int dev = 0;
-    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
 }
 
 }  // namespace
