@@ -948,7 +948,7 @@ def gdn_glu_forward(x, w_gate, w_up, *, act: str = "silu", save: bool = False, h
     x [.., width], w_gate, w_up [inner, width], bf16 (rows may be strided: the weights may be halves of one matrix); ``act``
     "silu" or "gelu" (tanh form).  Returns (h [.., inner], saved): saved (with ``save``; else None) is what
     :func:`gdn_glu_backward` reads, 6 bytes per element of h.  Single tokens of a decode step are rows like any
-    other.  ``status``: an optional int32 that records a wait that ran out."""
+    other; the order of h's sums goes by the number of rows and by inner.  ``status``: an optional int32 that records a wait that ran out."""
     what = "gdn_glu_forward"
     dev = _gpu(what, x)
     s = _glu_struct(what, x, w_gate, w_up, act, dev)
@@ -971,7 +971,7 @@ def gdn_glu_backward(x, w_gate, w_up, dh, saved, *, act: str = "silu", workspace
 
     dh [.., inner] in x's type (rows may be strided).  Returns (dx in x's shape, dw_gate, dw_up), in x's type.
     ``grads``: an optional tuple of those three to write into; what is None in it is allocated.  The weights' gradients
-    may then be fp32, both: the one that is given decides."""
+    may then be fp32, both: the one that is given decides.  They hold the sums; the operands' own rounding to bf16 stays."""
     what = "gdn_glu_backward"
     dev = _gpu(what, x)
     s = _glu_struct(what, x, w_gate, w_up, act, dev)
@@ -1014,7 +1014,7 @@ def gdn_policy_loss_forward(logits, targets, *, old_logprob=None, advantages=Non
         loss = -min(ratio A, clip(ratio, 1 - clip_low, 1 + clip_high) A) + kl_coef (e^g - g - 1),  g = ref_logprob - logprob
 
     logits bf16 or fp32 (rows may be strided); targets int64 [rows], negative: the row takes no part (its results are 0);
-    old_logprob, advantages, ref_logprob fp32 [rows].  ref_logprob None: no KL term; old_logprob and advantages None: the
+    old_logprob, advantages, ref_logprob fp32 [rows]; temperature at least 2^-100.  ref_logprob None or kl_coef 0: no KL term; old_logprob and advantages None: the
     log-probabilities alone, as a rollout records them.  Returns (loss or None, logprob), fp32 [rows].  A row's
     log-probability has the same bits in every batch and in :func:`gdn_policy_loss_backward`.
     ``status``: an optional int32 that records a target outside the vocabulary."""
