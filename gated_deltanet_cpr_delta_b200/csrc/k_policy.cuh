@@ -130,7 +130,7 @@ __device__ __forceinline__ void policy_add(float& m, float& sum, float m1, float
 
 // A row whose maximum is far off, by NT threads: the maximum M itself and how many logits equal it, which are all that count: logits that
 // differ there differ by 64 or more in units of log2.  n: as a sum relative to M, not a number where a logit is not or M is infinite.
-// (As a call of its own it cost every row: losses of 200000 x 1000 301 us in place of 293; without it 282, of 2048 x 32000 34.8 either way.)
+// (As a call of its own it cost every row: losses of 200000 x 1000 301 us in place of 293.)
 template <typename T, int NT>
 __device__ __forceinline__ float2 policy_far(const T* z, int V, float* wm, float* ws)
 {
@@ -409,11 +409,12 @@ __global__ void __launch_bounds__(NT + 32, RES) k_policy(const PolicyArgs a)
         sum = lane < WARPS ? ws[lane] : 0.0f;
         policy_join<32>(m, sum);
         float C = a.c, bm = m;  // exponents are fma(z, C, -bm)
-        const float zt = SPLIT ? split_target : target_logit, at = __fmaf_rn(zt, a.c, -m), log_sum = log2f(sum);
-        float lp = (at - log_sum) * 0.69314718055994530942f;
-        if (__builtin_expect(!(fabsf(m) < kPolicyFar && fabsf(at) < INFINITY), 0)) {
+        const float zt = SPLIT ? split_target : target_logit, at = __fmaf_rn(zt, a.c, -m);
+        float head = at * 0.69314718055994530942f;  // lp = head - log(sum); where `near`, from log2(sum) with one product
+        const bool near = fabsf(m) < kPolicyFar && fabsf(at) < INFINITY;
+        if (__any_sync(kFullMask, !near)) {  // (the same for all; a vote costs a row less than a branch that could part its threads)
             if (fabsf(m) < kPolicyFar) {  // a target far below: out of range times log2(e), perhaps not by itself
-                lp = zt * a.inv_tau - (m + log_sum) * 0.69314718055994530942f;
+                head = zt * a.inv_tau - m * 0.69314718055994530942f;
             } else {
                 const float2 far = policy_far<T, NT>(static_cast<const T*>(a.z) + row * a.ldz, a.V, wm, ws);
                 m = far.x, sum = far.y;
@@ -421,7 +422,7 @@ __global__ void __launch_bounds__(NT + 32, RES) k_policy(const PolicyArgs a)
                 C = __uint_as_float((294u - (__float_as_uint(m) >> 23 & 0xffu)) << 23);
                 bm = m * C;
                 // (by halves: the difference may be out of range where its quotient is not)
-                lp = (zt == m ? 0.0f : (0.5f * zt - 0.5f * m) * a.inv_tau * 2.0f) - log2f(sum) * 0.69314718055994530942f;
+                head = zt == m ? 0.0f : (0.5f * zt - 0.5f * m) * a.inv_tau * 2.0f;
                 if constexpr (SPLIT && BWD) {  // the gradient may take the place of what another block still walks
                     together();
                     if (tid < S && !lost) mbar_arrive_peer(peer_addr(&joined, tid));
@@ -429,25 +430,31 @@ __global__ void __launch_bounds__(NT + 32, RES) k_policy(const PolicyArgs a)
                 }
             }
         }
-        float loss = 0.0f, d = 0.0f;
-        if (a.old != nullptr) {
-            const float ratio = ex2((lp - old) * kLog2e);
-            if (adv != 0.0f) {  // a zero takes no part, whatever the ratio
-                const float free = -adv * ratio, held = -adv * fminf(fmaxf(ratio, a.lo), a.hi);
-                loss = free < held ? held : free;  // not a number where the ratio is not
-                d = free < held ? 0.0f : free;
-            }
-            if (a.ref != nullptr && a.kl != 0.0f) {  // (0 times a term that overflowed is not a number)
-                float slope;
-                loss = __fmaf_rn(a.kl, policy_kl(ref - lp, slope), loss);
-                d = __fmaf_rn(a.kl, slope, d);
-            }
-        }
-        if (tid == 0 && rank == 0 && !lost) {
-            if (a.loss != nullptr) a.loss[row] = loss;
-            if (a.lp != nullptr) a.lp[row] = lp;
-        }
         together();  // the warps' sums have been read
+        [[maybe_unused]] float d = 0.0f;
+        // without a gradient the other warps go on to the next row (losses of 16384 x 8000 86 us in place of 94)
+        if (BWD || warp == 0) {
+            const float log_sum = log2f(sum);
+            const float lp = near ? (at - log_sum) * 0.69314718055994530942f : head - log_sum * 0.69314718055994530942f;
+            float loss = 0.0f;
+            if (a.old != nullptr) {
+                const float ratio = ex2((lp - old) * kLog2e);
+                if (adv != 0.0f) {  // a zero takes no part, whatever the ratio
+                    const float free = -adv * ratio, held = -adv * fminf(fmaxf(ratio, a.lo), a.hi);
+                    loss = free < held ? held : free;  // not a number where the ratio is not
+                    d = free < held ? 0.0f : free;
+                }
+                if (a.ref != nullptr && a.kl != 0.0f) {  // (0 times a term that overflowed is not a number)
+                    float slope;
+                    loss = __fmaf_rn(a.kl, policy_kl(ref - lp, slope), loss);
+                    d = __fmaf_rn(a.kl, slope, d);
+                }
+            }
+            if (tid == 0 && rank == 0 && !lost) {
+                if (a.loss != nullptr) a.loss[row] = loss;
+                if (a.lp != nullptr) a.lp[row] = lp;
+            }
+        }
         if constexpr (BWD) {
             // ---- the second walk: first the tiles that have stayed, then the others
             d *= dloss * a.inv_tau;
